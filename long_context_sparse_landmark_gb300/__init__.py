@@ -11,7 +11,8 @@ __all__ = ["WORKLOADS", "Workload", "generate", "sample_rows", "msa_attention",
            "ring_attention", "band_attention", "topk_attention", "compressed_attention", "landmarks",
            "msa_attention_backward", "msa_attention_trainable", "msa_attention_host",
            "compressed_attention_backward",
-           "SparseLandmarkAttention", "binding"]
+           "SparseLandmarkAttention", "KVCache", "cache_append", "cache_attention",
+           "cache_block_select", "cache_topk_attention", "cache_evict", "binding"]
 
 
 def __getattr__(name):
@@ -21,6 +22,10 @@ def __getattr__(name):
                 "compressed_attention_backward"):
         from . import api
         return getattr(api, name)
+    if name in ("KVCache", "cache_append", "cache_attention", "cache_block_select",
+                "cache_topk_attention", "cache_evict"):
+        from . import cache
+        return getattr(cache, name)
     if name == "binding":
         from . import _binding
         return _binding

@@ -31,9 +31,21 @@ EXPORTS = ("msa_version", "msa_last_error_string", "msa_landmark_pool", "msa_att
            "msa_attn_bwd", "msa_attn_bwd_workspace_size", "msa_attn_bwd_global_rows",
            "msa_attn_bwd_global_rows_workspace_size", "msa_attn_fwd_partial",
            "msa_attn_fwd_partial_merge", "msa_lse_merge",
+           "msa_cache_append", "msa_cache_attn_workspace_size", "msa_cache_attn",
+           "msa_cache_select_workspace_size", "msa_cache_select",
+           "msa_cache_attn_select_workspace_size", "msa_cache_attn_select",
+           "msa_cache_attn_topk_workspace_size", "msa_cache_attn_topk", "msa_cache_evict",
            "msa_attn_uses_tensor_cores", "msa_attn_fwd_topk_uses_tensor_cores",
            "msa_debug_bounds_build", "msa_device_status", "msa_debug_set_wait_limit_ns",
            "msa_debug_force_single_cta", "msa_debug_set_max_clusters")
+
+
+class KvCacheStruct(ctypes.Structure):
+    """msa_kv_cache."""
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("k_mean", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
+                ("Hkv", ctypes.c_int), ("d", ctypes.c_int), ("block", ctypes.c_int)]
 
 
 class MsaError(RuntimeError):
@@ -103,6 +115,32 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.msa_attn_fwd_partial_merge.restype = i32
     lib.msa_lse_merge.argtypes = [vp, vp, i32, vp, vp, i64, i32, i32, i32, vp]
     lib.msa_lse_merge.restype = i32
+    cp, sz = ctypes.POINTER(KvCacheStruct), ctypes.c_size_t
+    lib.msa_cache_append.argtypes = [cp, vp, vp, vp, i64, i64, vp, i32, vp, i32, i32, vp]
+    lib.msa_cache_append.restype = i32
+    lib.msa_cache_attn_workspace_size.argtypes = [cp, i32, i32, i32, i32, i32, i32]
+    lib.msa_cache_attn_workspace_size.restype = sz
+    lib.msa_cache_attn.argtypes = [cp, vp, vp, i32, vp, i32, i32, i32, i64, f32, vp, vp, vp, i64,
+                                   i32, i32, vp, sz, vp]
+    lib.msa_cache_attn.restype = i32
+    lib.msa_cache_select_workspace_size.argtypes = [cp, i32, i32, i32]
+    lib.msa_cache_select_workspace_size.restype = sz
+    lib.msa_cache_select.argtypes = [cp, vp, vp, i32, vp, i32, i32, i32, i64, i32, vp, vp, i32,
+                                     vp, sz, vp]
+    lib.msa_cache_select.restype = i32
+    lib.msa_cache_attn_select_workspace_size.argtypes = [cp, i32, i32, i32, i32, i32]
+    lib.msa_cache_attn_select_workspace_size.restype = sz
+    lib.msa_cache_attn_select.argtypes = [cp, vp, vp, i32, vp, i32, i32, i32, i64, vp, vp, i32,
+                                          f32, vp, vp, i32, i32, vp, sz, vp]
+    lib.msa_cache_attn_select.restype = i32
+    lib.msa_cache_attn_topk_workspace_size.argtypes = [cp, i32, i32, i32, i32, i32, i32]
+    lib.msa_cache_attn_topk_workspace_size.restype = sz
+    lib.msa_cache_attn_topk.argtypes = [cp, vp, vp, i32, vp, i32, i32, i32, i64, i32, f32, vp, vp,
+                                        i32, i32, vp, sz, vp]
+    lib.msa_cache_attn_topk.restype = i32
+    lib.msa_cache_evict.argtypes = [cp, vp, i32, vp, i32, vp, i64, i64, i64, vp, i32, vp, vp, vp,
+                                    i64, vp]
+    lib.msa_cache_evict.restype = i32
     lib.msa_attn_uses_tensor_cores.argtypes = [i32, i32, i32, i32]
     lib.msa_attn_uses_tensor_cores.restype = i32
     lib.msa_attn_fwd_topk_uses_tensor_cores.argtypes = [i64, i32, i32, i32, i32, i32]
@@ -412,3 +450,118 @@ def lse_merge(o_parts, lse_parts, out, lse, stream=None) -> None:
         _ptr(t)
     _check(_lib.msa_lse_merge(arr_o, arr_l, P, _ptr(out), _ptr(lse), n, Hq, d, _dt(out),
                               _stream(stream)))
+
+
+# -- the 8-bit KV cache ------------------------------------------------------
+# `cache` is a KvCacheStruct; table [batch, max_blocks] and lens [batch] are
+# int32 tensors.
+
+def _i32ptr(t, what):
+    if t.dtype != torch.int32:
+        raise TypeError(f"{what} must be int32")
+    return _ptr(t)
+
+
+def _f32ptr(t, what):
+    if t is None:
+        return None
+    if t.dtype != torch.float32:
+        raise TypeError(f"{what} must be float32")
+    return _ptr(t)
+
+
+def _ws_size(n: int, what: str) -> int:
+    if n == 0:
+        raise MsaError(MSA_ERR_INVALID_ARG, f"{what}: {_lib.msa_last_error_string().decode()}")
+    return n
+
+
+def cache_append(cache, k, v, cu, max_new: int, table, lens, stream=None) -> None:
+    """msa_cache_append: rows cu[b]..cu[b+1] of k, v become sequence b's last slots."""
+    _check(_lib.msa_cache_append(cache, _ptr(k), _ptr(v), _i32ptr(cu, "cu"), k.shape[0],
+                                 int(max_new), _i32ptr(table, "table"), table.shape[1],
+                                 _i32ptr(lens, "lens"), table.shape[0], _dt(k), _stream(stream)))
+
+
+def cache_attn_workspace_size(cache, max_blocks: int, batch: int, n_q: int, Hq: int,
+                              weights: bool, dtype: torch.dtype) -> int:
+    return _ws_size(int(_lib.msa_cache_attn_workspace_size(
+        cache, max_blocks, batch, n_q, Hq, 1 if weights else 0,
+        MSA_BF16 if dtype == torch.bfloat16 else MSA_F32)), "msa_cache_attn")
+
+
+def cache_attn(cache, q, table, lens, window: int, scale: float, out, lse, weights, workspace,
+               stream=None) -> None:
+    """msa_cache_attn: query tokens q [batch, n_q, Hq, d] over the cache."""
+    b, n_q, Hq, _ = q.shape
+    _check(_lib.msa_cache_attn(cache, _ptr(q), _i32ptr(table, "table"), table.shape[1],
+                               _i32ptr(lens, "lens"), b, n_q, Hq, int(window), float(scale),
+                               _ptr(out), _f32ptr(lse, "lse"), _f32ptr(weights, "weights"),
+                               0 if weights is None else weights.shape[2], _dt(q), _dt(out),
+                               _ptr(workspace), workspace.numel() * workspace.element_size(),
+                               _stream(stream)))
+
+
+def cache_select_workspace_size(cache, max_blocks: int, batch: int, n_q: int) -> int:
+    return _ws_size(int(_lib.msa_cache_select_workspace_size(cache, max_blocks, batch, n_q)),
+                    "msa_cache_select")
+
+
+def cache_select(cache, q, table, lens, window: int, top_k: int, sel, cnt, workspace,
+                 stream=None) -> None:
+    """msa_cache_select: the top_k blocks of each query token and KV head."""
+    b, n_q, Hq, _ = q.shape
+    _check(_lib.msa_cache_select(cache, _ptr(q), _i32ptr(table, "table"), table.shape[1],
+                                 _i32ptr(lens, "lens"), b, n_q, Hq, int(window), int(top_k),
+                                 _i32ptr(sel, "sel"), _i32ptr(cnt, "cnt"), _dt(q),
+                                 _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                 _stream(stream)))
+
+
+def cache_attn_select_workspace_size(cache, max_blocks: int, batch: int, n_q: int, Hq: int,
+                                     dtype: torch.dtype) -> int:
+    return _ws_size(int(_lib.msa_cache_attn_select_workspace_size(
+        cache, max_blocks, batch, n_q, Hq, MSA_BF16 if dtype == torch.bfloat16 else MSA_F32)),
+        "msa_cache_attn_select")
+
+
+def cache_attn_select(cache, q, table, lens, window: int, sel, cnt, scale: float, out, lse,
+                      workspace, stream=None) -> None:
+    """msa_cache_attn_select: window + the selected blocks."""
+    b, n_q, Hq, _ = q.shape
+    _check(_lib.msa_cache_attn_select(
+        cache, _ptr(q), _i32ptr(table, "table"), table.shape[1], _i32ptr(lens, "lens"), b, n_q,
+        Hq, int(window), _i32ptr(sel, "sel"), _i32ptr(cnt, "cnt"), sel.shape[3], float(scale),
+        _ptr(out), _f32ptr(lse, "lse"), _dt(q), _dt(out), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def cache_attn_topk_workspace_size(cache, max_blocks: int, batch: int, n_q: int, Hq: int,
+                                   top_k: int, dtype: torch.dtype) -> int:
+    return _ws_size(int(_lib.msa_cache_attn_topk_workspace_size(
+        cache, max_blocks, batch, n_q, Hq, int(top_k),
+        MSA_BF16 if dtype == torch.bfloat16 else MSA_F32)), "msa_cache_attn_topk")
+
+
+def cache_attn_topk(cache, q, table, lens, window: int, top_k: int, scale: float, out, lse,
+                    workspace, stream=None) -> None:
+    """msa_cache_attn_topk: select and attend in one call."""
+    b, n_q, Hq, _ = q.shape
+    _check(_lib.msa_cache_attn_topk(cache, _ptr(q), _i32ptr(table, "table"), table.shape[1],
+                                    _i32ptr(lens, "lens"), b, n_q, Hq, int(window), int(top_k),
+                                    float(scale), _ptr(out), _f32ptr(lse, "lse"), _dt(q),
+                                    _dt(out), _ptr(workspace),
+                                    workspace.numel() * workspace.element_size(),
+                                    _stream(stream)))
+
+
+def cache_evict(cache, table, lens, weights, dst_table, budget: int, recent: int, new_lens, kept,
+                new_weights, stream=None) -> None:
+    """msa_cache_evict: keep the recent slots and those of the greatest weight."""
+    _check(_lib.msa_cache_evict(cache, _i32ptr(table, "table"), table.shape[1],
+                                _i32ptr(lens, "lens"), table.shape[0],
+                                _f32ptr(weights, "weights"), weights.shape[2], int(budget),
+                                int(recent), _i32ptr(dst_table, "dst_table"), dst_table.shape[1],
+                                _i32ptr(new_lens, "new_lens"), _i32ptr(kept, "kept"),
+                                _f32ptr(new_weights, "new_weights"), new_weights.shape[2],
+                                _stream(stream)))

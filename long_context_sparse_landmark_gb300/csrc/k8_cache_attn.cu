@@ -1,0 +1,1036 @@
+// K8: attention of a few query tokens over the 8-bit KV cache, in full,
+// over a window, or over a window and selected blocks.
+//
+// Mathematics, per query row (position p, head h of KV group c), over its
+// slots j: s_j = scale <q, code_j> kscale(j), out = sum e^{s_j} code_j
+// vscale(j) / sum e^{s_j}, lse = ln sum e^{s_j}.  With u_j = s_j +
+// log2 vscale(j) (log2 units), out = 2^{M} sum 2^{u_j - M} code_j / sum
+// 2^{s_j - m} 2^{-m}...: the value scale goes into the exponent, so the
+// weights that meet the raw codes have a running maximum M of their own and
+// the denominator another one, m; both sums run in fp32.
+//
+// The work is read once: 2 d bytes a slot and KV head, shared by the group's
+// rows, so HBM bounds it.  The slots of all (sequence, KV head, row tile)
+// units form one list of 32-slot chunks that is cut into equal ranges, one a
+// CTA, whatever the lengths are (they are only known on the device); where a
+// cut falls inside a unit the parts are joined by their log-sum-exp in a
+// second kernel.
+//
+// bf16 rows run on the tensor cores (mma.sync, fp16 operands): codes turn
+// into halves exactly, a row of q is scaled by a power of two so that it
+// does too (an element 2^-31 of the row's largest and smaller is rounded),
+// and the weights are halves with 11 bits, scaled to use the whole range
+// (2^14 for the largest, so 2^-28 of it still has full precision).  Keys
+// are the MMA's 16 rows and query rows its 8 columns: a group of 8 heads
+// wastes nothing, and K and V go from global memory straight into the
+// fragments -- a lane's 16-byte load is its piece of four k-steps, with the
+// d (or slot) index permuted alike on both operands.  tcgen05 would need
+// the codes widened in shared memory first and 64 or 128 rows to fill its M;
+// the arithmetic is far below either unit's rate here.
+// fp32 rows run on the CUDA cores with fp32 arithmetic throughout.
+#include <math.h>
+
+#include "cache_common.cuh"
+
+namespace msa {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kSms = 152;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kPBits = 14.f;  // log2 of the largest half weight
+
+// ---- the list of chunks ----------------------------------------------------
+
+// Entry i of the outer list: a sequence (dense), or a query token of one
+// (selected blocks).  Its Hkv * n_tiles units have the same chunks.
+struct Entry {
+  int b, t;      // sequence, query token (dense: 0)
+  int len;       // slots held, the query tokens' own among them
+  int win0;      // first slot of the window part, a multiple of kChunk
+  int n_sel;     // selected blocks
+  int n_cand;    // blocks that may be selected
+  int n_chunks;  // of selected blocks, then of the window
+};
+
+__device__ __forceinline__ Entry entry_at(const CacheAttnArgs& a, int i) {
+  Entry e;
+  e.b = a.sel ? i / a.T : i;
+  e.t = a.sel ? i - e.b * a.T : 0;
+  e.len = cache_len(a.s, e.b, a.c.block, a.status);
+  const int p0 = e.len - a.T + e.t;       // first row's position
+  const int p1 = a.sel ? p0 : e.len - 1;  // last row's
+  const int lo = max(0, p0 - a.window + 1);
+  e.win0 = lo / kChunk * kChunk;
+  e.n_cand = e.n_sel = 0;
+  if (a.sel && p0 >= a.window) {
+    e.n_cand = (p0 - a.window + 1) / a.c.block;
+    e.n_sel = min(a.top_k, e.n_cand);
+  }
+  e.n_chunks = p1 < 0 ? 0 : e.n_sel * (a.c.block / kChunk) + (p1 - e.win0) / kChunk + 1;
+  return e;
+}
+
+struct Plan {
+  int n_entries, units;  // units an entry: Hkv * n_tiles
+  int rows, n_tiles;     // query rows of a unit's entry, and their tiles
+};
+
+__device__ __forceinline__ Plan plan_of(const CacheAttnArgs& a, int tile) {
+  Plan p;
+  const int g = a.Hq / a.c.Hkv;
+  p.n_entries = a.sel ? a.s.batch * a.T : a.s.batch;
+  p.rows = a.sel ? g : a.T * g;
+  p.n_tiles = (p.rows + tile - 1) / tile;
+  p.units = a.c.Hkv * p.n_tiles;
+  return p;
+}
+
+// Inclusive sum over the block; all threads get the total in *total.
+__device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* smem, int64_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) smem[warp] = x;
+  __syncthreads();
+  int64_t before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    before += w < warp ? smem[w] : 0;
+    all += smem[w];
+  }
+  *total = all;
+  return x + before;
+}
+
+// All chunks of the call (over one unit an entry: times p.units for all).
+__device__ __forceinline__ int64_t total_chunks(const CacheAttnArgs& a, const Plan& p,
+                                                int64_t* smem) {
+  int64_t x = 0, total;
+  for (int i = threadIdx.x; i < p.n_entries; i += kThreads) x += entry_at(a, i).n_chunks;
+  block_scan(x, smem, &total);
+  return total;
+}
+
+// CTAs that share W chunks: a CTA's warps take at least one each.
+__device__ __forceinline__ int64_t cta_count(const CacheAttnArgs& a, int64_t W) {
+  return max64(1, min64(a.n_ctas, (W + kWarps - 1) / kWarps));
+}
+__device__ __forceinline__ int64_t cta_begin(int64_t p, int64_t W, int64_t P) { return p * W / P; }
+// The CTA whose range holds chunk x.
+__device__ __forceinline__ int64_t cta_of(int64_t x, int64_t W, int64_t P) {
+  return ((x + 1) * P - 1) / W;
+}
+
+// ---- pieces of the tensor-core body ---------------------------------------
+
+__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float ex2(float x) { return exp2f(x); }
+__device__ __forceinline__ float finite_or_0(float m) { return m == -INFINITY ? 0.f : m; }
+
+// Row m of an entry: its query token and head.
+__device__ __forceinline__ void row_of(const CacheAttnArgs& a, const Entry& e, int c, int m,
+                                       int* t, int* h) {
+  const int g = a.Hq / a.c.Hkv;
+  *t = a.sel ? e.t : m / g;
+  *h = c * g + (a.sel ? m : m % g);
+}
+
+// What a warp knows of the chunk it works on.
+struct Chunk {
+  int64_t at;    // first slot's row in the codes [n_pages * Hkv * block, d]
+  int key0;      // first slot
+  float ks, vs;  // scales of K and V
+  bool on;       // false: nothing to attend (a selection shorter than top_k)
+  bool window;   // of the window part: rows' own limits apply
+};
+
+// Chunks x, x + kWarps, ... of a unit, read 32 ahead: lane l holds the page
+// and scales of chunk x + l * kWarps, so that a chunk's loads never wait on
+// the table.
+struct Ahead {
+  int64_t at;
+  int key0;
+  float ks, vs;
+  int flags;
+};
+
+__device__ __forceinline__ Ahead look_ahead(const CacheAttnArgs& a, const Entry& e, int c,
+                                            int x, int end) {
+  Ahead r;
+  r.at = 0;
+  r.key0 = 0;
+  r.ks = r.vs = 0.f;
+  r.flags = 0;
+  if (x >= end) return r;
+  const int per = a.c.block / kChunk;
+  int slot;
+  if (x < e.n_sel * per) {
+    const int64_t u = (static_cast<int64_t>(e.b) * a.T + e.t) * a.c.Hkv + c;
+    const int i = x / per;
+    const int64_t cnt = sel_count_checked(a.cnt[u], a.top_k, e.n_cand, a.status);
+    if (i >= cnt) return r;
+    const int blk = sel_block_checked(a.sel[u * a.top_k + i], e.n_cand, a.status);
+    slot = blk * a.c.block + (x - i * per) * kChunk;
+    r.flags = 1;
+  } else {
+    slot = e.win0 + (x - e.n_sel * per) * kChunk;
+    r.flags = 3;
+  }
+  const int j = slot / a.c.block;
+  int64_t page = cache_page(a.s, e.b, j, a.c.n_pages, a.status);
+  if (page < 0) {  // recorded; read a page that exists
+    page = 0;
+    r.flags = 0;
+  }
+  r.key0 = slot;
+  const int64_t head = page * a.c.Hkv + c;
+  r.at = head * a.c.block + (slot - j * a.c.block);
+  r.ks = a.c.k_scale[head];
+  r.vs = a.c.v_scale[head];
+  return r;
+}
+
+__device__ __forceinline__ Chunk chunk_of(const Ahead& r, int src) {
+  Chunk c;
+  c.key0 = __shfl_sync(0xffffffffu, r.key0, src);
+  c.at = __shfl_sync(0xffffffffu, r.at, src);
+  c.ks = __shfl_sync(0xffffffffu, r.ks, src);
+  c.vs = __shfl_sync(0xffffffffu, r.vs, src);
+  const int f = __shfl_sync(0xffffffffu, r.flags, src);
+  c.on = f & 1;
+  c.window = f & 2;
+  return c;
+}
+
+// log2 of a block's value scale; a block of zeros (scale 0) counts as 1.
+__device__ __forceinline__ float log2_scale(float vs) { return vs == 0.f ? 0.f : log2f(vs); }
+
+// The joined result of a CTA's warps for one unit's range, or a whole unit.
+// Row r: osum[w][r][dim] holds warp w's sum scaled to the row's common M,
+// stat[w][r] = {m, l, M}.
+struct Stat {
+  float m, l, M;
+};
+
+// Writes row m's output element pair and, once a row, its lse.  `whole`: the
+// unit lies in this CTA alone and goes to out; else to its part.
+__device__ __forceinline__ void store_lse(const CacheAttnArgs& a, const Plan& p, const Entry& e,
+                                          int c, int m, float lse2) {
+  int t, h;
+  row_of(a, e, c, m, &t, &h);
+  const int64_t at = (static_cast<int64_t>(e.b) * a.Hq + h) * a.T + t;
+  if (MSA_IN_RANGE(at, 1, static_cast<int64_t>(a.s.batch) * a.Hq * a.T, a.status))
+    a.lse[at] = lse2 * kLn2;
+  if (a.weights) {
+    const int even = (p.rows + 1) & ~1;
+    a.lse2[(static_cast<int64_t>(e.b) * a.c.Hkv + c) * even + m] = lse2;
+  }
+}
+__device__ __forceinline__ void store_out(const CacheAttnArgs& a, const Entry& e, int c, int m,
+                                          int dim, float4 v) {
+  int t, h;
+  row_of(a, e, c, m, &t, &h);
+  const int64_t at = ((static_cast<int64_t>(e.b) * a.T + t) * a.Hq + h) * a.c.d + dim;
+  if (!MSA_IN_RANGE(at, 4, static_cast<int64_t>(a.s.batch) * a.T * a.Hq * a.c.d, a.status)) return;
+  if (a.out_bf16) {
+    __nv_bfloat162 x = __floats2bfloat162_rn(v.x, v.y), y = __floats2bfloat162_rn(v.z, v.w);
+    uint2 w;
+    w.x = *reinterpret_cast<uint32_t*>(&x);
+    w.y = *reinterpret_cast<uint32_t*>(&y);
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at) = w;
+  } else {
+    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = v;
+  }
+}
+
+// Joins the warps' sums of a unit's range and writes them.  osum rows are
+// padded by 4 floats.
+template <int D, int kTile>
+__device__ __forceinline__ void join_warps(const CacheAttnArgs& a, const Plan& p, const Entry& e,
+                                           int c, int rt, const float* osum, const Stat* stat,
+                                           bool whole, int64_t slot) {
+  constexpr int kLd = D + 4;
+  for (int i = threadIdx.x; i < kTile * (D / 4); i += kThreads) {
+    const int r = i / (D / 4), dim = (i - r * (D / 4)) * 4;
+    const int m = rt * kTile + r;
+    if (m >= p.rows) break;
+    float mx = -INFINITY, M = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      mx = fmaxf(mx, stat[w * kTile + r].m);
+      M = fmaxf(M, stat[w * kTile + r].M);
+    }
+    mx = finite_or_0(mx);
+    M = finite_or_0(M);
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const Stat& s = stat[w * kTile + r];
+      if (s.m == -INFINITY && s.l == 0.f) continue;
+      l += s.l * ex2(s.m - mx);
+      const float f = ex2(finite_or_0(s.M) - M);
+      const float4 x = *reinterpret_cast<const float4*>(osum + (w * kTile + r) * kLd + dim);
+      v.x += x.x * f;
+      v.y += x.y * f;
+      v.z += x.z * f;
+      v.w += x.w * f;
+    }
+    // l == 0: no slot attended.
+    const float f = l == 0.f ? 0.f : ex2(M - mx) / l;
+    const float lse2 = l == 0.f ? -INFINITY : mx + log2f(l);
+    v.x *= f;
+    v.y *= f;
+    v.z *= f;
+    v.w *= f;
+    if (whole) {
+      store_out(a, e, c, m, dim, v);
+      if (dim == 0) store_lse(a, p, e, c, m, lse2);
+    } else {
+      *reinterpret_cast<float4*>(a.o_part + (slot * kTile + r) * D + dim) = v;
+      if (dim == 0) a.lse_part[slot * kTile + r] = lse2;
+    }
+  }
+}
+
+// ---- the bodies ------------------------------------------------------------
+
+// Tensor cores: 8 * kNt query rows.
+template <int D, int kNt>
+struct MmaBody {
+  static constexpr int kTile = 8 * kNt;
+  static constexpr int kPerSm = kNt == 1 ? 3 : 2;
+  static constexpr int kKs = D / 16;   // k-steps over d
+  static constexpr int kMt = D / 16;   // 16-row tiles of O^T
+  static constexpr int kKw = D / 16;   // words of a K row a lane holds
+  static constexpr int kVw = D / 32;   // words of a V row a lane holds
+
+  uint32_t q[kKs][kNt][2];
+  float qs[kNt][2];   // score scale of rows 2t, 2t+1 (log2 units)
+  float o[kMt][kNt][4];
+  float m[kNt][2], l[kNt][2], M[kNt][2];
+
+  __device__ __forceinline__ void begin(const CacheAttnArgs& a, const Plan& p, const Entry& e,
+                                        int c, int rt, uint8_t*) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+#pragma unroll
+    for (int n = 0; n < kNt; ++n) {
+      // The lane's pieces of row 8n + g: d = 64 hf + 16 t4 + 0..15.
+      const int row = rt * kTile + 8 * n + g;
+      float v[kKw * 4];
+      float mx = 0.f;
+#pragma unroll
+      for (int i = 0; i < kKw * 4; ++i) v[i] = 0.f;
+      if (row < p.rows) {
+        int t, h;
+        row_of(a, e, c, row, &t, &h);
+        const uint16_t* src = static_cast<const uint16_t*>(a.q) +
+                              ((static_cast<int64_t>(e.b) * a.T + t) * a.Hq + h) * D;
+#pragma unroll
+        for (int hf = 0; hf < D / 64; ++hf)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint4 x = *reinterpret_cast<const uint4*>(src + 64 * hf + 16 * t4 + 8 * k);
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              v[16 * hf + 8 * k + 2 * i] = __uint_as_float(w[i] << 16);
+              v[16 * hf + 8 * k + 2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < kKw * 4; ++i) mx = fmaxf(mx, fabsf(v[i]));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      // 2^k brings the row's largest magnitude to [2^14, 2^15).
+      int k = mx > 0.f ? 14 + 127 - static_cast<int>(__float_as_uint(mx) >> 23) : 0;
+      k = k > 100 ? 100 : k;
+      const float up = pow2i(k);
+#pragma unroll
+      for (int s = 0; s < kKs; ++s) {
+        q[s][n][0] = half2_of(v[4 * s] * up, v[4 * s + 1] * up);
+        q[s][n][1] = half2_of(v[4 * s + 2] * up, v[4 * s + 3] * up);
+      }
+      const float mine = a.scale * kLog2e * pow2i(-k);
+      qs[n][0] = __shfl_sync(0xffffffffu, mine, 8 * t4);
+      qs[n][1] = __shfl_sync(0xffffffffu, mine, 8 * t4 + 4);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        m[n][r] = M[n][r] = -INFINITY;
+        l[n][r] = 0.f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kMt; ++i)
+#pragma unroll
+      for (int n = 0; n < kNt; ++n)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[i][n][k] = 0.f;
+  }
+
+  uint32_t kw[2][2][kKw];   // [16-slot step][slot g / g + 8][word]
+  uint32_t vw[2][4][kVw];   // [16-slot step][slot 2t, 2t+1, 2t+8, 2t+9][word]
+
+  __device__ __forceinline__ void load_k(const CacheAttnArgs& a, const Chunk& x) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+    const uint8_t* base = a.c.k_codes + x.at * D;
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int hf = 0; hf < D / 64; ++hf) {
+          const uint4 w = __ldg(reinterpret_cast<const uint4*>(
+              base + (16 * s + 8 * r + g) * D + 64 * hf + 16 * t4));
+          kw[s][r][4 * hf] = w.x;
+          kw[s][r][4 * hf + 1] = w.y;
+          kw[s][r][4 * hf + 2] = w.z;
+          kw[s][r][4 * hf + 3] = w.w;
+        }
+  }
+  __device__ __forceinline__ void load_v(const CacheAttnArgs& a, const Chunk& x) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+    const uint8_t* base = a.c.v_codes + x.at * D;
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const uint8_t* at = base + (16 * s + 8 * (r >> 1) + 2 * t4 + (r & 1)) * D + g * (D / 8);
+        if constexpr (D == 128) {
+          const uint4 w = __ldg(reinterpret_cast<const uint4*>(at));
+          vw[s][r][0] = w.x;
+          vw[s][r][1] = w.y;
+          vw[s][r][2] = w.z;
+          vw[s][r][3] = w.w;
+        } else {
+          const uint2 w = __ldg(reinterpret_cast<const uint2*>(at));
+          vw[s][r][0] = w.x;
+          vw[s][r][1] = w.y;
+        }
+      }
+  }
+
+  float s[2][kNt][4];
+
+  __device__ __forceinline__ void scores() {
+#pragma unroll
+    for (int st = 0; st < 2; ++st) {
+#pragma unroll
+      for (int n = 0; n < kNt; ++n)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[st][n][k] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < kKs; ++ks) {
+        const uint32_t fa[4] = {e4m3x2_to_half2(static_cast<uint16_t>(kw[st][0][ks])),
+                                e4m3x2_to_half2(static_cast<uint16_t>(kw[st][1][ks])),
+                                e4m3x2_to_half2(static_cast<uint16_t>(kw[st][0][ks] >> 16)),
+                                e4m3x2_to_half2(static_cast<uint16_t>(kw[st][1][ks] >> 16))};
+#pragma unroll
+        for (int n = 0; n < kNt; ++n) mma16816(s[st][n], fa, q[ks][n][0], q[ks][n][1]);
+      }
+    }
+  }
+
+  // Softmax of the chunk's scores into halves p[step][nt][b0, b1], and the
+  // running sums.  kEdge: some slot is masked for some row.
+  uint32_t pf[2][kNt][2];
+
+  template <bool kEdge>
+  __device__ __forceinline__ void softmax(const CacheAttnArgs& a, const Plan& p, const Entry& e,
+                                          int c, int rt, const Chunk& x) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+    const float lvs = log2_scale(x.vs);
+#pragma unroll
+    for (int n = 0; n < kNt; ++n) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float f = qs[n][r] * x.ks;
+        int pos = 0;
+        if (kEdge) {
+          int t, h;
+          row_of(a, e, c, min(rt * kTile + 8 * n + 2 * t4 + r, p.rows - 1), &t, &h);
+          pos = e.len - a.T + t;
+        }
+#pragma unroll
+        for (int st = 0; st < 2; ++st)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float& y = s[st][n][2 * k + r];
+            y *= f;
+            if (kEdge) {
+              const int key = x.key0 + 16 * st + 8 * k + g;
+              if (!x.on || (x.window && (key > pos || pos - key >= a.window))) y = -INFINITY;
+            }
+          }
+      }
+      if (a.weights) {
+        // Scores for the weights pass: [slot][row], rows padded to even.
+        const int even = (p.rows + 1) & ~1;
+        const int row = rt * kTile + 8 * n + 2 * t4;
+        if (row < even) {
+          const int64_t slots = static_cast<int64_t>(a.s.max_blocks) * a.c.block;
+          float* to = a.scores + ((static_cast<int64_t>(e.b) * a.c.Hkv + c) * slots + x.key0) * even;
+#pragma unroll
+          for (int st = 0; st < 2; ++st)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              *reinterpret_cast<float2*>(to + static_cast<int64_t>(16 * st + 8 * k + g) * even +
+                                         row) =
+                  make_float2(s[st][n][2 * k], s[st][n][2 * k + 1]);
+        }
+      }
+      float pv[2][4];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float mx = fmaxf(fmaxf(s[0][n][r], s[0][n][2 + r]), fmaxf(s[1][n][r], s[1][n][2 + r]));
+        // The denominator: the lane's own slots, its own maximum.
+        const float mn = fmaxf(m[n][r], mx), mu = finite_or_0(mn);
+        float sum = 0.f;
+#pragma unroll
+        for (int st = 0; st < 2; ++st)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) sum += ex2(s[st][n][2 * k + r] - mu);
+        l[n][r] = l[n][r] * ex2(m[n][r] - mu) + sum;
+        m[n][r] = mn;
+        // The weights: one maximum for all lanes.
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+        const float Mn = fmaxf(M[n][r], mx + lvs);
+        if (Mn > M[n][r]) {
+          const float f = ex2(M[n][r] - Mn);
+#pragma unroll
+          for (int i = 0; i < kMt; ++i) {
+            o[i][n][r] *= f;
+            o[i][n][2 + r] *= f;
+          }
+          M[n][r] = Mn;
+        }
+        const float base = kPBits + lvs - finite_or_0(M[n][r]);
+#pragma unroll
+        for (int st = 0; st < 2; ++st)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float y = s[st][n][2 * k + r];
+            const float w = ex2(y + base);
+            pv[st][2 * k + r] = kEdge && y == -INFINITY ? 0.f : w;
+          }
+      }
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {
+        pf[st][n][0] = transpose8x8(half2_of(pv[st][0], pv[st][1]));
+        pf[st][n][1] = transpose8x8(half2_of(pv[st][2], pv[st][3]));
+      }
+    }
+  }
+
+  // A slot no row may attend holds anything, NaN codes too: its weight is 0,
+  // its value must be as well.
+  __device__ __forceinline__ void clear_masked(const Chunk& x, int first, int last) {
+    const int t4 = threadIdx.x & 3;
+#pragma unroll
+    for (int st = 0; st < 2; ++st)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int key = x.key0 + 16 * st + 8 * (r >> 1) + 2 * t4 + (r & 1);
+        if (!x.on || (x.window && (key < first || key > last))) {
+#pragma unroll
+          for (int w = 0; w < kVw; ++w) vw[st][r][w] = 0u;
+        }
+      }
+  }
+
+  __device__ __forceinline__ void values() {
+#pragma unroll
+    for (int st = 0; st < 2; ++st) {
+      // Row index g of m-tile i is dim (D/8) g + i, index g + 8 is dim
+      // (D/8) g + D/16 + i: byte i and byte i + D/16 of the lane's piece.
+#pragma unroll
+      for (int w = 0; w < kVw / 2; ++w) {
+        const int w2 = w + kVw / 2;
+        uint32_t f01[2][2], f23[2][2];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const uint32_t sel = half ? 0x7362u : 0x5140u;
+          f01[0][half] = __byte_perm(vw[st][0][w], vw[st][1][w], sel);
+          f01[1][half] = __byte_perm(vw[st][0][w2], vw[st][1][w2], sel);
+          f23[0][half] = __byte_perm(vw[st][2][w], vw[st][3][w], sel);
+          f23[1][half] = __byte_perm(vw[st][2][w2], vw[st][3][w2], sel);
+        }
+#pragma unroll
+        for (int byte = 0; byte < 4; ++byte) {
+          const int half = byte >> 1, sh = (byte & 1) * 16;
+          const uint32_t fa[4] = {e4m3x2_to_half2(static_cast<uint16_t>(f01[0][half] >> sh)),
+                                  e4m3x2_to_half2(static_cast<uint16_t>(f01[1][half] >> sh)),
+                                  e4m3x2_to_half2(static_cast<uint16_t>(f23[0][half] >> sh)),
+                                  e4m3x2_to_half2(static_cast<uint16_t>(f23[1][half] >> sh))};
+#pragma unroll
+          for (int n = 0; n < kNt; ++n)
+            mma16816(o[4 * w + byte][n], fa, pf[st][n][0], pf[st][n][1]);
+        }
+      }
+    }
+  }
+
+  // The warp's sums to shared memory.
+  __device__ __forceinline__ void finish(float* osum, Stat* stat) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t4 = lane & 3;
+    constexpr int kLd = D + 4;
+#pragma unroll
+    for (int n = 0; n < kNt; ++n)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float mx = m[n][r];
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+        float sum = l[n][r] * ex2(m[n][r] - finite_or_0(mx));
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+        const int row = warp * kTile + 8 * n + 2 * t4 + r;
+        if (g == 0) stat[row] = Stat{mx, sum, M[n][r] - kPBits};
+        float* to = osum + row * kLd + g * (D / 8);
+#pragma unroll
+        for (int i = 0; i < kMt; ++i) {
+          to[i] = o[i][n][r];
+          to[D / 16 + i] = o[i][n][2 + r];
+        }
+      }
+  }
+
+  static constexpr int kSmemQ = 0;
+};
+
+// CUDA cores, fp32 throughout: 8 query rows, a lane a slot for the scores
+// and D/32 dims for the output.
+template <int D>
+struct SimtBody {
+  static constexpr int kTile = 8;
+  static constexpr int kPerSm = 3;
+  static constexpr int kDl = D / 32;
+  // q rows [8][D] for the CTA, then weights [32][8] for each warp
+  static constexpr int kSmemQ = (kTile * D + kWarps * kChunk * kTile) * 4;
+
+  float o[kTile][kDl];
+  float m[kTile], l[kTile], M[kTile];
+  float* qsm;
+  float* psm;
+
+  __device__ __forceinline__ void begin(const CacheAttnArgs& a, const Plan& p, const Entry& e,
+                                        int c, int rt, uint8_t* smem) {
+    qsm = reinterpret_cast<float*>(smem);
+    psm = qsm + kTile * D + (threadIdx.x >> 5) * kChunk * kTile;
+    __syncthreads();  // the last unit's rows are done with
+    for (int i = threadIdx.x; i < kTile * D; i += kThreads) {
+      const int r = i / D, row = rt * kTile + r;
+      float v = 0.f;
+      if (row < p.rows) {
+        int t, h;
+        row_of(a, e, c, row, &t, &h);
+        v = static_cast<const float*>(
+            a.q)[((static_cast<int64_t>(e.b) * a.T + t) * a.Hq + h) * D + (i - r * D)];
+      }
+      qsm[i] = v * (a.scale * kLog2e);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kTile; ++r) {
+      m[r] = M[r] = -INFINITY;
+      l[r] = 0.f;
+#pragma unroll
+      for (int k = 0; k < kDl; ++k) o[r][k] = 0.f;
+    }
+  }
+
+  __device__ __forceinline__ void chunk(const CacheAttnArgs& a, const Plan& p, const Entry& e,
+                                        int c, int rt, const Chunk& x) {
+    const int lane = threadIdx.x & 31;
+    const uint8_t* krow = a.c.k_codes + (x.at + lane) * D;
+    float s[kTile];
+#pragma unroll
+    for (int r = 0; r < kTile; ++r) s[r] = 0.f;
+#pragma unroll 2
+    for (int d0 = 0; d0 < D; d0 += 16) {
+      const uint4 w4 = __ldg(reinterpret_cast<const uint4*>(krow + d0));
+      const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+      float kf[16];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) e4m3x4_to_float(w[i], kf + 4 * i);
+#pragma unroll
+      for (int r = 0; r < kTile; ++r)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 qv = *reinterpret_cast<const float4*>(qsm + r * D + d0 + 4 * i);
+          s[r] = fmaf(qv.x, kf[4 * i], s[r]);
+          s[r] = fmaf(qv.y, kf[4 * i + 1], s[r]);
+          s[r] = fmaf(qv.z, kf[4 * i + 2], s[r]);
+          s[r] = fmaf(qv.w, kf[4 * i + 3], s[r]);
+        }
+    }
+    const int key = x.key0 + lane;
+    const float lvs = log2_scale(x.vs);
+    bool any = false;
+#pragma unroll
+    for (int r = 0; r < kTile; ++r) {
+      const int row = min(rt * kTile + r, p.rows - 1);
+      int t, h;
+      row_of(a, e, c, row, &t, &h);
+      const int pos = e.len - a.T + t;
+      const bool in = x.on && (!x.window || (key <= pos && pos - key < a.window));
+      any |= in;
+      s[r] = in ? s[r] * x.ks : -INFINITY;
+    }
+    if (a.weights) {
+      const int even = (p.rows + 1) & ~1;
+      const int64_t slots = static_cast<int64_t>(a.s.max_blocks) * a.c.block;
+      float* to = a.scores +
+                  ((static_cast<int64_t>(e.b) * a.c.Hkv + c) * slots + key) * even + rt * kTile;
+#pragma unroll
+      for (int r = 0; r < kTile; ++r)
+        if (rt * kTile + r < even) to[r] = s[r];
+    }
+    float pw[kTile];
+#pragma unroll
+    for (int r = 0; r < kTile; ++r) {
+      const float mn = fmaxf(m[r], s[r]), mu = finite_or_0(mn);
+      l[r] = l[r] * ex2(m[r] - mu) + ex2(s[r] - mu);
+      m[r] = mn;
+      float mx = s[r];
+#pragma unroll
+      for (int x2 = 16; x2 > 0; x2 >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x2));
+      const float Mn = fmaxf(M[r], mx + lvs);
+      if (Mn > M[r]) {
+        const float f = ex2(M[r] - Mn);
+#pragma unroll
+        for (int k = 0; k < kDl; ++k) o[r][k] *= f;
+        M[r] = Mn;
+      }
+      pw[r] = s[r] == -INFINITY ? 0.f : ex2(s[r] + lvs - finite_or_0(M[r]));
+    }
+    __syncwarp();
+    *reinterpret_cast<float4*>(psm + lane * kTile) = make_float4(pw[0], pw[1], pw[2], pw[3]);
+    *reinterpret_cast<float4*>(psm + lane * kTile + 4) = make_float4(pw[4], pw[5], pw[6], pw[7]);
+    const uint32_t held = __ballot_sync(0xffffffffu, any);
+    __syncwarp();
+    const uint8_t* vbase = a.c.v_codes + x.at * D + lane * kDl;
+#pragma unroll 8
+    for (int j = 0; j < kChunk; ++j) {
+      float vf[kDl];
+      if constexpr (D == 128) {
+        uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(vbase + j * D));
+        w = held >> j & 1 ? w : 0u;  // a masked slot holds anything
+        e4m3x4_to_float(w, vf);
+      } else {
+        uint16_t w = __ldg(reinterpret_cast<const uint16_t*>(vbase + j * D));
+        w = held >> j & 1 ? w : static_cast<uint16_t>(0);
+        const float2 f = e4m3x2_to_float2(w);
+        vf[0] = f.x;
+        vf[1] = f.y;
+      }
+      const float4 p0 = *reinterpret_cast<const float4*>(psm + j * kTile);
+      const float4 p1 = *reinterpret_cast<const float4*>(psm + j * kTile + 4);
+      const float pr[kTile] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
+#pragma unroll
+      for (int r = 0; r < kTile; ++r)
+#pragma unroll
+        for (int k = 0; k < kDl; ++k) o[r][k] = fmaf(pr[r], vf[k], o[r][k]);
+    }
+  }
+
+  __device__ __forceinline__ void finish(float* osum, Stat* stat) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int kLd = D + 4;
+#pragma unroll
+    for (int r = 0; r < kTile; ++r) {
+      float mx = m[r];
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+      float sum = l[r] * ex2(m[r] - finite_or_0(mx));
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+      if (lane == 0) stat[warp * kTile + r] = Stat{mx, sum, M[r]};
+#pragma unroll
+      for (int k = 0; k < kDl; ++k) osum[(warp * kTile + r) * kLd + lane * kDl + k] = o[r][k];
+    }
+  }
+};
+
+template <class Body>
+struct IsMma {
+  static constexpr bool value = false;
+};
+template <int D, int kNt>
+struct IsMma<MmaBody<D, kNt>> {
+  static constexpr bool value = true;
+};
+
+template <int D, class Body>
+__global__ void __launch_bounds__(kThreads, Body::kPerSm) cache_attn_kernel(const CacheAttnArgs a) {
+  constexpr int kTile = Body::kTile;
+  __shared__ int64_t scan[kWarps];
+  __shared__ int64_t found[2];
+  __shared__ __align__(16) float osum[kWarps * kTile * (D + 4)];
+  __shared__ Stat stat[kWarps * kTile];
+  __shared__ __align__(16) uint8_t extra[Body::kSmemQ > 0 ? Body::kSmemQ : 16];
+
+  const Plan p = plan_of(a, kTile);
+  const int64_t W = total_chunks(a, p, scan) * p.units;
+  if (W == 0) return;
+  const int64_t P = cta_count(a, W);
+  if (blockIdx.x >= P) return;
+  const int64_t begin = cta_begin(blockIdx.x, W, P), end = cta_begin(blockIdx.x + 1, W, P);
+
+  // The entry that holds chunk `begin`, and its first chunk.
+  {
+    int64_t before = 0;
+    for (int i0 = 0; i0 < p.n_entries; i0 += kThreads) {
+      const int i = i0 + threadIdx.x;
+      const int64_t x = i < p.n_entries ? entry_at(a, i).n_chunks * p.units : 0;
+      int64_t total;
+      const int64_t upto = before + block_scan(x, scan, &total);
+      if (begin >= upto - x && begin < upto) {
+        found[0] = i;
+        found[1] = upto - x;
+      }
+      before += total;
+      if (before > begin) break;
+    }
+    __syncthreads();
+  }
+  int i = static_cast<int>(found[0]);
+  int64_t base = found[1];  // first chunk of entry i
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+
+  Body body;
+  for (int64_t at = begin; at < end;) {
+    Entry e = entry_at(a, i);
+    while (at >= base + e.n_chunks * p.units) {
+      base += e.n_chunks * p.units;
+      e = entry_at(a, ++i);
+    }
+    const int u = static_cast<int>((at - base) / e.n_chunks);
+    const int64_t u0 = base + u * e.n_chunks;
+    const int64_t stop = min64(end, u0 + e.n_chunks);
+    const int c = u / p.n_tiles, rt = u - c * p.n_tiles;
+    // This CTA's chunks of the unit: [x0, x1) of its n_chunks.
+    const int x0 = static_cast<int>(at - u0), x1 = static_cast<int>(stop - u0);
+
+    body.begin(a, p, e, c, rt, extra);
+    if constexpr (IsMma<Body>::value) {
+      // Rows of this tile: query tokens t0..t1.
+      int t0, t1, h;
+      row_of(a, e, c, rt * kTile, &t0, &h);
+      row_of(a, e, c, min((rt + 1) * kTile, p.rows) - 1, &t1, &h);
+      const int first = e.len - a.T + t0 - a.window + 1;  // any row's first slot
+      const int last = e.len - a.T + t1;                  // and last
+      const int all0 = e.len - a.T + t1 - a.window + 1;   // every row's
+      const int all1 = e.len - a.T + t0;
+      int x = x0 + warp;
+      if (x < x1) {
+        Ahead ahead = look_ahead(a, e, c, x + lane * kWarps, x1);
+        int used = 0;
+        Chunk cur = chunk_of(ahead, 0);
+        body.load_k(a, cur);
+        body.load_v(a, cur);
+        for (; x < x1; x += kWarps) {
+          if (++used == 32) {
+            ahead = look_ahead(a, e, c, x + kWarps + lane * kWarps, x1);
+            used = 0;
+          }
+          const bool more = x + kWarps < x1;
+          const Chunk next = chunk_of(ahead, used);
+          body.scores();
+          if (more) body.load_k(a, next);
+          const bool edge = !cur.on || (cur.window && (cur.key0 < all0 || cur.key0 + kChunk - 1 > all1));
+          if (edge) {
+            body.template softmax<true>(a, p, e, c, rt, cur);
+            body.clear_masked(cur, first, last);
+          } else {
+            body.template softmax<false>(a, p, e, c, rt, cur);
+          }
+          body.values();
+          if (more) body.load_v(a, next);
+          cur = next;
+        }
+      }
+    } else {
+      int x = x0 + warp;
+      if (x < x1) {
+        Ahead ahead = look_ahead(a, e, c, x + lane * kWarps, x1);
+        int used = 0;
+        for (; x < x1; x += kWarps) {
+          const Chunk cur = chunk_of(ahead, used);
+          body.chunk(a, p, e, c, rt, cur);
+          if (++used == 32) {
+            ahead = look_ahead(a, e, c, x + kWarps + lane * kWarps, x1);
+            used = 0;
+          }
+        }
+      }
+    }
+    __syncthreads();
+    body.finish(osum, stat);
+    __syncthreads();
+    const bool whole = x0 == 0 && x1 == e.n_chunks;
+    join_warps<D, kTile>(a, p, e, c, rt, osum, stat, whole, 2 * static_cast<int64_t>(blockIdx.x) + (x0 == 0));
+    at = stop;
+  }
+}
+
+// Joins the parts of the units that several CTAs share, and writes the rows
+// that attend nothing.  One CTA a unit.
+template <int D, int kTile>
+__global__ void __launch_bounds__(kThreads) cache_attn_join_kernel(const CacheAttnArgs a) {
+  __shared__ int64_t scan[kWarps];
+  __shared__ int64_t found;
+  const Plan p = plan_of(a, kTile);
+  const int i = blockIdx.x / p.units, u = blockIdx.x - i * p.units;
+  const Entry e = entry_at(a, i);
+  const int c = u / p.n_tiles, rt = u - c * p.n_tiles;
+  const int rows = min(kTile, p.rows - rt * kTile);
+  if (e.n_chunks == 0) {
+    for (int k = threadIdx.x; k < rows * (D / 4); k += kThreads) {
+      const int r = k / (D / 4), dim = (k - r * (D / 4)) * 4;
+      store_out(a, e, c, rt * kTile + r, dim, make_float4(0.f, 0.f, 0.f, 0.f));
+      if (dim == 0) store_lse(a, p, e, c, rt * kTile + r, -INFINITY);
+    }
+    return;
+  }
+  const int64_t total = total_chunks(a, p, scan);
+  {
+    int64_t before = 0;
+    for (int i0 = 0; i0 <= i; i0 += kThreads) {
+      const int k = i0 + threadIdx.x;
+      const int64_t x = k < p.n_entries ? entry_at(a, k).n_chunks : 0;
+      int64_t sum;
+      const int64_t upto = before + block_scan(x, scan, &sum);
+      if (k == i) found = upto - x;
+      before += sum;
+    }
+    __syncthreads();
+  }
+  const int64_t W = total * p.units, P = cta_count(a, W);
+  const int64_t u0 = found * p.units + u * e.n_chunks;
+  const int64_t c0 = cta_of(u0, W, P), c1 = cta_of(u0 + e.n_chunks - 1, W, P);
+  if (c0 == c1) return;  // written whole
+  for (int k = threadIdx.x; k < rows * (D / 4); k += kThreads) {
+    const int r = k / (D / 4), dim = (k - r * (D / 4)) * 4;
+    float mx = -INFINITY;
+    for (int64_t x = c0; x <= c1; ++x)
+      mx = fmaxf(mx, a.lse_part[(2 * x + (x == c0)) * kTile + r]);
+    mx = finite_or_0(mx);
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+    for (int64_t x = c0; x <= c1; ++x) {
+      const int64_t s = (2 * x + (x == c0)) * kTile + r;
+      const float f = ex2(a.lse_part[s] - mx);
+      if (f == 0.f) continue;
+      const float4 y = *reinterpret_cast<const float4*>(a.o_part + s * D + dim);
+      l += f;
+      v.x += y.x * f;
+      v.y += y.y * f;
+      v.z += y.z * f;
+      v.w += y.w * f;
+    }
+    const float f = l == 0.f ? 0.f : 1.f / l;
+    v.x *= f;
+    v.y *= f;
+    v.z *= f;
+    v.w *= f;
+    store_out(a, e, c, rt * kTile + r, dim, v);
+    if (dim == 0) store_lse(a, p, e, c, rt * kTile + r, l == 0.f ? -INFINITY : mx + log2f(l));
+  }
+}
+
+// weights[b, c, j] += sum over the rows of KV head c of their probability of
+// slot j, from the scores the attention left.  A thread a slot: no atomics,
+// rows summed in order.
+__global__ void __launch_bounds__(256) cache_weights_kernel(const CacheAttnArgs a) {
+  extern __shared__ float lse[];
+  const int rows = a.T * (a.Hq / a.c.Hkv), even = (rows + 1) & ~1;
+  const int c = blockIdx.y % a.c.Hkv, b = blockIdx.y / a.c.Hkv;
+  const int64_t len = cache_len(a.s, b, a.c.block, a.status);
+  const int64_t j = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  const int64_t lo = max(0, static_cast<int>(len) - a.T - a.window + 1);
+  if (static_cast<int64_t>(blockIdx.x) * blockDim.x >= len) return;
+  const int64_t u = static_cast<int64_t>(b) * a.c.Hkv + c;
+  for (int r = threadIdx.x; r < rows; r += blockDim.x) lse[r] = a.lse2[u * even + r];
+  __syncthreads();
+  if (j < lo || j >= len) return;
+  const int64_t slots = static_cast<int64_t>(a.s.max_blocks) * a.c.block;
+  const float* s = a.scores + (u * slots + j) * even;
+  float sum = 0.f;
+  for (int r = 0; r < rows; r += 2) {
+    const float2 x = *reinterpret_cast<const float2*>(s + r);
+    // A row that attends nothing (lse -inf) has scores of -inf alone.
+    sum += x.x == -INFINITY ? 0.f : ex2(x.x - lse[r]);
+    if (r + 1 < rows) sum += x.y == -INFINITY ? 0.f : ex2(x.y - lse[r + 1]);
+  }
+  if (MSA_IN_RANGE(u * a.weights_ld + j, 1,
+                   static_cast<int64_t>(a.s.batch) * a.c.Hkv * a.weights_ld, a.status))
+    a.weights[u * a.weights_ld + j] += sum;
+}
+
+template <int D, class Body>
+cudaError_t launch_body(const CacheAttnArgs& a, cudaStream_t st) {
+  cache_attn_kernel<D, Body><<<a.n_ctas, kThreads, 0, st>>>(a);
+  cudaError_t e = cudaPeekAtLastError();
+  if (e != cudaSuccess) return e;
+  const int g = a.Hq / a.c.Hkv;
+  const int rows = a.sel ? g : a.T * g;
+  const int64_t units = static_cast<int64_t>(a.sel ? a.s.batch * a.T : a.s.batch) * a.c.Hkv *
+                        ((rows + Body::kTile - 1) / Body::kTile);
+  cache_attn_join_kernel<D, Body::kTile><<<static_cast<unsigned>(units), kThreads, 0, st>>>(a);
+  e = cudaPeekAtLastError();
+  if (e != cudaSuccess || !a.weights) return e;
+  const int64_t slots = static_cast<int64_t>(a.s.max_blocks) * a.c.block;
+  const dim3 grid(static_cast<unsigned>((slots + 255) / 256),
+                  static_cast<unsigned>(a.s.batch * a.c.Hkv));
+  cache_weights_kernel<<<grid, 256, rows * sizeof(float), st>>>(a);
+  return cudaPeekAtLastError();
+}
+
+}  // namespace
+
+int cache_attn_tile_rows(int rows, int in_bf16) { return in_bf16 && rows > 8 ? 16 : 8; }
+
+int cache_attn_max_ctas(int tile_rows, int in_bf16) {
+  return kSms * (in_bf16 ? (tile_rows == 8 ? MmaBody<128, 1>::kPerSm : MmaBody<128, 2>::kPerSm)
+                         : SimtBody<128>::kPerSm);
+}
+
+cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t st) {
+  const int g = a.Hq / a.c.Hkv;
+  const int tile = cache_attn_tile_rows(a.sel ? g : a.T * g, a.in_bf16);
+  if (!a.in_bf16)
+    return a.c.d == 128 ? launch_body<128, SimtBody<128>>(a, st)
+                        : launch_body<64, SimtBody<64>>(a, st);
+  if (tile == 8)
+    return a.c.d == 128 ? launch_body<128, MmaBody<128, 1>>(a, st)
+                        : launch_body<64, MmaBody<64, 1>>(a, st);
+  return a.c.d == 128 ? launch_body<128, MmaBody<128, 2>>(a, st)
+                      : launch_body<64, MmaBody<64, 2>>(a, st);
+}
+
+}  // namespace msa

@@ -169,6 +169,12 @@ msa_status topk_forward(const void* q, const void* k, const void* v, void* out, 
 
 }  // namespace
 
+namespace msa {
+msa_status api_error(msa_status st, const char* message) { return fail(st, "%s", message); }
+msa_status api_ok() { return ok(); }
+msa_status api_status_word(int** out) { return device_status_ptr(out); }
+}  // namespace msa
+
 // Fixed per-device scratch of msa_attn_fwd_topk_noalloc: the block-mean
 // keys, the selection and its counts of one call, laid out as the caller
 // workspace of msa_attn_fwd_topk.  Nothing in it needs to start at zero:

@@ -25,7 +25,8 @@ def __getattr__(name):
     if name in ("KVCache", "cache_append", "cache_attention", "cache_block_select",
                 "cache_topk_attention", "cache_evict"):
         from . import cache
-        return getattr(cache, name)
+        # Bound once: a decoding step should not pay for the lookup again.
+        return globals().setdefault(name, getattr(cache, name))
     if name == "binding":
         from . import _binding
         return _binding

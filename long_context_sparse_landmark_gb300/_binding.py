@@ -453,13 +453,27 @@ def lse_merge(o_parts, lse_parts, out, lse, stream=None) -> None:
 
 
 # -- the 8-bit KV cache ------------------------------------------------------
-# `cache` is a KvCacheStruct; table [batch, max_blocks] and lens [batch] are
-# int32 tensors.
+# `cache` is a KvCacheStruct (or a reference to one); table [batch, max_blocks]
+# and lens [batch] are int32 tensors.  `stream` is a torch stream, the address
+# of a CUDA stream, or None for the current one.  A decoding step is a few
+# microseconds of GPU work, so these pass plain integers to ctypes.
+
+def _raw_stream(stream) -> int:
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _addr(t) -> int:
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError("tensors must be contiguous and on a CUDA device")
+    return t.data_ptr()
+
 
 def _i32ptr(t, what):
     if t.dtype != torch.int32:
         raise TypeError(f"{what} must be int32")
-    return _ptr(t)
+    return _addr(t)
 
 
 def _f32ptr(t, what):
@@ -467,7 +481,7 @@ def _f32ptr(t, what):
         return None
     if t.dtype != torch.float32:
         raise TypeError(f"{what} must be float32")
-    return _ptr(t)
+    return _addr(t)
 
 
 def _ws_size(n: int, what: str) -> int:
@@ -478,9 +492,9 @@ def _ws_size(n: int, what: str) -> int:
 
 def cache_append(cache, k, v, cu, max_new: int, table, lens, stream=None) -> None:
     """msa_cache_append: rows cu[b]..cu[b+1] of k, v become sequence b's last slots."""
-    _check(_lib.msa_cache_append(cache, _ptr(k), _ptr(v), _i32ptr(cu, "cu"), k.shape[0],
+    _check(_lib.msa_cache_append(cache, _addr(k), _addr(v), _i32ptr(cu, "cu"), k.shape[0],
                                  int(max_new), _i32ptr(table, "table"), table.shape[1],
-                                 _i32ptr(lens, "lens"), table.shape[0], _dt(k), _stream(stream)))
+                                 _i32ptr(lens, "lens"), table.shape[0], _dt(k), _raw_stream(stream)))
 
 
 def cache_attn_workspace_size(cache, max_blocks: int, batch: int, n_q: int, Hq: int,
@@ -494,12 +508,12 @@ def cache_attn(cache, q, table, lens, window: int, scale: float, out, lse, weigh
                stream=None) -> None:
     """msa_cache_attn: query tokens q [batch, n_q, Hq, d] over the cache."""
     b, n_q, Hq, _ = q.shape
-    _check(_lib.msa_cache_attn(cache, _ptr(q), _i32ptr(table, "table"), table.shape[1],
+    _check(_lib.msa_cache_attn(cache, _addr(q), _i32ptr(table, "table"), table.shape[1],
                                _i32ptr(lens, "lens"), b, n_q, Hq, int(window), float(scale),
-                               _ptr(out), _f32ptr(lse, "lse"), _f32ptr(weights, "weights"),
+                               _addr(out), _f32ptr(lse, "lse"), _f32ptr(weights, "weights"),
                                0 if weights is None else weights.shape[2], _dt(q), _dt(out),
-                               _ptr(workspace), workspace.numel() * workspace.element_size(),
-                               _stream(stream)))
+                               _addr(workspace), workspace.nbytes,
+                               _raw_stream(stream)))
 
 
 def cache_select_workspace_size(cache, max_blocks: int, batch: int, n_q: int) -> int:
@@ -511,11 +525,11 @@ def cache_select(cache, q, table, lens, window: int, top_k: int, sel, cnt, works
                  stream=None) -> None:
     """msa_cache_select: the top_k blocks of each query token and KV head."""
     b, n_q, Hq, _ = q.shape
-    _check(_lib.msa_cache_select(cache, _ptr(q), _i32ptr(table, "table"), table.shape[1],
+    _check(_lib.msa_cache_select(cache, _addr(q), _i32ptr(table, "table"), table.shape[1],
                                  _i32ptr(lens, "lens"), b, n_q, Hq, int(window), int(top_k),
                                  _i32ptr(sel, "sel"), _i32ptr(cnt, "cnt"), _dt(q),
-                                 _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                 _stream(stream)))
+                                 _addr(workspace), workspace.nbytes,
+                                 _raw_stream(stream)))
 
 
 def cache_attn_select_workspace_size(cache, max_blocks: int, batch: int, n_q: int, Hq: int,
@@ -530,10 +544,10 @@ def cache_attn_select(cache, q, table, lens, window: int, sel, cnt, scale: float
     """msa_cache_attn_select: window + the selected blocks."""
     b, n_q, Hq, _ = q.shape
     _check(_lib.msa_cache_attn_select(
-        cache, _ptr(q), _i32ptr(table, "table"), table.shape[1], _i32ptr(lens, "lens"), b, n_q,
+        cache, _addr(q), _i32ptr(table, "table"), table.shape[1], _i32ptr(lens, "lens"), b, n_q,
         Hq, int(window), _i32ptr(sel, "sel"), _i32ptr(cnt, "cnt"), sel.shape[3], float(scale),
-        _ptr(out), _f32ptr(lse, "lse"), _dt(q), _dt(out), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+        _addr(out), _f32ptr(lse, "lse"), _dt(q), _dt(out), _addr(workspace),
+        workspace.nbytes, _raw_stream(stream)))
 
 
 def cache_attn_topk_workspace_size(cache, max_blocks: int, batch: int, n_q: int, Hq: int,
@@ -547,12 +561,12 @@ def cache_attn_topk(cache, q, table, lens, window: int, top_k: int, scale: float
                     workspace, stream=None) -> None:
     """msa_cache_attn_topk: select and attend in one call."""
     b, n_q, Hq, _ = q.shape
-    _check(_lib.msa_cache_attn_topk(cache, _ptr(q), _i32ptr(table, "table"), table.shape[1],
+    _check(_lib.msa_cache_attn_topk(cache, _addr(q), _i32ptr(table, "table"), table.shape[1],
                                     _i32ptr(lens, "lens"), b, n_q, Hq, int(window), int(top_k),
-                                    float(scale), _ptr(out), _f32ptr(lse, "lse"), _dt(q),
-                                    _dt(out), _ptr(workspace),
-                                    workspace.numel() * workspace.element_size(),
-                                    _stream(stream)))
+                                    float(scale), _addr(out), _f32ptr(lse, "lse"), _dt(q),
+                                    _dt(out), _addr(workspace),
+                                    workspace.nbytes,
+                                    _raw_stream(stream)))
 
 
 def cache_evict(cache, table, lens, weights, dst_table, budget: int, recent: int, new_lens, kept,
@@ -564,4 +578,4 @@ def cache_evict(cache, table, lens, weights, dst_table, budget: int, recent: int
                                 int(recent), _i32ptr(dst_table, "dst_table"), dst_table.shape[1],
                                 _i32ptr(new_lens, "new_lens"), _i32ptr(kept, "kept"),
                                 _f32ptr(new_weights, "new_weights"), new_weights.shape[2],
-                                _stream(stream)))
+                                _raw_stream(stream)))

@@ -88,17 +88,17 @@ def _query(cache: KVCache, q: torch.Tensor, table: torch.Tensor):
 
 
 def _run(cache: KVCache, stream, call):
-    """call(stream) with the cache's device current and allocations made for
-    the stream that the kernels run on."""
-    if stream is None and torch.cuda.current_device() == cache.index:
-        return call(torch.cuda.current_stream())
-    if stream is not None and stream.device.index != cache.index:
+    """call(stream address) with the cache's device current and allocations
+    made for the stream that the kernels run on."""
+    if stream is None:
+        if torch.cuda.current_device() == cache.index:
+            return call(torch._C._cuda_getCurrentRawStream(cache.index))
+        with torch.cuda.device(cache.index):
+            return call(torch._C._cuda_getCurrentRawStream(cache.index))
+    if stream.device.index != cache.index:
         raise ValueError("stream and cache are on different devices")
-    with torch.cuda.device(cache.index):
-        if stream is None:
-            return call(torch.cuda.current_stream())
-        with torch.cuda.stream(stream):
-            return call(stream)
+    with torch.cuda.stream(stream):
+        return call(stream.cuda_stream)
 
 
 def cache_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor,

@@ -28,6 +28,7 @@ struct CacheView {
   __nv_bfloat16* k_mean;
   int64_t n_pages;
   int Hkv, d, block;
+  int lb;  // log2 of block
 };
 
 // Batch of sequences in a cache: table [batch][max_blocks] page of each
@@ -39,8 +40,11 @@ struct CacheBatch {
   int batch;
 };
 
+constexpr int kSms = 152;  // of a GB300: grids of persistent kernels
+
 // Keys a warp takes at a time; every block is a whole number of them.
-constexpr int kChunk = 32;
+constexpr int kChunkLog2 = 5;
+constexpr int kChunk = 1 << kChunkLog2;
 
 // Length of sequence b, clamped to what its table row can hold.
 __device__ __forceinline__ int cache_len(const CacheBatch& s, int b, int block, int* status) {
@@ -99,6 +103,38 @@ __device__ __forceinline__ float pow2i(int e) {  // -126 <= e <= 127
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
+// A kernel of a chain starts while the one before it drains: what it does
+// before this call must not depend on that kernel.  The wait ends when the
+// kernel before has finished and its writes are visible, so every kernel of
+// a chain makes it on every path, before it exits; without a kernel to wait
+// for it returns at once.
+__device__ __forceinline__ void wait_for_inputs() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// Lets the next kernel of a chain start as soon as every CTA of this one has.
+__device__ __forceinline__ void let_next_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Launches a kernel; with `chained`, as the dependent of the kernel that the
+// same call has just put on the stream (programmatic stream serialization).
+template <typename... Params, typename... Args>
+inline cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, size_t smem,
+                                cudaStream_t st, bool chained, const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = chained ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Launchers of the cache kernels (return the launch's cudaError_t).
 struct AppendArgs {
   CacheView c;
@@ -107,6 +143,7 @@ struct AppendArgs {
   const void* v;
   const int32_t* cu;  // [batch + 1] rows of each sequence's new tokens
   int64_t total, max_new;
+  uint32_t blocks;  // blocks that a range of max_new tokens can touch
   int bf16;
   int* status;
 };
@@ -134,6 +171,7 @@ struct CacheAttnArgs {
   float* lse;  // [batch, Hq, T]
   const int32_t* sel;  // [batch, T, Hkv, top_k], null: dense
   const int32_t* cnt;  // [batch, T, Hkv]
+  int sel_from_kernel;  // sel was put on the stream just before, by the same call
   int top_k;
   float* weights;  // [batch, Hkv, weights_ld], null: none
   int64_t weights_ld;

@@ -4,12 +4,15 @@
 // gathers them into fresh blocks.
 //
 // One cluster of CTAs a (sequence, KV head), each with a contiguous part of
-// the slots: a radix selection of the least kept weight by bytes (histograms
-// in shared memory, joined through the cluster's), then one pass that counts
-// and one that writes the kept slots in order.  Weights compare as they are:
-// the choice is exact.  The weights are read once from HBM and again, twice
-// to five times more, from L2: 4 bytes a slot, against the 2 d bytes a kept
-// slot costs in the gather.
+// the slots, whose keys its threads keep in registers: a radix selection of
+// the least kept weight by 11 + 11 + 10 bits (histograms in shared memory,
+// joined through the cluster's), then one pass of ballots that puts the kept
+// slots in order.  Weights compare as they are: the choice is exact.  The
+// first digit is sign, exponent and two bits of the mantissa, so that weights
+// of a few binades do not all meet at a few counters.  The weights are read
+// once (parts too long for the registers: once a digit, from L2): 4 bytes a
+// slot, against the 2 d bytes a kept slot costs in the gather; what bounds a
+// call is the chain of some ten barriers.
 #include <math.h>
 
 #include <cooperative_groups.h>
@@ -24,6 +27,7 @@ namespace {
 constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kClusterMax = 8;
+constexpr int kBins = 2048;
 
 // Unsigned key that orders as the weight does; -0 as +0, NaN above all.
 __device__ __forceinline__ uint32_t weight_key(float x) {
@@ -32,12 +36,15 @@ __device__ __forceinline__ uint32_t weight_key(float x) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+// kKeys keys a thread: warp w of CTA r has the slots from r * per + w * 32 *
+// kKeys on, lane by lane.  kKeys = 0: any number, read again for each pass.
+template <int kKeys>
 __global__ void __launch_bounds__(kEvictThreads) cache_evict_kernel(const EvictArgs a) {
-  __shared__ int hist[256];
-  __shared__ int total[256];
+  __shared__ __align__(16) int hist[kBins];
   __shared__ int digit, left_s;
   __shared__ int counts[2];  // this CTA's slots above the least kept weight, and equal to it
   __shared__ int wsum[2][kEvictWarps];
+  let_next_start();
   cg::cluster_group cl = cg::this_cluster();
   const int ranks = static_cast<int>(cl.num_blocks()), rank = static_cast<int>(cl.block_rank());
   const int u = blockIdx.x / ranks;
@@ -51,8 +58,42 @@ __global__ void __launch_bounds__(kEvictThreads) cache_evict_kernel(const EvictA
   const float* w = a.weights + static_cast<int64_t>(u) * a.weights_ld;
   int32_t* out = a.kept + static_cast<int64_t>(u) * a.budget;
   float* out_w = a.new_weights + static_cast<int64_t>(u) * a.new_ld;
-  const int per = (n + ranks - 1) / ranks;
-  const int i0 = min(n, rank * per), i1 = min(n, i0 + per);
+  // The warp's slots [i0, i1), a multiple of 32 apart from the last.
+  int i0, i1;
+  if constexpr (kKeys > 0) {
+    i0 = min(n, (rank * kEvictWarps + warp) * 32 * kKeys);
+    i1 = min(n, i0 + 32 * kKeys);
+  } else {
+    const int warps = ranks * kEvictWarps;
+    const int per = ((n + warps - 1) / warps + 31) & ~31;
+    const int64_t from = static_cast<int64_t>(rank * kEvictWarps + warp) * per;
+    i0 = static_cast<int>(min64(n, from));
+    i1 = static_cast<int>(min64(n, from + per));
+  }
+
+  const bool all = need == n;
+  const bool pick = need > 0 && !all;  // the same for the whole cluster
+  float x[kKeys > 0 ? kKeys : 1];
+  if constexpr (kKeys > 0) {
+#pragma unroll
+    for (int k = 0; k < kKeys; ++k) {
+      const int i = i0 + 32 * k + lane;
+      x[k] = i < i1 ? w[i] : 0.f;
+    }
+  }
+  // Calls f(slot or -1, weight) for the warp's slots in order, 32 at a time.
+  const auto each = [&](auto f) {
+    if constexpr (kKeys > 0) {
+#pragma unroll
+      for (int k = 0; k < kKeys; ++k) {
+        if (i0 + 32 * k >= i1) break;
+        const int i = i0 + 32 * k + lane;
+        f(i < i1 ? i : -1, x[k]);
+      }
+    } else {
+      for (int i = i0 + lane; i - lane < i1; i += 32) f(i < i1 ? i : -1, i < i1 ? w[i] : 0.f);
+    }
+  };
 
   if (rank == 0 && threadIdx.x == 0 && h == 0) a.new_lens[b] = kept;
   // Past the kept: -1 and 0.
@@ -69,131 +110,129 @@ __global__ void __launch_bounds__(kEvictThreads) cache_evict_kernel(const EvictA
 
   uint32_t prefix = 0, mask = 0;
   int left = need;
-  if (need > 0 && need < n) {  // the same for the whole cluster
-    for (int byte = 3; byte >= 0; --byte) {
-      for (int i = threadIdx.x; i < 256; i += kEvictThreads) hist[i] = 0;
+  if (pick) {
+#pragma unroll
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+      const uint32_t bits = pass == 2 ? 0x3ffu : 0x7ffu;
+      *reinterpret_cast<int4*>(hist + 4 * threadIdx.x) = make_int4(0, 0, 0, 0);
       __syncthreads();
-      for (int i = i0 + threadIdx.x; i < i1; i += kEvictThreads) {
-        const uint32_t k = weight_key(w[i]);
-        if ((k & mask) == prefix) atomicAdd(&hist[(k >> (8 * byte)) & 255], 1);
-      }
+      each([&](int i, float v) {
+        const uint32_t k = weight_key(v);
+        if (i >= 0 && (k & mask) == prefix) atomicAdd(&hist[(k >> shift) & bits], 1);
+      });
       cl.sync();
-      if (threadIdx.x < 256) {
-        int s = 0;
-        for (int r = 0; r < ranks; ++r) s += cl.map_shared_rank(hist, r)[threadIdx.x];
-        total[threadIdx.x] = s;
+      // Thread t sums the bins 4 * (511 - t) + 3 .. + 0 of all ranks: the
+      // threads' order is that of falling keys.
+      const int at = 4 * (kEvictThreads - 1 - threadIdx.x);
+      int4 s = *reinterpret_cast<const int4*>(hist + at);
+      for (int r = 1; r < ranks; ++r) {
+        const int4 y = *reinterpret_cast<const int4*>(
+            cl.map_shared_rank(hist, rank + r < ranks ? rank + r : rank + r - ranks) + at);
+        s.x += y.x;
+        s.y += y.y;
+        s.z += y.z;
+        s.w += y.w;
       }
-      __syncthreads();
-      if (threadIdx.x < 32) {
-        int s = 0;
+      const int mine = s.x + s.y + s.z + s.w;
+      int upto = mine;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s += total[255 - 8 * threadIdx.x - i];
-        int upto = s;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+      }
+      if (lane == 31) wsum[0][warp] = upto;
+      // Also: all ranks have read this histogram before any clears it.
+      cl.sync();
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, upto, o);
-          if (lane >= o) upto += y;
-        }
-        int before = upto - s;
-        if (before < left && left <= upto) {
-          for (int i = 0; i < 8; ++i) {
-            const int dgt = 255 - 8 * threadIdx.x - i;
-            if (left <= before + total[dgt]) {
-              digit = dgt;
-              left_s = left - before;
-              break;
-            }
-            before += total[dgt];
+      for (int v = 0; v < kEvictWarps; ++v) upto += v < warp ? wsum[0][v] : 0;
+      int before = upto - mine;
+      if (before < left && left <= upto) {
+        const int bin[4] = {s.w, s.z, s.y, s.x};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (before < left && left <= before + bin[k]) {
+            digit = at + 3 - k;
+            left_s = left - before;
           }
+          before += bin[k];
         }
       }
-      // All ranks have read this histogram before any clears it again.
-      cl.sync();
-      prefix |= static_cast<uint32_t>(digit) << (8 * byte);
-      mask |= 255u << (8 * byte);
+      __syncthreads();
+      prefix |= static_cast<uint32_t>(digit) << shift;
+      mask |= bits << shift;
       left = left_s;
     }
   }
-  const bool all = need == n;
-  // How many of this CTA's slots lie above the least kept weight, and at it.
+  // How many of this warp's slots lie above the least kept weight, and at it.
   int above = 0, equal = 0;
-  if (need > 0) {
-    for (int i = i0 + threadIdx.x; i < i1; i += kEvictThreads) {
-      const uint32_t k = weight_key(w[i]);
-      above += all || k > prefix;
-      equal += !all && k == prefix;
-    }
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    above += __shfl_xor_sync(0xffffffffu, above, o);
-    equal += __shfl_xor_sync(0xffffffffu, equal, o);
-  }
+  if (need > 0)
+    each([&](int i, float v) {
+      const uint32_t k = weight_key(v);
+      above += i >= 0 && (all || k > prefix);
+      equal += i >= 0 && !all && k == prefix;
+    });
+  above = __reduce_add_sync(0xffffffffu, above);
+  equal = __reduce_add_sync(0xffffffffu, equal);
+  __syncthreads();  // wsum is done with
   if (lane == 0) {
     wsum[0][warp] = above;
     wsum[1][warp] = equal;
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    int x = 0, y = 0;
-    for (int i = 0; i < kEvictWarps; ++i) {
-      x += wsum[0][i];
-      y += wsum[1][i];
+  int before_above = 0, before_equal = 0, t_above = 0, t_equal = 0;
+#pragma unroll
+  for (int v = 0; v < kEvictWarps; ++v) {
+    before_above += v < warp ? wsum[0][v] : 0;
+    before_equal += v < warp ? wsum[1][v] : 0;
+    t_above += wsum[0][v];
+    t_equal += wsum[1][v];
+  }
+  if (ranks > 1) {
+    if (threadIdx.x == 0) {
+      counts[0] = t_above;
+      counts[1] = t_equal;
     }
-    counts[0] = x;
-    counts[1] = y;
+    cl.sync();
+    for (int r = 0; r < rank; ++r) {
+      before_above += cl.map_shared_rank(counts, r)[0];
+      before_equal += cl.map_shared_rank(counts, r)[1];
+    }
+    cl.sync();  // no CTA leaves while another reads its counts
   }
-  cl.sync();
-  int before_above = 0, before_equal = 0;
-  for (int r = 0; r < rank; ++r) {
-    before_above += cl.map_shared_rank(counts, r)[0];
-    before_equal += cl.map_shared_rank(counts, r)[1];
-  }
-  cl.sync();  // no CTA leaves while another reads its counts
   if (need == 0) return;
   // `left` of the equal ones stay, the lowest slots first.  Position of a
   // kept slot: kept above before it, and kept equals before it.
-  for (int j0 = i0; j0 < i1; j0 += kEvictThreads) {
-    const int i = j0 + threadIdx.x;
-    const float x = i < i1 ? w[i] : 0.f;
-    const uint32_t k = weight_key(x);
-    const bool up = i < i1 && (all || k > prefix), eq = i < i1 && !all && k == prefix;
+  each([&](int i, float v) {
+    const uint32_t k = weight_key(v);
+    const bool up = i >= 0 && (all || k > prefix), eq = i >= 0 && !all && k == prefix;
     const uint32_t mu = __ballot_sync(0xffffffffu, up), me = __ballot_sync(0xffffffffu, eq);
-    if (lane == 0) {
-      wsum[0][warp] = __popc(mu);
-      wsum[1][warp] = __popc(me);
-    }
-    __syncthreads();
-    int au = before_above, ae = before_equal, tu = 0, te = 0;
-#pragma unroll
-    for (int v = 0; v < kEvictWarps; ++v) {
-      au += v < warp ? wsum[0][v] : 0;
-      ae += v < warp ? wsum[1][v] : 0;
-      tu += wsum[0][v];
-      te += wsum[1][v];
-    }
-    au += __popc(mu & ((1u << lane) - 1u));
-    ae += __popc(me & ((1u << lane) - 1u));
+    const int au = before_above + __popc(mu & ((1u << lane) - 1u));
+    const int ae = before_equal + __popc(me & ((1u << lane) - 1u));
     if (up || (eq && ae < left)) {
-      const int at = au + min(ae, all ? 0 : left);
+      const int at = au + min(ae, left);
       out[at] = i;
-      out_w[at] = x;
+      out_w[at] = v;
     }
-    before_above += tu;
-    before_equal += te;
-    __syncthreads();
-  }
+    before_above += __popc(mu);
+    before_equal += __popc(me);
+  });
 }
 
 }  // namespace
 
 cudaError_t launch_cache_evict_select(const EvictArgs& a, cudaStream_t st) {
+  // Keys in registers: 16 a thread up to 8192 slots in one CTA, 32 up to
+  // 16384 a CTA and clusters of 2, 4 and 8; longer rows are read four times.
+  const int64_t slots = static_cast<int64_t>(a.s.max_blocks) * a.c.block;
+  const int64_t per = 32 * kEvictThreads;
+  int ranks = 1;
+  while (ranks < kClusterMax && slots > ranks * per) ranks *= 2;
+  const auto kernel = slots <= per / 2       ? cache_evict_kernel<16>
+                      : slots <= ranks * per ? cache_evict_kernel<32>
+                                             : cache_evict_kernel<0>;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[1];
-  // A CTA reads 16K weights a pass in about a microsecond; more than that is
-  // split over a cluster.
-  const int64_t slots = static_cast<int64_t>(a.s.max_blocks) * a.c.block;
-  const int ranks = slots <= 16384 ? 1 : kClusterMax;
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = ranks;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
@@ -202,7 +241,7 @@ cudaError_t launch_cache_evict_select(const EvictArgs& a, cudaStream_t st) {
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_evict_kernel, a);
+  return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 }  // namespace msa

@@ -37,7 +37,6 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kSms = 152;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kPBits = 14.f;  // log2 of the largest half weight
@@ -66,10 +65,10 @@ __device__ __forceinline__ Entry entry_at(const CacheAttnArgs& a, int i) {
   e.win0 = lo / kChunk * kChunk;
   e.n_cand = e.n_sel = 0;
   if (a.sel && p0 >= a.window) {
-    e.n_cand = (p0 - a.window + 1) / a.c.block;
+    e.n_cand = (p0 - a.window + 1) >> a.c.lb;
     e.n_sel = min(a.top_k, e.n_cand);
   }
-  e.n_chunks = p1 < 0 ? 0 : e.n_sel * (a.c.block / kChunk) + (p1 - e.win0) / kChunk + 1;
+  e.n_chunks = p1 < 0 ? 0 : (e.n_sel << (a.c.lb - kChunkLog2)) + (p1 - e.win0) / kChunk + 1;
   return e;
 }
 
@@ -88,7 +87,8 @@ __device__ __forceinline__ Plan plan_of(const CacheAttnArgs& a, int tile) {
   return p;
 }
 
-// Inclusive sum over the block; all threads get the total in *total.
+// Inclusive sum over the CTA's kNw warps; all threads get the total in *total.
+template <int kNw>
 __device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* smem, int64_t* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -101,7 +101,7 @@ __device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* smem, int64_t*
   __syncthreads();
   int64_t before = 0, all = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
+  for (int w = 0; w < kNw; ++w) {
     before += w < warp ? smem[w] : 0;
     all += smem[w];
   }
@@ -109,13 +109,42 @@ __device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* smem, int64_t*
   return x + before;
 }
 
-// All chunks of the call (over one unit an entry: times p.units for all).
-__device__ __forceinline__ int64_t total_chunks(const CacheAttnArgs& a, const Plan& p,
-                                                int64_t* smem) {
-  int64_t x = 0, total;
-  for (int i = threadIdx.x; i < p.n_entries; i += kThreads) x += entry_at(a, i).n_chunks;
-  block_scan(x, smem, &total);
-  return total;
+// The chunks of all entries; up to a CTA of them are read once.
+struct Scan {
+  int64_t total;   // chunks of one unit of every entry
+  int64_t first;   // this thread's entry: chunks before it (one unit an entry)
+  int64_t n;       // and its own
+};
+template <int kNw>
+__device__ __forceinline__ Scan scan_entries(const CacheAttnArgs& a, const Plan& p, int64_t* smem) {
+  Scan r;
+  int64_t more = 0;
+  r.n = static_cast<int>(threadIdx.x) < p.n_entries ? entry_at(a, threadIdx.x).n_chunks : 0;
+  for (int i = threadIdx.x + 32 * kNw; i < p.n_entries; i += 32 * kNw)
+    more += entry_at(a, i).n_chunks;
+  int64_t first_total, rest = 0;
+  r.first = block_scan<kNw>(r.n, smem, &first_total) - r.n;
+  if (p.n_entries > 32 * kNw) block_scan<kNw>(more, smem, &rest);
+  r.total = first_total + rest;
+  return r;
+}
+
+// Calls hit(i, before, n) in the thread of each entry: its index, the chunks
+// (one unit an entry) before it and its own.
+template <int kNw, typename Hit>
+__device__ __forceinline__ void each_entry(const CacheAttnArgs& a, const Plan& p, const Scan& s,
+                                           int64_t* smem, Hit hit) {
+  if (static_cast<int>(threadIdx.x) < p.n_entries) hit(threadIdx.x, s.first, s.n);
+  if (p.n_entries <= 32 * kNw) return;
+  int64_t before = 0;
+  for (int i0 = 0; i0 < p.n_entries; i0 += 32 * kNw) {
+    const int i = i0 + threadIdx.x;
+    const int64_t n = i < p.n_entries ? entry_at(a, i).n_chunks : 0;
+    int64_t total;
+    const int64_t upto = before + block_scan<kNw>(n, smem, &total);
+    if (i0 > 0 && i < p.n_entries) hit(i, upto - n, n);
+    before += total;
+  }
 }
 
 // CTAs that share W chunks: a CTA's warps take at least one each.
@@ -184,21 +213,21 @@ __device__ __forceinline__ Ahead look_ahead(const CacheAttnArgs& a, const Entry&
   r.ks = r.vs = 0.f;
   r.flags = 0;
   if (x >= end) return r;
-  const int per = a.c.block / kChunk;
+  const int per_log2 = a.c.lb - kChunkLog2, x_win = e.n_sel << per_log2;
   int slot;
-  if (x < e.n_sel * per) {
+  if (x < x_win) {
     const int64_t u = (static_cast<int64_t>(e.b) * a.T + e.t) * a.c.Hkv + c;
-    const int i = x / per;
+    const int i = x >> per_log2;
     const int64_t cnt = sel_count_checked(a.cnt[u], a.top_k, e.n_cand, a.status);
     if (i >= cnt) return r;
     const int blk = sel_block_checked(a.sel[u * a.top_k + i], e.n_cand, a.status);
-    slot = blk * a.c.block + (x - i * per) * kChunk;
+    slot = (blk << a.c.lb) + (x - (i << per_log2)) * kChunk;
     r.flags = 1;
   } else {
-    slot = e.win0 + (x - e.n_sel * per) * kChunk;
+    slot = e.win0 + (x - x_win) * kChunk;
     r.flags = 3;
   }
-  const int j = slot / a.c.block;
+  const int j = slot >> a.c.lb;
   int64_t page = cache_page(a.s, e.b, j, a.c.n_pages, a.status);
   if (page < 0) {  // recorded; read a page that exists
     page = 0;
@@ -206,7 +235,7 @@ __device__ __forceinline__ Ahead look_ahead(const CacheAttnArgs& a, const Entry&
   }
   r.key0 = slot;
   const int64_t head = page * a.c.Hkv + c;
-  r.at = head * a.c.block + (slot - j * a.c.block);
+  r.at = (head << a.c.lb) + (slot & (a.c.block - 1));
   r.ks = a.c.k_scale[head];
   r.vs = a.c.v_scale[head];
   return r;
@@ -262,6 +291,27 @@ __device__ __forceinline__ void store_out(const CacheAttnArgs& a, const Entry& e
     *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at) = w;
   } else {
     *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = v;
+  }
+}
+
+// kN dims of a row, times f.
+template <int kN>
+__device__ __forceinline__ void store_dims(const CacheAttnArgs& a, const Entry& e, int c, int m,
+                                           int dim, const float* v, float f) {
+  if constexpr (kN == 4) {
+    store_out(a, e, c, m, dim, make_float4(v[0] * f, v[1] * f, v[2] * f, v[3] * f));
+  } else {
+    int t, h;
+    row_of(a, e, c, m, &t, &h);
+    const int64_t at = ((static_cast<int64_t>(e.b) * a.T + t) * a.Hq + h) * a.c.d + dim;
+    if (!MSA_IN_RANGE(at, 2, static_cast<int64_t>(a.s.batch) * a.T * a.Hq * a.c.d, a.status))
+      return;
+    if (a.out_bf16)
+      *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(a.out) + at) =
+          __floats2bfloat162_rn(v[0] * f, v[1] * f);
+    else
+      *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at) =
+          make_float2(v[0] * f, v[1] * f);
   }
 }
 
@@ -795,29 +845,22 @@ __global__ void __launch_bounds__(kThreads, Body::kPerSm) cache_attn_kernel(cons
   __shared__ __align__(16) uint8_t extra[Body::kSmemQ > 0 ? Body::kSmemQ : 16];
 
   const Plan p = plan_of(a, kTile);
-  const int64_t W = total_chunks(a, p, scan) * p.units;
+  let_next_start();
+  wait_for_inputs();
+  const Scan sc = scan_entries<kWarps>(a, p, scan);
+  const int64_t W = sc.total * p.units;
   if (W == 0) return;
   const int64_t P = cta_count(a, W);
   if (blockIdx.x >= P) return;
   const int64_t begin = cta_begin(blockIdx.x, W, P), end = cta_begin(blockIdx.x + 1, W, P);
-
   // The entry that holds chunk `begin`, and its first chunk.
-  {
-    int64_t before = 0;
-    for (int i0 = 0; i0 < p.n_entries; i0 += kThreads) {
-      const int i = i0 + threadIdx.x;
-      const int64_t x = i < p.n_entries ? entry_at(a, i).n_chunks * p.units : 0;
-      int64_t total;
-      const int64_t upto = before + block_scan(x, scan, &total);
-      if (begin >= upto - x && begin < upto) {
-        found[0] = i;
-        found[1] = upto - x;
-      }
-      before += total;
-      if (before > begin) break;
+  each_entry<kWarps>(a, p, sc, scan, [&](int i, int64_t before, int64_t n) {
+    if (begin >= before * p.units && begin < (before + n) * p.units) {
+      found[0] = i;
+      found[1] = before * p.units;
     }
-    __syncthreads();
-  }
+  });
+  __syncthreads();
   int i = static_cast<int>(found[0]);
   int64_t base = found[1];  // first chunk of entry i
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -899,68 +942,103 @@ __global__ void __launch_bounds__(kThreads, Body::kPerSm) cache_attn_kernel(cons
 }
 
 // Joins the parts of the units that several CTAs share, and writes the rows
-// that attend nothing.  One CTA a unit.
-template <int D, int kTile>
-__global__ void __launch_bounds__(kThreads) cache_attn_join_kernel(const CacheAttnArgs a) {
-  __shared__ int64_t scan[kWarps];
-  __shared__ int64_t found;
+// that attend nothing.  kWpr warps a row: 1 where a unit has a few parts (and
+// 4 rows a CTA), 16 where it has many, every 16th part each; a lane has D/32
+// dims.  The parts come from L2 one latency after the other, so several are
+// kept under way.
+constexpr int kJoinMany = 16;
+
+template <int D, int kTile, int kWpr>
+__global__ void __launch_bounds__(kWpr == 1 ? kThreads : 32 * kWpr)
+    cache_attn_join_kernel(const CacheAttnArgs a) {
+  constexpr int kDl = D / 32;
+  constexpr int kWarpsJ = kWpr == 1 ? kWarps : kWpr, kRows = kWarpsJ / kWpr;
+  __shared__ int64_t scan[kWarpsJ];
+  __shared__ int64_t found[kRows];
+  __shared__ float red[kWarpsJ], lsum[kWarpsJ];
+  __shared__ __align__(16) float osum[kWarpsJ][kWpr == 1 ? 1 : D];
   const Plan p = plan_of(a, kTile);
-  const int i = blockIdx.x / p.units, u = blockIdx.x - i * p.units;
+  const int rows = a.c.Hkv * p.rows;  // of an entry, all KV heads
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kRows;
+  const int64_t all = static_cast<int64_t>(p.n_entries) * rows;
+  let_next_start();
+  const Scan sc = scan_entries<kWarpsJ>(a, p, scan);
+  each_entry<kWarpsJ>(a, p, sc, scan, [&](int k, int64_t before, int64_t) {
+#pragma unroll
+    for (int w = 0; w < kRows; ++w)
+      if ((row0 + w) / rows == k) found[w] = before;
+  });
+  __syncthreads();
+  const int mine = kWpr == 1 ? warp : 0, part = kWpr == 1 ? 0 : warp;
+  wait_for_inputs();  // every path: whoever waits for this kernel waits for the parts too
+  if (row0 + mine >= all) return;
+  const int i = static_cast<int>((row0 + mine) / rows);
+  const int cm = static_cast<int>(row0 + mine - static_cast<int64_t>(i) * rows);
+  const int c = cm / p.rows, m = cm - c * p.rows, rt = m / kTile, r = m - rt * kTile;
   const Entry e = entry_at(a, i);
-  const int c = u / p.n_tiles, rt = u - c * p.n_tiles;
-  const int rows = min(kTile, p.rows - rt * kTile);
   if (e.n_chunks == 0) {
-    for (int k = threadIdx.x; k < rows * (D / 4); k += kThreads) {
-      const int r = k / (D / 4), dim = (k - r * (D / 4)) * 4;
-      store_out(a, e, c, rt * kTile + r, dim, make_float4(0.f, 0.f, 0.f, 0.f));
-      if (dim == 0) store_lse(a, p, e, c, rt * kTile + r, -INFINITY);
-    }
+    if (part == 0 && lane < D / 4) store_out(a, e, c, m, 4 * lane, make_float4(0.f, 0.f, 0.f, 0.f));
+    if (part == 0 && lane == 0) store_lse(a, p, e, c, m, -INFINITY);
     return;
   }
-  const int64_t total = total_chunks(a, p, scan);
-  {
-    int64_t before = 0;
-    for (int i0 = 0; i0 <= i; i0 += kThreads) {
-      const int k = i0 + threadIdx.x;
-      const int64_t x = k < p.n_entries ? entry_at(a, k).n_chunks : 0;
-      int64_t sum;
-      const int64_t upto = before + block_scan(x, scan, &sum);
-      if (k == i) found = upto - x;
-      before += sum;
-    }
-    __syncthreads();
-  }
-  const int64_t W = total * p.units, P = cta_count(a, W);
-  const int64_t u0 = found * p.units + u * e.n_chunks;
-  const int64_t c0 = cta_of(u0, W, P), c1 = cta_of(u0 + e.n_chunks - 1, W, P);
+  const int64_t W = sc.total * p.units, P = cta_count(a, W);
+  const int64_t u0 = found[mine] * p.units + static_cast<int64_t>(c * p.n_tiles + rt) * e.n_chunks;
+  const int c0 = static_cast<int>(cta_of(u0, W, P));
+  const int c1 = static_cast<int>(cta_of(u0 + e.n_chunks - 1, W, P));
   if (c0 == c1) return;  // written whole
-  for (int k = threadIdx.x; k < rows * (D / 4); k += kThreads) {
-    const int r = k / (D / 4), dim = (k - r * (D / 4)) * 4;
-    float mx = -INFINITY;
-    for (int64_t x = c0; x <= c1; ++x)
-      mx = fmaxf(mx, a.lse_part[(2 * x + (x == c0)) * kTile + r]);
-    mx = finite_or_0(mx);
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-    for (int64_t x = c0; x <= c1; ++x) {
-      const int64_t s = (2 * x + (x == c0)) * kTile + r;
-      const float f = ex2(a.lse_part[s] - mx);
-      if (f == 0.f) continue;
-      const float4 y = *reinterpret_cast<const float4*>(a.o_part + s * D + dim);
-      l += f;
-      v.x += y.x * f;
-      v.y += y.y * f;
-      v.z += y.z * f;
-      v.w += y.w * f;
-    }
-    const float f = l == 0.f ? 0.f : 1.f / l;
-    v.x *= f;
-    v.y *= f;
-    v.z *= f;
-    v.w *= f;
-    store_out(a, e, c, rt * kTile + r, dim, v);
-    if (dim == 0) store_lse(a, p, e, c, rt * kTile + r, l == 0.f ? -INFINITY : mx + log2f(l));
+  const auto at = [&](int x) { return (2 * static_cast<int64_t>(x) + (x == c0)) * kTile + r; };
+  float mx = -INFINITY;
+  for (int x = c0 + 32 * part + lane; x <= c1; x += 32 * kWpr) mx = fmaxf(mx, a.lse_part[at(x)]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  if (kWpr > 1) {
+    if (lane == 0) red[warp] = mx;
+    __syncthreads();
+    mx = lane < kWpr ? red[lane] : -INFINITY;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   }
+  mx = finite_or_0(mx);
+  float v[kDl], l = 0.f;
+#pragma unroll
+  for (int k = 0; k < kDl; ++k) v[k] = 0.f;
+#pragma unroll 8
+  for (int x = c0 + part; x <= c1; x += kWpr) {
+    const int64_t s = at(x);
+    const float f = ex2(a.lse_part[s] - mx);
+    const float* src = a.o_part + s * D + lane * kDl;
+    float y[kDl];
+    if constexpr (kDl == 4) {
+      const float4 z = *reinterpret_cast<const float4*>(src);
+      y[0] = z.x, y[1] = z.y, y[2] = z.z, y[3] = z.w;
+    } else {
+      const float2 z = *reinterpret_cast<const float2*>(src);
+      y[0] = z.x, y[1] = z.y;
+    }
+    l += f;
+#pragma unroll
+    for (int k = 0; k < kDl; ++k) v[k] += f == 0.f ? 0.f : y[k] * f;
+  }
+  if (kWpr > 1) {
+#pragma unroll
+    for (int k = 0; k < kDl; ++k) osum[warp][lane * kDl + k] = v[k];
+    if (lane == 0) lsum[warp] = l;
+    __syncthreads();
+    if (warp > 0) return;
+    l = 0.f;
+#pragma unroll
+    for (int k = 0; k < kDl; ++k) v[k] = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWpr; ++w) {
+      l += lsum[w];
+#pragma unroll
+      for (int k = 0; k < kDl; ++k) v[k] += osum[w][lane * kDl + k];
+    }
+  }
+  const float f = l == 0.f ? 0.f : 1.f / l;
+  store_dims<kDl>(a, e, c, m, lane * kDl, v, f);
+  if (lane == 0) store_lse(a, p, e, c, m, l == 0.f ? -INFINITY : mx + log2f(l));
 }
 
 // weights[b, c, j] += sum over the rows of KV head c of their probability of
@@ -973,19 +1051,34 @@ __global__ void __launch_bounds__(256) cache_weights_kernel(const CacheAttnArgs 
   const int64_t len = cache_len(a.s, b, a.c.block, a.status);
   const int64_t j = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
   const int64_t lo = max(0, static_cast<int>(len) - a.T - a.window + 1);
-  if (static_cast<int64_t>(blockIdx.x) * blockDim.x >= len) return;
+  if (static_cast<int64_t>(blockIdx.x) * blockDim.x >= len) {
+    wait_for_inputs();
+    return;
+  }
   const int64_t u = static_cast<int64_t>(b) * a.c.Hkv + c;
+  wait_for_inputs();
   for (int r = threadIdx.x; r < rows; r += blockDim.x) lse[r] = a.lse2[u * even + r];
   __syncthreads();
   if (j < lo || j >= len) return;
   const int64_t slots = static_cast<int64_t>(a.s.max_blocks) * a.c.block;
   const float* s = a.scores + (u * slots + j) * even;
   float sum = 0.f;
-  for (int r = 0; r < rows; r += 2) {
-    const float2 x = *reinterpret_cast<const float2*>(s + r);
-    // A row that attends nothing (lse -inf) has scores of -inf alone.
-    sum += x.x == -INFINITY ? 0.f : ex2(x.x - lse[r]);
-    if (r + 1 < rows) sum += x.y == -INFINITY ? 0.f : ex2(x.y - lse[r + 1]);
+  // A row that attends nothing (lse -inf) has scores of -inf alone.
+  const auto add = [&](float x, int r) { sum += x == -INFINITY ? 0.f : ex2(x - lse[r]); };
+  if ((even & 3) == 0) {
+    for (int r = 0; r < rows; r += 4) {
+      const float4 x = __ldcs(reinterpret_cast<const float4*>(s + r));
+      add(x.x, r);
+      if (r + 1 < rows) add(x.y, r + 1);
+      if (r + 2 < rows) add(x.z, r + 2);
+      if (r + 3 < rows) add(x.w, r + 3);
+    }
+  } else {
+    for (int r = 0; r < rows; r += 2) {
+      const float2 x = __ldcs(reinterpret_cast<const float2*>(s + r));
+      add(x.x, r);
+      if (r + 1 < rows) add(x.y, r + 1);
+    }
   }
   if (MSA_IN_RANGE(u * a.weights_ld + j, 1,
                    static_cast<int64_t>(a.s.batch) * a.c.Hkv * a.weights_ld, a.status))
@@ -994,21 +1087,28 @@ __global__ void __launch_bounds__(256) cache_weights_kernel(const CacheAttnArgs 
 
 template <int D, class Body>
 cudaError_t launch_body(const CacheAttnArgs& a, cudaStream_t st) {
-  cache_attn_kernel<D, Body><<<a.n_ctas, kThreads, 0, st>>>(a);
-  cudaError_t e = cudaPeekAtLastError();
+  cudaError_t e = launch_after(cache_attn_kernel<D, Body>, dim3(a.n_ctas), kThreads, 0, st,
+                               a.sel_from_kernel != 0, a);
   if (e != cudaSuccess) return e;
   const int g = a.Hq / a.c.Hkv;
   const int rows = a.sel ? g : a.T * g;
+  const int64_t all = static_cast<int64_t>(a.s.batch) * a.T * a.Hq;
+  // Parts of a unit: at most about the CTAs over the units (all of them where
+  // one sequence is long and the others are not).
   const int64_t units = static_cast<int64_t>(a.sel ? a.s.batch * a.T : a.s.batch) * a.c.Hkv *
                         ((rows + Body::kTile - 1) / Body::kTile);
-  cache_attn_join_kernel<D, Body::kTile><<<static_cast<unsigned>(units), kThreads, 0, st>>>(a);
-  e = cudaPeekAtLastError();
+  if (a.n_ctas > kJoinMany * units)
+    e = launch_after(cache_attn_join_kernel<D, Body::kTile, kJoinMany>,
+                     dim3(static_cast<unsigned>(all)), 32 * kJoinMany, 0, st, true, a);
+  else
+    e = launch_after(cache_attn_join_kernel<D, Body::kTile, 1>,
+                     dim3(static_cast<unsigned>((all + kWarps - 1) / kWarps)), kThreads, 0, st,
+                     true, a);
   if (e != cudaSuccess || !a.weights) return e;
   const int64_t slots = static_cast<int64_t>(a.s.max_blocks) * a.c.block;
   const dim3 grid(static_cast<unsigned>((slots + 255) / 256),
                   static_cast<unsigned>(a.s.batch * a.c.Hkv));
-  cache_weights_kernel<<<grid, 256, rows * sizeof(float), st>>>(a);
-  return cudaPeekAtLastError();
+  return launch_after(cache_weights_kernel, grid, 256, rows * sizeof(float), st, true, a);
 }
 
 }  // namespace

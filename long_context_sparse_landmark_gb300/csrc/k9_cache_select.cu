@@ -31,7 +31,7 @@ constexpr int kListMax = 1024;  // near-ties ranked in shared memory
 
 __device__ __forceinline__ int candidates(const CacheSelectArgs& a, int len, int t) {
   const int p = len - a.T + t;
-  return p >= a.window ? (p - a.window + 1) / a.c.block : 0;
+  return p >= a.window ? (p - a.window + 1) >> a.c.lb : 0;
 }
 
 template <bool kBf16>
@@ -46,6 +46,7 @@ __device__ __forceinline__ float q_at(const void* q, int64_t i) {
 template <int D, bool kBf16>
 __global__ void __launch_bounds__(kScoreThreads) cache_score_kernel(const CacheSelectArgs a) {
   __shared__ __align__(16) float qs[kScoreT][D], qa[kScoreT][D];
+  let_next_start();
   const int c = blockIdx.y, b = blockIdx.z, g = a.Hq / a.c.Hkv;
   const int len = cache_len(a.s, b, a.c.block, a.status);
   const int most = candidates(a, len, a.T - 1);  // the last token sees the most
@@ -218,6 +219,8 @@ __global__ void __launch_bounds__(kPickThreads) cache_pick_kernel(const CacheSel
   const int n = candidates(a, cache_len(a.s, b, a.c.block, a.status), t);
   int32_t* sel = a.sel + u * a.top_k;
   const int k = min(a.top_k, n);
+  let_next_start();
+  wait_for_inputs();
   if (threadIdx.x == 0) a.cnt[u] = k;
   for (int i = k + threadIdx.x; i < a.top_k; i += kPickThreads) sel[i] = -1;
   if (k == n) {
@@ -375,12 +378,9 @@ cudaError_t launch_scores(const CacheSelectArgs& a, cudaStream_t st) {
 cudaError_t launch_cache_select(const CacheSelectArgs& a, cudaStream_t st) {
   cudaError_t e = a.c.d == 128 ? launch_scores<128>(a, st) : launch_scores<64>(a, st);
   if (e != cudaSuccess) return e;
-  const unsigned units = static_cast<unsigned>(a.s.batch) * a.T * a.c.Hkv;
-  if (a.bf16)
-    cache_pick_kernel<true><<<units, kPickThreads, 0, st>>>(a);
-  else
-    cache_pick_kernel<false><<<units, kPickThreads, 0, st>>>(a);
-  return cudaPeekAtLastError();
+  const dim3 units(static_cast<unsigned>(a.s.batch) * a.T * a.c.Hkv);
+  return launch_after(a.bf16 ? cache_pick_kernel<true> : cache_pick_kernel<false>, units,
+                      kPickThreads, 0, st, true, a);
 }
 
 }  // namespace msa

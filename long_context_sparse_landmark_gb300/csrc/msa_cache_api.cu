@@ -116,7 +116,8 @@ msa_status check_workspace(const void* ws, size_t bytes, size_t need) {
 
 msa::CacheView view(const msa_kv_cache* c) {
   return {static_cast<uint8_t*>(c->k_codes), static_cast<uint8_t*>(c->v_codes), c->k_scale,
-          c->v_scale, static_cast<__nv_bfloat16*>(c->k_mean), c->n_pages, c->Hkv, c->d, c->block};
+          c->v_scale, static_cast<__nv_bfloat16*>(c->k_mean), c->n_pages, c->Hkv, c->d, c->block,
+          c->block == 32 ? 5 : c->block == 64 ? 6 : c->block == 128 ? 7 : 8};
 }
 
 size_t up(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -172,8 +173,8 @@ SelectPlan select_plan(int Hkv, int batch, int n_q, int max_blocks) {
 msa_status run_attn(const msa_kv_cache* c, const void* q, const int32_t* table, int max_blocks,
                     const int32_t* lens, int batch, int n_q, int Hq, int64_t window, float scale,
                     void* out, float* lse, const int32_t* sel, const int32_t* cnt, int top_k,
-                    float* weights, int64_t weights_ld, msa_dtype in_dt, msa_dtype out_dt,
-                    uint8_t* ws, msa_stream_t stream) {
+                    bool sel_from_kernel, float* weights, int64_t weights_ld, msa_dtype in_dt,
+                    msa_dtype out_dt, uint8_t* ws, msa_stream_t stream) {
   const AttnPlan p = attn_plan(c->Hkv, c->d, c->block, batch, n_q, Hq, max_blocks, sel != nullptr,
                                weights != nullptr, in_dt == MSA_BF16);
   msa::CacheAttnArgs a{};
@@ -188,6 +189,7 @@ msa_status run_attn(const msa_kv_cache* c, const void* q, const int32_t* table, 
   a.lse = lse;
   a.sel = sel;
   a.cnt = cnt;
+  a.sel_from_kernel = sel_from_kernel;
   a.top_k = top_k;
   a.weights = weights;
   a.weights_ld = weights_ld;
@@ -271,6 +273,7 @@ msa_status msa_cache_append(const msa_kv_cache* cache, const void* k, const void
   a.cu = cu;
   a.total = total;
   a.max_new = max_new;
+  a.blocks = static_cast<uint32_t>(blocks);
   a.bf16 = in_dt == MSA_BF16;
   MSA_TRY(msa::api_status_word(&a.status));
   return launched(msa::launch_cache_append(a, reinterpret_cast<cudaStream_t>(stream)),
@@ -309,7 +312,7 @@ msa_status msa_cache_attn(const msa_kv_cache* cache, const void* q, const int32_
                                false, weights != nullptr, in_dt == MSA_BF16);
   MSA_TRY(check_workspace(workspace, workspace_bytes, p.total));
   return run_attn(cache, q, table, max_blocks, lens, batch, n_q, Hq, window, scale, out, lse,
-                  nullptr, nullptr, 0, weights, weights_ld, in_dt, out_dt,
+                  nullptr, nullptr, 0, false, weights, weights_ld, in_dt, out_dt,
                   static_cast<uint8_t*>(workspace), stream);
 }
 
@@ -370,7 +373,7 @@ msa_status msa_cache_attn_select(const msa_kv_cache* cache, const void* q, const
                                true, false, in_dt == MSA_BF16);
   MSA_TRY(check_workspace(workspace, workspace_bytes, p.total));
   return run_attn(cache, q, table, max_blocks, lens, batch, n_q, Hq, window, scale, out, lse, sel,
-                  cnt, top_k, nullptr, 0, in_dt, out_dt, static_cast<uint8_t*>(workspace), stream);
+                  cnt, top_k, false, nullptr, 0, in_dt, out_dt, static_cast<uint8_t*>(workspace), stream);
 }
 
 // Workspace of the one-call form: the attention's, the selection's, sel, cnt.
@@ -418,7 +421,7 @@ msa_status msa_cache_attn_topk(const msa_kv_cache* cache, const void* q, const i
   MSA_TRY(run_select(cache, q, table, max_blocks, lens, batch, n_q, Hq, window, top_k, sel, cnt,
                      in_dt, ws + p.select, stream));
   return run_attn(cache, q, table, max_blocks, lens, batch, n_q, Hq, window, scale, out, lse, sel,
-                  cnt, top_k, nullptr, 0, in_dt, out_dt, ws, stream);
+                  cnt, top_k, true, nullptr, 0, in_dt, out_dt, ws, stream);
 }
 
 msa_status msa_cache_evict(const msa_kv_cache* cache, const int32_t* table, int max_blocks,

@@ -4,15 +4,15 @@
 // gathers them into fresh blocks.
 //
 // One cluster of CTAs a (sequence, KV head), each with a contiguous part of
-// the slots, whose keys its threads keep in registers: a radix selection of
-// the least kept weight by 11 + 11 + 10 bits (histograms in shared memory,
-// joined through the cluster's), then one pass of ballots that puts the kept
-// slots in order.  Weights compare as they are: the choice is exact.  The
-// first digit is sign, exponent and two bits of the mantissa, so that weights
-// of a few binades do not all meet at a few counters.  The weights are read
-// once (parts too long for the registers: once a digit, from L2): 4 bytes a
-// slot, against the 2 d bytes a kept slot costs in the gather; what bounds a
-// call is the chain of some ten barriers.
+// the slots, whose keys it keeps in shared memory: a radix selection of the
+// least kept weight by 11 + 11 + 10 bits (histograms joined through the
+// cluster's shared memory), then one pass of ballots that puts the kept slots
+// in order.  Weights compare as they are: the choice is exact.  The first
+// digit is sign, exponent and two bits of the mantissa, so that weights of a
+// few binades do not all meet at a few counters.  The weights are read once
+// (parts too long for shared memory: once a digit, from L2): 4 bytes a slot,
+// against the 2 d bytes a kept slot costs in the gather; what bounds a call is
+// the chain of some ten barriers.
 #include <math.h>
 
 #include <cooperative_groups.h>
@@ -27,6 +27,7 @@ namespace {
 constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kClusterMax = 8;
+constexpr int kKeysMax = 48 * 1024;  // of a CTA, in shared memory
 constexpr int kBins = 2048;
 
 // Unsigned key that orders as the weight does; -0 as +0, NaN above all.
@@ -36,17 +37,23 @@ __device__ __forceinline__ uint32_t weight_key(float x) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// kKeys keys a thread: warp w of CTA r has the slots from r * per + w * 32 *
-// kKeys on, lane by lane.  kKeys = 0: any number, read again for each pass.
-template <int kKeys>
+// kStaged: the keys stay in shared memory (kKeysMax of them at most).
+template <bool kStaged>
 __global__ void __launch_bounds__(kEvictThreads) cache_evict_kernel(const EvictArgs a) {
-  __shared__ __align__(16) int hist[kBins];
+  extern __shared__ uint32_t keys[];
+  __shared__ __align__(16) int hist[3][kBins];
   __shared__ int digit, left_s;
   __shared__ int counts[2];  // this CTA's slots above the least kept weight, and equal to it
   __shared__ int wsum[2][kEvictWarps];
   let_next_start();
   cg::cluster_group cl = cg::this_cluster();
   const int ranks = static_cast<int>(cl.num_blocks()), rank = static_cast<int>(cl.block_rank());
+  const auto sync_all = [&] {
+    if (ranks > 1)
+      cl.sync();
+    else
+      __syncthreads();
+  };
   const int u = blockIdx.x / ranks;
   const int b = u / a.c.Hkv, h = u - b * a.c.Hkv;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -58,42 +65,24 @@ __global__ void __launch_bounds__(kEvictThreads) cache_evict_kernel(const EvictA
   const float* w = a.weights + static_cast<int64_t>(u) * a.weights_ld;
   int32_t* out = a.kept + static_cast<int64_t>(u) * a.budget;
   float* out_w = a.new_weights + static_cast<int64_t>(u) * a.new_ld;
-  // The warp's slots [i0, i1), a multiple of 32 apart from the last.
-  int i0, i1;
-  if constexpr (kKeys > 0) {
-    i0 = min(n, (rank * kEvictWarps + warp) * 32 * kKeys);
-    i1 = min(n, i0 + 32 * kKeys);
-  } else {
-    const int warps = ranks * kEvictWarps;
-    const int per = ((n + warps - 1) / warps + 31) & ~31;
-    const int64_t from = static_cast<int64_t>(rank * kEvictWarps + warp) * per;
-    i0 = static_cast<int>(min64(n, from));
-    i1 = static_cast<int>(min64(n, from + per));
-  }
+  // The warp's slots [i0, i1): whole groups of 32, the last of all cut short.
+  // The launcher's kKeysMax covers what the rounding adds.
+  const int warps = ranks * kEvictWarps;
+  const int per = ((n + warps - 1) / warps + 31) & ~31;
+  const int64_t from = static_cast<int64_t>(rank * kEvictWarps + warp) * per;
+  const int i0 = static_cast<int>(min64(n, from)), i1 = static_cast<int>(min64(n, from + per));
+  uint32_t* mine = keys + warp * per;
 
   const bool all = need == n;
   const bool pick = need > 0 && !all;  // the same for the whole cluster
-  float x[kKeys > 0 ? kKeys : 1];
-  if constexpr (kKeys > 0) {
 #pragma unroll
-    for (int k = 0; k < kKeys; ++k) {
-      const int i = i0 + 32 * k + lane;
-      x[k] = i < i1 ? w[i] : 0.f;
-    }
+  for (int k = 0; k < 3; ++k)
+    *reinterpret_cast<int4*>(&hist[k][4 * threadIdx.x]) = make_int4(0, 0, 0, 0);
+  if constexpr (kStaged) {
+#pragma unroll 8
+    for (int i = i0 + lane; i < i1; i += 32) mine[i - i0] = weight_key(w[i]);
   }
-  // Calls f(slot or -1, weight) for the warp's slots in order, 32 at a time.
-  const auto each = [&](auto f) {
-    if constexpr (kKeys > 0) {
-#pragma unroll
-      for (int k = 0; k < kKeys; ++k) {
-        if (i0 + 32 * k >= i1) break;
-        const int i = i0 + 32 * k + lane;
-        f(i < i1 ? i : -1, x[k]);
-      }
-    } else {
-      for (int i = i0 + lane; i - lane < i1; i += 32) f(i < i1 ? i : -1, i < i1 ? w[i] : 0.f);
-    }
-  };
+  const auto key_at = [&](int i) { return kStaged ? mine[i - i0] : weight_key(w[i]); };
 
   if (rank == 0 && threadIdx.x == 0 && h == 0) a.new_lens[b] = kept;
   // Past the kept: -1 and 0.
@@ -110,43 +99,45 @@ __global__ void __launch_bounds__(kEvictThreads) cache_evict_kernel(const EvictA
 
   uint32_t prefix = 0, mask = 0;
   int left = need;
+  __syncthreads();
   if (pick) {
-#pragma unroll
+#pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
       const uint32_t bits = pass == 2 ? 0x3ffu : 0x7ffu;
-      *reinterpret_cast<int4*>(hist + 4 * threadIdx.x) = make_int4(0, 0, 0, 0);
-      __syncthreads();
-      each([&](int i, float v) {
-        const uint32_t k = weight_key(v);
-        if (i >= 0 && (k & mask) == prefix) atomicAdd(&hist[(k >> shift) & bits], 1);
-      });
-      cl.sync();
+#pragma unroll 8
+      for (int i = i0 + lane; i < i1; i += 32) {
+        const uint32_t k = key_at(i);
+        if ((k & mask) == prefix) atomicAdd(&hist[pass][(k >> shift) & bits], 1);
+      }
+      sync_all();
       // Thread t sums the bins 4 * (511 - t) + 3 .. + 0 of all ranks: the
       // threads' order is that of falling keys.
       const int at = 4 * (kEvictThreads - 1 - threadIdx.x);
-      int4 s = *reinterpret_cast<const int4*>(hist + at);
-      for (int r = 1; r < ranks; ++r) {
+      int4 s = *reinterpret_cast<const int4*>(&hist[pass][at]);
+#pragma unroll
+      for (int r = 1; r < kClusterMax; ++r) {
+        if (r >= ranks) break;
         const int4 y = *reinterpret_cast<const int4*>(
-            cl.map_shared_rank(hist, rank + r < ranks ? rank + r : rank + r - ranks) + at);
+            cl.map_shared_rank(&hist[pass][0], rank + r < ranks ? rank + r : rank + r - ranks) +
+            at);
         s.x += y.x;
         s.y += y.y;
         s.z += y.z;
         s.w += y.w;
       }
-      const int mine = s.x + s.y + s.z + s.w;
-      int upto = mine;
+      const int sum = s.x + s.y + s.z + s.w;
+      int upto = sum;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, upto, o);
         if (lane >= o) upto += y;
       }
       if (lane == 31) wsum[0][warp] = upto;
-      // Also: all ranks have read this histogram before any clears it.
-      cl.sync();
+      __syncthreads();
 #pragma unroll
       for (int v = 0; v < kEvictWarps; ++v) upto += v < warp ? wsum[0][v] : 0;
-      int before = upto - mine;
+      int before = upto - sum;
       if (before < left && left <= upto) {
         const int bin[4] = {s.w, s.z, s.y, s.x};
 #pragma unroll
@@ -162,19 +153,21 @@ __global__ void __launch_bounds__(kEvictThreads) cache_evict_kernel(const EvictA
       prefix |= static_cast<uint32_t>(digit) << shift;
       mask |= bits << shift;
       left = left_s;
+      __syncthreads();
     }
   }
   // How many of this warp's slots lie above the least kept weight, and at it.
   int above = 0, equal = 0;
-  if (need > 0)
-    each([&](int i, float v) {
-      const uint32_t k = weight_key(v);
-      above += i >= 0 && (all || k > prefix);
-      equal += i >= 0 && !all && k == prefix;
-    });
+  if (need > 0) {
+#pragma unroll 8
+    for (int i = i0 + lane; i < i1; i += 32) {
+      const uint32_t k = key_at(i);
+      above += all || k > prefix;
+      equal += !all && k == prefix;
+    }
+  }
   above = __reduce_add_sync(0xffffffffu, above);
   equal = __reduce_add_sync(0xffffffffu, equal);
-  __syncthreads();  // wsum is done with
   if (lane == 0) {
     wsum[0][warp] = above;
     wsum[1][warp] = equal;
@@ -198,39 +191,44 @@ __global__ void __launch_bounds__(kEvictThreads) cache_evict_kernel(const EvictA
       before_above += cl.map_shared_rank(counts, r)[0];
       before_equal += cl.map_shared_rank(counts, r)[1];
     }
-    cl.sync();  // no CTA leaves while another reads its counts
+    cl.sync();  // no CTA leaves while another reads its counts or histograms
   }
   if (need == 0) return;
   // `left` of the equal ones stay, the lowest slots first.  Position of a
   // kept slot: kept above before it, and kept equals before it.
-  each([&](int i, float v) {
-    const uint32_t k = weight_key(v);
-    const bool up = i >= 0 && (all || k > prefix), eq = i >= 0 && !all && k == prefix;
+#pragma unroll 4
+  for (int j = i0; j < i1; j += 32) {
+    const int i = j + lane;
+    const uint32_t k = i < i1 ? key_at(i) : 0u;
+    const bool up = i < i1 && (all || k > prefix), eq = i < i1 && !all && k == prefix;
     const uint32_t mu = __ballot_sync(0xffffffffu, up), me = __ballot_sync(0xffffffffu, eq);
     const int au = before_above + __popc(mu & ((1u << lane) - 1u));
     const int ae = before_equal + __popc(me & ((1u << lane) - 1u));
     if (up || (eq && ae < left)) {
       const int at = au + min(ae, left);
       out[at] = i;
-      out_w[at] = v;
+      out_w[at] = w[i];
     }
     before_above += __popc(mu);
     before_equal += __popc(me);
-  });
+  }
 }
 
 }  // namespace
 
 cudaError_t launch_cache_evict_select(const EvictArgs& a, cudaStream_t st) {
-  // Keys in registers: 16 a thread up to 8192 slots in one CTA, 32 up to
-  // 16384 a CTA and clusters of 2, 4 and 8; longer rows are read four times.
+  // 8192 slots a CTA up to a cluster of 8, then up to kKeysMax a CTA; longer
+  // rows are read again for each digit.
   const int64_t slots = static_cast<int64_t>(a.s.max_blocks) * a.c.block;
-  const int64_t per = 32 * kEvictThreads;
   int ranks = 1;
-  while (ranks < kClusterMax && slots > ranks * per) ranks *= 2;
-  const auto kernel = slots <= per / 2       ? cache_evict_kernel<16>
-                      : slots <= ranks * per ? cache_evict_kernel<32>
-                                             : cache_evict_kernel<0>;
+  while (ranks < kClusterMax && slots > ranks * 8192) ranks *= 2;
+  const int64_t each = (slots / ranks + 1) + 32 * kEvictWarps;
+  const bool staged = each <= kKeysMax;
+  const auto kernel = staged ? cache_evict_kernel<true> : cache_evict_kernel<false>;
+  const int smem = staged ? static_cast<int>(each) * 4 : 0;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -238,6 +236,7 @@ cudaError_t launch_cache_evict_select(const EvictArgs& a, cudaStream_t st) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.gridDim = dim3(static_cast<unsigned>(a.s.batch) * a.c.Hkv * ranks);
   cfg.blockDim = dim3(kEvictThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;

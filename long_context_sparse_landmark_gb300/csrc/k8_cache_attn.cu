@@ -89,17 +89,17 @@ __device__ __forceinline__ Plan plan_of(const CacheAttnArgs& a, int tile) {
 
 // Inclusive sum over the CTA's kNw warps; all threads get the total in *total.
 template <int kNw>
-__device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* smem, int64_t* total) {
+__device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* smem, uint32_t* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
   __syncthreads();
   if (lane == 31) smem[warp] = x;
   __syncthreads();
-  int64_t before = 0, all = 0;
+  uint32_t before = 0, all = 0;
 #pragma unroll
   for (int w = 0; w < kNw; ++w) {
     before += w < warp ? smem[w] : 0;
@@ -111,18 +111,18 @@ __device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* smem, int64_t*
 
 // The chunks of all entries; up to a CTA of them are read once.
 struct Scan {
-  int64_t total;   // chunks of one unit of every entry
-  int64_t first;   // this thread's entry: chunks before it (one unit an entry)
-  int64_t n;       // and its own
+  uint32_t total;   // chunks of one unit of every entry
+  uint32_t first;   // this thread's entry: chunks before it (one unit an entry)
+  uint32_t n;       // and its own
 };
 template <int kNw>
-__device__ __forceinline__ Scan scan_entries(const CacheAttnArgs& a, const Plan& p, int64_t* smem) {
+__device__ __forceinline__ Scan scan_entries(const CacheAttnArgs& a, const Plan& p, uint32_t* smem) {
   Scan r;
-  int64_t more = 0;
+  uint32_t more = 0;
   r.n = static_cast<int>(threadIdx.x) < p.n_entries ? entry_at(a, threadIdx.x).n_chunks : 0;
   for (int i = threadIdx.x + 32 * kNw; i < p.n_entries; i += 32 * kNw)
     more += entry_at(a, i).n_chunks;
-  int64_t first_total, rest = 0;
+  uint32_t first_total, rest = 0;
   r.first = block_scan<kNw>(r.n, smem, &first_total) - r.n;
   if (p.n_entries > 32 * kNw) block_scan<kNw>(more, smem, &rest);
   r.total = first_total + rest;
@@ -133,28 +133,45 @@ __device__ __forceinline__ Scan scan_entries(const CacheAttnArgs& a, const Plan&
 // (one unit an entry) before it and its own.
 template <int kNw, typename Hit>
 __device__ __forceinline__ void each_entry(const CacheAttnArgs& a, const Plan& p, const Scan& s,
-                                           int64_t* smem, Hit hit) {
+                                           uint32_t* smem, Hit hit) {
   if (static_cast<int>(threadIdx.x) < p.n_entries) hit(threadIdx.x, s.first, s.n);
   if (p.n_entries <= 32 * kNw) return;
-  int64_t before = 0;
+  uint32_t before = 0;
   for (int i0 = 0; i0 < p.n_entries; i0 += 32 * kNw) {
     const int i = i0 + threadIdx.x;
-    const int64_t n = i < p.n_entries ? entry_at(a, i).n_chunks : 0;
-    int64_t total;
-    const int64_t upto = before + block_scan<kNw>(n, smem, &total);
+    const uint32_t n = i < p.n_entries ? entry_at(a, i).n_chunks : 0;
+    uint32_t total;
+    const uint32_t upto = before + block_scan<kNw>(n, smem, &total);
     if (i0 > 0 && i < p.n_entries) hit(i, upto - n, n);
     before += total;
   }
 }
 
-// CTAs that share W chunks: a CTA's warps take at least one each.
-__device__ __forceinline__ int64_t cta_count(const CacheAttnArgs& a, int64_t W) {
-  return max64(1, min64(a.n_ctas, (W + kWarps - 1) / kWarps));
+// The W chunks of all units, cut into P ranges, one a CTA: the first W % P
+// have one chunk more.  A CTA's warps take at least one chunk each.  W fits 31
+// bits (the entry points check).
+struct Cut {
+  uint32_t P, each, more;
+};
+__device__ __forceinline__ Cut cut_of(const CacheAttnArgs& a, uint32_t W) {
+  Cut k;
+  k.P = max(1u, min(static_cast<uint32_t>(a.n_ctas), (W + kWarps - 1) / kWarps));
+  k.each = W / k.P;
+  k.more = W - k.each * k.P;
+  return k;
 }
-__device__ __forceinline__ int64_t cta_begin(int64_t p, int64_t W, int64_t P) { return p * W / P; }
+__device__ __forceinline__ uint32_t cta_begin(const Cut& k, uint32_t p) {
+  return p * k.each + min(p, k.more);
+}
 // The CTA whose range holds chunk x.
-__device__ __forceinline__ int64_t cta_of(int64_t x, int64_t W, int64_t P) {
-  return ((x + 1) * P - 1) / W;
+__device__ __forceinline__ uint32_t cta_of(const Cut& k, uint32_t x) {
+  const uint32_t longer = k.more * (k.each + 1);
+  return x < longer ? x / (k.each + 1) : k.more + (x - longer) / k.each;
+}
+
+__device__ __forceinline__ void copy_async16(void* smem, const void* global) {
+  const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(global) : "memory");
 }
 
 // ---- pieces of the tensor-core body ---------------------------------------
@@ -175,7 +192,12 @@ __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ float ex2(float x) { return exp2f(x); }
+// 2^x, within 2 ulp; results below the normal range are 0.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ float finite_or_0(float m) { return m == -INFINITY ? 0.f : m; }
 
 // Row m of an entry: its query token and head.
@@ -190,7 +212,7 @@ __device__ __forceinline__ void row_of(const CacheAttnArgs& a, const Entry& e, i
 struct Chunk {
   int64_t at;    // first slot's row in the codes [n_pages * Hkv * block, d]
   int key0;      // first slot
-  float ks, vs;  // scales of K and V
+  float ks, lvs;  // scale of K, log2 of that of V
   bool on;       // false: nothing to attend (a selection shorter than top_k)
   bool window;   // of the window part: rows' own limits apply
 };
@@ -201,7 +223,7 @@ struct Chunk {
 struct Ahead {
   int64_t at;
   int key0;
-  float ks, vs;
+  float ks, lvs;
   int flags;
 };
 
@@ -210,7 +232,7 @@ __device__ __forceinline__ Ahead look_ahead(const CacheAttnArgs& a, const Entry&
   Ahead r;
   r.at = 0;
   r.key0 = 0;
-  r.ks = r.vs = 0.f;
+  r.ks = r.lvs = 0.f;
   r.flags = 0;
   if (x >= end) return r;
   const int per_log2 = a.c.lb - kChunkLog2, x_win = e.n_sel << per_log2;
@@ -237,7 +259,8 @@ __device__ __forceinline__ Ahead look_ahead(const CacheAttnArgs& a, const Entry&
   const int64_t head = page * a.c.Hkv + c;
   r.at = (head << a.c.lb) + (slot & (a.c.block - 1));
   r.ks = a.c.k_scale[head];
-  r.vs = a.c.v_scale[head];
+  const float vs = a.c.v_scale[head];
+  r.lvs = vs == 0.f ? 0.f : log2f(vs);  // a block of zeros (scale 0) counts as scale 1
   return r;
 }
 
@@ -246,15 +269,12 @@ __device__ __forceinline__ Chunk chunk_of(const Ahead& r, int src) {
   c.key0 = __shfl_sync(0xffffffffu, r.key0, src);
   c.at = __shfl_sync(0xffffffffu, r.at, src);
   c.ks = __shfl_sync(0xffffffffu, r.ks, src);
-  c.vs = __shfl_sync(0xffffffffu, r.vs, src);
+  c.lvs = __shfl_sync(0xffffffffu, r.lvs, src);
   const int f = __shfl_sync(0xffffffffu, r.flags, src);
   c.on = f & 1;
   c.window = f & 2;
   return c;
 }
-
-// log2 of a block's value scale; a block of zeros (scale 0) counts as 1.
-__device__ __forceinline__ float log2_scale(float vs) { return vs == 0.f ? 0.f : log2f(vs); }
 
 // The joined result of a CTA's warps for one unit's range, or a whole unit.
 // Row r: osum[w][r][dim] holds warp w's sum scaled to the row's common M,
@@ -370,20 +390,26 @@ __device__ __forceinline__ void join_warps(const CacheAttnArgs& a, const Plan& p
 template <int D, int kNt>
 struct MmaBody {
   static constexpr int kTile = 8 * kNt;
+  // 12 warps an SM with 16 KB of chunks under way each, or 8 with 24 KB (four
+  // tiles: 16 KB, and 8 KB for the rows, which no longer fit the registers).
   static constexpr int kPerSm = kNt == 1 ? 3 : 2;
+  static constexpr int kStages = (kNt == 2 ? 3 : 2) * (D == 128 ? 1 : 2);
+  static constexpr bool kQShared = kNt > 2;
   static constexpr int kKs = D / 16;   // k-steps over d
   static constexpr int kMt = D / 16;   // 16-row tiles of O^T
   static constexpr int kKw = D / 16;   // words of a K row a lane holds
   static constexpr int kVw = D / 32;   // words of a V row a lane holds
 
-  uint32_t q[kKs][kNt][2];
+  uint32_t q[kQShared ? 1 : kKs][kQShared ? 1 : kNt][2];
+  uint2* qsm;         // [k-step][tile][lane]
   float qs[kNt][2];   // score scale of rows 2t, 2t+1 (log2 units)
   float o[kMt][kNt][4];
   float m[kNt][2], l[kNt][2], M[kNt][2];
 
   __device__ __forceinline__ void begin(const CacheAttnArgs& a, const Plan& p, const Entry& e,
-                                        int c, int rt, uint8_t*) {
+                                        int c, int rt, uint8_t* smem) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+    qsm = reinterpret_cast<uint2*>(smem + kRingBytes) + lane;
 #pragma unroll
     for (int n = 0; n < kNt; ++n) {
       // The lane's pieces of row 8n + g: d = 64 hf + 16 t4 + 0..15.
@@ -420,8 +446,14 @@ struct MmaBody {
       const float up = pow2i(k);
 #pragma unroll
       for (int s = 0; s < kKs; ++s) {
-        q[s][n][0] = half2_of(v[4 * s] * up, v[4 * s + 1] * up);
-        q[s][n][1] = half2_of(v[4 * s + 2] * up, v[4 * s + 3] * up);
+        const uint32_t b0 = half2_of(v[4 * s] * up, v[4 * s + 1] * up);
+        const uint32_t b1 = half2_of(v[4 * s + 2] * up, v[4 * s + 3] * up);
+        if constexpr (kQShared) {  // read by the same lane alone
+          qsm[(s * kNt + n) * 32] = make_uint2(b0, b1);
+        } else {
+          q[s][n][0] = b0;
+          q[s][n][1] = b1;
+        }
       }
       const float mine = a.scale * kLog2e * pow2i(-k);
       qs[n][0] = __shfl_sync(0xffffffffu, mine, 8 * t4);
@@ -440,42 +472,69 @@ struct MmaBody {
         for (int k = 0; k < 4; ++k) o[i][n][k] = 0.f;
   }
 
+  // A warp's chunks pass through a ring of its own in shared memory: K and V
+  // codes as [32][D] each, 16-byte pieces (and for d = 64 rows of V) moved
+  // about so that the fragment reads below meet no bank twice.
+  static constexpr int kStageBytes = 2 * kChunk * D;
+  static constexpr int kRingBytes = kStages * kStageBytes;
+
+  __device__ __forceinline__ static int k_at(int row, int piece) {
+    return D == 128 ? row * 128 + ((piece ^ ((row & 1) << 2)) << 4) : row * 64 + (piece << 4);
+  }
+  __device__ __forceinline__ static int v_at(int row, int piece) {
+    return kChunk * D + (D == 128 ? row * 128 + ((piece ^ (row & 6)) << 4)
+                                  : (row ^ ((row >> 2) & 1)) * 64 + ((piece ^ (row & 2)) << 4));
+  }
+  // Starts the copy of the chunk whose first slot is row `at` of the codes.
+  __device__ __forceinline__ static void copy(const CacheAttnArgs& a, int64_t at, uint8_t* stage) {
+    constexpr int kPer = D / 16;        // pieces a row
+    constexpr int kStep = 32 / kPer;    // rows the warp copies at a time
+    const int lane = threadIdx.x & 31, piece = lane % kPer, row0 = lane / kPer;
+    const uint8_t* k = a.c.k_codes + at * D + lane * 16;
+    const uint8_t* v = a.c.v_codes + at * D + lane * 16;
+#pragma unroll
+    for (int i = 0; i < kChunk / kStep; ++i)
+      copy_async16(stage + k_at(row0 + i * kStep, piece), k + i * 512);
+#pragma unroll
+    for (int i = 0; i < kChunk / kStep; ++i)
+      copy_async16(stage + v_at(row0 + i * kStep, piece), v + i * 512);
+  }
+
   uint32_t kw[2][2][kKw];   // [16-slot step][slot g / g + 8][word]
   uint32_t vw[2][4][kVw];   // [16-slot step][slot 2t, 2t+1, 2t+8, 2t+9][word]
 
-  __device__ __forceinline__ void load_k(const CacheAttnArgs& a, const Chunk& x) {
+  __device__ __forceinline__ void read_k(const uint8_t* stage) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
-    const uint8_t* base = a.c.k_codes + x.at * D;
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
       for (int r = 0; r < 2; ++r)
 #pragma unroll
         for (int hf = 0; hf < D / 64; ++hf) {
-          const uint4 w = __ldg(reinterpret_cast<const uint4*>(
-              base + (16 * s + 8 * r + g) * D + 64 * hf + 16 * t4));
+          const uint4 w =
+              *reinterpret_cast<const uint4*>(stage + k_at(16 * s + 8 * r + g, 4 * hf + t4));
           kw[s][r][4 * hf] = w.x;
           kw[s][r][4 * hf + 1] = w.y;
           kw[s][r][4 * hf + 2] = w.z;
           kw[s][r][4 * hf + 3] = w.w;
         }
   }
-  __device__ __forceinline__ void load_v(const CacheAttnArgs& a, const Chunk& x) {
+  __device__ __forceinline__ void read_v(const uint8_t* stage) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
-    const uint8_t* base = a.c.v_codes + x.at * D;
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const uint8_t* at = base + (16 * s + 8 * (r >> 1) + 2 * t4 + (r & 1)) * D + g * (D / 8);
+        const int row = 16 * s + 8 * (r >> 1) + 2 * t4 + (r & 1);
         if constexpr (D == 128) {
-          const uint4 w = __ldg(reinterpret_cast<const uint4*>(at));
+          const uint4 w = *reinterpret_cast<const uint4*>(stage + v_at(row, g));
           vw[s][r][0] = w.x;
           vw[s][r][1] = w.y;
           vw[s][r][2] = w.z;
           vw[s][r][3] = w.w;
         } else {
-          const uint2 w = __ldg(reinterpret_cast<const uint2*>(at));
+          const uint2 w =
+              *reinterpret_cast<const uint2*>(stage + v_at(row, g >> 1) + 8 * (g & 1));
           vw[s][r][0] = w.x;
           vw[s][r][1] = w.y;
         }
@@ -486,24 +545,38 @@ struct MmaBody {
 
   __device__ __forceinline__ void scores() {
 #pragma unroll
-    for (int st = 0; st < 2; ++st) {
+    for (int st = 0; st < 2; ++st)
 #pragma unroll
       for (int n = 0; n < kNt; ++n)
 #pragma unroll
         for (int k = 0; k < 4; ++k) s[st][n][k] = 0.f;
 #pragma unroll
-      for (int ks = 0; ks < kKs; ++ks) {
+    for (int ks = 0; ks < kKs; ++ks) {
+      uint32_t b[kNt][2];
+#pragma unroll
+      for (int n = 0; n < kNt; ++n) {
+        if constexpr (kQShared) {
+          const uint2 x = qsm[(ks * kNt + n) * 32];
+          b[n][0] = x.x;
+          b[n][1] = x.y;
+        } else {
+          b[n][0] = q[ks][n][0];
+          b[n][1] = q[ks][n][1];
+        }
+      }
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {
         const uint32_t fa[4] = {e4m3x2_to_half2(static_cast<uint16_t>(kw[st][0][ks])),
                                 e4m3x2_to_half2(static_cast<uint16_t>(kw[st][1][ks])),
                                 e4m3x2_to_half2(static_cast<uint16_t>(kw[st][0][ks] >> 16)),
                                 e4m3x2_to_half2(static_cast<uint16_t>(kw[st][1][ks] >> 16))};
 #pragma unroll
-        for (int n = 0; n < kNt; ++n) mma16816(s[st][n], fa, q[ks][n][0], q[ks][n][1]);
+        for (int n = 0; n < kNt; ++n) mma16816(s[st][n], fa, b[n][0], b[n][1]);
       }
     }
   }
 
-  // Softmax of the chunk's scores into halves p[step][nt][b0, b1], and the
+  // Softmax of the chunk's scores into halves pf[step][nt][b0, b1], and the
   // running sums.  kEdge: some slot is masked for some row.
   uint32_t pf[2][kNt][2];
 
@@ -511,32 +584,37 @@ struct MmaBody {
   __device__ __forceinline__ void softmax(const CacheAttnArgs& a, const Plan& p, const Entry& e,
                                           int c, int rt, const Chunk& x) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
-    const float lvs = log2_scale(x.vs);
+    // All tiles step by step together, so that their shuffles and
+    // exponentials overlap.
+    float f[kNt][2], mx[kNt][2];
+    bool rise = false;
 #pragma unroll
     for (int n = 0; n < kNt; ++n) {
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const float f = qs[n][r] * x.ks;
-        int pos = 0;
-        if (kEdge) {
+        f[n][r] = qs[n][r] * x.ks;  // >= 0, or NaN
+        if (kEdge || a.weights) {
+          // Scores proper, -inf where masked.
           int t, h;
           row_of(a, e, c, min(rt * kTile + 8 * n + 2 * t4 + r, p.rows - 1), &t, &h);
-          pos = e.len - a.T + t;
-        }
+          const int pos = e.len - a.T + t;
 #pragma unroll
-        for (int st = 0; st < 2; ++st)
+          for (int st = 0; st < 2; ++st)
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float& y = s[st][n][2 * k + r];
-            y *= f;
-            if (kEdge) {
+            for (int k = 0; k < 2; ++k) {
+              float& y = s[st][n][2 * k + r];
+              y *= f[n][r];
               const int key = x.key0 + 16 * st + 8 * k + g;
-              if (!x.on || (x.window && (key > pos || pos - key >= a.window))) y = -INFINITY;
+              if (kEdge && (!x.on || (x.window && (key > pos || pos - key >= a.window))))
+                y = -INFINITY;
             }
-          }
+          f[n][r] = 1.f;
+        }
+        mx[n][r] = fmaxf(fmaxf(s[0][n][r], s[0][n][2 + r]), fmaxf(s[1][n][r], s[1][n][2 + r])) *
+                   f[n][r];
       }
       if (a.weights) {
-        // Scores for the weights pass: [slot][row], rows padded to even.
+        // For the weights pass: [slot][row], rows padded to even.
         const int even = (p.rows + 1) & ~1;
         const int row = rt * kTile + 8 * n + 2 * t4;
         if (row < even) {
@@ -551,42 +629,66 @@ struct MmaBody {
                   make_float2(s[st][n][2 * k], s[st][n][2 * k + 1]);
         }
       }
+    }
+#pragma unroll
+    for (int o2 = 4; o2 < 32; o2 <<= 1)
+#pragma unroll
+      for (int n = 0; n < kNt; ++n)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          mx[n][r] = fmaxf(mx[n][r], __shfl_xor_sync(0xffffffffu, mx[n][r], o2));
+#pragma unroll
+    for (int n = 0; n < kNt; ++n)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) rise |= mx[n][r] + x.lvs > M[n][r];
+    if (__any_sync(0xffffffffu, rise)) {
+#pragma unroll
+      for (int n = 0; n < kNt; ++n)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float Mn = fmaxf(M[n][r], mx[n][r] + x.lvs);
+          const float up = Mn > M[n][r] ? ex2(M[n][r] - Mn) : 1.f;
+          M[n][r] = Mn;
+#pragma unroll
+          for (int i = 0; i < kMt; ++i) {
+            o[i][n][r] *= up;
+            o[i][n][2 + r] *= up;
+          }
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < kNt; ++n) {
       float pv[2][4];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        float mx = fmaxf(fmaxf(s[0][n][r], s[0][n][2 + r]), fmaxf(s[1][n][r], s[1][n][2 + r]));
-        // The denominator: the lane's own slots, its own maximum.
-        const float mn = fmaxf(m[n][r], mx), mu = finite_or_0(mn);
+        const float Mu = finite_or_0(M[n][r]), base = kPBits + x.lvs - Mu;
         float sum = 0.f;
-#pragma unroll
-        for (int st = 0; st < 2; ++st)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) sum += ex2(s[st][n][2 * k + r] - mu);
-        l[n][r] = l[n][r] * ex2(m[n][r] - mu) + sum;
-        m[n][r] = mn;
-        // The weights: one maximum for all lanes.
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-        const float Mn = fmaxf(M[n][r], mx + lvs);
-        if (Mn > M[n][r]) {
-          const float f = ex2(M[n][r] - Mn);
-#pragma unroll
-          for (int i = 0; i < kMt; ++i) {
-            o[i][n][r] *= f;
-            o[i][n][2 + r] *= f;
-          }
-          M[n][r] = Mn;
-        }
-        const float base = kPBits + lvs - finite_or_0(M[n][r]);
 #pragma unroll
         for (int st = 0; st < 2; ++st)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const float y = s[st][n][2 * k + r];
-            const float w = ex2(y + base);
-            pv[st][2 * k + r] = kEdge && y == -INFINITY ? 0.f : w;
+            float w = ex2(fmaf(y, f[n][r], base));
+            if (kEdge && y == -INFINITY) w = 0.f;  // whatever the block's scales are
+            pv[st][2 * k + r] = w;
+            sum += w;
           }
+        // The denominator, relative to the row's largest score: from the
+        // weights, whose scale is taken out again, ...
+        const float mn = fmaxf(m[n][r], mx[n][r]), mu = finite_or_0(mn);
+        float part = sum * ex2(Mu - kPBits - x.lvs - mu);
+        if (kEdge && sum == 0.f) part = 0.f;
+        // ... unless they are too small to tell it: values 2^60 below other
+        // blocks'.
+        if (mx[n][r] + x.lvs - Mu < -60.f) {
+          part = 0.f;
+#pragma unroll
+          for (int st = 0; st < 2; ++st)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) part += ex2(fmaf(s[st][n][2 * k + r], f[n][r], -mu));
+        }
+        l[n][r] = fmaf(l[n][r], ex2(m[n][r] - mu), part);
+        m[n][r] = mn;
       }
 #pragma unroll
       for (int st = 0; st < 2; ++st) {
@@ -652,14 +754,11 @@ struct MmaBody {
     for (int n = 0; n < kNt; ++n)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        float mx = m[n][r];
-#pragma unroll
-        for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-        float sum = l[n][r] * ex2(m[n][r] - finite_or_0(mx));
+        float sum = l[n][r];  // the lane's slots'; m and M are the warp's
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
         const int row = warp * kTile + 8 * n + 2 * t4 + r;
-        if (g == 0) stat[row] = Stat{mx, sum, M[n][r] - kPBits};
+        if (g == 0) stat[row] = Stat{m[n][r], sum, M[n][r] - kPBits};
         float* to = osum + row * kLd + g * (D / 8);
 #pragma unroll
         for (int i = 0; i < kMt; ++i) {
@@ -669,7 +768,10 @@ struct MmaBody {
       }
   }
 
-  static constexpr int kSmemQ = 0;
+  // The warps' rings (and rows); their sums take the place at a unit's end.
+  static constexpr int kWarpBytes = kRingBytes + (kQShared ? kKs * kNt * 256 : 0);
+  static constexpr int kSmem = kWarps * kWarpBytes;
+  static_assert(kSmem >= kWarps * kTile * (D + 4) * 4, "sums must fit the ring");
 };
 
 // CUDA cores, fp32 throughout: 8 query rows, a lane a slot for the scores
@@ -679,8 +781,11 @@ struct SimtBody {
   static constexpr int kTile = 8;
   static constexpr int kPerSm = 3;
   static constexpr int kDl = D / 32;
-  // q rows [8][D] for the CTA, then weights [32][8] for each warp
-  static constexpr int kSmemQ = (kTile * D + kWarps * kChunk * kTile) * 4;
+  // The warps' sums, then q rows [8][D] for the CTA and weights [32][8] for
+  // each warp.
+  static constexpr int kSums = kWarps * kTile * (D + 4) * 4;
+  static constexpr int kWarpBytes = 0;
+  static constexpr int kSmem = kSums + (kTile * D + kWarps * kChunk * kTile) * 4;
 
   float o[kTile][kDl];
   float m[kTile], l[kTile], M[kTile];
@@ -689,9 +794,8 @@ struct SimtBody {
 
   __device__ __forceinline__ void begin(const CacheAttnArgs& a, const Plan& p, const Entry& e,
                                         int c, int rt, uint8_t* smem) {
-    qsm = reinterpret_cast<float*>(smem);
+    qsm = reinterpret_cast<float*>(smem + kSums);
     psm = qsm + kTile * D + (threadIdx.x >> 5) * kChunk * kTile;
-    __syncthreads();  // the last unit's rows are done with
     for (int i = threadIdx.x; i < kTile * D; i += kThreads) {
       const int r = i / D, row = rt * kTile + r;
       float v = 0.f;
@@ -739,7 +843,7 @@ struct SimtBody {
         }
     }
     const int key = x.key0 + lane;
-    const float lvs = log2_scale(x.vs);
+    const float lvs = x.lvs;
     bool any = false;
 #pragma unroll
     for (int r = 0; r < kTile; ++r) {
@@ -838,23 +942,24 @@ struct IsMma<MmaBody<D, kNt>> {
 template <int D, class Body>
 __global__ void __launch_bounds__(kThreads, Body::kPerSm) cache_attn_kernel(const CacheAttnArgs a) {
   constexpr int kTile = Body::kTile;
-  __shared__ int64_t scan[kWarps];
-  __shared__ int64_t found[2];
-  __shared__ __align__(16) float osum[kWarps * kTile * (D + 4)];
+  __shared__ uint32_t scan[kWarps];
+  __shared__ uint32_t found[2];
+  extern __shared__ __align__(128) uint8_t dyn[];
   __shared__ Stat stat[kWarps * kTile];
-  __shared__ __align__(16) uint8_t extra[Body::kSmemQ > 0 ? Body::kSmemQ : 16];
+  __shared__ __align__(16) float4 info[kWarps][8];  // of a stage: K and V scale, first slot, flags
+  float* osum = reinterpret_cast<float*>(dyn);
 
   const Plan p = plan_of(a, kTile);
   let_next_start();
   wait_for_inputs();
   const Scan sc = scan_entries<kWarps>(a, p, scan);
-  const int64_t W = sc.total * p.units;
+  const uint32_t W = sc.total * p.units;
   if (W == 0) return;
-  const int64_t P = cta_count(a, W);
-  if (blockIdx.x >= P) return;
-  const int64_t begin = cta_begin(blockIdx.x, W, P), end = cta_begin(blockIdx.x + 1, W, P);
+  const Cut cut = cut_of(a, W);
+  if (blockIdx.x >= cut.P) return;
+  const uint32_t begin = cta_begin(cut, blockIdx.x), end = cta_begin(cut, blockIdx.x + 1);
   // The entry that holds chunk `begin`, and its first chunk.
-  each_entry<kWarps>(a, p, sc, scan, [&](int i, int64_t before, int64_t n) {
+  each_entry<kWarps>(a, p, sc, scan, [&](int i, uint32_t before, uint32_t n) {
     if (begin >= before * p.units && begin < (before + n) * p.units) {
       found[0] = i;
       found[1] = before * p.units;
@@ -862,24 +967,24 @@ __global__ void __launch_bounds__(kThreads, Body::kPerSm) cache_attn_kernel(cons
   });
   __syncthreads();
   int i = static_cast<int>(found[0]);
-  int64_t base = found[1];  // first chunk of entry i
+  uint32_t base = found[1];  // first chunk of entry i
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 
   Body body;
-  for (int64_t at = begin; at < end;) {
+  for (uint32_t at = begin; at < end;) {
     Entry e = entry_at(a, i);
     while (at >= base + e.n_chunks * p.units) {
       base += e.n_chunks * p.units;
       e = entry_at(a, ++i);
     }
-    const int u = static_cast<int>((at - base) / e.n_chunks);
-    const int64_t u0 = base + u * e.n_chunks;
-    const int64_t stop = min64(end, u0 + e.n_chunks);
+    const int u = (at - base) / static_cast<uint32_t>(e.n_chunks);
+    const uint32_t u0 = base + u * e.n_chunks;
+    const uint32_t stop = min(end, u0 + e.n_chunks);
     const int c = u / p.n_tiles, rt = u - c * p.n_tiles;
     // This CTA's chunks of the unit: [x0, x1) of its n_chunks.
     const int x0 = static_cast<int>(at - u0), x1 = static_cast<int>(stop - u0);
 
-    body.begin(a, p, e, c, rt, extra);
+    body.begin(a, p, e, c, rt, IsMma<Body>::value ? dyn + warp * Body::kWarpBytes : dyn);
     if constexpr (IsMma<Body>::value) {
       // Rows of this tile: query tokens t0..t1.
       int t0, t1, h;
@@ -889,33 +994,58 @@ __global__ void __launch_bounds__(kThreads, Body::kPerSm) cache_attn_kernel(cons
       const int last = e.len - a.T + t1;                  // and last
       const int all0 = e.len - a.T + t1 - a.window + 1;   // every row's
       const int all1 = e.len - a.T + t0;
-      int x = x0 + warp;
-      if (x < x1) {
-        Ahead ahead = look_ahead(a, e, c, x + lane * kWarps, x1);
-        int used = 0;
-        Chunk cur = chunk_of(ahead, 0);
-        body.load_k(a, cur);
-        body.load_v(a, cur);
-        for (; x < x1; x += kWarps) {
-          if (++used == 32) {
-            ahead = look_ahead(a, e, c, x + kWarps + lane * kWarps, x1);
-            used = 0;
-          }
-          const bool more = x + kWarps < x1;
-          const Chunk next = chunk_of(ahead, used);
-          body.scores();
-          if (more) body.load_k(a, next);
-          const bool edge = !cur.on || (cur.window && (cur.key0 < all0 || cur.key0 + kChunk - 1 > all1));
-          if (edge) {
-            body.template softmax<true>(a, p, e, c, rt, cur);
-            body.clear_masked(cur, first, last);
-          } else {
-            body.template softmax<false>(a, p, e, c, rt, cur);
-          }
-          body.values();
-          if (more) body.load_v(a, next);
-          cur = next;
+      constexpr int kStages = Body::kStages;
+      const int n = x0 + warp < x1 ? (x1 - x0 - warp + kWarps - 1) / kWarps : 0;
+      uint8_t* ring = dyn + warp * Body::kWarpBytes;
+      Ahead ahead;
+      // Chunk k of the warp's n: its copy, then (once its scales are there)
+      // what the softmax needs of it.
+      const auto start = [&](int k) {
+        if ((k & 31) == 0) ahead = look_ahead(a, e, c, x0 + warp + (k + lane) * kWarps, x1);
+        const int64_t at = __shfl_sync(0xffffffffu, ahead.at, k & 31);
+        Body::copy(a, at, ring + (k % kStages) * Body::kStageBytes);
+      };
+      const auto note = [&](int k) {
+        if (lane == (k & 31))
+          info[warp][k % kStages] = make_float4(ahead.ks, ahead.lvs, __int_as_float(ahead.key0),
+                                                __int_as_float(ahead.flags));
+      };
+#pragma unroll
+      for (int k = 0; k < kStages; ++k) {
+        if (k < n) start(k);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      }
+#pragma unroll
+      for (int k = 0; k < kStages; ++k)
+        if (k < n) note(k);
+      for (int k = 0; k < n; ++k) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+        __syncwarp();
+        uint8_t* stage = ring + (k % kStages) * Body::kStageBytes;
+        const float4 of = info[warp][k % kStages];
+        Chunk cur;
+        cur.ks = of.x;
+        cur.lvs = of.y;
+        cur.key0 = __float_as_int(of.z);
+        cur.on = __float_as_int(of.w) & 1;
+        cur.window = __float_as_int(of.w) & 2;
+        body.read_k(stage);
+        body.scores();
+        const bool edge =
+            !cur.on || (cur.window && (cur.key0 < all0 || cur.key0 + kChunk - 1 > all1));
+        if (edge)
+          body.template softmax<true>(a, p, e, c, rt, cur);
+        else
+          body.template softmax<false>(a, p, e, c, rt, cur);
+        body.read_v(stage);
+        if (edge) body.clear_masked(cur, first, last);
+        body.values();
+        __syncwarp();
+        if (k + kStages < n) {
+          start(k + kStages);
+          note(k + kStages);
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
       }
     } else {
       int x = x0 + warp;
@@ -936,7 +1066,9 @@ __global__ void __launch_bounds__(kThreads, Body::kPerSm) cache_attn_kernel(cons
     body.finish(osum, stat);
     __syncthreads();
     const bool whole = x0 == 0 && x1 == e.n_chunks;
-    join_warps<D, kTile>(a, p, e, c, rt, osum, stat, whole, 2 * static_cast<int64_t>(blockIdx.x) + (x0 == 0));
+    join_warps<D, kTile>(a, p, e, c, rt, osum, stat, whole,
+                         2 * static_cast<int64_t>(blockIdx.x) + (x0 == 0));
+    __syncthreads();  // the sums make room for the next unit's chunks
     at = stop;
   }
 }
@@ -953,18 +1085,17 @@ __global__ void __launch_bounds__(kWpr == 1 ? kThreads : 32 * kWpr)
     cache_attn_join_kernel(const CacheAttnArgs a) {
   constexpr int kDl = D / 32;
   constexpr int kWarpsJ = kWpr == 1 ? kWarps : kWpr, kRows = kWarpsJ / kWpr;
-  __shared__ int64_t scan[kWarpsJ];
-  __shared__ int64_t found[kRows];
+  __shared__ uint32_t scan[kWarpsJ];
+  __shared__ uint32_t found[kRows];
   __shared__ float red[kWarpsJ], lsum[kWarpsJ];
   __shared__ __align__(16) float osum[kWarpsJ][kWpr == 1 ? 1 : D];
   const Plan p = plan_of(a, kTile);
   const int rows = a.c.Hkv * p.rows;  // of an entry, all KV heads
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kRows;
-  const int64_t all = static_cast<int64_t>(p.n_entries) * rows;
+  const int row0 = blockIdx.x * kRows, all = p.n_entries * rows;  // fit: the entry points check
   let_next_start();
   const Scan sc = scan_entries<kWarpsJ>(a, p, scan);
-  each_entry<kWarpsJ>(a, p, sc, scan, [&](int k, int64_t before, int64_t) {
+  each_entry<kWarpsJ>(a, p, sc, scan, [&](int k, uint32_t before, uint32_t) {
 #pragma unroll
     for (int w = 0; w < kRows; ++w)
       if ((row0 + w) / rows == k) found[w] = before;
@@ -973,8 +1104,7 @@ __global__ void __launch_bounds__(kWpr == 1 ? kThreads : 32 * kWpr)
   const int mine = kWpr == 1 ? warp : 0, part = kWpr == 1 ? 0 : warp;
   wait_for_inputs();  // every path: whoever waits for this kernel waits for the parts too
   if (row0 + mine >= all) return;
-  const int i = static_cast<int>((row0 + mine) / rows);
-  const int cm = static_cast<int>(row0 + mine - static_cast<int64_t>(i) * rows);
+  const int i = (row0 + mine) / rows, cm = row0 + mine - i * rows;
   const int c = cm / p.rows, m = cm - c * p.rows, rt = m / kTile, r = m - rt * kTile;
   const Entry e = entry_at(a, i);
   if (e.n_chunks == 0) {
@@ -982,10 +1112,9 @@ __global__ void __launch_bounds__(kWpr == 1 ? kThreads : 32 * kWpr)
     if (part == 0 && lane == 0) store_lse(a, p, e, c, m, -INFINITY);
     return;
   }
-  const int64_t W = sc.total * p.units, P = cta_count(a, W);
-  const int64_t u0 = found[mine] * p.units + static_cast<int64_t>(c * p.n_tiles + rt) * e.n_chunks;
-  const int c0 = static_cast<int>(cta_of(u0, W, P));
-  const int c1 = static_cast<int>(cta_of(u0 + e.n_chunks - 1, W, P));
+  const Cut cut = cut_of(a, sc.total * p.units);
+  const uint32_t u0 = found[mine] * p.units + (c * p.n_tiles + rt) * e.n_chunks;
+  const int c0 = cta_of(cut, u0), c1 = cta_of(cut, u0 + e.n_chunks - 1);
   if (c0 == c1) return;  // written whole
   const auto at = [&](int x) { return (2 * static_cast<int64_t>(x) + (x == c0)) * kTile + r; };
   float mx = -INFINITY;
@@ -1087,8 +1216,11 @@ __global__ void __launch_bounds__(256) cache_weights_kernel(const CacheAttnArgs 
 
 template <int D, class Body>
 cudaError_t launch_body(const CacheAttnArgs& a, cudaStream_t st) {
-  cudaError_t e = launch_after(cache_attn_kernel<D, Body>, dim3(a.n_ctas), kThreads, 0, st,
-                               a.sel_from_kernel != 0, a);
+  cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<D, Body>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, Body::kSmem);
+  if (e != cudaSuccess) return e;
+  e = launch_after(cache_attn_kernel<D, Body>, dim3(a.n_ctas), kThreads, Body::kSmem, st,
+                   a.sel_from_kernel != 0, a);
   if (e != cudaSuccess) return e;
   const int g = a.Hq / a.c.Hkv;
   const int rows = a.sel ? g : a.T * g;
@@ -1113,11 +1245,16 @@ cudaError_t launch_body(const CacheAttnArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-int cache_attn_tile_rows(int rows, int in_bf16) { return in_bf16 && rows > 8 ? 16 : 8; }
+// Tiles of 8, 16 or 32 rows: as many as the rows fill (K and V are read once
+// for each tile; a tile costs the arithmetic of all its rows, held or not).
+int cache_attn_tile_rows(int rows, int in_bf16) {
+  return !in_bf16 || rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+}
 
 int cache_attn_max_ctas(int tile_rows, int in_bf16) {
-  return kSms * (in_bf16 ? (tile_rows == 8 ? MmaBody<128, 1>::kPerSm : MmaBody<128, 2>::kPerSm)
-                         : SimtBody<128>::kPerSm);
+  return kSms * (!in_bf16         ? SimtBody<128>::kPerSm
+                 : tile_rows == 8 ? MmaBody<128, 1>::kPerSm
+                                  : MmaBody<128, 2>::kPerSm);
 }
 
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t st) {
@@ -1129,8 +1266,11 @@ cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t st) {
   if (tile == 8)
     return a.c.d == 128 ? launch_body<128, MmaBody<128, 1>>(a, st)
                         : launch_body<64, MmaBody<64, 1>>(a, st);
-  return a.c.d == 128 ? launch_body<128, MmaBody<128, 2>>(a, st)
-                      : launch_body<64, MmaBody<64, 2>>(a, st);
+  if (tile == 16)
+    return a.c.d == 128 ? launch_body<128, MmaBody<128, 2>>(a, st)
+                        : launch_body<64, MmaBody<64, 2>>(a, st);
+  return a.c.d == 128 ? launch_body<128, MmaBody<128, 4>>(a, st)
+                      : launch_body<64, MmaBody<64, 4>>(a, st);
 }
 
 }  // namespace msa

@@ -75,7 +75,8 @@ msa_status check_cache(const msa_kv_cache* c, const int32_t* table, int max_bloc
   return check_sizes(c->n_pages, c->Hkv, c->d, c->block, batch, max_blocks);
 }
 
-msa_status check_query_sizes(int Hkv, int batch, int n_q, int Hq) {
+msa_status check_query_sizes(const msa_kv_cache* c, int batch, int n_q, int Hq, int max_blocks) {
+  const int Hkv = c->Hkv, block = c->block;
   if (Hq < 1 || Hq % Hkv != 0)
     return fail(MSA_ERR_INVALID_ARG, "Hq=%d not a multiple of Hkv=%d", Hq, Hkv);
   if (n_q < 1) return fail(MSA_ERR_INVALID_ARG, "n_q=%d must be >= 1", n_q);
@@ -84,7 +85,12 @@ msa_status check_query_sizes(int Hkv, int batch, int n_q, int Hq) {
     return fail(MSA_ERR_UNSUPPORTED, "%lld query rows of a sequence and KV head (at most %d)",
                 (long long)rows, kMaxRows);
   if (static_cast<int64_t>(batch) * n_q * Hq > INT32_MAX)
-    return fail(MSA_ERR_INVALID_ARG, "batch=%d n_q=%d Hq=%d: too many rows", batch, n_q, Hq);
+    return fail(MSA_ERR_UNSUPPORTED, "batch=%d n_q=%d Hq=%d: too many rows", batch, n_q, Hq);
+  // Chunks of 32 slots of every 8 rows are counted in 32 bits.
+  if (static_cast<int64_t>(batch) * n_q * Hkv * ((Hq / Hkv + 7) / 8) >
+      INT32_MAX / (static_cast<int64_t>(max_blocks) * block / msa::kChunk + 1))
+    return fail(MSA_ERR_UNSUPPORTED, "batch=%d n_q=%d Hq=%d max_blocks=%d: too much for one call",
+                batch, n_q, Hq, max_blocks);
   return MSA_OK;
 }
 
@@ -284,7 +290,7 @@ size_t msa_cache_attn_workspace_size(const msa_kv_cache* cache, int max_blocks, 
                                      int Hq, int with_weights, msa_dtype in_dt) {
   if (!cache ||
       check_sizes(cache->n_pages, cache->Hkv, cache->d, cache->block, batch, max_blocks) != MSA_OK ||
-      check_query_sizes(cache->Hkv, batch, n_q, Hq) != MSA_OK || !valid_dtype(in_dt))
+      check_query_sizes(cache, batch, n_q, Hq, max_blocks) != MSA_OK || !valid_dtype(in_dt))
     return 0;
   return attn_plan(cache->Hkv, cache->d, cache->block, batch, n_q, Hq, max_blocks, false,
                    with_weights != 0, in_dt == MSA_BF16)
@@ -298,7 +304,7 @@ msa_status msa_cache_attn(const msa_kv_cache* cache, const void* q, const int32_
                           size_t workspace_bytes, msa_stream_t stream) {
   MSA_NVTX_RANGE();
   MSA_TRY(check_cache(cache, table, max_blocks, lens, batch));
-  MSA_TRY(check_query_sizes(cache->Hkv, batch, n_q, Hq));
+  MSA_TRY(check_query_sizes(cache, batch, n_q, Hq, max_blocks));
   MSA_TRY(check_query(q, out, lse, window, scale, in_dt, out_dt));
   if (weights) {
     if (!aligned(weights, 4)) return fail(MSA_ERR_INVALID_ARG, "weights not 4-byte aligned");
@@ -320,7 +326,7 @@ size_t msa_cache_select_workspace_size(const msa_kv_cache* cache, int max_blocks
                                        int n_q) {
   if (!cache ||
       check_sizes(cache->n_pages, cache->Hkv, cache->d, cache->block, batch, max_blocks) != MSA_OK ||
-      check_query_sizes(cache->Hkv, batch, n_q, cache->Hkv) != MSA_OK)
+      check_query_sizes(cache, batch, n_q, cache->Hkv, max_blocks) != MSA_OK)
     return 0;
   return select_plan(cache->Hkv, batch, n_q, max_blocks).total;
 }
@@ -332,7 +338,7 @@ msa_status msa_cache_select(const msa_kv_cache* cache, const void* q, const int3
                             msa_stream_t stream) {
   MSA_NVTX_RANGE();
   MSA_TRY(check_cache(cache, table, max_blocks, lens, batch));
-  MSA_TRY(check_query_sizes(cache->Hkv, batch, n_q, Hq));
+  MSA_TRY(check_query_sizes(cache, batch, n_q, Hq, max_blocks));
   if (!q || !sel || !cnt) return fail(MSA_ERR_INVALID_ARG, "null tensor pointer");
   if (!aligned(q, 16) || !aligned(sel, 4) || !aligned(cnt, 4))
     return fail(MSA_ERR_INVALID_ARG, "tensor pointer not aligned (q: 16 bytes, sel, cnt: 4)");
@@ -349,7 +355,7 @@ size_t msa_cache_attn_select_workspace_size(const msa_kv_cache* cache, int max_b
                                             int n_q, int Hq, msa_dtype in_dt) {
   if (!cache ||
       check_sizes(cache->n_pages, cache->Hkv, cache->d, cache->block, batch, max_blocks) != MSA_OK ||
-      check_query_sizes(cache->Hkv, batch, n_q, Hq) != MSA_OK || !valid_dtype(in_dt))
+      check_query_sizes(cache, batch, n_q, Hq, max_blocks) != MSA_OK || !valid_dtype(in_dt))
     return 0;
   return attn_plan(cache->Hkv, cache->d, cache->block, batch, n_q, Hq, max_blocks, true, false,
                    in_dt == MSA_BF16)
@@ -364,7 +370,7 @@ msa_status msa_cache_attn_select(const msa_kv_cache* cache, const void* q, const
                                  msa_stream_t stream) {
   MSA_NVTX_RANGE();
   MSA_TRY(check_cache(cache, table, max_blocks, lens, batch));
-  MSA_TRY(check_query_sizes(cache->Hkv, batch, n_q, Hq));
+  MSA_TRY(check_query_sizes(cache, batch, n_q, Hq, max_blocks));
   MSA_TRY(check_query(q, out, lse, window, scale, in_dt, out_dt));
   if (!sel || !cnt || !aligned(sel, 4) || !aligned(cnt, 4))
     return fail(MSA_ERR_INVALID_ARG, "sel or cnt null or not 4-byte aligned");
@@ -397,7 +403,7 @@ size_t msa_cache_attn_topk_workspace_size(const msa_kv_cache* cache, int max_blo
                                           int n_q, int Hq, int top_k, msa_dtype in_dt) {
   if (!cache ||
       check_sizes(cache->n_pages, cache->Hkv, cache->d, cache->block, batch, max_blocks) != MSA_OK ||
-      check_query_sizes(cache->Hkv, batch, n_q, Hq) != MSA_OK || !valid_dtype(in_dt) ||
+      check_query_sizes(cache, batch, n_q, Hq, max_blocks) != MSA_OK || !valid_dtype(in_dt) ||
       check_top_k(top_k, max_blocks) != MSA_OK)
     return 0;
   return topk_plan(cache, max_blocks, batch, n_q, Hq, top_k, in_dt).total;
@@ -410,7 +416,7 @@ msa_status msa_cache_attn_topk(const msa_kv_cache* cache, const void* q, const i
                                size_t workspace_bytes, msa_stream_t stream) {
   MSA_NVTX_RANGE();
   MSA_TRY(check_cache(cache, table, max_blocks, lens, batch));
-  MSA_TRY(check_query_sizes(cache->Hkv, batch, n_q, Hq));
+  MSA_TRY(check_query_sizes(cache, batch, n_q, Hq, max_blocks));
   MSA_TRY(check_query(q, out, lse, window, scale, in_dt, out_dt));
   MSA_TRY(check_top_k(top_k, max_blocks));
   const TopkPlan p = topk_plan(cache, max_blocks, batch, n_q, Hq, top_k, in_dt);

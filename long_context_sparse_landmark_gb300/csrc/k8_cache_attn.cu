@@ -390,76 +390,92 @@ __device__ __forceinline__ void join_warps(const CacheAttnArgs& a, const Plan& p
 template <int D, int kNt>
 struct MmaBody {
   static constexpr int kTile = 8 * kNt;
-  // 12 warps an SM with 16 KB of chunks under way each, or 8 with 24 KB (four
-  // tiles: 16 KB, and 8 KB for the rows, which no longer fit the registers).
+  // 12 warps an SM with 16 KB of chunks under way each, or 8 with 24 KB; the
+  // rows of four tiles no longer fit the registers.
   static constexpr int kPerSm = kNt == 1 ? 3 : 2;
-  static constexpr int kStages = (kNt == 2 ? 3 : 2) * (D == 128 ? 1 : 2);
+  static constexpr int kStages = (kNt == 1 ? 2 : 3) * (D == 128 ? 1 : 2);
   static constexpr bool kQShared = kNt > 2;
+  static constexpr int kStageBytes = 2 * kChunk * D;
+  static constexpr int kRingBytes = kStages * kStageBytes;
   static constexpr int kKs = D / 16;   // k-steps over d
   static constexpr int kMt = D / 16;   // 16-row tiles of O^T
   static constexpr int kKw = D / 16;   // words of a K row a lane holds
   static constexpr int kVw = D / 32;   // words of a V row a lane holds
 
   uint32_t q[kQShared ? 1 : kKs][kQShared ? 1 : kNt][2];
-  uint2* qsm;         // [k-step][tile][lane]
   float qs[kNt][2];   // score scale of rows 2t, 2t+1 (log2 units)
   float o[kMt][kNt][4];
   float m[kNt][2], l[kNt][2], M[kNt][2];
 
-  __device__ __forceinline__ void begin(const CacheAttnArgs& a, const Plan& p, const Entry& e,
-                                        int c, int rt, uint8_t* smem) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
-    qsm = reinterpret_cast<uint2*>(smem + kRingBytes) + lane;
+  // Rows of a unit, in shared memory for all its warps: their fragments
+  // [k-step][tile][lane], score scales and positions.
+  struct Rows {
+    uint2 q[kKs * kNt * 32];
+    float scale[kTile];
+    int pos[kTile];
+  };
+  static constexpr int kSmem = kWarps * kRingBytes + static_cast<int>(sizeof(Rows));
+  static_assert(kWarps * kRingBytes >= kWarps * kTile * (D + 4) * 4, "sums must fit the rings");
+
+  // The CTA writes them: a thread takes 16-byte pieces of rows.
+  __device__ __forceinline__ static void load_rows(const CacheAttnArgs& a, const Plan& p,
+                                                   const Entry& e, int c, int rt, uint8_t* smem) {
+    constexpr int kP = D / 8;
+    Rows& rows = *reinterpret_cast<Rows*>(smem + kWarps * kRingBytes);
+#pragma unroll 1
+    for (int i = threadIdx.x; i < kTile * kP; i += kThreads) {  // whole warps
+      const int r = i / kP, pc = i - r * kP, m = rt * kTile + r;
+      int t, h;
+      row_of(a, e, c, min(m, p.rows - 1), &t, &h);
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (m < p.rows)
+        x = *reinterpret_cast<const uint4*>(
+            static_cast<const uint16_t*>(a.q) +
+            ((static_cast<int64_t>(e.b) * a.T + t) * a.Hq + h) * D + 8 * pc);
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      float v[8], mx = 0.f;
 #pragma unroll
-    for (int n = 0; n < kNt; ++n) {
-      // The lane's pieces of row 8n + g: d = 64 hf + 16 t4 + 0..15.
-      const int row = rt * kTile + 8 * n + g;
-      float v[kKw * 4];
-      float mx = 0.f;
-#pragma unroll
-      for (int i = 0; i < kKw * 4; ++i) v[i] = 0.f;
-      if (row < p.rows) {
-        int t, h;
-        row_of(a, e, c, row, &t, &h);
-        const uint16_t* src = static_cast<const uint16_t*>(a.q) +
-                              ((static_cast<int64_t>(e.b) * a.T + t) * a.Hq + h) * D;
-#pragma unroll
-        for (int hf = 0; hf < D / 64; ++hf)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint4 x = *reinterpret_cast<const uint4*>(src + 64 * hf + 16 * t4 + 8 * k);
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              v[16 * hf + 8 * k + 2 * i] = __uint_as_float(w[i] << 16);
-              v[16 * hf + 8 * k + 2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-            }
-          }
+      for (int k = 0; k < 4; ++k) {
+        v[2 * k] = __uint_as_float(w[k] << 16);
+        v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+        mx = fmaxf(mx, fmaxf(fabsf(v[2 * k]), fabsf(v[2 * k + 1])));
       }
 #pragma unroll
-      for (int i = 0; i < kKw * 4; ++i) mx = fmaxf(mx, fabsf(v[i]));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      for (int o2 = 1; o2 < kP; o2 <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o2));
       // 2^k brings the row's largest magnitude to [2^14, 2^15).
       int k = mx > 0.f ? 14 + 127 - static_cast<int>(__float_as_uint(mx) >> 23) : 0;
       k = k > 100 ? 100 : k;
       const float up = pow2i(k);
+      // d = 64 hf + 16 t4 + 4 w + 0..3 is word w of lane t4's piece: k-step 4 hf + w.
+      const int ks = 4 * (pc >> 3) + 2 * (pc & 1);
+      uint2* to = rows.q + (ks * kNt + (r >> 3)) * 32 + (r & 7) * 4 + ((pc & 7) >> 1);
+      to[0] = make_uint2(half2_of(v[0] * up, v[1] * up), half2_of(v[2] * up, v[3] * up));
+      to[kNt * 32] = make_uint2(half2_of(v[4] * up, v[5] * up), half2_of(v[6] * up, v[7] * up));
+      if (pc == 0) {
+        rows.scale[r] = a.scale * kLog2e * pow2i(-k);
+        rows.pos[r] = e.len - a.T + t;
+      }
+    }
+  }
+
+  const Rows* rows;
+
+  __device__ __forceinline__ void begin(const uint8_t* smem) {
+    const int lane = threadIdx.x & 31, t4 = lane & 3;
+    rows = reinterpret_cast<const Rows*>(smem + kWarps * kRingBytes);
 #pragma unroll
-      for (int s = 0; s < kKs; ++s) {
-        const uint32_t b0 = half2_of(v[4 * s] * up, v[4 * s + 1] * up);
-        const uint32_t b1 = half2_of(v[4 * s + 2] * up, v[4 * s + 3] * up);
-        if constexpr (kQShared) {  // read by the same lane alone
-          qsm[(s * kNt + n) * 32] = make_uint2(b0, b1);
-        } else {
-          q[s][n][0] = b0;
-          q[s][n][1] = b1;
+    for (int n = 0; n < kNt; ++n) {
+      if constexpr (!kQShared) {
+#pragma unroll
+        for (int ks = 0; ks < kKs; ++ks) {
+          const uint2 x = rows->q[(ks * kNt + n) * 32 + lane];
+          q[ks][n][0] = x.x;
+          q[ks][n][1] = x.y;
         }
       }
-      const float mine = a.scale * kLog2e * pow2i(-k);
-      qs[n][0] = __shfl_sync(0xffffffffu, mine, 8 * t4);
-      qs[n][1] = __shfl_sync(0xffffffffu, mine, 8 * t4 + 4);
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
+        qs[n][r] = rows->scale[8 * n + 2 * t4 + r];
         m[n][r] = M[n][r] = -INFINITY;
         l[n][r] = 0.f;
       }
@@ -475,8 +491,6 @@ struct MmaBody {
   // A warp's chunks pass through a ring of its own in shared memory: K and V
   // codes as [32][D] each, 16-byte pieces (and for d = 64 rows of V) moved
   // about so that the fragment reads below meet no bank twice.
-  static constexpr int kStageBytes = 2 * kChunk * D;
-  static constexpr int kRingBytes = kStages * kStageBytes;
 
   __device__ __forceinline__ static int k_at(int row, int piece) {
     return D == 128 ? row * 128 + ((piece ^ ((row & 1) << 2)) << 4) : row * 64 + (piece << 4);
@@ -556,7 +570,7 @@ struct MmaBody {
 #pragma unroll
       for (int n = 0; n < kNt; ++n) {
         if constexpr (kQShared) {
-          const uint2 x = qsm[(ks * kNt + n) * 32];
+          const uint2 x = rows->q[(ks * kNt + n) * 32 + (threadIdx.x & 31)];
           b[n][0] = x.x;
           b[n][1] = x.y;
         } else {
@@ -580,7 +594,7 @@ struct MmaBody {
   // running sums.  kEdge: some slot is masked for some row.
   uint32_t pf[2][kNt][2];
 
-  template <bool kEdge>
+  template <bool kEdge, bool kWeights>
   __device__ __forceinline__ void softmax(const CacheAttnArgs& a, const Plan& p, const Entry& e,
                                           int c, int rt, const Chunk& x) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
@@ -593,11 +607,9 @@ struct MmaBody {
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         f[n][r] = qs[n][r] * x.ks;  // >= 0, or NaN
-        if (kEdge || a.weights) {
+        if (kEdge || kWeights) {
           // Scores proper, -inf where masked.
-          int t, h;
-          row_of(a, e, c, min(rt * kTile + 8 * n + 2 * t4 + r, p.rows - 1), &t, &h);
-          const int pos = e.len - a.T + t;
+          const int pos = rows->pos[8 * n + 2 * t4 + r];
 #pragma unroll
           for (int st = 0; st < 2; ++st)
 #pragma unroll
@@ -613,7 +625,7 @@ struct MmaBody {
         mx[n][r] = fmaxf(fmaxf(s[0][n][r], s[0][n][2 + r]), fmaxf(s[1][n][r], s[1][n][2 + r])) *
                    f[n][r];
       }
-      if (a.weights) {
+      if constexpr (kWeights) {
         // For the weights pass: [slot][row], rows padded to even.
         const int even = (p.rows + 1) & ~1;
         const int row = rt * kTile + 8 * n + 2 * t4;
@@ -767,11 +779,6 @@ struct MmaBody {
         }
       }
   }
-
-  // The warps' rings (and rows); their sums take the place at a unit's end.
-  static constexpr int kWarpBytes = kRingBytes + (kQShared ? kKs * kNt * 256 : 0);
-  static constexpr int kSmem = kWarps * kWarpBytes;
-  static_assert(kSmem >= kWarps * kTile * (D + 4) * 4, "sums must fit the ring");
 };
 
 // CUDA cores, fp32 throughout: 8 query rows, a lane a slot for the scores
@@ -784,30 +791,38 @@ struct SimtBody {
   // The warps' sums, then q rows [8][D] for the CTA and weights [32][8] for
   // each warp.
   static constexpr int kSums = kWarps * kTile * (D + 4) * 4;
-  static constexpr int kWarpBytes = 0;
-  static constexpr int kSmem = kSums + (kTile * D + kWarps * kChunk * kTile) * 4;
+  static constexpr int kSmem = kSums + (kTile * D + kTile + kWarps * kChunk * kTile) * 4;
 
   float o[kTile][kDl];
   float m[kTile], l[kTile], M[kTile];
   float* qsm;
   float* psm;
 
-  __device__ __forceinline__ void begin(const CacheAttnArgs& a, const Plan& p, const Entry& e,
-                                        int c, int rt, uint8_t* smem) {
-    qsm = reinterpret_cast<float*>(smem + kSums);
-    psm = qsm + kTile * D + (threadIdx.x >> 5) * kChunk * kTile;
+  // The CTA writes the unit's rows: q times the score scale, and positions.
+  __device__ __forceinline__ static void load_rows(const CacheAttnArgs& a, const Plan& p,
+                                                   const Entry& e, int c, int rt, uint8_t* smem) {
+    float* q = reinterpret_cast<float*>(smem + kSums);
+    int* pos = reinterpret_cast<int*>(q + kTile * D);
+#pragma unroll 1
     for (int i = threadIdx.x; i < kTile * D; i += kThreads) {
       const int r = i / D, row = rt * kTile + r;
+      int t, h;
+      row_of(a, e, c, min(row, p.rows - 1), &t, &h);
       float v = 0.f;
-      if (row < p.rows) {
-        int t, h;
-        row_of(a, e, c, row, &t, &h);
+      if (row < p.rows)
         v = static_cast<const float*>(
             a.q)[((static_cast<int64_t>(e.b) * a.T + t) * a.Hq + h) * D + (i - r * D)];
-      }
-      qsm[i] = v * (a.scale * kLog2e);
+      q[i] = v * (a.scale * kLog2e);
+      if (i == r * D) pos[r] = e.len - a.T + t;
     }
-    __syncthreads();
+  }
+
+  const int* pos;
+
+  __device__ __forceinline__ void begin(uint8_t* smem) {
+    qsm = reinterpret_cast<float*>(smem + kSums);
+    pos = reinterpret_cast<const int*>(qsm + kTile * D);
+    psm = qsm + kTile * D + kTile + (threadIdx.x >> 5) * kChunk * kTile;
 #pragma unroll
     for (int r = 0; r < kTile; ++r) {
       m[r] = M[r] = -INFINITY;
@@ -847,11 +862,7 @@ struct SimtBody {
     bool any = false;
 #pragma unroll
     for (int r = 0; r < kTile; ++r) {
-      const int row = min(rt * kTile + r, p.rows - 1);
-      int t, h;
-      row_of(a, e, c, row, &t, &h);
-      const int pos = e.len - a.T + t;
-      const bool in = x.on && (!x.window || (key <= pos && pos - key < a.window));
+      const bool in = x.on && (!x.window || (key <= pos[r] && pos[r] - key < a.window));
       any |= in;
       s[r] = in ? s[r] * x.ks : -INFINITY;
     }
@@ -984,19 +995,10 @@ __global__ void __launch_bounds__(kThreads, Body::kPerSm) cache_attn_kernel(cons
     // This CTA's chunks of the unit: [x0, x1) of its n_chunks.
     const int x0 = static_cast<int>(at - u0), x1 = static_cast<int>(stop - u0);
 
-    body.begin(a, p, e, c, rt, IsMma<Body>::value ? dyn + warp * Body::kWarpBytes : dyn);
     if constexpr (IsMma<Body>::value) {
-      // Rows of this tile: query tokens t0..t1.
-      int t0, t1, h;
-      row_of(a, e, c, rt * kTile, &t0, &h);
-      row_of(a, e, c, min((rt + 1) * kTile, p.rows) - 1, &t1, &h);
-      const int first = e.len - a.T + t0 - a.window + 1;  // any row's first slot
-      const int last = e.len - a.T + t1;                  // and last
-      const int all0 = e.len - a.T + t1 - a.window + 1;   // every row's
-      const int all1 = e.len - a.T + t0;
       constexpr int kStages = Body::kStages;
       const int n = x0 + warp < x1 ? (x1 - x0 - warp + kWarps - 1) / kWarps : 0;
-      uint8_t* ring = dyn + warp * Body::kWarpBytes;
+      uint8_t* ring = dyn + warp * Body::kRingBytes;
       Ahead ahead;
       // Chunk k of the warp's n: its copy, then (once its scales are there)
       // what the softmax needs of it.
@@ -1015,9 +1017,16 @@ __global__ void __launch_bounds__(kThreads, Body::kPerSm) cache_attn_kernel(cons
         if (k < n) start(k);
         asm volatile("cp.async.commit_group;" ::: "memory");
       }
+      Body::load_rows(a, p, e, c, rt, dyn);
 #pragma unroll
       for (int k = 0; k < kStages; ++k)
         if (k < n) note(k);
+      __syncthreads();
+      body.begin(dyn);
+      const int pos0 = body.rows->pos[0];  // the first row's position, the last's
+      const int pos1 = body.rows->pos[min(kTile, p.rows - rt * kTile) - 1];
+      const int first = pos0 - a.window + 1, last = pos1;  // slots that some row attends
+      const int all0 = pos1 - a.window + 1, all1 = pos0;   // slots that every row attends
       for (int k = 0; k < n; ++k) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
         __syncwarp();
@@ -1033,10 +1042,16 @@ __global__ void __launch_bounds__(kThreads, Body::kPerSm) cache_attn_kernel(cons
         body.scores();
         const bool edge =
             !cur.on || (cur.window && (cur.key0 < all0 || cur.key0 + kChunk - 1 > all1));
-        if (edge)
-          body.template softmax<true>(a, p, e, c, rt, cur);
-        else
-          body.template softmax<false>(a, p, e, c, rt, cur);
+        if (a.weights) {
+          if (edge)
+            body.template softmax<true, true>(a, p, e, c, rt, cur);
+          else
+            body.template softmax<false, true>(a, p, e, c, rt, cur);
+        } else if (edge) {
+          body.template softmax<true, false>(a, p, e, c, rt, cur);
+        } else {
+          body.template softmax<false, false>(a, p, e, c, rt, cur);
+        }
         body.read_v(stage);
         if (edge) body.clear_masked(cur, first, last);
         body.values();
@@ -1048,6 +1063,9 @@ __global__ void __launch_bounds__(kThreads, Body::kPerSm) cache_attn_kernel(cons
         asm volatile("cp.async.commit_group;" ::: "memory");
       }
     } else {
+      body.load_rows(a, p, e, c, rt, dyn);
+      __syncthreads();
+      body.begin(dyn);
       int x = x0 + warp;
       if (x < x1) {
         Ahead ahead = look_ahead(a, e, c, x + lane * kWarps, x1);

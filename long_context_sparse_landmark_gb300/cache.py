@@ -24,13 +24,20 @@ from . import _binding as B
 _E4M3 = torch.float8_e4m3fn
 
 
+_INT32, _F32, _BF16 = torch.int32, torch.float32, torch.bfloat16
+_CODES, _INPUTS = (_E4M3, torch.uint8), (_F32, _BF16)
+
+
 def _want(t: torch.Tensor, what: str, dtypes, shape, dev: int):
+    """Raise unless t has one of the dtypes, the shape and the device (that it
+    is contiguous the binding checks)."""
+    if t.dtype in dtypes and t.shape == shape and t.get_device() == dev:
+        return
     if t.dtype not in dtypes:
         raise TypeError(f"{what} must be {' or '.join(str(x) for x in dtypes)}, not {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if t.get_device() != dev or not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous and on cuda:{dev}")
+    raise ValueError(f"{what} must be on cuda:{dev}, not {t.device}")
 
 
 class KVCache:
@@ -49,16 +56,19 @@ class KVCache:
         shape = k_codes.shape
         n, h, block, d = shape
         dev = k_codes.get_device()
-        _want(k_codes, "k_codes", (_E4M3, torch.uint8), shape, dev)
-        _want(v_codes, "v_codes", (_E4M3, torch.uint8), shape, dev)
-        _want(k_scale, "k_scale", (torch.float32,), (n, h), dev)
-        _want(v_scale, "v_scale", (torch.float32,), (n, h), dev)
-        _want(k_mean, "k_mean", (torch.bfloat16,), (n, h, d), dev)
+        _want(k_codes, "k_codes", _CODES, shape, dev)
+        _want(v_codes, "v_codes", _CODES, shape, dev)
+        _want(k_scale, "k_scale", (_F32,), (n, h), dev)
+        _want(v_scale, "v_scale", (_F32,), (n, h), dev)
+        _want(k_mean, "k_mean", (_BF16,), (n, h, d), dev)
         self.k_codes, self.v_codes = k_codes, v_codes
         self.k_scale, self.v_scale, self.k_mean = k_scale, v_scale, k_mean
         self.n_pages, self.Hkv, self.block, self.d = n, h, block, d
         self.device = k_codes.device
         self.index = dev
+        for t in (k_codes, v_codes, k_scale, v_scale, k_mean):
+            if not t.is_contiguous():
+                raise ValueError("the pool's tensors must be contiguous")
         self.struct = B.KvCacheStruct(k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(),
                                       v_scale.data_ptr(), k_mean.data_ptr(), n, h, d, block)
         self.ref = ctypes.byref(self.struct)
@@ -68,23 +78,28 @@ class KVCache:
         """A pool of n_pages pages; nothing in it needs a value before the
         first append."""
         codes = torch.empty((2, n_pages, Hkv, block, d), dtype=torch.uint8, device=device)
-        scale = torch.empty((2, n_pages, Hkv), dtype=torch.float32, device=device)
+        scale = torch.empty((2, n_pages, Hkv), dtype=_F32, device=device)
         mean = torch.empty((n_pages, Hkv, d), dtype=torch.bfloat16, device=device)
         return cls(codes[0].view(_E4M3), codes[1].view(_E4M3), scale[0], scale[1], mean)
 
 
 def _batch(cache: KVCache, table: torch.Tensor, lens: torch.Tensor):
-    if table.dim() != 2:
+    """Checks a batch's block table and lengths; returns their sizes."""
+    shape = table.shape
+    if len(shape) != 2:
         raise ValueError("block_table must be [batch, max_blocks]")
-    _want(table, "block_table", (torch.int32,), table.shape, cache.index)
-    _want(lens, "lens", (torch.int32,), (table.shape[0],), cache.index)
+    _want(table, "block_table", (_INT32,), shape, cache.index)
+    _want(lens, "lens", (_INT32,), shape[:1], cache.index)
+    return shape
 
 
-def _query(cache: KVCache, q: torch.Tensor, table: torch.Tensor):
-    if q.dim() != 4:
+def _query(cache: KVCache, q: torch.Tensor, batch: int):
+    """Checks query tokens; returns n_q and Hq."""
+    shape = q.shape
+    if len(shape) != 4:
         raise ValueError("q must be [batch, n_q, Hq, d]")
-    _want(q, "q", (torch.float32, torch.bfloat16),
-          (table.shape[0], q.shape[1], q.shape[2], cache.d), cache.index)
+    _want(q, "q", _INPUTS, (batch, shape[1], shape[2], cache.d), cache.index)
+    return shape[1], shape[2]
 
 
 def _run(cache: KVCache, stream, call):
@@ -111,12 +126,12 @@ def cache_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, cu: torch.Ten
     the lengths with them; no sequence has more than max_new of them.
     block_table [batch, max_blocks] int32 names the pages.
     """
-    _batch(cache, block_table, lens)
+    b, _ = _batch(cache, block_table, lens)
     if k.dim() != 3:
         raise ValueError("k must be [total, Hkv, d]")
-    _want(k, "k", (torch.float32, torch.bfloat16), (k.shape[0], cache.Hkv, cache.d), cache.index)
+    _want(k, "k", _INPUTS, (k.shape[0], cache.Hkv, cache.d), cache.index)
     _want(v, "v", (k.dtype,), k.shape, cache.index)
-    _want(cu, "cu", (torch.int32,), (block_table.shape[0] + 1,), cache.index)
+    _want(cu, "cu", (_INT32,), (b + 1,), cache.index)
     _run(cache, stream, lambda s: B.cache_append(cache.ref, k, v, cu, max_new, block_table, lens,
                                                  stream=s))
 
@@ -130,23 +145,22 @@ def cache_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
     over the last ``window`` slots (None: all).  ``weights`` [batch, Hkv, ld]
     fp32, ld >= max_blocks * block, is added the softmax weight each slot
     drew.  Returns (out [batch, n_q, Hq, d], lse [batch, Hq, n_q] fp32)."""
-    _batch(cache, block_table, lens)
-    _query(cache, q, block_table)
-    b, n_q, Hq, d = q.shape
-    nb = block_table.shape[1]
+    b, nb = _batch(cache, block_table, lens)
+    n_q, Hq = _query(cache, q, b)
+    d = cache.d
     window = nb * cache.block if window is None else int(window)
     scale = 1.0 / math.sqrt(d) if scale is None else scale
     if weights is not None:
         if weights.dim() != 3:
             raise ValueError("weights must be [batch, Hkv, ld]")
-        _want(weights, "weights", (torch.float32,), (b, cache.Hkv, weights.shape[2]), cache.index)
+        _want(weights, "weights", (_F32,), (b, cache.Hkv, weights.shape[2]), cache.index)
 
     def call(s):
-        out = torch.empty((b, n_q, Hq, d), dtype=out_dtype or q.dtype, device=q.device)
-        lse = torch.empty((b, Hq, n_q), dtype=torch.float32, device=q.device)
+        out = torch.empty((b, n_q, Hq, d), dtype=out_dtype or q.dtype, device=cache.device)
+        lse = torch.empty((b, Hq, n_q), dtype=_F32, device=cache.device)
         ws = torch.empty((B.cache_attn_workspace_size(cache.ref, nb, b, n_q, Hq,
                                                       weights is not None, q.dtype),),
-                         dtype=torch.uint8, device=q.device)
+                         dtype=torch.uint8, device=cache.device)
         B.cache_attn(cache.ref, q, block_table, lens, window, scale, out, lse, weights, ws,
                      stream=s)
         return out, lse
@@ -160,17 +174,15 @@ def cache_block_select(q: torch.Tensor, cache: KVCache, block_table: torch.Tenso
     n_q, Hq, d] and KV head scores best by their mean keys
     (msa_cache_select).  Returns (sel [batch, n_q, Hkv, top_k] int32
     ascending, then -1; cnt [batch, n_q, Hkv] int32)."""
-    _batch(cache, block_table, lens)
-    _query(cache, q, block_table)
-    b, n_q = q.shape[:2]
-    nb = block_table.shape[1]
+    b, nb = _batch(cache, block_table, lens)
+    n_q, _ = _query(cache, q, b)
     top_k = min(int(top_k), nb)
 
     def call(s):
-        sel = torch.empty((b, n_q, cache.Hkv, top_k), dtype=torch.int32, device=q.device)
-        cnt = torch.empty((b, n_q, cache.Hkv), dtype=torch.int32, device=q.device)
+        sel = torch.empty((b, n_q, cache.Hkv, top_k), dtype=_INT32, device=cache.device)
+        cnt = torch.empty((b, n_q, cache.Hkv), dtype=_INT32, device=cache.device)
         ws = torch.empty((B.cache_select_workspace_size(cache.ref, nb, b, n_q),),
-                         dtype=torch.uint8, device=q.device)
+                         dtype=torch.uint8, device=cache.device)
         B.cache_select(cache.ref, q, block_table, lens, window, top_k, sel, cnt, ws, stream=s)
         return sel, cnt
 
@@ -183,19 +195,18 @@ def cache_topk_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Ten
                          stream=None):
     """``cache_attention`` over each query token's window and its own top_k
     blocks (msa_cache_attn_topk).  Returns (out, lse)."""
-    _batch(cache, block_table, lens)
-    _query(cache, q, block_table)
-    b, n_q, Hq, d = q.shape
-    nb = block_table.shape[1]
+    b, nb = _batch(cache, block_table, lens)
+    n_q, Hq = _query(cache, q, b)
+    d = cache.d
     top_k = min(int(top_k), nb)
     scale = 1.0 / math.sqrt(d) if scale is None else scale
 
     def call(s):
-        out = torch.empty((b, n_q, Hq, d), dtype=out_dtype or q.dtype, device=q.device)
-        lse = torch.empty((b, Hq, n_q), dtype=torch.float32, device=q.device)
+        out = torch.empty((b, n_q, Hq, d), dtype=out_dtype or q.dtype, device=cache.device)
+        lse = torch.empty((b, Hq, n_q), dtype=_F32, device=cache.device)
         ws = torch.empty((B.cache_attn_topk_workspace_size(cache.ref, nb, b, n_q, Hq, top_k,
                                                            q.dtype),),
-                         dtype=torch.uint8, device=q.device)
+                         dtype=torch.uint8, device=cache.device)
         B.cache_attn_topk(cache.ref, q, block_table, lens, window, top_k, scale, out, lse, ws,
                           stream=s)
         return out, lse
@@ -212,19 +223,18 @@ def cache_evict(cache: KVCache, block_table: torch.Tensor, lens: torch.Tensor,
     dst_blocks], which must not be among those in use.  Returns (new_lens
     [batch] int32, kept [batch, Hkv, budget] int32 slots ascending, then -1,
     new_weights [batch, Hkv, dst_blocks * block] fp32)."""
-    _batch(cache, block_table, lens)
-    b, h = block_table.shape[0], cache.Hkv
+    b, h = _batch(cache, block_table, lens)[0], cache.Hkv
     if weights.dim() != 3 or dst_table.dim() != 2:
         raise ValueError("weights must be [batch, Hkv, ld], dst_table [batch, dst_blocks]")
-    _want(weights, "weights", (torch.float32,), (b, h, weights.shape[2]), cache.index)
-    _want(dst_table, "dst_table", (torch.int32,), (b, dst_table.shape[1]), cache.index)
+    _want(weights, "weights", (_F32,), (b, h, weights.shape[2]), cache.index)
+    _want(dst_table, "dst_table", (_INT32,), (b, dst_table.shape[1]), cache.index)
     budget = int(budget)
     if budget < 1:
         raise ValueError("budget must be >= 1")
 
     def call(s):
-        new_lens = torch.empty((b,), dtype=torch.int32, device=cache.device)
-        kept = torch.empty((b, h, budget), dtype=torch.int32, device=cache.device)
+        new_lens = torch.empty((b,), dtype=_INT32, device=cache.device)
+        kept = torch.empty((b, h, budget), dtype=_INT32, device=cache.device)
         new_w = torch.empty((b, h, dst_table.shape[1] * cache.block), dtype=torch.float32,
                             device=cache.device)
         B.cache_evict(cache.ref, block_table, lens, weights, dst_table, budget, recent, new_lens,

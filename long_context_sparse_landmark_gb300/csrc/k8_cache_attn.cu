@@ -798,7 +798,7 @@ struct SimtBody {
   float* qsm;
   float* psm;
 
-  // The CTA writes the unit's rows: q times the score scale, and positions.
+  // The CTA writes the unit's rows and their positions.
   __device__ __forceinline__ static void load_rows(const CacheAttnArgs& a, const Plan& p,
                                                    const Entry& e, int c, int rt, uint8_t* smem) {
     float* q = reinterpret_cast<float*>(smem + kSums);
@@ -812,7 +812,7 @@ struct SimtBody {
       if (row < p.rows)
         v = static_cast<const float*>(
             a.q)[((static_cast<int64_t>(e.b) * a.T + t) * a.Hq + h) * D + (i - r * D)];
-      q[i] = v * (a.scale * kLog2e);
+      q[i] = v;
       if (i == r * D) pos[r] = e.len - a.T + t;
     }
   }
@@ -839,7 +839,7 @@ struct SimtBody {
     float s[kTile];
 #pragma unroll
     for (int r = 0; r < kTile; ++r) s[r] = 0.f;
-#pragma unroll 2
+#pragma unroll 1
     for (int d0 = 0; d0 < D; d0 += 16) {
       const uint4 w4 = __ldg(reinterpret_cast<const uint4*>(krow + d0));
       const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
@@ -858,13 +858,20 @@ struct SimtBody {
         }
     }
     const int key = x.key0 + lane;
-    const float lvs = x.lvs;
+    // Scores in log2 units as a float and what it leaves, and maxima rounded
+    // up to whole numbers: the exponentials see differences whose error goes by
+    // their own size, and a change of maximum scales by a power of two.
+    const float c_hi = a.scale * kLog2e;
+    const float c_lo = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634 - c_hi);
+    float lo[kTile];
     bool any = false;
 #pragma unroll
     for (int r = 0; r < kTile; ++r) {
       const bool in = x.on && (!x.window || (key <= pos[r] && pos[r] - key < a.window));
       any |= in;
-      s[r] = in ? s[r] * x.ks : -INFINITY;
+      const float y = s[r] * x.ks, t = y * c_hi;
+      lo[r] = in && !isinf(t) ? fmaf(y, c_hi, -t) + y * c_lo : 0.f;
+      s[r] = in ? t : -INFINITY;
     }
     if (a.weights) {
       const int even = (p.rows + 1) & ~1;
@@ -873,25 +880,26 @@ struct SimtBody {
                   ((static_cast<int64_t>(e.b) * a.c.Hkv + c) * slots + key) * even + rt * kTile;
 #pragma unroll
       for (int r = 0; r < kTile; ++r)
-        if (rt * kTile + r < even) to[r] = s[r];
+        if (rt * kTile + r < even) to[r] = s[r] + lo[r];
     }
     float pw[kTile];
 #pragma unroll
     for (int r = 0; r < kTile; ++r) {
-      const float mn = fmaxf(m[r], s[r]), mu = finite_or_0(mn);
-      l[r] = l[r] * ex2(m[r] - mu) + ex2(s[r] - mu);
+      const float mn = fmaxf(m[r], ceilf(s[r])), mu = finite_or_0(mn);
+      l[r] = l[r] * exp2f(m[r] - mu) + exp2f((s[r] - mu) + lo[r]);
       m[r] = mn;
       float mx = s[r];
 #pragma unroll
       for (int x2 = 16; x2 > 0; x2 >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x2));
-      const float Mn = fmaxf(M[r], mx + lvs);
+      const float Mn = fmaxf(M[r], ceilf(mx + x.lvs));
       if (Mn > M[r]) {
-        const float f = ex2(M[r] - Mn);
+        const float f = exp2f(M[r] - Mn);
 #pragma unroll
         for (int k = 0; k < kDl; ++k) o[r][k] *= f;
         M[r] = Mn;
       }
-      pw[r] = s[r] == -INFINITY ? 0.f : ex2(s[r] + lvs - finite_or_0(M[r]));
+      pw[r] = s[r] == -INFINITY ? 0.f
+                                : exp2f((s[r] - (finite_or_0(M[r]) - x.lvs)) + lo[r]);
     }
     __syncwarp();
     *reinterpret_cast<float4*>(psm + lane * kTile) = make_float4(pw[0], pw[1], pw[2], pw[3]);

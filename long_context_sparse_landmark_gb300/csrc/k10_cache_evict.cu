@@ -37,6 +37,12 @@ __device__ __forceinline__ uint32_t weight_key(float x) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+// And back (a -0 comes back as 0, a NaN as the standard one).
+__device__ __forceinline__ float key_weight(uint32_t k) {
+  if (k == 0xffffffffu) return __uint_as_float(0x7fc00000u);
+  return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
+
 // kStaged: the keys stay in shared memory (kKeysMax of them at most).
 template <bool kStaged>
 __global__ void __launch_bounds__(kEvictThreads) cache_evict_kernel(const EvictArgs a) {
@@ -115,16 +121,20 @@ __global__ void __launch_bounds__(kEvictThreads) cache_evict_kernel(const EvictA
       // threads' order is that of falling keys.
       const int at = 4 * (kEvictThreads - 1 - threadIdx.x);
       int4 s = *reinterpret_cast<const int4*>(&hist[pass][at]);
+      if (ranks > 1) {
+        int4 y[kClusterMax - 1];  // all under way at once
 #pragma unroll
-      for (int r = 1; r < kClusterMax; ++r) {
-        if (r >= ranks) break;
-        const int4 y = *reinterpret_cast<const int4*>(
-            cl.map_shared_rank(&hist[pass][0], rank + r < ranks ? rank + r : rank + r - ranks) +
-            at);
-        s.x += y.x;
-        s.y += y.y;
-        s.z += y.z;
-        s.w += y.w;
+        for (int r = 1; r < kClusterMax; ++r)
+          y[r - 1] = r < ranks ? *reinterpret_cast<const int4*>(
+                                     cl.map_shared_rank(&hist[pass][0], (rank + r) & (ranks - 1)) + at)
+                               : make_int4(0, 0, 0, 0);
+#pragma unroll
+        for (int r = 1; r < kClusterMax; ++r) {
+          s.x += y[r - 1].x;
+          s.y += y[r - 1].y;
+          s.z += y[r - 1].z;
+          s.w += y[r - 1].w;
+        }
       }
       const int sum = s.x + s.y + s.z + s.w;
       int upto = sum;
@@ -207,7 +217,7 @@ __global__ void __launch_bounds__(kEvictThreads) cache_evict_kernel(const EvictA
     if (up || (eq && ae < left)) {
       const int at = au + min(ae, left);
       out[at] = i;
-      out_w[at] = w[i];
+      out_w[at] = key_weight(k);
     }
     before_above += __popc(mu);
     before_equal += __popc(me);

@@ -115,15 +115,25 @@ struct Raw<false> {
   }
 };
 
-// Codes of scale s rounded again to the scale 1 / inv.
+// Codes of scale s rounded again to the scale 1 / inv >= s, in halves: code *
+// 2^-k is exact in them down to 2^-24, and what is smaller than that is far
+// below the 2^-10 at which e4m3 rounds to its least value.
 __device__ __forceinline__ uint4 rescale(const uint4& x, float s, float inv) {
+  const __half2 f = __float2half2_rn(s * inv);
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   uint32_t c[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float f[4];
-    e4m3x4_to_float(w[i], f);
-    c[i] = encode4(f[0] * s, f[1] * s, f[2] * s, f[3] * s, inv);
+    const uint32_t a = e4m3x2_to_half2(static_cast<uint16_t>(w[i]));
+    const uint32_t b = e4m3x2_to_half2(static_cast<uint16_t>(w[i] >> 16));
+    const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&a), f);
+    const __half2 z = __hmul2(*reinterpret_cast<const __half2*>(&b), f);
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;"
+        : "=h"(lo) : "r"(*reinterpret_cast<const uint32_t*>(&y)));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;"
+        : "=h"(hi) : "r"(*reinterpret_cast<const uint32_t*>(&z)));
+    c[i] = static_cast<uint32_t>(lo) | static_cast<uint32_t>(hi) << 16;
   }
   return make_uint4(c[0], c[1], c[2], c[3]);
 }
@@ -267,7 +277,7 @@ __global__ void __launch_bounds__(kMaxThreads, kMaxThreads == 512 ? 1 : kBf16 ? 
 // Kept slots of one (sequence, head) into block j of its new pages, K and V:
 // blockIdx.x = (j, head), blockIdx.y = sequence.
 template <int kMaxThreads>
-__global__ void __launch_bounds__(kMaxThreads, kMaxThreads == 512 ? 1 : 6)
+__global__ void __launch_bounds__(kMaxThreads, kMaxThreads == 512 ? 1 : 7)
     cache_gather_kernel(const GatherArgs a) {
   __shared__ uint32_t red[2][32];
   __shared__ int sums[128];

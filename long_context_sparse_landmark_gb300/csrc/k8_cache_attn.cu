@@ -240,9 +240,9 @@ __device__ __forceinline__ Ahead look_ahead(const CacheAttnArgs& a, const Entry&
   if (x < x_win) {
     const int64_t u = (static_cast<int64_t>(e.b) * a.T + e.t) * a.c.Hkv + c;
     const int i = x >> per_log2;
-    const int64_t cnt = sel_count_checked(a.cnt[u], a.top_k, e.n_cand, a.status);
-    if (i >= cnt) return r;
-    const int blk = sel_block_checked(a.sel[u * a.top_k + i], e.n_cand, a.status);
+    const int32_t cnt = a.cnt[u], chosen = a.sel[u * a.top_k + i];
+    if (i >= sel_count_checked(cnt, a.top_k, e.n_cand, a.status)) return r;
+    const int blk = sel_block_checked(chosen, e.n_cand, a.status);
     slot = (blk << a.c.lb) + (x - (i << per_log2)) * kChunk;
     r.flags = 1;
   } else {
@@ -598,8 +598,10 @@ struct MmaBody {
   __device__ __forceinline__ void softmax(const CacheAttnArgs& a, const Plan& p, const Entry& e,
                                           int c, int rt, const Chunk& x) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
-    // All tiles step by step together, so that their shuffles and
-    // exponentials overlap.
+    // The maxima M and m are not kept up to the last bit: a weight may exceed
+    // 2^14 by a factor 2^1.5 (the half's range allows it) and a term of the
+    // denominator 2^40, so that most chunks move neither them nor the sums,
+    // and the lanes need not agree on a maximum.
     float f[kNt][2], mx[kNt][2];
     bool rise = false;
 #pragma unroll
@@ -643,24 +645,24 @@ struct MmaBody {
       }
     }
 #pragma unroll
-    for (int o2 = 4; o2 < 32; o2 <<= 1)
-#pragma unroll
-      for (int n = 0; n < kNt; ++n)
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-          mx[n][r] = fmaxf(mx[n][r], __shfl_xor_sync(0xffffffffu, mx[n][r], o2));
-#pragma unroll
     for (int n = 0; n < kNt; ++n)
 #pragma unroll
-      for (int r = 0; r < 2; ++r) rise |= mx[n][r] + x.lvs > M[n][r];
+      for (int r = 0; r < 2; ++r)
+        rise |= mx[n][r] + x.lvs > M[n][r] + 1.5f || mx[n][r] > m[n][r] + 40.f;
     if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
       for (int n = 0; n < kNt; ++n)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const float Mn = fmaxf(M[n][r], mx[n][r] + x.lvs);
+          float top = mx[n][r];
+#pragma unroll
+          for (int o2 = 4; o2 < 32; o2 <<= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o2));
+          const float Mn = fmaxf(M[n][r], top + x.lvs), mn = fmaxf(m[n][r], top);
           const float up = Mn > M[n][r] ? ex2(M[n][r] - Mn) : 1.f;
+          l[n][r] *= mn > m[n][r] ? ex2(m[n][r] - mn) : 1.f;
           M[n][r] = Mn;
+          m[n][r] = mn;
 #pragma unroll
           for (int i = 0; i < kMt; ++i) {
             o[i][n][r] *= up;
@@ -685,10 +687,10 @@ struct MmaBody {
             pv[st][2 * k + r] = w;
             sum += w;
           }
-        // The denominator, relative to the row's largest score: from the
-        // weights, whose scale is taken out again, ...
-        const float mn = fmaxf(m[n][r], mx[n][r]), mu = finite_or_0(mn);
-        float part = sum * ex2(Mu - kPBits - x.lvs - mu);
+        // The denominator, in units of 2^m: from the weights, whose scale is
+        // taken out again, ...
+        const float mu = finite_or_0(m[n][r]);
+        float part = sum * ex2(-base - mu);
         if (kEdge && sum == 0.f) part = 0.f;
         // ... unless they are too small to tell it: values 2^60 below other
         // blocks'.
@@ -699,8 +701,7 @@ struct MmaBody {
 #pragma unroll
             for (int k = 0; k < 2; ++k) part += ex2(fmaf(s[st][n][2 * k + r], f[n][r], -mu));
         }
-        l[n][r] = fmaf(l[n][r], ex2(m[n][r] - mu), part);
-        m[n][r] = mn;
+        l[n][r] += part;
       }
 #pragma unroll
       for (int st = 0; st < 2; ++st) {
@@ -1197,47 +1198,74 @@ __global__ void __launch_bounds__(kWpr == 1 ? kThreads : 32 * kWpr)
 }
 
 // weights[b, c, j] += sum over the rows of KV head c of their probability of
-// slot j, from the scores the attention left.  A thread a slot: no atomics,
-// rows summed in order.
+// slot j, from the scores the attention left.  A thread kSlotsT slots, 256
+// apart: no atomics, rows summed in order; HBM bounds the reading of the
+// scores.
+constexpr int kSlotsT = 4;
+
 __global__ void __launch_bounds__(256) cache_weights_kernel(const CacheAttnArgs a) {
   extern __shared__ float lse[];
   const int rows = a.T * (a.Hq / a.c.Hkv), even = (rows + 1) & ~1;
   const int c = blockIdx.y % a.c.Hkv, b = blockIdx.y / a.c.Hkv;
-  const int64_t len = cache_len(a.s, b, a.c.block, a.status);
-  const int64_t j = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  const int64_t lo = max(0, static_cast<int>(len) - a.T - a.window + 1);
-  if (static_cast<int64_t>(blockIdx.x) * blockDim.x >= len) {
-    wait_for_inputs();
-    return;
-  }
-  const int64_t u = static_cast<int64_t>(b) * a.c.Hkv + c;
+  const int len = cache_len(a.s, b, a.c.block, a.status);
+  const int lo = max(0, len - a.T - a.window + 1);
   wait_for_inputs();
-  for (int r = threadIdx.x; r < rows; r += blockDim.x) lse[r] = a.lse2[u * even + r];
+  const int64_t u = static_cast<int64_t>(b) * a.c.Hkv + c;
+  for (int r = threadIdx.x; r < rows; r += 256) lse[r] = a.lse2[u * even + r];
   __syncthreads();
-  if (j < lo || j >= len) return;
-  const int64_t slots = static_cast<int64_t>(a.s.max_blocks) * a.c.block;
-  const float* s = a.scores + (u * slots + j) * even;
-  float sum = 0.f;
-  // A row that attends nothing (lse -inf) has scores of -inf alone.
-  const auto add = [&](float x, int r) { sum += x == -INFINITY ? 0.f : ex2(x - lse[r]); };
-  if ((even & 3) == 0) {
-    for (int r = 0; r < rows; r += 4) {
-      const float4 x = __ldcs(reinterpret_cast<const float4*>(s + r));
-      add(x.x, r);
-      if (r + 1 < rows) add(x.y, r + 1);
-      if (r + 2 < rows) add(x.z, r + 2);
-      if (r + 3 < rows) add(x.w, r + 3);
+  for (int64_t j0 = static_cast<int64_t>(blockIdx.x) * 256 * kSlotsT; j0 < len;
+       j0 += static_cast<int64_t>(gridDim.x) * 256 * kSlotsT) {
+    const float* s = a.scores + (u * a.s.max_blocks * a.c.block + j0 + threadIdx.x) * even;
+    float* to = a.weights + u * a.weights_ld + j0 + threadIdx.x;
+    float sum[kSlotsT], had[kSlotsT];
+    bool in[kSlotsT];
+#pragma unroll
+    for (int k = 0; k < kSlotsT; ++k) {
+      const int64_t j = j0 + threadIdx.x + 256 * k;
+      in[k] = j >= lo && j < len &&
+              MSA_IN_RANGE(u * a.weights_ld + j, 1,
+                           static_cast<int64_t>(a.s.batch) * a.c.Hkv * a.weights_ld, a.status);
+      sum[k] = 0.f;
+      had[k] = in[k] ? to[256 * k] : 0.f;
     }
-  } else {
-    for (int r = 0; r < rows; r += 2) {
-      const float2 x = __ldcs(reinterpret_cast<const float2*>(s + r));
-      add(x.x, r);
-      if (r + 1 < rows) add(x.y, r + 1);
+    // A row that attends nothing (lse -inf) has scores of -inf alone.
+    const auto add = [&](int k, float x, int r) {
+      sum[k] += x == -INFINITY ? 0.f : ex2(x - lse[r]);
+    };
+    if ((even & 3) == 0) {
+#pragma unroll 2
+      for (int r = 0; r < rows; r += 4) {
+        float4 x[kSlotsT];
+#pragma unroll
+        for (int k = 0; k < kSlotsT; ++k)
+          if (in[k])
+            x[k] = __ldcs(reinterpret_cast<const float4*>(
+                s + static_cast<int64_t>(256 * k) * even + r));
+#pragma unroll
+        for (int k = 0; k < kSlotsT; ++k)
+          if (in[k]) {
+            add(k, x[k].x, r);
+            if (r + 1 < rows) add(k, x[k].y, r + 1);
+            if (r + 2 < rows) add(k, x[k].z, r + 2);
+            if (r + 3 < rows) add(k, x[k].w, r + 3);
+          }
+      }
+    } else {
+      for (int r = 0; r < rows; r += 2) {
+#pragma unroll
+        for (int k = 0; k < kSlotsT; ++k)
+          if (in[k]) {
+            const float2 x = __ldcs(
+                reinterpret_cast<const float2*>(s + static_cast<int64_t>(256 * k) * even + r));
+            add(k, x.x, r);
+            if (r + 1 < rows) add(k, x.y, r + 1);
+          }
+      }
     }
+#pragma unroll
+    for (int k = 0; k < kSlotsT; ++k)
+      if (in[k]) to[256 * k] = had[k] + sum[k];
   }
-  if (MSA_IN_RANGE(u * a.weights_ld + j, 1,
-                   static_cast<int64_t>(a.s.batch) * a.c.Hkv * a.weights_ld, a.status))
-    a.weights[u * a.weights_ld + j] += sum;
 }
 
 template <int D, class Body>
@@ -1264,8 +1292,10 @@ cudaError_t launch_body(const CacheAttnArgs& a, cudaStream_t st) {
                      true, a);
   if (e != cudaSuccess || !a.weights) return e;
   const int64_t slots = static_cast<int64_t>(a.s.max_blocks) * a.c.block;
-  const dim3 grid(static_cast<unsigned>((slots + 255) / 256),
-                  static_cast<unsigned>(a.s.batch * a.c.Hkv));
+  const int64_t tiles = (slots + 256 * kSlotsT - 1) / (256 * kSlotsT);
+  const int64_t heads = static_cast<int64_t>(a.s.batch) * a.c.Hkv;
+  const dim3 grid(static_cast<unsigned>(min64(tiles, max64(1, kSms * 4 / heads))),
+                  static_cast<unsigned>(heads));
   return launch_after(cache_weights_kernel, grid, 256, rows * sizeof(float), st, true, a);
 }
 

@@ -6,16 +6,19 @@
 // before the window) scores sum over the group's heads h of <q_h, kmean_l>;
 // the top_k best are chosen, ties to the lower block.  The result is that of
 // the sum in 64 bits: the scores are computed in fp32 with a bound of their
-// rounding each, E_l = (g + 48) 2^-24 sum_d (sum_h |q_h|) |kmean_l| (a lane
-// adds D/4 <= 32 products one by one, two more additions join four lanes,
-// and the sum over g heads rounds g times); only the blocks whose score is
+// rounding each, E_l = (g + 16) 2^-24 |sum_h |q_h||_2 |kmean_l|_2 (the sum over
+// g heads rounds g times, a lane's 8 products of each 32 dims 8 times, and
+// four joins follow; each is relative to sum_d (sum_h |q_h|) |kmean_l| at most,
+// which the norms bound); only the blocks whose score is
 // within 2 max E of the k-th are computed again in 64 bits.  So the choice
 // does not depend on the order of any fp32 sum.
 //
 // The block means are read once for all query tokens of a sequence: 2 d
 // bytes a block and KV head, four lanes a block with four 16-byte loads in
-// flight each; HBM (or L2) bounds the scores.  The choice is one CTA a
-// (token, group): a radix selection of the k-th score over the CTA's list.
+// flight each.  The choice is one CTA a (token, group), whose warps have
+// contiguous runs of the blocks with their keys in shared memory: a radix
+// selection of the k-th score by 11 + 11 + 10 bits, then a pass of ballots
+// that writes the chosen in order; what bounds it is the chain of barriers.
 #include <math.h>
 
 #include "cache_common.cuh"
@@ -27,7 +30,10 @@ constexpr int kScoreThreads = 256;
 constexpr int kScoreBlocks = kScoreThreads / 4;  // blocks a CTA scores at a time
 constexpr int kScoreT = 4;                       // query tokens taken together
 constexpr int kPickThreads = 512;
-constexpr int kListMax = 1024;  // near-ties ranked in shared memory
+constexpr int kPickWarps = kPickThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kListMax = 512;          // near-ties ranked in shared memory
+constexpr int kStagedMax = 40 * 1024;  // keys in shared memory; more are kept in the workspace
 
 __device__ __forceinline__ int candidates(const CacheSelectArgs& a, int len, int t) {
   const int p = len - a.T + t;
@@ -42,36 +48,54 @@ __device__ __forceinline__ float q_at(const void* q, int64_t i) {
     return static_cast<const float*>(q)[i];
 }
 
-// blockIdx = (tile of 64 blocks, KV head, sequence).
+// blockIdx = (share of the tiles of 64 blocks, KV head, sequence).  A tile's
+// means are under way while the one before is scored, and its pages are looked
+// up one tile earlier still.
 template <int D, bool kBf16>
 __global__ void __launch_bounds__(kScoreThreads) cache_score_kernel(const CacheSelectArgs a) {
   __shared__ __align__(16) float qs[kScoreT][D], qa[kScoreT][D];
+  __shared__ float norm[kScoreT];  // of qa, times the bound's factor
   let_next_start();
   const int c = blockIdx.y, b = blockIdx.z, g = a.Hq / a.c.Hkv;
+  const int step = gridDim.x * kScoreBlocks;
+  const int l0 = blockIdx.x * kScoreBlocks + (threadIdx.x >> 2), lane4 = threadIdx.x & 3;
+  const float eps = (g + 16) * 5.9604645e-8f * 1.001f;  // with room for its own rounding
+  const int32_t* table = a.s.table + static_cast<int64_t>(b) * a.s.max_blocks;
+  const auto entry = [&](int l) { return l < a.s.max_blocks ? table[l] : -1; };
+  int32_t page1 = entry(l0);  // not looked at unless the block is a candidate
   const int len = cache_len(a.s, b, a.c.block, a.status);
   const int most = candidates(a, len, a.T - 1);  // the last token sees the most
-  const int l = blockIdx.x * kScoreBlocks + (threadIdx.x >> 2), lane4 = threadIdx.x & 3;
   if (static_cast<int>(blockIdx.x) * kScoreBlocks >= most) return;
-  // Four 16-byte pieces of the block's mean a lane: d = 32 i + 8 lane4 + 0..7.
-  uint4 km[D / 32];
-  if (l < most) {
-    int64_t page = cache_page(a.s, b, l, a.c.n_pages, a.status);
-    page = page < 0 ? 0 : page;
-    const uint4* src = reinterpret_cast<const uint4*>(a.c.k_mean + (page * a.c.Hkv + c) * D);
+  struct Mean {
+    uint4 x[D / 32];  // 16-byte pieces of a mean: d = 32 i + 8 lane4 + 0..7
+  };
+  const auto fetch = [&](int l, int32_t page) {
+    Mean k;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) km[i] = __ldg(src + 4 * i + lane4);
-  } else {
+    for (int i = 0; i < D / 32; ++i) k.x[i] = make_uint4(0, 0, 0, 0);
+    if (l < most) {
+      if (page < 0 || page >= a.c.n_pages) {
+        record_status(a.status, MSA_ERR_INVALID_ARG);
+        page = 0;
+      }
+      const uint4* src = reinterpret_cast<const uint4*>(
+          a.c.k_mean + (static_cast<int64_t>(page) * a.c.Hkv + c) * D);
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) km[i] = make_uint4(0, 0, 0, 0);
-  }
-  const float eps = (g + 48) * 5.9604645e-8f;
+      for (int i = 0; i < D / 32; ++i) k.x[i] = __ldg(src + 4 * i + lane4);
+    }
+    return k;
+  };
   for (int t0 = 0; t0 < a.T; t0 += kScoreT) {
     const int nt = min(kScoreT, a.T - t0);
+    if (t0 > 0) page1 = entry(l0);
+    Mean next = fetch(l0, page1);
+    page1 = entry(l0 + step);
     __syncthreads();
     for (int i = threadIdx.x; i < nt * D; i += kScoreThreads) {
       const int t = i / D, e = i - t * D;
       const int64_t at = ((static_cast<int64_t>(b) * a.T + t0 + t) * a.Hq + c * g) * D + e;
       float s = 0.f, m = 0.f;
+#pragma unroll 8
       for (int h = 0; h < g; ++h) {
         const float x = q_at<kBf16>(a.q, at + static_cast<int64_t>(h) * D);
         s += x;
@@ -81,33 +105,59 @@ __global__ void __launch_bounds__(kScoreThreads) cache_score_kernel(const CacheS
       qa[t][e] = m;
     }
     __syncthreads();
-    for (int t = 0; t < nt; ++t) {
-      float s = 0.f, m = 0.f;
+    if (static_cast<int>(threadIdx.x >> 5) < nt) {
+      const int t = threadIdx.x >> 5;
+      float n2 = 0.f;
+      for (int e = threadIdx.x & 31; e < D; e += 32) n2 = fmaf(qa[t][e], qa[t][e], n2);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) n2 += __shfl_xor_sync(0xffffffffu, n2, o);
+      if ((threadIdx.x & 31) == 0) norm[t] = sqrtf(n2) * eps;
+    }
+    __syncthreads();
+    for (int l = l0; l - (static_cast<int>(threadIdx.x) >> 2) < most; l += step) {
+      const Mean km = next;
+      next = fetch(l + step, page1);
+      page1 = entry(l + 2 * step);
+      float k2 = 0.f;
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
-        const uint32_t w[4] = {km[i].x, km[i].y, km[i].z, km[i].w};
+        const uint32_t w[4] = {km.x[i].x, km.x[i].y, km.x[i].z, km.x[i].w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const float lo = __uint_as_float(w[k] << 16), hi = __uint_as_float(w[k] & 0xffff0000u);
-          const int e = 32 * i + 8 * lane4 + 2 * k;
-          const float2 qv = *reinterpret_cast<const float2*>(&qs[t][e]);
-          const float2 av = *reinterpret_cast<const float2*>(&qa[t][e]);
-          s = fmaf(qv.x, lo, s);
-          s = fmaf(qv.y, hi, s);
-          m = fmaf(av.x, fabsf(lo), m);
-          m = fmaf(av.y, fabsf(hi), m);
+          const float lo = __uint_as_float(w[k] << 16);
+          const float hi = __uint_as_float(w[k] & 0xffff0000u);
+          k2 = fmaf(lo, lo, fmaf(hi, hi, k2));
         }
       }
-      s += __shfl_xor_sync(0xffffffffu, s, 1);
-      m += __shfl_xor_sync(0xffffffffu, m, 1);
-      s += __shfl_xor_sync(0xffffffffu, s, 2);
-      m += __shfl_xor_sync(0xffffffffu, m, 2);
-      if (lane4 == 0 && l < most) {
-        const int64_t at =
-            ((static_cast<int64_t>(b) * a.T + t0 + t) * a.c.Hkv + c) * a.s.max_blocks + l;
-        // NaN ranks last, as -inf; a bound that is not finite asks for 64 bits.
-        a.score[at] = s;
-        a.err[at] = m * eps;
+      k2 += __shfl_xor_sync(0xffffffffu, k2, 1);
+      k2 += __shfl_xor_sync(0xffffffffu, k2, 2);
+      const float k_norm = sqrtf(k2);
+      for (int t = 0; t < nt; ++t) {
+        float s[D / 32];
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          const float4 q0 = *reinterpret_cast<const float4*>(&qs[t][32 * i + 8 * lane4]);
+          const float4 q1 = *reinterpret_cast<const float4*>(&qs[t][32 * i + 8 * lane4 + 4]);
+          const uint4 w = km.x[i];
+          s[i] = q0.x * __uint_as_float(w.x << 16);
+          s[i] = fmaf(q0.y, __uint_as_float(w.x & 0xffff0000u), s[i]);
+          s[i] = fmaf(q0.z, __uint_as_float(w.y << 16), s[i]);
+          s[i] = fmaf(q0.w, __uint_as_float(w.y & 0xffff0000u), s[i]);
+          s[i] = fmaf(q1.x, __uint_as_float(w.z << 16), s[i]);
+          s[i] = fmaf(q1.y, __uint_as_float(w.z & 0xffff0000u), s[i]);
+          s[i] = fmaf(q1.z, __uint_as_float(w.w << 16), s[i]);
+          s[i] = fmaf(q1.w, __uint_as_float(w.w & 0xffff0000u), s[i]);
+        }
+        float sum = s[0] + s[1];
+        if constexpr (D == 128) sum += s[2] + s[3];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        if (lane4 == 0 && l < most) {
+          const int64_t at =
+              ((static_cast<int64_t>(b) * a.T + t0 + t) * a.c.Hkv + c) * a.s.max_blocks + l;
+          a.score[at] = sum;
+          a.err[at] = k_norm * norm[t];  // not finite: asks for 64 bits
+        }
       }
     }
   }
@@ -129,61 +179,45 @@ __device__ __forceinline__ uint64_t key_of(double x) {
 }
 
 struct PickShared {
-  int hist[256];
-  int warp[kPickThreads / 32];
-  int base, digit, left;
+  int hist[3][kBins];
+  int warp[kPickWarps], warp2[kPickWarps];
+  int digit, left;
   int n_list;
   int list[kListMax];
   double val[kListMax];
-  float emax[kPickThreads / 32];
+  float emax[kPickWarps];
 };
 
-// The `need`-th largest of the keys get(0..n): by bytes from the top, a
-// histogram of the keys that share the bytes found so far.
-template <typename K, typename Get>
-__device__ __forceinline__ K kth_largest(int n, int need, Get get, PickShared& sh) {
-  constexpr int kBytes = sizeof(K);
-  K prefix = 0, mask = 0;
-  int left = need;
-  for (int byte = kBytes - 1; byte >= 0; --byte) {
-    for (int i = threadIdx.x; i < 256; i += blockDim.x) sh.hist[i] = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < n; i += blockDim.x) {
-      K k;
-      if (get(i, &k) && (k & mask) == prefix)
-        atomicAdd(&sh.hist[static_cast<int>(k >> (8 * byte)) & 255], 1);
-    }
-    __syncthreads();
-    if (threadIdx.x < 32) {
-      // Lane l sums digits 255 - 8 l .. 248 - 8 l, then the lanes scan.
-      int s = 0;
+// In hist[pass], the bin that holds the `left`-th largest key (bins fall as
+// keys do); sh.digit and sh.left, the keys still wanted of that bin.
+__device__ __forceinline__ void find_bin(int* hist, int left, PickShared& sh) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int at = 4 * (kPickThreads - 1 - threadIdx.x);
+  const int4 s = *reinterpret_cast<const int4*>(hist + at);
+  const int sum = s.x + s.y + s.z + s.w;
+  int upto = sum;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s += sh.hist[255 - 8 * threadIdx.x - i];
-      int upto = s;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, upto, o);
-        if (threadIdx.x >= o) upto += y;
-      }
-      int before = upto - s;
-      if (before < left && left <= upto) {
-        for (int i = 0; i < 8; ++i) {
-          const int dgt = 255 - 8 * threadIdx.x - i, h = sh.hist[dgt];
-          if (left <= before + h) {
-            sh.digit = dgt;
-            sh.left = left - before;
-            break;
-          }
-          before += h;
-        }
-      }
-    }
-    __syncthreads();
-    prefix |= static_cast<K>(sh.digit) << (8 * byte);
-    mask |= static_cast<K>(255) << (8 * byte);
-    left = sh.left;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += y;
   }
-  return prefix;
+  if (lane == 31) sh.warp[warp] = upto;
+  __syncthreads();
+#pragma unroll
+  for (int v = 0; v < kPickWarps; ++v) upto += v < warp ? sh.warp[v] : 0;
+  int before = upto - sum;
+  if (before < left && left <= upto) {
+    const int bin[4] = {s.w, s.z, s.y, s.x};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (before < left && left <= before + bin[k]) {
+        sh.digit = at + 3 - k;
+        sh.left = left - before;
+      }
+      before += bin[k];
+    }
+  }
+  __syncthreads();
 }
 
 // Score of block l in 64 bits, by one warp: the products of bf16 are exact,
@@ -199,6 +233,7 @@ __device__ __forceinline__ double exact_score(const CacheSelectArgs& a, int b, i
   double s = 0.0;
   for (int e = lane; e < d; e += 32) {
     double x = 0.0;
+#pragma unroll 8
     for (int h = 0; h < g; ++h)
       x += static_cast<double>(q_at<kBf16>(a.q, q0 + static_cast<int64_t>(h) * d + e));
     s += x * static_cast<double>(__bfloat162float(km[e]));
@@ -208,18 +243,24 @@ __device__ __forceinline__ double exact_score(const CacheSelectArgs& a, int b, i
   return s;
 }
 
-// One CTA a (token, KV head).
-template <bool kBf16>
+// One CTA a (token, KV head).  kStaged: the keys are in shared memory, else
+// in the place of the scores' error bounds in the workspace.
+template <bool kBf16, bool kStaged>
 __global__ void __launch_bounds__(kPickThreads) cache_pick_kernel(const CacheSelectArgs a) {
-  __shared__ PickShared sh;
+  __shared__ __align__(16) PickShared sh;
+  extern __shared__ uint32_t staged[];
   const int c = blockIdx.x % a.c.Hkv, bt = blockIdx.x / a.c.Hkv;
   const int b = bt / a.T, t = bt - b * a.T;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t u = static_cast<int64_t>(bt) * a.c.Hkv + c;
+  let_next_start();
   const int n = candidates(a, cache_len(a.s, b, a.c.block, a.status), t);
   int32_t* sel = a.sel + u * a.top_k;
   const int k = min(a.top_k, n);
-  let_next_start();
+#pragma unroll
+  for (int i = 0; i < 3; ++i)
+    *reinterpret_cast<int4*>(&sh.hist[i][4 * threadIdx.x]) = make_int4(0, 0, 0, 0);
+  if (threadIdx.x == 0) sh.n_list = 0;
   wait_for_inputs();
   if (threadIdx.x == 0) a.cnt[u] = k;
   for (int i = k + threadIdx.x; i < a.top_k; i += kPickThreads) sel[i] = -1;
@@ -228,62 +269,78 @@ __global__ void __launch_bounds__(kPickThreads) cache_pick_kernel(const CacheSel
     return;
   }
   const float* score = a.score + u * a.s.max_blocks;
-  const float* err = a.err + u * a.s.max_blocks;
-  double* exact = a.exact + u * a.s.max_blocks;
+  uint32_t* err = reinterpret_cast<uint32_t*>(a.err + u * a.s.max_blocks);
+  uint32_t* keys = kStaged ? staged : err;
+  // The warp's blocks [i0, i1): whole groups of 32, the last of all cut short.
+  const int per = ((n + kPickWarps - 1) / kPickWarps + 31) & ~31;
+  const int i0 = min(n, warp * per), i1 = min(n, i0 + per);
 
   float em = 0.f;
-  for (int i = threadIdx.x; i < n; i += kPickThreads) {
-    const float e = err[i];
+#pragma unroll 4
+  for (int i = i0 + lane; i < i1; i += 32) {
+    const float e = __uint_as_float(err[i]);
     em = fmaxf(em, isnan(e) ? INFINITY : e);
+    keys[i] = key_of(score[i]);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) em = fmaxf(em, __shfl_xor_sync(0xffffffffu, em, o));
   if (lane == 0) sh.emax[warp] = em;
-  if (threadIdx.x == 0) sh.n_list = 0;
-  const float kth = value_of(kth_largest<uint32_t>(
-      n, k,
-      [&](int i, uint32_t* key) {
-        *key = key_of(score[i]);
-        return true;
-      },
-      sh));
+  __syncthreads();
+  uint32_t prefix = 0, mask = 0;
+  int left = k;
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    const uint32_t bits = pass == 2 ? 0x3ffu : 0x7ffu;
+#pragma unroll 4
+    for (int i = i0 + lane; i < i1; i += 32) {
+      const uint32_t key = keys[i];
+      if ((key & mask) == prefix) atomicAdd(&sh.hist[pass][(key >> shift) & bits], 1);
+    }
+    __syncthreads();
+    find_bin(sh.hist[pass], left, sh);
+    prefix |= static_cast<uint32_t>(sh.digit) << shift;
+    mask |= bits << shift;
+    left = sh.left;
+    __syncthreads();
+  }
+  const float kth = value_of(prefix);
   em = sh.emax[0];
-  for (int w = 1; w < kPickThreads / 32; ++w) em = fmaxf(em, sh.emax[w]);
-  // Twice the bound on either side, widened for the roundings of these two.
+#pragma unroll
+  for (int w = 1; w < kPickWarps; ++w) em = fmaxf(em, sh.emax[w]);
+  // Twice the bound on either side, widened for the roundings of these two;
+  // keys above `above` are chosen whatever the rest, keys from `below` on are
+  // near the k-th.  Where a side is not a number (infinite scores or bounds)
+  // all are near.
   const float room = 2.0001f * em + fabsf(kth) * 2.4e-7f + 1e-38f;
-  const float above = kth + room, below = kth - room;
-  // 2: chosen whatever the rest, 1: near the k-th, 0: not chosen.
-  auto cls = [&](float s) {
-    s = isnan(s) ? -INFINITY : s;
-    if (s > above) return 2;
-    return s < below ? 0 : 1;
-  };
-  int sure = 0;
-  for (int i = threadIdx.x; i < n; i += kPickThreads) {
-    const int x = cls(score[i]);
-    sure += x == 2;
-    if (x == 1) {
+  const float hi = kth + room, lo = kth - room;
+  const uint32_t above = isnan(hi) ? 0xffffffffu : key_of(hi);
+  const uint32_t below = isnan(lo) ? 0u : key_of(lo);
+  int sure = 0, near = 0;
+  for (int i = i0 + lane; i < i1; i += 32) {
+    const uint32_t key = keys[i];
+    sure += key > above;
+    if (key <= above && key >= below) {
       const int at = atomicAdd(&sh.n_list, 1);
       if (at < kListMax) sh.list[at] = i;  // in any order: ranked by value, then block
     }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sure += __shfl_xor_sync(0xffffffffu, sure, o);
+  sure = __reduce_add_sync(0xffffffffu, sure);
   if (lane == 0) sh.warp[warp] = sure;
   __syncthreads();
   sure = 0;
-  for (int w = 0; w < kPickThreads / 32; ++w) sure += sh.warp[w];
-  const int near = sh.n_list, need = k - sure;
-  __syncthreads();
-
-  // Which of the near ones: all; by rank in shared memory; or, for more than
-  // a list of them (equal blocks), by another radix selection.
-  double cut = 0.0;   // near values above are taken
-  int ties = 0;       // of those equal to it, the lowest so many
-  const bool listed = near <= kListMax;
+#pragma unroll
+  for (int w = 0; w < kPickWarps; ++w) sure += sh.warp[w];
+  near = sh.n_list;
+  const int need = k - sure;
+  // Keys from `from` on are chosen; near ones get the key of one that is, or
+  // 0, where not all of them are.
+  uint32_t from = below;
   if (near > need) {
-    if (listed) {
-      for (int i = warp; i < near; i += kPickThreads / 32) {
+    constexpr uint32_t kTaken = 0xffffffffu;
+    from = above == kTaken ? kTaken : above + 1;
+    if (near <= kListMax) {
+      for (int i = warp; i < near; i += kPickWarps) {
         const double s = exact_score<kBf16>(a, b, t, c, sh.list[i]);
         if (lane == 0) sh.val[i] = isnan(s) ? -INFINITY : s;
       }
@@ -294,83 +351,90 @@ __global__ void __launch_bounds__(kPickThreads) cache_pick_kernel(const CacheSel
         int rank = 0;
         for (int j = 0; j < near; ++j)
           rank += sh.val[j] > s || (sh.val[j] == s && sh.list[j] < me);
-        exact[me] = rank < need ? 1.0 : 0.0;
+        keys[me] = rank < need ? kTaken : 0u;
       }
-      __syncthreads();
     } else {
-      for (int i = warp; i < n; i += kPickThreads / 32) {
-        if (cls(score[i]) != 1) continue;
+      // More than the list holds (equal blocks): 64-bit scores in the
+      // workspace, and a selection among them by six digits.
+      double* exact = a.exact + u * a.s.max_blocks;
+      for (int i = i0; i < i1; ++i) {
+        if (keys[i] > above || keys[i] < below) continue;
         const double s = exact_score<kBf16>(a, b, t, c, i);
         if (lane == 0) exact[i] = isnan(s) ? -INFINITY : s + 0.0;
       }
+      uint64_t found = 0, known = 0;
+      int want = need;
+      for (int shift = 55; shift >= 0; shift -= 11) {
+        constexpr uint64_t bits = 0x7ff;
+        __syncthreads();
+        *reinterpret_cast<int4*>(&sh.hist[0][4 * threadIdx.x]) = make_int4(0, 0, 0, 0);
+        __syncthreads();
+        for (int i = i0 + lane; i < i1; i += 32)
+          if (keys[i] <= above && keys[i] >= below) {
+            const uint64_t key = key_of(exact[i]);
+            if ((key & known) == found)
+              atomicAdd(&sh.hist[0][static_cast<int>((key >> shift) & bits)], 1);
+          }
+        __syncthreads();
+        find_bin(sh.hist[0], want, sh);
+        found |= static_cast<uint64_t>(sh.digit) << shift;
+        known |= bits << shift;
+        want = sh.left;
+      }
+      // Of the scores equal to the last one in, the `want` lowest blocks.
+      int ties = 0;
+      for (int i = i0 + lane; i < i1; i += 32)
+        ties += keys[i] <= above && keys[i] >= below && key_of(exact[i]) == found;
+      ties = __reduce_add_sync(0xffffffffu, ties);
       __syncthreads();
-      const uint64_t key = kth_largest<uint64_t>(
-          n, need,
-          [&](int i, uint64_t* kk) {
-            if (cls(score[i]) != 1) return false;
-            *kk = key_of(exact[i]);
-            return true;
-          },
-          sh);
-      cut = __longlong_as_double(key >> 63 ? key & ~(1ull << 63) : ~key);
-      ties = sh.left;
+      if (lane == 0) sh.warp2[warp] = ties;
+      __syncthreads();
+      int before = 0;
+      for (int w = 0; w < warp; ++w) before += sh.warp2[w];
+      for (int j = i0; j < i1; j += 32) {
+        const int i = j + lane;
+        const bool is_near = i < i1 && keys[i] <= above && keys[i] >= below;
+        const uint64_t key = is_near ? key_of(exact[i]) : 0;
+        const bool tie = is_near && key == found;
+        const uint32_t m = __ballot_sync(0xffffffffu, tie);
+        if (is_near) {
+          const bool take =
+              key > found || (tie && before + __popc(m & ((1u << lane) - 1u)) < want);
+          keys[i] = take ? kTaken : 0u;
+        }
+        before += __popc(m);
+      }
     }
+    __syncthreads();
   }
-  // Ascending: scan the flags, kPickThreads blocks at a time.
-  if (threadIdx.x == 0) sh.base = 0;
-  int tied = 0;  // blocks equal to the cut in earlier rounds
-  for (int i0 = 0; i0 < n; i0 += kPickThreads) {
-    const int i = i0 + threadIdx.x;
-    const int x = i < n ? cls(score[i]) : 0;
-    bool take = x == 2;
-    bool tie = false;
-    if (x == 1) {
-      if (near <= need)
-        take = true;
-      else if (listed)
-        take = exact[i] != 0.0;
-      else {
-        take = exact[i] > cut;
-        tie = exact[i] == cut;
-      }
-    }
-    if (!listed && near > need) {
-      const uint32_t m = __ballot_sync(0xffffffffu, tie);
-      if (lane == 0) sh.warp[warp] = __popc(m);
-      __syncthreads();
-      int before = tied, all = 0;
-      for (int w = 0; w < kPickThreads / 32; ++w) {
-        before += w < warp ? sh.warp[w] : 0;
-        all += sh.warp[w];
-      }
-      tied += all;
-      take |= tie && before + __popc(m & ((1u << lane) - 1u)) < ties;
-      __syncthreads();
-    }
+  // Ascending: each warp's run starts after those of the warps before.
+  int mine = 0;
+  for (int i = i0 + lane; i < i1; i += 32) mine += keys[i] >= from;
+  mine = __reduce_add_sync(0xffffffffu, mine);
+  if (lane == 0) sh.warp2[warp] = mine;
+  __syncthreads();
+  int at = 0;
+#pragma unroll
+  for (int w = 0; w < kPickWarps; ++w) at += w < warp ? sh.warp2[w] : 0;
+  for (int j = i0; j < i1; j += 32) {
+    const int i = j + lane;
+    const bool take = i < i1 && keys[i] >= from;
     const uint32_t m = __ballot_sync(0xffffffffu, take);
-    if (lane == 0) sh.warp[warp] = __popc(m);
-    __syncthreads();
-    int before = sh.base, all = 0;
-    for (int w = 0; w < kPickThreads / 32; ++w) {
-      before += w < warp ? sh.warp[w] : 0;
-      all += sh.warp[w];
-    }
-    const int at = before + __popc(m & ((1u << lane) - 1u));
-    if (take && at < k) sel[at] = i;
-    __syncthreads();
-    if (threadIdx.x == 0) sh.base += all;
-    __syncthreads();
+    const int to = at + __popc(m & ((1u << lane) - 1u));
+    if (take && to < k) sel[to] = i;
+    at += __popc(m);
   }
 }
 
 template <int D>
 cudaError_t launch_scores(const CacheSelectArgs& a, cudaStream_t st) {
-  const dim3 grid((a.s.max_blocks + kScoreBlocks - 1) / kScoreBlocks, a.c.Hkv, a.s.batch);
-  if (a.bf16)
-    cache_score_kernel<D, true><<<grid, kScoreThreads, 0, st>>>(a);
-  else
-    cache_score_kernel<D, false><<<grid, kScoreThreads, 0, st>>>(a);
-  return cudaPeekAtLastError();
+  // CTAs that the device holds at once, each with as many tiles as that leaves.
+  const int64_t tiles = (a.s.max_blocks + kScoreBlocks - 1) / kScoreBlocks;
+  const int64_t others = static_cast<int64_t>(a.c.Hkv) * a.s.batch;
+  const int64_t x = min64(tiles, max64(1, kSms * 3 / others));
+  const dim3 grid(static_cast<unsigned>(x), a.c.Hkv, a.s.batch);
+  return launch_after(a.bf16 ? cache_score_kernel<D, true> : cache_score_kernel<D, false>, grid,
+                      kScoreThreads, 0, st, false, a);
 }
 
 }  // namespace
@@ -379,8 +443,16 @@ cudaError_t launch_cache_select(const CacheSelectArgs& a, cudaStream_t st) {
   cudaError_t e = a.c.d == 128 ? launch_scores<128>(a, st) : launch_scores<64>(a, st);
   if (e != cudaSuccess) return e;
   const dim3 units(static_cast<unsigned>(a.s.batch) * a.T * a.c.Hkv);
-  return launch_after(a.bf16 ? cache_pick_kernel<true> : cache_pick_kernel<false>, units,
-                      kPickThreads, 0, st, true, a);
+  const bool staged = a.s.max_blocks <= kStagedMax;
+  const int smem = staged ? a.s.max_blocks * 4 : 0;
+  const auto kernel = a.bf16 ? (staged ? cache_pick_kernel<true, true> : cache_pick_kernel<true, false>)
+                             : (staged ? cache_pick_kernel<false, true>
+                                       : cache_pick_kernel<false, false>);
+  if (smem > 8 * 1024) {  // with the static part, more than 48 KB needs leave
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_after(kernel, units, kPickThreads, smem, st, true, a);
 }
 
 }  // namespace msa

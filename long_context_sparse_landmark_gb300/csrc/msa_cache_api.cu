@@ -459,8 +459,9 @@ msa_status msa_cache_evict(const msa_kv_cache* cache, const int32_t* table, int 
                 (long long)new_weights_ld);
   if (new_lens == lens || new_weights == weights)
     return fail(MSA_ERR_INVALID_ARG, "outputs must not be the inputs");
+  const int64_t blocks = (budget + cache->block - 1) / cache->block;
   if (static_cast<int64_t>(batch) * cache->Hkv * 8 > INT32_MAX ||
-      (budget + cache->block - 1) / cache->block * cache->Hkv * 2 > INT32_MAX)
+      blocks * cache->Hkv > INT32_MAX)
     return fail(MSA_ERR_UNSUPPORTED, "batch, Hkv or budget too large for one call");
   msa::EvictArgs a{};
   a.c = view(cache);

@@ -393,9 +393,10 @@ def mean_cache(means, block=32):
     return cache, np.arange(n, dtype=np.int32)[None], [n * block + 1]
 
 
-@pytest.mark.parametrize("n,top_k", [(40, 7), (1500, 700), (3000, 1), (1200, 1199)])
+@pytest.mark.parametrize("n,top_k", [(40, 7), (1500, 700), (3000, 1), (1200, 1199), (41500, 600)])
 def test_equal_scores_go_to_the_lower_block(n, top_k):
-    """All blocks alike, few and more than the shared-memory list of near ties."""
+    """All blocks alike: few, more than the list of near ties holds, and more
+    than shared memory holds keys."""
     cache, t, lens = mean_cache(np.ones((n, 2, 64)))
     q = torch.randn((1, 1, 4, 64), device=DEV)
     t = np.concatenate([t, [[n]]], axis=1)
@@ -403,7 +404,7 @@ def test_equal_scores_go_to_the_lower_block(n, top_k):
     assert selected(sel, cnt)[0][0] == [list(range(top_k))] * 2
 
 
-@pytest.mark.parametrize("n", [100, 2500])
+@pytest.mark.parametrize("n", [100, 2500, 41000])
 def test_scores_that_fp32_cannot_tell_apart(n):
     """Large parts that cancel leave differences below fp32's rounding of the
     terms: the choice is that of 64 bits."""
@@ -508,6 +509,13 @@ def test_evict_ties_and_special_weights(kind, n):
         w[0, 0, 3], w[0, 0, 9], w[0, 0, 12], w[0, 0, 13], w[0, 0, 14] = (
             math.inf, -math.inf, 1e-45, 0.0, -0.0)
     check_evict(cache, pool, t, [n], w, dst, budget, 10)
+
+
+def test_evict_of_rows_longer_than_shared_memory():
+    n, budget = 400_003, 777
+    cache, pool, t, free = filled([n], 1, 64, 256, seed=31, extra=4)
+    w = torch.randint(0, 50_000, (1, 1, t.shape[1] * 256), device=DEV).float() / 64   # many ties
+    check_evict(cache, pool, t, [n], w, free[:4].reshape(1, 4), budget, 50)
 
 
 def test_evict_of_poisoned_blocks():

@@ -32,9 +32,10 @@
  * selection only read, an append writes only the blocks that take new slots,
  * an eviction writes only dst_table's pages.
  * Device data is checked by the kernels: a length outside [0, max_blocks *
- * block] is clamped, a slot whose page is not in [0, n_pages) is left out (not
- * written, not attended), and MSA_ERR_INVALID_ARG is recorded in the device
- * status word (msa_device_status).
+ * block] is clamped (an append skips the sequence), a slot whose page is not in
+ * [0, n_pages) is left out (not written, not attended; an eviction that keeps it
+ * gathers zeros), and MSA_ERR_INVALID_ARG is recorded in the device status word
+ * (msa_device_status).
  * Conventions of every entry point: as in msa.h.
  */
 #ifndef MSA_CACHE_H_
@@ -73,8 +74,8 @@ typedef struct msa_kv_cache {
  * Errors: INVALID_ARG for null or misaligned pointers, sizes below 1 or out
  * of range, max_new > total; UNSUPPORTED if d is not 64 or 128 or block not
  * one of the four.  A sequence whose rows do not lie in [0, total], number
- * more than max_new or exceed lens[b] is skipped and MSA_ERR_INVALID_ARG
- * recorded in the device status word.
+ * more than max_new or exceed lens[b], or whose length cannot be, is skipped
+ * and MSA_ERR_INVALID_ARG recorded in the device status word.
  */
 msa_status msa_cache_append(const msa_kv_cache *cache, const void *k,
                             const void *v, const int32_t *cu, int64_t total,

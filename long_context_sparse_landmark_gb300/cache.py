@@ -61,8 +61,7 @@ class KVCache:
         _want(k_scale, "k_scale", (_F32,), (n, h), dev)
         _want(v_scale, "v_scale", (_F32,), (n, h), dev)
         _want(k_mean, "k_mean", (_BF16,), (n, h, d), dev)
-        self.k_codes, self.v_codes = k_codes, v_codes
-        self.k_scale, self.v_scale, self.k_mean = k_scale, v_scale, k_mean
+        self._pool = (k_codes, v_codes, k_scale, v_scale, k_mean)
         self.n_pages, self.Hkv, self.block, self.d = n, h, block, d
         self.device = k_codes.device
         self.index = dev
@@ -72,6 +71,14 @@ class KVCache:
         self.struct = B.KvCacheStruct(k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(),
                                       v_scale.data_ptr(), k_mean.data_ptr(), n, h, d, block)
         self.ref = ctypes.byref(self.struct)
+
+    # The kernels are given these tensors' addresses once: they can be written
+    # to, not replaced.
+    k_codes = property(lambda self: self._pool[0])
+    v_codes = property(lambda self: self._pool[1])
+    k_scale = property(lambda self: self._pool[2])
+    v_scale = property(lambda self: self._pool[3])
+    k_mean = property(lambda self: self._pool[4])
 
     @classmethod
     def empty(cls, n_pages: int, Hkv: int, d: int, block: int = 64, device="cuda") -> "KVCache":

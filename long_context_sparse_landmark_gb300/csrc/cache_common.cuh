@@ -177,9 +177,9 @@ struct CacheAttnArgs {
   int64_t weights_ld;
   // workspace
   float* o_part;    // [2 * n_ctas][tile rows][d]
-  float* lse_part;  // [2 * n_ctas][tile rows] (log2 units)
+  float2* part_stat;  // [2 * n_ctas][tile rows]: a score m (log2 units), sum of 2^(s - m)
   float* scores;    // [batch, Hkv, max_blocks * block, rows padded to even] (log2 units)
-  float* lse2;      // [batch, Hkv, rows padded to even]
+  float2* row_stat;  // [batch, Hkv, rows padded to even]: m, 1 / sum of 2^(s - m)
   int n_ctas;
   int in_bf16, out_bf16;
   int* status;

@@ -216,8 +216,10 @@ __global__ void __launch_bounds__(kEvictThreads) cache_evict_kernel(const EvictA
     const int ae = before_equal + __popc(me & ((1u << lane) - 1u));
     if (up || (eq && ae < left)) {
       const int at = au + min(ae, left);
-      out[at] = i;
-      out_w[at] = key_weight(k);
+      if (MSA_IN_RANGE(at, 1, kept, a.status)) {
+        out[at] = i;
+        out_w[at] = key_weight(k);
+      }
     }
     before_above += __popc(mu);
     before_equal += __popc(me);

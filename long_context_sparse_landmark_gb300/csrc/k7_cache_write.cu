@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kMaxThreads, kMaxThreads == 512 ? 1 : kBf16 ? 
   const int jj = jh / Hkv, h = jh - jj * Hkv;
   const int r0 = a.cu[b], r1 = a.cu[b + 1];
   const int len = cache_len(a.s, b, block, a.status);
-  if (r0 == r1) return;
+  if (r0 == r1 || len != a.s.lens[b]) return;  // nothing new, or a length that cannot be
   if (r0 < 0 || r1 < r0 || r1 > a.total || r1 - r0 > a.max_new || r1 - r0 > len) {
     if (threadIdx.x == 0) record_status(a.status, MSA_ERR_INVALID_ARG);
     return;
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(kMaxThreads, kMaxThreads == 512 ? 1 : 7)
     for (int kv = 0; kv < 2; ++kv) {
       c[kv][i] = make_uint4(0, 0, 0, 0);
       scale[kv][i] = 0.f;
-      if (at >= 0) {
+      if (at >= 0 && MSA_IN_RANGE(at, 1, a.c.n_pages * Hkv << lb, a.status)) {
         c[kv][i] = __ldcs(reinterpret_cast<const uint4*>(
             (kv ? a.c.v_codes : a.c.k_codes) + at * d + col * kVec));
         scale[kv][i] = (kv ? a.c.v_scale : a.c.k_scale)[at >> lb];
@@ -376,8 +376,9 @@ __global__ void __launch_bounds__(kMaxThreads, kMaxThreads == 512 ? 1 : 7)
         x = make_uint4(0, 0, 0, 0);
       else if (s0 != s)  // codes of the same scale stay as they are
         x = rescale(x, s0, inv);
-      *reinterpret_cast<uint4*>((kv ? a.c.v_codes : a.c.k_codes) + ((head << lb) + r) * d +
-                                col * kVec) = x;
+      if (MSA_IN_RANGE((head << lb) + r, 1, a.c.n_pages * Hkv << lb, a.status))
+        *reinterpret_cast<uint4*>((kv ? a.c.v_codes : a.c.k_codes) + ((head << lb) + r) * d +
+                                  col * kVec) = x;
       if (kv == 0 && mean) column_sums(x, part);
     }
     if (threadIdx.x == 0) (kv ? a.c.v_scale : a.c.k_scale)[head] = s;

@@ -2,12 +2,13 @@
 // over a window, or over a window and selected blocks.
 //
 // Mathematics, per query row (position p, head h of KV group c), over its
-// slots j: s_j = scale <q, code_j> kscale(j), out = sum e^{s_j} code_j
-// vscale(j) / sum e^{s_j}, lse = ln sum e^{s_j}.  With u_j = s_j +
-// log2 vscale(j) (log2 units), out = 2^{M} sum 2^{u_j - M} code_j / sum
-// 2^{s_j - m} 2^{-m}...: the value scale goes into the exponent, so the
-// weights that meet the raw codes have a running maximum M of their own and
-// the denominator another one, m; both sums run in fp32.
+// slots j, in log2 units: s_j = scale log2e <q, code_j> kscale(j), v_j = log2
+// vscale(j); out = sum_j 2^{s_j + v_j} code_j / sum_j 2^{s_j}.  The value scale
+// goes into the exponent of the weights that meet the raw codes: w_j = 2^{s_j -
+// R + v_j - S}, with (R, S) the s and v of a slot whose s + v is the largest (to
+// 1.5) so far -- a pair, not a sum, so that a large score does not round the
+// value scale away.  The denominator is kept in units of its own, 2^m, m near
+// the largest s.  All sums are fp32.
 //
 // The work is read once: 2 d bytes a slot and KV head, shared by the group's
 // rows, so HBM bounds it.  The slots of all (sequence, KV head, row tile)
@@ -277,24 +278,25 @@ __device__ __forceinline__ Chunk chunk_of(const Ahead& r, int src) {
 }
 
 // The joined result of a CTA's warps for one unit's range, or a whole unit.
-// Row r: osum[w][r][dim] holds warp w's sum scaled to the row's common M,
-// stat[w][r] = {m, l, M}.
+// Row r: osum[w][r][dim] holds warp w's sum in units of 2^{R + S}, stat[w][r]
+// its maxima and denominator.
 struct Stat {
-  float m, l, M;
+  float m, l, R, S;
 };
 
 // Writes row m's output element pair and, once a row, its lse.  `whole`: the
 // unit lies in this CTA alone and goes to out; else to its part.
 __device__ __forceinline__ void store_lse(const CacheAttnArgs& a, const Plan& p, const Entry& e,
-                                          int c, int m, float lse2) {
+                                          int c, int m, float mx, float l) {
   int t, h;
   row_of(a, e, c, m, &t, &h);
   const int64_t at = (static_cast<int64_t>(e.b) * a.Hq + h) * a.T + t;
   if (MSA_IN_RANGE(at, 1, static_cast<int64_t>(a.s.batch) * a.Hq * a.T, a.status))
-    a.lse[at] = lse2 * kLn2;
+    a.lse[at] = l == 0.f ? -INFINITY : (mx + log2f(l)) * kLn2;
   if (a.weights) {
     const int even = (p.rows + 1) & ~1;
-    a.lse2[(static_cast<int64_t>(e.b) * a.c.Hkv + c) * even + m] = lse2;
+    a.row_stat[(static_cast<int64_t>(e.b) * a.c.Hkv + c) * even + m] =
+        make_float2(mx, l == 0.f ? 0.f : 1.f / l);
   }
 }
 __device__ __forceinline__ void store_out(const CacheAttnArgs& a, const Entry& e, int c, int m,
@@ -346,21 +348,25 @@ __device__ __forceinline__ void join_warps(const CacheAttnArgs& a, const Plan& p
     const int r = i / (D / 4), dim = (i - r * (D / 4)) * 4;
     const int m = rt * kTile + r;
     if (m >= p.rows) break;
-    float mx = -INFINITY, M = -INFINITY, l = 0.f;
+    float mx = -INFINITY, l = 0.f, R = -INFINITY, S = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      mx = fmaxf(mx, stat[w * kTile + r].m);
-      M = fmaxf(M, stat[w * kTile + r].M);
+      const Stat& s = stat[w * kTile + r];
+      mx = fmaxf(mx, s.m);
+      if ((s.R - R) + (s.S - S) > 0.f) {
+        R = s.R;
+        S = s.S;
+      }
     }
     mx = finite_or_0(mx);
-    M = finite_or_0(M);
+    R = finite_or_0(R);
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       const Stat& s = stat[w * kTile + r];
       if (s.m == -INFINITY && s.l == 0.f) continue;
       l += s.l * ex2(s.m - mx);
-      const float f = ex2(finite_or_0(s.M) - M);
+      const float f = ex2((finite_or_0(s.R) - R) + (s.S - S));
       const float4 x = *reinterpret_cast<const float4*>(osum + (w * kTile + r) * kLd + dim);
       v.x += x.x * f;
       v.y += x.y * f;
@@ -368,18 +374,17 @@ __device__ __forceinline__ void join_warps(const CacheAttnArgs& a, const Plan& p
       v.w += x.w * f;
     }
     // l == 0: no slot attended.
-    const float f = l == 0.f ? 0.f : ex2(M - mx) / l;
-    const float lse2 = l == 0.f ? -INFINITY : mx + log2f(l);
+    const float f = l == 0.f ? 0.f : ex2((R - mx) + (S - kPBits)) / l;
     v.x *= f;
     v.y *= f;
     v.z *= f;
     v.w *= f;
     if (whole) {
       store_out(a, e, c, m, dim, v);
-      if (dim == 0) store_lse(a, p, e, c, m, lse2);
+      if (dim == 0) store_lse(a, p, e, c, m, mx, l);
     } else {
       *reinterpret_cast<float4*>(a.o_part + (slot * kTile + r) * D + dim) = v;
-      if (dim == 0) a.lse_part[slot * kTile + r] = lse2;
+      if (dim == 0) a.part_stat[slot * kTile + r] = make_float2(l == 0.f ? -INFINITY : mx, l);
     }
   }
 }
@@ -405,7 +410,7 @@ struct MmaBody {
   uint32_t q[kQShared ? 1 : kKs][kQShared ? 1 : kNt][2];
   float qs[kNt][2];   // score scale of rows 2t, 2t+1 (log2 units)
   float o[kMt][kNt][4];
-  float m[kNt][2], l[kNt][2], M[kNt][2];
+  float m[kNt][2], l[kNt][2], R[kNt][2], S[kNt][2];
 
   // Rows of a unit, in shared memory for all its warps: their fragments
   // [k-step][tile][lane], score scales and positions.
@@ -476,8 +481,8 @@ struct MmaBody {
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         qs[n][r] = rows->scale[8 * n + 2 * t4 + r];
-        m[n][r] = M[n][r] = -INFINITY;
-        l[n][r] = 0.f;
+        m[n][r] = R[n][r] = -INFINITY;
+        l[n][r] = S[n][r] = 0.f;
       }
     }
 #pragma unroll
@@ -504,6 +509,7 @@ struct MmaBody {
     constexpr int kPer = D / 16;        // pieces a row
     constexpr int kStep = 32 / kPer;    // rows the warp copies at a time
     const int lane = threadIdx.x & 31, piece = lane % kPer, row0 = lane / kPer;
+    if (!MSA_IN_RANGE(at, kChunk, a.c.n_pages * a.c.Hkv * a.c.block, a.status)) return;
     const uint8_t* k = a.c.k_codes + at * D + lane * 16;
     const uint8_t* v = a.c.v_codes + at * D + lane * 16;
 #pragma unroll
@@ -598,34 +604,31 @@ struct MmaBody {
   __device__ __forceinline__ void softmax(const CacheAttnArgs& a, const Plan& p, const Entry& e,
                                           int c, int rt, const Chunk& x) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
-    // The maxima M and m are not kept up to the last bit: a weight may exceed
-    // 2^14 by a factor 2^1.5 (the half's range allows it) and a term of the
+    // The maxima are not kept up to the last bit: a weight may exceed 2^14 by
+    // a factor 2^1.5 (the half's range allows it) and a term of the
     // denominator 2^40, so that most chunks move neither them nor the sums,
     // and the lanes need not agree on a maximum.
-    float f[kNt][2], mx[kNt][2];
+    float mx[kNt][2];
     bool rise = false;
 #pragma unroll
     for (int n = 0; n < kNt; ++n) {
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        f[n][r] = qs[n][r] * x.ks;  // >= 0, or NaN
-        if (kEdge || kWeights) {
-          // Scores proper, -inf where masked.
-          const int pos = rows->pos[8 * n + 2 * t4 + r];
+        const float f = qs[n][r] * x.ks;  // >= 0, or NaN
+        int pos = 0;
+        if (kEdge) pos = rows->pos[8 * n + 2 * t4 + r];
 #pragma unroll
-          for (int st = 0; st < 2; ++st)
+        for (int st = 0; st < 2; ++st)
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              float& y = s[st][n][2 * k + r];
-              y *= f[n][r];
-              const int key = x.key0 + 16 * st + 8 * k + g;
-              if (kEdge && (!x.on || (x.window && (key > pos || pos - key >= a.window))))
-                y = -INFINITY;
-            }
-          f[n][r] = 1.f;
-        }
-        mx[n][r] = fmaxf(fmaxf(s[0][n][r], s[0][n][2 + r]), fmaxf(s[1][n][r], s[1][n][2 + r])) *
-                   f[n][r];
+          for (int k = 0; k < 2; ++k) {
+            float& y = s[st][n][2 * k + r];
+            y *= f;
+            const int key = x.key0 + 16 * st + 8 * k + g;
+            if (kEdge && (!x.on || (x.window && (key > pos || pos - key >= a.window))))
+              y = -INFINITY;
+          }
+        mx[n][r] = fmaxf(fmaxf(s[0][n][r], s[0][n][2 + r]), fmaxf(s[1][n][r], s[1][n][2 + r]));
+        rise |= (mx[n][r] - R[n][r]) + (x.lvs - S[n][r]) > 1.5f || mx[n][r] > m[n][r] + 40.f;
       }
       if constexpr (kWeights) {
         // For the weights pass: [slot][row], rows padded to even.
@@ -634,21 +637,17 @@ struct MmaBody {
         if (row < even) {
           const int64_t slots = static_cast<int64_t>(a.s.max_blocks) * a.c.block;
           float* to = a.scores + ((static_cast<int64_t>(e.b) * a.c.Hkv + c) * slots + x.key0) * even;
+          if (MSA_IN_RANGE(x.key0, kChunk, slots, a.status))
 #pragma unroll
-          for (int st = 0; st < 2; ++st)
+            for (int st = 0; st < 2; ++st)
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-              *reinterpret_cast<float2*>(to + static_cast<int64_t>(16 * st + 8 * k + g) * even +
-                                         row) =
-                  make_float2(s[st][n][2 * k], s[st][n][2 * k + 1]);
+              for (int k = 0; k < 2; ++k)
+                *reinterpret_cast<float2*>(to + static_cast<int64_t>(16 * st + 8 * k + g) * even +
+                                           row) =
+                    make_float2(s[st][n][2 * k], s[st][n][2 * k + 1]);
         }
       }
     }
-#pragma unroll
-    for (int n = 0; n < kNt; ++n)
-#pragma unroll
-      for (int r = 0; r < 2; ++r)
-        rise |= mx[n][r] + x.lvs > M[n][r] + 1.5f || mx[n][r] > m[n][r] + 40.f;
     if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
       for (int n = 0; n < kNt; ++n)
@@ -658,15 +657,20 @@ struct MmaBody {
 #pragma unroll
           for (int o2 = 4; o2 < 32; o2 <<= 1)
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o2));
-          const float Mn = fmaxf(M[n][r], top + x.lvs), mn = fmaxf(m[n][r], top);
-          const float up = Mn > M[n][r] ? ex2(M[n][r] - Mn) : 1.f;
-          l[n][r] *= mn > m[n][r] ? ex2(m[n][r] - mn) : 1.f;
-          M[n][r] = Mn;
-          m[n][r] = mn;
+          const float up = (top - R[n][r]) + (x.lvs - S[n][r]);
+          if (up > 0.f) {
+            const float down = ex2(-up);
 #pragma unroll
-          for (int i = 0; i < kMt; ++i) {
-            o[i][n][r] *= up;
-            o[i][n][2 + r] *= up;
+            for (int i = 0; i < kMt; ++i) {
+              o[i][n][r] *= down;
+              o[i][n][2 + r] *= down;
+            }
+            R[n][r] = top;
+            S[n][r] = x.lvs;
+          }
+          if (top > m[n][r]) {
+            l[n][r] *= ex2(m[n][r] - top);
+            m[n][r] = top;
           }
         }
     }
@@ -675,31 +679,31 @@ struct MmaBody {
       float pv[2][4];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const float Mu = finite_or_0(M[n][r]), base = kPBits + x.lvs - Mu;
+        const float Ru = finite_or_0(R[n][r]), mu = finite_or_0(m[n][r]);
+        const float v = x.lvs - S[n][r], base = kPBits + v;
         float sum = 0.f;
 #pragma unroll
         for (int st = 0; st < 2; ++st)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const float y = s[st][n][2 * k + r];
-            float w = ex2(fmaf(y, f[n][r], base));
+            float w = ex2((y - Ru) + base);
             if (kEdge && y == -INFINITY) w = 0.f;  // whatever the block's scales are
             pv[st][2 * k + r] = w;
             sum += w;
           }
         // The denominator, in units of 2^m: from the weights, whose scale is
         // taken out again, ...
-        const float mu = finite_or_0(m[n][r]);
-        float part = sum * ex2(-base - mu);
+        float part = sum * ex2((Ru - mu) - base);
         if (kEdge && sum == 0.f) part = 0.f;
         // ... unless they are too small to tell it: values 2^60 below other
         // blocks'.
-        if (mx[n][r] + x.lvs - Mu < -60.f) {
+        if ((mx[n][r] - Ru) + v < -60.f) {
           part = 0.f;
 #pragma unroll
           for (int st = 0; st < 2; ++st)
 #pragma unroll
-            for (int k = 0; k < 2; ++k) part += ex2(fmaf(s[st][n][2 * k + r], f[n][r], -mu));
+            for (int k = 0; k < 2; ++k) part += ex2(s[st][n][2 * k + r] - mu);
         }
         l[n][r] += part;
       }
@@ -767,11 +771,11 @@ struct MmaBody {
     for (int n = 0; n < kNt; ++n)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        float sum = l[n][r];  // the lane's slots'; m and M are the warp's
+        float sum = l[n][r];  // the lane's slots'; the maxima are the warp's
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
         const int row = warp * kTile + 8 * n + 2 * t4 + r;
-        if (g == 0) stat[row] = Stat{m[n][r], sum, M[n][r] - kPBits};
+        if (g == 0) stat[row] = Stat{m[n][r], sum, R[n][r], S[n][r]};
         float* to = osum + row * kLd + g * (D / 8);
 #pragma unroll
         for (int i = 0; i < kMt; ++i) {
@@ -795,7 +799,7 @@ struct SimtBody {
   static constexpr int kSmem = kSums + (kTile * D + kTile + kWarps * kChunk * kTile) * 4;
 
   float o[kTile][kDl];
-  float m[kTile], l[kTile], M[kTile];
+  float m[kTile], l[kTile], R[kTile], S[kTile];
   float* qsm;
   float* psm;
 
@@ -826,8 +830,8 @@ struct SimtBody {
     psm = qsm + kTile * D + kTile + (threadIdx.x >> 5) * kChunk * kTile;
 #pragma unroll
     for (int r = 0; r < kTile; ++r) {
-      m[r] = M[r] = -INFINITY;
-      l[r] = 0.f;
+      m[r] = R[r] = -INFINITY;
+      l[r] = S[r] = 0.f;
 #pragma unroll
       for (int k = 0; k < kDl; ++k) o[r][k] = 0.f;
     }
@@ -836,6 +840,7 @@ struct SimtBody {
   __device__ __forceinline__ void chunk(const CacheAttnArgs& a, const Plan& p, const Entry& e,
                                         int c, int rt, const Chunk& x) {
     const int lane = threadIdx.x & 31;
+    if (!MSA_IN_RANGE(x.at, kChunk, a.c.n_pages * a.c.Hkv * a.c.block, a.status)) return;
     const uint8_t* krow = a.c.k_codes + (x.at + lane) * D;
     float s[kTile];
 #pragma unroll
@@ -871,7 +876,8 @@ struct SimtBody {
       const bool in = x.on && (!x.window || (key <= pos[r] && pos[r] - key < a.window));
       any |= in;
       const float y = s[r] * x.ks, t = y * c_hi;
-      lo[r] = in && !isinf(t) ? fmaf(y, c_hi, -t) + y * c_lo : 0.f;
+      // Beyond 2^20 what is left is no fraction any more.
+      lo[r] = in && fabsf(t) < 1048576.f ? fmaf(y, c_hi, -t) + y * c_lo : 0.f;
       s[r] = in ? t : -INFINITY;
     }
     if (a.weights) {
@@ -881,7 +887,7 @@ struct SimtBody {
                   ((static_cast<int64_t>(e.b) * a.c.Hkv + c) * slots + key) * even + rt * kTile;
 #pragma unroll
       for (int r = 0; r < kTile; ++r)
-        if (rt * kTile + r < even) to[r] = s[r] + lo[r];
+        if (rt * kTile + r < even && MSA_IN_RANGE(key, 1, slots, a.status)) to[r] = s[r] + lo[r];
     }
     float pw[kTile];
 #pragma unroll
@@ -892,15 +898,17 @@ struct SimtBody {
       float mx = s[r];
 #pragma unroll
       for (int x2 = 16; x2 > 0; x2 >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x2));
-      const float Mn = fmaxf(M[r], ceilf(mx + x.lvs));
-      if (Mn > M[r]) {
-        const float f = exp2f(M[r] - Mn);
+      const float top = ceilf(mx), up = (top - R[r]) + (x.lvs - S[r]);
+      if (up > 0.f) {
+        const float down = exp2f(-up);
 #pragma unroll
-        for (int k = 0; k < kDl; ++k) o[r][k] *= f;
-        M[r] = Mn;
+        for (int k = 0; k < kDl; ++k) o[r][k] *= down;
+        R[r] = top;
+        S[r] = x.lvs;
       }
-      pw[r] = s[r] == -INFINITY ? 0.f
-                                : exp2f((s[r] - (finite_or_0(M[r]) - x.lvs)) + lo[r]);
+      pw[r] = s[r] == -INFINITY
+                  ? 0.f
+                  : exp2f(((s[r] - finite_or_0(R[r])) + lo[r]) + (x.lvs - S[r]));
     }
     __syncwarp();
     *reinterpret_cast<float4*>(psm + lane * kTile) = make_float4(pw[0], pw[1], pw[2], pw[3]);
@@ -943,7 +951,8 @@ struct SimtBody {
       float sum = l[r] * ex2(m[r] - finite_or_0(mx));
 #pragma unroll
       for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-      if (lane == 0) stat[warp * kTile + r] = Stat{mx, sum, M[r]};
+      // (a weight of 1 is 2^0 here, 2^kPBits in the other body)
+      if (lane == 0) stat[warp * kTile + r] = Stat{mx, sum, R[r], S[r] + kPBits};
 #pragma unroll
       for (int k = 0; k < kDl; ++k) osum[(warp * kTile + r) * kLd + lane * kDl + k] = o[r][k];
     }
@@ -1136,7 +1145,7 @@ __global__ void __launch_bounds__(kWpr == 1 ? kThreads : 32 * kWpr)
   const Entry e = entry_at(a, i);
   if (e.n_chunks == 0) {
     if (part == 0 && lane < D / 4) store_out(a, e, c, m, 4 * lane, make_float4(0.f, 0.f, 0.f, 0.f));
-    if (part == 0 && lane == 0) store_lse(a, p, e, c, m, -INFINITY);
+    if (part == 0 && lane == 0) store_lse(a, p, e, c, m, 0.f, 0.f);
     return;
   }
   const Cut cut = cut_of(a, sc.total * p.units);
@@ -1145,7 +1154,7 @@ __global__ void __launch_bounds__(kWpr == 1 ? kThreads : 32 * kWpr)
   if (c0 == c1) return;  // written whole
   const auto at = [&](int x) { return (2 * static_cast<int64_t>(x) + (x == c0)) * kTile + r; };
   float mx = -INFINITY;
-  for (int x = c0 + 32 * part + lane; x <= c1; x += 32 * kWpr) mx = fmaxf(mx, a.lse_part[at(x)]);
+  for (int x = c0 + 32 * part + lane; x <= c1; x += 32 * kWpr) mx = fmaxf(mx, a.part_stat[at(x)].x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   if (kWpr > 1) {
@@ -1162,7 +1171,8 @@ __global__ void __launch_bounds__(kWpr == 1 ? kThreads : 32 * kWpr)
 #pragma unroll 8
   for (int x = c0 + part; x <= c1; x += kWpr) {
     const int64_t s = at(x);
-    const float f = ex2(a.lse_part[s] - mx);
+    const float2 of = a.part_stat[s];
+    const float f = of.y * ex2(of.x - mx);
     const float* src = a.o_part + s * D + lane * kDl;
     float y[kDl];
     if constexpr (kDl == 4) {
@@ -1194,7 +1204,7 @@ __global__ void __launch_bounds__(kWpr == 1 ? kThreads : 32 * kWpr)
   }
   const float f = l == 0.f ? 0.f : 1.f / l;
   store_dims<kDl>(a, e, c, m, lane * kDl, v, f);
-  if (lane == 0) store_lse(a, p, e, c, m, l == 0.f ? -INFINITY : mx + log2f(l));
+  if (lane == 0) store_lse(a, p, e, c, m, mx, l);
 }
 
 // weights[b, c, j] += sum over the rows of KV head c of their probability of
@@ -1204,14 +1214,14 @@ __global__ void __launch_bounds__(kWpr == 1 ? kThreads : 32 * kWpr)
 constexpr int kSlotsT = 4;
 
 __global__ void __launch_bounds__(256) cache_weights_kernel(const CacheAttnArgs a) {
-  extern __shared__ float lse[];
+  extern __shared__ float2 stat[];  // of each row: its reference score, 1 / denominator
   const int rows = a.T * (a.Hq / a.c.Hkv), even = (rows + 1) & ~1;
   const int c = blockIdx.y % a.c.Hkv, b = blockIdx.y / a.c.Hkv;
   const int len = cache_len(a.s, b, a.c.block, a.status);
   const int lo = max(0, len - a.T - a.window + 1);
   wait_for_inputs();
   const int64_t u = static_cast<int64_t>(b) * a.c.Hkv + c;
-  for (int r = threadIdx.x; r < rows; r += 256) lse[r] = a.lse2[u * even + r];
+  for (int r = threadIdx.x; r < rows; r += 256) stat[r] = a.row_stat[u * even + r];
   __syncthreads();
   for (int64_t j0 = static_cast<int64_t>(blockIdx.x) * 256 * kSlotsT; j0 < len;
        j0 += static_cast<int64_t>(gridDim.x) * 256 * kSlotsT) {
@@ -1228,9 +1238,9 @@ __global__ void __launch_bounds__(256) cache_weights_kernel(const CacheAttnArgs 
       sum[k] = 0.f;
       had[k] = in[k] ? to[256 * k] : 0.f;
     }
-    // A row that attends nothing (lse -inf) has scores of -inf alone.
     const auto add = [&](int k, float x, int r) {
-      sum[k] += x == -INFINITY ? 0.f : ex2(x - lse[r]);
+      const float2 st = stat[r];
+      sum[k] += x == -INFINITY ? 0.f : ex2(x - st.x) * st.y;
     };
     if ((even & 3) == 0) {
 #pragma unroll 2
@@ -1296,7 +1306,7 @@ cudaError_t launch_body(const CacheAttnArgs& a, cudaStream_t st) {
   const int64_t heads = static_cast<int64_t>(a.s.batch) * a.c.Hkv;
   const dim3 grid(static_cast<unsigned>(min64(tiles, max64(1, kSms * 4 / heads))),
                   static_cast<unsigned>(heads));
-  return launch_after(cache_weights_kernel, grid, 256, rows * sizeof(float), st, true, a);
+  return launch_after(cache_weights_kernel, grid, 256, rows * sizeof(float2), st, true, a);
 }
 
 }  // namespace

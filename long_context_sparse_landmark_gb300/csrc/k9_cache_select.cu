@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kScoreThreads) cache_score_kernel(const CacheS
         if constexpr (D == 128) sum += s[2] + s[3];
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        if (lane4 == 0 && l < most) {
+        if (lane4 == 0 && l < most && MSA_IN_RANGE(l, 1, a.s.max_blocks, a.status)) {
           const int64_t at =
               ((static_cast<int64_t>(b) * a.T + t0 + t) * a.c.Hkv + c) * a.s.max_blocks + l;
           a.score[at] = sum;
@@ -421,7 +421,9 @@ __global__ void __launch_bounds__(kPickThreads) cache_pick_kernel(const CacheSel
     const bool take = i < i1 && keys[i] >= from;
     const uint32_t m = __ballot_sync(0xffffffffu, take);
     const int to = at + __popc(m & ((1u << lane) - 1u));
-    if (take && to < k) sel[to] = i;
+    if (take && to < k && MSA_IN_RANGE(u * a.top_k + to, 1,
+                                       static_cast<int64_t>(gridDim.x) * a.top_k, a.status))
+      sel[to] = i;
     at += __popc(m);
   }
 }

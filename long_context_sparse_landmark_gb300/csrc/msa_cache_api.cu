@@ -132,7 +132,7 @@ size_t up(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 // for weights every row's scores and lse.
 struct AttnPlan {
   int n_ctas;
-  size_t o, lse, scores, lse2, total;
+  size_t o, part_stat, scores, row_stat, total;
 };
 
 AttnPlan attn_plan(int Hkv, int d, int block, int batch, int n_q, int Hq, int max_blocks,
@@ -149,14 +149,14 @@ AttnPlan attn_plan(int Hkv, int d, int block, int batch, int n_q, int Hq, int ma
   size_t at = 0;
   p.o = at;
   at += up(static_cast<size_t>(2) * p.n_ctas * tile * d * sizeof(float));
-  p.lse = at;
-  at += up(static_cast<size_t>(2) * p.n_ctas * tile * sizeof(float));
+  p.part_stat = at;
+  at += up(static_cast<size_t>(2) * p.n_ctas * tile * sizeof(float2));
   if (weights) {
     const size_t even = (static_cast<size_t>(rows) + 1) & ~static_cast<size_t>(1);
     p.scores = at;
     at += up(static_cast<size_t>(batch) * Hkv * max_blocks * block * even * sizeof(float));
-    p.lse2 = at;
-    at += up(static_cast<size_t>(batch) * Hkv * even * sizeof(float));
+    p.row_stat = at;
+    at += up(static_cast<size_t>(batch) * Hkv * even * sizeof(float2));
   }
   p.total = at;
   return p;
@@ -200,9 +200,9 @@ msa_status run_attn(const msa_kv_cache* c, const void* q, const int32_t* table, 
   a.weights = weights;
   a.weights_ld = weights_ld;
   a.o_part = reinterpret_cast<float*>(ws + p.o);
-  a.lse_part = reinterpret_cast<float*>(ws + p.lse);
+  a.part_stat = reinterpret_cast<float2*>(ws + p.part_stat);
   a.scores = reinterpret_cast<float*>(ws + p.scores);
-  a.lse2 = reinterpret_cast<float*>(ws + p.lse2);
+  a.row_stat = reinterpret_cast<float2*>(ws + p.row_stat);
   a.n_ctas = p.n_ctas;
   a.in_bf16 = in_dt == MSA_BF16;
   a.out_bf16 = out_dt == MSA_BF16;

@@ -164,7 +164,7 @@ def test_workspace_sizes(lib):
     plain = f(cache(), 4, 3, 2, 8, 0, 1)
     assert plain > 0 and f(cache(), 4, 3, 2, 8, 1, 1) >= plain + 4 * 3 * 2 * 8 * 4 * 64
     # never more than two parts of 32 rows for each of 8 warps an SM
-    assert f(cache(), 1 << 14, 64, 8, 64, 0, 1) <= 2 * 152 * 8 * 32 * (128 + 1) * 4 + 512
+    assert f(cache(), 1 << 14, 64, 8, 64, 0, 1) <= 2 * 152 * 8 * 32 * (128 + 2) * 4 + 512
     s = lib.msa_cache_select_workspace_size
     assert s(cache(), 0, 1, 1) == 0
     assert s(cache(), 100, 3, 2) >= 16 * 3 * 2 * 2 * 100

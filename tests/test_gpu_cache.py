@@ -223,14 +223,12 @@ def test_attention(lens, n_q, hkv, group, d, block, window, dtype):
     w.copy_(w0)
     ref = R.attention(pool, q.double().cpu().numpy(), t, lens, window or 1 << 30, 1 / math.sqrt(d))
     vmax = max(np.abs(R.held(pool, "v", t[b], h, n)).max(initial=0) for b, n in enumerate(lens) for h in range(hkv))
-    for out_dtype in (dt, torch.float32):
+    for out_dtype in (dt, torch.float32 if dt == torch.bfloat16 else torch.bfloat16):
         out, lse = msa.cache_attention(q, cache, i32(t), i32(lens), window=window, out_dtype=out_dtype,
                                        weights=w if out_dtype == dt else None)
         torch.cuda.synchronize()
         assert binding().device_status() == 0
         check_attention(out, lse, ref, d, dtype == "bf16", vmax)
-        if dt == torch.float32:
-            break
     # weights: a sum of probabilities of relative error 2 ds + 2^-20 + n 2^-23 each
     ds = (d + 4) * 2.0 ** -23 * ref[3].max(initial=0)
     rows = n_q * group
@@ -346,6 +344,23 @@ def test_queries_of_any_size():
         ref = R.attention(pool, q.to(dt).double().cpu().numpy(), t, lens, 1 << 30, 0.1)
         out, lse = msa.cache_attention(q.to(dt), cache, i32(t), i32(lens), scale=0.1)
         check_attention(out, lse, ref, d, dt == torch.bfloat16, 6.0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("size", [1e4, 1e8, 1e12])
+def test_scores_far_beyond_an_exponential(dtype, size):
+    """Scores whose rounding is many units: the largest takes all, finitely."""
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    lens, d = [500], 64
+    cache, pool, t, _ = filled(lens, 2, d, 64, seed=14)
+    q = torch.randn((1, 1, 8, d), device=DEV, generator=torch.Generator(device=DEV).manual_seed(3)) * size
+    q = q.to(dt)
+    ref = R.attention(pool, q.double().cpu().numpy(), t, lens, 1 << 30, 0.125)
+    out, lse = msa.cache_attention(q, cache, i32(t), i32(lens))
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    # one slot leads every row by more than the scores' rounding
+    assert np.abs(out.double().cpu().numpy() - ref[0]).max() <= np.abs(ref[0]).max() * 2.0 ** -7
+    assert np.abs(lse.double().cpu().numpy() / ref[1] - 1).max() <= (d + 4) * 2.0 ** -22 * (ref[3].max() / np.abs(ref[1]).min())
 
 
 # -- selection ---------------------------------------------------------------
@@ -668,7 +683,7 @@ def test_pages_that_do_not_exist_and_lengths_that_cannot_be():
     msa.cache_append(cache, k, k, i32([0, 1, 2]), i32(bad), i32([101, 101]), 1)
     assert B.device_status() == B.MSA_ERR_INVALID_ARG
     same_pool(cache, before)
-    for cu, ln, most in (([0, 3, 2], [101, 101], 2), ([0, 1, 2], [0, 101], 2), ([-1, 1, 2], [101, 0], 2)):
+    for cu, ln, most in (([0, 1, 2], [1 << 20, -3], 2), ([0, 3, 2], [101, 101], 2), ([0, 1, 2], [0, 101], 2), ([-1, 1, 2], [101, 0], 2)):
         msa.cache_append(cache, k, k, i32(cu), i32(np.full_like(t, -1)), i32(ln), most)
         assert B.device_status() == B.MSA_ERR_INVALID_ARG
         same_pool(cache, before)

@@ -7,8 +7,7 @@
 // goes into the exponent of the weights that meet the raw codes: w_j = 2^{s_j -
 // R + v_j - S}, with (R, S) the s and v of a slot whose s + v is the largest (to
 // 1.5) so far -- a pair, not a sum, so that a large score does not round the
-// value scale away.  The denominator is kept in units of its own, 2^m, m near
-// the largest s.  All sums are fp32.
+// value scale away.  All sums are fp32.
 //
 // The work is read once: 2 d bytes a slot and KV head, shared by the group's
 // rows, so HBM bounds it.  The slots of all (sequence, KV head, row tile)
@@ -410,7 +409,7 @@ struct MmaBody {
   uint32_t q[kQShared ? 1 : kKs][kQShared ? 1 : kNt][2];
   float qs[kNt][2];   // score scale of rows 2t, 2t+1 (log2 units)
   float o[kMt][kNt][4];
-  float m[kNt][2], l[kNt][2], R[kNt][2], S[kNt][2];
+  float l[kNt][2], R[kNt][2], S[kNt][2];  // l in units of 2^R
 
   // Rows of a unit, in shared memory for all its warps: their fragments
   // [k-step][tile][lane], score scales and positions.
@@ -481,7 +480,7 @@ struct MmaBody {
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         qs[n][r] = rows->scale[8 * n + 2 * t4 + r];
-        m[n][r] = R[n][r] = -INFINITY;
+        R[n][r] = -INFINITY;
         l[n][r] = S[n][r] = 0.f;
       }
     }
@@ -604,31 +603,42 @@ struct MmaBody {
   __device__ __forceinline__ void softmax(const CacheAttnArgs& a, const Plan& p, const Entry& e,
                                           int c, int rt, const Chunk& x) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
-    // The maxima are not kept up to the last bit: a weight may exceed 2^14 by
-    // a factor 2^1.5 (the half's range allows it) and a term of the
-    // denominator 2^40, so that most chunks move neither them nor the sums,
-    // and the lanes need not agree on a maximum.
+    // (R, S) is not kept up to the last bit: a weight may exceed 2^14 by a
+    // factor 2^1.5 (the half's range allows it) and a term of the denominator
+    // 1 by 2^60, so that most chunks move neither it nor the sums, and the
+    // lanes need not agree on a maximum.
     float mx[kNt][2];
     bool rise = false;
 #pragma unroll
     for (int n = 0; n < kNt; ++n) {
+      // Rows 2t and 2t + 1 side by side, as the fragments have them.
+      const float2 f = make_float2(qs[n][0] * x.ks, qs[n][1] * x.ks);  // >= 0, or NaN
+      int pos[2] = {0, 0};
+      if (kEdge) {
+        pos[0] = rows->pos[8 * n + 2 * t4];
+        pos[1] = rows->pos[8 * n + 2 * t4 + 1];
+      }
+#pragma unroll
+      for (int st = 0; st < 2; ++st)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float2 y =
+              __fmul2_rn(make_float2(s[st][n][2 * k], s[st][n][2 * k + 1]), f);
+          s[st][n][2 * k] = y.x;
+          s[st][n][2 * k + 1] = y.y;
+          if (kEdge) {
+            const int key = x.key0 + 16 * st + 8 * k + g;
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+              if (!x.on || (x.window && (key > pos[r] || pos[r] - key >= a.window)))
+                s[st][n][2 * k + r] = -INFINITY;
+          }
+        }
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const float f = qs[n][r] * x.ks;  // >= 0, or NaN
-        int pos = 0;
-        if (kEdge) pos = rows->pos[8 * n + 2 * t4 + r];
-#pragma unroll
-        for (int st = 0; st < 2; ++st)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float& y = s[st][n][2 * k + r];
-            y *= f;
-            const int key = x.key0 + 16 * st + 8 * k + g;
-            if (kEdge && (!x.on || (x.window && (key > pos || pos - key >= a.window))))
-              y = -INFINITY;
-          }
         mx[n][r] = fmaxf(fmaxf(s[0][n][r], s[0][n][2 + r]), fmaxf(s[1][n][r], s[1][n][2 + r]));
-        rise |= (mx[n][r] - R[n][r]) + (x.lvs - S[n][r]) > 1.5f || mx[n][r] > m[n][r] + 40.f;
+        const float up = mx[n][r] - R[n][r];
+        rise |= up + (x.lvs - S[n][r]) > 1.5f || up > 60.f;
       }
       if constexpr (kWeights) {
         // For the weights pass: [slot][row], rows padded to even.
@@ -658,8 +668,9 @@ struct MmaBody {
           for (int o2 = 4; o2 < 32; o2 <<= 1)
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o2));
           const float up = (top - R[n][r]) + (x.lvs - S[n][r]);
-          if (up > 0.f) {
-            const float down = ex2(-up);
+          if (up > 0.f || top - R[n][r] > 60.f) {
+            const float down = ex2(fminf(-up, 100.f));
+            l[n][r] *= ex2(R[n][r] - top);
 #pragma unroll
             for (int i = 0; i < kMt; ++i) {
               o[i][n][r] *= down;
@@ -668,42 +679,44 @@ struct MmaBody {
             R[n][r] = top;
             S[n][r] = x.lvs;
           }
-          if (top > m[n][r]) {
-            l[n][r] *= ex2(m[n][r] - top);
-            m[n][r] = top;
-          }
         }
     }
 #pragma unroll
     for (int n = 0; n < kNt; ++n) {
       float pv[2][4];
+      const float2 minus_R = make_float2(-finite_or_0(R[n][0]), -finite_or_0(R[n][1]));
+      const float2 v = make_float2(x.lvs - S[n][0], x.lvs - S[n][1]);
+      const float2 base = make_float2(kPBits + v.x, kPBits + v.y);
+      float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int st = 0; st < 2; ++st)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float2 y = make_float2(s[st][n][2 * k], s[st][n][2 * k + 1]);
+          const float2 z = __fadd2_rn(__fadd2_rn(y, minus_R), base);
+          float2 w = make_float2(ex2(z.x), ex2(z.y));
+          if (kEdge) {  // whatever the block's scales are
+            if (y.x == -INFINITY) w.x = 0.f;
+            if (y.y == -INFINITY) w.y = 0.f;
+          }
+          pv[st][2 * k] = w.x;
+          pv[st][2 * k + 1] = w.y;
+          sum = __fadd2_rn(sum, w);
+        }
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const float Ru = finite_or_0(R[n][r]), mu = finite_or_0(m[n][r]);
-        const float v = x.lvs - S[n][r], base = kPBits + v;
-        float sum = 0.f;
-#pragma unroll
-        for (int st = 0; st < 2; ++st)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float y = s[st][n][2 * k + r];
-            float w = ex2((y - Ru) + base);
-            if (kEdge && y == -INFINITY) w = 0.f;  // whatever the block's scales are
-            pv[st][2 * k + r] = w;
-            sum += w;
-          }
-        // The denominator, in units of 2^m: from the weights, whose scale is
-        // taken out again, ...
-        float part = sum * ex2((Ru - mu) - base);
-        if (kEdge && sum == 0.f) part = 0.f;
+        const float mR = r ? minus_R.y : minus_R.x, sr = r ? sum.y : sum.x;
+        // The denominator: the weights with the value scale taken out again, ...
+        float part = sr * ex2(-(r ? base.y : base.x));
+        if (kEdge && sr == 0.f) part = 0.f;
         // ... unless they are too small to tell it: values 2^60 below other
         // blocks'.
-        if ((mx[n][r] - Ru) + v < -60.f) {
+        if ((mx[n][r] + mR) + (r ? v.y : v.x) < -60.f) {
           part = 0.f;
 #pragma unroll
           for (int st = 0; st < 2; ++st)
 #pragma unroll
-            for (int k = 0; k < 2; ++k) part += ex2(s[st][n][2 * k + r] - mu);
+            for (int k = 0; k < 2; ++k) part += ex2(s[st][n][2 * k + r] + mR);
         }
         l[n][r] += part;
       }
@@ -775,7 +788,7 @@ struct MmaBody {
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
         const int row = warp * kTile + 8 * n + 2 * t4 + r;
-        if (g == 0) stat[row] = Stat{m[n][r], sum, R[n][r], S[n][r]};
+        if (g == 0) stat[row] = Stat{R[n][r], sum, R[n][r], S[n][r]};
         float* to = osum + row * kLd + g * (D / 8);
 #pragma unroll
         for (int i = 0; i < kMt; ++i) {

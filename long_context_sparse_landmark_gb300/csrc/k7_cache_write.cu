@@ -5,7 +5,12 @@
 // of one head, finds their largest magnitude, forms the power-of-two scale
 // (cache_common.cuh), and stores the codes.  Every thread keeps its values in
 // registers (64 of them: 4 rows of 16 columns), all their loads under way at
-// once, so the data is read once and written once.
+// once, so the data is read once and written once.  HBM bounds a long append:
+// 128K tokens of 8 heads of 128 (bf16) in 128 us, 6.3 TB/s, 93 % of a measured
+// copy; with 32 values a thread the instructions did (182 us), and a loop over
+// tasks with copies under way in shared memory, one barrier a task, took 296.
+// The gather is bound by its chain of lookups and by some 900 instructions a
+// thread: 2 x 33.5 MB in 24 us, 4096 slots of 64 heads.
 #include "cache_common.cuh"
 
 namespace msa {

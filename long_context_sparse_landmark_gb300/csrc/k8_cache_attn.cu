@@ -10,23 +10,31 @@
 // value scale away.  All sums are fp32.
 //
 // The work is read once: 2 d bytes a slot and KV head, shared by the group's
-// rows, so HBM bounds it.  The slots of all (sequence, KV head, row tile)
-// units form one list of 32-slot chunks that is cut into equal ranges, one a
-// CTA, whatever the lengths are (they are only known on the device); where a
-// cut falls inside a unit the parts are joined by their log-sum-exp in a
-// second kernel.
+// rows, so HBM bounds it: 64 sequences of 16K to 32K tokens, 64 heads on 8 of
+// 128, take 495 us, 6.66 TB/s (98 % of a measured copy's 6.79).  The slots of
+// all (sequence, KV head, row tile) units form one list of 32-slot chunks that
+// is cut into equal ranges, one a CTA, whatever the lengths are (they are only
+// known on the device); where a cut falls inside a unit the parts are joined
+// by a second kernel, which starts while this one drains.
 //
 // bf16 rows run on the tensor cores (mma.sync, fp16 operands): codes turn
 // into halves exactly, a row of q is scaled by a power of two so that it
 // does too (an element 2^-31 of the row's largest and smaller is rounded),
 // and the weights are halves with 11 bits, scaled to use the whole range
 // (2^14 for the largest, so 2^-28 of it still has full precision).  Keys
-// are the MMA's 16 rows and query rows its 8 columns: a group of 8 heads
-// wastes nothing, and K and V go from global memory straight into the
-// fragments -- a lane's 16-byte load is its piece of four k-steps, with the
-// d (or slot) index permuted alike on both operands.  tcgen05 would need
-// the codes widened in shared memory first and 64 or 128 rows to fill its M;
-// the arithmetic is far below either unit's rate here.
+// are the MMA's 16 rows and query rows its 8 columns, so a group of 8 heads
+// wastes nothing; a warp's chunks come by cp.async into a ring of its own,
+// and a lane's 16-byte piece of a row is its share of four k-steps, the d (or
+// slot) index permuted alike on both operands.  tcgen05 would need the codes
+// widened in shared memory first and 64 or 128 rows to fill its M; one token
+// needs 32 operations a byte, far below what either unit does.
+//   Up to 8, 16 or 32 rows share a read.  At 32 (four tokens of eight heads)
+// the loop's some 950 instructions a chunk on 8 warps an SM bound it: 16
+// sequences of 32K take 140 us with one token (6.05 TB/s), 150 with two, 218
+// with four (362 as two passes of 16 rows).  Short calls are bound by latency:
+// 32K tokens of one KV head take 13 us with the join, of which 6.3 are here;
+// a part's first pass through the code, cold in the instruction cache, costs
+// more than its chunks.
 // fp32 rows run on the CUDA cores with fp32 arithmetic throughout.
 #include <math.h>
 
@@ -495,7 +503,6 @@ struct MmaBody {
   // A warp's chunks pass through a ring of its own in shared memory: K and V
   // codes as [32][D] each, 16-byte pieces (and for d = 64 rows of V) moved
   // about so that the fragment reads below meet no bank twice.
-
   __device__ __forceinline__ static int k_at(int row, int piece) {
     return D == 128 ? row * 128 + ((piece ^ ((row & 1) << 2)) << 4) : row * 64 + (piece << 4);
   }
@@ -988,7 +995,7 @@ __global__ void __launch_bounds__(kThreads, Body::kPerSm) cache_attn_kernel(cons
   __shared__ uint32_t found[2];
   extern __shared__ __align__(128) uint8_t dyn[];
   __shared__ Stat stat[kWarps * kTile];
-  __shared__ __align__(16) float4 info[kWarps][8];  // of a stage: K and V scale, first slot, flags
+  __shared__ __align__(16) float4 info[kWarps][8];  // of a stage: K scale, log2 of V's, first slot, flags
   float* osum = reinterpret_cast<float*>(dyn);
 
   const Plan p = plan_of(a, kTile);
@@ -1124,9 +1131,8 @@ __global__ void __launch_bounds__(kThreads, Body::kPerSm) cache_attn_kernel(cons
 
 // Joins the parts of the units that several CTAs share, and writes the rows
 // that attend nothing.  kWpr warps a row: 1 where a unit has a few parts (and
-// 4 rows a CTA), 16 where it has many, every 16th part each; a lane has D/32
-// dims.  The parts come from L2 one latency after the other, so several are
-// kept under way.
+// 4 rows a CTA), 16 where it has many, every 16th part each (32K tokens of one
+// KV head, 256 parts: 5 us, with 4 warps 12); a lane has D/32 dims.
 constexpr int kJoinMany = 16;
 
 template <int D, int kTile, int kWpr>
@@ -1142,7 +1148,6 @@ __global__ void __launch_bounds__(kWpr == 1 ? kThreads : 32 * kWpr)
   const int rows = a.c.Hkv * p.rows;  // of an entry, all KV heads
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int row0 = blockIdx.x * kRows, all = p.n_entries * rows;  // fit: the entry points check
-  let_next_start();
   const Scan sc = scan_entries<kWarpsJ>(a, p, scan);
   each_entry<kWarpsJ>(a, p, sc, scan, [&](int k, uint32_t before, uint32_t) {
 #pragma unroll
@@ -1221,9 +1226,11 @@ __global__ void __launch_bounds__(kWpr == 1 ? kThreads : 32 * kWpr)
 }
 
 // weights[b, c, j] += sum over the rows of KV head c of their probability of
-// slot j, from the scores the attention left.  A thread kSlotsT slots, 256
-// apart: no atomics, rows summed in order; HBM bounds the reading of the
-// scores.
+// slot j, from the scores the attention left (4 bytes a row and slot, an
+// eighth of the codes for 8 rows; computing them again would read the keys
+// again, half of the codes).  A thread kSlotsT slots, 256 apart: no atomics,
+// rows summed in order.  HBM bounds it: a million slots of 8 heads, 285 MB, in
+// 53 us.  Not started early: waiting CTAs cost the attention 40 us there.
 constexpr int kSlotsT = 4;
 
 __global__ void __launch_bounds__(256) cache_weights_kernel(const CacheAttnArgs a) {
@@ -1319,7 +1326,7 @@ cudaError_t launch_body(const CacheAttnArgs& a, cudaStream_t st) {
   const int64_t heads = static_cast<int64_t>(a.s.batch) * a.c.Hkv;
   const dim3 grid(static_cast<unsigned>(min64(tiles, max64(1, kSms * 4 / heads))),
                   static_cast<unsigned>(heads));
-  return launch_after(cache_weights_kernel, grid, 256, rows * sizeof(float2), st, true, a);
+  return launch_after(cache_weights_kernel, grid, 256, rows * sizeof(float2), st, false, a);
 }
 
 }  // namespace

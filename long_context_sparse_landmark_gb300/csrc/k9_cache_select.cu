@@ -19,6 +19,9 @@
 // contiguous runs of the blocks with their keys in shared memory: a radix
 // selection of the k-th score by 11 + 11 + 10 bits, then a pass of ballots
 // that writes the chosen in order; what bounds it is the chain of barriers.
+// 512 blocks of 8 heads: scores 3.5 us, choice 5; 130560 (16 sequences, 2
+// tokens each, 33 MB of means): 15 and 14 (a CTA that has to score in 64 bits,
+// which this GPU does slowly, adds some 3 us).
 #include <math.h>
 
 #include "cache_common.cuh"

@@ -47,7 +47,7 @@ __device__ __forceinline__ float key_weight(uint32_t k) {
 // kStaged: the keys stay in shared memory (kKeysMax of them at most).
 template <bool kStaged>
 __global__ void __launch_bounds__(kEvictThreads) cache_evict_kernel(const EvictArgs a) {
-  extern __shared__ uint32_t keys[];
+  extern __shared__ __align__(16) uint32_t keys[];
   __shared__ __align__(16) int hist[3][kBins];
   __shared__ int digit, left_s;
   __shared__ int counts[2];  // this CTA's slots above the least kept weight, and equal to it
@@ -90,6 +90,24 @@ __global__ void __launch_bounds__(kEvictThreads) cache_evict_kernel(const EvictA
     for (int i = i0 + lane; i < i1; i += 32) mine[i - i0] = weight_key(w[i]);
   }
   const auto key_at = [&](int i) { return kStaged ? mine[i - i0] : weight_key(w[i]); };
+  // The warp's keys in any order, four a lane at a time from shared memory (a
+  // run starts on a multiple of 32 keys).
+  const auto each_key = [&](auto f) {
+    if constexpr (kStaged) {
+      const int n4 = (i1 - i0) & ~127;
+#pragma unroll 2
+      for (int i = 4 * lane; i < n4; i += 128) {
+        const uint4 k = *reinterpret_cast<const uint4*>(mine + i);
+        f(k.x);
+        f(k.y);
+        f(k.z);
+        f(k.w);
+      }
+      for (int i = n4 + lane; i < i1 - i0; i += 32) f(mine[i]);
+    } else {
+      for (int i = i0 + lane; i < i1; i += 32) f(weight_key(w[i]));
+    }
+  };
 
   if (rank == 0 && threadIdx.x == 0 && h == 0) a.new_lens[b] = kept;
   // Past the kept: -1 and 0.
@@ -112,11 +130,9 @@ __global__ void __launch_bounds__(kEvictThreads) cache_evict_kernel(const EvictA
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
       const uint32_t bits = pass == 2 ? 0x3ffu : 0x7ffu;
-#pragma unroll 8
-      for (int i = i0 + lane; i < i1; i += 32) {
-        const uint32_t k = key_at(i);
+      each_key([&](uint32_t k) {
         if ((k & mask) == prefix) atomicAdd(&hist[pass][(k >> shift) & bits], 1);
-      }
+      });
       sync_all();
       // Thread t sums the bins 4 * (511 - t) + 3 .. + 0 of all ranks: the
       // threads' order is that of falling keys.
@@ -170,12 +186,10 @@ __global__ void __launch_bounds__(kEvictThreads) cache_evict_kernel(const EvictA
   // How many of this warp's slots lie above the least kept weight, and at it.
   int above = 0, equal = 0;
   if (need > 0) {
-#pragma unroll 8
-    for (int i = i0 + lane; i < i1; i += 32) {
-      const uint32_t k = key_at(i);
+    each_key([&](uint32_t k) {
       above += all || k > prefix;
       equal += !all && k == prefix;
-    }
+    });
   }
   above = __reduce_add_sync(0xffffffffu, above);
   equal = __reduce_add_sync(0xffffffffu, equal);

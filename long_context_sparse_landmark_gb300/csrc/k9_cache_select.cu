@@ -223,24 +223,63 @@ __device__ __forceinline__ void find_bin(int* hist, int left, PickShared& sh) {
   __syncthreads();
 }
 
-// Score of block l in 64 bits, by one warp: the products of bf16 are exact,
-// so what rounds is a sum of g * D / 32 terms a lane and five joins.
-template <bool kBf16>
+// kN consecutive values of a row as floats, in one load.
+template <int kN, bool kBf16>
+__device__ __forceinline__ void load_row(const void* p, int64_t at, float* v) {
+  if constexpr (kBf16) {
+    const uint16_t* src = static_cast<const uint16_t*>(p) + at;
+    uint32_t w[kN / 2];
+    if constexpr (kN == 4) {
+      const uint2 x = *reinterpret_cast<const uint2*>(src);
+      w[0] = x.x;
+      w[1] = x.y;
+    } else {
+      w[0] = *reinterpret_cast<const uint32_t*>(src);
+    }
+#pragma unroll
+    for (int i = 0; i < kN / 2; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kN; i += 2) {
+      const float2 x = *reinterpret_cast<const float2*>(static_cast<const float*>(p) + at + i);
+      v[i] = x.x;
+      v[i + 1] = x.y;
+    }
+  }
+}
+
+// Score of block l in 64 bits, by one warp, a lane D/32 dims: the products of
+// bf16 are exact, so what rounds is the sums.  Eight heads' loads go together.
+template <int D, bool kBf16>
 __device__ __forceinline__ double exact_score(const CacheSelectArgs& a, int b, int t, int c,
                                               int l) {
-  const int lane = threadIdx.x & 31, g = a.Hq / a.c.Hkv, d = a.c.d;
+  constexpr int kN = D / 32;
+  const int lane = threadIdx.x & 31, g = a.Hq / a.c.Hkv;
   int64_t page = cache_page(a.s, b, l, a.c.n_pages, a.status);
   page = page < 0 ? 0 : page;
-  const __nv_bfloat16* km = a.c.k_mean + (page * a.c.Hkv + c) * d;
-  const int64_t q0 = ((static_cast<int64_t>(b) * a.T + t) * a.Hq + c * g) * d;
-  double s = 0.0;
-  for (int e = lane; e < d; e += 32) {
-    double x = 0.0;
-#pragma unroll 8
-    for (int h = 0; h < g; ++h)
-      x += static_cast<double>(q_at<kBf16>(a.q, q0 + static_cast<int64_t>(h) * d + e));
-    s += x * static_cast<double>(__bfloat162float(km[e]));
+  float km[kN];
+  load_row<kN, true>(a.c.k_mean, (page * a.c.Hkv + c) * D + kN * lane, km);
+  const int64_t q0 = ((static_cast<int64_t>(b) * a.T + t) * a.Hq + c * g) * D + kN * lane;
+  double x[kN];
+#pragma unroll
+  for (int i = 0; i < kN; ++i) x[i] = 0.0;
+  for (int h0 = 0; h0 < g; h0 += 8) {
+    float q[8][kN];
+#pragma unroll
+    for (int h = 0; h < 8; ++h)
+      if (h0 + h < g) load_row<kN, kBf16>(a.q, q0 + static_cast<int64_t>(h0 + h) * D, q[h]);
+#pragma unroll
+    for (int h = 0; h < 8; ++h)
+      if (h0 + h < g)
+#pragma unroll
+        for (int i = 0; i < kN; ++i) x[i] += static_cast<double>(q[h][i]);
   }
+  double s = 0.0;
+#pragma unroll
+  for (int i = 0; i < kN; ++i) s += x[i] * static_cast<double>(km[i]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   return s;
@@ -248,8 +287,8 @@ __device__ __forceinline__ double exact_score(const CacheSelectArgs& a, int b, i
 
 // One CTA a (token, KV head).  kStaged: the keys are in shared memory, else
 // in the place of the scores' error bounds in the workspace.
-template <bool kBf16, bool kStaged>
-__global__ void __launch_bounds__(kPickThreads) cache_pick_kernel(const CacheSelectArgs a) {
+template <int D, bool kBf16, bool kStaged>
+__global__ void __launch_bounds__(kPickThreads, 2) cache_pick_kernel(const CacheSelectArgs a) {
   __shared__ __align__(16) PickShared sh;
   extern __shared__ uint32_t staged[];
   const int c = blockIdx.x % a.c.Hkv, bt = blockIdx.x / a.c.Hkv;
@@ -344,7 +383,7 @@ __global__ void __launch_bounds__(kPickThreads) cache_pick_kernel(const CacheSel
     from = above == kTaken ? kTaken : above + 1;
     if (near <= kListMax) {
       for (int i = warp; i < near; i += kPickWarps) {
-        const double s = exact_score<kBf16>(a, b, t, c, sh.list[i]);
+        const double s = exact_score<D, kBf16>(a, b, t, c, sh.list[i]);
         if (lane == 0) sh.val[i] = isnan(s) ? -INFINITY : s;
       }
       __syncthreads();
@@ -362,7 +401,7 @@ __global__ void __launch_bounds__(kPickThreads) cache_pick_kernel(const CacheSel
       double* exact = a.exact + u * a.s.max_blocks;
       for (int i = i0; i < i1; ++i) {
         if (keys[i] > above || keys[i] < below) continue;
-        const double s = exact_score<kBf16>(a, b, t, c, i);
+        const double s = exact_score<D, kBf16>(a, b, t, c, i);
         if (lane == 0) exact[i] = isnan(s) ? -INFINITY : s + 0.0;
       }
       uint64_t found = 0, known = 0;
@@ -450,9 +489,15 @@ cudaError_t launch_cache_select(const CacheSelectArgs& a, cudaStream_t st) {
   const dim3 units(static_cast<unsigned>(a.s.batch) * a.T * a.c.Hkv);
   const bool staged = a.s.max_blocks <= kStagedMax;
   const int smem = staged ? a.s.max_blocks * 4 : 0;
-  const auto kernel = a.bf16 ? (staged ? cache_pick_kernel<true, true> : cache_pick_kernel<true, false>)
-                             : (staged ? cache_pick_kernel<false, true>
-                                       : cache_pick_kernel<false, false>);
+  void (*kernel)(CacheSelectArgs);
+  if (a.c.d == 128)
+    kernel = a.bf16 ? (staged ? cache_pick_kernel<128, true, true> : cache_pick_kernel<128, true, false>)
+                    : (staged ? cache_pick_kernel<128, false, true>
+                              : cache_pick_kernel<128, false, false>);
+  else
+    kernel = a.bf16 ? (staged ? cache_pick_kernel<64, true, true> : cache_pick_kernel<64, true, false>)
+                    : (staged ? cache_pick_kernel<64, false, true>
+                              : cache_pick_kernel<64, false, false>);
   if (smem > 8 * 1024) {  // with the static part, more than 48 KB needs leave
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;

@@ -20,8 +20,8 @@
 // selection of the k-th score by 11 + 11 + 10 bits, then a pass of ballots
 // that writes the chosen in order; what bounds it is the chain of barriers.
 // 512 blocks of 8 heads: scores 3.5 us, choice 5; 130560 (16 sequences, 2
-// tokens each, 33 MB of means): 15 and 14 (a CTA that has to score in 64 bits,
-// which this GPU does slowly, adds some 3 us).
+// tokens each, 33 MB of means): 15 and 11, of which 2 for the CTAs that have to
+// score in 64 bits.
 #include <math.h>
 
 #include "cache_common.cuh"
@@ -32,8 +32,7 @@ namespace {
 constexpr int kScoreThreads = 256;
 constexpr int kScoreBlocks = kScoreThreads / 4;  // blocks a CTA scores at a time
 constexpr int kScoreT = 4;                       // query tokens taken together
-constexpr int kPickThreads = 512;
-constexpr int kPickWarps = kPickThreads / 32;
+constexpr int kPickWarpsMax = 16;
 constexpr int kBins = 2048;
 constexpr int kListMax = 512;          // near-ties ranked in shared memory
 constexpr int kStagedMax = 40 * 1024;  // keys in shared memory; more are kept in the workspace
@@ -183,21 +182,31 @@ __device__ __forceinline__ uint64_t key_of(double x) {
 
 struct PickShared {
   int hist[3][kBins];
-  int warp[kPickWarps], warp2[kPickWarps];
+  int warp[kPickWarpsMax], warp2[kPickWarpsMax];
   int digit, left;
   int n_list;
   int list[kListMax];
   double val[kListMax];
-  float emax[kPickWarps];
+  float emax[kPickWarpsMax];
 };
 
-// In hist[pass], the bin that holds the `left`-th largest key (bins fall as
-// keys do); sh.digit and sh.left, the keys still wanted of that bin.
-__device__ __forceinline__ void find_bin(int* hist, int left, PickShared& sh) {
+// In hist, the bin that holds the `left`-th largest key (bins fall as keys
+// do); sh.digit and sh.left, the keys still wanted of that bin.
+template <int kThreads>
+__device__ __forceinline__ void find_bin(const int* hist, int left, PickShared& sh) {
+  constexpr int kOwn = kBins / kThreads;  // bins of a thread, the first has the highest
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int at = 4 * (kPickThreads - 1 - threadIdx.x);
-  const int4 s = *reinterpret_cast<const int4*>(hist + at);
-  const int sum = s.x + s.y + s.z + s.w;
+  const int at = kOwn * (kThreads - 1 - threadIdx.x);
+  int bin[kOwn], sum = 0;
+#pragma unroll
+  for (int i = 0; i < kOwn; i += 4) {
+    const int4 s = *reinterpret_cast<const int4*>(hist + at + i);
+    bin[i] = s.x;
+    bin[i + 1] = s.y;
+    bin[i + 2] = s.z;
+    bin[i + 3] = s.w;
+    sum += s.x + s.y + s.z + s.w;
+  }
   int upto = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -207,14 +216,13 @@ __device__ __forceinline__ void find_bin(int* hist, int left, PickShared& sh) {
   if (lane == 31) sh.warp[warp] = upto;
   __syncthreads();
 #pragma unroll
-  for (int v = 0; v < kPickWarps; ++v) upto += v < warp ? sh.warp[v] : 0;
+  for (int v = 0; v < kThreads / 32; ++v) upto += v < warp ? sh.warp[v] : 0;
   int before = upto - sum;
   if (before < left && left <= upto) {
-    const int bin[4] = {s.w, s.z, s.y, s.x};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = kOwn - 1; k >= 0; --k) {
       if (before < left && left <= before + bin[k]) {
-        sh.digit = at + 3 - k;
+        sh.digit = at + k;
         sh.left = left - before;
       }
       before += bin[k];
@@ -251,8 +259,11 @@ __device__ __forceinline__ void load_row(const void* p, int64_t at, float* v) {
   }
 }
 
-// Score of block l in 64 bits, by one warp, a lane D/32 dims: the products of
-// bf16 are exact, so what rounds is the sums.  Eight heads' loads go together.
+// Score of block l in 64 bits, by one warp, a lane D/32 dims.  The sum over
+// the heads is kept as an fp32 value and the exact error of each addition (the
+// error-free sum of two floats), which is as good and spares most of the
+// 64-bit operations, each 16 cycles of an SM for a warp; the rest are the
+// products and their sum.  Eight heads' loads go together.
 template <int D, bool kBf16>
 __device__ __forceinline__ double exact_score(const CacheSelectArgs& a, int b, int t, int c,
                                               int l) {
@@ -263,9 +274,9 @@ __device__ __forceinline__ double exact_score(const CacheSelectArgs& a, int b, i
   float km[kN];
   load_row<kN, true>(a.c.k_mean, (page * a.c.Hkv + c) * D + kN * lane, km);
   const int64_t q0 = ((static_cast<int64_t>(b) * a.T + t) * a.Hq + c * g) * D + kN * lane;
-  double x[kN];
+  float sum[kN], rest[kN];
 #pragma unroll
-  for (int i = 0; i < kN; ++i) x[i] = 0.0;
+  for (int i = 0; i < kN; ++i) sum[i] = rest[i] = 0.f;
   for (int h0 = 0; h0 < g; h0 += 8) {
     float q[8][kN];
 #pragma unroll
@@ -275,11 +286,19 @@ __device__ __forceinline__ double exact_score(const CacheSelectArgs& a, int b, i
     for (int h = 0; h < 8; ++h)
       if (h0 + h < g)
 #pragma unroll
-        for (int i = 0; i < kN; ++i) x[i] += static_cast<double>(q[h][i]);
+        for (int i = 0; i < kN; ++i) {
+          const float x = q[h][i], t = sum[i] + x, b = t - sum[i];
+          rest[i] += (sum[i] - (t - b)) + (x - b);
+          sum[i] = t;
+        }
   }
   double s = 0.0;
 #pragma unroll
-  for (int i = 0; i < kN; ++i) s += x[i] * static_cast<double>(km[i]);
+  for (int i = 0; i < kN; ++i) {
+    const double k = km[i];
+    s += static_cast<double>(sum[i]) * k;
+    if (rest[i] != 0.f && !isinf(sum[i])) s += static_cast<double>(rest[i]) * k;
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   return s;
@@ -287,8 +306,10 @@ __device__ __forceinline__ double exact_score(const CacheSelectArgs& a, int b, i
 
 // One CTA a (token, KV head).  kStaged: the keys are in shared memory, else
 // in the place of the scores' error bounds in the workspace.
-template <int D, bool kBf16, bool kStaged>
-__global__ void __launch_bounds__(kPickThreads, 2) cache_pick_kernel(const CacheSelectArgs a) {
+template <int D, bool kBf16, bool kStaged, int kPickThreads>
+__global__ void __launch_bounds__(kPickThreads, 1024 / kPickThreads)
+    cache_pick_kernel(const CacheSelectArgs a) {
+  constexpr int kPickWarps = kPickThreads / 32;
   __shared__ __align__(16) PickShared sh;
   extern __shared__ uint32_t staged[];
   const int c = blockIdx.x % a.c.Hkv, bt = blockIdx.x / a.c.Hkv;
@@ -300,8 +321,8 @@ __global__ void __launch_bounds__(kPickThreads, 2) cache_pick_kernel(const Cache
   int32_t* sel = a.sel + u * a.top_k;
   const int k = min(a.top_k, n);
 #pragma unroll
-  for (int i = 0; i < 3; ++i)
-    *reinterpret_cast<int4*>(&sh.hist[i][4 * threadIdx.x]) = make_int4(0, 0, 0, 0);
+  for (int i = 0; i < 3 * kBins; i += 4 * kPickThreads)
+    *reinterpret_cast<int4*>(&sh.hist[0][i + 4 * threadIdx.x]) = make_int4(0, 0, 0, 0);
   if (threadIdx.x == 0) sh.n_list = 0;
   wait_for_inputs();
   if (threadIdx.x == 0) a.cnt[u] = k;
@@ -340,7 +361,7 @@ __global__ void __launch_bounds__(kPickThreads, 2) cache_pick_kernel(const Cache
       if ((key & mask) == prefix) atomicAdd(&sh.hist[pass][(key >> shift) & bits], 1);
     }
     __syncthreads();
-    find_bin(sh.hist[pass], left, sh);
+    find_bin<kPickThreads>(sh.hist[pass], left, sh);
     prefix |= static_cast<uint32_t>(sh.digit) << shift;
     mask |= bits << shift;
     left = sh.left;
@@ -409,7 +430,8 @@ __global__ void __launch_bounds__(kPickThreads, 2) cache_pick_kernel(const Cache
       for (int shift = 55; shift >= 0; shift -= 11) {
         constexpr uint64_t bits = 0x7ff;
         __syncthreads();
-        *reinterpret_cast<int4*>(&sh.hist[0][4 * threadIdx.x]) = make_int4(0, 0, 0, 0);
+        for (int i = 4 * threadIdx.x; i < kBins; i += 4 * kPickThreads)
+          *reinterpret_cast<int4*>(&sh.hist[0][i]) = make_int4(0, 0, 0, 0);
         __syncthreads();
         for (int i = i0 + lane; i < i1; i += 32)
           if (keys[i] <= above && keys[i] >= below) {
@@ -418,7 +440,7 @@ __global__ void __launch_bounds__(kPickThreads, 2) cache_pick_kernel(const Cache
               atomicAdd(&sh.hist[0][static_cast<int>((key >> shift) & bits)], 1);
           }
         __syncthreads();
-        find_bin(sh.hist[0], want, sh);
+        find_bin<kPickThreads>(sh.hist[0], want, sh);
         found |= static_cast<uint64_t>(sh.digit) << shift;
         known |= bits << shift;
         want = sh.left;
@@ -481,28 +503,31 @@ cudaError_t launch_scores(const CacheSelectArgs& a, cudaStream_t st) {
                       kScoreThreads, 0, st, false, a);
 }
 
+template <int D, bool kBf16>
+cudaError_t launch_pick(const CacheSelectArgs& a, cudaStream_t st) {
+  // 256 threads up to 4096 blocks, whose few keys leave most instructions to
+  // the bins and barriers, 512 above.
+  const bool few = a.s.max_blocks <= 4096, staged = a.s.max_blocks <= kStagedMax;
+  const int smem = staged ? a.s.max_blocks * 4 : 0;
+  const auto kernel = few      ? cache_pick_kernel<D, kBf16, true, 256>
+                      : staged ? cache_pick_kernel<D, kBf16, true, 512>
+                               : cache_pick_kernel<D, kBf16, false, 512>;
+  if (smem > 8 * 1024) {  // with the static part, more than 48 KB needs leave
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  const dim3 units(static_cast<unsigned>(a.s.batch) * a.T * a.c.Hkv);
+  return launch_after(kernel, units, few ? 256 : 512, smem, st, true, a);
+}
+
 }  // namespace
 
 cudaError_t launch_cache_select(const CacheSelectArgs& a, cudaStream_t st) {
   cudaError_t e = a.c.d == 128 ? launch_scores<128>(a, st) : launch_scores<64>(a, st);
   if (e != cudaSuccess) return e;
-  const dim3 units(static_cast<unsigned>(a.s.batch) * a.T * a.c.Hkv);
-  const bool staged = a.s.max_blocks <= kStagedMax;
-  const int smem = staged ? a.s.max_blocks * 4 : 0;
-  void (*kernel)(CacheSelectArgs);
-  if (a.c.d == 128)
-    kernel = a.bf16 ? (staged ? cache_pick_kernel<128, true, true> : cache_pick_kernel<128, true, false>)
-                    : (staged ? cache_pick_kernel<128, false, true>
-                              : cache_pick_kernel<128, false, false>);
-  else
-    kernel = a.bf16 ? (staged ? cache_pick_kernel<64, true, true> : cache_pick_kernel<64, true, false>)
-                    : (staged ? cache_pick_kernel<64, false, true>
-                              : cache_pick_kernel<64, false, false>);
-  if (smem > 8 * 1024) {  // with the static part, more than 48 KB needs leave
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-  }
-  return launch_after(kernel, units, kPickThreads, smem, st, true, a);
+  if (a.c.d == 128) return a.bf16 ? launch_pick<128, true>(a, st) : launch_pick<128, false>(a, st);
+  return a.bf16 ? launch_pick<64, true>(a, st) : launch_pick<64, false>(a, st);
 }
 
 }  // namespace msa

@@ -25,12 +25,16 @@
  * (>= -126) with amax <= 448 * 2^e over the block's slots; 0 for a block of
  * zeros; NaN, with codes of 0, for a block that holds a NaN or an infinity
  * (every row that attends a slot of such a block gets NaN).  The attention
- * takes any finite scale >= 0 and finite codes.  k_mean is written when a
- * block becomes full: the mean of its keys code * scale, rounded once.
+ * takes any finite scale >= 0 and finite codes; an append to a block that holds
+ * slots and an eviction take the powers of two that these two write.  k_mean
+ * is written when a block becomes full: the mean of its keys code * scale,
+ * rounded once.
  *   The pages of one sequence are distinct.  Pages of full blocks may be
  * shared between sequences (a common prefix): the attention and the
- * selection only read, an append writes only the blocks that take new slots,
- * an eviction writes only dst_table's pages.
+ * selection only read, an append writes only the blocks that take new slots
+ * (which must not be shared), an eviction writes only dst_table's pages.  A
+ * sequence's last slots (rejected drafts) are dropped by lowering its length;
+ * the block that then ends it keeps its scale.
  * Device data is checked by the kernels: a length outside [0, max_blocks *
  * block] is clamped (an append skips the sequence), a slot whose page is not in
  * [0, n_pages) is left out (not written, not attended; an eviction that keeps it
@@ -133,7 +137,8 @@ size_t msa_cache_select_workspace_size(const msa_kv_cache *cache,
  *   score(l) = sum over query heads h of c's group of <q_h, k_mean_l>,
  * for the blocks wholly before the window, (l+1) * block <= p - window + 1.
  * The min(top_k, #candidates) best are chosen, ties to the lower index, as
- * the scores are in 64-bit arithmetic; NaN ranks last.
+ * the scores are in 64-bit arithmetic (a head sum's own rounding 2^-48 * Hq /
+ * Hkv of its magnitudes at most); NaN ranks last.
  *   sel  [batch, n_q, Hkv, top_k] int32, written: chosen blocks ascending,
  *        then -1
  *   cnt  [batch, n_q, Hkv] int32, written: how many were chosen

@@ -13,7 +13,7 @@
 // (parts too long for shared memory: once a digit, from L2): 4 bytes a slot,
 // against the 2 d bytes a kept slot costs in the gather; what bounds a call is
 // the chain of some ten barriers: 4160 slots of 64 (sequence, head) pairs in
-// 10 us, 131072 of 16 (clusters of 8) in 32.
+// 10 us, 131072 of 16 (clusters of 8) in 29.
 #include <math.h>
 
 #include <cooperative_groups.h>

@@ -120,19 +120,28 @@ struct Raw<false> {
   }
 };
 
-// Codes of scale s rounded again to the scale 1 / inv >= s, in halves: code *
-// 2^-k is exact in them down to 2^-24, and what is smaller than that is far
-// below the 2^-10 at which e4m3 rounds to its least value.
+// Codes of scale s rounded again to the scale 1 / inv, in halves: code * 2^-k
+// is exact in them down to 2^-24, and what is smaller than that is far below
+// the 2^-10 at which e4m3 rounds to its least value.  The new scale is the
+// smaller one, by up to 2^17, where the slots kept of a block are all tiny: a
+// factor that halves do not hold is applied in two steps, each exact.
 __device__ __forceinline__ uint4 rescale(const uint4& x, float s, float inv) {
-  const __half2 f = __float2half2_rn(s * inv);
+  float by = s * inv;
+  const bool twice = by > 32768.f;
+  if (twice) by *= 1.f / 256.f;
+  const __half2 f = __float2half2_rn(by);
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   uint32_t c[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t a = e4m3x2_to_half2(static_cast<uint16_t>(w[i]));
     const uint32_t b = e4m3x2_to_half2(static_cast<uint16_t>(w[i] >> 16));
-    const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&a), f);
-    const __half2 z = __hmul2(*reinterpret_cast<const __half2*>(&b), f);
+    __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&a), f);
+    __half2 z = __hmul2(*reinterpret_cast<const __half2*>(&b), f);
+    if (twice) {
+      y = __hmul2(y, __float2half2_rn(256.f));
+      z = __hmul2(z, __float2half2_rn(256.f));
+    }
     uint16_t lo, hi;
     asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;"
         : "=h"(lo) : "r"(*reinterpret_cast<const uint32_t*>(&y)));
@@ -216,7 +225,7 @@ __global__ void __launch_bounds__(kMaxThreads, kMaxThreads == 512 ? 1 : kBf16 ? 
   Raw<kBf16> v[kRows];
   {
     const int64_t off =
-        (static_cast<int64_t>(r0 + slot0 + row - first) * Hkv + h) * d + col * kVec;
+        ((static_cast<int64_t>(r0) + (slot0 - first) + row) * Hkv + h) * d + col * kVec;
     const int64_t step = static_cast<int64_t>(apart) * Hkv * d;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {

@@ -261,9 +261,11 @@ __device__ __forceinline__ void load_row(const void* p, int64_t at, float* v) {
 
 // Score of block l in 64 bits, by one warp, a lane D/32 dims.  The sum over
 // the heads is kept as an fp32 value and the exact error of each addition (the
-// error-free sum of two floats), which is as good and spares most of the
-// 64-bit operations, each 16 cycles of an SM for a warp; the rest are the
-// products and their sum.  Eight heads' loads go together.
+// error-free sum of two floats); the errors' own sum may round, 2^-48 g of the
+// sum of magnitudes at most, where heads differ by many binades.  That spares
+// most of the 64-bit operations, each 16 cycles of an SM for a warp; left are
+// the products, their sum, and heads whose sum is beyond fp32.  Eight heads'
+// loads go together.
 template <int D, bool kBf16>
 __device__ __forceinline__ double exact_score(const CacheSelectArgs& a, int b, int t, int c,
                                               int l) {
@@ -296,8 +298,14 @@ __device__ __forceinline__ double exact_score(const CacheSelectArgs& a, int b, i
 #pragma unroll
   for (int i = 0; i < kN; ++i) {
     const double k = km[i];
-    s += static_cast<double>(sum[i]) * k;
-    if (rest[i] != 0.f && !isinf(sum[i])) s += static_cast<double>(rest[i]) * k;
+    double x = sum[i];
+    if (!isfinite(sum[i])) {
+      x = 0.0;
+      for (int h = 0; h < g; ++h)
+        x += static_cast<double>(q_at<kBf16>(a.q, q0 + static_cast<int64_t>(h) * D + i));
+    }
+    s += x * k;
+    if (rest[i] != 0.f && isfinite(sum[i])) s += static_cast<double>(rest[i]) * k;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);

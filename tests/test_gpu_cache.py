@@ -439,6 +439,21 @@ def test_scores_that_fp32_cannot_tell_apart(n):
         assert selected(sel, cnt) == want
 
 
+def test_head_sums_beyond_fp32():
+    """The heads' sum overflows 32 bits, the 64-bit scores order the blocks."""
+    n = 70
+    rng = np.random.default_rng(24)
+    means = np.zeros((n, 1, 64))
+    means[:, 0, 0] = rng.permutation(n) * 2.0 ** -6
+    cache, t, lens = mean_cache(means)
+    t = np.concatenate([t, [[n]]], axis=1)
+    q = torch.zeros((1, 1, 4, 64), device=DEV, dtype=torch.bfloat16)
+    q[..., 0] = 2.0 ** 127
+    sel, cnt = msa.cache_block_select(q, cache, i32(t), i32(lens), 1, 9)
+    best = sorted(np.argsort(-means[:, 0, 0])[:9].tolist())
+    assert sel[0, 0, 0].tolist() == best and cnt.item() == 9
+
+
 def test_not_a_number_ranks_last():
     means = np.random.default_rng(3).normal(size=(50, 1, 64))
     means[7] = np.nan
@@ -531,6 +546,22 @@ def test_evict_of_rows_longer_than_shared_memory():
     cache, pool, t, free = filled([n], 1, 64, 256, seed=31, extra=4)
     w = torch.randint(0, 50_000, (1, 1, t.shape[1] * 256), device=DEV).float() / 64   # many ties
     check_evict(cache, pool, t, [n], w, free[:4].reshape(1, 4), budget, 50)
+
+
+@pytest.mark.parametrize("tiny", [2.0 ** -9, 2.0 ** -8, 1.75 * 2.0 ** -7, 2.0 ** -6])
+def test_evict_leaves_only_tiny_codes_of_a_block(tiny):
+    """The new scale is far below the old one when the outlier is evicted."""
+    rng = np.random.default_rng(33)
+    k = rng.choice([0.0, tiny, -tiny, 2.0 ** -9], size=(128, 1, 64)).astype(np.float32)
+    k[:, 0, 0] = tiny
+    k[::32, 0, 5] = 448.0                # every block's scale is 1
+    t, dst = np.array([[0, 1, 2, 3]], dtype=np.int32), np.array([[6, 4]], dtype=np.int32)
+    cache = new_cache(8, 1, 64, 32)
+    kt = torch.as_tensor(k, device=DEV)
+    msa.cache_append(cache, kt, kt, i32([0, 128]), i32(t), i32([128]), 128)
+    w = torch.rand((1, 1, 128), device=DEV) + 1
+    w[..., ::32] = 0
+    check_evict(cache, pool_of(cache), t, [128], w, dst, 50, 8)
 
 
 def test_evict_of_poisoned_blocks():
@@ -692,6 +723,26 @@ def test_pages_that_do_not_exist_and_lengths_that_cannot_be():
 
 
 @pytest.mark.large
+def test_rejected_drafts_are_dropped_by_the_length():
+    """Lengths go back by some drafts and other tokens take their slots."""
+    cache, pool, t, free = filled([61, 30], 2, 64, 32, seed=61, extra=2, width=3)
+    t[0, 2], t[1, 1] = free[:2]
+    rng = np.random.default_rng(62)
+    q = torch.as_tensor(rng.normal(size=(2, 1, 4, 64)), device=DEV).to(torch.bfloat16)
+    lens = [61, 30]
+    for new, back in ((4, 3), (4, 4), (2, 0), (4, 1)):
+        k, v = (torch.as_tensor(rng.normal(size=(2 * new, 2, 64)) * 4, device=DEV).to(torch.bfloat16)
+                for _ in range(2))
+        lens, cu = [n + new for n in lens], [0, new, 2 * new]
+        msa.cache_append(cache, k, v, i32(cu), i32(t), i32(lens), new)
+        R.append(pool, k.double().cpu().numpy(), v.double().cpu().numpy(), cu, t, lens)
+        lens = [n - back for n in lens]
+        out, lse = msa.cache_attention(q, cache, i32(t), i32(lens))
+        ref = R.attention(pool, q.double().cpu().numpy(), t, lens, 1 << 30, 1 / 8)
+        check_attention(out, lse, ref, 64, True, 30.0)
+    same_pool(cache, pool)
+
+
 def test_offsets_past_32_bits():
     """A pool of more than 2^32 bytes of codes: pages at its far end."""
     hkv, d, block = 8, 128, 256

@@ -32,7 +32,7 @@
 // the loop's some 950 instructions a chunk on 8 warps an SM bound it: 16
 // sequences of 32K take 140 us with one token (6.05 TB/s), 150 with two, 218
 // with four (362 as two passes of 16 rows).  Short calls are bound by latency:
-// 32K tokens of two KV heads take 11.7 us with the join, of which 6.6 are here;
+// 32K tokens of one KV head take 11.7 us with the join, of which 6.6 are here;
 // a part's first pass through the code, cold in the instruction cache, costs
 // more than its chunks.
 // fp32 rows run on the CUDA cores with fp32 arithmetic throughout.
@@ -158,7 +158,7 @@ __device__ __forceinline__ void each_entry(const CacheAttnArgs& a, const Plan& p
 // The W chunks of all units, cut into P ranges, one a CTA: the first W % P
 // have one chunk more.  A CTA's warps take at least one chunk each in fp32, two
 // in bf16, where a second chunk costs less than the parts to join (one sequence
-// of 32K slots, two KV heads: 13.1 us with one, 11.7 with two; fp32 with 2K
+// of 32K slots, one KV head: 13.1 us with one, 11.7 with two; fp32 with 2K
 // slots: 13.8 with one, 17.2 with two).  W fits 31 bits (the entry points check).
 struct Cut {
   uint32_t P, each, more;
@@ -346,55 +346,71 @@ __device__ __forceinline__ void store_dims(const CacheAttnArgs& a, const Entry& 
   }
 }
 
-// Joins the warps' sums of a unit's range and writes them.  osum rows are
-// padded by 4 floats.
+// Place of a row's dim in the warps' sums [warp][row][D]: rows padded by 4
+// floats, and every second group of D/8 dims with neighbouring 16-byte pieces
+// swapped, so that the fragments' stores meet no bank twice.
+template <int D>
+__device__ __forceinline__ int sum_at(int row, int dim) {
+  const int piece = dim >> 2;
+  return row * (D + 4) + ((piece ^ (piece / (D / 32) & 1)) << 2) + (dim & 3);
+}
+
+// Joins the warps' sums of a unit's range and writes them: a thread a row for
+// the statistics, which become each warp's factor, then all of them the dims.
 template <int D, int kTile>
 __device__ __forceinline__ void join_warps(const CacheAttnArgs& a, const Plan& p, const Entry& e,
-                                           int c, int rt, const float* osum, const Stat* stat,
+                                           int c, int rt, const float* osum, Stat* stat,
                                            bool whole, int64_t slot) {
-  constexpr int kLd = D + 4;
-  for (int i = threadIdx.x; i < kTile * (D / 4); i += kThreads) {
-    const int r = i / (D / 4), dim = (i - r * (D / 4)) * 4;
-    const int m = rt * kTile + r;
-    if (m >= p.rows) break;
+  const int left = p.rows - rt * kTile;  // rows from the tile's first on
+  if (static_cast<int>(threadIdx.x) < min(kTile, left)) {
+    const int r = threadIdx.x;
+    Stat s[kWarps];
     float mx = -INFINITY, l = 0.f, R = -INFINITY, S = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const Stat& s = stat[w * kTile + r];
-      mx = fmaxf(mx, s.m);
-      if ((s.R - R) + (s.S - S) > 0.f) {
-        R = s.R;
-        S = s.S;
+      s[w] = stat[w * kTile + r];
+      mx = fmaxf(mx, s[w].m);
+      if ((s[w].R - R) + (s[w].S - S) > 0.f) {
+        R = s[w].R;
+        S = s[w].S;
       }
     }
     mx = finite_or_0(mx);
     R = finite_or_0(R);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w)
+      if (!(s[w].m == -INFINITY && s[w].l == 0.f)) l += s[w].l * ex2(s[w].m - mx);
+    // l == 0: no slot attended.
+    const float f = l == 0.f ? 0.f : ex2((R - mx) + (S - kPBits)) / l;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w)
+      stat[w * kTile + r].l = s[w].m == -INFINITY && s[w].l == 0.f
+                                  ? 0.f
+                                  : ex2((finite_or_0(s[w].R) - R) + (s[w].S - S)) * f;
+    if (whole)
+      store_lse(a, p, e, c, rt * kTile + r, mx, l);
+    else
+      a.part_stat[slot * kTile + r] = make_float2(l == 0.f ? -INFINITY : mx, l);
+  }
+  __syncthreads();
+#pragma unroll 2
+  for (int i = threadIdx.x; i < kTile * (D / 4); i += kThreads) {
+    const int r = i / (D / 4), dim = (i - r * (D / 4)) * 4;
+    if (r >= left) break;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const Stat& s = stat[w * kTile + r];
-      if (s.m == -INFINITY && s.l == 0.f) continue;
-      l += s.l * ex2(s.m - mx);
-      const float f = ex2((finite_or_0(s.R) - R) + (s.S - S));
-      const float4 x = *reinterpret_cast<const float4*>(osum + (w * kTile + r) * kLd + dim);
+      const float f = stat[w * kTile + r].l;
+      const float4 x = *reinterpret_cast<const float4*>(osum + sum_at<D>(w * kTile + r, dim));
       v.x += x.x * f;
       v.y += x.y * f;
       v.z += x.z * f;
       v.w += x.w * f;
     }
-    // l == 0: no slot attended.
-    const float f = l == 0.f ? 0.f : ex2((R - mx) + (S - kPBits)) / l;
-    v.x *= f;
-    v.y *= f;
-    v.z *= f;
-    v.w *= f;
-    if (whole) {
-      store_out(a, e, c, m, dim, v);
-      if (dim == 0) store_lse(a, p, e, c, m, mx, l);
-    } else {
+    if (whole)
+      store_out(a, e, c, rt * kTile + r, dim, v);
+    else
       *reinterpret_cast<float4*>(a.o_part + (slot * kTile + r) * D + dim) = v;
-      if (dim == 0) a.part_stat[slot * kTile + r] = make_float2(l == 0.f ? -INFINITY : mx, l);
-    }
   }
 }
 
@@ -788,7 +804,6 @@ struct MmaBody {
   // The warp's sums to shared memory.
   __device__ __forceinline__ void finish(float* osum, Stat* stat) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t4 = lane & 3;
-    constexpr int kLd = D + 4;
 #pragma unroll
     for (int n = 0; n < kNt; ++n)
 #pragma unroll
@@ -798,12 +813,13 @@ struct MmaBody {
         for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
         const int row = warp * kTile + 8 * n + 2 * t4 + r;
         if (g == 0) stat[row] = Stat{R[n][r], sum, R[n][r], S[n][r]};
-        float* to = osum + row * kLd + g * (D / 8);
 #pragma unroll
-        for (int i = 0; i < kMt; ++i) {
-          to[i] = o[i][n][r];
-          to[D / 16 + i] = o[i][n][2 + r];
-        }
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+          for (int i = 0; i < kMt; i += 4)
+            *reinterpret_cast<float4*>(osum + sum_at<D>(row, g * (D / 8) + half * (D / 16) + i)) =
+                make_float4(o[i][n][2 * half + r], o[i + 1][n][2 * half + r],
+                            o[i + 2][n][2 * half + r], o[i + 3][n][2 * half + r]);
       }
   }
 };
@@ -964,7 +980,6 @@ struct SimtBody {
 
   __device__ __forceinline__ void finish(float* osum, Stat* stat) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    constexpr int kLd = D + 4;
 #pragma unroll
     for (int r = 0; r < kTile; ++r) {
       float mx = m[r];
@@ -976,7 +991,7 @@ struct SimtBody {
       // (a weight of 1 is 2^0 here, 2^kPBits in the other body)
       if (lane == 0) stat[warp * kTile + r] = Stat{mx, sum, R[r], S[r] + kPBits};
 #pragma unroll
-      for (int k = 0; k < kDl; ++k) osum[(warp * kTile + r) * kLd + lane * kDl + k] = o[r][k];
+      for (int k = 0; k < kDl; ++k) osum[sum_at<D>(warp * kTile + r, lane * kDl + k)] = o[r][k];
     }
   }
 };

@@ -645,6 +645,38 @@ def test_calls_on_a_side_stream():
     torch.testing.assert_close(top[0], msa.cache_topk_attention(q, cache, tt, tl, 50, 2)[0], rtol=0, atol=0)
 
 
+def test_calls_on_two_streams_and_two_graphs_at_once():
+    """Calls that overlap have workspaces of their own."""
+    lens = [9000, 300, 4096]
+    cache, _, t, _ = filled(lens, 2, 128, 64, seed=51)
+    tt, tl = i32(t), i32(lens)
+    qs = [torch.randn((3, n, 16, 128), device=DEV).to(torch.bfloat16) for n in (1, 2)]
+
+    def calls(q):
+        w = torch.zeros((3, 2, t.shape[1] * 64), device=DEV)
+        return (*msa.cache_attention(q, cache, tt, tl, weights=w), w,
+                *msa.cache_topk_attention(q, cache, tt, tl, 100, 9))
+
+    want = [calls(q) for q in qs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in qs]
+    graphs, held = [torch.cuda.CUDAGraph() for _ in qs], []
+    for q, g in zip(qs, graphs):
+        with torch.cuda.graph(g):
+            held.append(calls(q))
+    got = [[], []]
+    for _ in range(5):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(calls(qs[i]))
+                graphs[1 - i].replay()
+        torch.cuda.synchronize()
+    for i in range(2):
+        for run in (*got[i], held[i]):
+            for x, y in zip(run, want[i]):
+                assert torch.equal(x, y)
+
+
 def test_a_step_replays_from_a_graph():
     """Append, attention with weights, top-k attention and eviction captured
     once: replays on new inputs, longer sequences and other pages give the

@@ -159,14 +159,18 @@ __device__ __forceinline__ void each_entry(const CacheAttnArgs& a, const Plan& p
 // have one chunk more.  A CTA's warps take at least one chunk each in fp32, two
 // in bf16, where a second chunk costs less than the parts to join (one sequence
 // of 32K slots, one KV head: 13.1 us with one, 11.7 with two; fp32 with 2K
-// slots: 13.8 with one, 17.2 with two).  W fits 31 bits (the entry points check).
+// slots: 13.8 with one, 17.2 with two) -- unless that is more than a unit: a
+// unit's rows and sums cost a CTA more than its chunks (200 units of one chunk,
+// 24 rows: 84 us at eight units a CTA, 14 at one).  W fits 31 bits (the entry
+// points check).
 struct Cut {
   uint32_t P, each, more;
 };
-__device__ __forceinline__ Cut cut_of(const CacheAttnArgs& a, uint32_t W) {
+__device__ __forceinline__ Cut cut_of(const CacheAttnArgs& a, const Plan& p, uint32_t W) {
   Cut k;
   const uint32_t least = a.in_bf16 ? 2 * kWarps : kWarps;
-  k.P = max(1u, min(static_cast<uint32_t>(a.n_ctas), (W + least - 1) / least));
+  const uint32_t units = static_cast<uint32_t>(p.n_entries) * p.units;
+  k.P = max(1u, min(static_cast<uint32_t>(a.n_ctas), min(W, max((W + least - 1) / least, units))));
   k.each = W / k.P;
   k.more = W - k.each * k.P;
   return k;
@@ -1021,7 +1025,7 @@ __global__ void __launch_bounds__(kThreads, Body::kPerSm) cache_attn_kernel(cons
   const Scan sc = scan_entries<kWarps>(a, p, scan);
   const uint32_t W = sc.total * p.units;
   if (W == 0) return;
-  const Cut cut = cut_of(a, W);
+  const Cut cut = cut_of(a, p, W);
   if (blockIdx.x >= cut.P) return;
   const uint32_t begin = cta_begin(cut, blockIdx.x), end = cta_begin(cut, blockIdx.x + 1);
   // The entry that holds chunk `begin`, and its first chunk.
@@ -1183,7 +1187,7 @@ __global__ void __launch_bounds__(kWpr == 1 ? kThreads : 32 * kWpr)
     if (part == 0 && lane == 0) store_lse(a, p, e, c, m, 0.f, 0.f);
     return;
   }
-  const Cut cut = cut_of(a, sc.total * p.units);
+  const Cut cut = cut_of(a, p, sc.total * p.units);
   const uint32_t u0 = found[mine] * p.units + (c * p.n_tiles + rt) * e.n_chunks;
   const int c0 = cta_of(cut, u0), c1 = cta_of(cut, u0 + e.n_chunks - 1);
   if (c0 == c1) return;  // written whole

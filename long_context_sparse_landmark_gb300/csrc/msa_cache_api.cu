@@ -145,7 +145,8 @@ AttnPlan attn_plan(int Hkv, int d, int block, int batch, int n_q, int Hq, int ma
   const int64_t chunks = units * (static_cast<int64_t>(max_blocks) * block / msa::kChunk);
   AttnPlan p{};
   p.n_ctas = static_cast<int>(msa::max64(
-      1, msa::min64(msa::cache_attn_max_ctas(tile, in_bf16), (chunks + 3) / 4)));
+      1, msa::min64(msa::cache_attn_max_ctas(tile, in_bf16),
+                    msa::max64(units, (chunks + 3) / 4))));
   size_t at = 0;
   p.o = at;
   at += up(static_cast<size_t>(2) * p.n_ctas * tile * d * sizeof(float));

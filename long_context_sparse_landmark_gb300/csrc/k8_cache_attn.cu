@@ -840,7 +840,7 @@ struct SimtBody {
   static constexpr int kSums = kWarps * kTile * (D + 4) * 4;
   static constexpr int kSmem = kSums + (kTile * D + kTile + kWarps * kChunk * kTile) * 4;
 
-  float o[kTile][kDl];
+  float2 o[kTile / 2][kDl];  // rows 2i, 2i + 1
   float m[kTile], l[kTile], R[kTile], S[kTile];
   float* qsm;
   float* psm;
@@ -851,16 +851,17 @@ struct SimtBody {
     float* q = reinterpret_cast<float*>(smem + kSums);
     int* pos = reinterpret_cast<int*>(q + kTile * D);
 #pragma unroll 1
-    for (int i = threadIdx.x; i < kTile * D; i += kThreads) {
-      const int r = i / D, row = rt * kTile + r;
+    for (int i = threadIdx.x; i < kTile * D / 4; i += kThreads) {
+      const int r = i / (D / 4), dim = (i - r * (D / 4)) * 4, row = rt * kTile + r;
       int t, h;
       row_of(a, e, c, min(row, p.rows - 1), &t, &h);
-      float v = 0.f;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (row < p.rows)
-        v = static_cast<const float*>(
-            a.q)[((static_cast<int64_t>(e.b) * a.T + t) * a.Hq + h) * D + (i - r * D)];
-      q[i] = v;
-      if (i == r * D) pos[r] = e.len - a.T + t;
+        v = *reinterpret_cast<const float4*>(
+            static_cast<const float*>(a.q) +
+            ((static_cast<int64_t>(e.b) * a.T + t) * a.Hq + h) * D + dim);
+      *reinterpret_cast<float4*>(q + r * D + dim) = v;
+      if (dim == 0) pos[r] = e.len - a.T + t;
     }
   }
 
@@ -874,8 +875,21 @@ struct SimtBody {
     for (int r = 0; r < kTile; ++r) {
       m[r] = R[r] = -INFINITY;
       l[r] = S[r] = 0.f;
+    }
 #pragma unroll
-      for (int k = 0; k < kDl; ++k) o[r][k] = 0.f;
+    for (int r = 0; r < kTile / 2; ++r)
+#pragma unroll
+      for (int k = 0; k < kDl; ++k) o[r][k] = make_float2(0.f, 0.f);
+  }
+
+  // 8 slots' codes of the lane's dims.
+  __device__ __forceinline__ static void load_v(const uint8_t* at, uint32_t* w) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if constexpr (D == 128)
+        w[j] = __ldg(reinterpret_cast<const uint32_t*>(at + j * D));
+      else
+        w[j] = __ldg(reinterpret_cast<const uint16_t*>(at + j * D));
     }
   }
 
@@ -883,14 +897,19 @@ struct SimtBody {
                                         int c, int rt, const Chunk& x) {
     const int lane = threadIdx.x & 31;
     if (!MSA_IN_RANGE(x.at, kChunk, a.c.n_pages * a.c.Hkv * a.c.block, a.status)) return;
-    const uint8_t* krow = a.c.k_codes + (x.at + lane) * D;
-    float s[kTile];
+    const uint4* krow = reinterpret_cast<const uint4*>(a.c.k_codes + (x.at + lane) * D);
+    const uint8_t* vbase = a.c.v_codes + x.at * D + lane * kDl;
+    // Even and odd dims side by side; a piece of the row is under way while
+    // the one before is multiplied, and eight slots' values likewise.
+    float2 s2[kTile];
 #pragma unroll
-    for (int r = 0; r < kTile; ++r) s[r] = 0.f;
+    for (int r = 0; r < kTile; ++r) s2[r] = make_float2(0.f, 0.f);
+    uint4 w0 = __ldg(krow), w1 = __ldg(krow + 1);
 #pragma unroll 1
     for (int d0 = 0; d0 < D; d0 += 16) {
-      const uint4 w4 = __ldg(reinterpret_cast<const uint4*>(krow + d0));
-      const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+      const uint32_t w[4] = {w0.x, w0.y, w0.z, w0.w};
+      w0 = w1;
+      if (d0 + 32 < D) w1 = __ldg(krow + d0 / 16 + 2);
       float kf[16];
 #pragma unroll
       for (int i = 0; i < 4; ++i) e4m3x4_to_float(w[i], kf + 4 * i);
@@ -899,12 +918,16 @@ struct SimtBody {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float4 qv = *reinterpret_cast<const float4*>(qsm + r * D + d0 + 4 * i);
-          s[r] = fmaf(qv.x, kf[4 * i], s[r]);
-          s[r] = fmaf(qv.y, kf[4 * i + 1], s[r]);
-          s[r] = fmaf(qv.z, kf[4 * i + 2], s[r]);
-          s[r] = fmaf(qv.w, kf[4 * i + 3], s[r]);
+          s2[r] = __ffma2_rn(make_float2(qv.x, qv.y), make_float2(kf[4 * i], kf[4 * i + 1]), s2[r]);
+          s2[r] =
+              __ffma2_rn(make_float2(qv.z, qv.w), make_float2(kf[4 * i + 2], kf[4 * i + 3]), s2[r]);
         }
     }
+    uint32_t vw[8];
+    load_v(vbase, vw);
+    float s[kTile];
+#pragma unroll
+    for (int r = 0; r < kTile; ++r) s[r] = s2[r].x + s2[r].y;
     const int key = x.key0 + lane;
     // Scores in log2 units as a float and what it leaves, and maxima rounded
     // up to whole numbers: the exponentials see differences whose error goes by
@@ -944,7 +967,7 @@ struct SimtBody {
       if (up > 0.f) {
         const float down = exp2f(-up);
 #pragma unroll
-        for (int k = 0; k < kDl; ++k) o[r][k] *= down;
+        for (int k = 0; k < kDl; ++k) (r & 1 ? o[r / 2][k].y : o[r / 2][k].x) *= down;
         R[r] = top;
         S[r] = x.lvs;
       }
@@ -957,28 +980,32 @@ struct SimtBody {
     *reinterpret_cast<float4*>(psm + lane * kTile + 4) = make_float4(pw[4], pw[5], pw[6], pw[7]);
     const uint32_t held = __ballot_sync(0xffffffffu, any);
     __syncwarp();
-    const uint8_t* vbase = a.c.v_codes + x.at * D + lane * kDl;
-#pragma unroll 8
-    for (int j = 0; j < kChunk; ++j) {
-      float vf[kDl];
-      if constexpr (D == 128) {
-        uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(vbase + j * D));
-        w = held >> j & 1 ? w : 0u;  // a masked slot holds anything
-        e4m3x4_to_float(w, vf);
-      } else {
-        uint16_t w = __ldg(reinterpret_cast<const uint16_t*>(vbase + j * D));
-        w = held >> j & 1 ? w : static_cast<uint16_t>(0);
-        const float2 f = e4m3x2_to_float2(w);
-        vf[0] = f.x;
-        vf[1] = f.y;
+#pragma unroll 1
+    for (int j0 = 0; j0 < kChunk; j0 += 8) {
+      uint32_t cur[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) cur[j] = held >> (j0 + j) & 1 ? vw[j] : 0u;  // masked: anything
+      if (j0 + 8 < kChunk) load_v(vbase + (j0 + 8) * D, vw);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float vf[4];
+        if constexpr (D == 128) {
+          e4m3x4_to_float(cur[j], vf);
+        } else {
+          const float2 f = e4m3x2_to_float2(static_cast<uint16_t>(cur[j]));
+          vf[0] = f.x;
+          vf[1] = f.y;
+        }
+        const float4 p0 = *reinterpret_cast<const float4*>(psm + (j0 + j) * kTile);
+        const float4 p1 = *reinterpret_cast<const float4*>(psm + (j0 + j) * kTile + 4);
+        const float2 pr[kTile / 2] = {make_float2(p0.x, p0.y), make_float2(p0.z, p0.w),
+                                      make_float2(p1.x, p1.y), make_float2(p1.z, p1.w)};
+#pragma unroll
+        for (int k = 0; k < kDl; ++k)
+#pragma unroll
+          for (int r = 0; r < kTile / 2; ++r)
+            o[r][k] = __ffma2_rn(pr[r], make_float2(vf[k], vf[k]), o[r][k]);
       }
-      const float4 p0 = *reinterpret_cast<const float4*>(psm + j * kTile);
-      const float4 p1 = *reinterpret_cast<const float4*>(psm + j * kTile + 4);
-      const float pr[kTile] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
-#pragma unroll
-      for (int r = 0; r < kTile; ++r)
-#pragma unroll
-        for (int k = 0; k < kDl; ++k) o[r][k] = fmaf(pr[r], vf[k], o[r][k]);
     }
   }
 
@@ -995,7 +1022,8 @@ struct SimtBody {
       // (a weight of 1 is 2^0 here, 2^kPBits in the other body)
       if (lane == 0) stat[warp * kTile + r] = Stat{mx, sum, R[r], S[r] + kPBits};
 #pragma unroll
-      for (int k = 0; k < kDl; ++k) osum[sum_at<D>(warp * kTile + r, lane * kDl + k)] = o[r][k];
+      for (int k = 0; k < kDl; ++k) 
+        osum[sum_at<D>(warp * kTile + r, lane * kDl + k)] = r & 1 ? o[r / 2][k].y : o[r / 2][k].x;
     }
   }
 };

@@ -841,7 +841,7 @@ struct SimtBody {
   static constexpr int kSmem = kSums + (kTile * D + kTile + kWarps * kChunk * kTile) * 4;
 
   float2 o[kTile / 2][kDl];  // rows 2i, 2i + 1
-  float m[kTile], l[kTile], R[kTile], S[kTile];
+  float l[kTile], R[kTile], S[kTile];  // l: the lane's slots, in units of 2^R
   float* qsm;
   float* psm;
 
@@ -873,7 +873,7 @@ struct SimtBody {
     psm = qsm + kTile * D + kTile + (threadIdx.x >> 5) * kChunk * kTile;
 #pragma unroll
     for (int r = 0; r < kTile; ++r) {
-      m[r] = R[r] = -INFINITY;
+      R[r] = -INFINITY;
       l[r] = S[r] = 0.f;
     }
 #pragma unroll
@@ -929,9 +929,9 @@ struct SimtBody {
 #pragma unroll
     for (int r = 0; r < kTile; ++r) s[r] = s2[r].x + s2[r].y;
     const int key = x.key0 + lane;
-    // Scores in log2 units as a float and what it leaves, and maxima rounded
-    // up to whole numbers: the exponentials see differences whose error goes by
-    // their own size, and a change of maximum scales by a power of two.
+    // Scores in log2 units as a float and what it leaves, and references
+    // rounded up to whole numbers: the exponentials see differences whose error
+    // goes by their own size, and a change of reference scales by a power of two.
     const float c_hi = a.scale * kLog2e;
     const float c_lo = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634 - c_hi);
     float lo[kTile];
@@ -954,26 +954,43 @@ struct SimtBody {
       for (int r = 0; r < kTile; ++r)
         if (rt * kTile + r < even && MSA_IN_RANGE(key, 1, slots, a.status)) to[r] = s[r] + lo[r];
     }
-    float pw[kTile];
+    // (R, S) as in the other body, R a whole number; a weight may exceed 1 by
+    // 2^20 before it moves.
+    bool rise = false, apart = false;
 #pragma unroll
     for (int r = 0; r < kTile; ++r) {
-      const float mn = fmaxf(m[r], ceilf(s[r])), mu = finite_or_0(mn);
-      l[r] = l[r] * exp2f(m[r] - mu) + exp2f((s[r] - mu) + lo[r]);
-      m[r] = mn;
-      float mx = s[r];
+      const float up = s[r] - R[r], v = x.lvs - S[r];
+      rise |= up + v > 20.f || up > 60.f;
+    }
+    if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
-      for (int x2 = 16; x2 > 0; x2 >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x2));
-      const float top = ceilf(mx), up = (top - R[r]) + (x.lvs - S[r]);
-      if (up > 0.f) {
-        const float down = exp2f(-up);
+      for (int r = 0; r < kTile; ++r) {
+        float top = s[r];
 #pragma unroll
-        for (int k = 0; k < kDl; ++k) (r & 1 ? o[r / 2][k].y : o[r / 2][k].x) *= down;
-        R[r] = top;
-        S[r] = x.lvs;
+        for (int x2 = 16; x2 > 0; x2 >>= 1)
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x2));
+        top = ceilf(top);
+        const float up = (top - R[r]) + (x.lvs - S[r]);
+        if (up > 0.f || top - R[r] > 60.f) {
+          const float down = exp2f(fminf(-up, 100.f));
+          l[r] *= exp2f(R[r] - top);
+#pragma unroll
+          for (int k = 0; k < kDl; ++k) (r & 1 ? o[r / 2][k].y : o[r / 2][k].x) *= down;
+          R[r] = top;
+          S[r] = x.lvs;
+        }
       }
-      pw[r] = s[r] == -INFINITY
-                  ? 0.f
-                  : exp2f(((s[r] - finite_or_0(R[r])) + lo[r]) + (x.lvs - S[r]));
+    }
+    float pw[kTile];
+#pragma unroll
+    for (int r = 0; r < kTile; ++r) apart |= fabsf(x.lvs - S[r]) > 60.f;
+#pragma unroll
+    for (int r = 0; r < kTile; ++r) {
+      const float y = (s[r] - finite_or_0(R[r])) + lo[r], e = exp2f(y);
+      l[r] += e;
+      // Value scales 2^60 apart: the two exponents go together.
+      const float w = apart ? exp2f(y + (x.lvs - S[r])) : e * exp2f(x.lvs - S[r]);
+      pw[r] = s[r] == -INFINITY ? 0.f : w;
     }
     __syncwarp();
     *reinterpret_cast<float4*>(psm + lane * kTile) = make_float4(pw[0], pw[1], pw[2], pw[3]);
@@ -1013,14 +1030,11 @@ struct SimtBody {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int r = 0; r < kTile; ++r) {
-      float mx = m[r];
-#pragma unroll
-      for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-      float sum = l[r] * ex2(m[r] - finite_or_0(mx));
+      float sum = l[r];
 #pragma unroll
       for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
       // (a weight of 1 is 2^0 here, 2^kPBits in the other body)
-      if (lane == 0) stat[warp * kTile + r] = Stat{mx, sum, R[r], S[r] + kPBits};
+      if (lane == 0) stat[warp * kTile + r] = Stat{R[r], sum, R[r], S[r] + kPBits};
 #pragma unroll
       for (int k = 0; k < kDl; ++k) 
         osum[sum_at<D>(warp * kTile + r, lane * kDl + k)] = r & 1 ? o[r / 2][k].y : o[r / 2][k].x;

@@ -244,11 +244,17 @@ __global__ void __launch_bounds__(kEvictThreads) cache_evict_kernel(const EvictA
 }  // namespace
 
 cudaError_t launch_cache_evict_select(const EvictArgs& a, cudaStream_t st) {
-  // 8192 slots a CTA up to a cluster of 8, then up to kKeysMax a CTA; longer
-  // rows are read again for each digit.
+  // 8192 slots a CTA up to a cluster of 8 while every CTA has an SM, else 32768
+  // a CTA: a cluster's barriers cost more than the counting that it shares (256
+  // lists of 60000 slots: 158 us with clusters of 8, 65 with 2; 128 of 12000:
+  // 13.9 with 2, 11.1 without; but 16 of 30000: 13.2 with 4, 14.7 with 2).
+  // Then up to kKeysMax a CTA; longer rows are read again for each digit.
   const int64_t slots = static_cast<int64_t>(a.s.max_blocks) * a.c.block;
+  const int64_t lists = static_cast<int64_t>(a.s.batch) * a.c.Hkv;
   int ranks = 1;
-  while (ranks < kClusterMax && slots > ranks * 8192) ranks *= 2;
+  while (ranks < kClusterMax && slots > ranks * 8192 &&
+         (lists * ranks * 2 <= kSms || slots > ranks * 32768))
+    ranks *= 2;
   const int64_t each = (slots / ranks + 1) + 32 * kEvictWarps;
   const bool staged = each <= kKeysMax;
   const auto kernel = staged ? cache_evict_kernel<true> : cache_evict_kernel<false>;

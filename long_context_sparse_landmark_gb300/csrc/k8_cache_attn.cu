@@ -29,13 +29,17 @@
 // widened in shared memory first and 64 or 128 rows to fill its M; one token
 // needs 32 operations a byte, far below what either unit does.
 //   Up to 8, 16 or 32 rows share a read.  At 32 (four tokens of eight heads)
-// the loop's some 950 instructions a chunk on 8 warps an SM bound it: 16
-// sequences of 32K take 140 us with one token (6.05 TB/s), 150 with two, 218
-// with four (362 as two passes of 16 rows).  Short calls are bound by latency:
+// the latencies of the loop's some 950 instructions a chunk on 8 warps an SM
+// bound it (tensor pipe 20 % busy, issue slots 29 %): 16 sequences of 32K take
+// 139 us with one token (6.07 TB/s), 146 with two, 211 with four (362 as two
+// passes of 16 rows, when four took 218).  Short calls are bound by latency:
 // 32K tokens of one KV head take 11.7 us with the join, of which 6.6 are here;
 // a part's first pass through the code, cold in the instruction cache, costs
 // more than its chunks.
-// fp32 rows run on the CUDA cores with fp32 arithmetic throughout.
+// fp32 rows run on the CUDA cores with fp32 arithmetic throughout: packed
+// multiply-adds, 8 rows a read.  8 sequences of 32K, 64 heads on 8 of 128, take
+// 251 us, 34 TFLOP/s of the 80 that the fp32 lanes have; the shared-memory reads
+// of q and the weights and the registers (12 warps an SM) bound it.
 #include <math.h>
 
 #include "cache_common.cuh"

@@ -176,8 +176,8 @@ struct CacheAttnArgs {
   float* weights;  // [batch, Hkv, weights_ld], null: none
   int64_t weights_ld;
   // workspace
-  float* o_part;    // [2 * n_ctas][tile rows][d]
-  float2* part_stat;  // [2 * n_ctas][tile rows]: a score m (log2 units), sum of 2^(s - m)
+  float* o_part;    // [2 * n_ctas][tile rows][d], in units of 2^(r + u)
+  float4* part_stat;  // [2 * n_ctas][tile rows]: a score m (log2 units), sum of 2^(s - m), r, u
   float* scores;    // [batch, Hkv, max_blocks * block, rows padded to even] (log2 units)
   float2* row_stat;  // [batch, Hkv, rows padded to even]: m, 1 / sum of 2^(s - m)
   int n_ctas;

@@ -365,6 +365,9 @@ __device__ __forceinline__ int sum_at(int row, int dim) {
 
 // Joins the warps' sums of a unit's range and writes them: a thread a row for
 // the statistics, which become each warp's factor, then all of them the dims.
+// Of a range that is not whole the sums stay in units of their own: over its
+// denominator, a range of little weight and great values would be lost when the
+// ranges' weights are compared.
 template <int D, int kTile>
 __device__ __forceinline__ void join_warps(const CacheAttnArgs& a, const Plan& p, const Entry& e,
                                            int c, int rt, const float* osum, Stat* stat,
@@ -388,8 +391,9 @@ __device__ __forceinline__ void join_warps(const CacheAttnArgs& a, const Plan& p
 #pragma unroll
     for (int w = 0; w < kWarps; ++w)
       if (!(s[w].m == -INFINITY && s[w].l == 0.f)) l += s[w].l * ex2(s[w].m - mx);
+    const float unit = S - kPBits;
     // l == 0: no slot attended.
-    const float f = l == 0.f ? 0.f : ex2((R - mx) + (S - kPBits)) / l;
+    const float f = !whole ? 1.f : l == 0.f ? 0.f : ex2((R - mx) + unit) / l;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w)
       stat[w * kTile + r].l = s[w].m == -INFINITY && s[w].l == 0.f
@@ -398,7 +402,9 @@ __device__ __forceinline__ void join_warps(const CacheAttnArgs& a, const Plan& p
     if (whole)
       store_lse(a, p, e, c, rt * kTile + r, mx, l);
     else
-      a.part_stat[slot * kTile + r] = make_float2(l == 0.f ? -INFINITY : mx, l);
+      // (a part that attends nothing: references below any other's)
+      a.part_stat[slot * kTile + r] =
+          l == 0.f ? make_float4(-INFINITY, 0.f, -1e38f, 0.f) : make_float4(mx, l, R, unit);
   }
   __syncthreads();
 #pragma unroll 2
@@ -1209,7 +1215,7 @@ __global__ void __launch_bounds__(kWpr == 1 ? kThreads : 32 * kWpr)
   constexpr int kWarpsJ = kWpr == 1 ? kWarps : kWpr, kRows = kWarpsJ / kWpr;
   __shared__ uint32_t scan[kWarpsJ];
   __shared__ uint32_t found[kRows];
-  __shared__ float red[kWarpsJ], lsum[kWarpsJ];
+  __shared__ float4 red[kWarpsJ];
   __shared__ __align__(16) float osum[kWarpsJ][kWpr == 1 ? 1 : D];
   const Plan p = plan_of(a, kTile);
   const int rows = a.c.Hkv * p.rows;  // of an entry, all KV heads
@@ -1238,57 +1244,102 @@ __global__ void __launch_bounds__(kWpr == 1 ? kThreads : 32 * kWpr)
   const int c0 = cta_of(cut, u0), c1 = cta_of(cut, u0 + e.n_chunks - 1);
   if (c0 == c1) return;  // written whole
   const auto at = [&](int x) { return (2 * static_cast<int64_t>(x) + (x == c0)) * kTile + r; };
-  // A warp's parts, in units of 2^mx: everything is loaded at once, and the
-  // sums are scaled where the maximum rises.
-  float mx = -INFINITY, v[kDl], l = 0.f;
+  // A warp's parts, kAhead of them loaded at once: the denominators in units of
+  // 2^mx, the sums in units of 2^(ref + unit).
+  constexpr int kAhead = kWpr == 1 ? 4 : 8;
+  float mx = -INFINITY, l = 0.f, ref = -INFINITY, unit = 0.f, v[kDl];
 #pragma unroll
   for (int k = 0; k < kDl; ++k) v[k] = 0.f;
-#pragma unroll 8
-  for (int x = c0 + part; x <= c1; x += kWpr) {
-    const int64_t s = at(x);
-    const float2 of = a.part_stat[s];
-    const float* src = a.o_part + s * D + lane * kDl;
-    float y[kDl];
-    if constexpr (kDl == 4) {
-      const float4 z = *reinterpret_cast<const float4*>(src);
-      y[0] = z.x, y[1] = z.y, y[2] = z.z, y[3] = z.w;
-    } else {
-      const float2 z = *reinterpret_cast<const float2*>(src);
-      y[0] = z.x, y[1] = z.y;
-    }
-    const float mn = fmaxf(mx, of.x), mu = finite_or_0(mn);
-    const float down = ex2(mx - mu), f = of.y * ex2(of.x - mu);
-    l = l * down + f;
+#pragma unroll 1
+  for (int x0 = c0 + part; x0 <= c1; x0 += kAhead * kWpr) {
+    float4 of[kAhead], best[kAhead];
+    float y[kAhead][kDl];
 #pragma unroll
-    for (int k = 0; k < kDl; ++k) v[k] = v[k] * down + (f == 0.f ? 0.f : y[k] * f);
+    for (int j = 0; j < kAhead; ++j) {
+      const int x = x0 + j * kWpr;
+      of[j] = make_float4(-INFINITY, 0.f, -1e38f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kDl; ++k) y[j][k] = 0.f;
+      if (x <= c1) {
+        const int64_t s = at(x);
+        of[j] = a.part_stat[s];
+        const float* src = a.o_part + s * D + lane * kDl;
+        if constexpr (kDl == 4) {
+          const float4 z = *reinterpret_cast<const float4*>(src);
+          y[j][0] = z.x, y[j][1] = z.y, y[j][2] = z.z, y[j][3] = z.w;
+        } else {
+          const float2 z = *reinterpret_cast<const float2*>(src);
+          y[j][0] = z.x, y[j][1] = z.y;
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) best[j] = of[j];
+#pragma unroll
+    for (int n = 1; n < kAhead; n *= 2)
+#pragma unroll
+      for (int j = 0; j < kAhead; j += 2 * n) {
+        best[j].x = fmaxf(best[j].x, best[j + n].x);
+        if ((best[j + n].z - best[j].z) + (best[j + n].w - best[j].w) > 0.f) {
+          best[j].z = best[j + n].z;
+          best[j].w = best[j + n].w;
+        }
+      }
+    const float mn = fmaxf(mx, best[0].x), mu = finite_or_0(mn);
+    l *= ex2(mx - mu);
     mx = mn;
+    const float up = (best[0].z - ref) + (best[0].w - unit);
+    if (up > 0.f) {
+      const float down = ex2(-up);
+#pragma unroll
+      for (int k = 0; k < kDl; ++k) v[k] *= down;
+      ref = best[0].z;
+      unit = best[0].w;
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      l += of[j].y * ex2(of[j].x - mu);
+      const float f = ex2((of[j].z - ref) + (of[j].w - unit));
+#pragma unroll
+      for (int k = 0; k < kDl; ++k) v[k] += y[j][k] * f;
+    }
   }
   if (kWpr > 1) {
 #pragma unroll
     for (int k = 0; k < kDl; ++k) osum[warp][lane * kDl + k] = v[k];
-    if (lane == 0) {
-      red[warp] = mx;
-      lsum[warp] = l;
-    }
+    if (lane == 0) red[warp] = make_float4(mx, l, ref, unit);
     __syncthreads();
     if (warp > 0) return;
-    mx = lane < kWpr ? red[lane] : -INFINITY;
+    const float4 own = red[lane < kWpr ? lane : 0];
+    mx = own.x;
+    ref = own.z;
+    unit = own.w;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    for (int o = 16; o > 0; o >>= 1) {
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const float ref2 = __shfl_xor_sync(0xffffffffu, ref, o);
+      const float unit2 = __shfl_xor_sync(0xffffffffu, unit, o);
+      if ((ref2 - ref) + (unit2 - unit) > 0.f) {
+        ref = ref2;
+        unit = unit2;
+      }
+    }
     const float mu = finite_or_0(mx);
     l = 0.f;
 #pragma unroll
     for (int k = 0; k < kDl; ++k) v[k] = 0.f;
 #pragma unroll
     for (int w = 0; w < kWpr; ++w) {
-      const float f = ex2(red[w] - mu);
-      l += lsum[w] * f;
+      const float4 of = red[w];
+      l += of.y * ex2(of.x - mu);
+      // No part (a warp without any): no reference.
+      const float f = of.z == -INFINITY ? 0.f : ex2((of.z - ref) + (of.w - unit));
 #pragma unroll
       for (int k = 0; k < kDl; ++k) v[k] += osum[w][lane * kDl + k] * f;
     }
   }
   mx = finite_or_0(mx);
-  const float f = l == 0.f ? 0.f : 1.f / l;
+  const float f = l == 0.f ? 0.f : ex2((ref - mx) + unit) / l;
   store_dims<kDl>(a, e, c, m, lane * kDl, v, f);
   if (lane == 0) store_lse(a, p, e, c, m, mx, l);
 }

@@ -151,7 +151,7 @@ AttnPlan attn_plan(int Hkv, int d, int block, int batch, int n_q, int Hq, int ma
   p.o = at;
   at += up(static_cast<size_t>(2) * p.n_ctas * tile * d * sizeof(float));
   p.part_stat = at;
-  at += up(static_cast<size_t>(2) * p.n_ctas * tile * sizeof(float2));
+  at += up(static_cast<size_t>(2) * p.n_ctas * tile * sizeof(float4));
   if (weights) {
     const size_t even = (static_cast<size_t>(rows) + 1) & ~static_cast<size_t>(1);
     p.scores = at;
@@ -201,7 +201,7 @@ msa_status run_attn(const msa_kv_cache* c, const void* q, const int32_t* table, 
   a.weights = weights;
   a.weights_ld = weights_ld;
   a.o_part = reinterpret_cast<float*>(ws + p.o);
-  a.part_stat = reinterpret_cast<float2*>(ws + p.part_stat);
+  a.part_stat = reinterpret_cast<float4*>(ws + p.part_stat);
   a.scores = reinterpret_cast<float*>(ws + p.scores);
   a.row_stat = reinterpret_cast<float2*>(ws + p.row_stat);
   a.n_ctas = p.n_ctas;

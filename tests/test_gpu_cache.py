@@ -839,3 +839,79 @@ def test_python_refusals():
     refused(ValueError, msa.KVCache, cache.k_codes, cache.v_codes[:1], cache.k_scale, cache.v_scale, cache.k_mean)
     refused(msa.binding.MsaError, msa.cache_attention, torch.zeros((1, 1, 4, 32), device=DEV),
             msa.KVCache.empty(2, 2, 32, 32), tt, tl)
+
+
+# -- values and scores of any size -------------------------------------------
+
+def check_in_fp32(cache, t, lens, q, dtype, scale=1.0):
+    """Attention with an fp32 output against the reference, relative to each
+    row's own weighted values: halves' subnormals are 2^-39 of the row's largest
+    weighted block (values of one size in a block: twice a slot's at most)."""
+    q = q.to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    ref = R.attention(pool_of(cache), q.double().cpu().numpy(), t, lens, 1 << 30, scale)
+    out, lse = msa.cache_attention(q, cache, i32(t), i32(lens), scale=scale, out_dtype=torch.float32)
+    tol_o, tol_l = bounds(ref, q.shape[3], dtype == "bf16", torch.float32)
+    tol_o = tol_o + 2.0 ** -149
+    if dtype == "bf16":
+        tol_o += ref[4][..., None] * 2.0 ** -38 * ref[2]
+    o, l = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    assert np.isfinite(o).all() and np.isfinite(l).all()
+    err = np.abs(o - ref[0])
+    assert (err <= tol_o).all(), f"out: worst {np.max(err / tol_o):.3g} of the bound"
+    err = np.abs(l - ref[1])
+    assert (err <= tol_l).all(), f"lse: worst {np.max(err / tol_l):.3g} of the bound"
+
+
+def long_sequence(n, k, v, d=128, block=64, seed=91):
+    """One sequence of one KV head: keys and values [n, d]."""
+    rng = np.random.default_rng(seed)
+    nb = -(-n // block)
+    cache, t = new_cache(nb, 1, d, block), rng.permutation(nb).astype(np.int32)[None]
+    kt, vt = (torch.as_tensor(x[:, None], device=DEV).float() for x in (k, v))
+    msa.cache_append(cache, kt, vt, i32([0, n]), i32(t), i32([n]), n)
+    return cache, t, [n]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [500, 9000])
+def test_values_near_the_end_of_the_range(n, dtype):
+    """A sequence that several CTAs share: their parts are joined without
+    multiplying values by anything above 1."""
+    rng = np.random.default_rng(92)
+    cache, t, lens = long_sequence(n, rng.normal(size=(n, 128)), rng.uniform(1, 2, size=(n, 128)) * 1e36)
+    check_in_fp32(cache, t, lens, torch.randn((1, 1, 8, 128), device=DEV), dtype, 1 / math.sqrt(128))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("first", [True, False])
+def test_parts_of_little_weight_and_great_values(first, dtype):
+    """Half of a sequence leads by 2^130 in weight and trails by 2^200 in
+    value: the other half's parts make the output."""
+    rng = np.random.default_rng(93)
+    n, d = 8192, 128
+    lead = (np.arange(n) < n // 2) == first
+    k = rng.normal(size=(n, d)) * 0.25
+    k[:, 0] = np.where(lead, 90.0, 0.0)
+    v = rng.uniform(1, 2, size=(n, d)) * np.where(lead, 1e-30, 1e30)[:, None]
+    q = torch.randn((1, 1, 8, d), device=DEV) * 0.05
+    q[..., 0] = 1.0
+    check_in_fp32(*long_sequence(n, k, v), q, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("at", [70, 8100])
+def test_poison_of_no_weight_reaches_its_rows(at, dtype):
+    """A NaN value whose slot's weight is below fp32, in a part before or after
+    those that lead."""
+    rng = np.random.default_rng(94)
+    n, d = 8192, 128
+    k = rng.normal(size=(n, d)) * 0.25
+    k[:, 0] = np.where((np.arange(n) < 4096) == (at < 4096), 0.0, 200.0)
+    v = rng.normal(size=(n, d))
+    v[at, 3] = np.nan
+    cache, t, lens = long_sequence(n, k, v)
+    q = torch.randn((1, 1, 8, d), device=DEV) * 0.05
+    q[..., 0] = 1.0
+    out, _ = msa.cache_attention(q.to(torch.bfloat16 if dtype == "bf16" else torch.float32), cache, i32(t), i32(lens),
+                                 scale=1.0)
+    assert torch.isnan(out).all()

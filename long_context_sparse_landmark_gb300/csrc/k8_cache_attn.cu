@@ -4,10 +4,12 @@
 // Mathematics, per query row (position p, head h of KV group c), over its
 // slots j, in log2 units: s_j = scale log2e <q, code_j> kscale(j), v_j = log2
 // vscale(j); out = sum_j 2^{s_j + v_j} code_j / sum_j 2^{s_j}.  The value scale
-// goes into the exponent of the weights that meet the raw codes: w_j = 2^{s_j -
-// R + v_j - S}, with (R, S) the s and v of a slot whose s + v is the largest (to
-// 1.5) so far -- a pair, not a sum, so that a large score does not round the
-// value scale away.  All sums are fp32.
+// goes into the exponent of the weights that meet the raw codes: w_j = 2^{(s_j -
+// M) + (v_j - D)}, with M the largest s so far (to 60), the denominator's
+// reference, and M + D the largest s + v (to 1.5), the output's.  Kept as an
+// offset D of M, so that a large score does not round the value scale away; M
+// never falls, so that neither sum leaves fp32 where the largest s and the
+// largest s + v are slots far apart.  All sums are fp32.
 //
 // The work is read once: 2 d bytes a slot and KV head, shared by the group's
 // rows, so HBM bounds it: 64 sequences of 16K to 32K tokens, 64 heads on 8 of
@@ -296,10 +298,10 @@ __device__ __forceinline__ Chunk chunk_of(const Ahead& r, int src) {
 }
 
 // The joined result of a CTA's warps for one unit's range, or a whole unit.
-// Row r: osum[w][r][dim] holds warp w's sum in units of 2^{R + S}, stat[w][r]
-// its maxima and denominator.
+// Row r: osum[w][r][dim] holds warp w's sum in units of 2^{M + D}, stat[w][r]
+// its references and denominator, l in units of 2^M.
 struct Stat {
-  float m, l, R, S;
+  float M, D, l;
 };
 
 // Writes row m's lse and, for the weights pass, its reference and denominator.
@@ -376,35 +378,35 @@ __device__ __forceinline__ void join_warps(const CacheAttnArgs& a, const Plan& p
   if (static_cast<int>(threadIdx.x) < min(kTile, left)) {
     const int r = threadIdx.x;
     Stat s[kWarps];
-    float mx = -INFINITY, l = 0.f, R = -INFINITY, S = 0.f;
+    float mx = -INFINITY, l = 0.f, M = -INFINITY, D0 = 0.f;  // (M, D0): the largest M + D
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       s[w] = stat[w * kTile + r];
-      mx = fmaxf(mx, s[w].m);
-      if ((s[w].R - R) + (s[w].S - S) > 0.f) {
-        R = s[w].R;
-        S = s[w].S;
+      mx = fmaxf(mx, s[w].M);
+      if ((s[w].M - M) + (s[w].D - D0) > 0.f) {
+        M = s[w].M;
+        D0 = s[w].D;
       }
     }
     mx = finite_or_0(mx);
-    R = finite_or_0(R);
+    M = finite_or_0(M);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w)
-      if (!(s[w].m == -INFINITY && s[w].l == 0.f)) l += s[w].l * ex2(s[w].m - mx);
-    const float unit = S - kPBits;
+      if (!(s[w].M == -INFINITY && s[w].l == 0.f)) l += s[w].l * ex2(s[w].M - mx);
+    const float unit = D0 - kPBits;
     // l == 0: no slot attended.
-    const float f = !whole ? 1.f : l == 0.f ? 0.f : ex2((R - mx) + unit) / l;
+    const float f = !whole ? 1.f : l == 0.f ? 0.f : ex2((M - mx) + unit) / l;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w)
-      stat[w * kTile + r].l = s[w].m == -INFINITY && s[w].l == 0.f
+      stat[w * kTile + r].l = s[w].M == -INFINITY && s[w].l == 0.f
                                   ? 0.f
-                                  : ex2((finite_or_0(s[w].R) - R) + (s[w].S - S)) * f;
+                                  : ex2((finite_or_0(s[w].M) - M) + (s[w].D - D0)) * f;
     if (whole)
       store_lse(a, p, e, c, rt * kTile + r, mx, l);
     else
       // (a part that attends nothing: references below any other's)
       a.part_stat[slot * kTile + r] =
-          l == 0.f ? make_float4(-INFINITY, 0.f, -1e38f, 0.f) : make_float4(mx, l, R, unit);
+          l == 0.f ? make_float4(-INFINITY, 0.f, -1e38f, 0.f) : make_float4(mx, l, M, unit);
   }
   __syncthreads();
 #pragma unroll 2
@@ -449,7 +451,7 @@ struct MmaBody {
   uint32_t q[kQShared ? 1 : kKs][kQShared ? 1 : kNt][2];
   float qs[kNt][2];   // score scale of rows 2t, 2t+1 (log2 units)
   float o[kMt][kNt][4];
-  float l[kNt][2], R[kNt][2], S[kNt][2];  // l in units of 2^R
+  float l[kNt][2], M[kNt][2], D0[kNt][2];  // l in units of 2^M, o of 2^{M + D0 - kPBits}
 
   // Rows of a unit, in shared memory for all its warps: their fragments
   // [k-step][tile][lane], score scales and positions.
@@ -520,8 +522,8 @@ struct MmaBody {
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         qs[n][r] = rows->scale[8 * n + 2 * t4 + r];
-        R[n][r] = -INFINITY;
-        l[n][r] = S[n][r] = 0.f;
+        M[n][r] = -INFINITY;
+        l[n][r] = D0[n][r] = 0.f;
       }
     }
 #pragma unroll
@@ -642,10 +644,10 @@ struct MmaBody {
   __device__ __forceinline__ void softmax(const CacheAttnArgs& a, const Plan& p, const Entry& e,
                                           int c, int rt, const Chunk& x) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
-    // (R, S) is not kept up to the last bit: a weight may exceed 2^14 by a
-    // factor 2^1.5 (the half's range allows it) and a term of the denominator
-    // 1 by 2^60, so that most chunks move neither it nor the sums, and the
-    // lanes need not agree on a maximum.
+    // The references are not kept up to the last bit: a weight may exceed 2^14
+    // by a factor 2^1.5 (the half's range allows it) and a term of the
+    // denominator 1 by 2^60, so that most chunks move neither them nor the sums,
+    // and the lanes need not agree on a maximum.
     float mx[kNt][2];
     bool rise = false;
 #pragma unroll
@@ -676,8 +678,8 @@ struct MmaBody {
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         mx[n][r] = fmaxf(fmaxf(s[0][n][r], s[0][n][2 + r]), fmaxf(s[1][n][r], s[1][n][2 + r]));
-        const float up = mx[n][r] - R[n][r];
-        rise |= up + (x.lvs - S[n][r]) > 1.5f || up > 60.f;
+        const float up = mx[n][r] - M[n][r];
+        rise |= up + (x.lvs - D0[n][r]) > 1.5f || up > 60.f;
       }
       if constexpr (kWeights) {
         // For the weights pass: [slot][row], rows padded to even.
@@ -706,25 +708,27 @@ struct MmaBody {
 #pragma unroll
           for (int o2 = 4; o2 < 32; o2 <<= 1)
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o2));
-          const float up = (top - R[n][r]) + (x.lvs - S[n][r]);
-          if (up > 0.f || top - R[n][r] > 60.f) {
-            const float down = ex2(fminf(-up, 100.f));
-            l[n][r] *= ex2(R[n][r] - top);
+          const float up = top - M[n][r];
+          if (up + (x.lvs - D0[n][r]) > 0.f || up > 60.f) {
+            const float to = fmaxf(M[n][r], top), kept = D0[n][r] - (to - M[n][r]);
+            const float off = fmaxf(kept, x.lvs + (top - to));  // kept: the output's unit stays
+            const float down = ex2(kept - off);
+            l[n][r] *= ex2(M[n][r] - to);
 #pragma unroll
             for (int i = 0; i < kMt; ++i) {
               o[i][n][r] *= down;
               o[i][n][2 + r] *= down;
             }
-            R[n][r] = top;
-            S[n][r] = x.lvs;
+            M[n][r] = to;
+            D0[n][r] = off;
           }
         }
     }
 #pragma unroll
     for (int n = 0; n < kNt; ++n) {
       float pv[2][4];
-      const float2 minus_R = make_float2(-finite_or_0(R[n][0]), -finite_or_0(R[n][1]));
-      const float2 v = make_float2(x.lvs - S[n][0], x.lvs - S[n][1]);
+      const float2 minus_M = make_float2(-finite_or_0(M[n][0]), -finite_or_0(M[n][1]));
+      const float2 v = make_float2(x.lvs - D0[n][0], x.lvs - D0[n][1]);
       const float2 base = make_float2(kPBits + v.x, kPBits + v.y);
       float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
@@ -732,7 +736,7 @@ struct MmaBody {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const float2 y = make_float2(s[st][n][2 * k], s[st][n][2 * k + 1]);
-          const float2 z = __fadd2_rn(__fadd2_rn(y, minus_R), base);
+          const float2 z = __fadd2_rn(__fadd2_rn(y, minus_M), base);
           float2 w = make_float2(ex2(z.x), ex2(z.y));
           if (kEdge) {  // whatever the block's scales are
             if (y.x == -INFINITY) w.x = 0.f;
@@ -744,18 +748,18 @@ struct MmaBody {
         }
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const float mR = r ? minus_R.y : minus_R.x, sr = r ? sum.y : sum.x;
+        const float mM = r ? minus_M.y : minus_M.x, sr = r ? sum.y : sum.x;
         // The denominator: the weights with the value scale taken out again, ...
         float part = sr * ex2(-(r ? base.y : base.x));
         if (kEdge && sr == 0.f) part = 0.f;
         // ... unless they are too small to tell it: values 2^60 below other
         // blocks'.
-        if ((mx[n][r] + mR) + (r ? v.y : v.x) < -60.f) {
+        if ((mx[n][r] + mM) + (r ? v.y : v.x) < -60.f) {
           part = 0.f;
 #pragma unroll
           for (int st = 0; st < 2; ++st)
 #pragma unroll
-            for (int k = 0; k < 2; ++k) part += ex2(s[st][n][2 * k + r] + mR);
+            for (int k = 0; k < 2; ++k) part += ex2(s[st][n][2 * k + r] + mM);
         }
         l[n][r] += part;
       }
@@ -826,7 +830,7 @@ struct MmaBody {
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
         const int row = warp * kTile + 8 * n + 2 * t4 + r;
-        if (g == 0) stat[row] = Stat{R[n][r], sum, R[n][r], S[n][r]};
+        if (g == 0) stat[row] = Stat{M[n][r], D0[n][r], sum};
 #pragma unroll
         for (int half = 0; half < 2; ++half)
 #pragma unroll
@@ -851,7 +855,7 @@ struct SimtBody {
   static constexpr int kSmem = kSums + (kTile * D + kTile + kWarps * kChunk * kTile) * 4;
 
   float2 o[kTile / 2][kDl];  // rows 2i, 2i + 1
-  float l[kTile], R[kTile], S[kTile];  // l: the lane's slots, in units of 2^R
+  float l[kTile], M[kTile], D0[kTile];  // l: the lane's slots, in units of 2^M; o: of 2^{M + D0}
   float* qsm;
   float* psm;
 
@@ -883,8 +887,8 @@ struct SimtBody {
     psm = qsm + kTile * D + kTile + (threadIdx.x >> 5) * kChunk * kTile;
 #pragma unroll
     for (int r = 0; r < kTile; ++r) {
-      R[r] = -INFINITY;
-      l[r] = S[r] = 0.f;
+      M[r] = -INFINITY;
+      l[r] = D0[r] = 0.f;
     }
 #pragma unroll
     for (int r = 0; r < kTile / 2; ++r)
@@ -964,12 +968,12 @@ struct SimtBody {
       for (int r = 0; r < kTile; ++r)
         if (rt * kTile + r < even && MSA_IN_RANGE(key, 1, slots, a.status)) to[r] = s[r] + lo[r];
     }
-    // (R, S) as in the other body, R a whole number; a weight may exceed 1 by
-    // 2^20 before it moves.
+    // References as in the other body, but whole numbers, so that a move of
+    // either is exact; a weight may exceed 1 by 2^20 before they do.
     bool rise = false, apart = false;
 #pragma unroll
     for (int r = 0; r < kTile; ++r) {
-      const float up = s[r] - R[r], v = x.lvs - S[r];
+      const float up = s[r] - M[r], v = x.lvs - D0[r];
       rise |= up + v > 20.f || up > 60.f;
     }
     if (__any_sync(0xffffffffu, rise)) {
@@ -980,26 +984,28 @@ struct SimtBody {
         for (int x2 = 16; x2 > 0; x2 >>= 1)
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x2));
         top = ceilf(top);
-        const float up = (top - R[r]) + (x.lvs - S[r]);
-        if (up > 0.f || top - R[r] > 60.f) {
-          const float down = exp2f(fminf(-up, 100.f));
-          l[r] *= exp2f(R[r] - top);
+        const float up = top - M[r];
+        if (up + (x.lvs - D0[r]) > 0.f || up > 60.f) {
+          const float to = fmaxf(M[r], top), kept = D0[r] - (to - M[r]);
+          const float off = ceilf(fmaxf(kept, x.lvs + (top - to)));
+          const float down = exp2f(kept - off);
+          l[r] *= exp2f(M[r] - to);
 #pragma unroll
           for (int k = 0; k < kDl; ++k) (r & 1 ? o[r / 2][k].y : o[r / 2][k].x) *= down;
-          R[r] = top;
-          S[r] = x.lvs;
+          M[r] = to;
+          D0[r] = off;
         }
       }
     }
     float pw[kTile];
 #pragma unroll
-    for (int r = 0; r < kTile; ++r) apart |= fabsf(x.lvs - S[r]) > 60.f;
+    for (int r = 0; r < kTile; ++r) apart |= fabsf(x.lvs - D0[r]) > 60.f;
 #pragma unroll
     for (int r = 0; r < kTile; ++r) {
-      const float y = (s[r] - finite_or_0(R[r])) + lo[r], e = exp2f(y);
+      const float y = (s[r] - finite_or_0(M[r])) + lo[r], e = exp2f(y);
       l[r] += e;
       // Value scales 2^60 apart: the two exponents go together.
-      const float w = apart ? exp2f(y + (x.lvs - S[r])) : e * exp2f(x.lvs - S[r]);
+      const float w = apart ? exp2f(y + (x.lvs - D0[r])) : e * exp2f(x.lvs - D0[r]);
       pw[r] = s[r] == -INFINITY ? 0.f : w;
     }
     __syncwarp();
@@ -1044,7 +1050,7 @@ struct SimtBody {
 #pragma unroll
       for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
       // (a weight of 1 is 2^0 here, 2^kPBits in the other body)
-      if (lane == 0) stat[warp * kTile + r] = Stat{R[r], sum, R[r], S[r] + kPBits};
+      if (lane == 0) stat[warp * kTile + r] = Stat{M[r], D0[r] + kPBits, sum};
 #pragma unroll
       for (int k = 0; k < kDl; ++k) 
         osum[sum_at<D>(warp * kTile + r, lane * kDl + k)] = r & 1 ? o[r / 2][k].y : o[r / 2][k].x;

@@ -915,3 +915,34 @@ def test_poison_of_no_weight_reaches_its_rows(at, dtype):
     out, _ = msa.cache_attention(q.to(torch.bfloat16 if dtype == "bf16" else torch.float32), cache, i32(t), i32(lens),
                                  scale=1.0)
     assert torch.isnan(out).all()
+
+
+def layered(first, second, seed=90):
+    """8 sequences of 64 blocks of 32 slots, 4 KV heads of 64, whose kind
+    changes every four blocks, so that each warp meets both kinds in turn:
+    first, second = (score, size of the values); odd heads begin with the
+    second.  Queries for a scale of 1."""
+    B, H, d, blocks = 8, 4, 64, 64
+    n = 32 * blocks
+    rng = np.random.default_rng(seed)
+    kind = (np.arange(n)[:, None] // 128 + np.arange(H)[None]) % 2
+    k = rng.normal(size=(B, n, H, d)) * 0.25
+    k[..., 0] = np.where(kind == 0, first[0], second[0])[None]
+    v = rng.uniform(1, 2, size=(B, n, H, d)) * rng.choice([-1.0, 1.0], size=(B, n, H, 1))
+    v *= np.where(kind == 0, first[1], second[1])[None, :, :, None]
+    cache = new_cache(B * blocks, H, d, 32)
+    t = rng.permutation(B * blocks).astype(np.int32).reshape(B, blocks)
+    kt, vt = (torch.as_tensor(x.reshape(B * n, H, d), device=DEV).float() for x in (k, v))
+    msa.cache_append(cache, kt, vt, i32(np.arange(B + 1) * n), i32(t), i32([n] * B), n)
+    q = torch.randn((B, 1, 2 * H, d), device=DEV, generator=torch.Generator(device=DEV).manual_seed(seed)) * 0.05
+    q[..., 0] = 1.0
+    return cache, t, [n] * B, q
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lead", [30.0, 44.0, 104.0, 288.0])
+@pytest.mark.parametrize("big,small", [(1e30, 1e-30), (1e30, 1e10), (1e4, 1e-30)])
+def test_a_leading_score_over_far_smaller_values(big, small, lead, dtype):
+    """Blocks that lead by e^lead in weight and trail by up to 2^200 in value:
+    the largest score and the largest weighted value are slots of their own."""
+    check_in_fp32(*layered((0.0, big), (lead, small)), dtype)

@@ -221,6 +221,15 @@ __device__ __forceinline__ float ex2(float x) {
 }
 __device__ __forceinline__ float finite_or_0(float m) { return m == -INFINITY ? 0.f : m; }
 
+// 2^x as a product, applied one after the other: for x down to -226, where a
+// result in fp32's range is left of a sum times 2^x although 2^x is not.
+struct Pow2 {
+  float f, post;
+};
+__device__ __forceinline__ Pow2 pow2_of(float x) {
+  return {ex2(fmaxf(x, -100.f)), ex2(fminf(x + 100.f, 0.f))};
+}
+
 // Row m of an entry: its query token and head.
 __device__ __forceinline__ void row_of(const CacheAttnArgs& a, const Entry& e, int c, int m,
                                        int* t, int* h) {
@@ -394,13 +403,15 @@ __device__ __forceinline__ void join_warps(const CacheAttnArgs& a, const Plan& p
     for (int w = 0; w < kWarps; ++w)
       if (!(s[w].M == -INFINITY && s[w].l == 0.f)) l += s[w].l * ex2(s[w].M - mx);
     const float unit = D0 - kPBits;
+    const Pow2 to = pow2_of((M - mx) + unit);
     // l == 0: no slot attended.
-    const float f = !whole ? 1.f : l == 0.f ? 0.f : ex2((M - mx) + unit) / l;
+    const float f = !whole ? 1.f : l == 0.f ? 0.f : to.f / l;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w)
       stat[w * kTile + r].l = s[w].M == -INFINITY && s[w].l == 0.f
                                   ? 0.f
                                   : ex2((finite_or_0(s[w].M) - M) + (s[w].D - D0)) * f;
+    stat[r].M = whole ? to.post : 1.f;
     if (whole)
       store_lse(a, p, e, c, rt * kTile + r, mx, l);
     else
@@ -423,6 +434,11 @@ __device__ __forceinline__ void join_warps(const CacheAttnArgs& a, const Plan& p
       v.z += x.z * f;
       v.w += x.w * f;
     }
+    const float post = stat[r].M;
+    v.x *= post;
+    v.y *= post;
+    v.z *= post;
+    v.w *= post;
     if (whole)
       store_out(a, e, c, rt * kTile + r, dim, v);
     else
@@ -1345,8 +1361,11 @@ __global__ void __launch_bounds__(kWpr == 1 ? kThreads : 32 * kWpr)
     }
   }
   mx = finite_or_0(mx);
-  const float f = l == 0.f ? 0.f : ex2((ref - mx) + unit) / l;
-  store_dims<kDl>(a, e, c, m, lane * kDl, v, f);
+  const Pow2 to = pow2_of((ref - mx) + unit);
+  const float f = l == 0.f ? 0.f : to.f / l;
+#pragma unroll
+  for (int k = 0; k < kDl; ++k) v[k] *= f;
+  store_dims<kDl>(a, e, c, m, lane * kDl, v, to.post);
   if (lane == 0) store_lse(a, p, e, c, m, mx, l);
 }
 

@@ -946,3 +946,13 @@ def test_a_leading_score_over_far_smaller_values(big, small, lead, dtype):
     """Blocks that lead by e^lead in weight and trail by up to 2^200 in value:
     the largest score and the largest weighted value are slots of their own."""
     check_in_fp32(*layered((0.0, big), (lead, small)), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [500, 9000])
+@pytest.mark.parametrize("size", [1e-32, 1e-35, 1e-37, 1e-43])
+def test_values_at_the_bottom_of_the_range(size, n, dtype):
+    """Down to fp32's subnormals, with scales of 2^-126."""
+    rng = np.random.default_rng(95)
+    cache, t, lens = long_sequence(n, rng.normal(size=(n, 128)), rng.uniform(1, 2, size=(n, 128)) * size)
+    check_in_fp32(cache, t, lens, torch.randn((1, 1, 8, 128), device=DEV), dtype, 1 / math.sqrt(128))

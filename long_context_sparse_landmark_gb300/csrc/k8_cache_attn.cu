@@ -54,6 +54,10 @@ constexpr int kThreads = 32 * kWarps;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kPBits = 14.f;  // log2 of the largest half weight
+// log2 of a value scale of 0 (finite: no difference of two is a NaN).  Such a
+// block counts in the denominator; its values weigh nothing beside any others,
+// and what they leave where there are no others is scaled to 0 in the end.
+constexpr float kLogZero = -0x1p126f;
 
 // ---- the list of chunks ----------------------------------------------------
 
@@ -221,10 +225,11 @@ __device__ __forceinline__ float ex2(float x) {
 }
 __device__ __forceinline__ float finite_or_0(float m) { return m == -INFINITY ? 0.f : m; }
 
-// 2^x as a product, applied one after the other: for x down to -226, where a
-// result in fp32's range is left of a sum times 2^x although 2^x is not.
+// 2^x as a product, applied one after the other (and apart from a denominator
+// of up to 2^91): for x down to -226, where a result in fp32's range is left of
+// a sum times 2^x although 2^x is not.
 struct Pow2 {
-  float f, post;
+  float a, b;
 };
 __device__ __forceinline__ Pow2 pow2_of(float x) {
   return {ex2(fmaxf(x, -100.f)), ex2(fminf(x + 100.f, 0.f))};
@@ -290,7 +295,7 @@ __device__ __forceinline__ Ahead look_ahead(const CacheAttnArgs& a, const Entry&
   r.at = (head << a.c.lb) + (slot & (a.c.block - 1));
   r.ks = a.c.k_scale[head];
   const float vs = a.c.v_scale[head];
-  r.lvs = vs == 0.f ? 0.f : log2f(vs);  // a block of zeros (scale 0) counts as scale 1
+  r.lvs = vs == 0.f ? kLogZero : log2f(vs);
   return r;
 }
 
@@ -405,13 +410,14 @@ __device__ __forceinline__ void join_warps(const CacheAttnArgs& a, const Plan& p
     const float unit = D0 - kPBits;
     const Pow2 to = pow2_of((M - mx) + unit);
     // l == 0: no slot attended.
-    const float f = !whole ? 1.f : l == 0.f ? 0.f : to.f / l;
+    const float f = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w)
       stat[w * kTile + r].l = s[w].M == -INFINITY && s[w].l == 0.f
                                   ? 0.f
                                   : ex2((finite_or_0(s[w].M) - M) + (s[w].D - D0)) * f;
-    stat[r].M = whole ? to.post : 1.f;
+    stat[r].M = whole ? to.a : 1.f;
+    stat[r].D = whole ? to.b : 1.f;
     if (whole)
       store_lse(a, p, e, c, rt * kTile + r, mx, l);
     else
@@ -434,11 +440,11 @@ __device__ __forceinline__ void join_warps(const CacheAttnArgs& a, const Plan& p
       v.z += x.z * f;
       v.w += x.w * f;
     }
-    const float post = stat[r].M;
-    v.x *= post;
-    v.y *= post;
-    v.z *= post;
-    v.w *= post;
+    const Pow2 to{stat[r].M, stat[r].D};
+    v.x = v.x * to.a * to.b;
+    v.y = v.y * to.a * to.b;
+    v.z = v.z * to.a * to.b;
+    v.w = v.w * to.a * to.b;
     if (whole)
       store_out(a, e, c, rt * kTile + r, dim, v);
     else
@@ -1362,10 +1368,10 @@ __global__ void __launch_bounds__(kWpr == 1 ? kThreads : 32 * kWpr)
   }
   mx = finite_or_0(mx);
   const Pow2 to = pow2_of((ref - mx) + unit);
-  const float f = l == 0.f ? 0.f : to.f / l;
+  const float f = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-  for (int k = 0; k < kDl; ++k) v[k] *= f;
-  store_dims<kDl>(a, e, c, m, lane * kDl, v, to.post);
+  for (int k = 0; k < kDl; ++k) v[k] = v[k] * f * to.a;
+  store_dims<kDl>(a, e, c, m, lane * kDl, v, to.b);
   if (lane == 0) store_lse(a, p, e, c, m, mx, l);
 }
 

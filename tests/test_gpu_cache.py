@@ -956,3 +956,23 @@ def test_values_at_the_bottom_of_the_range(size, n, dtype):
     rng = np.random.default_rng(95)
     cache, t, lens = long_sequence(n, rng.normal(size=(n, 128)), rng.uniform(1, 2, size=(n, 128)) * size)
     check_in_fp32(cache, t, lens, torch.randn((1, 1, 8, 128), device=DEV), dtype, 1 / math.sqrt(128))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("value", [1.0, 1e-8, 1e-12, 1e-30])
+@pytest.mark.parametrize("lead", [0.0, 30.0, 208.0])
+def test_blocks_of_zeros_beside_small_values(lead, value, dtype):
+    """They take their share of the weight and none of the other values' bits."""
+    check_in_fp32(*layered((lead, 0.0), (0.0, value)), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lead", [0.0, 30.0])
+def test_a_scale_of_zero_over_any_codes(lead, dtype):
+    """A slot is code * scale: 0 where the scale is, whatever the codes are."""
+    cache, t, lens, q = layered((lead, 1.0), (0.0, 1e-3))
+    cache.v_scale[cache.v_scale > 1e-4] = 0.0
+    check_in_fp32(cache, t, lens, q, dtype)
+    cache.v_scale.zero_()
+    cache.k_scale.zero_()
+    check_in_fp32(cache, t, lens, q, dtype)

@@ -259,9 +259,13 @@ cudaError_t launch_cache_evict_select(const EvictArgs& a, cudaStream_t st) {
   const bool staged = each <= kKeysMax;
   const auto kernel = staged ? cache_evict_kernel<true> : cache_evict_kernel<false>;
   const int smem = staged ? static_cast<int>(each) * 4 : 0;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
+  if (staged) {
+    // The kernel's most, not this call's: the limit is the function's, and
+    // another host thread may launch between this and the launch below.
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeysMax * 4);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -36,6 +36,7 @@ constexpr int kPickWarpsMax = 16;
 constexpr int kBins = 2048;
 constexpr int kListMax = 512;          // near-ties ranked in shared memory
 constexpr int kStagedMax = 40 * 1024;  // keys in shared memory; more are kept in the workspace
+constexpr int kFewMax = 4096;          // blocks of a list that 256 threads take
 
 __device__ __forceinline__ int candidates(const CacheSelectArgs& a, int len, int t) {
   const int p = len - a.T + t;
@@ -513,16 +514,20 @@ cudaError_t launch_scores(const CacheSelectArgs& a, cudaStream_t st) {
 
 template <int D, bool kBf16>
 cudaError_t launch_pick(const CacheSelectArgs& a, cudaStream_t st) {
-  // 256 threads up to 4096 blocks, whose few keys leave most instructions to
+  // 256 threads up to kFewMax blocks, whose few keys leave most instructions to
   // the bins and barriers, 512 above.
-  const bool few = a.s.max_blocks <= 4096, staged = a.s.max_blocks <= kStagedMax;
+  const bool few = a.s.max_blocks <= kFewMax, staged = a.s.max_blocks <= kStagedMax;
   const int smem = staged ? a.s.max_blocks * 4 : 0;
   const auto kernel = few      ? cache_pick_kernel<D, kBf16, true, 256>
                       : staged ? cache_pick_kernel<D, kBf16, true, 512>
                                : cache_pick_kernel<D, kBf16, false, 512>;
-  if (smem > 8 * 1024) {  // with the static part, more than 48 KB needs leave
+  static_assert(sizeof(PickShared) + kFewMax * 4 <= 48 * 1024, "few: no leave needed");
+  if (staged && !few) {
+    // More than 48 KB needs leave: for the kernel's most, not this call's, since
+    // the limit is the function's and another host thread may launch between
+    // this and the launch below.
     const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStagedMax * 4);
     if (e != cudaSuccess) return e;
   }
   const dim3 units(static_cast<unsigned>(a.s.batch) * a.T * a.c.Hkv);

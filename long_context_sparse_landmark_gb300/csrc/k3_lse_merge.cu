@@ -127,8 +127,10 @@ cudaError_t launch_lse_merge(const MergeArgs& a, cudaStream_t s) {
   if (static_cast<int64_t>(a.n_parts) * a.Hq * R > kMergeMaxWeights * 4) return cudaErrorInvalidValue;
   const size_t smem = static_cast<size_t>(a.n_parts) * a.Hq * R * sizeof(float);
   if (smem > 48 * 1024) {
+    // The kernel's most, not this call's: the limit is the function's, and
+    // another host thread may launch between this and the launch below.
     cudaError_t e = cudaFuncSetAttribute(lse_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
+                                         kMergeMaxWeights * 4 * static_cast<int>(sizeof(float)));
     if (e != cudaSuccess) return e;
   }
   const int64_t blocks = (a.n + R - 1) / R;

@@ -92,4 +92,43 @@ def test_evictions(blocks):
 
 @pytest.mark.parametrize("n", [(2100, 3900), (4200, 40000)])
 def test_selections(n):
-    at_once(*(selecting(x) for x in n), times=4000 if n[1] < 4000 else 400)
+    at_once(*(selecting(x) for x in n), times=4000)
+
+
+def merging(parts, heads):
+    """A call that merges partial results; enough parts and heads take more
+    than 48 KB of weights."""
+    B = binding()
+    o = [torch.randn((8, heads, 64), device=DEV) for _ in range(parts)]
+    l = [torch.randn((heads, 8), device=DEV) for _ in range(parts)]
+    out, lse = gempty((8, heads, 64)), gempty((heads, 8))
+    po, pl = ((ctypes.c_void_p * parts)(*[t.data_ptr() for t in x]) for x in (o, l))
+    want = (torch.stack(o).double() * torch.softmax(torch.stack(l).double(), 0).transpose(1, 2)[..., None]).sum(0)
+
+    def call(stream, _keep=(o, l)):
+        return B._lib.msa_lse_merge(po, pl, parts, out.data_ptr(), lse.data_ptr(), 8, heads, 64, 0, stream)
+    return call, out, want
+
+
+def test_merges():
+    small, large = merging(64, 200), merging(64, 500)
+    at_once(small[0], large[0])
+    for _, out, want in (small, large):
+        assert (out.double() - want).abs().max() < 1e-5
+
+
+def choosing(G):
+    """A call of the prefill's block selection with G key blocks."""
+    B = binding()
+    n = 1024
+    q, lm = torch.randn((n, 1, 64), device=DEV), torch.randn((G, 1, 64), device=DEV)
+    sel, cnt = gempty((n // 128, 1, 1), torch.int32), gempty((n // 128, 1), torch.int32)
+
+    def call(stream, _keep=(q, lm, sel, cnt)):
+        return B._lib.msa_block_select(q.data_ptr(), lm.data_ptr(), sel.data_ptr(), cnt.data_ptr(), n, 1, 1, 64, 32, G, 1,
+                                       0, stream)
+    return call
+
+
+def test_prefill_selections():
+    at_once(choosing(2), choosing(1024))

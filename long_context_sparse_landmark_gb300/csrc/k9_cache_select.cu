@@ -9,7 +9,8 @@
 // rounding each, E_l = (g + 16) 2^-24 |sum_h |q_h||_2 |kmean_l|_2 (the sum over
 // g heads rounds g times, a lane's 8 products of each 32 dims 8 times, and
 // four joins follow; each is relative to sum_d (sum_h |q_h|) |kmean_l| at most,
-// which the norms bound); only the blocks whose score is
+// which the norms bound, each with kNormLost more for the squares that
+// fall below fp32); only the blocks whose score is
 // within 2 max E of the k-th are computed again in 64 bits.  So the choice
 // does not depend on the order of any fp32 sum.
 //
@@ -32,6 +33,9 @@ namespace {
 constexpr int kScoreThreads = 256;
 constexpr int kScoreBlocks = kScoreThreads / 4;  // blocks a CTA scores at a time
 constexpr int kScoreT = 4;                       // query tokens taken together
+// What a norm of 128 values may lack by squares that are flushed or rounded below
+// 2^-126: sqrt(128 * 2^-126).
+constexpr float kNormLost = 0x1p-59f;
 constexpr int kPickWarpsMax = 16;
 constexpr int kBins = 2048;
 constexpr int kListMax = 512;          // near-ties ranked in shared memory
@@ -114,7 +118,7 @@ __global__ void __launch_bounds__(kScoreThreads) cache_score_kernel(const CacheS
       for (int e = threadIdx.x & 31; e < D; e += 32) n2 = fmaf(qa[t][e], qa[t][e], n2);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) n2 += __shfl_xor_sync(0xffffffffu, n2, o);
-      if ((threadIdx.x & 31) == 0) norm[t] = sqrtf(n2) * eps;
+      if ((threadIdx.x & 31) == 0) norm[t] = (sqrtf(n2) + kNormLost) * eps;
     }
     __syncthreads();
     for (int l = l0; l - (static_cast<int>(threadIdx.x) >> 2) < most; l += step) {
@@ -134,7 +138,7 @@ __global__ void __launch_bounds__(kScoreThreads) cache_score_kernel(const CacheS
       }
       k2 += __shfl_xor_sync(0xffffffffu, k2, 1);
       k2 += __shfl_xor_sync(0xffffffffu, k2, 2);
-      const float k_norm = sqrtf(k2);
+      const float k_norm = sqrtf(k2) + kNormLost;
       for (int t = 0; t < nt; ++t) {
         float s[D / 32];
 #pragma unroll

@@ -976,3 +976,25 @@ def test_a_scale_of_zero_over_any_codes(lead, dtype):
     cache.v_scale.zero_()
     cache.k_scale.zero_()
     check_in_fp32(cache, t, lens, q, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("q_size,k_size", [(2.0 ** -83, 1.0), (1.0, 2.0 ** -90), (2.0 ** -60, 2.0 ** -30),
+                                           (2.0 ** -70, 2.0 ** -70), (1.0, 1.0)])
+def test_near_ties_of_tiny_scores(q_size, k_size, dtype):
+    """Norms whose squares fall below fp32 still bound the scores' rounding:
+    large parts that cancel, differences below fp32's rounding of them."""
+    n, d, half = 2500, 64, 31
+    rng = np.random.default_rng(n)
+    means = np.zeros((n, 1, d))
+    big = R.round_bf16(rng.normal(size=(n, half)) * 1000)
+    means[:, 0, :half], means[:, 0, 32:63] = big, -big[:, rng.permutation(half)]   # cancels in the end
+    means[:, 0, 63] = R.round_bf16(rng.integers(1, 256, n) * 2.0 ** -14)
+    means *= k_size
+    cache, t, lens = mean_cache(means)
+    t = np.concatenate([t, [[n]]], axis=1)
+    q = torch.full((1, 1, 2, d), q_size, device=DEV, dtype=torch.bfloat16 if dtype == "bf16" else torch.float32)
+    pool = {"k_codes": np.zeros((1, 1, 32, d)), "k_mean": np.concatenate([means, means[:1]])}
+    for top_k in (1, 17, n // 2):
+        sel, cnt = msa.cache_block_select(q, cache, i32(t), i32(lens), 1, top_k)
+        assert selected(sel, cnt) == R.select(pool, q.double().cpu().numpy(), t, lens, 1, top_k)

@@ -12,7 +12,8 @@ __all__ = ["WORKLOADS", "Workload", "generate", "sample_rows", "msa_attention",
            "msa_attention_backward", "msa_attention_trainable", "msa_attention_host",
            "compressed_attention_backward",
            "SparseLandmarkAttention", "KVCache", "cache_append", "cache_attention",
-           "cache_block_select", "cache_topk_attention", "cache_evict", "binding"]
+           "cache_block_select", "cache_select_attention", "cache_topk_attention", "cache_evict",
+           "binding"]
 
 
 def __getattr__(name):
@@ -23,7 +24,7 @@ def __getattr__(name):
         from . import api
         return getattr(api, name)
     if name in ("KVCache", "cache_append", "cache_attention", "cache_block_select",
-                "cache_topk_attention", "cache_evict"):
+                "cache_select_attention", "cache_topk_attention", "cache_evict"):
         from . import cache
         # Bound once: a decoding step should not pay for the lookup again.
         return globals().setdefault(name, getattr(cache, name))

@@ -3,8 +3,9 @@
 A ``KVCache`` is a pool of pages, each one block of token slots of one
 sequence (include/msa_cache.h has the format); a block table and the lengths say
 which pages a batch of sequences uses.  ``cache_append`` quantises new keys
-and values into it, ``cache_attention`` and ``cache_topk_attention`` attend
-to it, ``cache_evict`` keeps the slots that drew the most attention.  As in
+and values into it, ``cache_attention``, ``cache_topk_attention`` and
+``cache_select_attention`` attend to it, ``cache_evict`` keeps the slots that
+drew the most attention.  As in
 ``api``, these only allocate outputs and marshal arguments; they are not
 differentiable.
 
@@ -180,7 +181,8 @@ def cache_block_select(q: torch.Tensor, cache: KVCache, block_table: torch.Tenso
     """The top_k blocks before the window that each query token of q [batch,
     n_q, Hq, d] and KV head scores best by their mean keys
     (msa_cache_select).  Returns (sel [batch, n_q, Hkv, top_k] int32
-    ascending, then -1; cnt [batch, n_q, Hkv] int32)."""
+    ascending, then -1; cnt [batch, n_q, Hkv] int32), as
+    ``cache_select_attention`` takes them."""
     b, nb = _batch(cache, block_table, lens)
     n_q, _ = _query(cache, q, b)
     top_k = min(int(top_k), nb)
@@ -216,6 +218,35 @@ def cache_topk_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Ten
                          dtype=torch.uint8, device=cache.device)
         B.cache_attn_topk(cache.ref, q, block_table, lens, window, top_k, scale, out, lse, ws,
                           stream=s)
+        return out, lse
+
+    return _run(cache, stream, call)
+
+
+def cache_select_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
+                           lens: torch.Tensor, window: int, sel: torch.Tensor, cnt: torch.Tensor,
+                           scale: float | None = None, out_dtype: torch.dtype | None = None,
+                           stream=None):
+    """``cache_attention`` over each query token's window and given blocks
+    before it (msa_cache_attn_select): the first cnt [batch, n_q, Hkv] of sel
+    [batch, n_q, Hkv, top_k], int32, as ``cache_block_select`` returned them for
+    the same window or shorter lists without repeats.  Returns (out, lse)."""
+    b, nb = _batch(cache, block_table, lens)
+    n_q, Hq = _query(cache, q, b)
+    if sel.dim() != 4:
+        raise ValueError("sel must be [batch, n_q, Hkv, top_k]")
+    _want(sel, "sel", (_INT32,), (b, n_q, cache.Hkv, sel.shape[3]), cache.index)
+    _want(cnt, "cnt", (_INT32,), (b, n_q, cache.Hkv), cache.index)
+    d = cache.d
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+
+    def call(s):
+        out = torch.empty((b, n_q, Hq, d), dtype=out_dtype or q.dtype, device=cache.device)
+        lse = torch.empty((b, Hq, n_q), dtype=_F32, device=cache.device)
+        ws = torch.empty((B.cache_attn_select_workspace_size(cache.ref, nb, b, n_q, Hq, q.dtype),),
+                         dtype=torch.uint8, device=cache.device)
+        B.cache_attn_select(cache.ref, q, block_table, lens, window, sel, cnt, scale, out, lse, ws,
+                            stream=s)
         return out, lse
 
     return _run(cache, stream, call)

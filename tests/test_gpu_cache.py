@@ -998,3 +998,41 @@ def test_near_ties_of_tiny_scores(q_size, k_size, dtype):
     for top_k in (1, 17, n // 2):
         sel, cnt = msa.cache_block_select(q, cache, i32(t), i32(lens), 1, top_k)
         assert selected(sel, cnt) == R.select(pool, q.double().cpu().numpy(), t, lens, 1, top_k)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_selection_is_attended_through_the_package(dtype):
+    """What cache_block_select returns, attended, is cache_topk_attention; a
+    caller's shorter lists, an empty one among them, are the reference's; and a
+    call on another stream and from a graph gives the same."""
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    lens, d, window, top_k = [900, 130, 0], 128, 50, 5
+    cache, pool, t, _ = filled(lens, 2, d, 64, seed=96)
+    tt, tl = i32(t), i32(lens)
+    q = torch.randn((3, 2, 8, d), device=DEV).to(dt)
+    sel, cnt = msa.cache_block_select(q, cache, tt, tl, window, top_k)
+    out, lse = msa.cache_select_attention(q, cache, tt, tl, window, sel, cnt)
+    want = msa.cache_topk_attention(q, cache, tt, tl, window, top_k)
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    cnt = torch.minimum(cnt, i32([[[0, 2], [1, 4]]] * 3))
+    out, lse = msa.cache_select_attention(q, cache, tt, tl, window, sel, cnt, scale=0.1, out_dtype=torch.float32)
+    ref = R.attention(pool, q.double().cpu().numpy(), t, lens, window, 0.1, sel=selected(sel.where(
+        torch.arange(top_k, device=DEV) < cnt[..., None], -1), cnt))
+    check_attention(out, lse, ref, d, dtype == "bf16", 6.0)
+    assert binding().device_status() == 0
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    other = msa.cache_select_attention(q, cache, tt, tl, window, sel, cnt, 0.1, torch.float32, stream=side)
+    side.synchronize()
+    with torch.cuda.graph(graph):
+        captured = msa.cache_select_attention(q, cache, tt, tl, window, sel, cnt, 0.1, torch.float32)
+    graph.replay()
+    torch.cuda.synchronize()
+    for x in (other, captured):
+        assert torch.equal(x[0], out) and torch.equal(x[1], lse)
+    for error, bad in ((ValueError, (sel[0], cnt)), (ValueError, (sel[:, :1], cnt)), (ValueError, (sel, cnt[..., :1])),
+                       (TypeError, (sel.long(), cnt)), (TypeError, (sel, cnt.long())), (ValueError, (sel, cnt.cpu())),
+                       (msa.binding.MsaError, (sel[..., :0], cnt)),
+                       (ValueError, (sel.transpose(0, 1).contiguous().transpose(0, 1), cnt))):
+        with pytest.raises(error):
+            msa.cache_select_attention(q, cache, tt, tl, window, *bad)

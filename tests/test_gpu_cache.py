@@ -1036,3 +1036,109 @@ def test_a_selection_is_attended_through_the_package(dtype):
                        (ValueError, (sel.transpose(0, 1).contiguous().transpose(0, 1), cnt))):
         with pytest.raises(error):
             msa.cache_select_attention(q, cache, tt, tl, window, *bad)
+
+
+# -- sizes and layouts beyond the cases above --------------------------------
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_scales_that_are_no_powers_of_two(d, dtype):
+    """The attention takes any finite scale: a pool filled from elsewhere."""
+    lens = [700, 65]
+    cache, _, t, _ = filled(lens, 2, d, 64, seed=100)
+    for scale in (cache.k_scale, cache.v_scale):
+        scale.nan_to_num_(nan=1.0)
+        scale *= 0.3 + torch.rand_like(scale)
+    check_in_fp32(cache, t, lens, torch.randn((2, 1, 8, d), device=DEV), dtype, 0.1)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n_q,group,d", [(8, 8, 128), (9, 5, 64), (40, 3, 128), (130, 1, 64)])
+def test_more_rows_than_a_tile(n_q, group, d, dtype):
+    """Several 32-row tiles of a (sequence, KV head), the last one partly filled."""
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    lens = [700, 65, 20]
+    cache, pool, t, _ = filled(lens, 2, d, 64, seed=101)
+    q = torch.randn((3, n_q, 2 * group, d), device=DEV).to(dt)
+    for window in (None, 33):
+        ref = R.attention(pool, q.double().cpu().numpy(), t, lens, window or 1 << 30, 0.1)
+        w = torch.zeros((3, 2, t.shape[1] * 64), device=DEV)
+        out, lse = msa.cache_attention(q, cache, i32(t), i32(lens), window, scale=0.1, weights=w)
+        check_attention(out, lse, ref, d, dtype == "bf16", 6.0)
+        ds = (d + 4) * 2.0 ** -23 * ref[3].max()
+        tol = ref[5] * (2 * ds + 2.0 ** -20 + max(lens) * 2.0 ** -23 + n_q * group * 2.0 ** -24) + 1e-30
+        assert (np.abs(w.double().cpu().numpy() - ref[5]) <= tol).all()
+    assert binding().device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("batch,top", [(129, 70), (400, 300)])
+def test_more_sequences_than_a_cta_has_threads(batch, top, dtype):
+    """The list of sequences, or of query tokens, is scanned in rounds."""
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    rng = np.random.default_rng(batch)
+    lens = rng.integers(0, top, batch).tolist()
+    lens[0], lens[batch // 2], lens[-1] = 0, 0, top
+    cache, pool, t, _ = filled(lens, 1, 64, 32, seed=batch)
+    tt, tl = i32(t), i32(lens)
+    q = torch.randn((batch, 2, 2, 64), device=DEV).to(dt)
+    qn = q.double().cpu().numpy()
+    w = torch.zeros((batch, 1, t.shape[1] * 32), device=DEV)
+    out, lse = msa.cache_attention(q, cache, tt, tl, weights=w)
+    ref = R.attention(pool, qn, t, lens, 1 << 30, 0.125)
+    check_attention(out, lse, ref, 64, dtype == "bf16", 6.0)
+    ds = (64 + 4) * 2.0 ** -23 * ref[3].max()
+    tol = ref[5] * (2 * ds + 2.0 ** -20 + top * 2.0 ** -23 + 4 * 2.0 ** -24) + 1e-30
+    assert (np.abs(w.double().cpu().numpy() - ref[5]) <= tol).all()
+    sel, cnt = msa.cache_block_select(q, cache, tt, tl, 20, 2)
+    want = R.select(pool, qn, t, lens, 20, 2)
+    assert selected(sel, cnt) == want
+    out, lse = msa.cache_topk_attention(q, cache, tt, tl, 20, 2)
+    check_attention(out, lse, R.attention(pool, qn, t, lens, 20, 0.125, sel=want), 64, dtype == "bf16", 6.0)
+    assert binding().device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_sequences_that_share_a_prefix(dtype):
+    """Full pages in two tables: both attend them, appends and evictions of one
+    leave the other's slots as they were."""
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    cache, pool, t, free = filled([140, 40], 2, 64, 32, seed=102, extra=8, width=7)
+    t[1, :6] = [*t[0, :4], *t[1, :2]]      # 128 shared slots, then 40 of its own
+    t[1, 6] = free[0]
+    lens = [140, 168]
+    q = torch.randn((2, 1, 4, 64), device=DEV)
+    check_in_fp32(cache, t, lens, q, dtype, 0.125)
+    k = torch.randn((31, 2, 64), device=DEV).to(dt)
+    lens = [141, 198]
+    msa.cache_append(cache, k, k, i32([0, 1, 31]), i32(t), i32(lens), 30)
+    kn = k.double().cpu().numpy()
+    R.append(pool, kn, kn, [0, 1, 31], t, lens)
+    same_pool(cache, pool)
+    check_in_fp32(cache, t, lens, q, dtype, 0.125)
+    w = torch.rand((2, 2, t.shape[1] * 32), device=DEV)
+    check_evict(cache, pool, t, lens, w, free[1:7].reshape(2, 3), 90, 10)
+
+
+def test_drafts_dropped_under_range_checks():
+    """Shorter lengths after drafts, then other tokens in their slots (with
+    windows and selections, beside the test of the lengths alone)."""
+    cache, pool, t, free = filled([61, 30], 2, 64, 32, seed=103, extra=2, width=3)
+    t[0, 2], t[1, 1] = free[:2]
+    rng = np.random.default_rng(104)
+    lens = [61, 30]
+    for new, back in ((4, 3), (4, 4), (2, 0), (4, 1)):
+        k, v, q = (torch.as_tensor(rng.normal(size=s), device=DEV).to(torch.bfloat16)
+                   for s in ((2 * new, 2, 64), (2 * new, 2, 64), (2, 1, 4, 64)))
+        lens, cu = [n + new for n in lens], [0, new, 2 * new]
+        msa.cache_append(cache, k, v, i32(cu), i32(t), i32(lens), new)
+        R.append(pool, k.double().cpu().numpy(), v.double().cpu().numpy(), cu, t, lens)
+        same_pool(cache, pool)
+        lens = [n - back for n in lens]
+        qn = q.double().cpu().numpy()
+        out, lse = msa.cache_attention(q, cache, i32(t), i32(lens), 20)
+        check_attention(out, lse, R.attention(pool, qn, t, lens, 20, 1 / 8), 64, True, 6.0)
+        out, lse = msa.cache_topk_attention(q, cache, i32(t), i32(lens), 5, 1)
+        want = R.select(pool, qn, t, lens, 5, 1)
+        check_attention(out, lse, R.attention(pool, qn, t, lens, 5, 1 / 8, sel=want), 64, True, 6.0)
+    assert binding().device_status() == 0

@@ -11,9 +11,11 @@
 // digit is sign, exponent and two bits of the mantissa, so that weights of a
 // few binades do not all meet at a few counters.  The weights are read once
 // (parts too long for shared memory: once a digit, from L2): 4 bytes a slot,
-// against the 2 d bytes a kept slot costs in the gather; what bounds a call is
-// the chain of some ten barriers: 4160 slots of 64 (sequence, head) pairs in
-// 10 us, 131072 of 16 (clusters of 8) in 29.
+// against the 2 d bytes a kept slot costs in the gather.  A call is bound by
+// latency: of the warps a scheduler has waiting per issue 4.7 wait for loads from
+// global or another CTA's shared memory, 2.0 for fixed latencies, 1.6 at the ten or
+// so barriers.  2273 to 4160 slots of 64 (sequence, head) pairs take 9.4 us,
+// 131072 and 76276 of 8 heads each (clusters of 8) 29.
 #include <math.h>
 
 #include <cooperative_groups.h>

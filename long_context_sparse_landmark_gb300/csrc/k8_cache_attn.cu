@@ -32,16 +32,18 @@
 // needs 32 operations a byte, far below what either unit does.
 //   Up to 8, 16 or 32 rows share a read.  At 32 (four tokens of eight heads)
 // the latencies of the loop's some 950 instructions a chunk on 8 warps an SM
-// bound it (tensor pipe 20 % busy, issue slots 29 %): 16 sequences of 32K take
-// 139 us with one token (6.07 TB/s), 146 with two, 211 with four (362 as two
-// passes of 16 rows, when four took 218).  Short calls are bound by latency:
-// 32K tokens of one KV head take 11.7 us with the join, of which 6.6 are here;
+// bound it (tensor pipe 21 % busy, issue slots 23 %): 16 sequences of 17K to 32K
+// slots take 139 us with one token (6.05 TB/s), 143 with two, 208 with four (362
+// as two passes of 16 rows, when four took 218).  Short calls are bound by
+// latency: 32K tokens of one KV head take 11.0 us with the join, 6.4 of them here;
 // a part's first pass through the code, cold in the instruction cache, costs
 // more than its chunks.
 // fp32 rows run on the CUDA cores with fp32 arithmetic throughout: packed
-// multiply-adds, 8 rows a read.  8 sequences of 32K, 64 heads on 8 of 128, take
-// 251 us, 34 TFLOP/s of the 80 that the fp32 lanes have; the shared-memory reads
-// of q and the weights and the registers (12 warps an SM) bound it.
+// multiply-adds, 8 rows a read.  8 sequences of 20K to 32K slots, 64 heads on 8 of
+// 128, take 247 us, 26 TFLOP/s of the 80 that the fp32 lanes have.  No unit is
+// full (issue slots 37 %, the shared-memory pipe 53 %, fp32 lanes 35 %): the
+// registers allow 12 warps an SM, which wait for loads (1.7 warps a scheduler and
+// issue), fixed latencies (1.3) and shared memory (1.1).
 #include <math.h>
 
 #include "cache_common.cuh"
@@ -1233,7 +1235,8 @@ __global__ void __launch_bounds__(kThreads, Body::kPerSm) cache_attn_kernel(cons
 // Joins the parts of the units that several CTAs share, and writes the rows
 // that attend nothing.  kWpr warps a row: 1 where a unit has a few parts (and
 // 4 rows a CTA), 16 where it has many, every 16th part each (32K tokens of one
-// KV head, 256 parts: 5 us, with 4 warps 12); a lane has D/32 dims.
+// KV head: 128 parts in 5.2 us; 256 parts took 5 with 16 warps, 12 with 4); a
+// lane has D/32 dims.
 constexpr int kJoinMany = 16;
 
 template <int D, int kTile, int kWpr>

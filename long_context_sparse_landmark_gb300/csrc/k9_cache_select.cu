@@ -20,9 +20,10 @@
 // contiguous runs of the blocks with their keys in shared memory: a radix
 // selection of the k-th score by 11 + 11 + 10 bits, then a pass of ballots
 // that writes the chosen in order; what bounds it is the chain of barriers.
-// 512 blocks of 8 heads: scores 3.5 us, choice 5; 130560 (16 sequences, 2
-// tokens each, 33 MB of means): 15 and 11, of which 2 for the CTAs that have to
-// score in 64 bits.
+// 508 blocks of 8 heads: scores 3.9 us, choice 5.6 (5.0 and 7.7 one by one with
+// cold caches); 104104 blocks and heads (16 sequences of 38K to 65K slots, 2 tokens
+// each, 27 MB of means): 15 and 12, of which 2 for the CTAs that have to score in
+// 64 bits.
 #include <math.h>
 
 #include "cache_common.cuh"

@@ -125,9 +125,11 @@ struct Raw<false> {
 // is exact in them down to 2^-24, and what is smaller than that is far below
 // the 2^-10 at which e4m3 rounds to its least value.  The new scale is the
 // smaller one, by up to 2^17, where the slots kept of a block are all tiny: a
-// factor that halves do not hold is applied in two steps, each exact.
+// factor that halves do not hold is applied in two steps, each exact.  Slots of
+// zeros say nothing of the new scale: there the factor may be anything, and is
+// bounded, since 0 times an infinity is none.
 __device__ __forceinline__ uint4 rescale(const uint4& x, float s, float inv) {
-  float by = s * inv;
+  float by = fminf(s * inv, 0x1p17f);
   const bool twice = by > 32768.f;
   if (twice) by *= 1.f / 256.f;
   const __half2 f = __float2half2_rn(by);

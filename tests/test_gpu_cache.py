@@ -1142,3 +1142,21 @@ def test_drafts_dropped_under_range_checks():
         want = R.select(pool, qn, t, lens, 5, 1)
         check_attention(out, lse, R.attention(pool, qn, t, lens, 5, 1 / 8, sel=want), 64, True, 6.0)
     assert binding().device_status() == 0
+
+
+@pytest.mark.parametrize("size", [2.0 ** 26, 1e30])
+def test_evict_of_zeros_beside_far_larger_values(size):
+    """Slots whose codes are all 0 in a block of large values join a block of
+    small ones: they stay zeros."""
+    rng = np.random.default_rng(105)
+    k = rng.normal(size=(128, 1, 64)).astype(np.float32)
+    k[:32] *= 1e-30 if size > 1e20 else 1.0
+    k[32:64] = 0.0
+    k[40, 0, 7] = size                   # dropped, with its scale
+    t, dst = np.array([[0, 1, 2, 3]], dtype=np.int32), np.array([[6, 4]], dtype=np.int32)
+    cache = new_cache(8, 1, 64, 32)
+    kt = torch.as_tensor(k, device=DEV)
+    msa.cache_append(cache, kt, kt, i32([0, 128]), i32(t), i32([128]), 128)
+    w = torch.zeros((1, 1, 128), device=DEV)
+    w[..., 10:39] = 1.0                  # 22 small slots and 7 of zeros in one block
+    check_evict(cache, pool_of(cache), t, [128], w, dst, 40, 8)

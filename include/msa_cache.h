@@ -24,7 +24,8 @@
  *   The scale msa_cache_append gives a block is 2^e, e the least exponent
  * (>= -126) with amax <= 448 * 2^e over the block's slots; 0 for a block of
  * zeros; NaN, with codes of 0, for a block that holds a NaN or an infinity
- * (every row that attends a slot of such a block gets NaN).  The attention
+ * (every row that attends a slot of such a block gets NaN; its lse and weights
+ * too where the block's keys hold it).  The attention
  * takes any finite scale >= 0 and finite codes; an append to a block that holds
  * slots and an eviction take the powers of two that these two write.  k_mean
  * is written when a block becomes full: the mean of its keys code * scale,

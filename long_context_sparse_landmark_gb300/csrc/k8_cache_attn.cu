@@ -777,8 +777,8 @@ struct MmaBody {
         float part = sr * ex2(-(r ? base.y : base.x));
         if (kEdge && sr == 0.f) part = 0.f;
         // ... unless they are too small to tell it: values 2^60 below other
-        // blocks'.
-        if ((mx[n][r] + mM) + (r ? v.y : v.x) < -60.f) {
+        // blocks', or not numbers.
+        if (!((mx[n][r] + mM) + (r ? v.y : v.x) >= -60.f)) {
           part = 0.f;
 #pragma unroll
           for (int st = 0; st < 2; ++st)

@@ -1160,3 +1160,25 @@ def test_evict_of_zeros_beside_far_larger_values(size):
     w = torch.zeros((1, 1, 128), device=DEV)
     w[..., 10:39] = 1.0                  # 22 small slots and 7 of zeros in one block
     check_evict(cache, pool_of(cache), t, [128], w, dst, 40, 8)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [100, 9000])
+def test_poisoned_values_leave_lse_and_weights(n, dtype):
+    """The softmax does not know the values: a NaN among them makes the output
+    NaN, the lse and the weights are those of the keys."""
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    rng = np.random.default_rng(106)
+    k, v = rng.normal(size=(2, n, 128))
+    cache, t, lens = long_sequence(n, k, np.where(np.arange(n)[:, None] == 70, np.inf, v))
+    clean, t2, _ = long_sequence(n, k, v)
+    q = torch.randn((1, 1, 8, 128), device=DEV).to(dt)
+    w = torch.zeros((1, 1, t.shape[1] * 64), device=DEV)
+    out, lse = msa.cache_attention(q, cache, i32(t), i32(lens), weights=w)
+    assert torch.isnan(out).all()
+    ref = R.attention(pool_of(clean), q.double().cpu().numpy(), t2, lens, 1 << 30, 1 / math.sqrt(128))
+    tol_l = bounds(ref, 128, dtype == "bf16", dt)[1]
+    assert (np.abs(lse.double().cpu().numpy() - ref[1]) <= tol_l).all()
+    ds = (128 + 4) * 2.0 ** -23 * ref[3].max()
+    tol = ref[5] * (2 * ds + 2.0 ** -20 + n * 2.0 ** -23 + 8 * 2.0 ** -24) + 1e-30
+    assert (np.abs(w.double().cpu().numpy() - ref[5]) <= tol).all()

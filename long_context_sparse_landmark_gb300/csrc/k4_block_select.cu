@@ -210,19 +210,16 @@ cudaError_t launch_block_select(const SelectArgs& a, cudaStream_t s) {
   const size_t smem = block_select_smem(a.d, a.G);
   const int64_t n_qb = (a.n + kSelQBlock - 1) / kSelQBlock;
   dim3 grid(static_cast<unsigned>(n_qb), a.Hkv);
-  if (a.bf16) {
-    cudaError_t e = cudaFuncSetAttribute(block_select_kernel<true>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
+  // 48 KB hold the largest G that the entry points accept (its sort buffer is no
+  // longer than it), so no function attribute is set: it would be the size of
+  // this call, and another host thread could launch under it.
+  static_assert(sizeof(float) * (128 + kSelThreads * 8 + 4 * MSA_MAX_SELECT_BLOCKS) <= 48 * 1024 &&
+                    (MSA_MAX_SELECT_BLOCKS & (MSA_MAX_SELECT_BLOCKS - 1)) == 0,
+                "shared memory of the block selection");
+  if (a.bf16)
     block_select_kernel<true><<<grid, kSelThreads, smem, s>>>(a);
-  } else {
-    cudaError_t e = cudaFuncSetAttribute(block_select_kernel<false>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
+  else
     block_select_kernel<false><<<grid, kSelThreads, smem, s>>>(a);
-  }
   return cudaPeekAtLastError();
 }
 

@@ -11,8 +11,9 @@ __all__ = ["WORKLOADS", "Workload", "generate", "sample_rows", "msa_attention",
            "ring_attention", "band_attention", "topk_attention", "compressed_attention", "landmarks",
            "msa_attention_backward", "msa_attention_trainable", "msa_attention_host",
            "compressed_attention_backward",
-           "SparseLandmarkAttention", "KVCache", "cache_append", "cache_attention",
+           "SparseLandmarkAttention", "KVCache", "KVCache4", "cache_append", "cache_attention",
            "cache_block_select", "cache_select_attention", "cache_topk_attention", "cache_evict",
+           "cache_read",
            "binding"]
 
 
@@ -23,7 +24,7 @@ def __getattr__(name):
                 "compressed_attention_backward"):
         from . import api
         return getattr(api, name)
-    if name in ("KVCache", "cache_append", "cache_attention", "cache_block_select",
+    if name in ("KVCache", "KVCache4", "cache_read", "cache_append", "cache_attention", "cache_block_select",
                 "cache_select_attention", "cache_topk_attention", "cache_evict"):
         from . import cache
         # Bound once: a decoding step should not pay for the lookup again.

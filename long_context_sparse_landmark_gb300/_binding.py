@@ -35,6 +35,8 @@ EXPORTS = ("msa_version", "msa_last_error_string", "msa_landmark_pool", "msa_att
            "msa_cache_select_workspace_size", "msa_cache_select",
            "msa_cache_attn_select_workspace_size", "msa_cache_attn_select",
            "msa_cache_attn_topk_workspace_size", "msa_cache_attn_topk", "msa_cache_evict",
+           "msa_cache4_append", "msa_cache4_attn_workspace_size", "msa_cache4_attn",
+           "msa_cache_read", "msa_cache4_read",
            "msa_attn_uses_tensor_cores", "msa_attn_fwd_topk_uses_tensor_cores",
            "msa_debug_bounds_build", "msa_device_status", "msa_debug_set_wait_limit_ns",
            "msa_debug_force_single_cta", "msa_debug_set_max_clusters")
@@ -46,6 +48,14 @@ class KvCacheStruct(ctypes.Structure):
                 ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
                 ("k_mean", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
                 ("Hkv", ctypes.c_int), ("d", ctypes.c_int), ("block", ctypes.c_int)]
+
+
+class KvCache4Struct(ctypes.Structure):
+    """msa_kv_cache4."""
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int64), ("Hkv", ctypes.c_int), ("d", ctypes.c_int),
+                ("block", ctypes.c_int)]
 
 
 class MsaError(RuntimeError):
@@ -141,6 +151,18 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.msa_cache_evict.argtypes = [cp, vp, i32, vp, i32, vp, i64, i64, i64, vp, i32, vp, vp, vp,
                                     i64, vp]
     lib.msa_cache_evict.restype = i32
+    cp4 = ctypes.POINTER(KvCache4Struct)
+    lib.msa_cache4_append.argtypes = [cp4, vp, vp, vp, i64, i64, vp, i32, vp, i32, i32, vp]
+    lib.msa_cache4_append.restype = i32
+    lib.msa_cache4_attn_workspace_size.argtypes = [cp4, i32, i32, i32, i32, i32]
+    lib.msa_cache4_attn_workspace_size.restype = sz
+    lib.msa_cache4_attn.argtypes = [cp4, vp, vp, i32, vp, i32, i32, i32, i64, f32, vp, vp, i32,
+                                    i32, vp, sz, vp]
+    lib.msa_cache4_attn.restype = i32
+    lib.msa_cache_read.argtypes = [cp, vp, i64, i64, vp, i32, vp, i32, vp, vp, i32, vp]
+    lib.msa_cache_read.restype = i32
+    lib.msa_cache4_read.argtypes = [cp4, vp, i64, i64, vp, i32, vp, i32, vp, vp, i32, vp]
+    lib.msa_cache4_read.restype = i32
     lib.msa_attn_uses_tensor_cores.argtypes = [i32, i32, i32, i32]
     lib.msa_attn_uses_tensor_cores.restype = i32
     lib.msa_attn_fwd_topk_uses_tensor_cores.argtypes = [i64, i32, i32, i32, i32, i32]
@@ -579,3 +601,39 @@ def cache_evict(cache, table, lens, weights, dst_table, budget: int, recent: int
                                 _i32ptr(new_lens, "new_lens"), _i32ptr(kept, "kept"),
                                 _f32ptr(new_weights, "new_weights"), new_weights.shape[2],
                                 _raw_stream(stream)))
+
+
+# -- the 4-bit KV cache, and reading either back: `cache` a KvCache4Struct ------
+
+def cache4_append(cache, k, v, cu, max_new: int, table, lens, stream=None) -> None:
+    """msa_cache4_append: rows cu[b]..cu[b+1] of k, v become sequence b's last slots."""
+    _check(_lib.msa_cache4_append(cache, _addr(k), _addr(v), _i32ptr(cu, "cu"), k.shape[0],
+                                  int(max_new), _i32ptr(table, "table"), table.shape[1],
+                                  _i32ptr(lens, "lens"), table.shape[0], _dt(k),
+                                  _raw_stream(stream)))
+
+
+def cache4_attn_workspace_size(cache, max_blocks: int, batch: int, n_q: int, Hq: int,
+                               dtype: torch.dtype) -> int:
+    return _ws_size(int(_lib.msa_cache4_attn_workspace_size(
+        cache, max_blocks, batch, n_q, Hq, MSA_BF16 if dtype == torch.bfloat16 else MSA_F32)),
+        "msa_cache4_attn")
+
+
+def cache4_attn(cache, q, table, lens, window: int, scale: float, out, lse, workspace,
+                stream=None) -> None:
+    """msa_cache4_attn: query tokens q [batch, n_q, Hq, d] over the cache."""
+    b, n_q, Hq, _ = q.shape
+    _check(_lib.msa_cache4_attn(cache, _addr(q), _i32ptr(table, "table"), table.shape[1],
+                                _i32ptr(lens, "lens"), b, n_q, Hq, int(window), float(scale),
+                                _addr(out), _f32ptr(lse, "lse"), _dt(q), _dt(out),
+                                _addr(workspace), workspace.nbytes, _raw_stream(stream)))
+
+
+def cache_read(cache, bits: int, cu, max_rows: int, table, lens, k, v, stream=None) -> None:
+    """msa_cache_read (bits 8) or msa_cache4_read (4): sequence b's last slots
+    into rows cu[b]..cu[b+1] of k, v [total, Hkv, d]."""
+    f = _lib.msa_cache_read if bits == 8 else _lib.msa_cache4_read
+    _check(f(cache, _i32ptr(cu, "cu"), k.shape[0], int(max_rows), _i32ptr(table, "table"),
+             table.shape[1], _i32ptr(lens, "lens"), table.shape[0], _addr(k), _addr(v), _dt(k),
+             _raw_stream(stream)))

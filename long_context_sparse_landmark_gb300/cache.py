@@ -1,13 +1,15 @@
-"""The 8-bit KV cache: the tokens generated after a long prefill.
+"""The 8-bit and the 4-bit KV cache: the tokens generated after a long prefill.
 
 A ``KVCache`` is a pool of pages, each one block of token slots of one
 sequence (include/msa_cache.h has the format); a block table and the lengths say
 which pages a batch of sequences uses.  ``cache_append`` quantises new keys
 and values into it, ``cache_attention``, ``cache_topk_attention`` and
 ``cache_select_attention`` attend to it, ``cache_evict`` keeps the slots that
-drew the most attention.  As in
-``api``, these only allocate outputs and marshal arguments; they are not
-differentiable.
+drew the most attention, ``cache_read`` reads it back as rows of keys and
+values.  A ``KVCache4`` holds a token in half the bytes (include/msa_cache4.h);
+``cache_append``, ``cache_attention`` and ``cache_read`` take either, the others
+the 8-bit one.  As in ``api``, these only allocate outputs and marshal
+arguments; they are not differentiable.
 
 Every call runs on the device of its tensors and, unless ``stream`` says
 otherwise, on that device's current stream; outputs and workspaces are
@@ -91,7 +93,58 @@ class KVCache:
         return cls(codes[0].view(_E4M3), codes[1].view(_E4M3), scale[0], scale[1], mean)
 
 
-def _batch(cache: KVCache, table: torch.Tensor, lens: torch.Tensor):
+class KVCache4:
+    """Pages of 4-bit keys and values (include/msa_cache4.h).
+
+    k_codes, v_codes [n_pages, Hkv, block, d / 2] uint8, two e2m1 codes a byte,
+    k_scale, v_scale [n_pages, Hkv, block, d / 32] uint8, the e8m0 scale of 32
+    values; block 32, 64, 128 or 256, d 64 or 128.  ``KVCache4.empty``
+    allocates them.
+    """
+
+    def __init__(self, k_codes: torch.Tensor, v_codes: torch.Tensor, k_scale: torch.Tensor,
+                 v_scale: torch.Tensor):
+        if k_codes.dim() != 4 or not k_codes.is_cuda:
+            raise ValueError("k_codes must be [n_pages, Hkv, block, d / 2] on a CUDA device")
+        shape = k_codes.shape
+        n, h, block, half = shape
+        dev = k_codes.get_device()
+        _want(k_codes, "k_codes", (torch.uint8,), shape, dev)
+        _want(v_codes, "v_codes", (torch.uint8,), shape, dev)
+        _want(k_scale, "k_scale", (torch.uint8,), (n, h, block, half // 16), dev)
+        _want(v_scale, "v_scale", (torch.uint8,), (n, h, block, half // 16), dev)
+        self._pool = (k_codes, v_codes, k_scale, v_scale)
+        self.n_pages, self.Hkv, self.block, self.d = n, h, block, 2 * half
+        self.device = k_codes.device
+        self.index = dev
+        for t in self._pool:
+            if not t.is_contiguous():
+                raise ValueError("the pool's tensors must be contiguous")
+        self.struct = B.KvCache4Struct(k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(),
+                                       v_scale.data_ptr(), n, h, self.d, block)
+        self.ref = ctypes.byref(self.struct)
+
+    # As with KVCache: they can be written to, not replaced.
+    k_codes = property(lambda self: self._pool[0])
+    v_codes = property(lambda self: self._pool[1])
+    k_scale = property(lambda self: self._pool[2])
+    v_scale = property(lambda self: self._pool[3])
+
+    @classmethod
+    def empty(cls, n_pages: int, Hkv: int, d: int, block: int = 64, device="cuda") -> "KVCache4":
+        """A pool of n_pages pages; nothing in it needs a value before the
+        first append."""
+        codes = torch.empty((2, n_pages, Hkv, block, d // 2), dtype=torch.uint8, device=device)
+        scale = torch.empty((2, n_pages, Hkv, block, d // 32), dtype=torch.uint8, device=device)
+        return cls(codes[0], codes[1], scale[0], scale[1])
+
+
+def _eight_bit(cache, call: str):
+    if not isinstance(cache, KVCache):
+        raise TypeError(f"{call} takes a KVCache, not {type(cache).__name__}")
+
+
+def _batch(cache: KVCache | KVCache4, table: torch.Tensor, lens: torch.Tensor):
     """Checks a batch's block table and lengths; returns their sizes."""
     shape = table.shape
     if len(shape) != 2:
@@ -124,10 +177,10 @@ def _run(cache: KVCache, stream, call):
         return call(stream.cuda_stream)
 
 
-def cache_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor,
+def cache_append(cache: KVCache | KVCache4, k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor,
                  block_table: torch.Tensor, lens: torch.Tensor, max_new: int,
                  stream=None) -> None:
-    """Quantise new tokens into the cache (msa_cache_append).
+    """Quantise new tokens into the cache (msa_cache_append, msa_cache4_append).
 
     k, v [total, Hkv, d] (bf16 or fp32): rows cu[b] .. cu[b+1] (cu
     [batch + 1] int32) are sequence b's last tokens; lens [batch] int32 are
@@ -140,25 +193,64 @@ def cache_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, cu: torch.Ten
     _want(k, "k", _INPUTS, (k.shape[0], cache.Hkv, cache.d), cache.index)
     _want(v, "v", (k.dtype,), k.shape, cache.index)
     _want(cu, "cu", (_INT32,), (b + 1,), cache.index)
-    _run(cache, stream, lambda s: B.cache_append(cache.ref, k, v, cu, max_new, block_table, lens,
-                                                 stream=s))
+    append = B.cache4_append if isinstance(cache, KVCache4) else B.cache_append
+    _run(cache, stream, lambda s: append(cache.ref, k, v, cu, max_new, block_table, lens,
+                                         stream=s))
 
 
-def cache_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
+def cache_read(cache: KVCache | KVCache4, cu: torch.Tensor, block_table: torch.Tensor,
+               lens: torch.Tensor, total: int, max_rows: int,
+               dtype: torch.dtype = torch.bfloat16, out=None, stream=None):
+    """Read cached tokens back as rows of keys and values (msa_cache_read,
+    msa_cache4_read), as the prefill's calls take them.
+
+    Of each sequence b the last cu[b+1] - cu[b] of its lens[b] slots (at most
+    max_rows; lower lens[b] for an earlier range) become the rows cu[b] ..
+    cu[b+1] of k, v [total, Hkv, d] (``dtype``, bf16 or fp32).  ``out`` gives the
+    two tensors to write; rows of no sequence are left as they were there, and
+    hold anything in new ones.  Returns (k, v)."""
+    b, _ = _batch(cache, block_table, lens)
+    _want(cu, "cu", (_INT32,), (b + 1,), cache.index)
+    shape = (int(total), cache.Hkv, cache.d)
+    if dtype not in _INPUTS:
+        raise TypeError(f"dtype must be float32 or bfloat16, not {dtype}")
+    if out is not None:
+        k, v = out
+        _want(k, "out", (dtype,), shape, cache.index)
+        _want(v, "out", (dtype,), shape, cache.index)
+        if shape[0] and k.data_ptr() == v.data_ptr():
+            raise ValueError("out: k and v must not be the same memory")
+
+    def call(s):
+        if out is not None:
+            kv = out
+        else:
+            kv = (torch.empty(shape, dtype=dtype, device=cache.device),
+                  torch.empty(shape, dtype=dtype, device=cache.device))
+        B.cache_read(cache.ref, 4 if isinstance(cache, KVCache4) else 8, cu, max_rows,
+                     block_table, lens, kv[0], kv[1], stream=s)
+        return kv[0], kv[1]
+
+    return _run(cache, stream, call)
+
+
+def cache_attention(q: torch.Tensor, cache: KVCache | KVCache4, block_table: torch.Tensor,
                     lens: torch.Tensor, window: int | None = None, scale: float | None = None,
                     weights: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
                     stream=None):
     """Attention of the last n_q tokens of each sequence over its cached
-    slots (msa_cache_attn): q [batch, n_q, Hq, d], causal among themselves,
-    over the last ``window`` slots (None: all).  ``weights`` [batch, Hkv, ld]
-    fp32, ld >= max_blocks * block, is added the softmax weight each slot
-    drew.  Returns (out [batch, n_q, Hq, d], lse [batch, Hq, n_q] fp32)."""
+    slots (msa_cache_attn, msa_cache4_attn): q [batch, n_q, Hq, d], causal
+    among themselves, over the last ``window`` slots (None: all).  ``weights``
+    [batch, Hkv, ld] fp32, ld >= max_blocks * block, is added the softmax weight
+    each slot drew (8-bit cache).  Returns (out [batch, n_q, Hq, d], lse [batch, Hq, n_q] fp32)."""
     b, nb = _batch(cache, block_table, lens)
     n_q, Hq = _query(cache, q, b)
     d = cache.d
     window = nb * cache.block if window is None else int(window)
     scale = 1.0 / math.sqrt(d) if scale is None else scale
+    four = isinstance(cache, KVCache4)
     if weights is not None:
+        _eight_bit(cache, "cache_attention with weights")
         if weights.dim() != 3:
             raise ValueError("weights must be [batch, Hkv, ld]")
         _want(weights, "weights", (_F32,), (b, cache.Hkv, weights.shape[2]), cache.index)
@@ -166,6 +258,11 @@ def cache_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
     def call(s):
         out = torch.empty((b, n_q, Hq, d), dtype=out_dtype or q.dtype, device=cache.device)
         lse = torch.empty((b, Hq, n_q), dtype=_F32, device=cache.device)
+        if four:
+            ws = torch.empty((B.cache4_attn_workspace_size(cache.ref, nb, b, n_q, Hq, q.dtype),),
+                             dtype=torch.uint8, device=cache.device)
+            B.cache4_attn(cache.ref, q, block_table, lens, window, scale, out, lse, ws, stream=s)
+            return out, lse
         ws = torch.empty((B.cache_attn_workspace_size(cache.ref, nb, b, n_q, Hq,
                                                       weights is not None, q.dtype),),
                          dtype=torch.uint8, device=cache.device)
@@ -183,6 +280,7 @@ def cache_block_select(q: torch.Tensor, cache: KVCache, block_table: torch.Tenso
     (msa_cache_select).  Returns (sel [batch, n_q, Hkv, top_k] int32
     ascending, then -1; cnt [batch, n_q, Hkv] int32), as
     ``cache_select_attention`` takes them."""
+    _eight_bit(cache, "cache_block_select")
     b, nb = _batch(cache, block_table, lens)
     n_q, _ = _query(cache, q, b)
     top_k = min(int(top_k), nb)
@@ -204,6 +302,7 @@ def cache_topk_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Ten
                          stream=None):
     """``cache_attention`` over each query token's window and its own top_k
     blocks (msa_cache_attn_topk).  Returns (out, lse)."""
+    _eight_bit(cache, "cache_topk_attention")
     b, nb = _batch(cache, block_table, lens)
     n_q, Hq = _query(cache, q, b)
     d = cache.d
@@ -231,6 +330,7 @@ def cache_select_attention(q: torch.Tensor, cache: KVCache, block_table: torch.T
     before it (msa_cache_attn_select): the first cnt [batch, n_q, Hkv] of sel
     [batch, n_q, Hkv, top_k], int32, as ``cache_block_select`` returned them for
     the same window or shorter lists without repeats.  Returns (out, lse)."""
+    _eight_bit(cache, "cache_select_attention")
     b, nb = _batch(cache, block_table, lens)
     n_q, Hq = _query(cache, q, b)
     if sel.dim() != 4:
@@ -261,6 +361,7 @@ def cache_evict(cache: KVCache, block_table: torch.Tensor, lens: torch.Tensor,
     dst_blocks], which must not be among those in use.  Returns (new_lens
     [batch] int32, kept [batch, Hkv, budget] int32 slots ascending, then -1,
     new_weights [batch, Hkv, dst_blocks * block] fp32)."""
+    _eight_bit(cache, "cache_evict")
     b, h = _batch(cache, block_table, lens)[0], cache.Hkv
     if weights.dim() != 3 or dst_table.dim() != 2:
         raise ValueError("weights must be [batch, Hkv, ld], dst_table [batch, dst_blocks]")

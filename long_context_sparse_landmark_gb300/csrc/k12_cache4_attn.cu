@@ -1,0 +1,664 @@
+// K12: attention of a few query tokens over the 4-bit KV cache, in full or over a
+// window.
+//
+// Mathematics, per query row, in log2 units: s_j = scale log2e <q, k_j>, out =
+// sum_j 2^{s_j} v_j / sum_j 2^{s_j}.  A slot's codes times their scales over the
+// slot's own largest, 2^x, are halves (code * 2^{13 - delta}, exact for a delta
+// of up to 27; 0 beyond): k_j = 2^{x_j - 13} kh_j, and likewise v_j = 2^{y_j} vh_j.
+// x goes into the score, y into the exponent of the weight that meets vh: w_j =
+// 2^{(s_j - M) + (y_j - D)}.  M, to 2^60, is the largest s so far, the
+// denominator's reference, and M + D, to 2^1.5, the largest s + y, the output's;
+// D is kept as an offset of M, so that a large score does not round the value
+// scale away.  No slot's scales touch another's.
+//
+// The work is read once, 136 bytes a slot and KV head of 128 dims, shared by the
+// group's rows: half of what the 8-bit cache takes, with the same arithmetic, so
+// that instructions bound it about as much as HBM does.  The list of 32-slot
+// chunks, its cut and the join are the 8-bit cache's (cache_attn.cuh).
+//
+// All rows run on the tensor cores (mma.sync, fp16 operands): keys are the MMA's
+// 16 rows and query rows its 8 columns, so that a group of 8 heads wastes nothing.
+// A lane's share of a slot is a run of d / 4 dims of K, d / 8 of V: each within one
+// scale, so a fragment takes a conversion of two codes and one multiplication.
+// fp32 rows are two halves each, their weights too: 22 bits.
+#include "cache4.cuh"
+#include "cache_attn.cuh"
+
+namespace msa {
+namespace {
+
+constexpr float kTop = 13.f;  // a code of the slot's largest scale is code * 2^13
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&a),
+                            *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&x);
+}
+// Bits of m from a, the others from b.
+__device__ __forceinline__ uint32_t select_bits(uint32_t m, uint32_t a, uint32_t b) {
+  return (a & m) | (b & ~m);
+}
+
+// Scales of a slot (bytes of w) as halves 2^{13 - delta} below the largest, which
+// is returned: groups 0 and 2 in h[0], 1 and 3 in h[1].
+__device__ __forceinline__ uint32_t slot_scales(uint32_t w, uint32_t* h) {
+  const uint32_t a = w & 0x00ff00ffu, b = (w >> 8) & 0x00ff00ffu;
+  uint32_t m = __vmaxu2(a, b);
+  m = max(m >> 16, m & 0xffffu);
+  // (13 + 15) - delta as exponents of halves, 0 at the least: a half of 0.
+  const uint32_t off = __byte_perm(28u - m, 0, 0x1010);
+  h[0] = __viaddmax_s16x2(a, off, 0u) << 10;
+  h[1] = __viaddmax_s16x2(b, off, 0u) << 10;
+  return m;
+}
+
+template <int D, int kNt, int kTerms>
+struct Body4 {
+  static constexpr int kTile = 8 * kNt;
+  static constexpr int kPerSm = kNt == 1 ? 3 : 2;
+  static constexpr int kStages = (kNt == 4 ? 4 : 3) * (D == 128 ? 1 : 2);
+  static constexpr bool kQShared = kNt * kTerms > 2;
+  static constexpr int kCodes = kChunk * D / 2, kScales = kChunk * D / kGroup4;  // of K, or of V
+  static constexpr int kStageBytes = 2 * kCodes + 2 * kScales;
+  static constexpr int kRingBytes = kStages * kStageBytes;
+  static constexpr int kKs = D / 16;  // k-steps over d
+  static constexpr int kMt = D / 16;  // 16-row tiles of O^T
+  static constexpr int kGroups = D / kGroup4;
+
+  // What a warp makes of a chunk's scales.
+  struct Scales {
+    float4 slot[kChunk];              // 2^x, twice, and y, twice
+    uint32_t k[kChunk * kGroups];     // half 2^{13 - delta}, twice: [slot][group]
+    uint16_t v[kGroups][40];          // the half: [group][slot], rows 80 bytes apart
+  };
+  // Rows of a unit, for all warps: their fragments [term][k-step][tile][lane],
+  // score scales and positions.
+  struct Rows {
+    uint2 q[kTerms][kKs * kNt * 32];
+    float scale[kTile];
+    int pos[kTile];
+  };
+  static constexpr int kSmem = kWarps * (kRingBytes + static_cast<int>(sizeof(Scales))) +
+                               static_cast<int>(sizeof(Rows));
+  static_assert(kWarps * kRingBytes >= kWarps * kTile * (D + 4) * 4, "sums must fit the rings");
+  static_assert(sizeof(Scales) % 16 == 0 && kStageBytes % 16 == 0, "16-byte pieces");
+
+  uint32_t q[kTerms][kQShared ? 1 : kKs][kQShared ? 1 : kNt][2];
+  float qs[kNt][2];  // score scale of rows 2t, 2t+1 (log2 units)
+  float o[kMt][kNt][4];
+  float l[kNt][2], M[kNt][2], D0[kNt][2];  // l in units of 2^M, o of 2^{M + D0 - kPBits}
+
+  __device__ __forceinline__ static Rows& rows_of(uint8_t* smem) {
+    return *reinterpret_cast<Rows*>(smem +
+                                    kWarps * (kRingBytes + static_cast<int>(sizeof(Scales))));
+  }
+
+  // The CTA writes them: a thread takes 8 values of a row.
+  __device__ __forceinline__ static void load_rows(const CacheAttnArgs& a, const Plan& p,
+                                                   const Entry& e, int c, int rt, uint8_t* smem) {
+    constexpr int kP = D / 8, kOwn = D / 32;  // pieces of a row, and of a lane
+    Rows& rows = rows_of(smem);
+#pragma unroll 1
+    for (int i = threadIdx.x; i < kTile * kP; i += kThreads) {  // whole warps
+      const int r = i / kP, pc = i - r * kP, m = rt * kTile + r;
+      int t, h;
+      row_of(a, e, c, min(m, p.rows - 1), &t, &h);
+      const int64_t at = ((static_cast<int64_t>(e.b) * a.T + t) * a.Hq + h) * D + 8 * pc;
+      float v[8], mx = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = 0.f;
+      if (m < p.rows) {
+        if constexpr (kTerms == 1) {
+          const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at);
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            v[2 * k] = __uint_as_float(w[k] << 16);
+            v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+          }
+        } else {
+          const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at);
+          const float4 x = s[0], y = s[1];
+          v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+          v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) mx = fmaxf(mx, fabsf(v[k]));
+#pragma unroll
+      for (int o2 = 1; o2 < kP; o2 <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o2));
+      // 2^k brings the row's largest magnitude to [2^14, 2^15).
+      int k2 = mx > 0.f ? 14 + 127 - static_cast<int>(__float_as_uint(mx) >> 23) : 0;
+      k2 = k2 > 100 ? 100 : k2;
+      const float up = pow2i(k2);
+      // Lane t4's dims of k-step ks are (D / 4) t4 + 4 ks + 0..3.
+      const int ks = 2 * (pc % kOwn);
+      const int lane = (r & 7) * 4 + pc / kOwn;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] *= up;
+#pragma unroll
+      for (int term = 0; term < kTerms; ++term) {
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const __half2 x = __floats2half2_rn(v[2 * k], v[2 * k + 1]);
+          w[k] = *reinterpret_cast<const uint32_t*>(&x);
+          if (term + 1 < kTerms) {  // what the half leaves, exactly
+            const float2 f = __half22float2(x);
+            v[2 * k] -= f.x;
+            v[2 * k + 1] -= f.y;
+          }
+        }
+        uint2* to = rows.q[term] + (ks * kNt + (r >> 3)) * 32 + lane;
+        to[0] = make_uint2(w[0], w[1]);
+        to[kNt * 32] = make_uint2(w[2], w[3]);
+      }
+      if (pc == 0) {
+        rows.scale[r] = a.scale * kLog2e * pow2i(-k2) * 0x1p-13f;
+        rows.pos[r] = e.len - a.T + t;
+      }
+    }
+  }
+
+  const Rows* rows;
+  Scales* scales;
+
+  __device__ __forceinline__ void begin(uint8_t* smem) {
+    const int lane = threadIdx.x & 31, t4 = lane & 3;
+    rows = &rows_of(smem);
+    scales = reinterpret_cast<Scales*>(smem + kWarps * kRingBytes) + (threadIdx.x >> 5);
+#pragma unroll
+    for (int n = 0; n < kNt; ++n) {
+      if constexpr (!kQShared) {
+#pragma unroll
+        for (int term = 0; term < kTerms; ++term)
+#pragma unroll
+          for (int ks = 0; ks < kKs; ++ks) {
+            const uint2 x = rows->q[term][(ks * kNt + n) * 32 + lane];
+            q[term][ks][n][0] = x.x;
+            q[term][ks][n][1] = x.y;
+          }
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        qs[n][r] = rows->scale[8 * n + 2 * t4 + r];
+        M[n][r] = -INFINITY;
+        l[n][r] = D0[n][r] = 0.f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kMt; ++i)
+#pragma unroll
+      for (int n = 0; n < kNt; ++n)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[i][n][k] = 0.f;
+  }
+
+  // A warp's chunks pass through a ring of its own: K codes [32][D / 2], V codes
+  // likewise with rows and 16-byte pieces moved about so that the fragment reads
+  // below meet no bank twice, then the scales.
+  __device__ __forceinline__ static int k_at(int row, int piece) {
+    return row * (D / 2) + (piece << 4);
+  }
+  __device__ __forceinline__ static int v_at(int row, int piece) {
+    return kCodes + (D == 128 ? (row ^ ((row >> 1) & 1)) * 64 + ((piece ^ ((row >> 1) & 2)) << 4)
+                              : (row ^ ((row >> 2) & 1)) * 32 + (piece << 4));
+  }
+  // Starts the copy of the chunk whose first slot is row `at` of the pool.
+  __device__ __forceinline__ static void copy(const Cache4AttnArgs& a, int64_t at,
+                                              uint8_t* stage) {
+    constexpr int kPer = D / 32;      // pieces a row
+    constexpr int kStep = 32 / kPer;  // rows the warp copies at a time
+    const int lane = threadIdx.x & 31, piece = lane % kPer, row0 = lane / kPer;
+    if (!MSA_IN_RANGE(at, kChunk, a.c.n_pages * a.c.Hkv * a.c.block, a.status)) return;
+    const uint8_t* k = a.c.k_codes + at * (D / 2) + lane * 16;
+    const uint8_t* v = a.c.v_codes + at * (D / 2) + lane * 16;
+#pragma unroll
+    for (int i = 0; i < kChunk / kStep; ++i)
+      copy_async16(stage + k_at(row0 + i * kStep, piece), k + i * 512);
+#pragma unroll
+    for (int i = 0; i < kChunk / kStep; ++i)
+      copy_async16(stage + v_at(row0 + i * kStep, piece), v + i * 512);
+    constexpr int kSp = kScales / 16;  // pieces of K's scales, and of V's
+    if (lane < 2 * kSp) {
+      const uint8_t* s = (lane < kSp ? a.k_exp : a.v_exp) + at * kGroups + (lane % kSp) * 16;
+      copy_async16(stage + 2 * kCodes + lane * 16, s);
+    }
+  }
+
+  // A lane a slot: its scales.
+  __device__ __forceinline__ void read_scales(const uint8_t* stage) {
+    const int lane = threadIdx.x & 31;
+    const uint8_t* at = stage + 2 * kCodes;
+    uint32_t kw, vw;
+    if constexpr (D == 128) {
+      kw = reinterpret_cast<const uint32_t*>(at)[lane];
+      vw = reinterpret_cast<const uint32_t*>(at + kScales)[lane];
+    } else {
+      kw = reinterpret_cast<const uint16_t*>(at)[lane];
+      vw = reinterpret_cast<const uint16_t*>(at + kScales)[lane];
+    }
+    uint32_t kh[2], vh[2];
+    const uint32_t x = slot_scales(kw, kh), y = slot_scales(vw, vh);
+    const float ks = e8m0_to_float(x);
+    const float lvs = y == 255 ? __uint_as_float(0x7fc00000u) : static_cast<float>(y) - 127.f - kTop;
+    scales->slot[lane] = make_float4(ks, ks, lvs, lvs);
+    if constexpr (D == 128) {
+      reinterpret_cast<uint4*>(scales->k)[lane] =
+          make_uint4(__byte_perm(kh[0], 0, 0x1010), __byte_perm(kh[1], 0, 0x1010),
+                     __byte_perm(kh[0], 0, 0x3232), __byte_perm(kh[1], 0, 0x3232));
+      scales->v[2][lane] = static_cast<uint16_t>(vh[0] >> 16);
+      scales->v[3][lane] = static_cast<uint16_t>(vh[1] >> 16);
+    } else {
+      reinterpret_cast<uint2*>(scales->k)[lane] =
+          make_uint2(__byte_perm(kh[0], 0, 0x1010), __byte_perm(kh[1], 0, 0x1010));
+    }
+    scales->v[0][lane] = static_cast<uint16_t>(vh[0]);
+    scales->v[1][lane] = static_cast<uint16_t>(vh[1]);
+  }
+
+  float s[2][kNt][4];  // [16-slot step][tile][slot g, row 2t, 2t+1; slot g + 8, ...]
+
+  __device__ __forceinline__ void scores(const uint8_t* stage) {
+    constexpr int kW = D / 32;  // words of a K row a lane holds, 8 dims each
+    const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+#pragma unroll
+    for (int st = 0; st < 2; ++st)
+#pragma unroll
+      for (int n = 0; n < kNt; ++n)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[st][n][k] = 0.f;
+    uint32_t kw[2][2][kW], sc[2][2];
+#pragma unroll
+    for (int st = 0; st < 2; ++st)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int row = 16 * st + 8 * r + g;
+        sc[st][r] = scales->k[row * kGroups + (D == 128 ? t4 : t4 >> 1)];
+        if constexpr (D == 128) {
+          const uint4 w = *reinterpret_cast<const uint4*>(stage + k_at(row, t4));
+          kw[st][r][0] = w.x, kw[st][r][1] = w.y, kw[st][r][2] = w.z, kw[st][r][3] = w.w;
+        } else {
+          const uint2 w = *reinterpret_cast<const uint2*>(stage + k_at(row, t4 >> 1) + 8 * (t4 & 1));
+          kw[st][r][0] = w.x, kw[st][r][1] = w.y;
+        }
+      }
+#pragma unroll
+    for (int w = 0; w < kW; ++w)
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {
+        uint32_t f[2][4];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          e2m1x8_to_half2(kw[st][r][w], f[r]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) f[r][k] = hmul2(f[r][k], sc[st][r]);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int ks = 2 * w + h;
+          const uint32_t fa[4] = {f[0][2 * h], f[1][2 * h], f[0][2 * h + 1], f[1][2 * h + 1]};
+#pragma unroll
+          for (int term = kTerms - 1; term >= 0; --term)  // the smaller products first
+#pragma unroll
+            for (int n = 0; n < kNt; ++n) {
+              uint32_t b0, b1;
+              if constexpr (kQShared) {
+                const uint2 x = rows->q[term][(ks * kNt + n) * 32 + lane];
+                b0 = x.x, b1 = x.y;
+              } else {
+                b0 = q[term][ks][n][0], b1 = q[term][ks][n][1];
+              }
+              mma16816(s[st][n], fa, b0, b1);
+            }
+        }
+      }
+  }
+
+  // Softmax of the chunk's scores into halves pf[term][step][tile][b0, b1], and
+  // the running sums.  kEdge: some slot is masked for some row.
+  uint32_t pf[kTerms][2][kNt][2];
+
+  template <bool kEdge>
+  __device__ __forceinline__ void softmax(const CacheAttnArgs& a, int key0, bool on) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+    float2 lvs[2][2];  // [step][slot g, g + 8]
+    float mx[kNt][2];
+    bool rise = false;
+#pragma unroll
+    for (int n = 0; n < kNt; ++n) mx[n][0] = mx[n][1] = -INFINITY;
+#pragma unroll
+    for (int st = 0; st < 2; ++st)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float4 of = scales->slot[16 * st + 8 * k + g];
+        lvs[st][k] = make_float2(of.z, of.w);
+#pragma unroll
+        for (int n = 0; n < kNt; ++n) {
+          const float2 f = __fmul2_rn(make_float2(qs[n][0], qs[n][1]), make_float2(of.x, of.y));
+          float2 y = __fmul2_rn(make_float2(s[st][n][2 * k], s[st][n][2 * k + 1]), f);
+          if (kEdge) {
+            const int key = key0 + 16 * st + 8 * k + g;
+            const int p0 = rows->pos[8 * n + 2 * t4], p1 = rows->pos[8 * n + 2 * t4 + 1];
+            if (!on || key > p0 || p0 - key >= a.window) y.x = -INFINITY;
+            if (!on || key > p1 || p1 - key >= a.window) y.y = -INFINITY;
+          }
+          s[st][n][2 * k] = y.x;
+          s[st][n][2 * k + 1] = y.y;
+          mx[n][0] = fmaxf(mx[n][0], y.x);
+          mx[n][1] = fmaxf(mx[n][1], y.y);
+        }
+      }
+    // A weight may exceed 2^14 by a factor 2^1.5 (the half's range allows it) and a
+    // term of the denominator 1 by 2^60 before the references move, so that most
+    // chunks move neither them nor the sums, and the lanes need not agree.
+#pragma unroll
+    for (int n = 0; n < kNt; ++n)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float z = -INFINITY;
+#pragma unroll
+        for (int st = 0; st < 2; ++st)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            z = fmaxf(z, (s[st][n][2 * k + r] - M[n][r]) + (lvs[st][k].x - D0[n][r]));
+        rise |= z > 1.5f || mx[n][r] - M[n][r] > 60.f;
+      }
+    if (__any_sync(0xffffffffu, rise)) {
+#pragma unroll
+      for (int n = 0; n < kNt; ++n)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          float top = mx[n][r];
+#pragma unroll
+          for (int o2 = 4; o2 < 32; o2 <<= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o2));
+          const float to = fmaxf(M[n][r], top);
+          float v = -INFINITY;  // the largest s + y, from `to`
+#pragma unroll
+          for (int st = 0; st < 2; ++st)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) v = fmaxf(v, (s[st][n][2 * k + r] - to) + lvs[st][k].x);
+#pragma unroll
+          for (int o2 = 4; o2 < 32; o2 <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o2));
+          const float up = top - M[n][r], kept = D0[n][r] - (to - M[n][r]);
+          if (v - kept > 0.f || up > 60.f) {
+            const float off = fmaxf(kept, v);  // kept: the output's unit stays
+            const float down = ex2(kept - off);
+            l[n][r] *= ex2(M[n][r] - to);
+#pragma unroll
+            for (int i = 0; i < kMt; ++i) {
+              o[i][n][r] *= down;
+              o[i][n][2 + r] *= down;
+            }
+            M[n][r] = to;
+            D0[n][r] = off;
+          }
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < kNt; ++n) {
+      const float2 minus_M = make_float2(-finite_or_0(M[n][0]), -finite_or_0(M[n][1]));
+      const float2 base = make_float2(kPBits - D0[n][0], kPBits - D0[n][1]);
+      float2 sum = make_float2(l[n][0], l[n][1]);
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {
+        float2 w[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float2 y = make_float2(s[st][n][2 * k], s[st][n][2 * k + 1]);
+          const float2 t = __fadd2_rn(y, minus_M);
+          const float2 z = __fadd2_rn(t, __fadd2_rn(lvs[st][k], base));
+          sum = __fadd2_rn(sum, make_float2(ex2(t.x), ex2(t.y)));
+          w[k] = make_float2(ex2(z.x), ex2(z.y));
+          if (kEdge) {  // whatever the slot's scales are
+            if (y.x == -INFINITY) w[k].x = 0.f;
+            if (y.y == -INFINITY) w[k].y = 0.f;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int term = 0; term < kTerms; ++term) {
+            const __half2 h = __floats2half2_rn(w[k].x, w[k].y);
+            pf[term][st][n][k] = transpose8x8(*reinterpret_cast<const uint32_t*>(&h));
+            if (term + 1 < kTerms) {
+              const float2 f = __half22float2(h);
+              w[k].x -= f.x;
+              w[k].y -= f.y;
+            }
+          }
+      }
+      l[n][0] = sum.x;
+      l[n][1] = sum.y;
+    }
+  }
+
+  __device__ __forceinline__ void values(const uint8_t* stage) {
+    constexpr int kW = D / 64;       // words of a V row a lane holds
+    constexpr int kHalfT = kMt / 2;  // dims of a lane's share that are rows g: the first half
+    const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+#pragma unroll
+    for (int st = 0; st < 2; ++st) {
+      uint32_t vw[4][kW];  // slots 2t, 2t+1, 2t+8, 2t+9
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = 16 * st + 8 * (r >> 1) + 2 * t4 + (r & 1);
+        if constexpr (D == 128) {
+          const uint2 w = *reinterpret_cast<const uint2*>(stage + v_at(row, g >> 1) + 8 * (g & 1));
+          vw[r][0] = w.x, vw[r][1] = w.y;
+        } else {
+          vw[r][0] = *reinterpret_cast<const uint32_t*>(stage + v_at(row, g >> 2) + 4 * (g & 3));
+        }
+      }
+      const uint16_t* vs = scales->v[D == 128 ? g >> 1 : g >> 2] + 16 * st + 2 * t4;
+      const uint32_t sc[2] = {*reinterpret_cast<const uint32_t*>(vs),
+                              *reinterpret_cast<const uint32_t*>(vs + 8)};
+      // Halves of the slot pairs: [pair][dim of the lane's D / 8].
+      uint32_t f[2][D / 8];
+#pragma unroll
+      for (int pr = 0; pr < 2; ++pr)
+#pragma unroll
+        for (int w = 0; w < kW; ++w) {
+          const uint32_t x = vw[2 * pr][w], y = vw[2 * pr + 1][w];
+          uint32_t even[4], odd[4];
+          e2m1x8_to_half2(select_bits(0x0f0f0f0fu, x, y << 4), even);
+          e2m1x8_to_half2(select_bits(0x0f0f0f0fu, x >> 4, y), odd);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            f[pr][8 * w + 2 * k] = hmul2(even[k], sc[pr]);
+            f[pr][8 * w + 2 * k + 1] = hmul2(odd[k], sc[pr]);
+          }
+        }
+      // Row g of m-tile i is dim (D/8) g + i, row g + 8 is dim (D/8) g + D/16 + i.
+      static_assert(kHalfT * 2 == kMt && D / 16 == kMt, "");
+#pragma unroll
+      for (int i = 0; i < kMt; ++i) {
+        const uint32_t fa[4] = {f[0][i], f[0][D / 16 + i], f[1][i], f[1][D / 16 + i]};
+#pragma unroll
+        for (int term = kTerms - 1; term >= 0; --term)
+#pragma unroll
+          for (int n = 0; n < kNt; ++n)
+            mma16816(o[i][n], fa, pf[term][st][n][0], pf[term][st][n][1]);
+      }
+    }
+  }
+
+  // The warp's sums to shared memory.
+  __device__ __forceinline__ void finish(float* osum, Stat* stat) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t4 = lane & 3;
+#pragma unroll
+    for (int n = 0; n < kNt; ++n)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float sum = l[n][r];  // the lane's slots'; the maxima are the warp's
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+        const int row = warp * kTile + 8 * n + 2 * t4 + r;
+        if (g == 0) stat[row] = Stat{M[n][r], D0[n][r], sum};
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+          for (int i = 0; i < kMt; i += 4)
+            *reinterpret_cast<float4*>(osum + sum_at<D>(row, g * (D / 8) + half * (D / 16) + i)) =
+                make_float4(o[i][n][2 * half + r], o[i + 1][n][2 * half + r],
+                            o[i + 2][n][2 * half + r], o[i + 3][n][2 * half + r]);
+      }
+  }
+};
+
+// Chunks of a warp, read 32 ahead: lane l holds the place of the one l * kWarps on,
+// so that a chunk's copy never waits on the table.
+struct Ahead4 {
+  int64_t at;  // first slot's row in the pool
+  int on;
+};
+__device__ __forceinline__ Ahead4 look_ahead4(const CacheAttnArgs& a, const Entry& e, int c, int x,
+                                              int end) {
+  Ahead4 r{0, 0};
+  if (x >= end) return r;
+  const int slot = e.win0 + x * kChunk;
+  const int64_t page = cache_page(a.s, e.b, slot >> a.c.lb, a.c.n_pages, a.status);
+  if (page < 0) return r;  // recorded; page 0 is read, and nothing of it attended
+  r.at = ((page * a.c.Hkv + c) << a.c.lb) + (slot & (a.c.block - 1));
+  r.on = 1;
+  return r;
+}
+
+template <int D, class Body>
+__global__ void __launch_bounds__(kThreads, Body::kPerSm)
+    cache4_attn_kernel(const Cache4AttnArgs a) {
+  constexpr int kTile = Body::kTile, kStages = Body::kStages;
+  __shared__ uint32_t scan[kWarps];
+  __shared__ uint32_t found[2];
+  extern __shared__ __align__(128) uint8_t dyn[];
+  __shared__ Stat stat[kWarps * kTile];
+  float* osum = reinterpret_cast<float*>(dyn);
+
+  const Plan p = plan_of(a, kTile);
+  let_next_start();
+  const Scan sc = scan_entries<kWarps>(a, p, scan);
+  const uint32_t W = sc.total * p.units;
+  if (W == 0) return;
+  const Cut cut = cut_of(a, p, W);
+  if (blockIdx.x >= cut.P) return;
+  const uint32_t begin = cta_begin(cut, blockIdx.x), end = cta_begin(cut, blockIdx.x + 1);
+  // The entry that holds chunk `begin`, and its first chunk.
+  each_entry<kWarps>(a, p, sc, scan, [&](int i, uint32_t before, uint32_t n) {
+    if (begin >= before * p.units && begin < (before + n) * p.units) {
+      found[0] = i;
+      found[1] = before * p.units;
+    }
+  });
+  __syncthreads();
+  int i = static_cast<int>(found[0]);
+  uint32_t base = found[1];  // first chunk of entry i
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint8_t* ring = dyn + warp * Body::kRingBytes;
+
+  Body body;
+  for (uint32_t at = begin; at < end;) {
+    Entry e = entry_at(a, i);
+    while (at >= base + e.n_chunks * p.units) {
+      base += e.n_chunks * p.units;
+      e = entry_at(a, ++i);
+    }
+    const int u = (at - base) / static_cast<uint32_t>(e.n_chunks);
+    const uint32_t u0 = base + u * e.n_chunks;
+    const uint32_t stop = min(end, u0 + e.n_chunks);
+    const int c = u / p.n_tiles, rt = u - c * p.n_tiles;
+    // This CTA's chunks of the unit: [x0, x1) of its n_chunks; the warp's n.
+    const int x0 = static_cast<int>(at - u0), x1 = static_cast<int>(stop - u0);
+    const int n = x0 + warp < x1 ? (x1 - x0 - warp + kWarps - 1) / kWarps : 0;
+    Ahead4 ahead;
+    uint32_t on = 0;  // bit k & 31: chunk k of the 32 looked ahead to names a page
+    uint32_t on_next = 0;
+    const auto start = [&](int k) {
+      if ((k & 31) == 0) {
+        ahead = look_ahead4(a, e, c, x0 + warp + (k + lane) * kWarps, x1);
+        on = on_next;
+        on_next = __ballot_sync(0xffffffffu, ahead.on);
+      }
+      const int64_t from = __shfl_sync(0xffffffffu, ahead.at, k & 31);
+      Body::copy(a, from, ring + (k % kStages) * Body::kStageBytes);
+    };
+#pragma unroll
+    for (int k = 0; k < kStages; ++k) {
+      if (k < n) start(k);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    Body::load_rows(a, p, e, c, rt, dyn);
+    __syncthreads();
+    body.begin(dyn);
+    const int pos0 = body.rows->pos[0];  // the first row's position, the last's
+    const int pos1 = body.rows->pos[min(kTile, p.rows - rt * kTile) - 1];
+    const int all0 = pos1 - a.window + 1, all1 = pos0;  // slots that every row attends
+    for (int k = 0; k < n; ++k) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+      __syncwarp();
+      uint8_t* stage = ring + (k % kStages) * Body::kStageBytes;
+      // Chunk k was looked ahead to with the latest 32, or with those before.
+      const int newest = min(k + kStages, n) - 1;
+      const bool live = ((newest >> 5) == (k >> 5) ? on_next : on) >> (k & 31) & 1;
+      const int key0 = e.win0 + (x0 + warp + k * kWarps) * kChunk;
+      body.read_scales(stage);
+      __syncwarp();
+      body.scores(stage);
+      if (!live || key0 < all0 || key0 + kChunk - 1 > all1)
+        body.template softmax<true>(a, key0, live);
+      else
+        body.template softmax<false>(a, key0, live);
+      body.values(stage);
+      __syncwarp();
+      if (k + kStages < n) start(k + kStages);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    __syncthreads();
+    body.finish(osum, stat);
+    __syncthreads();
+    const bool whole = x0 == 0 && x1 == e.n_chunks;
+    join_warps<D, kTile>(a, p, e, c, rt, osum, stat, whole,
+                         2 * static_cast<int64_t>(blockIdx.x) + (x0 == 0));
+    __syncthreads();  // the sums make room for the next unit's chunks
+    at = stop;
+  }
+}
+
+template <int D, class Body>
+cudaError_t launch_body4(const Cache4AttnArgs& a, cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(cache4_attn_kernel<D, Body>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, Body::kSmem);
+  if (e != cudaSuccess) return e;
+  e = launch_after(cache4_attn_kernel<D, Body>, dim3(a.n_ctas), kThreads, Body::kSmem, st, false,
+                   a);
+  if (e != cudaSuccess) return e;
+  return launch_join<D, Body::kTile>(a, st);
+}
+
+template <int D>
+cudaError_t launch_d(const Cache4AttnArgs& a, cudaStream_t st) {
+  const int tile = cache4_attn_tile_rows(a.T * (a.Hq / a.c.Hkv), a.in_bf16);
+  if (!a.in_bf16)
+    return tile == 8 ? launch_body4<D, Body4<D, 1, 2>>(a, st)
+                     : launch_body4<D, Body4<D, 2, 2>>(a, st);
+  return tile == 8    ? launch_body4<D, Body4<D, 1, 1>>(a, st)
+         : tile == 16 ? launch_body4<D, Body4<D, 2, 1>>(a, st)
+                      : launch_body4<D, Body4<D, 4, 1>>(a, st);
+}
+
+}  // namespace
+
+// Tiles of 8, 16 or (bf16) 32 rows: as many as the rows fill.
+int cache4_attn_tile_rows(int rows, int in_bf16) {
+  return rows <= 8 ? 8 : rows <= 16 || !in_bf16 ? 16 : 32;
+}
+int cache4_attn_max_ctas(int tile_rows, int in_bf16) {
+  (void)in_bf16;
+  return kSms * (tile_rows == 8 ? Body4<128, 1, 1>::kPerSm : Body4<128, 2, 1>::kPerSm);
+}
+
+cudaError_t launch_cache4_attn(const Cache4AttnArgs& a, cudaStream_t st) {
+  return a.c.d == 128 ? launch_d<128>(a, st) : launch_d<64>(a, st);
+}
+
+}  // namespace msa

@@ -13,7 +13,8 @@ __all__ = ["WORKLOADS", "Workload", "generate", "sample_rows", "msa_attention",
            "compressed_attention_backward",
            "SparseLandmarkAttention", "KVCache", "KVCache4", "cache_append", "cache_attention",
            "cache_block_select", "cache_select_attention", "cache_topk_attention", "cache_evict",
-           "cache_read",
+           "cache_read", "rotary_frequencies", "qk_norm_rope", "qk_norm_rope_backward",
+           "qk_norm_rope_trainable",
            "binding"]
 
 
@@ -24,6 +25,10 @@ def __getattr__(name):
                 "compressed_attention_backward"):
         from . import api
         return getattr(api, name)
+    if name in ("rotary_frequencies", "qk_norm_rope", "qk_norm_rope_backward",
+                "qk_norm_rope_trainable"):
+        from . import rope
+        return globals().setdefault(name, getattr(rope, name))
     if name in ("KVCache", "KVCache4", "cache_read", "cache_append", "cache_attention", "cache_block_select",
                 "cache_select_attention", "cache_topk_attention", "cache_evict"):
         from . import cache

@@ -36,7 +36,8 @@ EXPORTS = ("msa_version", "msa_last_error_string", "msa_landmark_pool", "msa_att
            "msa_cache_attn_select_workspace_size", "msa_cache_attn_select",
            "msa_cache_attn_topk_workspace_size", "msa_cache_attn_topk", "msa_cache_evict",
            "msa_cache4_append", "msa_cache4_attn_workspace_size", "msa_cache4_attn",
-           "msa_cache_read", "msa_cache4_read",
+           "msa_cache_read", "msa_cache4_read", "msa_qk_norm_rope",
+           "msa_qk_norm_rope_bwd_workspace_size", "msa_qk_norm_rope_bwd",
            "msa_attn_uses_tensor_cores", "msa_attn_fwd_topk_uses_tensor_cores",
            "msa_debug_bounds_build", "msa_device_status", "msa_debug_set_wait_limit_ns",
            "msa_debug_force_single_cta", "msa_debug_set_max_clusters")
@@ -163,6 +164,15 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.msa_cache_read.restype = i32
     lib.msa_cache4_read.argtypes = [cp4, vp, i64, i64, vp, i32, vp, i32, vp, vp, i32, vp]
     lib.msa_cache4_read.restype = i32
+    lib.msa_qk_norm_rope.argtypes = [vp, i64, vp, i64, i64, i32, i32, i32, vp, vp, vp, vp, f32,
+                                     f32, i32, vp, vp, i32, i32, vp]
+    lib.msa_qk_norm_rope.restype = i32
+    lib.msa_qk_norm_rope_bwd_workspace_size.argtypes = [i64, i32, i32, i32]
+    lib.msa_qk_norm_rope_bwd_workspace_size.restype = sz
+    lib.msa_qk_norm_rope_bwd.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, i64, i32, i32, i32,
+                                         vp, vp, vp, vp, f32, f32, i32, vp, vp, vp, vp, i32, i32,
+                                         vp, sz, vp]
+    lib.msa_qk_norm_rope_bwd.restype = i32
     lib.msa_attn_uses_tensor_cores.argtypes = [i32, i32, i32, i32]
     lib.msa_attn_uses_tensor_cores.restype = i32
     lib.msa_attn_fwd_topk_uses_tensor_cores.argtypes = [i64, i32, i32, i32, i32, i32]
@@ -637,3 +647,59 @@ def cache_read(cache, bits: int, cu, max_rows: int, table, lens, k, v, stream=No
     _check(f(cache, _i32ptr(cu, "cu"), k.shape[0], int(max_rows), _i32ptr(table, "table"),
              table.shape[1], _i32ptr(lens, "lens"), table.shape[0], _addr(k), _addr(v), _dt(k),
              _raw_stream(stream)))
+
+
+# -- norms of queries and keys with rotation ---------------------------------
+
+def _tokens(t, what):
+    """Address and token stride of [n, heads, d], a token's heads next to each other."""
+    if not t.is_cuda:
+        raise ValueError("tensors must be on a CUDA device")
+    n, heads, d = t.shape
+    if heads and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d)):
+        raise ValueError(f"{what}: the heads of a token must lie next to each other")
+    return t.data_ptr(), heads * d if n <= 1 else t.stride(0)
+
+
+def _i64ptr(t, what):
+    if t.dtype != torch.int64:
+        raise TypeError(f"{what} must be int64")
+    return _addr(t)
+
+
+def _opt(t):
+    return None if t is None else _addr(t)
+
+
+def qk_norm_rope(q, k, positions, freqs, q_weight, k_weight, eps: float, mscale: float,
+                 interleaved: bool, q_out, k_out, stream=None) -> None:
+    """msa_qk_norm_rope: q [n, Hq, d], k [n, Hkv, d] into q_out, k_out."""
+    n, Hq, d = q.shape
+    w = q_weight if q_weight is not None else k_weight
+    (pq, sq), (pk, sk) = _tokens(q, "q"), _tokens(k, "k")
+    _check(_lib.msa_qk_norm_rope(pq, sq, pk, sk, n, Hq, k.shape[1], d,
+                                 _i64ptr(positions, "positions"), _i64ptr(freqs, "freqs"),
+                                 _opt(q_weight), _opt(k_weight), float(eps), float(mscale),
+                                 1 if interleaved else 0, _addr(q_out), _addr(k_out), _dt(q),
+                                 _dt(q) if w is None else _dt(w), _raw_stream(stream)))
+
+
+def qk_norm_rope_bwd_workspace_size(n: int, Hq: int, Hkv: int, d: int) -> int:
+    return _ws_size(int(_lib.msa_qk_norm_rope_bwd_workspace_size(n, Hq, Hkv, d)),
+                    "msa_qk_norm_rope_bwd")
+
+
+def qk_norm_rope_bwd(dq_out, dk_out, q, k, positions, freqs, q_weight, k_weight, eps: float,
+                     mscale: float, interleaved: bool, dq, dk, dq_weight, dk_weight, workspace,
+                     stream=None) -> None:
+    """msa_qk_norm_rope_bwd: the gradients of q, k and the weights."""
+    n, Hq, d = q.shape
+    w = q_weight if q_weight is not None else k_weight
+    (pq, sq), (pk, sk) = _tokens(q, "q"), _tokens(k, "k")
+    (gq, tq), (gk, tk) = _tokens(dq_out, "dq_out"), _tokens(dk_out, "dk_out")
+    _check(_lib.msa_qk_norm_rope_bwd(
+        gq, tq, gk, tk, pq, sq, pk, sk, n, Hq, k.shape[1], d, _i64ptr(positions, "positions"),
+        _i64ptr(freqs, "freqs"), _opt(q_weight), _opt(k_weight), float(eps), float(mscale),
+        1 if interleaved else 0, _addr(dq), _addr(dk), _opt(dq_weight), _opt(dk_weight), _dt(q),
+        _dt(q) if w is None else _dt(w), _opt(workspace),
+        0 if workspace is None else workspace.nbytes, _raw_stream(stream)))

@@ -312,10 +312,19 @@ class SparseLandmarkAttention(torch.nn.Module):
     forward(q, k, v): q [n, Hq, d] or [batch, n, Hq, d], k and v with Hkv
     heads; num_global must divide n.  Differentiable (msa_attn_bwd) for bf16
     inputs with d = 128 when gradients are required.
+
+    ``rotary`` (``rotary_frequencies``) turns the queries and keys by their
+    positions before they attend, and ``qk_norm`` norms each head of them with
+    the weights q_weight, k_weight [head_dim] before that, in one pass
+    (``qk_norm_rope``, which has ``eps``, ``interleaved`` and ``mscale``);
+    forward(..., positions=) gives the positions, [n] or [batch, n] int64, by
+    default 0 .. n - 1.
     """
 
     def __init__(self, window: int | None = None, num_global: int | None = None,
-                 scale: float | None = None):
+                 scale: float | None = None, rotary: torch.Tensor | None = None,
+                 qk_norm: bool = False, head_dim: int | None = None, eps: float = 1e-6,
+                 interleaved: bool = False, mscale: float = 1.0):
         super().__init__()
         import os
         self.window = int(os.environ.get("SPARSE_WINDOW", "4096")) if window is None else int(window)
@@ -324,17 +333,43 @@ class SparseLandmarkAttention(torch.nn.Module):
         self.scale = scale
         if self.window < 1 or self.num_global < 0:
             raise ValueError("window must be >= 1 and num_global >= 0")
+        if rotary is None and qk_norm:
+            raise ValueError("qk_norm needs rotary: the norms are part of the rotation's pass")
+        if qk_norm and (head_dim is None or head_dim < 1):
+            raise ValueError("qk_norm needs head_dim")
+        self.eps, self.interleaved, self.mscale = eps, interleaved, mscale
+        self.register_buffer("rotary", rotary, persistent=False)
+        for name in ("q_weight", "k_weight"):
+            self.register_parameter(
+                name, torch.nn.Parameter(torch.ones(head_dim)) if qk_norm else None)
 
-    def _one(self, q, k, v):
+    def _turned(self, q, k, positions):
+        from . import rope
+        if positions is None:
+            positions = torch.arange(q.shape[0], device=q.device)
+        args = (q, k, positions, self.rotary, self.q_weight, self.k_weight, self.eps,
+                self.interleaved, self.mscale)
+        needed = [x for x in (q, k, self.q_weight, self.k_weight) if x is not None]
+        if torch.is_grad_enabled() and any(x.requires_grad for x in needed):
+            return rope.qk_norm_rope_trainable(*args)
+        return rope.qk_norm_rope(*args)
+
+    def _one(self, q, k, v, positions):
         n = q.shape[0]
         if self.num_global and n % self.num_global != 0:
             raise ValueError(f"num_global={self.num_global} must divide the sequence length {n}")
+        if self.rotary is not None:
+            q, k = self._turned(q, k, positions)
         scale = 1.0 / math.sqrt(q.shape[2]) if self.scale is None else self.scale
         if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):
             return msa_attention_trainable(q, k, v, self.window, self.num_global, scale)
         return msa_attention(q, k, v, self.window, self.num_global, scale)[0]
 
-    def forward(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor) -> torch.Tensor:
+    def forward(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                positions: torch.Tensor | None = None) -> torch.Tensor:
+        if positions is not None and self.rotary is None:
+            raise ValueError("positions without rotary")
         if q.dim() == 3:
-            return self._one(q, k, v)
-        return torch.stack([self._one(q[b], k[b], v[b]) for b in range(q.shape[0])])
+            return self._one(q, k, v, positions)
+        return torch.stack([self._one(q[b], k[b], v[b], None if positions is None else positions[b])
+                            for b in range(q.shape[0])])

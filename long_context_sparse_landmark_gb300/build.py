@@ -30,7 +30,7 @@ SOURCES = ["msa_api.cu", "k1_landmark_pool.cu", "k2_attn_simt.cu", "k2_attn_tc.c
            "k2_attn_tc2.cu", "k3_lse_merge.cu", "k4_block_select.cu", "k5_global_rows.cu",
            "k6_attn_bwd.cu", "k6_bwd_dq_pair.cu", "msa_cache_api.cu", "k7_cache_write.cu",
            "k8_cache_attn.cu", "k9_cache_select.cu", "k10_cache_evict.cu", "msa_cache4_api.cu",
-           "k11_cache4_rows.cu", "k12_cache4_attn.cu"]
+           "k11_cache4_rows.cu", "k12_cache4_attn.cu", "msa_rope_api.cu", "k13_norm_rope.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
 

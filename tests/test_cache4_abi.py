@@ -112,11 +112,49 @@ def test_workspace_sizes(lib):
     assert f(cache(4), 4, 0, 1, 8, 1) == 0
     assert f(cache(4), 4, 1, 1, 7, 1) == 0
     assert 0 < f(cache(4), 1 << 14, 64, 8, 64, 1) <= 2 * 152 * 8 * 32 * (128 + 4) * 4 + 512
+    g = lib.msa_qk_norm_rope_bwd_workspace_size
+    assert g(-1, 1, 1, 128) == 0 and g(1, 0, 1, 128) == 0 and g(1, 1, 1, 96) == 0
+    assert g(1 << 20, 64, 8, 128) >= 152 * 128 * 4
+
+
+def rope(lib, **kw):
+    a = dict(q=GOOD, qs=8 * 128, k=GOOD, ks=2 * 128, n=4, hq=8, hkv=2, d=128, pos=GOOD, f=GOOD, qw=GOOD, kw=GOOD, eps=1e-6,
+             m=1.0, inter=0, qo=GOOD, ko=GOOD, dt=1, wdt=0)
+    a.update(kw)
+    return lib.msa_qk_norm_rope(a["q"], a["qs"], a["k"], a["ks"], a["n"], a["hq"], a["hkv"], a["d"], a["pos"], a["f"],
+                                a["qw"], a["kw"], a["eps"], a["m"], a["inter"], a["qo"], a["ko"], a["dt"], a["wdt"], None)
+
+
+def rope_bwd(lib, **kw):
+    a = dict(gq=GOOD, gqs=8 * 128, gk=GOOD, gks=2 * 128, q=GOOD, qs=8 * 128, k=GOOD, ks=2 * 128, n=4, hq=8, hkv=2, d=128,
+             pos=GOOD, f=GOOD, qw=GOOD, kw=GOOD, eps=1e-6, m=1.0, inter=0, qo=GOOD, ko=GOOD, dqw=GOOD, dkw=GOOD, dt=1, wdt=0,
+             ws=GOOD, bytes=1 << 40)
+    a.update(kw)
+    return lib.msa_qk_norm_rope_bwd(a["gq"], a["gqs"], a["gk"], a["gks"], a["q"], a["qs"], a["k"], a["ks"], a["n"], a["hq"],
+                                    a["hkv"], a["d"], a["pos"], a["f"], a["qw"], a["kw"], a["eps"], a["m"], a["inter"],
+                                    a["qo"], a["ko"], a["dqw"], a["dkw"], a["dt"], a["wdt"], a["ws"], a["bytes"], None)
+
+
+@pytest.mark.parametrize("call", [rope, rope_bwd])
+def test_rope_refusals(lib, call):
+    for kw, want in [(dict(q=0), INVALID), (dict(q=GOOD + 8), INVALID), (dict(k=0), INVALID), (dict(qs=8 * 128 - 8), INVALID),
+                     (dict(ks=2 * 128 + 4), INVALID), (dict(dt=0, wdt=0, ks=2 * 128 + 2), INVALID), (dict(n=-1), INVALID),
+                     (dict(n=1 << 31), INVALID), (dict(hq=0), INVALID), (dict(hkv=-1), INVALID), (dict(hq=1 << 15), INVALID),
+                     (dict(d=96), UNSUPPORTED), (dict(pos=0), INVALID), (dict(pos=GOOD + 4), INVALID), (dict(f=0), INVALID),
+                     (dict(qw=GOOD + 2), INVALID), (dict(eps=-1.0), INVALID), (dict(eps=float("inf")), INVALID),
+                     (dict(m=float("nan")), INVALID), (dict(qo=0), INVALID), (dict(ko=GOOD + 4), INVALID), (dict(dt=5), INVALID),
+                     (dict(wdt=5), INVALID)]:
+        assert call(lib, **dict(kw)) == want, kw
+    if call is rope:
+        assert rope(lib, n=0, q=0, k=0, pos=0, f=0, qo=0, ko=0) == 0
+    else:
+        for kw in (dict(gq=0), dict(gk=GOOD + 8), dict(gqs=64), dict(dqw=0), dict(dkw=GOOD + 1), dict(ws=0), dict(bytes=100)):
+            assert rope_bwd(lib, **kw) == INVALID, kw
 
 
 def test_every_entry_point_opens_an_nvtx_range():
     csrc = os.path.join(ROOT, "long_context_sparse_landmark_gb300", "csrc")
-    for header, source, n in (("msa_cache4.h", "msa_cache4_api.cu", 4),):
+    for header, source, n in (("msa_cache4.h", "msa_cache4_api.cu", 4), ("msa_rope.h", "msa_rope_api.cu", 2)):
         src = open(os.path.join(csrc, source)).read()
         declared = set(re.findall(r"^msa_status (msa_\w+)\(", open(os.path.join(ROOT, "include", header)).read(), re.M))
         assert len(declared) == n
@@ -129,6 +167,11 @@ def test_python_calls_refuse_host_tensors():
     codes, scale = torch.zeros((2, 1, 32, 32), dtype=torch.uint8), torch.zeros((2, 1, 32, 2), dtype=torch.uint8)
     with pytest.raises(ValueError, match="CUDA"):
         msa.KVCache4(codes, codes, scale, scale)
+    q = torch.zeros((2, 1, 64))
+    with pytest.raises(ValueError, match="CUDA"):
+        msa.qk_norm_rope(q, q, torch.zeros((2,), dtype=torch.int64), torch.zeros((32,), dtype=torch.int64))
+    f = msa.rotary_frequencies(64, device="cpu")
+    assert f.shape == (32,) and f[0].item() == round(2 ** 64 / (2 * 3.141592653589793))
 
 
 def test_the_reference_of_the_format():

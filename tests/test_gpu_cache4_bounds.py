@@ -18,7 +18,7 @@ def test_cache4_and_rope_tests_under_range_checks():
     build.build(debug_bounds=True)
     env = dict(os.environ, MSA_DEBUG_BOUNDS="1")
     cmd = [sys.executable, "-m", "pytest", "-q", "-x", "-p", "no:cacheprovider",
-           "-m", "gpu and not large", "tests/test_gpu_cache4.py"]
+           "-m", "gpu and not large", "tests/test_gpu_cache4.py", "tests/test_gpu_rope.py"]
     r = subprocess.run(cmd, cwd=ROOT, env=env, capture_output=True, text=True, timeout=1500)
     out = r.stdout + r.stderr
     assert r.returncode == 0, out[-3000:]

@@ -1,11 +1,10 @@
 // K11: tokens' rows and cache slots -- writing the 4-bit KV cache, and reading
 // it or the 8-bit one back.
 //
-// A row is the d values of one token and KV head; a thread takes 8 of them, so
-// a row is 16 lanes (d = 128) or 8, and a group of 32 values 4 neighbouring
-// lanes.  Writing: the group's largest magnitude m (two shuffles), its scale
-// 2^e, the least with m <= 7 * 2^e, and codes of x * 2^-e, exact but for one
-// rounding.  Reading: code * 2^e, rounded once.  Both move every byte once, and
+// A row is the d values of one token and KV head; a thread takes 16 of them, so
+// a row is 8 lanes (d = 128) or 4, and a group of 32 values 2 neighbouring
+// lanes.  Writing: the group's largest magnitude m, its scale 2^e, the least
+// with m <= 7 * 2^e, and codes of x * 2^-e, exact but for one rounding.  Reading: code * 2^e, rounded once.  Both move every byte once, and
 // HBM bounds them; a thread has kRows rows under way, K and V in CTAs of their
 // own.
 #include "cache4.cuh"
@@ -14,7 +13,7 @@ namespace msa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPer = 8;   // values a thread
+constexpr int kPer = 16;  // values a thread
 constexpr int kRows = 4;  // rows a thread
 
 // Rows (token, head) that a CTA takes.
@@ -48,18 +47,28 @@ struct Rows {
   int head[kRows];
   int64_t slot[kRows];
 
-  __device__ __forceinline__ bool find(const RowsArgs& a, int b, const Span& s, int64_t cta) {
+  __device__ __forceinline__ bool find(const RowsArgs& a, const Span& s, uint32_t cta) {
     constexpr int kLanes = D / kPer, kStep = kThreads / kLanes;
-    const int64_t row0 = cta * (kStep * kRows);
-    const int64_t t0 = row0 / a.Hkv;
+    const int64_t row0 = static_cast<int64_t>(cta) * (kStep * kRows);
+    // Most launches have fewer than 2^32 rows: one 32-bit division for the CTA.
+    const int64_t t0 = row0 >> 32 ? row0 / a.Hkv
+                                  : static_cast<uint32_t>(row0) / static_cast<uint32_t>(a.Hkv);
     if (t0 >= s.n) return false;
-    const int h0 = static_cast<int>(row0 - t0 * a.Hkv) + threadIdx.x / kLanes;
+    uint32_t h = static_cast<uint32_t>(row0 - t0 * a.Hkv) + threadIdx.x / kLanes;
+    uint32_t up = h / a.Hkv;
+    h -= up * a.Hkv;
+    int64_t t = t0 + up;
+    const int dt = kStep / a.Hkv, dh = kStep - dt * a.Hkv;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      const int x = h0 + i * kStep, up = x / a.Hkv;
-      const int64_t t = t0 + up;
       token[i] = t < s.n ? static_cast<int>(t) : -1;
-      head[i] = x - up * a.Hkv;
+      head[i] = h;
+      t += dt;
+      h += dh;
+      if (h >= static_cast<uint32_t>(a.Hkv)) {
+        h -= a.Hkv;
+        ++t;
+      }
     }
     return true;
   }
@@ -75,39 +84,93 @@ struct Rows {
   }
 };
 
-// 8 values of a row.
+// 16 values of a row, as they are in memory.
 template <bool kBf16>
-__device__ __forceinline__ void load8(const void* src, int64_t off, float* v) {
-  if constexpr (kBf16) {
-    const uint4 x = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(src) + off));
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+struct Raw;
+template <>
+struct Raw<true> {
+  uint32_t w[8];
+  __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  } else {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(src) + off);
-    const float4 x = __ldcs(p), y = __ldcs(p + 1);
-    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-    v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+    for (int i = 0; i < 8; ++i) w[i] = 0;
   }
-}
-template <bool kBf16>
-__device__ __forceinline__ void store8(void* dst, int64_t off, const float* v) {
-  if constexpr (kBf16) {
-    uint32_t w[4];
+  __device__ __forceinline__ void load(const void* src, int64_t off) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(src) + off);
+    const uint4 x = __ldcs(p), y = __ldcs(p + 1);
+    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+    w[4] = y.x, w[5] = y.y, w[6] = y.z, w[7] = y.w;
+  }
+  // The largest magnitude, as bits of a float: two halves of a word at a time.
+  __device__ __forceinline__ uint32_t max_bits() const {
+    uint32_t x = 0;
+#pragma unroll
+    for (int i = 0; i < 8; i += 2)
+      x = __vimax3_u16x2(x, w[i] & 0x7fff7fffu, w[i + 1] & 0x7fff7fffu);
+    return max(x << 16, x & 0xffff0000u);
+  }
+  // Codes of the values times inv, a power of two that leaves none above 7:
+  // exact in bf16 but for what rounds to a zero of the same sign either way.
+  __device__ __forceinline__ uint2 encode(float inv) const {
+    const __nv_bfloat162 f = __float2bfloat162_rn(inv);
+    float v[16];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]), f);
+      const uint32_t u = *reinterpret_cast<const uint32_t*>(&x);
+      v[2 * i] = __uint_as_float(u << 16);
+      v[2 * i + 1] = __uint_as_float(u & 0xffff0000u);
+    }
+    return make_uint2(floats_to_e2m1x8(v), floats_to_e2m1x8(v + 8));
+  }
+};
+template <>
+struct Raw<false> {
+  float v[16];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = 0.f;
+  }
+  __device__ __forceinline__ void load(const void* src, int64_t off) {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(src) + off);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+      const float4 x = __ldcs(p + i);
+      v[4 * i] = x.x, v[4 * i + 1] = x.y, v[4 * i + 2] = x.z, v[4 * i + 3] = x.w;
+    }
+  }
+  __device__ __forceinline__ uint32_t max_bits() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 16; i += 2)
+      m = __vimax3_u32(m, __float_as_uint(v[i]) & 0x7fffffffu,
+                       __float_as_uint(v[i + 1]) & 0x7fffffffu);
+    return m;
+  }
+  __device__ __forceinline__ uint2 encode(float inv) const {
+    float y[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) y[i] = v[i] * inv;
+    return make_uint2(floats_to_e2m1x8(y), floats_to_e2m1x8(y + 8));
+  }
+};
+
+template <bool kBf16>
+__device__ __forceinline__ void store16(void* dst, int64_t off, const float* v) {
+  if constexpr (kBf16) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
       const __nv_bfloat162 x = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
       w[i] = *reinterpret_cast<const uint32_t*>(&x);
     }
-    __stcs(reinterpret_cast<uint4*>(static_cast<uint16_t*>(dst) + off),
-           make_uint4(w[0], w[1], w[2], w[3]));
+    uint4* p = reinterpret_cast<uint4*>(static_cast<uint16_t*>(dst) + off);
+    __stcs(p, make_uint4(w[0], w[1], w[2], w[3]));
+    __stcs(p + 1, make_uint4(w[4], w[5], w[6], w[7]));
   } else {
     float4* p = reinterpret_cast<float4*>(static_cast<float*>(dst) + off);
-    __stcs(p, make_float4(v[0], v[1], v[2], v[3]));
-    __stcs(p + 1, make_float4(v[4], v[5], v[6], v[7]));
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      __stcs(p + i, make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
   }
 }
 
@@ -119,45 +182,40 @@ __global__ void __launch_bounds__(kThreads) cache4_append_kernel(const Append4Ar
   Span s;
   if (!span_of(a, b, &s)) return;
   Rows<D> rows;
-  if (!rows.find(a, b, s, blockIdx.x >> 1)) return;
+  if (!rows.find(a, s, blockIdx.x >> 1)) return;
   const int lane = threadIdx.x & (kLanes - 1);
   const void* src = kv ? a.v : a.k;
-  float v[kRows][kPer];
+  Raw<kBf16> v[kRows];
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
     const int64_t off =
         ((static_cast<int64_t>(s.r0) + max(rows.token[i], 0)) * a.Hkv + rows.head[i]) * D +
         lane * kPer;
-    if (rows.token[i] >= 0 && MSA_IN_RANGE(off, kPer, a.total * a.Hkv * D, a.status)) {
-      load8<kBf16>(src, off, v[i]);
-    } else {
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) v[i][k] = 0.f;
-    }
+    if (rows.token[i] >= 0 && MSA_IN_RANGE(off, kPer, a.total * a.Hkv * D, a.status))
+      v[i].load(src, off);
+    else
+      v[i].clear();
   }
   rows.look_up(a, b, s);
   uint8_t* codes = kv ? a.v_codes : a.k_codes;
   uint8_t* scale = kv ? a.v_scale : a.k_scale;
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) m = max(m, __float_as_uint(v[i][k]) & 0x7fffffffu);
+    uint32_t m = v[i].max_bits();
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
     // A lane of the row holds what no code stands for.
     const uint32_t bad = __ballot_sync(0xffffffffu, m > kMost4);
     const uint32_t mine = ((1u << kLanes) - 1u) << (threadIdx.x & 31 & ~(kLanes - 1));
     const bool poisoned = bad & mine;
     const int e = poisoned ? 0 : group_exponent4(m);
-    const float inv = pow2i(-e);
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) v[i][k] = poisoned ? 0.f : v[i][k] * inv;
-    const uint32_t w = floats_to_e2m1x8(v[i]);
-    if (rows.slot[i] < 0 || !MSA_IN_RANGE(rows.slot[i], 1, a.n_pages * a.Hkv << a.lb, a.status)) continue;
-    *reinterpret_cast<uint32_t*>(codes + rows.slot[i] * (D / 2) + lane * (kPer / 2)) = w;
-    if ((lane & 3) == 0)
-      scale[rows.slot[i] * (D / kGroup4) + (lane >> 2)] =
+    uint2 w = v[i].encode(pow2i(-e));
+    if (poisoned) w = make_uint2(0, 0);
+    if (rows.slot[i] < 0 ||
+        !MSA_IN_RANGE(rows.slot[i], 1, a.n_pages * a.Hkv << a.lb, a.status))
+      continue;
+    *reinterpret_cast<uint2*>(codes + rows.slot[i] * (D / 2) + lane * (kPer / 2)) = w;
+    if ((lane & 1) == 0)
+      scale[rows.slot[i] * (D / kGroup4) + (lane >> 1)] =
           static_cast<uint8_t>(poisoned ? 255 : e + 127);
   }
 }
@@ -170,24 +228,27 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReadArgs a) 
   Span s;
   if (!span_of(a, b, &s)) return;
   Rows<D> rows;
-  if (!rows.find(a, b, s, blockIdx.x >> 1)) return;
+  if (!rows.find(a, s, blockIdx.x >> 1)) return;
   rows.look_up(a, b, s);
   const int lane = threadIdx.x & (kLanes - 1);
   const uint8_t* codes = kv ? a.v_codes : a.k_codes;
   const void* scale = kv ? a.v_scale : a.k_scale;
-  uint2 w[kRows];
+  uint32_t w[kRows][kBits / 2];
   float f[kRows];
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
-    w[i] = make_uint2(0, 0);
+#pragma unroll
+    for (int k = 0; k < kBits / 2; ++k) w[i][k] = 0;
     f[i] = 0.f;
     const int64_t at = rows.slot[i];
     if (at < 0 || !MSA_IN_RANGE(at, 1, a.n_pages * a.Hkv << a.lb, a.status)) continue;
     if constexpr (kBits == 4) {
-      w[i].x = *reinterpret_cast<const uint32_t*>(codes + at * (D / 2) + lane * 4);
-      f[i] = e8m0_to_float(static_cast<const uint8_t*>(scale)[at * (D / kGroup4) + (lane >> 2)]);
+      const uint2 x = __ldcs(reinterpret_cast<const uint2*>(codes + at * (D / 2) + lane * 8));
+      w[i][0] = x.x, w[i][1] = x.y;
+      f[i] = e8m0_to_float(static_cast<const uint8_t*>(scale)[at * (D / kGroup4) + (lane >> 1)]);
     } else {
-      w[i] = *reinterpret_cast<const uint2*>(codes + at * D + lane * 8);
+      const uint4 x = __ldcs(reinterpret_cast<const uint4*>(codes + at * D + lane * 16));
+      w[i][0] = x.x, w[i][1] = x.y, w[i][2] = x.z, w[i][3] = x.w;
       f[i] = static_cast<const float*>(scale)[at >> a.lb];
     }
   }
@@ -197,23 +258,24 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReadArgs a) 
     if (rows.token[i] < 0) continue;
     float v[kPer];
     if constexpr (kBits == 4) {
-      uint32_t h[4];
-      e2m1x8_to_half2(w[i].x, h);
+      uint32_t h[8];
+      e2m1x8_to_half2(w[i][0], h);
+      e2m1x8_to_half2(w[i][1], h + 4);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < 8; ++k) {
         const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h[k]));
         v[2 * k] = x.x;
         v[2 * k + 1] = x.y;
       }
     } else {
-      e4m3x4_to_float(w[i].x, v);
-      e4m3x4_to_float(w[i].y, v + 4);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) e4m3x4_to_float(w[i][k], v + 4 * k);
     }
 #pragma unroll
     for (int k = 0; k < kPer; ++k) v[k] *= f[i];
     const int64_t off =
         ((static_cast<int64_t>(s.r0) + rows.token[i]) * a.Hkv + rows.head[i]) * D + lane * kPer;
-    if (MSA_IN_RANGE(off, kPer, a.total * a.Hkv * D, a.status)) store8<kBf16>(dst, off, v);
+    if (MSA_IN_RANGE(off, kPer, a.total * a.Hkv * D, a.status)) store16<kBf16>(dst, off, v);
   }
 }
 

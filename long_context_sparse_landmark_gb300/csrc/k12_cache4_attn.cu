@@ -55,8 +55,8 @@ __device__ __forceinline__ uint32_t slot_scales(uint32_t w, uint32_t* h) {
 template <int D, int kNt, int kTerms>
 struct Body4 {
   static constexpr int kTile = 8 * kNt;
-  static constexpr int kPerSm = kNt == 1 ? 3 : 2;
-  static constexpr int kStages = (kNt == 4 ? 4 : 3) * (D == 128 ? 1 : 2);
+  static constexpr int kPerSm = kNt * kTerms == 1 ? 4 : kNt == 1 ? 3 : 2;
+  static constexpr int kStages = (kNt == 4 ? 4 : kPerSm == 4 ? 2 : 3) * (D == 128 ? 1 : 2);
   static constexpr bool kQShared = kNt * kTerms > 2;
   static constexpr int kCodes = kChunk * D / 2, kScales = kChunk * D / kGroup4;  // of K, or of V
   static constexpr int kStageBytes = 2 * kCodes + 2 * kScales;
@@ -64,6 +64,7 @@ struct Body4 {
   static constexpr int kKs = D / 16;  // k-steps over d
   static constexpr int kMt = D / 16;  // 16-row tiles of O^T
   static constexpr int kGroups = D / kGroup4;
+  static constexpr int kUnset = -1000;
 
   // What a warp makes of a chunk's scales.
   struct Scales {
@@ -160,6 +161,15 @@ struct Body4 {
     }
   }
 
+  // What the scales are taken over by a chunk that fits (see fits()): bytes of K
+  // and V, or kUnset; and what follows from them and the references above.
+  int rk, rv;
+  float2 f[kNt];     // of a raw score, to log2 units
+  float2 base[kNt];  // added to a score: the exponent of its weight
+  float2 back[kNt];  // of a weight, to units of 2^M
+  float lvs;         // log2 of V's unit
+  bool level;        // a weight tells the denominator's term in every row
+
   const Rows* rows;
   Scales* scales;
 
@@ -167,6 +177,8 @@ struct Body4 {
     const int lane = threadIdx.x & 31, t4 = lane & 3;
     rows = &rows_of(smem);
     scales = reinterpret_cast<Scales*>(smem + kWarps * kRingBytes) + (threadIdx.x >> 5);
+    rk = rv = kUnset;
+    level = false;
 #pragma unroll
     for (int n = 0; n < kNt; ++n) {
       if constexpr (!kQShared) {
@@ -226,6 +238,73 @@ struct Body4 {
     }
   }
 
+  // Whether no scale of the chunk is above the warp's references or more than 27
+  // binades below: then code * 2^{13 - (r - x)} are halves, exactly, and the slots'
+  // own scales need no looking at.  Of a chunk that is not masked.
+  __device__ __forceinline__ bool fits(const uint8_t* stage) const {
+    const int lane = threadIdx.x & 31;
+    const uint8_t* at = stage + 2 * kCodes;
+    const uint32_t k2 = __byte_perm(rk, 0, 0x1010), v2 = __byte_perm(rv, 0, 0x1010);
+    uint32_t m;
+    if constexpr (D == 128) {
+      const uint32_t kw = reinterpret_cast<const uint32_t*>(at)[lane];
+      const uint32_t vw = reinterpret_cast<const uint32_t*>(at + kScales)[lane];
+      m = __vmaxu2(__vmaxu2(k2 - __byte_perm(kw, 0, 0x4240), k2 - __byte_perm(kw, 0, 0x4341)),
+                   __vmaxu2(v2 - __byte_perm(vw, 0, 0x4240), v2 - __byte_perm(vw, 0, 0x4341)));
+    } else {
+      const uint32_t kw = reinterpret_cast<const uint16_t*>(at)[lane];
+      const uint32_t vw = reinterpret_cast<const uint16_t*>(at + kScales)[lane];
+      m = __vmaxu2(k2 - __byte_perm(kw, 0, 0x4140), v2 - __byte_perm(vw, 0, 0x4140));
+    }
+    // (A byte above its reference leaves a borrow, and 0xff.. in its own half.)
+    return __all_sync(0xffffffffu, __vmaxu2(m, 0x001b001bu) == 0x001b001bu);
+  }
+  // References for a chunk that does not fit, with some room above its largest
+  // scales; false if there are none.
+  __device__ __forceinline__ bool refer(const uint8_t* stage) {
+    const int lane = threadIdx.x & 31;
+    uint32_t top[2];
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      const uint8_t* at = stage + 2 * kCodes + kv * kScales + lane * kGroups;
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i) m = max(m, static_cast<uint32_t>(at[i]));
+      top[kv] = __reduce_max_sync(0xffffffffu, m);
+    }
+    if (top[0] == 255 || top[1] == 255) return false;
+    const int k0 = rk, v0 = rv;
+    rk = max(top[0], 1u) + 4;
+    rv = max(top[1], 1u) + 4;
+    if (!fits(stage)) {
+      rk = k0;
+      rv = v0;
+      return false;
+    }
+    follow();
+    return true;
+  }
+  // What follows from the references.
+  __device__ __forceinline__ void follow() {
+    if (rk == kUnset) return;
+    // 2^{rk - 127} may pass a float's range by the room above: two factors.
+    const float k = pow2i(rk - 131);
+    lvs = static_cast<float>(rv) - 127.f - kTop;
+    bool in = true;
+#pragma unroll
+    for (int n = 0; n < kNt; ++n) {
+      f[n] = make_float2(qs[n][0] * 16.f * k, qs[n][1] * 16.f * k);
+      const float2 up = make_float2(kPBits + (lvs - D0[n][0]), kPBits + (lvs - D0[n][1]));
+      base[n] = make_float2(up.x - M[n][0], up.y - M[n][1]);
+      back[n] = make_float2(ex2(-up.x), ex2(-up.y));
+      // No slot yet: the first score moves the references.
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+        in &= M[n][r] == -INFINITY || lvs - D0[n][r] >= -40.f;
+    }
+    level = __all_sync(0xffffffffu, in);
+  }
+
   // A lane a slot: its scales.
   __device__ __forceinline__ void read_scales(const uint8_t* stage) {
     const int lane = threadIdx.x & 31;
@@ -259,6 +338,7 @@ struct Body4 {
 
   float s[2][kNt][4];  // [16-slot step][tile][slot g, row 2t, 2t+1; slot g + 8, ...]
 
+  template <bool kOwn>
   __device__ __forceinline__ void scores(const uint8_t* stage) {
     constexpr int kW = D / 32;  // words of a K row a lane holds, 8 dims each
     const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
@@ -274,7 +354,11 @@ struct Body4 {
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int row = 16 * st + 8 * r + g;
-        sc[st][r] = scales->k[row * kGroups + (D == 128 ? t4 : t4 >> 1)];
+        const int at = row * kGroups + (D == 128 ? t4 : t4 >> 1);
+        if constexpr (kOwn)
+          sc[st][r] = scales->k[at];
+        else  // 28 - (rk - x) as the exponent of a half, twice
+          sc[st][r] = stage[2 * kCodes + at] * 0x04000400u + (28u - rk) * 0x04000400u;
         if constexpr (D == 128) {
           const uint4 w = *reinterpret_cast<const uint4*>(stage + k_at(row, t4));
           kw[st][r][0] = w.x, kw[st][r][1] = w.y, kw[st][r][2] = w.z, kw[st][r][3] = w.w;
@@ -319,12 +403,108 @@ struct Body4 {
   // the running sums.  kEdge: some slot is masked for some row.
   uint32_t pf[kTerms][2][kNt][2];
 
+  // The warp's largest of a row's value.
+  __device__ __forceinline__ static float row_max(float x) {
+#pragma unroll
+    for (int o2 = 4; o2 < 32; o2 <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o2));
+    return x;
+  }
+  // Moves a row's references: `top` its largest score, `to` that or M, `v` the
+  // largest s + y, from `to`.
+  __device__ __forceinline__ void move(int n, int r, float top, float to, float v) {
+    const float up = top - M[n][r], kept = D0[n][r] - (to - M[n][r]);
+    if (v - kept > 0.f || up > 60.f) {
+      const float off = fmaxf(kept, v);  // kept: the output's unit stays
+      const float down = ex2(kept - off);
+      l[n][r] *= ex2(M[n][r] - to);
+#pragma unroll
+      for (int i = 0; i < kMt; ++i) {
+        o[i][n][r] *= down;
+        o[i][n][2 + r] *= down;
+      }
+      M[n][r] = to;
+      D0[n][r] = off;
+    }
+  }
+
+  __device__ __forceinline__ void put_weights(int st, int n, int k, float2 w) {
+#pragma unroll
+    for (int term = 0; term < kTerms; ++term) {
+      const __half2 h = __floats2half2_rn(w.x, w.y);
+      pf[term][st][n][k] = transpose8x8(*reinterpret_cast<const uint32_t*>(&h));
+      if (term + 1 < kTerms) {
+        const float2 x = __half22float2(h);
+        w.x -= x.x;
+        w.y -= x.y;
+      }
+    }
+  }
+
+  // Of a chunk that fits: its scores are raw, its values in one unit.
+  __device__ __forceinline__ void softmax_one() {
+    constexpr bool kKeep = kNt < 4;  // else they are computed twice: registers
+    float2 z[2][kKeep ? kNt : 1][2];
+    const auto exponents = [&] {
+      bool high = false;
+#pragma unroll
+      for (int n = 0; n < kNt; ++n) {
+        float most[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int st = 0; st < 2; ++st)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float2 y = make_float2(s[st][n][2 * k], s[st][n][2 * k + 1]);
+            const float2 x = __ffma2_rn(y, f[n], base[n]);
+            if constexpr (kKeep) z[st][n][k] = x;
+            most[0] = fmaxf(most[0], x.x);
+            most[1] = fmaxf(most[1], x.y);
+          }
+        high |= fmaxf(most[0], most[1]) > kPBits + 1.5f;
+      }
+      return high;
+    };
+    if (__any_sync(0xffffffffu, exponents())) {
+#pragma unroll
+      for (int n = 0; n < kNt; ++n)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          float mx = -INFINITY;
+#pragma unroll
+          for (int st = 0; st < 2; ++st)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              mx = fmaxf(mx, s[st][n][2 * k + r] * (r ? f[n].y : f[n].x));
+          const float top = row_max(mx), to = fmaxf(M[n][r], top);
+          move(n, r, top, to, (top - to) + lvs);
+        }
+      follow();
+      exponents();
+    }
+#pragma unroll
+    for (int n = 0; n < kNt; ++n) {
+      float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int st = 0; st < 2; ++st)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float2 x =
+              kKeep ? z[st][kKeep ? n : 0][k]
+                    : __ffma2_rn(make_float2(s[st][n][2 * k], s[st][n][2 * k + 1]), f[n], base[n]);
+          const float2 w = make_float2(ex2(x.x), ex2(x.y));
+          sum = __fadd2_rn(sum, w);
+          put_weights(st, n, k, w);
+        }
+      const float2 d = __ffma2_rn(sum, back[n], make_float2(l[n][0], l[n][1]));
+      l[n][0] = d.x;
+      l[n][1] = d.y;
+    }
+  }
+
   template <bool kEdge>
   __device__ __forceinline__ void softmax(const CacheAttnArgs& a, int key0, bool on) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     float2 lvs[2][2];  // [step][slot g, g + 8]
     float mx[kNt][2];
-    bool rise = false;
 #pragma unroll
     for (int n = 0; n < kNt; ++n) mx[n][0] = mx[n][1] = -INFINITY;
 #pragma unroll
@@ -352,88 +532,70 @@ struct Body4 {
     // A weight may exceed 2^14 by a factor 2^1.5 (the half's range allows it) and a
     // term of the denominator 1 by 2^60 before the references move, so that most
     // chunks move neither them nor the sums, and the lanes need not agree.
+    float2 z[2][kNt][2];  // exponents of the weights
+    const auto exponents = [&] {
+      bool high = false;
 #pragma unroll
-    for (int n = 0; n < kNt; ++n)
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        float z = -INFINITY;
+      for (int n = 0; n < kNt; ++n) {
+        const float2 minus_M = make_float2(-M[n][0], -M[n][1]);
+        const float2 base = make_float2(kPBits - D0[n][0], kPBits - D0[n][1]);
+        float most[2] = {-INFINITY, -INFINITY};
 #pragma unroll
         for (int st = 0; st < 2; ++st)
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
-            z = fmaxf(z, (s[st][n][2 * k + r] - M[n][r]) + (lvs[st][k].x - D0[n][r]));
-        rise |= z > 1.5f || mx[n][r] - M[n][r] > 60.f;
+          for (int k = 0; k < 2; ++k) {
+            const float2 t =
+                __fadd2_rn(make_float2(s[st][n][2 * k], s[st][n][2 * k + 1]), minus_M);
+            z[st][n][k] = __fadd2_rn(t, __fadd2_rn(lvs[st][k], base));
+            most[0] = fmaxf(most[0], z[st][n][k].x);
+            most[1] = fmaxf(most[1], z[st][n][k].y);
+          }
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          high |= most[r] > kPBits + 1.5f || mx[n][r] - M[n][r] > 60.f;
       }
-    if (__any_sync(0xffffffffu, rise)) {
+      return high;
+    };
+    if (__any_sync(0xffffffffu, exponents())) {
 #pragma unroll
       for (int n = 0; n < kNt; ++n)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          float top = mx[n][r];
-#pragma unroll
-          for (int o2 = 4; o2 < 32; o2 <<= 1)
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o2));
-          const float to = fmaxf(M[n][r], top);
+          const float top = row_max(mx[n][r]), to = fmaxf(M[n][r], top);
           float v = -INFINITY;  // the largest s + y, from `to`
 #pragma unroll
           for (int st = 0; st < 2; ++st)
 #pragma unroll
             for (int k = 0; k < 2; ++k) v = fmaxf(v, (s[st][n][2 * k + r] - to) + lvs[st][k].x);
-#pragma unroll
-          for (int o2 = 4; o2 < 32; o2 <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o2));
-          const float up = top - M[n][r], kept = D0[n][r] - (to - M[n][r]);
-          if (v - kept > 0.f || up > 60.f) {
-            const float off = fmaxf(kept, v);  // kept: the output's unit stays
-            const float down = ex2(kept - off);
-            l[n][r] *= ex2(M[n][r] - to);
-#pragma unroll
-            for (int i = 0; i < kMt; ++i) {
-              o[i][n][r] *= down;
-              o[i][n][2 + r] *= down;
-            }
-            M[n][r] = to;
-            D0[n][r] = off;
-          }
+          move(n, r, top, to, row_max(v));
         }
+      exponents();
     }
 #pragma unroll
     for (int n = 0; n < kNt; ++n) {
       const float2 minus_M = make_float2(-finite_or_0(M[n][0]), -finite_or_0(M[n][1]));
-      const float2 base = make_float2(kPBits - D0[n][0], kPBits - D0[n][1]);
       float2 sum = make_float2(l[n][0], l[n][1]);
 #pragma unroll
-      for (int st = 0; st < 2; ++st) {
-        float2 w[2];
+      for (int st = 0; st < 2; ++st)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const float2 y = make_float2(s[st][n][2 * k], s[st][n][2 * k + 1]);
           const float2 t = __fadd2_rn(y, minus_M);
-          const float2 z = __fadd2_rn(t, __fadd2_rn(lvs[st][k], base));
           sum = __fadd2_rn(sum, make_float2(ex2(t.x), ex2(t.y)));
-          w[k] = make_float2(ex2(z.x), ex2(z.y));
-          if (kEdge) {  // whatever the slot's scales are
-            if (y.x == -INFINITY) w[k].x = 0.f;
-            if (y.y == -INFINITY) w[k].y = 0.f;
+          float2 w = make_float2(ex2(z[st][n][k].x), ex2(z[st][n][k].y));
+          if (kEdge) {  // whatever the slot's scales are, and where no slot was attended yet
+            if (y.x == -INFINITY) w.x = 0.f;
+            if (y.y == -INFINITY) w.y = 0.f;
           }
+          put_weights(st, n, k, w);
         }
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-          for (int term = 0; term < kTerms; ++term) {
-            const __half2 h = __floats2half2_rn(w[k].x, w[k].y);
-            pf[term][st][n][k] = transpose8x8(*reinterpret_cast<const uint32_t*>(&h));
-            if (term + 1 < kTerms) {
-              const float2 f = __half22float2(h);
-              w[k].x -= f.x;
-              w[k].y -= f.y;
-            }
-          }
-      }
       l[n][0] = sum.x;
       l[n][1] = sum.y;
     }
+    follow();
   }
 
+  template <bool kOwn>
   __device__ __forceinline__ void values(const uint8_t* stage) {
     constexpr int kW = D / 64;       // words of a V row a lane holds
     constexpr int kHalfT = kMt / 2;  // dims of a lane's share that are rows g: the first half
@@ -451,9 +613,19 @@ struct Body4 {
           vw[r][0] = *reinterpret_cast<const uint32_t*>(stage + v_at(row, g >> 2) + 4 * (g & 3));
         }
       }
-      const uint16_t* vs = scales->v[D == 128 ? g >> 1 : g >> 2] + 16 * st + 2 * t4;
-      const uint32_t sc[2] = {*reinterpret_cast<const uint32_t*>(vs),
-                              *reinterpret_cast<const uint32_t*>(vs + 8)};
+      uint32_t sc[2];
+      if constexpr (kOwn) {
+        const uint16_t* vs = scales->v[D == 128 ? g >> 1 : g >> 2] + 16 * st + 2 * t4;
+        sc[0] = *reinterpret_cast<const uint32_t*>(vs);
+        sc[1] = *reinterpret_cast<const uint32_t*>(vs + 8);
+      } else {
+        const uint8_t* vs = stage + 2 * kCodes + kScales + (16 * st + 2 * t4) * kGroups +
+                            (D == 128 ? g >> 1 : g >> 2);
+        const uint32_t c = (28u - rv) * 0x04000400u;
+#pragma unroll
+        for (int pr = 0; pr < 2; ++pr)
+          sc[pr] = vs[8 * pr * kGroups] * 0x0400u + (vs[(8 * pr + 1) * kGroups] * 0x04000000u + c);
+      }
       // Halves of the slot pairs: [pair][dim of the lane's D / 8].
       uint32_t f[2][D / 8];
 #pragma unroll
@@ -601,14 +773,18 @@ __global__ void __launch_bounds__(kThreads, Body::kPerSm)
       const int newest = min(k + kStages, n) - 1;
       const bool live = ((newest >> 5) == (k >> 5) ? on_next : on) >> (k & 31) & 1;
       const int key0 = e.win0 + (x0 + warp + k * kWarps) * kChunk;
-      body.read_scales(stage);
-      __syncwarp();
-      body.scores(stage);
-      if (!live || key0 < all0 || key0 + kChunk - 1 > all1)
+      const bool edge = !live || key0 < all0 || key0 + kChunk - 1 > all1;
+      if (!edge && (body.fits(stage) || body.refer(stage)) && body.level) {
+        body.template scores<false>(stage);
+        body.softmax_one();
+        body.template values<false>(stage);
+      } else {
+        body.read_scales(stage);
+        __syncwarp();
+        body.template scores<true>(stage);
         body.template softmax<true>(a, key0, live);
-      else
-        body.template softmax<false>(a, key0, live);
-      body.values(stage);
+        body.template values<true>(stage);
+      }
       __syncwarp();
       if (k + kStages < n) start(k + kStages);
       asm volatile("cp.async.commit_group;" ::: "memory");
@@ -653,8 +829,9 @@ int cache4_attn_tile_rows(int rows, int in_bf16) {
   return rows <= 8 ? 8 : rows <= 16 || !in_bf16 ? 16 : 32;
 }
 int cache4_attn_max_ctas(int tile_rows, int in_bf16) {
-  (void)in_bf16;
-  return kSms * (tile_rows == 8 ? Body4<128, 1, 1>::kPerSm : Body4<128, 2, 1>::kPerSm);
+  return kSms * (tile_rows > 8 ? Body4<128, 2, 1>::kPerSm
+                 : in_bf16     ? Body4<128, 1, 1>::kPerSm
+                               : Body4<128, 1, 2>::kPerSm);
 }
 
 cudaError_t launch_cache4_attn(const Cache4AttnArgs& a, cudaStream_t st) {

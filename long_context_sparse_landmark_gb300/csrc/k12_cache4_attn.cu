@@ -34,6 +34,46 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
                             *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&x);
 }
+// Reads of shared memory at an address and a constant: one instruction each, the
+// lane's part of an address held over the chunks.
+template <int kAt>
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4 + %5];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a), "n"(kAt));
+  return v;
+}
+template <int kAt>
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2 + %3];" : "=r"(v.x), "=r"(v.y) : "r"(a), "n"(kAt));
+  return v;
+}
+template <int kAt>
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1 + %2];" : "=r"(v) : "r"(a), "n"(kAt));
+  return v;
+}
+template <int kAt>
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1 + %2];" : "=r"(v) : "r"(a), "n"(kAt));
+  return v;
+}
+// f(0), f(1), ... f(kN - 1), each with a constant.
+template <int kI>
+struct Const {
+  static constexpr int value = kI;
+};
+template <int kN, int kI = 0, typename F>
+__device__ __forceinline__ void each(F f) {
+  if constexpr (kI < kN) {
+    f(Const<kI>{});
+    each<kN, kI + 1>(f);
+  }
+}
 // Bits of m from a, the others from b.
 __device__ __forceinline__ uint32_t select_bits(uint32_t m, uint32_t a, uint32_t b) {
   return (a & m) | (b & ~m);
@@ -170,12 +210,23 @@ struct Body4 {
   float lvs;         // log2 of V's unit
   bool level;        // a weight tells the denominator's term in every row
 
+  // The lane's parts of the addresses below, from a stage's start.
+  uint32_t at_k, at_v[2], at_ks, at_vs;
+
   const Rows* rows;
   Scales* scales;
 
   __device__ __forceinline__ void begin(uint8_t* smem) {
-    const int lane = threadIdx.x & 31, t4 = lane & 3;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     rows = &rows_of(smem);
+    // Slots g (+ 8, + 16 st) of K: words t4's; slots 2 t4 + q (+ 8, + 16 st) of V: g's.
+    at_k = D == 128 ? k_at(g, t4) : k_at(g, t4 >> 1) + 8 * (t4 & 1);
+#pragma unroll
+    for (int q2 = 0; q2 < 2; ++q2)
+      at_v[q2] = D == 128 ? v_at(2 * t4 + q2, g >> 1) + 8 * (g & 1)
+                          : v_at(2 * t4 + q2, g >> 2) + 4 * (g & 3);
+    at_ks = 2 * kCodes + g * kGroups + (D == 128 ? t4 : t4 >> 1);
+    at_vs = 2 * kCodes + kScales + 2 * t4 * kGroups + (D == 128 ? g >> 1 : g >> 2);
     scales = reinterpret_cast<Scales*>(smem + kWarps * kRingBytes) + (threadIdx.x >> 5);
     rk = rv = kUnset;
     level = false;
@@ -216,66 +267,81 @@ struct Body4 {
     return kCodes + (D == 128 ? (row ^ ((row >> 1) & 1)) * 64 + ((piece ^ ((row >> 1) & 2)) << 4)
                               : (row ^ ((row >> 2) & 1)) * 32 + (piece << 4));
   }
-  // Starts the copy of the chunk whose first slot is row `at` of the pool.
-  __device__ __forceinline__ static void copy(const Cache4AttnArgs& a, int64_t at,
-                                              uint8_t* stage) {
-    constexpr int kPer = D / 32;      // pieces a row
-    constexpr int kStep = 32 / kPer;  // rows the warp copies at a time
-    const int lane = threadIdx.x & 31, piece = lane % kPer, row0 = lane / kPer;
-    if (!MSA_IN_RANGE(at, kChunk, a.c.n_pages * a.c.Hkv * a.c.block, a.status)) return;
-    const uint8_t* k = a.c.k_codes + at * (D / 2) + lane * 16;
-    const uint8_t* v = a.c.v_codes + at * (D / 2) + lane * 16;
-#pragma unroll
-    for (int i = 0; i < kChunk / kStep; ++i)
-      copy_async16(stage + k_at(row0 + i * kStep, piece), k + i * 512);
-#pragma unroll
-    for (int i = 0; i < kChunk / kStep; ++i)
-      copy_async16(stage + v_at(row0 + i * kStep, piece), v + i * 512);
+  // Starts the copy of chunk `x` of the pool (32 slots of a page and head) to `to`,
+  // the lane's place in a stage; k, v, e: the lane's place in chunk 0 of the codes
+  // and of K's or V's scales.
+  struct Place {
+    const uint8_t *k, *v, *e;
+    uint32_t to_v;  // of V's pieces, from `to`
+  };
+  __device__ __forceinline__ static Place place(const Cache4AttnArgs& a) {
     constexpr int kSp = kScales / 16;  // pieces of K's scales, and of V's
-    if (lane < 2 * kSp) {
-      const uint8_t* s = (lane < kSp ? a.k_exp : a.v_exp) + at * kGroups + (lane % kSp) * 16;
-      copy_async16(stage + 2 * kCodes + lane * 16, s);
-    }
+    const int lane = threadIdx.x & 31;
+    Place p;
+    p.k = a.c.k_codes + lane * 16;
+    p.v = a.c.v_codes + lane * 16;
+    p.e = (lane < kSp ? a.k_exp : a.v_exp) + (lane % kSp) * 16;
+    p.to_v = v_at(lane / (D / 32), lane % (D / 32)) - lane * 16;
+    return p;
+  }
+  __device__ __forceinline__ static void copy(const Cache4AttnArgs& a, const Place& p, uint32_t x,
+                                              uint32_t to) {
+    static_assert(32 * 16 % (8 * D / 2) == 0, "a warp's pieces: rows whose places are alike");
+    if (!MSA_IN_RANGE(static_cast<int64_t>(x) * kChunk, kChunk,
+                      a.c.n_pages * a.c.Hkv * a.c.block, a.status))
+      return;
+    const uint8_t* k = p.k + static_cast<uint64_t>(x) * kCodes;
+    const uint8_t* v = p.v + static_cast<uint64_t>(x) * kCodes;
+    each<kCodes / 512>([&](auto i) {
+      asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %2], 16;" ::"r"(to), "l"(k),
+                   "n"(decltype(i)::value * 512)
+                   : "memory");
+    });
+    each<kCodes / 512>([&](auto i) {
+      asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %2], 16;" ::"r"(to + p.to_v),
+                   "l"(v), "n"(decltype(i)::value * 512)
+                   : "memory");
+    });
+    if ((threadIdx.x & 31) < 2 * (kScales / 16))
+      asm volatile("cp.async.cg.shared.global [%0 + %2], [%1], 16;" ::"r"(to),
+                   "l"(p.e + static_cast<uint64_t>(x) * kScales), "n"(2 * kCodes)
+                   : "memory");
   }
 
   // Whether no scale of the chunk is above the warp's references or more than 27
   // binades below: then code * 2^{13 - (r - x)} are halves, exactly, and the slots'
   // own scales need no looking at.  Of a chunk that is not masked.
-  __device__ __forceinline__ bool fits(const uint8_t* stage) const {
-    const int lane = threadIdx.x & 31;
-    const uint8_t* at = stage + 2 * kCodes;
+  __device__ __forceinline__ bool fits(uint32_t stage) const {
+    const uint32_t at = stage + (threadIdx.x & 31) * kGroups;
     const uint32_t k2 = __byte_perm(rk, 0, 0x1010), v2 = __byte_perm(rv, 0, 0x1010);
     uint32_t m;
     if constexpr (D == 128) {
-      const uint32_t kw = reinterpret_cast<const uint32_t*>(at)[lane];
-      const uint32_t vw = reinterpret_cast<const uint32_t*>(at + kScales)[lane];
+      const uint32_t kw = lds32<2 * kCodes>(at), vw = lds32<2 * kCodes + kScales>(at);
       m = __vmaxu2(__vmaxu2(k2 - __byte_perm(kw, 0, 0x4240), k2 - __byte_perm(kw, 0, 0x4341)),
                    __vmaxu2(v2 - __byte_perm(vw, 0, 0x4240), v2 - __byte_perm(vw, 0, 0x4341)));
     } else {
-      const uint32_t kw = reinterpret_cast<const uint16_t*>(at)[lane];
-      const uint32_t vw = reinterpret_cast<const uint16_t*>(at + kScales)[lane];
-      m = __vmaxu2(k2 - __byte_perm(kw, 0, 0x4140), v2 - __byte_perm(vw, 0, 0x4140));
+      const uint32_t k0 = lds8<2 * kCodes>(at), k1 = lds8<2 * kCodes + 1>(at);
+      const uint32_t v0 = lds8<2 * kCodes + kScales>(at), v1 = lds8<2 * kCodes + kScales + 1>(at);
+      m = __vmaxu2(k2 - (k0 | k1 << 16), v2 - (v0 | v1 << 16));
     }
     // (A byte above its reference leaves a borrow, and 0xff.. in its own half.)
     return __all_sync(0xffffffffu, __vmaxu2(m, 0x001b001bu) == 0x001b001bu);
   }
   // References for a chunk that does not fit, with some room above its largest
   // scales; false if there are none.
-  __device__ __forceinline__ bool refer(const uint8_t* stage) {
-    const int lane = threadIdx.x & 31;
-    uint32_t top[2];
-#pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-      const uint8_t* at = stage + 2 * kCodes + kv * kScales + lane * kGroups;
-      uint32_t m = 0;
-#pragma unroll
-      for (int i = 0; i < kGroups; ++i) m = max(m, static_cast<uint32_t>(at[i]));
-      top[kv] = __reduce_max_sync(0xffffffffu, m);
-    }
-    if (top[0] == 255 || top[1] == 255) return false;
+  __device__ __forceinline__ bool refer(uint32_t stage) {
+    const uint32_t at = stage + (threadIdx.x & 31) * kGroups;
+    uint32_t k = 1, v = 1;
+    each<kGroups>([&](auto i) {
+      k = max(k, lds8<2 * kCodes + decltype(i)::value>(at));
+      v = max(v, lds8<2 * kCodes + kScales + decltype(i)::value>(at));
+    });
+    k = __reduce_max_sync(0xffffffffu, k);
+    v = __reduce_max_sync(0xffffffffu, v);
+    if (k == 255 || v == 255) return false;
     const int k0 = rk, v0 = rv;
-    rk = max(top[0], 1u) + 4;
-    rv = max(top[1], 1u) + 4;
+    rk = k + 4;
+    rv = v + 4;
     if (!fits(stage)) {
       rk = k0;
       rv = v0;
@@ -306,16 +372,16 @@ struct Body4 {
   }
 
   // A lane a slot: its scales.
-  __device__ __forceinline__ void read_scales(const uint8_t* stage) {
+  __device__ __forceinline__ void read_scales(uint32_t stage) {
     const int lane = threadIdx.x & 31;
-    const uint8_t* at = stage + 2 * kCodes;
+    const uint32_t at = stage + lane * kGroups;
     uint32_t kw, vw;
     if constexpr (D == 128) {
-      kw = reinterpret_cast<const uint32_t*>(at)[lane];
-      vw = reinterpret_cast<const uint32_t*>(at + kScales)[lane];
+      kw = lds32<2 * kCodes>(at);
+      vw = lds32<2 * kCodes + kScales>(at);
     } else {
-      kw = reinterpret_cast<const uint16_t*>(at)[lane];
-      vw = reinterpret_cast<const uint16_t*>(at + kScales)[lane];
+      kw = lds8<2 * kCodes>(at) | lds8<2 * kCodes + 1>(at) << 8;
+      vw = lds8<2 * kCodes + kScales>(at) | lds8<2 * kCodes + kScales + 1>(at) << 8;
     }
     uint32_t kh[2], vh[2];
     const uint32_t x = slot_scales(kw, kh), y = slot_scales(vw, vh);
@@ -339,7 +405,7 @@ struct Body4 {
   float s[2][kNt][4];  // [16-slot step][tile][slot g, row 2t, 2t+1; slot g + 8, ...]
 
   template <bool kOwn>
-  __device__ __forceinline__ void scores(const uint8_t* stage) {
+  __device__ __forceinline__ void scores(uint32_t stage) {
     constexpr int kW = D / 32;  // words of a K row a lane holds, 8 dims each
     const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
 #pragma unroll
@@ -349,24 +415,22 @@ struct Body4 {
 #pragma unroll
         for (int k = 0; k < 4; ++k) s[st][n][k] = 0.f;
     uint32_t kw[2][2][kW], sc[2][2];
-#pragma unroll
-    for (int st = 0; st < 2; ++st)
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int row = 16 * st + 8 * r + g;
-        const int at = row * kGroups + (D == 128 ? t4 : t4 >> 1);
-        if constexpr (kOwn)
-          sc[st][r] = scales->k[at];
-        else  // 28 - (rk - x) as the exponent of a half, twice
-          sc[st][r] = stage[2 * kCodes + at] * 0x04000400u + (28u - rk) * 0x04000400u;
-        if constexpr (D == 128) {
-          const uint4 w = *reinterpret_cast<const uint4*>(stage + k_at(row, t4));
-          kw[st][r][0] = w.x, kw[st][r][1] = w.y, kw[st][r][2] = w.z, kw[st][r][3] = w.w;
-        } else {
-          const uint2 w = *reinterpret_cast<const uint2*>(stage + k_at(row, t4 >> 1) + 8 * (t4 & 1));
-          kw[st][r][0] = w.x, kw[st][r][1] = w.y;
-        }
+    const uint32_t from = stage + at_k, from_s = stage + at_ks;
+    each<4>([&](auto i) {
+      constexpr int st = decltype(i)::value >> 1, r = decltype(i)::value & 1;
+      constexpr int row = 16 * st + 8 * r;
+      if constexpr (kOwn)
+        sc[st][r] = scales->k[(row + g) * kGroups + (D == 128 ? t4 : t4 >> 1)];
+      else  // 28 - (rk - x) as the exponent of a half, twice
+        sc[st][r] = lds8<row * kGroups>(from_s) * 0x04000400u + (28u - rk) * 0x04000400u;
+      if constexpr (D == 128) {
+        const uint4 w = lds128<row * (D / 2)>(from);
+        kw[st][r][0] = w.x, kw[st][r][1] = w.y, kw[st][r][2] = w.z, kw[st][r][3] = w.w;
+      } else {
+        const uint2 w = lds64<row * (D / 2)>(from);
+        kw[st][r][0] = w.x, kw[st][r][1] = w.y;
       }
+    });
 #pragma unroll
     for (int w = 0; w < kW; ++w)
 #pragma unroll
@@ -596,35 +660,35 @@ struct Body4 {
   }
 
   template <bool kOwn>
-  __device__ __forceinline__ void values(const uint8_t* stage) {
+  __device__ __forceinline__ void values(uint32_t stage) {
     constexpr int kW = D / 64;       // words of a V row a lane holds
     constexpr int kHalfT = kMt / 2;  // dims of a lane's share that are rows g: the first half
     const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
-#pragma unroll
-    for (int st = 0; st < 2; ++st) {
+    const uint32_t from[2] = {stage + at_v[0], stage + at_v[1]}, from_s = stage + at_vs;
+    each<2>([&](auto step) {
+      constexpr int st = decltype(step)::value;
       uint32_t vw[4][kW];  // slots 2t, 2t+1, 2t+8, 2t+9
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = 16 * st + 8 * (r >> 1) + 2 * t4 + (r & 1);
+      each<4>([&](auto i) {
+        constexpr int r = decltype(i)::value, row = 16 * st + 8 * (r >> 1);
         if constexpr (D == 128) {
-          const uint2 w = *reinterpret_cast<const uint2*>(stage + v_at(row, g >> 1) + 8 * (g & 1));
+          const uint2 w = lds64<row * (D / 2)>(from[r & 1]);
           vw[r][0] = w.x, vw[r][1] = w.y;
         } else {
-          vw[r][0] = *reinterpret_cast<const uint32_t*>(stage + v_at(row, g >> 2) + 4 * (g & 3));
+          vw[r][0] = lds32<row * (D / 2)>(from[r & 1]);
         }
-      }
+      });
       uint32_t sc[2];
       if constexpr (kOwn) {
         const uint16_t* vs = scales->v[D == 128 ? g >> 1 : g >> 2] + 16 * st + 2 * t4;
         sc[0] = *reinterpret_cast<const uint32_t*>(vs);
         sc[1] = *reinterpret_cast<const uint32_t*>(vs + 8);
       } else {
-        const uint8_t* vs = stage + 2 * kCodes + kScales + (16 * st + 2 * t4) * kGroups +
-                            (D == 128 ? g >> 1 : g >> 2);
         const uint32_t c = (28u - rv) * 0x04000400u;
-#pragma unroll
-        for (int pr = 0; pr < 2; ++pr)
-          sc[pr] = vs[8 * pr * kGroups] * 0x0400u + (vs[(8 * pr + 1) * kGroups] * 0x04000000u + c);
+        each<2>([&](auto i) {
+          constexpr int at = (16 * st + 8 * decltype(i)::value) * kGroups;
+          sc[decltype(i)::value] = lds8<at>(from_s) * 0x0400u +
+                                   (lds8<at + kGroups>(from_s) * 0x04000000u + c);
+        });
       }
       // Halves of the slot pairs: [pair][dim of the lane's D / 8].
       uint32_t f[2][D / 8];
@@ -653,7 +717,7 @@ struct Body4 {
           for (int n = 0; n < kNt; ++n)
             mma16816(o[i][n], fa, pf[term][st][n][0], pf[term][st][n][1]);
       }
-    }
+    });
   }
 
   // The warp's sums to shared memory.
@@ -682,7 +746,7 @@ struct Body4 {
 // Chunks of a warp, read 32 ahead: lane l holds the place of the one l * kWarps on,
 // so that a chunk's copy never waits on the table.
 struct Ahead4 {
-  int64_t at;  // first slot's row in the pool
+  uint32_t x;  // the chunk's number in the pool (136 bytes a slot: they fit)
   int on;
 };
 __device__ __forceinline__ Ahead4 look_ahead4(const CacheAttnArgs& a, const Entry& e, int c, int x,
@@ -692,7 +756,8 @@ __device__ __forceinline__ Ahead4 look_ahead4(const CacheAttnArgs& a, const Entr
   const int slot = e.win0 + x * kChunk;
   const int64_t page = cache_page(a.s, e.b, slot >> a.c.lb, a.c.n_pages, a.status);
   if (page < 0) return r;  // recorded; page 0 is read, and nothing of it attended
-  r.at = ((page * a.c.Hkv + c) << a.c.lb) + (slot & (a.c.block - 1));
+  r.x = static_cast<uint32_t>((page * a.c.Hkv + c) << (a.c.lb - kChunkLog2)) +
+        ((slot & (a.c.block - 1)) >> kChunkLog2);
   r.on = 1;
   return r;
 }
@@ -726,7 +791,10 @@ __global__ void __launch_bounds__(kThreads, Body::kPerSm)
   int i = static_cast<int>(found[0]);
   uint32_t base = found[1];  // first chunk of entry i
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint8_t* ring = dyn + warp * Body::kRingBytes;
+  const uint32_t ring =
+      static_cast<uint32_t>(__cvta_generic_to_shared(dyn)) + warp * Body::kRingBytes;
+  constexpr uint32_t kRing = Body::kRingBytes, kStage = Body::kStageBytes;
+  const typename Body::Place place = Body::place(a);
 
   Body body;
   for (uint32_t at = begin; at < end;) {
@@ -745,14 +813,15 @@ __global__ void __launch_bounds__(kThreads, Body::kPerSm)
     Ahead4 ahead;
     uint32_t on = 0;  // bit k & 31: chunk k of the 32 looked ahead to names a page
     uint32_t on_next = 0;
+    uint32_t to = ring + lane * 16;  // of the next copy
     const auto start = [&](int k) {
       if ((k & 31) == 0) {
         ahead = look_ahead4(a, e, c, x0 + warp + (k + lane) * kWarps, x1);
         on = on_next;
         on_next = __ballot_sync(0xffffffffu, ahead.on);
       }
-      const int64_t from = __shfl_sync(0xffffffffu, ahead.at, k & 31);
-      Body::copy(a, from, ring + (k % kStages) * Body::kStageBytes);
+      Body::copy(a, place, __shfl_sync(0xffffffffu, ahead.x, k & 31), to);
+      to = to == ring + lane * 16 + (kRing - kStage) ? ring + lane * 16 : to + kStage;
     };
 #pragma unroll
     for (int k = 0; k < kStages; ++k) {
@@ -764,16 +833,17 @@ __global__ void __launch_bounds__(kThreads, Body::kPerSm)
     body.begin(dyn);
     const int pos0 = body.rows->pos[0];  // the first row's position, the last's
     const int pos1 = body.rows->pos[min(kTile, p.rows - rt * kTile) - 1];
-    const int all0 = pos1 - a.window + 1, all1 = pos0;  // slots that every row attends
-    for (int k = 0; k < n; ++k) {
+    // Slots that every row attends, as first slots of chunks that lie in them.
+    const int all0 = pos1 - a.window + 1, all1 = pos0 - (kChunk - 1);
+    uint32_t stage = ring;
+    int key0 = e.win0 + (x0 + warp) * kChunk;
+    for (int k = 0; k < n; ++k, key0 += kWarps * kChunk) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
       __syncwarp();
-      uint8_t* stage = ring + (k % kStages) * Body::kStageBytes;
       // Chunk k was looked ahead to with the latest 32, or with those before.
       const int newest = min(k + kStages, n) - 1;
       const bool live = ((newest >> 5) == (k >> 5) ? on_next : on) >> (k & 31) & 1;
-      const int key0 = e.win0 + (x0 + warp + k * kWarps) * kChunk;
-      const bool edge = !live || key0 < all0 || key0 + kChunk - 1 > all1;
+      const bool edge = !live || key0 < all0 || key0 > all1;
       if (!edge && (body.fits(stage) || body.refer(stage)) && body.level) {
         body.template scores<false>(stage);
         body.softmax_one();
@@ -786,6 +856,7 @@ __global__ void __launch_bounds__(kThreads, Body::kPerSm)
         body.template values<true>(stage);
       }
       __syncwarp();
+      stage = stage == ring + (kRing - kStage) ? ring : stage + kStage;
       if (k + kStages < n) start(k + kStages);
       asm volatile("cp.async.commit_group;" ::: "memory");
     }

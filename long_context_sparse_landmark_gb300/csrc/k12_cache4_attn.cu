@@ -74,9 +74,12 @@ __device__ __forceinline__ void each(F f) {
     each<kN, kI + 1>(f);
   }
 }
-// Bits of m from a, the others from b.
+// Bits of m from a, the others from b: one instruction, which the compiler does
+// not find behind a shift.
 __device__ __forceinline__ uint32_t select_bits(uint32_t m, uint32_t a, uint32_t b) {
-  return (a & m) | (b & ~m);
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xca;" : "=r"(r) : "r"(m), "r"(a), "r"(b));
+  return r;
 }
 
 // Scales of a slot (bytes of w) as halves 2^{13 - delta} below the largest, which
@@ -751,14 +754,16 @@ struct Ahead4 {
 };
 __device__ __forceinline__ Ahead4 look_ahead4(const CacheAttnArgs& a, const Entry& e, int c, int x,
                                               int end) {
-  Ahead4 r{0, 0};
+  Ahead4 r{0, 1};
   if (x >= end) return r;
   const int slot = e.win0 + x * kChunk;
   const int64_t page = cache_page(a.s, e.b, slot >> a.c.lb, a.c.n_pages, a.status);
-  if (page < 0) return r;  // recorded; page 0 is read, and nothing of it attended
+  if (page < 0) {  // recorded; page 0 is read, and nothing of it attended
+    r.on = 0;
+    return r;
+  }
   r.x = static_cast<uint32_t>((page * a.c.Hkv + c) << (a.c.lb - kChunkLog2)) +
         ((slot & (a.c.block - 1)) >> kChunkLog2);
-  r.on = 1;
   return r;
 }
 
@@ -811,21 +816,18 @@ __global__ void __launch_bounds__(kThreads, Body::kPerSm)
     const int x0 = static_cast<int>(at - u0), x1 = static_cast<int>(stop - u0);
     const int n = x0 + warp < x1 ? (x1 - x0 - warp + kWarps - 1) / kWarps : 0;
     Ahead4 ahead;
-    uint32_t on = 0;  // bit k & 31: chunk k of the 32 looked ahead to names a page
-    uint32_t on_next = 0;
-    uint32_t to = ring + lane * 16;  // of the next copy
-    const auto start = [&](int k) {
+    uint32_t dead[2] = {0, 0};  // of the last 64 chunks looked ahead to: bits of those off
+    const auto start = [&](int k, uint32_t to) {
       if ((k & 31) == 0) {
         ahead = look_ahead4(a, e, c, x0 + warp + (k + lane) * kWarps, x1);
-        on = on_next;
-        on_next = __ballot_sync(0xffffffffu, ahead.on);
+        dead[0] = dead[1];
+        dead[1] = __ballot_sync(0xffffffffu, !ahead.on);
       }
-      Body::copy(a, place, __shfl_sync(0xffffffffu, ahead.x, k & 31), to);
-      to = to == ring + lane * 16 + (kRing - kStage) ? ring + lane * 16 : to + kStage;
+      Body::copy(a, place, __shfl_sync(0xffffffffu, ahead.x, k & 31), to + lane * 16);
     };
 #pragma unroll
     for (int k = 0; k < kStages; ++k) {
-      if (k < n) start(k);
+      if (k < n) start(k, ring + k * kStage);
       asm volatile("cp.async.commit_group;" ::: "memory");
     }
     Body::load_rows(a, p, e, c, rt, dyn);
@@ -840,9 +842,12 @@ __global__ void __launch_bounds__(kThreads, Body::kPerSm)
     for (int k = 0; k < n; ++k, key0 += kWarps * kChunk) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
       __syncwarp();
-      // Chunk k was looked ahead to with the latest 32, or with those before.
-      const int newest = min(k + kStages, n) - 1;
-      const bool live = ((newest >> 5) == (k >> 5) ? on_next : on) >> (k & 31) & 1;
+      bool live = true;
+      if (dead[0] | dead[1]) {
+        // Chunk k was looked ahead to with the latest 32, or with those before.
+        const int newest = min(k + kStages, n) - 1;
+        live = !(((newest >> 5) == (k >> 5) ? dead[1] : dead[0]) >> (k & 31) & 1);
+      }
       const bool edge = !live || key0 < all0 || key0 > all1;
       if (!edge && (body.fits(stage) || body.refer(stage)) && body.level) {
         body.template scores<false>(stage);
@@ -856,9 +861,12 @@ __global__ void __launch_bounds__(kThreads, Body::kPerSm)
         body.template values<true>(stage);
       }
       __syncwarp();
-      stage = stage == ring + (kRing - kStage) ? ring : stage + kStage;
-      if (k + kStages < n) start(k + kStages);
+      if (k + kStages < n) start(k + kStages, stage);
       asm volatile("cp.async.commit_group;" ::: "memory");
+      if constexpr (kStages == 2)
+        stage = 2 * ring + kStage - stage;
+      else
+        stage = stage == ring + (kRing - kStage) ? ring : stage + kStage;
     }
     __syncthreads();
     body.finish(osum, stat);

@@ -98,11 +98,15 @@ __device__ __forceinline__ uint32_t slot_scales(uint32_t w, uint32_t* h) {
 template <int D, int kNt, int kTerms>
 struct Body4 {
   static constexpr int kTile = 8 * kNt;
-  static constexpr int kPerSm = kNt * kTerms == 1 ? 4 : kNt == 1 ? 3 : 2;
-  static constexpr int kStages = (kNt == 4 ? 4 : kPerSm == 4 ? 2 : 3) * (D == 128 ? 1 : 2);
+  static constexpr int kPerSm = kNt == 1 ? 3 : 2;
+  // Chunks that a warp takes together: two, where the registers allow it, so that
+  // one's fixed latencies pass in the other's shadow.
+  static constexpr int kPair = kNt * kTerms == 1 ? 2 : 1;
+  static constexpr int kStages = (kPair == 2 || kNt == 4 ? 4 : 3) / kPair * (D == 128 ? 1 : 2);  // pairs
   static constexpr bool kQShared = kNt * kTerms > 2;
   static constexpr int kCodes = kChunk * D / 2, kScales = kChunk * D / kGroup4;  // of K, or of V
-  static constexpr int kStageBytes = 2 * kCodes + 2 * kScales;
+  static constexpr int kChunkBytes = 2 * kCodes + 2 * kScales;
+  static constexpr int kStageBytes = kPair * kChunkBytes;
   static constexpr int kRingBytes = kStages * kStageBytes;
   static constexpr int kKs = D / 16;  // k-steps over d
   static constexpr int kMt = D / 16;  // 16-row tiles of O^T
@@ -111,7 +115,7 @@ struct Body4 {
 
   // What a warp makes of a chunk's scales.
   struct Scales {
-    float4 slot[kChunk];              // 2^x, twice, and y, twice
+    float2 slot[kChunk];              // 2^x, and y
     uint32_t k[kChunk * kGroups];     // half 2^{13 - delta}, twice: [slot][group]
     uint16_t v[kGroups][40];          // the half: [group][slot], rows 80 bytes apart
   };
@@ -311,33 +315,37 @@ struct Body4 {
                    : "memory");
   }
 
-  // Whether no scale of the chunk is above the warp's references or more than 27
+  // Whether no scale of the pair is above the warp's references or more than 27
   // binades below: then code * 2^{13 - (r - x)} are halves, exactly, and the slots'
-  // own scales need no looking at.  Of a chunk that is not masked.
+  // own scales need no looking at.  Of chunks that are not masked.
   __device__ __forceinline__ bool fits(uint32_t stage) const {
     const uint32_t at = stage + (threadIdx.x & 31) * kGroups;
     const uint32_t k2 = __byte_perm(rk, 0, 0x1010), v2 = __byte_perm(rv, 0, 0x1010);
-    uint32_t m;
-    if constexpr (D == 128) {
-      const uint32_t kw = lds32<2 * kCodes>(at), vw = lds32<2 * kCodes + kScales>(at);
-      m = __vmaxu2(__vmaxu2(k2 - __byte_perm(kw, 0, 0x4240), k2 - __byte_perm(kw, 0, 0x4341)),
-                   __vmaxu2(v2 - __byte_perm(vw, 0, 0x4240), v2 - __byte_perm(vw, 0, 0x4341)));
-    } else {
-      const uint32_t k0 = lds8<2 * kCodes>(at), k1 = lds8<2 * kCodes + 1>(at);
-      const uint32_t v0 = lds8<2 * kCodes + kScales>(at), v1 = lds8<2 * kCodes + kScales + 1>(at);
-      m = __vmaxu2(k2 - (k0 | k1 << 16), v2 - (v0 | v1 << 16));
-    }
+    uint32_t m = 0;
+    each<kPair>([&](auto c) {
+      constexpr int k_from = decltype(c)::value * kChunkBytes + 2 * kCodes, v_from = k_from + kScales;
+      if constexpr (D == 128) {
+        const uint32_t kw = lds32<k_from>(at), vw = lds32<v_from>(at);
+        m = __vimax3_u16x2(m, k2 - __byte_perm(kw, 0, 0x4240), k2 - __byte_perm(kw, 0, 0x4341));
+        m = __vimax3_u16x2(m, v2 - __byte_perm(vw, 0, 0x4240), v2 - __byte_perm(vw, 0, 0x4341));
+      } else {
+        const uint32_t k0 = lds8<k_from>(at), k1 = lds8<k_from + 1>(at);
+        const uint32_t v0 = lds8<v_from>(at), v1 = lds8<v_from + 1>(at);
+        m = __vimax3_u16x2(m, k2 - (k0 | k1 << 16), v2 - (v0 | v1 << 16));
+      }
+    });
     // (A byte above its reference leaves a borrow, and 0xff.. in its own half.)
     return __all_sync(0xffffffffu, __vmaxu2(m, 0x001b001bu) == 0x001b001bu);
   }
-  // References for a chunk that does not fit, with some room above its largest
+  // References for a pair that does not fit, with some room above its largest
   // scales; false if there are none.
   __device__ __forceinline__ bool refer(uint32_t stage) {
     const uint32_t at = stage + (threadIdx.x & 31) * kGroups;
     uint32_t k = 1, v = 1;
-    each<kGroups>([&](auto i) {
-      k = max(k, lds8<2 * kCodes + decltype(i)::value>(at));
-      v = max(v, lds8<2 * kCodes + kScales + decltype(i)::value>(at));
+    each<kPair * kGroups>([&](auto i) {
+      constexpr int c = decltype(i)::value / kGroups, j = decltype(i)::value % kGroups;
+      k = max(k, lds8<c * kChunkBytes + 2 * kCodes + j>(at));
+      v = max(v, lds8<c * kChunkBytes + 2 * kCodes + kScales + j>(at));
     });
     k = __reduce_max_sync(0xffffffffu, k);
     v = __reduce_max_sync(0xffffffffu, v);
@@ -390,7 +398,7 @@ struct Body4 {
     const uint32_t x = slot_scales(kw, kh), y = slot_scales(vw, vh);
     const float ks = e8m0_to_float(x);
     const float lvs = y == 255 ? __uint_as_float(0x7fc00000u) : static_cast<float>(y) - 127.f - kTop;
-    scales->slot[lane] = make_float4(ks, ks, lvs, lvs);
+    scales->slot[lane] = make_float2(ks, lvs);
     if constexpr (D == 128) {
       reinterpret_cast<uint4*>(scales->k)[lane] =
           make_uint4(__byte_perm(kh[0], 0, 0x1010), __byte_perm(kh[1], 0, 0x1010),
@@ -405,9 +413,10 @@ struct Body4 {
     scales->v[1][lane] = static_cast<uint16_t>(vh[1]);
   }
 
-  float s[2][kNt][4];  // [16-slot step][tile][slot g, row 2t, 2t+1; slot g + 8, ...]
+  float s[2 * kPair][kNt][4];  // [16-slot step][tile][slot g, row 2t, 2t+1; slot g + 8, ...]
 
-  template <bool kOwn>
+  // Raw scores of the chunk at `stage`, the kC-th of a pair.
+  template <bool kOwn, int kC>
   __device__ __forceinline__ void scores(uint32_t stage) {
     constexpr int kW = D / 32;  // words of a K row a lane holds, 8 dims each
     const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
@@ -416,7 +425,7 @@ struct Body4 {
 #pragma unroll
       for (int n = 0; n < kNt; ++n)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) s[st][n][k] = 0.f;
+        for (int k = 0; k < 4; ++k) s[2 * kC + st][n][k] = 0.f;
     uint32_t kw[2][2][kW], sc[2][2];
     const uint32_t from = stage + at_k, from_s = stage + at_ks;
     each<4>([&](auto i) {
@@ -460,7 +469,7 @@ struct Body4 {
               } else {
                 b0 = q[term][ks][n][0], b1 = q[term][ks][n][1];
               }
-              mma16816(s[st][n], fa, b0, b1);
+              mma16816(s[2 * kC + st][n], fa, b0, b1);
             }
         }
       }
@@ -468,7 +477,7 @@ struct Body4 {
 
   // Softmax of the chunk's scores into halves pf[term][step][tile][b0, b1], and
   // the running sums.  kEdge: some slot is masked for some row.
-  uint32_t pf[kTerms][2][kNt][2];
+  uint32_t pf[kTerms][2 * kPair][kNt][2];
 
   // The warp's largest of a row's value.
   __device__ __forceinline__ static float row_max(float x) {
@@ -507,17 +516,17 @@ struct Body4 {
     }
   }
 
-  // Of a chunk that fits: its scores are raw, its values in one unit.
+  // Of a pair that fits: its scores are raw, its values in one unit.
   __device__ __forceinline__ void softmax_one() {
     constexpr bool kKeep = kNt < 4;  // else they are computed twice: registers
-    float2 z[2][kKeep ? kNt : 1][2];
+    float2 z[2 * kPair][kKeep ? kNt : 1][2];
     const auto exponents = [&] {
       bool high = false;
 #pragma unroll
       for (int n = 0; n < kNt; ++n) {
         float most[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int st = 0; st < 2; ++st)
+        for (int st = 0; st < 2 * kPair; ++st)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const float2 y = make_float2(s[st][n][2 * k], s[st][n][2 * k + 1]);
@@ -537,7 +546,7 @@ struct Body4 {
         for (int r = 0; r < 2; ++r) {
           float mx = -INFINITY;
 #pragma unroll
-          for (int st = 0; st < 2; ++st)
+          for (int st = 0; st < 2 * kPair; ++st)
 #pragma unroll
             for (int k = 0; k < 2; ++k)
               mx = fmaxf(mx, s[st][n][2 * k + r] * (r ? f[n].y : f[n].x));
@@ -551,7 +560,7 @@ struct Body4 {
     for (int n = 0; n < kNt; ++n) {
       float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int st = 0; st < 2; ++st)
+      for (int st = 0; st < 2 * kPair; ++st)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const float2 x =
@@ -578,11 +587,11 @@ struct Body4 {
     for (int st = 0; st < 2; ++st)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const float4 of = scales->slot[16 * st + 8 * k + g];
-        lvs[st][k] = make_float2(of.z, of.w);
+        const float2 of = scales->slot[16 * st + 8 * k + g];
+        lvs[st][k] = make_float2(of.y, of.y);
 #pragma unroll
         for (int n = 0; n < kNt; ++n) {
-          const float2 f = __fmul2_rn(make_float2(qs[n][0], qs[n][1]), make_float2(of.x, of.y));
+          const float2 f = __fmul2_rn(make_float2(qs[n][0], qs[n][1]), make_float2(of.x, of.x));
           float2 y = __fmul2_rn(make_float2(s[st][n][2 * k], s[st][n][2 * k + 1]), f);
           if (kEdge) {
             const int key = key0 + 16 * st + 8 * k + g;
@@ -662,7 +671,7 @@ struct Body4 {
     follow();
   }
 
-  template <bool kOwn>
+  template <bool kOwn, int kC>
   __device__ __forceinline__ void values(uint32_t stage) {
     constexpr int kW = D / 64;       // words of a V row a lane holds
     constexpr int kHalfT = kMt / 2;  // dims of a lane's share that are rows g: the first half
@@ -718,7 +727,7 @@ struct Body4 {
         for (int term = kTerms - 1; term >= 0; --term)
 #pragma unroll
           for (int n = 0; n < kNt; ++n)
-            mma16816(o[i][n], fa, pf[term][st][n][0], pf[term][st][n][1]);
+            mma16816(o[i][n], fa, pf[term][2 * kC + st][n][0], pf[term][2 * kC + st][n][1]);
       }
     });
   }
@@ -746,31 +755,21 @@ struct Body4 {
   }
 };
 
-// Chunks of a warp, read 32 ahead: lane l holds the place of the one l * kWarps on,
-// so that a chunk's copy never waits on the table.
-struct Ahead4 {
-  uint32_t x;  // the chunk's number in the pool (136 bytes a slot: they fit)
-  int on;
-};
-__device__ __forceinline__ Ahead4 look_ahead4(const CacheAttnArgs& a, const Entry& e, int c, int x,
-                                              int end) {
-  Ahead4 r{0, 1};
-  if (x >= end) return r;
+// Number in the pool of a unit's chunk x (136 bytes a slot: it fits 32 bits), or
+// kNoPage, which reads page 0 and attends nothing of it.
+constexpr uint32_t kNoPage = 0xffffffffu;
+__device__ __forceinline__ uint32_t chunk_at(const CacheAttnArgs& a, const Entry& e, int c, int x) {
   const int slot = e.win0 + x * kChunk;
   const int64_t page = cache_page(a.s, e.b, slot >> a.c.lb, a.c.n_pages, a.status);
-  if (page < 0) {  // recorded; page 0 is read, and nothing of it attended
-    r.on = 0;
-    return r;
-  }
-  r.x = static_cast<uint32_t>((page * a.c.Hkv + c) << (a.c.lb - kChunkLog2)) +
-        ((slot & (a.c.block - 1)) >> kChunkLog2);
-  return r;
+  if (page < 0) return kNoPage;  // recorded
+  return static_cast<uint32_t>((page * a.c.Hkv + c) << (a.c.lb - kChunkLog2)) +
+         ((slot & (a.c.block - 1)) >> kChunkLog2);
 }
 
 template <int D, class Body>
 __global__ void __launch_bounds__(kThreads, Body::kPerSm)
     cache4_attn_kernel(const Cache4AttnArgs a) {
-  constexpr int kTile = Body::kTile, kStages = Body::kStages;
+  constexpr int kTile = Body::kTile, kStages = Body::kStages, kPair = Body::kPair;
   __shared__ uint32_t scan[kWarps];
   __shared__ uint32_t found[2];
   extern __shared__ __align__(128) uint8_t dyn[];
@@ -812,18 +811,33 @@ __global__ void __launch_bounds__(kThreads, Body::kPerSm)
     const uint32_t u0 = base + u * e.n_chunks;
     const uint32_t stop = min(end, u0 + e.n_chunks);
     const int c = u / p.n_tiles, rt = u - c * p.n_tiles;
-    // This CTA's chunks of the unit: [x0, x1) of its n_chunks; the warp's n.
+    // This CTA's chunks of the unit: [x0, x1) of its n_chunks; the warp's n pairs of
+    // them, every kWarps-th from `mine` on, the last of all perhaps of one.
     const int x0 = static_cast<int>(at - u0), x1 = static_cast<int>(stop - u0);
-    const int n = x0 + warp < x1 ? (x1 - x0 - warp + kWarps - 1) / kWarps : 0;
-    Ahead4 ahead;
-    uint32_t dead[2] = {0, 0};  // of the last 64 chunks looked ahead to: bits of those off
+    const int mine = x0 + warp * kPair;
+    const int n = mine < x1 ? (x1 - mine + kWarps * kPair - 1) / (kWarps * kPair) : 0;
+    // Pairs are looked up 32 ahead, a lane each, so that a copy never waits on the
+    // table.
+    uint32_t ahead[kPair];
+    uint32_t dead[kPair][2];  // of the last 64 looked up, the chunks without a page
+#pragma unroll
+    for (int i = 0; i < kPair; ++i) dead[i][0] = dead[i][1] = 0;
     const auto start = [&](int k, uint32_t to) {
       if ((k & 31) == 0) {
-        ahead = look_ahead4(a, e, c, x0 + warp + (k + lane) * kWarps, x1);
-        dead[0] = dead[1];
-        dead[1] = __ballot_sync(0xffffffffu, !ahead.on);
+#pragma unroll
+        for (int i = 0; i < kPair; ++i) {
+          const int x = mine + (k + lane) * kWarps * kPair + i;
+          ahead[i] = x < x1 ? chunk_at(a, e, c, x) : 0;
+          dead[i][0] = dead[i][1];
+          dead[i][1] = __ballot_sync(0xffffffffu, ahead[i] == kNoPage);
+          if (ahead[i] == kNoPage) ahead[i] = 0;
+        }
       }
-      Body::copy(a, place, __shfl_sync(0xffffffffu, ahead.x, k & 31), to + lane * 16);
+#pragma unroll
+      for (int i = 0; i < kPair; ++i)
+        if (i == 0 || mine + k * kWarps * kPair + i < x1)
+          Body::copy(a, place, __shfl_sync(0xffffffffu, ahead[i], k & 31),
+                     to + i * Body::kChunkBytes + lane * 16);
     };
 #pragma unroll
     for (int k = 0; k < kStages; ++k) {
@@ -835,30 +849,44 @@ __global__ void __launch_bounds__(kThreads, Body::kPerSm)
     body.begin(dyn);
     const int pos0 = body.rows->pos[0];  // the first row's position, the last's
     const int pos1 = body.rows->pos[min(kTile, p.rows - rt * kTile) - 1];
-    // Slots that every row attends, as first slots of chunks that lie in them.
-    const int all0 = pos1 - a.window + 1, all1 = pos0 - (kChunk - 1);
+    // Slots that every row attends, as first slots of pairs that lie in them.
+    const int all0 = pos1 - a.window + 1, all1 = pos0 - (kPair * kChunk - 1);
     uint32_t stage = ring;
-    int key0 = e.win0 + (x0 + warp) * kChunk;
-    for (int k = 0; k < n; ++k, key0 += kWarps * kChunk) {
+    int key0 = e.win0 + mine * kChunk;
+    int x = mine;
+    for (int k = 0; k < n; ++k, key0 += kWarps * kPair * kChunk, x += kWarps * kPair) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
       __syncwarp();
-      bool live = true;
-      if (dead[0] | dead[1]) {
-        // Chunk k was looked ahead to with the latest 32, or with those before.
-        const int newest = min(k + kStages, n) - 1;
-        live = !(((newest >> 5) == (k >> 5) ? dead[1] : dead[0]) >> (k & 31) & 1);
-      }
-      const bool edge = !live || key0 < all0 || key0 > all1;
+      // Pair k was looked up with the latest 32, or with those before.
+      uint32_t off = 0;
+#pragma unroll
+      for (int i = 0; i < kPair; ++i) off |= dead[i][0] | dead[i][1];
+      const bool edge = off || key0 < all0 || key0 > all1 || x + kPair > x1;
       if (!edge && (body.fits(stage) || body.refer(stage)) && body.level) {
-        body.template scores<false>(stage);
+        each<kPair>([&](auto i) {
+          body.template scores<false, decltype(i)::value>(stage + decltype(i)::value *
+                                                                      Body::kChunkBytes);
+        });
         body.softmax_one();
-        body.template values<false>(stage);
+        each<kPair>([&](auto i) {
+          body.template values<false, decltype(i)::value>(stage + decltype(i)::value *
+                                                                      Body::kChunkBytes);
+        });
       } else {
-        body.read_scales(stage);
-        __syncwarp();
-        body.template scores<true>(stage);
-        body.template softmax<true>(a, key0, live);
-        body.template values<true>(stage);
+#pragma unroll 1
+        for (int i = 0; i < min(kPair, x1 - x); ++i) {
+          const int newest = min(k + kStages, n) - 1;
+          const bool now = (newest >> 5) == (k >> 5);
+          const uint32_t d = i == 0 ? (now ? dead[0][1] : dead[0][0]) : (now ? dead[kPair - 1][1] : dead[kPair - 1][0]);
+          const bool live = !(d >> (k & 31) & 1);
+          const uint32_t from = stage + i * Body::kChunkBytes;
+          body.read_scales(from);
+          __syncwarp();
+          body.template scores<true, 0>(from);
+          body.template softmax<true>(a, key0 + i * kChunk, live);
+          body.template values<true, 0>(from);
+          __syncwarp();
+        }
       }
       __syncwarp();
       if (k + kStages < n) start(k + kStages, stage);
@@ -908,9 +936,8 @@ int cache4_attn_tile_rows(int rows, int in_bf16) {
   return rows <= 8 ? 8 : rows <= 16 || !in_bf16 ? 16 : 32;
 }
 int cache4_attn_max_ctas(int tile_rows, int in_bf16) {
-  return kSms * (tile_rows > 8 ? Body4<128, 2, 1>::kPerSm
-                 : in_bf16     ? Body4<128, 1, 1>::kPerSm
-                               : Body4<128, 1, 2>::kPerSm);
+  (void)in_bf16;
+  return kSms * (tile_rows == 8 ? Body4<128, 1, 1>::kPerSm : Body4<128, 2, 1>::kPerSm);
 }
 
 cudaError_t launch_cache4_attn(const Cache4AttnArgs& a, cudaStream_t st) {

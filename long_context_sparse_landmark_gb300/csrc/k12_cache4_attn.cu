@@ -118,6 +118,7 @@ struct Body4 {
     float2 slot[kChunk];              // 2^x, and y
     uint32_t k[kChunk * kGroups];     // half 2^{13 - delta}, twice: [slot][group]
     uint16_t v[kGroups][40];          // the half: [group][slot], rows 80 bytes apart
+    float refs[kNt == 4 ? 4 * kNt * 32 : 4];  // see M() below
   };
   // Rows of a unit, for all warps: their fragments [term][k-step][tile][lane],
   // score scales and positions.
@@ -132,9 +133,34 @@ struct Body4 {
   static_assert(sizeof(Scales) % 16 == 0 && kStageBytes % 16 == 0, "16-byte pieces");
 
   uint32_t q[kTerms][kQShared ? 1 : kKs][kQShared ? 1 : kNt][2];
-  float qs[kNt][2];  // score scale of rows 2t, 2t+1 (log2 units)
   float o[kMt][kNt][4];
-  float l[kNt][2], M[kNt][2], D0[kNt][2];  // l in units of 2^M, o of 2^{M + D0 - kPBits}
+  float l[kNt][2];  // in units of 2^M, o of 2^{M + D0 - kPBits}
+  // M and D0 of rows 2t, 2t+1: looked at where a reference moves or a chunk does not
+  // fit.  Those of four tiles are in shared memory (registers: 304 spilled bytes).
+  static constexpr bool kCold = kNt == 4;
+  struct Refs {
+    float v[2][kNt][2];
+  } refs;
+  float* cold;
+  __device__ __forceinline__ float M(int n, int r) const {
+    return kCold ? cold[(2 * n + r) * 32] : refs.v[0][n][r];
+  }
+  __device__ __forceinline__ float D0(int n, int r) const {
+    return kCold ? cold[(2 * kNt + 2 * n + r) * 32] : refs.v[1][n][r];
+  }
+  __device__ __forceinline__ void set(int n, int r, float m, float d) {
+    if (kCold) {
+      cold[(2 * n + r) * 32] = m;
+      cold[(2 * kNt + 2 * n + r) * 32] = d;
+    } else {
+      refs.v[0][n][r] = m;
+      refs.v[1][n][r] = d;
+    }
+  }
+  // Score scale (log2 units).
+  __device__ __forceinline__ float qs(int n, int r) const {
+    return rows->scale[8 * n + 2 * (threadIdx.x & 3) + r];
+  }
 
   __device__ __forceinline__ static Rows& rows_of(uint8_t* smem) {
     return *reinterpret_cast<Rows*>(smem +
@@ -235,6 +261,7 @@ struct Body4 {
     at_ks = 2 * kCodes + g * kGroups + (D == 128 ? t4 : t4 >> 1);
     at_vs = 2 * kCodes + kScales + 2 * t4 * kGroups + (D == 128 ? g >> 1 : g >> 2);
     scales = reinterpret_cast<Scales*>(smem + kWarps * kRingBytes) + (threadIdx.x >> 5);
+    cold = scales->refs + lane;
     rk = rv = kUnset;
     level = false;
 #pragma unroll
@@ -251,9 +278,8 @@ struct Body4 {
       }
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        qs[n][r] = rows->scale[8 * n + 2 * t4 + r];
-        M[n][r] = -INFINITY;
-        l[n][r] = D0[n][r] = 0.f;
+        set(n, r, -INFINITY, 0.f);
+        l[n][r] = 0.f;
       }
     }
 #pragma unroll
@@ -370,14 +396,14 @@ struct Body4 {
     bool in = true;
 #pragma unroll
     for (int n = 0; n < kNt; ++n) {
-      f[n] = make_float2(qs[n][0] * 16.f * k, qs[n][1] * 16.f * k);
-      const float2 up = make_float2(kPBits + (lvs - D0[n][0]), kPBits + (lvs - D0[n][1]));
-      base[n] = make_float2(up.x - M[n][0], up.y - M[n][1]);
+      f[n] = make_float2(qs(n, 0) * 16.f * k, qs(n, 1) * 16.f * k);
+      const float2 up = make_float2(kPBits + (lvs - D0(n, 0)), kPBits + (lvs - D0(n, 1)));
+      base[n] = make_float2(up.x - M(n, 0), up.y - M(n, 1));
       back[n] = make_float2(ex2(-up.x), ex2(-up.y));
       // No slot yet: the first score moves the references.
 #pragma unroll
       for (int r = 0; r < 2; ++r)
-        in &= M[n][r] == -INFINITY || lvs - D0[n][r] >= -40.f;
+        in &= M(n, r) == -INFINITY || lvs - D0(n, r) >= -40.f;
     }
     level = __all_sync(0xffffffffu, in);
   }
@@ -444,35 +470,38 @@ struct Body4 {
       }
     });
 #pragma unroll
-    for (int w = 0; w < kW; ++w)
+    for (int w = 0; w < kW; ++w) {
+      uint32_t x[2][2][4];
 #pragma unroll
-      for (int st = 0; st < 2; ++st) {
-        uint32_t f[2][4];
+      for (int st = 0; st < 2; ++st)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          e2m1x8_to_half2(kw[st][r][w], f[r]);
+          e2m1x8_to_half2(kw[st][r][w], x[st][r]);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) f[r][k] = hmul2(f[r][k], sc[st][r]);
+          for (int k = 0; k < 4; ++k) x[st][r][k] = hmul2(x[st][r][k], sc[st][r]);
         }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int ks = 2 * w + h;
-          const uint32_t fa[4] = {f[0][2 * h], f[1][2 * h], f[0][2 * h + 1], f[1][2 * h + 1]};
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int term = kTerms - 1; term >= 0; --term)  // the smaller products first
+        for (int term = kTerms - 1; term >= 0; --term)  // the smaller products first
 #pragma unroll
-            for (int n = 0; n < kNt; ++n) {
-              uint32_t b0, b1;
-              if constexpr (kQShared) {
-                const uint2 x = rows->q[term][(ks * kNt + n) * 32 + lane];
-                b0 = x.x, b1 = x.y;
-              } else {
-                b0 = q[term][ks][n][0], b1 = q[term][ks][n][1];
-              }
+          for (int n = 0; n < kNt; ++n) {
+            const int ks = 2 * w + h;
+            uint32_t b0, b1;
+            if constexpr (kQShared) {
+              const uint2 y = rows->q[term][(ks * kNt + n) * 32 + lane];
+              b0 = y.x, b1 = y.y;
+            } else {
+              b0 = q[term][ks][n][0], b1 = q[term][ks][n][1];
+            }
+#pragma unroll
+            for (int st = 0; st < 2; ++st) {
+              const uint32_t fa[4] = {x[st][0][2 * h], x[st][1][2 * h], x[st][0][2 * h + 1],
+                                      x[st][1][2 * h + 1]};
               mma16816(s[2 * kC + st][n], fa, b0, b1);
             }
-        }
-      }
+          }
+    }
   }
 
   // Softmax of the chunk's scores into halves pf[term][step][tile][b0, b1], and
@@ -488,18 +517,17 @@ struct Body4 {
   // Moves a row's references: `top` its largest score, `to` that or M, `v` the
   // largest s + y, from `to`.
   __device__ __forceinline__ void move(int n, int r, float top, float to, float v) {
-    const float up = top - M[n][r], kept = D0[n][r] - (to - M[n][r]);
+    const float up = top - M(n, r), kept = D0(n, r) - (to - M(n, r));
     if (v - kept > 0.f || up > 60.f) {
       const float off = fmaxf(kept, v);  // kept: the output's unit stays
       const float down = ex2(kept - off);
-      l[n][r] *= ex2(M[n][r] - to);
+      l[n][r] *= ex2(M(n, r) - to);
 #pragma unroll
       for (int i = 0; i < kMt; ++i) {
         o[i][n][r] *= down;
         o[i][n][2 + r] *= down;
       }
-      M[n][r] = to;
-      D0[n][r] = off;
+      set(n, r, to, off);
     }
   }
 
@@ -550,7 +578,7 @@ struct Body4 {
 #pragma unroll
             for (int k = 0; k < 2; ++k)
               mx = fmaxf(mx, s[st][n][2 * k + r] * (r ? f[n].y : f[n].x));
-          const float top = row_max(mx), to = fmaxf(M[n][r], top);
+          const float top = row_max(mx), to = fmaxf(M(n, r), top);
           move(n, r, top, to, (top - to) + lvs);
         }
       follow();
@@ -591,7 +619,7 @@ struct Body4 {
         lvs[st][k] = make_float2(of.y, of.y);
 #pragma unroll
         for (int n = 0; n < kNt; ++n) {
-          const float2 f = __fmul2_rn(make_float2(qs[n][0], qs[n][1]), make_float2(of.x, of.x));
+          const float2 f = __fmul2_rn(make_float2(qs(n, 0), qs(n, 1)), make_float2(of.x, of.x));
           float2 y = __fmul2_rn(make_float2(s[st][n][2 * k], s[st][n][2 * k + 1]), f);
           if (kEdge) {
             const int key = key0 + 16 * st + 8 * k + g;
@@ -613,8 +641,8 @@ struct Body4 {
       bool high = false;
 #pragma unroll
       for (int n = 0; n < kNt; ++n) {
-        const float2 minus_M = make_float2(-M[n][0], -M[n][1]);
-        const float2 base = make_float2(kPBits - D0[n][0], kPBits - D0[n][1]);
+        const float2 minus_M = make_float2(-M(n, 0), -M(n, 1));
+        const float2 base = make_float2(kPBits - D0(n, 0), kPBits - D0(n, 1));
         float most[2] = {-INFINITY, -INFINITY};
 #pragma unroll
         for (int st = 0; st < 2; ++st)
@@ -628,7 +656,7 @@ struct Body4 {
           }
 #pragma unroll
         for (int r = 0; r < 2; ++r)
-          high |= most[r] > kPBits + 1.5f || mx[n][r] - M[n][r] > 60.f;
+          high |= most[r] > kPBits + 1.5f || mx[n][r] - M(n, r) > 60.f;
       }
       return high;
     };
@@ -637,7 +665,7 @@ struct Body4 {
       for (int n = 0; n < kNt; ++n)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const float top = row_max(mx[n][r]), to = fmaxf(M[n][r], top);
+          const float top = row_max(mx[n][r]), to = fmaxf(M(n, r), top);
           float v = -INFINITY;  // the largest s + y, from `to`
 #pragma unroll
           for (int st = 0; st < 2; ++st)
@@ -649,7 +677,7 @@ struct Body4 {
     }
 #pragma unroll
     for (int n = 0; n < kNt; ++n) {
-      const float2 minus_M = make_float2(-finite_or_0(M[n][0]), -finite_or_0(M[n][1]));
+      const float2 minus_M = make_float2(-finite_or_0(M(n, 0)), -finite_or_0(M(n, 1)));
       float2 sum = make_float2(l[n][0], l[n][1]);
 #pragma unroll
       for (int st = 0; st < 2; ++st)
@@ -743,7 +771,7 @@ struct Body4 {
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
         const int row = warp * kTile + 8 * n + 2 * t4 + r;
-        if (g == 0) stat[row] = Stat{M[n][r], D0[n][r], sum};
+        if (g == 0) stat[row] = Stat{M(n, r), D0(n, r), sum};
 #pragma unroll
         for (int half = 0; half < 2; ++half)
 #pragma unroll

@@ -27,6 +27,11 @@
 namespace msa {
 namespace {
 
+// Room above the largest weight when a reference is set, so that few chunks move
+// it again: a move scales all of a warp's sums, and of 32 rows some row's maximum
+// rises in most of a short range's chunks.  A weight's half keeps its 11 bits down
+// to 2^-23 of the largest.
+constexpr float kRoom = 5.f;
 constexpr float kTop = 13.f;  // a code of the slot's largest scale is code * 2^13
 
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
@@ -519,7 +524,7 @@ struct Body4 {
   __device__ __forceinline__ void move(int n, int r, float top, float to, float v) {
     const float up = top - M(n, r), kept = D0(n, r) - (to - M(n, r));
     if (v - kept > 0.f || up > 60.f) {
-      const float off = fmaxf(kept, v);  // kept: the output's unit stays
+      const float off = fmaxf(kept, v + kRoom);  // kept: the output's unit stays
       const float down = ex2(kept - off);
       l[n][r] *= ex2(M(n, r) - to);
 #pragma unroll

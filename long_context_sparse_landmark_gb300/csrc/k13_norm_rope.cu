@@ -8,17 +8,22 @@
 //
 // Each value is read and written once, and HBM bounds a long call.  A thread
 // takes 16 values of a row, two runs of 8 half a row apart, so that both
-// members of a pair are its own in either pairing; a row is d / 16 lanes.  The
-// angles are the same for all heads of a token: the CTA computes them once for
-// a tile of tokens, as 64-bit integers that wrap around at a full turn, reduced
-// to an eighth of a turn before they become floats.
+// members of a pair are its own in either pairing; a row is d / 16 lanes.  CTAs
+// take equal runs of rows of one side, whatever the tokens, with the next row's
+// values under way.  The angles are the same for all heads of a token: the CTA
+// computes them once for the tokens of some passes, as 64-bit integers that wrap
+// around at a full turn, reduced to an eighth of a turn before they become floats.
 #include "rope.cuh"
 
 namespace msa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTile = 32;  // tokens whose angles a CTA holds
+constexpr int kFwdPerSm = 4, kBwdPerSm = 2;  // CTAs
+constexpr int kGroup = 8;                    // passes over which the angles are held
+// Floats of the angles of a group's tokens: 8 passes of 32 rows (d = 128) or 64 are
+// 2 + 256 / heads tokens and more; fewer passes a group where that does not fit.
+constexpr int kAngles = 36 * 128;
 
 // cos and sin (times m) of position * f / 2^64 turns.  Products wrap at whole
 // turns; the nearest quarter turn is taken off as an integer, so the rest, at
@@ -42,29 +47,45 @@ __device__ __forceinline__ float2 turn_of(int64_t position, int64_t f, float m) 
   return make_float2(c * m, s * m);
 }
 
-// 16 values of a row: 8 at `p`, 8 half a row on.
+// 16 values of a row, 8 of them half a row on, as they are in memory.
 template <int D, bool kBf16>
-struct Piece {
-  float v[16];
+struct Raw {
+  static constexpr int kWords = kBf16 ? 8 : 16;
+  uint32_t w[kWords];
   __device__ __forceinline__ void load(const void* src, int64_t off) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      if constexpr (kBf16) {
-        const uint4 x = __ldcs(reinterpret_cast<const uint4*>(
-            static_cast<const uint16_t*>(src) + off + h * (D / 2)));
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      constexpr int kPer = kWords / 8;  // 16-byte pieces a run
+      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(src) +
+                                                      (off + h * (D / 2)) * (kBf16 ? 2 : 4));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          v[8 * h + 2 * i] = __uint_as_float(w[i] << 16);
-          v[8 * h + 2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
-      } else {
-        const float4* p =
-            reinterpret_cast<const float4*>(static_cast<const float*>(src) + off + h * (D / 2));
-        const float4 x = __ldcs(p), y = __ldcs(p + 1);
-        v[8 * h + 0] = x.x, v[8 * h + 1] = x.y, v[8 * h + 2] = x.z, v[8 * h + 3] = x.w;
-        v[8 * h + 4] = y.x, v[8 * h + 5] = y.y, v[8 * h + 6] = y.z, v[8 * h + 7] = y.w;
+      for (int i = 0; i < kPer; ++i) {
+        const uint4 x = __ldcs(p + i);
+        uint32_t* to = w + (h * kPer + i) * 4;
+        to[0] = x.x, to[1] = x.y, to[2] = x.z, to[3] = x.w;
       }
+    }
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = 0;
+  }
+};
+
+// The same, as floats.
+template <int D, bool kBf16>
+struct Piece {
+  float v[16];
+  __device__ __forceinline__ explicit Piece(const Raw<D, kBf16>& r) {
+    if constexpr (kBf16) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[2 * i] = __uint_as_float(r.w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(r.w[i] & 0xffff0000u);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r.w[i]);
     }
   }
   __device__ __forceinline__ void store(void* dst, int64_t off) const {
@@ -86,17 +107,15 @@ struct Piece {
       }
     }
   }
-  // Turns the pairs by the angles of cs (of pair i: [i] the cosine, [D / 2 + i]
-  // the sine), or back.
+  // Turns the pairs by the angles of cs (cosines, then sines), or back.
   template <bool kInterleaved, bool kBack>
   __device__ __forceinline__ void turn(const float* cs, int lane) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       // 4 pairs: of halves a run apart, dims 4h .. 4h + 3 of both; of
       // neighbours, the 8 dims of run h.
-      const int i0 = kInterleaved ? h * (D / 4) + lane * 4 : lane * 8 + 4 * h;
-      const float4 c4 = *reinterpret_cast<const float4*>(cs + i0);
-      const float4 s4 = *reinterpret_cast<const float4*>(cs + D / 2 + i0);
+      const float4 c4 = *reinterpret_cast<const float4*>(cs + h * (D / 4) + lane * 4);
+      const float4 s4 = *reinterpret_cast<const float4*>(cs + D / 2 + h * (D / 4) + lane * 4);
       const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -123,147 +142,222 @@ __device__ __forceinline__ float weight_at(const void* w, int bf16, int i) {
               : static_cast<const float*>(w)[i];
 }
 
-// The angles of a tile's tokens: [token][cosines, sines].
-template <int D>
+// The angles of tokens t0 .. t1: [token][cosines, sines], each in the order in which
+// the lanes take them, 16 bytes side by side.
+template <int D, bool kInterleaved>
 __device__ __forceinline__ void angles(const RopeArgs& a, int64_t t0, int tokens, float* cs) {
   for (int i = threadIdx.x; i < tokens * (D / 2); i += kThreads) {
     const int t = i / (D / 2), f = i - t * (D / 2);
     const float2 x = turn_of(a.positions[t0 + t], a.freqs[f], a.mscale);
-    cs[t * D + f] = x.x;
-    cs[t * D + D / 2 + f] = x.y;
+    const int at = kInterleaved ? f : (f >> 2 & 1) * (D / 4) + (f >> 3) * 4 + (f & 3);
+    cs[t * D + at] = x.x;
+    cs[t * D + D / 2 + at] = x.y;
   }
 }
 
-// A CTA takes tiles of tokens, all heads of queries and keys.
-template <int D, bool kBf16, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const RopeArgs a) {
-  constexpr int kLanes = D / 16, kStep = kThreads / kLanes;
-  __shared__ __align__(16) float cs[kMaxTile * D];
-  __shared__ __align__(16) float weight[2][D];
-  const int lane = threadIdx.x & (kLanes - 1), H = a.heads[0] + a.heads[1];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    if (a.weight[i])
-      for (int k = threadIdx.x; k < D; k += kThreads) weight[i][k] = weight_at(a.weight[i], a.w_bf16, k);
-  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tile; t0 < a.n;
-       t0 += static_cast<int64_t>(gridDim.x) * a.tile) {
-    const int tokens = static_cast<int>(min64(a.tile, a.n - t0));
-    __syncthreads();
-    angles<D>(a, t0, tokens, cs);
-    __syncthreads();
-    const int rows = tokens * H;
-    for (int r0 = 0; r0 < rows; r0 += kStep) {  // whole warps, for the sums
-      const int r = r0 + threadIdx.x / kLanes;
-      const bool in = r < rows;
-      const int t = in ? r / H : 0, hh = in ? r - t * H : 0;
-      const int side = hh >= a.heads[0];
-      const int h = side ? hh - a.heads[0] : hh;
-      Piece<D, kBf16> x;
-      const int64_t from = (t0 + t) * a.stride[side] + h * D + lane * 8;
-      if (in) {
-        x.load(a.x[side], from);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 16; ++k) x.v[k] = 0.f;
-      }
-      float ss = 0.f;
-#pragma unroll
-      for (int k = 0; k < 16; ++k) ss = fmaf(x.v[k], x.v[k], ss);
-      ss = row_sum<kLanes>(ss);
-      if (!in) continue;
-      if (a.weight[side]) {
-        const float s = rsqrtf(ss * (1.f / D) + a.eps);
-#pragma unroll
-        for (int k = 0; k < 16; ++k)
-          x.v[k] = x.v[k] * s * weight[side][(k >> 3) * (D / 2) + lane * 8 + (k & 7)];
-      }
-      x.template turn<kInterleaved, false>(cs + t * D, lane);
-      const int64_t to = ((t0 + t) * a.heads[side] + h) * D + lane * 8;
-      if (MSA_IN_RANGE(to, D / 2 + 8, a.n * a.heads[side] * D, a.status)) x.store(a.out[side], to);
+// A CTA's rows of one side: `passes` passes over kStep rows from row0 on, a thread
+// the same one of each.  Rows are counted from the first token's first.
+template <int D>
+struct Walk {
+  static constexpr int kLanes = D / 16, kStep = kThreads / kLanes;
+  int side, H, lane;
+  int64_t t0;         // token of the CTA's first row
+  uint32_t row, end;  // this thread's row and the end, from token t0's first
+  int t, h, dt, dh;   // of `row`: token (from t0) and head; their steps
+  uint32_t first;     // the CTA's first row of the pass
+
+  // False: nothing to do.
+  __device__ __forceinline__ bool begin(const RopeArgs& a) {
+    side = static_cast<int>(blockIdx.x) >= a.ctas[0];
+    H = a.heads[side];
+    lane = threadIdx.x & (kLanes - 1);
+    const int64_t all = a.n * H;
+    const int ctas = a.ctas[side], cta = static_cast<int>(blockIdx.x) - (side ? a.ctas[0] : 0);
+    // Whole passes, as many for each CTA as for any other but one more for the first.
+    const int64_t passes = (all + kStep - 1) / kStep;
+    const int64_t each = passes / ctas, more = passes - each * ctas;
+    const int64_t p0 = cta * each + min64(cta, more), p1 = p0 + each + (cta < more);
+    if (p0 == p1) return false;
+    const int64_t r0 = p0 * kStep, r1 = min64(all, p1 * kStep);
+    t0 = r0 / H;
+    first = static_cast<uint32_t>(r0 - t0 * H);
+    end = static_cast<uint32_t>(r1 - t0 * H);  // fits: the entry points check
+    row = first + threadIdx.x / kLanes;
+    t = row / H;
+    h = row - t * H;
+    dt = kStep / H;
+    dh = kStep - dt * H;
+    return true;
+  }
+  __device__ __forceinline__ bool in() const { return row < end; }
+  __device__ __forceinline__ void next() {
+    row += kStep;
+    t += dt;
+    h += dh;
+    if (h >= H) {
+      h -= H;
+      ++t;
     }
+  }
+  // Passes whose tokens' angles are held together.
+  __device__ __forceinline__ int group() const {
+    return max(1, min(kGroup, (kAngles / D - 2) * H / kStep));
+  }
+  // Tokens of the group of `passes` passes that starts at row `from`: the first, and
+  // how many.
+  __device__ __forceinline__ int tokens(uint32_t from, int passes, int* token) const {
+    const uint32_t to = min(end, from + static_cast<uint32_t>(passes) * kStep);
+    *token = from / H;
+    return static_cast<int>((to - 1) / H) - *token + 1;
+  }
+};
+
+// Calls row(cs of the row's token) for every pass, the angles of a group of passes
+// computed while the one before is under way.
+template <int D, bool kInterleaved, typename Row>
+__device__ __forceinline__ void walk_rows(const RopeArgs& a, const Walk<D>& w, float (*cs)[kAngles],
+                                          Row row) {
+  const int group = w.group();
+  int token, next_token;
+  int tokens = w.tokens(w.first, group, &token);
+  angles<D, kInterleaved>(a, w.t0 + token, tokens, cs[0]);
+  __syncthreads();
+  int buffer = 0;
+  for (uint32_t from = w.first; from < w.end; from += group * Walk<D>::kStep) {
+    const uint32_t then = from + group * Walk<D>::kStep;
+    if (then < w.end) {
+      tokens = w.tokens(then, group, &next_token);
+      angles<D, kInterleaved>(a, w.t0 + next_token, tokens, cs[buffer ^ 1]);
+    }
+    for (uint32_t r = from; r < min(then, w.end); r += Walk<D>::kStep) row(cs[buffer], token);
+    __syncthreads();
+    buffer ^= 1;
+    token = next_token;
   }
 }
 
 // The first ctas[0] CTAs take the queries' rows, the others the keys'.
 template <int D, bool kBf16, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const RopeArgs a) {
-  constexpr int kLanes = D / 16, kStep = kThreads / kLanes;
-  __shared__ __align__(16) float cs[kMaxTile * D];
-  __shared__ __align__(16) float weight[D];
-  const int side = static_cast<int>(blockIdx.x) >= a.ctas[0];
-  const int cta = blockIdx.x - (side ? a.ctas[0] : 0), ctas = a.ctas[side];
-  const int lane = threadIdx.x & (kLanes - 1), H = a.heads[side];
-  const bool norm = a.weight[side] != nullptr;
-  let_next_start();
-  if (norm)
-    for (int k = threadIdx.x; k < D; k += kThreads) weight[k] = weight_at(a.weight[side], a.w_bf16, k);
-  float dw[16];
+__global__ void __launch_bounds__(kThreads, kFwdPerSm) norm_rope_kernel(const RopeArgs a) {
+  __shared__ __align__(16) float cs[2][kAngles];
+  Walk<D> w;
+  if (!w.begin(a)) return;
+  const int lane = w.lane, H = w.H;
+  const void* src = a.x[w.side];
+  const int64_t stride = a.stride[w.side];
+  const bool norm = a.weight[w.side] != nullptr;
+  float weight[16];
 #pragma unroll
-  for (int k = 0; k < 16; ++k) dw[k] = 0.f;
-  for (int64_t t0 = static_cast<int64_t>(cta) * a.tile; t0 < a.n;
-       t0 += static_cast<int64_t>(ctas) * a.tile) {
-    const int tokens = static_cast<int>(min64(a.tile, a.n - t0));
-    __syncthreads();
-    angles<D>(a, t0, tokens, cs);
-    __syncthreads();
-    const int rows = tokens * H;
-    for (int r0 = 0; r0 < rows; r0 += kStep) {
-      const int r = r0 + threadIdx.x / kLanes;
-      const bool in = r < rows;
-      const int t = in ? r / H : 0, h = in ? r - t * H : 0;
-      Piece<D, kBf16> x, g;
-      if (in) {
-        g.load(a.dy[side], (t0 + t) * a.dy_stride[side] + h * D + lane * 8);
-        if (norm) x.load(a.x[side], (t0 + t) * a.stride[side] + h * D + lane * 8);
-      }
-      if (!in || !norm) {
+  for (int k = 0; k < 16; ++k)
+    weight[k] = norm ? weight_at(a.weight[w.side], a.w_bf16, (k >> 3) * (D / 2) + lane * 8 + (k & 7))
+                     : 1.f;
+  // A row's values come in while the one before is worked on.
+  Raw<D, kBf16> ahead;
+  const auto load = [&](const Walk<D>& at) {
+    if (at.in())
+      ahead.load(src, (at.t0 + at.t) * stride + at.h * D + lane * 8);
+    else
+      ahead.clear();
+  };
+  load(w);
+  walk_rows<D, kInterleaved>(a, w, cs, [&](const float* c, int token) {
+    const Walk<D> at = w;
+    Piece<D, kBf16> x(ahead);
+    w.next();
+    load(w);
+    if (norm) {
+      float ss = 0.f;
 #pragma unroll
-        for (int k = 0; k < 16; ++k) x.v[k] = 0.f;
-      }
-      if (!in) {
+      for (int k = 0; k < 16; ++k) ss = fmaf(x.v[k], x.v[k], ss);
+      ss = row_sum<Walk<D>::kLanes>(ss);
+      const float s = rsqrtf(ss * (1.f / D) + a.eps);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) g.v[k] = 0.f;
-      }
-      g.template turn<kInterleaved, true>(cs + t * D, lane);
-      if (norm) {
-        float ss = 0.f, xu = 0.f, w[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          w[k] = weight[(k >> 3) * (D / 2) + lane * 8 + (k & 7)];
-          ss = fmaf(x.v[k], x.v[k], ss);
-          xu = fmaf(x.v[k] * w[k], g.v[k], xu);
-        }
-        ss = row_sum<kLanes>(ss);
-        xu = row_sum<kLanes>(xu);
-        const float s = rsqrtf(ss * (1.f / D) + a.eps);
-        const float f = s * s * (xu * (1.f / D));
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          if (in) dw[k] = fmaf(g.v[k], x.v[k] * s, dw[k]);
-          g.v[k] = s * (w[k] * g.v[k] - x.v[k] * f);
-        }
-      }
-      const int64_t to = ((t0 + t) * H + h) * D + lane * 8;
-      if (in && MSA_IN_RANGE(to, D / 2 + 8, a.n * H * D, a.status)) g.store(a.out[side], to);
+      for (int k = 0; k < 16; ++k) x.v[k] = x.v[k] * s * weight[k];
     }
+    if (!at.in()) return;
+    x.template turn<kInterleaved, false>(c + (at.t - token) * D, lane);
+    const int64_t to = ((at.t0 + at.t) * H + at.h) * D + lane * 8;
+    if (MSA_IN_RANGE(to, D / 2 + 8, a.n * H * D, a.status)) x.store(a.out[w.side], to);
+  });
+}
+
+template <int D, bool kBf16, bool kInterleaved>
+__global__ void __launch_bounds__(kThreads, kBwdPerSm) norm_rope_bwd_kernel(const RopeArgs a) {
+  __shared__ __align__(16) float cs[2][kAngles];
+  Walk<D> w;
+  let_next_start();
+  if (!w.begin(a)) {  // its sums are read
+    if (a.weight[w.side] && threadIdx.x < D)
+      a.part[static_cast<int64_t>(blockIdx.x) * D + threadIdx.x] = 0.f;
+    return;
   }
+  const int lane = w.lane, H = w.H;
+  const bool norm = a.weight[w.side] != nullptr;
+  const void *src = a.x[w.side], *grad = a.dy[w.side];
+  const int64_t stride = a.stride[w.side], dy_stride = a.dy_stride[w.side];
+  float weight[16], dw[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    weight[k] = norm ? weight_at(a.weight[w.side], a.w_bf16, (k >> 3) * (D / 2) + lane * 8 + (k & 7))
+                     : 1.f;
+    dw[k] = 0.f;
+  }
+  Raw<D, kBf16> x_ahead, g_ahead;
+  x_ahead.clear();
+  const auto load = [&](const Walk<D>& at) {
+    if (at.in()) {
+      g_ahead.load(grad, (at.t0 + at.t) * dy_stride + at.h * D + lane * 8);
+      if (norm) x_ahead.load(src, (at.t0 + at.t) * stride + at.h * D + lane * 8);
+    } else {
+      g_ahead.clear();
+      x_ahead.clear();
+    }
+  };
+  load(w);
+  walk_rows<D, kInterleaved>(a, w, cs, [&](const float* c, int token) {
+    const Walk<D> at = w;
+    Piece<D, kBf16> g(g_ahead), x(x_ahead);
+    w.next();
+    load(w);
+    g.template turn<kInterleaved, true>(c + (at.in() ? at.t - token : 0) * D, lane);
+    if (norm) {
+      float ss = 0.f, xu = 0.f;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        ss = fmaf(x.v[k], x.v[k], ss);
+        xu = fmaf(x.v[k] * weight[k], g.v[k], xu);
+      }
+      ss = row_sum<Walk<D>::kLanes>(ss);
+      xu = row_sum<Walk<D>::kLanes>(xu);
+      const float s = rsqrtf(ss * (1.f / D) + a.eps);
+      const float f = s * s * (xu * (1.f / D));
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        if (at.in()) dw[k] = fmaf(g.v[k], x.v[k] * s, dw[k]);
+        g.v[k] = s * (weight[k] * g.v[k] - x.v[k] * f);
+      }
+    }
+    const int64_t to = ((at.t0 + at.t) * H + at.h) * D + lane * 8;
+    if (at.in() && MSA_IN_RANGE(to, D / 2 + 8, a.n * H * D, a.status)) g.store(a.out[w.side], to);
+  });
   if (!norm) return;
   // Lanes of the same dims are kLanes apart, then the warps, in order.
 #pragma unroll
   for (int k = 0; k < 16; ++k)
 #pragma unroll
-    for (int o = kLanes; o < 32; o <<= 1) dw[k] += __shfl_xor_sync(0xffffffffu, dw[k], o);
-  __syncthreads();
-  if ((threadIdx.x & 31) < kLanes) {
+    for (int o = Walk<D>::kLanes; o < 32; o <<= 1)
+      dw[k] += __shfl_xor_sync(0xffffffffu, dw[k], o);
+  float* sums = cs[0];
+  if ((threadIdx.x & 31) < Walk<D>::kLanes) {
 #pragma unroll
     for (int k = 0; k < 16; ++k)
-      cs[(threadIdx.x >> 5) * D + (k >> 3) * (D / 2) + lane * 8 + (k & 7)] = dw[k];
+      sums[(threadIdx.x >> 5) * D + (k >> 3) * (D / 2) + lane * 8 + (k & 7)] = dw[k];
   }
   __syncthreads();
   if (threadIdx.x < D) {
     float sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) sum += cs[w * D + threadIdx.x];
+    for (int i = 0; i < kThreads / 32; ++i) sum += sums[i * D + threadIdx.x];
     a.part[static_cast<int64_t>(blockIdx.x) * D + threadIdx.x] = sum;
   }
 }
@@ -292,22 +386,26 @@ __global__ void __launch_bounds__(D * kSlices) norm_rope_dw_kernel(const RopeArg
     static_cast<float*>(a.dweight[side])[k] = sum;
 }
 
-// Tokens a CTA takes at a time: enough rows for some passes of its threads, and
-// a tile for every CTA.
-int tile_of(int64_t n, int heads, int d, int ctas) {
+// CTAs of the two sides: at most `all`, in the proportion of their rows, and none
+// without a pass.
+void split_ctas(int64_t n, const int* heads, int d, int64_t all, int* ctas) {
   const int step = kThreads / (d / 16);
-  const int64_t t = min64(kMaxTile, max64(1, 8 * step / max64(1, heads)));
-  return static_cast<int>(max64(1, min64(t, (n + ctas - 1) / ctas)));
+  const int64_t q = (n * heads[0] + step - 1) / step, k = (n * heads[1] + step - 1) / step;
+  if (q + k > all) {
+    ctas[1] = k ? static_cast<int>(max64(1, all * k / (q + k))) : 0;
+    ctas[0] = static_cast<int>(all - ctas[1]);
+  } else {
+    ctas[0] = static_cast<int>(max64(1, q));
+    ctas[1] = static_cast<int>(k);
+  }
 }
-
-constexpr int kPerSm = 4;
 
 }  // namespace
 
 cudaError_t launch_norm_rope(const RopeArgs& a0, cudaStream_t st) {
   RopeArgs a = a0;
-  a.tile = tile_of(a.n, a.heads[0] + a.heads[1], a.d, kSms * kPerSm);
-  const dim3 grid(static_cast<unsigned>(min64((a.n + a.tile - 1) / a.tile, kSms * kPerSm)));
+  split_ctas(a.n, a.heads, a.d, kSms * kFwdPerSm, a.ctas);
+  const dim3 grid(static_cast<unsigned>(a.ctas[0] + a.ctas[1]));
   void (*kernel)(RopeArgs);
   if (a.d == 128)
     kernel = a.bf16 ? (a.interleaved ? norm_rope_kernel<128, true, true>
@@ -323,19 +421,11 @@ cudaError_t launch_norm_rope(const RopeArgs& a0, cudaStream_t st) {
 }
 
 void norm_rope_bwd_ctas(int64_t n, const int* heads, int d, int* ctas) {
-  const int64_t all = kSms * kPerSm;
-  const int H = heads[0] + heads[1];
-  ctas[1] = heads[1] ? static_cast<int>(max64(1, min64(n, all * heads[1] / H))) : 0;
-  ctas[0] = static_cast<int>(max64(1, min64(n, all - ctas[1])));
+  split_ctas(n, heads, d, kSms * kBwdPerSm, ctas);
 }
 
-cudaError_t launch_norm_rope_bwd(const RopeArgs& a0, cudaStream_t st) {
-  RopeArgs a = a0;
-  const bool norm = a.weight[0] || a.weight[1];
+cudaError_t launch_norm_rope_bwd(const RopeArgs& a, cudaStream_t st) {
   if (a.n > 0) {
-    const int t0 = tile_of(a.n, a.heads[0], a.d, a.ctas[0]);
-    const int t1 = a.heads[1] ? tile_of(a.n, a.heads[1], a.d, a.ctas[1]) : 1;
-    a.tile = t0 > t1 ? t0 : t1;
     const dim3 grid(static_cast<unsigned>(a.ctas[0] + a.ctas[1]));
     void (*kernel)(RopeArgs);
     if (a.d == 128)
@@ -351,7 +441,7 @@ cudaError_t launch_norm_rope_bwd(const RopeArgs& a0, cudaStream_t st) {
     const cudaError_t e = launch_after(kernel, grid, kThreads, 0, st, false, a);
     if (e != cudaSuccess) return e;
   }
-  if (!norm) return cudaSuccess;
+  if (!a.weight[0] && !a.weight[1]) return cudaSuccess;
   return launch_after(a.d == 128 ? norm_rope_dw_kernel<128> : norm_rope_dw_kernel<64>, dim3(2),
                       a.d * kSlices, 0, st, a.n > 0, a);
 }

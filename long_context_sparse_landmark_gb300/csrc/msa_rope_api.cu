@@ -10,6 +10,8 @@ msa_status check_rope_sizes(int64_t n, int Hq, int Hkv, int d) {
   if (Hq < 1 || Hq > kMaxHeads || Hkv < 0 || Hkv > kMaxHeads)
     return fail(MSA_ERR_INVALID_ARG, "Hq=%d Hkv=%d out of range", Hq, Hkv);
   if (d != 64 && d != 128) return fail(MSA_ERR_UNSUPPORTED, "head dim d=%d (supported: 64, 128)", d);
+  if (n * (Hq > Hkv ? Hq : Hkv) > int64_t(1) << 38)  // a CTA's rows are counted in 32 bits
+    return fail(MSA_ERR_UNSUPPORTED, "n=%lld Hq=%d Hkv=%d: too many rows", (long long)n, Hq, Hkv);
   return MSA_OK;
 }
 

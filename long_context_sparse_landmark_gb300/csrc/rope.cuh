@@ -17,14 +17,13 @@ struct RopeArgs {
   const void* weight[2];  // [d], null: no norm
   void* dweight[2];       // backward: [d]
   float* part;            // backward: [ctas][d] sums of the weights' gradients, queries' CTAs first
-  int ctas[2];            // backward: of queries, of keys
+  int ctas[2];            // of queries, of keys
   int64_t n;
   int d;
   const int64_t* positions;
   const int64_t* freqs;
   float eps, mscale;
   int interleaved, bf16, w_bf16;
-  int tile;  // tokens that a CTA takes at a time
   int* status;
 };
 cudaError_t launch_norm_rope(const RopeArgs& a, cudaStream_t st);

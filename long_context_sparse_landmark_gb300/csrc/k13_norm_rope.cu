@@ -72,11 +72,15 @@ struct Raw {
   }
 };
 
-// The same, as floats.
-template <int D, bool kBf16>
-struct Piece {
-  float v[16];
-  __device__ __forceinline__ explicit Piece(const Raw<D, kBf16>& r) {
+// The same as 8 pairs to turn, (a, b) of pair i in a[i / 2] and b[i / 2]: two
+// neighbours are worked on by one packed instruction.  Of halves a run apart pair
+// i is value i of both runs; of neighbours, values 2i and 2i + 1.
+template <int D, bool kBf16, bool kInterleaved>
+struct Pairs {
+  float2 a[4], b[4];
+  __device__ __forceinline__ Pairs() {}
+  __device__ __forceinline__ explicit Pairs(const Raw<D, kBf16>& r) {
+    float v[16];
     if constexpr (kBf16) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -87,8 +91,30 @@ struct Piece {
 #pragma unroll
       for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r.w[i]);
     }
+    set(v);
   }
+  __device__ __forceinline__ void set(const float* v) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      a[i] = kInterleaved ? make_float2(v[4 * i], v[4 * i + 2]) : make_float2(v[2 * i], v[2 * i + 1]);
+      b[i] = kInterleaved ? make_float2(v[4 * i + 1], v[4 * i + 3])
+                          : make_float2(v[8 + 2 * i], v[8 + 2 * i + 1]);
+    }
+  }
+  __device__ __forceinline__ void get(float* v) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int x = kInterleaved ? 4 * i : 2 * i;
+      v[x] = a[i].x;
+      v[x + (kInterleaved ? 2 : 1)] = a[i].y;
+      v[kInterleaved ? x + 1 : 8 + x] = b[i].x;
+      v[kInterleaved ? x + 3 : 8 + x + 1] = b[i].y;
+    }
+  }
+  // To a row's place in memory, as elements.
   __device__ __forceinline__ void store(void* dst, int64_t off) const {
+    float v[16];
+    get(v);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if constexpr (kBf16) {
@@ -108,27 +134,26 @@ struct Piece {
     }
   }
   // Turns the pairs by the angles of cs (cosines, then sines), or back.
-  template <bool kInterleaved, bool kBack>
+  template <bool kBack>
   __device__ __forceinline__ void turn(const float* cs, int lane) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      // 4 pairs: of halves a run apart, dims 4h .. 4h + 3 of both; of
-      // neighbours, the 8 dims of run h.
       const float4 c4 = *reinterpret_cast<const float4*>(cs + h * (D / 4) + lane * 4);
       const float4 s4 = *reinterpret_cast<const float4*>(cs + D / 2 + h * (D / 4) + lane * 4);
-      const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+      const float2 c[2] = {make_float2(c4.x, c4.y), make_float2(c4.z, c4.w)};
+      const float2 s[2] = {make_float2(s4.x, s4.y), make_float2(s4.z, s4.w)};
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float& a = kInterleaved ? v[8 * h + 2 * k] : v[4 * h + k];
-        float& b = kInterleaved ? v[8 * h + 2 * k + 1] : v[8 + 4 * h + k];
-        const float sn = kBack ? -s[k] : s[k];
-        const float x = a * c[k] - b * sn, y = a * sn + b * c[k];
-        a = x;
-        b = y;
+      for (int k = 0; k < 2; ++k) {
+        float2 &x = a[2 * h + k], &y = b[2 * h + k];
+        const float2 minus = make_float2(-s[k].x, -s[k].y);
+        const float2 u = __ffma2_rn(x, c[k], __fmul2_rn(y, kBack ? s[k] : minus));
+        y = __ffma2_rn(x, kBack ? minus : s[k], __fmul2_rn(y, c[k]));
+        x = u;
       }
     }
   }
 };
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 template <int kLanes>
 __device__ __forceinline__ float row_sum(float x) {
@@ -142,8 +167,10 @@ __device__ __forceinline__ float weight_at(const void* w, int bf16, int i) {
               : static_cast<const float*>(w)[i];
 }
 
-// The angles of tokens t0 .. t1: [token][cosines, sines], each in the order in which
-// the lanes take them, 16 bytes side by side.
+// The angles of tokens t0 .. t0 + tokens: [token][cosines, sines], each in the order
+// in which the lanes take them, 16 bytes side by side: the first 4 of all lanes'
+// pairs, then the others.  Of halves a run apart a lane's pairs are 8 lane .. 8 lane
+// + 7; of neighbours, 4 lane .. 4 lane + 3 and those d / 4 on.
 template <int D, bool kInterleaved>
 __device__ __forceinline__ void angles(const RopeArgs& a, int64_t t0, int tokens, float* cs) {
   for (int i = threadIdx.x; i < tokens * (D / 2); i += kThreads) {
@@ -246,11 +273,15 @@ __global__ void __launch_bounds__(kThreads, kFwdPerSm) norm_rope_kernel(const Ro
   const void* src = a.x[w.side];
   const int64_t stride = a.stride[w.side];
   const bool norm = a.weight[w.side] != nullptr;
-  float weight[16];
+  Pairs<D, kBf16, kInterleaved> weight;
+  {
+    float v[16];
 #pragma unroll
-  for (int k = 0; k < 16; ++k)
-    weight[k] = norm ? weight_at(a.weight[w.side], a.w_bf16, (k >> 3) * (D / 2) + lane * 8 + (k & 7))
-                     : 1.f;
+    for (int k = 0; k < 16; ++k)
+      v[k] = norm ? weight_at(a.weight[w.side], a.w_bf16, (k >> 3) * (D / 2) + lane * 8 + (k & 7))
+                  : 1.f;
+    weight.set(v);
+  }
   // A row's values come in while the one before is worked on.
   Raw<D, kBf16> ahead;
   const auto load = [&](const Walk<D>& at) {
@@ -262,20 +293,23 @@ __global__ void __launch_bounds__(kThreads, kFwdPerSm) norm_rope_kernel(const Ro
   load(w);
   walk_rows<D, kInterleaved>(a, w, cs, [&](const float* c, int token) {
     const Walk<D> at = w;
-    Piece<D, kBf16> x(ahead);
+    Pairs<D, kBf16, kInterleaved> x(ahead);
     w.next();
     load(w);
     if (norm) {
-      float ss = 0.f;
+      float2 ss = both(0.f);
 #pragma unroll
-      for (int k = 0; k < 16; ++k) ss = fmaf(x.v[k], x.v[k], ss);
-      ss = row_sum<Walk<D>::kLanes>(ss);
-      const float s = rsqrtf(ss * (1.f / D) + a.eps);
+      for (int k = 0; k < 4; ++k) ss = __ffma2_rn(x.a[k], x.a[k], __ffma2_rn(x.b[k], x.b[k], ss));
+      const float2 r = both(
+          rsqrtf(row_sum<Walk<D>::kLanes>(ss.x + ss.y) * (1.f / D) + a.eps));
 #pragma unroll
-      for (int k = 0; k < 16; ++k) x.v[k] = x.v[k] * s * weight[k];
+      for (int k = 0; k < 4; ++k) {
+        x.a[k] = __fmul2_rn(__fmul2_rn(x.a[k], r), weight.a[k]);
+        x.b[k] = __fmul2_rn(__fmul2_rn(x.b[k], r), weight.b[k]);
+      }
     }
     if (!at.in()) return;
-    x.template turn<kInterleaved, false>(c + (at.t - token) * D, lane);
+    x.template turn<false>(c + (at.t - token) * D, lane);
     const int64_t to = ((at.t0 + at.t) * H + at.h) * D + lane * 8;
     if (MSA_IN_RANGE(to, D / 2 + 8, a.n * H * D, a.status)) x.store(a.out[w.side], to);
   });
@@ -295,13 +329,17 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm) norm_rope_bwd_kernel(cons
   const bool norm = a.weight[w.side] != nullptr;
   const void *src = a.x[w.side], *grad = a.dy[w.side];
   const int64_t stride = a.stride[w.side], dy_stride = a.dy_stride[w.side];
-  float weight[16], dw[16];
+  Pairs<D, kBf16, kInterleaved> weight, dw;
+  {
+    float v[16];
 #pragma unroll
-  for (int k = 0; k < 16; ++k) {
-    weight[k] = norm ? weight_at(a.weight[w.side], a.w_bf16, (k >> 3) * (D / 2) + lane * 8 + (k & 7))
-                     : 1.f;
-    dw[k] = 0.f;
+    for (int k = 0; k < 16; ++k)
+      v[k] = norm ? weight_at(a.weight[w.side], a.w_bf16, (k >> 3) * (D / 2) + lane * 8 + (k & 7))
+                  : 1.f;
+    weight.set(v);
   }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) dw.a[k] = dw.b[k] = both(0.f);
   Raw<D, kBf16> x_ahead, g_ahead;
   x_ahead.clear();
   const auto load = [&](const Walk<D>& at) {
@@ -316,25 +354,29 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm) norm_rope_bwd_kernel(cons
   load(w);
   walk_rows<D, kInterleaved>(a, w, cs, [&](const float* c, int token) {
     const Walk<D> at = w;
-    Piece<D, kBf16> g(g_ahead), x(x_ahead);
+    Pairs<D, kBf16, kInterleaved> g(g_ahead), x(x_ahead);
     w.next();
     load(w);
-    g.template turn<kInterleaved, true>(c + (at.in() ? at.t - token : 0) * D, lane);
+    g.template turn<true>(c + (at.in() ? at.t - token : 0) * D, lane);
     if (norm) {
-      float ss = 0.f, xu = 0.f;
+      float2 ss = both(0.f), xu = both(0.f), u[8];
 #pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        ss = fmaf(x.v[k], x.v[k], ss);
-        xu = fmaf(x.v[k] * weight[k], g.v[k], xu);
+      for (int k = 0; k < 4; ++k) {
+        u[k] = __fmul2_rn(weight.a[k], g.a[k]);
+        u[4 + k] = __fmul2_rn(weight.b[k], g.b[k]);
+        ss = __ffma2_rn(x.a[k], x.a[k], __ffma2_rn(x.b[k], x.b[k], ss));
+        xu = __ffma2_rn(x.a[k], u[k], __ffma2_rn(x.b[k], u[4 + k], xu));
       }
-      ss = row_sum<Walk<D>::kLanes>(ss);
-      xu = row_sum<Walk<D>::kLanes>(xu);
-      const float s = rsqrtf(ss * (1.f / D) + a.eps);
-      const float f = s * s * (xu * (1.f / D));
+      const float r = rsqrtf(row_sum<Walk<D>::kLanes>(ss.x + ss.y) * (1.f / D) + a.eps);
+      // Rows past the end are zeros: they add none to dw, unless r is infinite.
+      const float rw = at.in() ? r : 0.f;
+      const float f = -r * r * (row_sum<Walk<D>::kLanes>(xu.x + xu.y) * (1.f / D));
 #pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        if (at.in()) dw[k] = fmaf(g.v[k], x.v[k] * s, dw[k]);
-        g.v[k] = s * (weight[k] * g.v[k] - x.v[k] * f);
+      for (int k = 0; k < 4; ++k) {
+        dw.a[k] = __ffma2_rn(g.a[k], __fmul2_rn(x.a[k], both(rw)), dw.a[k]);
+        dw.b[k] = __ffma2_rn(g.b[k], __fmul2_rn(x.b[k], both(rw)), dw.b[k]);
+        g.a[k] = __fmul2_rn(both(r), __ffma2_rn(x.a[k], both(f), u[k]));
+        g.b[k] = __fmul2_rn(both(r), __ffma2_rn(x.b[k], both(f), u[4 + k]));
       }
     }
     const int64_t to = ((at.t0 + at.t) * H + at.h) * D + lane * 8;
@@ -342,16 +384,17 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm) norm_rope_bwd_kernel(cons
   });
   if (!norm) return;
   // Lanes of the same dims are kLanes apart, then the warps, in order.
+  float v[16];
+  dw.get(v);
 #pragma unroll
   for (int k = 0; k < 16; ++k)
 #pragma unroll
-    for (int o = Walk<D>::kLanes; o < 32; o <<= 1)
-      dw[k] += __shfl_xor_sync(0xffffffffu, dw[k], o);
+    for (int o = Walk<D>::kLanes; o < 32; o <<= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
   float* sums = cs[0];
   if ((threadIdx.x & 31) < Walk<D>::kLanes) {
 #pragma unroll
     for (int k = 0; k < 16; ++k)
-      sums[(threadIdx.x >> 5) * D + (k >> 3) * (D / 2) + lane * 8 + (k & 7)] = dw[k];
+      sums[(threadIdx.x >> 5) * D + (k >> 3) * (D / 2) + lane * 8 + (k & 7)] = v[k];
   }
   __syncthreads();
   if (threadIdx.x < D) {

@@ -24,6 +24,8 @@ constexpr int kGroup = 8;                    // passes over which the angles are
 // Floats of the angles of a group's tokens: 8 passes of 32 rows (d = 128) or 64 are
 // 2 + 256 / heads tokens and more; fewer passes a group where that does not fit.
 constexpr int kAngles = 36 * 128;
+// A token's angles cost a CTA about as much as the rows of this many heads.
+constexpr int kTokenCost = 6;
 
 // cos and sin (times m) of position * f / 2^64 turns.  Products wrap at whole
 // turns; the nearest quarter turn is taken off as an integer, so the rest, at
@@ -69,6 +71,27 @@ struct Raw {
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int i = 0; i < kWords; ++i) w[i] = 0;
+  }
+  // The same through shared memory, where a thread has places of its own, 16 bytes
+  // in each kBytes / kPieces of a pass: it waits for its own copies only.
+  static constexpr int kPieces = kWords / 4, kBytes = kPieces * kThreads * 16;
+  __device__ __forceinline__ static void fetch(uint32_t to, const void* src, int64_t off) {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      constexpr int kPer = kPieces / 2;
+      const uint8_t* p = static_cast<const uint8_t*>(src) +
+                         (off + i / kPer * (D / 2)) * (kBf16 ? 2 : 4) + i % kPer * 16;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * kThreads * 16),
+                   "l"(p)
+                   : "memory");
+    }
+  }
+  __device__ __forceinline__ void read(const uint8_t* from) {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const uint4 x = *reinterpret_cast<const uint4*>(from + i * kThreads * 16);
+      w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+    }
   }
 };
 
@@ -171,12 +194,15 @@ __device__ __forceinline__ float weight_at(const void* w, int bf16, int i) {
 // in which the lanes take them, 16 bytes side by side: the first 4 of all lanes'
 // pairs, then the others.  Of halves a run apart a lane's pairs are 8 lane .. 8 lane
 // + 7; of neighbours, 4 lane .. 4 lane + 3 and those d / 4 on.
+// A thread computes those of one frequency.
 template <int D, bool kInterleaved>
-__device__ __forceinline__ void angles(const RopeArgs& a, int64_t t0, int tokens, float* cs) {
-  for (int i = threadIdx.x; i < tokens * (D / 2); i += kThreads) {
-    const int t = i / (D / 2), f = i - t * (D / 2);
-    const float2 x = turn_of(a.positions[t0 + t], a.freqs[f], a.mscale);
-    const int at = kInterleaved ? f : (f >> 2 & 1) * (D / 4) + (f >> 3) * 4 + (f & 3);
+__device__ __forceinline__ void angles(const RopeArgs& a, int64_t freq, int64_t t0, int tokens,
+                                       float* cs) {
+  constexpr int kFreqs = D / 2;
+  const int f = threadIdx.x % kFreqs;
+  const int at = kInterleaved ? f : (f >> 2 & 1) * (D / 4) + (f >> 3) * 4 + (f & 3);
+  for (int t = threadIdx.x / kFreqs; t < tokens; t += kThreads / kFreqs) {
+    const float2 x = turn_of(a.positions[t0 + t], freq, a.mscale);
     cs[t * D + at] = x.x;
     cs[t * D + D / 2 + at] = x.y;
   }
@@ -245,16 +271,17 @@ template <int D, bool kInterleaved, typename Row>
 __device__ __forceinline__ void walk_rows(const RopeArgs& a, const Walk<D>& w, float (*cs)[kAngles],
                                           Row row) {
   const int group = w.group();
+  const int64_t freq = a.freqs[threadIdx.x % (D / 2)];
   int token, next_token;
   int tokens = w.tokens(w.first, group, &token);
-  angles<D, kInterleaved>(a, w.t0 + token, tokens, cs[0]);
+  angles<D, kInterleaved>(a, freq, w.t0 + token, tokens, cs[0]);
   __syncthreads();
   int buffer = 0;
   for (uint32_t from = w.first; from < w.end; from += group * Walk<D>::kStep) {
     const uint32_t then = from + group * Walk<D>::kStep;
     if (then < w.end) {
       tokens = w.tokens(then, group, &next_token);
-      angles<D, kInterleaved>(a, w.t0 + next_token, tokens, cs[buffer ^ 1]);
+      angles<D, kInterleaved>(a, freq, w.t0 + next_token, tokens, cs[buffer ^ 1]);
     }
     for (uint32_t r = from; r < min(then, w.end); r += Walk<D>::kStep) row(cs[buffer], token);
     __syncthreads();
@@ -315,9 +342,26 @@ __global__ void __launch_bounds__(kThreads, kFwdPerSm) norm_rope_kernel(const Ro
   });
 }
 
+// The gradients' kernel has two inputs: bf16 values come through a ring in shared
+// memory, kDepth passes under way.  fp32 ones, which are twice the bytes a pass,
+// come in registers, one pass ahead, as the forward's do (32K tokens of 32 + 4 heads
+// of 128 in fp32: 455 us through the ring, 287 in registers; the bf16 forward of 64
+// + 8 heads 241 and 191).
+template <int D, bool kBf16>
+struct Ring {
+  using R = Raw<D, kBf16>;
+  static constexpr int kDepth = kBf16 ? 3 : 1;
+  static constexpr int kPass = kBf16 ? 2 * R::kBytes : 0;
+  static constexpr int kSmem = static_cast<int>(2 * kAngles * sizeof(float)) + kDepth * kPass;
+};
 template <int D, bool kBf16, bool kInterleaved>
 __global__ void __launch_bounds__(kThreads, kBwdPerSm) norm_rope_bwd_kernel(const RopeArgs a) {
-  __shared__ __align__(16) float cs[2][kAngles];
+  using R = Raw<D, kBf16>;
+  constexpr int kDepth = Ring<D, kBf16>::kDepth, kPass = Ring<D, kBf16>::kPass;
+  extern __shared__ __align__(16) uint8_t dyn[];  // the angles, then the ring
+  float(*cs)[kAngles] = reinterpret_cast<float(*)[kAngles]>(dyn);
+  uint8_t* mine = dyn + 2 * kAngles * sizeof(float) + threadIdx.x * 16;
+  const uint32_t place = static_cast<uint32_t>(__cvta_generic_to_shared(mine));
   Walk<D> w;
   let_next_start();
   if (!w.begin(a)) {  // its sums are read
@@ -340,23 +384,47 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm) norm_rope_bwd_kernel(cons
   }
 #pragma unroll
   for (int k = 0; k < 4; ++k) dw.a[k] = dw.b[k] = both(0.f);
-  Raw<D, kBf16> x_ahead, g_ahead;
-  x_ahead.clear();
-  const auto load = [&](const Walk<D>& at) {
-    if (at.in()) {
-      g_ahead.load(grad, (at.t0 + at.t) * dy_stride + at.h * D + lane * 8);
-      if (norm) x_ahead.load(src, (at.t0 + at.t) * stride + at.h * D + lane * 8);
-    } else {
-      g_ahead.clear();
-      x_ahead.clear();
+  Walk<D> ahead = w;
+  R next_g, next_x;  // fp32
+  const auto fetch = [&](int slot) {
+    if constexpr (!kBf16) {
+      next_g.clear();
+      next_x.clear();
     }
+    if (ahead.in()) {
+      const int64_t t = ahead.t0 + ahead.t, h = ahead.h * D + lane * 8;
+      if constexpr (kBf16) {
+        R::fetch(place + slot * kPass, grad, t * dy_stride + h);
+        if (norm) R::fetch(place + slot * kPass + R::kBytes, src, t * stride + h);
+      } else {
+        next_g.load(grad, t * dy_stride + h);
+        if (norm) next_x.load(src, t * stride + h);
+      }
+    }
+    ahead.next();
+    if constexpr (kBf16) asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  load(w);
+#pragma unroll
+  for (int k = 0; k < kDepth; ++k) fetch(k);
+  int slot = 0;
   walk_rows<D, kInterleaved>(a, w, cs, [&](const float* c, int token) {
     const Walk<D> at = w;
-    Pairs<D, kBf16, kInterleaved> g(g_ahead), x(x_ahead);
+    R raw_g, raw_x;
+    if constexpr (kBf16) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+      raw_g.clear();
+      raw_x.clear();
+      if (at.in()) {
+        raw_g.read(mine + slot * kPass);
+        if (norm) raw_x.read(mine + slot * kPass + R::kBytes);
+      }
+    } else {
+      raw_g = next_g;
+      raw_x = next_x;
+      fetch(0);
+    }
+    Pairs<D, kBf16, kInterleaved> g(raw_g), x(raw_x);
     w.next();
-    load(w);
     g.template turn<true>(c + (at.in() ? at.t - token : 0) * D, lane);
     if (norm) {
       float2 ss = both(0.f), xu = both(0.f), u[8];
@@ -381,6 +449,10 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm) norm_rope_bwd_kernel(cons
     }
     const int64_t to = ((at.t0 + at.t) * H + at.h) * D + lane * 8;
     if (at.in() && MSA_IN_RANGE(to, D / 2 + 8, a.n * H * D, a.status)) g.store(a.out[w.side], to);
+    if constexpr (kBf16) {
+      fetch(slot);
+      slot = slot + 1 == kDepth ? 0 : slot + 1;
+    }
   });
   if (!norm) return;
   // Lanes of the same dims are kLanes apart, then the warps, in order.
@@ -429,18 +501,31 @@ __global__ void __launch_bounds__(D * kSlices) norm_rope_dw_kernel(const RopeArg
     static_cast<float*>(a.dweight[side])[k] = sum;
 }
 
-// CTAs of the two sides: at most `all`, in the proportion of their rows, and none
-// without a pass.
+// CTAs of the two sides: at most `all`, shared by what their rows and angles cost
+// (with 64 + 8 heads by rows alone, the keys' CTAs ended last: 423 us for 276),
+// and none without a pass.
 void split_ctas(int64_t n, const int* heads, int d, int64_t all, int* ctas) {
   const int step = kThreads / (d / 16);
   const int64_t q = (n * heads[0] + step - 1) / step, k = (n * heads[1] + step - 1) / step;
   if (q + k > all) {
-    ctas[1] = k ? static_cast<int>(max64(1, all * k / (q + k))) : 0;
-    ctas[0] = static_cast<int>(all - ctas[1]);
+    const int64_t wq = heads[0] + kTokenCost, wk = heads[1] + kTokenCost;
+    ctas[1] = k ? static_cast<int>(max64(1, min64(k, (all * wk + (wq + wk) / 2) / (wq + wk)))) : 0;
+    ctas[0] = static_cast<int>(min64(q, all - ctas[1]));
   } else {
     ctas[0] = static_cast<int>(max64(1, q));
     ctas[1] = static_cast<int>(k);
   }
+}
+
+template <int D, bool kBf16, bool kInterleaved>
+cudaError_t launch_bwd(const RopeArgs& a, cudaStream_t st) {
+  constexpr int kSmem = Ring<D, kBf16>::kSmem;
+  const cudaError_t e = cudaFuncSetAttribute(norm_rope_bwd_kernel<D, kBf16, kInterleaved>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(static_cast<unsigned>(a.ctas[0] + a.ctas[1]));
+  return launch_after(norm_rope_bwd_kernel<D, kBf16, kInterleaved>, grid, kThreads, kSmem, st, false,
+                      a);
 }
 
 }  // namespace
@@ -469,19 +554,17 @@ void norm_rope_bwd_ctas(int64_t n, const int* heads, int d, int* ctas) {
 
 cudaError_t launch_norm_rope_bwd(const RopeArgs& a, cudaStream_t st) {
   if (a.n > 0) {
-    const dim3 grid(static_cast<unsigned>(a.ctas[0] + a.ctas[1]));
-    void (*kernel)(RopeArgs);
+    cudaError_t e;
     if (a.d == 128)
-      kernel = a.bf16 ? (a.interleaved ? norm_rope_bwd_kernel<128, true, true>
-                                       : norm_rope_bwd_kernel<128, true, false>)
-                      : (a.interleaved ? norm_rope_bwd_kernel<128, false, true>
-                                       : norm_rope_bwd_kernel<128, false, false>);
+      e = a.bf16 ? (a.interleaved ? launch_bwd<128, true, true>(a, st)
+                                  : launch_bwd<128, true, false>(a, st))
+                 : (a.interleaved ? launch_bwd<128, false, true>(a, st)
+                                  : launch_bwd<128, false, false>(a, st));
     else
-      kernel = a.bf16 ? (a.interleaved ? norm_rope_bwd_kernel<64, true, true>
-                                       : norm_rope_bwd_kernel<64, true, false>)
-                      : (a.interleaved ? norm_rope_bwd_kernel<64, false, true>
-                                       : norm_rope_bwd_kernel<64, false, false>);
-    const cudaError_t e = launch_after(kernel, grid, kThreads, 0, st, false, a);
+      e = a.bf16 ? (a.interleaved ? launch_bwd<64, true, true>(a, st)
+                                  : launch_bwd<64, true, false>(a, st))
+                 : (a.interleaved ? launch_bwd<64, false, true>(a, st)
+                                  : launch_bwd<64, false, false>(a, st));
     if (e != cudaSuccess) return e;
   }
   if (!a.weight[0] && !a.weight[1]) return cudaSuccess;

@@ -39,48 +39,52 @@ __device__ __forceinline__ bool span_of(const RowsArgs& a, int b, Span* s) {
   return true;
 }
 
-// This thread's rows: token and head of each, and the slot's row in the pool
-// ([n_pages * Hkv * block]; -1: no such page).
+// This thread's rows: kRows of the CTA's, kStep apart, in the order of k and v.
+constexpr uint32_t kNoSlot = 0xffffffffu;
 template <int D>
 struct Rows {
-  int token[kRows];   // within the sequence; -1: past its end
-  int head[kRows];
-  int64_t slot[kRows];
+  static constexpr int kLanes = D / kPer, kStep = kThreads / kLanes;
+  static_assert(kRows <= kLanes, "a lane looks up one row");
+  int64_t row0;          // first row of the CTA, of all rows of k and v
+  int left;              // rows of the CTA
+  uint32_t slot[kRows];  // row in the pool ([n_pages * Hkv * block], at 136 bytes a slot or
+                         // more: 32 bits), kNoSlot: no such page
 
-  __device__ __forceinline__ bool find(const RowsArgs& a, const Span& s, uint32_t cta) {
-    constexpr int kLanes = D / kPer, kStep = kThreads / kLanes;
-    const int64_t row0 = static_cast<int64_t>(cta) * (kStep * kRows);
-    // Most launches have fewer than 2^32 rows: one 32-bit division for the CTA.
-    const int64_t t0 = row0 >> 32 ? row0 / a.Hkv
-                                  : static_cast<uint32_t>(row0) / static_cast<uint32_t>(a.Hkv);
-    if (t0 >= s.n) return false;
-    uint32_t h = static_cast<uint32_t>(row0 - t0 * a.Hkv) + threadIdx.x / kLanes;
-    uint32_t up = h / a.Hkv;
-    h -= up * a.Hkv;
-    int64_t t = t0 + up;
-    const int dt = kStep / a.Hkv, dh = kStep - dt * a.Hkv;
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      token[i] = t < s.n ? static_cast<int>(t) : -1;
-      head[i] = h;
-      t += dt;
-      h += dh;
-      if (h >= static_cast<uint32_t>(a.Hkv)) {
-        h -= a.Hkv;
-        ++t;
-      }
-    }
-    return true;
+  __device__ __forceinline__ bool in(int i) const {
+    return static_cast<int>(threadIdx.x) / kLanes + i * kStep < left;
   }
-  __device__ __forceinline__ void look_up(const RowsArgs& a, int b, const Span& s) {
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      slot[i] = -1;
-      if (token[i] < 0) continue;
-      const int at = s.first + token[i];
+  // Offset of row i's values in k and v.
+  __device__ __forceinline__ int64_t at(int i) const {
+    return (row0 + threadIdx.x / kLanes + i * kStep) * D;
+  }
+  // The CTA's rows of the sequence; false: none.
+  __device__ __forceinline__ bool find(const RowsArgs& a, const Span& s, uint32_t cta) {
+    const int64_t from = static_cast<int64_t>(cta) * (kStep * kRows);
+    const int64_t all = static_cast<int64_t>(s.n) * a.Hkv;
+    row0 = static_cast<int64_t>(s.r0) * a.Hkv + from;
+    left = static_cast<int>(min64(all - from, kStep * kRows));
+    return all > from;
+  }
+  // Each lane of a row looks up one of its kRows rows for the others.
+  __device__ __forceinline__ void look_up(const RowsArgs& a, int b, const Span& s, uint32_t cta) {
+    const int lane = threadIdx.x & (kLanes - 1), i = lane % kRows;
+    const int64_t from = static_cast<int64_t>(cta) * (kStep * kRows);
+    // Most launches have fewer than 2^32 rows: one 32-bit division for the CTA.
+    const int64_t t0 = from >> 32 ? from / a.Hkv
+                                  : static_cast<uint32_t>(from) / static_cast<uint32_t>(a.Hkv);
+    const uint32_t x = static_cast<uint32_t>(from - t0 * a.Hkv) + threadIdx.x / kLanes + i * kStep;
+    const uint32_t up = x / static_cast<uint32_t>(a.Hkv);
+    uint32_t mine = kNoSlot;
+    if (in(i)) {
+      const int at = s.first + static_cast<int>(t0) + static_cast<int>(up);
       const int64_t page = cache_page(a.s, b, at >> a.lb, a.n_pages, a.status);
-      if (page >= 0) slot[i] = ((page * a.Hkv + head[i]) << a.lb) + (at & (a.block - 1));
+      if (page >= 0)
+        mine = (static_cast<uint32_t>(page * a.Hkv + (x - up * a.Hkv)) << a.lb) +
+               (at & (a.block - 1));
     }
+#pragma unroll
+    for (int k = 0; k < kRows; ++k)
+      slot[k] = __shfl_sync(0xffffffffu, mine, k, kLanes);
   }
 };
 
@@ -169,15 +173,13 @@ __global__ void __launch_bounds__(kThreads) cache4_append_kernel(const Append4Ar
   Raw<kBf16> v[kRows];
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
-    const int64_t off =
-        ((static_cast<int64_t>(s.r0) + max(rows.token[i], 0)) * a.Hkv + rows.head[i]) * D +
-        lane * kPer;
-    if (rows.token[i] >= 0 && MSA_IN_RANGE(off, kPer, a.total * a.Hkv * D, a.status))
+    const int64_t off = rows.at(i) + lane * kPer;
+    if (rows.in(i) && MSA_IN_RANGE(off, kPer, a.total * a.Hkv * D, a.status))
       v[i].load(src, off);
     else
       v[i].clear();
   }
-  rows.look_up(a, b, s);
+  rows.look_up(a, b, s, blockIdx.x >> 1);
   uint8_t* codes = kv ? a.v_codes : a.k_codes;
   uint8_t* scale = kv ? a.v_scale : a.k_scale;
 #pragma unroll
@@ -191,12 +193,13 @@ __global__ void __launch_bounds__(kThreads) cache4_append_kernel(const Append4Ar
     const int e = poisoned ? 0 : group_exponent4(m);
     uint2 w = v[i].encode(pow2i(-e));
     if (poisoned) w = make_uint2(0, 0);
-    if (rows.slot[i] < 0 ||
-        !MSA_IN_RANGE(rows.slot[i], 1, a.n_pages * a.Hkv << a.lb, a.status))
+    const int64_t at = rows.slot[i];
+    if (rows.slot[i] == kNoSlot ||
+        !MSA_IN_RANGE(at, 1, a.n_pages * a.Hkv << a.lb, a.status))
       continue;
-    *reinterpret_cast<uint2*>(codes + rows.slot[i] * (D / 2) + lane * (kPer / 2)) = w;
+    *reinterpret_cast<uint2*>(codes + at * (D / 2) + lane * (kPer / 2)) = w;
     if ((lane & 1) == 0)
-      scale[rows.slot[i] * (D / kGroup4) + (lane >> 1)] =
+      scale[at * (D / kGroup4) + (lane >> 1)] =
           static_cast<uint8_t>(poisoned ? 255 : e + 127);
   }
 }
@@ -215,7 +218,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReadArgs a) 
   if (!span_of(a, b, &s)) return;
   Rows<D> rows;
   if (!rows.find(a, s, blockIdx.x >> 1)) return;
-  rows.look_up(a, b, s);
+  rows.look_up(a, b, s, blockIdx.x >> 1);
   const int lane = threadIdx.x & (kLanes - 1);
   const uint8_t* codes = kv ? a.v_codes : a.k_codes;
   const void* scale = kv ? a.v_scale : a.k_scale;
@@ -224,7 +227,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReadArgs a) 
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
     const int64_t at = rows.slot[i];
-    const bool on = at >= 0 && MSA_IN_RANGE(at, 1, a.n_pages * a.Hkv << a.lb, a.status);
+    const bool on = rows.slot[i] != kNoSlot && MSA_IN_RANGE(at, 1, a.n_pages * a.Hkv << a.lb, a.status);
 #pragma unroll
     for (int r = 0; r < kRuns; ++r) {
       const int v = r * (D / kRuns) + lane * kRun;  // first value
@@ -249,9 +252,9 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReadArgs a) 
   void* dst = kv ? a.v : a.k;
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
-    if (rows.token[i] < 0) continue;
-    const int64_t row = (static_cast<int64_t>(s.r0) + rows.token[i]) * a.Hkv + rows.head[i];
-    if (!MSA_IN_RANGE(row * D, D, a.total * a.Hkv * D, a.status)) continue;
+    if (!rows.in(i)) continue;
+    const int64_t row = rows.at(i);
+    if (!MSA_IN_RANGE(row, D, a.total * a.Hkv * D, a.status)) continue;
 #pragma unroll
     for (int r = 0; r < kRuns; ++r) {
       float v[8];
@@ -271,7 +274,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReadArgs a) 
       const float g = kBits == 4 ? e8m0_to_float(f[i][kBits == 4 ? r : 0]) : __uint_as_float(f[i][0]);
 #pragma unroll
       for (int k = 0; k < kRun; ++k) v[k] *= g;
-      const int64_t off = row * D + r * (D / kRuns) + lane * kRun;
+      const int64_t off = row + r * (D / kRuns) + lane * kRun;
       if constexpr (kBf16) {
         uint32_t o[4];
 #pragma unroll

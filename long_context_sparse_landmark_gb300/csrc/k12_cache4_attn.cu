@@ -348,7 +348,7 @@ struct Body4 {
 
   // Whether no scale of the pair is above the warp's references or more than 27
   // binades below: then code * 2^{13 - (r - x)} are halves, exactly, and the slots'
-  // own scales need no looking at.  Of chunks that are not masked.
+  // own scales need no looking at.  (Slots that no row attends: see blank().)
   __device__ __forceinline__ bool fits(uint32_t stage) const {
     const uint32_t at = stage + (threadIdx.x & 31) * kGroups;
     const uint32_t k2 = __byte_perm(rk, 0, 0x1010), v2 = __byte_perm(rv, 0, 0x1010);
@@ -368,22 +368,52 @@ struct Body4 {
     // (A byte above its reference leaves a borrow, and 0xff.. in its own half.)
     return __all_sync(0xffffffffu, __vmaxu2(m, 0x001b001bu) == 0x001b001bu);
   }
+  // Slots that no row attends hold anything: their scales become the references,
+  // so that they fit and are finite.  `off`: bit c for the lane's slot of chunk c.
+  __device__ __forceinline__ void blank(uint32_t stage, uint32_t off) const {
+    const uint32_t at = stage + (threadIdx.x & 31) * kGroups;
+    const uint32_t k = rk == kUnset ? 0x01010101u : rk * 0x01010101u;
+    const uint32_t v = rv == kUnset ? 0x01010101u : rv * 0x01010101u;
+    each<kPair>([&](auto c) {
+      constexpr int from = decltype(c)::value * kChunkBytes + 2 * kCodes;
+      if (off >> decltype(c)::value & 1) {
+        if constexpr (D == 128) {
+          asm volatile("st.shared.u32 [%0 + %1], %2;" ::"r"(at), "n"(from), "r"(k) : "memory");
+          asm volatile("st.shared.u32 [%0 + %1], %2;" ::"r"(at), "n"(from + kScales), "r"(v)
+                       : "memory");
+        } else {
+          asm volatile("st.shared.u16 [%0 + %1], %2;" ::"r"(at), "n"(from),
+                       "h"(static_cast<uint16_t>(k))
+                       : "memory");
+          asm volatile("st.shared.u16 [%0 + %1], %2;" ::"r"(at), "n"(from + kScales),
+                       "h"(static_cast<uint16_t>(v))
+                       : "memory");
+        }
+      }
+    });
+    __syncwarp();
+  }
   // References for a pair that does not fit, with some room above its largest
   // scales; false if there are none.
-  __device__ __forceinline__ bool refer(uint32_t stage) {
+  __device__ __forceinline__ bool refer(uint32_t stage, uint32_t off) {
     const uint32_t at = stage + (threadIdx.x & 31) * kGroups;
     uint32_t k = 1, v = 1;
     each<kPair * kGroups>([&](auto i) {
       constexpr int c = decltype(i)::value / kGroups, j = decltype(i)::value % kGroups;
-      k = max(k, lds8<c * kChunkBytes + 2 * kCodes + j>(at));
-      v = max(v, lds8<c * kChunkBytes + 2 * kCodes + kScales + j>(at));
+      const uint32_t kb = lds8<c * kChunkBytes + 2 * kCodes + j>(at);
+      const uint32_t vb = lds8<c * kChunkBytes + 2 * kCodes + kScales + j>(at);
+      if (!(off >> c & 1)) {
+        k = max(k, kb);
+        v = max(v, vb);
+      }
     });
     k = __reduce_max_sync(0xffffffffu, k);
     v = __reduce_max_sync(0xffffffffu, v);
     if (k == 255 || v == 255) return false;
     const int k0 = rk, v0 = rv;
-    rk = k + 4;
-    rv = v + 4;
+    rk = min(static_cast<int>(k) + 4, 254);  // below NaN's, which never fits
+    rv = min(static_cast<int>(v) + 4, 254);
+    if (__any_sync(0xffffffffu, off)) blank(stage, off);
     if (!fits(stage)) {
       rk = k0;
       rv = v0;
@@ -550,7 +580,26 @@ struct Body4 {
   }
 
   // Of a pair that fits: its scores are raw, its values in one unit.
-  __device__ __forceinline__ void softmax_one() {
+  // kEdge: some slot is masked for some row; live: bit c for chunk c.
+  template <bool kEdge>
+  __device__ __forceinline__ void softmax_one(const CacheAttnArgs& a, int key0, uint32_t live) {
+    if constexpr (kEdge) {
+      const int g = (threadIdx.x & 31) >> 2, t4 = threadIdx.x & 3;
+#pragma unroll
+      for (int n = 0; n < kNt; ++n)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int p = rows->pos[8 * n + 2 * t4 + r];
+#pragma unroll
+          for (int st = 0; st < 2 * kPair; ++st)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int key = key0 + 16 * st + 8 * k + g;
+              if (!(live >> (st >> 1) & 1) || key > p || p - key >= a.window)
+                s[st][n][2 * k + r] = -INFINITY;
+            }
+        }
+    }
     constexpr bool kKeep = kNt < 4;  // else they are computed twice: registers
     float2 z[2 * kPair][kKeep ? kNt : 1][2];
     const auto exponents = [&] {
@@ -599,7 +648,11 @@ struct Body4 {
           const float2 x =
               kKeep ? z[st][kKeep ? n : 0][k]
                     : __ffma2_rn(make_float2(s[st][n][2 * k], s[st][n][2 * k + 1]), f[n], base[n]);
-          const float2 w = make_float2(ex2(x.x), ex2(x.y));
+          float2 w = make_float2(ex2(x.x), ex2(x.y));
+          if (kEdge) {  // also where no slot was attended yet
+            if (s[st][n][2 * k] == -INFINITY) w.x = 0.f;
+            if (s[st][n][2 * k + 1] == -INFINITY) w.y = 0.f;
+          }
           sum = __fadd2_rn(sum, w);
           put_weights(st, n, k, w);
         }
@@ -609,8 +662,8 @@ struct Body4 {
     }
   }
 
-  template <bool kEdge>
   __device__ __forceinline__ void softmax(const CacheAttnArgs& a, int key0, bool on) {
+    constexpr bool kEdge = true;
     const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     float2 lvs[2][2];  // [step][slot g, g + 8]
     float mx[kNt][2];
@@ -882,25 +935,43 @@ __global__ void __launch_bounds__(kThreads, Body::kPerSm)
     body.begin(dyn);
     const int pos0 = body.rows->pos[0];  // the first row's position, the last's
     const int pos1 = body.rows->pos[min(kTile, p.rows - rt * kTile) - 1];
-    // Slots that every row attends, as first slots of pairs that lie in them.
+    // Slots that every row attends, as first slots of pairs that lie in them; slots
+    // that some row does.
     const int all0 = pos1 - a.window + 1, all1 = pos0 - (kPair * kChunk - 1);
+    const int some0 = pos0 - a.window + 1, some1 = pos1;
     uint32_t stage = ring;
     int key0 = e.win0 + mine * kChunk;
     int x = mine;
     for (int k = 0; k < n; ++k, key0 += kWarps * kPair * kChunk, x += kWarps * kPair) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
       __syncwarp();
-      // Pair k was looked up with the latest 32, or with those before.
-      uint32_t off = 0;
+      uint32_t without = 0;
 #pragma unroll
-      for (int i = 0; i < kPair; ++i) off |= dead[i][0] | dead[i][1];
-      const bool edge = off || key0 < all0 || key0 > all1 || x + kPair > x1;
-      if (!edge && (body.fits(stage) || body.refer(stage)) && body.level) {
+      for (int i = 0; i < kPair; ++i) without |= dead[i][0] | dead[i][1];
+      const bool edge = without || key0 < all0 || key0 > all1 || x + kPair > x1;
+      uint32_t live = (1u << kPair) - 1, off = 0;
+      if (edge) {
+        // Pair k was looked up with the latest 32, or with those before.
+        const int newest = min(k + kStages, n) - 1;
+        const bool now = (newest >> 5) == (k >> 5);
+#pragma unroll
+        for (int i = 0; i < kPair; ++i) {
+          const uint32_t d = now ? dead[i][1] : dead[i][0];
+          if ((d >> (k & 31) & 1) || x + i >= x1) live &= ~(1u << i);
+          const int key = key0 + i * kChunk + lane;
+          if (!(live >> i & 1) || key < some0 || key > some1) off |= 1u << i;
+        }
+        body.blank(stage, off);
+      }
+      if ((body.fits(stage) || body.refer(stage, off)) && body.level) {
         each<kPair>([&](auto i) {
           body.template scores<false, decltype(i)::value>(stage + decltype(i)::value *
                                                                       Body::kChunkBytes);
         });
-        body.softmax_one();
+        if (edge)
+          body.template softmax_one<true>(a, key0, live);
+        else
+          body.template softmax_one<false>(a, key0, live);
         each<kPair>([&](auto i) {
           body.template values<false, decltype(i)::value>(stage + decltype(i)::value *
                                                                       Body::kChunkBytes);
@@ -908,15 +979,11 @@ __global__ void __launch_bounds__(kThreads, Body::kPerSm)
       } else {
 #pragma unroll 1
         for (int i = 0; i < min(kPair, x1 - x); ++i) {
-          const int newest = min(k + kStages, n) - 1;
-          const bool now = (newest >> 5) == (k >> 5);
-          const uint32_t d = i == 0 ? (now ? dead[0][1] : dead[0][0]) : (now ? dead[kPair - 1][1] : dead[kPair - 1][0]);
-          const bool live = !(d >> (k & 31) & 1);
           const uint32_t from = stage + i * Body::kChunkBytes;
           body.read_scales(from);
           __syncwarp();
           body.template scores<true, 0>(from);
-          body.template softmax<true>(a, key0 + i * kChunk, live);
+          body.softmax(a, key0 + i * kChunk, live >> i & 1);
           body.template values<true, 0>(from);
           __syncwarp();
         }

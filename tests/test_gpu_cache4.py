@@ -367,6 +367,28 @@ def test_nan_slots_reach_the_rows_that_attend_them_only(dtype):
                     assert np.abs(l[0, :, row] - ref[1][0, :, row]).max() < 1e-4
 
 
+def test_nan_slots_beside_the_largest_scales():
+    """Scales next to NaN's byte, and slots that hold NaN among them."""
+    n, d = 96, 64
+    rng = np.random.default_rng(6)
+    for kbig, vbig in ((True, False), (False, True)):
+        k, v = rng.normal(size=(2, n, 1, d))
+        (k if kbig else v)[:] *= 2.0 ** 123
+        for where, at in (("k", 40), ("v", 70)):
+            kk, vv = k.astype(np.float32), v.astype(np.float32)
+            (kk if where == "k" else vv)[at, 0, 5] = np.inf
+            cache = new_cache(4, 1, d, 32)
+            t = np.array([[1, 3, 0]], dtype=np.int32)
+            msa.cache_append(cache, torch.as_tensor(kk, device=DEV), torch.as_tensor(vv, device=DEV), i32([0, n]), i32(t),
+                             i32([n]), n)
+            q = torch.as_tensor(rng.normal(size=(1, 1, 2, d)) * (2.0 ** -123 if kbig else 1.0), device=DEV).float()
+            out, lse = msa.cache_attention(q, cache, i32(t), i32([n]))
+            assert torch.isnan(out).all()
+            assert torch.isnan(lse).all() == (where == "k")
+            short, _ = msa.cache_attention(q, cache, i32(t), i32([at]))
+            assert torch.isfinite(short).all()
+
+
 def test_bad_pages_and_lengths():
     """A page that does not exist is not attended; a length that cannot be is clamped."""
     cache, pool, t = filled([100, 64], 1, 64, 32, seed=4, extra=2)

@@ -103,12 +103,12 @@ __device__ __forceinline__ uint32_t slot_scales(uint32_t w, uint32_t* h) {
 template <int D, int kNt, int kTerms>
 struct Body4 {
   static constexpr int kTile = 8 * kNt;
-  static constexpr int kPerSm = kNt == 1 ? 3 : 2;
+  static constexpr int kPerSm = kNt == 1 || kNt * kTerms == 2 ? 3 : 2;
   // Chunks that a warp takes together: two, where the registers allow it, so that
   // one's fixed latencies pass in the other's shadow.
   static constexpr int kPair = kNt * kTerms == 1 ? 2 : 1;
   static constexpr int kStages = (kPair == 2 || kNt == 4 ? 4 : 3) / kPair * (D == 128 ? 1 : 2);  // pairs
-  static constexpr bool kQShared = kNt * kTerms > 2;
+  static constexpr bool kQShared = kNt > 1;
   static constexpr int kCodes = kChunk * D / 2, kScales = kChunk * D / kGroup4;  // of K, or of V
   static constexpr int kChunkBytes = 2 * kCodes + 2 * kScales;
   static constexpr int kStageBytes = kPair * kChunkBytes;
@@ -123,7 +123,7 @@ struct Body4 {
     float2 slot[kChunk];              // 2^x, and y
     uint32_t k[kChunk * kGroups];     // half 2^{13 - delta}, twice: [slot][group]
     uint16_t v[kGroups][40];          // the half: [group][slot], rows 80 bytes apart
-    float refs[kNt == 4 ? 4 * kNt * 32 : 4];  // see M() below
+    float refs[kNt >= 2 ? 4 * kNt * 32 : 4];  // see M() below
   };
   // Rows of a unit, for all warps: their fragments [term][k-step][tile][lane],
   // score scales and positions.
@@ -142,7 +142,7 @@ struct Body4 {
   float l[kNt][2];  // in units of 2^M, o of 2^{M + D0 - kPBits}
   // M and D0 of rows 2t, 2t+1: looked at where a reference moves or a chunk does not
   // fit.  Those of four tiles are in shared memory (registers: 304 spilled bytes).
-  static constexpr bool kCold = kNt == 4;
+  static constexpr bool kCold = kNt >= 2;
   struct Refs {
     float v[2][kNt][2];
   } refs;
@@ -600,7 +600,7 @@ struct Body4 {
             }
         }
     }
-    constexpr bool kKeep = kNt < 4;  // else they are computed twice: registers
+    constexpr bool kKeep = kNt < 2;  // else they are computed twice: registers
     float2 z[2 * kPair][kKeep ? kNt : 1][2];
     const auto exponents = [&] {
       bool high = false;
@@ -1036,8 +1036,10 @@ int cache4_attn_tile_rows(int rows, int in_bf16) {
   return rows <= 8 ? 8 : rows <= 16 || !in_bf16 ? 16 : 32;
 }
 int cache4_attn_max_ctas(int tile_rows, int in_bf16) {
-  (void)in_bf16;
-  return kSms * (tile_rows == 8 ? Body4<128, 1, 1>::kPerSm : Body4<128, 2, 1>::kPerSm);
+  return kSms * (tile_rows == 8    ? Body4<128, 1, 1>::kPerSm
+                 : tile_rows == 32 ? Body4<128, 4, 1>::kPerSm
+                 : in_bf16         ? Body4<128, 2, 1>::kPerSm
+                                   : Body4<128, 2, 2>::kPerSm);
 }
 
 cudaError_t launch_cache4_attn(const Cache4AttnArgs& a, cudaStream_t st) {

@@ -614,13 +614,31 @@ def cache_evict(cache, table, lens, weights, dst_table, budget: int, recent: int
 
 
 # -- the 4-bit KV cache, and reading either back: `cache` a KvCache4Struct ------
+# A step of these is mostly host time: each tensor is checked in one expression.
+
+def _refuse(*tensors):
+    """Raises what is wrong with them: ``_usable`` said that something is."""
+    for t in tensors:
+        _addr(t)
+    raise TypeError("table, lens and cu must be int32, lse float32")
+
+
+_I32, _FL32 = torch.int32, torch.float32
+
 
 def cache4_append(cache, k, v, cu, max_new: int, table, lens, stream=None) -> None:
     """msa_cache4_append: rows cu[b]..cu[b+1] of k, v become sequence b's last slots."""
-    _check(_lib.msa_cache4_append(cache, _addr(k), _addr(v), _i32ptr(cu, "cu"), k.shape[0],
-                                  int(max_new), _i32ptr(table, "table"), table.shape[1],
-                                  _i32ptr(lens, "lens"), table.shape[0], _dt(k),
-                                  _raw_stream(stream)))
+    if not (k.is_cuda and k.is_contiguous() and v.is_cuda and v.is_contiguous() and
+            cu.is_cuda and cu.is_contiguous() and cu.dtype is _I32 and
+            table.is_cuda and table.is_contiguous() and table.dtype is _I32 and
+            lens.is_cuda and lens.is_contiguous() and lens.dtype is _I32):
+        _refuse(k, v, cu, table, lens)
+    b, nb = table.shape
+    st = _lib.msa_cache4_append(cache, k.data_ptr(), v.data_ptr(), cu.data_ptr(), k.shape[0],
+                                max_new, table.data_ptr(), nb, lens.data_ptr(), b, _dt(k),
+                                _raw_stream(stream))
+    if st != MSA_OK:
+        _check(st)
 
 
 def cache4_attn_workspace_size(cache, max_blocks: int, batch: int, n_q: int, Hq: int,
@@ -633,20 +651,35 @@ def cache4_attn_workspace_size(cache, max_blocks: int, batch: int, n_q: int, Hq:
 def cache4_attn(cache, q, table, lens, window: int, scale: float, out, lse, workspace,
                 stream=None) -> None:
     """msa_cache4_attn: query tokens q [batch, n_q, Hq, d] over the cache."""
+    if not (q.is_cuda and q.is_contiguous() and table.is_cuda and table.is_contiguous() and
+            table.dtype is _I32 and lens.is_cuda and lens.is_contiguous() and
+            lens.dtype is _I32 and out.is_cuda and out.is_contiguous() and lse.is_cuda and
+            lse.is_contiguous() and lse.dtype is _FL32 and workspace.is_cuda and
+            workspace.is_contiguous()):
+        _refuse(q, table, lens, out, lse, workspace)
     b, n_q, Hq, _ = q.shape
-    _check(_lib.msa_cache4_attn(cache, _addr(q), _i32ptr(table, "table"), table.shape[1],
-                                _i32ptr(lens, "lens"), b, n_q, Hq, int(window), float(scale),
-                                _addr(out), _f32ptr(lse, "lse"), _dt(q), _dt(out),
-                                _addr(workspace), workspace.nbytes, _raw_stream(stream)))
+    st = _lib.msa_cache4_attn(cache, q.data_ptr(), table.data_ptr(), table.shape[1],
+                              lens.data_ptr(), b, n_q, Hq, window, scale, out.data_ptr(),
+                              lse.data_ptr(), _dt(q), _dt(out), workspace.data_ptr(),
+                              workspace.nbytes, _raw_stream(stream))
+    if st != MSA_OK:
+        _check(st)
 
 
 def cache_read(cache, bits: int, cu, max_rows: int, table, lens, k, v, stream=None) -> None:
     """msa_cache_read (bits 8) or msa_cache4_read (4): sequence b's last slots
     into rows cu[b]..cu[b+1] of k, v [total, Hkv, d]."""
+    if not (k.is_cuda and k.is_contiguous() and v.is_cuda and v.is_contiguous() and
+            cu.is_cuda and cu.is_contiguous() and cu.dtype is _I32 and
+            table.is_cuda and table.is_contiguous() and table.dtype is _I32 and
+            lens.is_cuda and lens.is_contiguous() and lens.dtype is _I32):
+        _refuse(k, v, cu, table, lens)
+    b, nb = table.shape
     f = _lib.msa_cache_read if bits == 8 else _lib.msa_cache4_read
-    _check(f(cache, _i32ptr(cu, "cu"), k.shape[0], int(max_rows), _i32ptr(table, "table"),
-             table.shape[1], _i32ptr(lens, "lens"), table.shape[0], _addr(k), _addr(v), _dt(k),
-             _raw_stream(stream)))
+    st = f(cache, cu.data_ptr(), k.shape[0], max_rows, table.data_ptr(), nb, lens.data_ptr(), b,
+           k.data_ptr(), v.data_ptr(), _dt(k), _raw_stream(stream))
+    if st != MSA_OK:
+        _check(st)
 
 
 # -- norms of queries and keys with rotation ---------------------------------
@@ -656,13 +689,14 @@ def _tokens(t, what):
     if not t.is_cuda:
         raise ValueError("tensors must be on a CUDA device")
     n, heads, d = t.shape
-    if heads and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d)):
+    sn, sh, sd = t.stride()
+    if heads and (sd != 1 or (heads > 1 and sh != d)):
         raise ValueError(f"{what}: the heads of a token must lie next to each other")
-    return t.data_ptr(), heads * d if n <= 1 else t.stride(0)
+    return t.data_ptr(), heads * d if n <= 1 else sn
 
 
 def _i64ptr(t, what):
-    if t.dtype != torch.int64:
+    if t.dtype is not torch.int64:
         raise TypeError(f"{what} must be int64")
     return _addr(t)
 
@@ -676,12 +710,15 @@ def qk_norm_rope(q, k, positions, freqs, q_weight, k_weight, eps: float, mscale:
     """msa_qk_norm_rope: q [n, Hq, d], k [n, Hkv, d] into q_out, k_out."""
     n, Hq, d = q.shape
     w = q_weight if q_weight is not None else k_weight
+    dt = _dt(q)
     (pq, sq), (pk, sk) = _tokens(q, "q"), _tokens(k, "k")
-    _check(_lib.msa_qk_norm_rope(pq, sq, pk, sk, n, Hq, k.shape[1], d,
-                                 _i64ptr(positions, "positions"), _i64ptr(freqs, "freqs"),
-                                 _opt(q_weight), _opt(k_weight), float(eps), float(mscale),
-                                 1 if interleaved else 0, _addr(q_out), _addr(k_out), _dt(q),
-                                 _dt(q) if w is None else _dt(w), _raw_stream(stream)))
+    st = _lib.msa_qk_norm_rope(pq, sq, pk, sk, n, Hq, k.shape[1], d,
+                               _i64ptr(positions, "positions"), _i64ptr(freqs, "freqs"),
+                               _opt(q_weight), _opt(k_weight), eps, mscale,
+                               1 if interleaved else 0, _addr(q_out), _addr(k_out), dt,
+                               dt if w is None else _dt(w), _raw_stream(stream))
+    if st != MSA_OK:
+        _check(st)
 
 
 def qk_norm_rope_bwd_workspace_size(n: int, Hq: int, Hkv: int, d: int) -> int:

@@ -18,6 +18,7 @@ allocated for the stream the call runs on.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 import torch
@@ -167,7 +168,7 @@ def _run(cache: KVCache, stream, call):
     """call(stream address) with the cache's device current and allocations
     made for the stream that the kernels run on."""
     if stream is None:
-        if torch.cuda.current_device() == cache.index:
+        if torch._C._cuda_getDevice() == cache.index:  # (CUDA is up: there are tensors)
             return call(torch._C._cuda_getCurrentRawStream(cache.index))
         with torch.cuda.device(cache.index):
             return call(torch._C._cuda_getCurrentRawStream(cache.index))
@@ -194,6 +195,7 @@ def cache_append(cache: KVCache | KVCache4, k: torch.Tensor, v: torch.Tensor, cu
     _want(v, "v", (k.dtype,), k.shape, cache.index)
     _want(cu, "cu", (_INT32,), (b + 1,), cache.index)
     append = B.cache4_append if isinstance(cache, KVCache4) else B.cache_append
+    max_new = int(max_new)
     _run(cache, stream, lambda s: append(cache.ref, k, v, cu, max_new, block_table, lens,
                                          stream=s))
 
@@ -212,6 +214,7 @@ def cache_read(cache: KVCache | KVCache4, cu: torch.Tensor, block_table: torch.T
     b, _ = _batch(cache, block_table, lens)
     _want(cu, "cu", (_INT32,), (b + 1,), cache.index)
     shape = (int(total), cache.Hkv, cache.d)
+    max_rows = int(max_rows)
     if dtype not in _INPUTS:
         raise TypeError(f"dtype must be float32 or bfloat16, not {dtype}")
     if out is not None:
@@ -223,13 +226,13 @@ def cache_read(cache: KVCache | KVCache4, cu: torch.Tensor, block_table: torch.T
 
     def call(s):
         if out is not None:
-            kv = out
+            k, v = out
         else:
-            kv = (torch.empty(shape, dtype=dtype, device=cache.device),
-                  torch.empty(shape, dtype=dtype, device=cache.device))
+            k = torch.empty(shape, dtype=dtype, device=cache.device)
+            v = torch.empty_like(k)
         B.cache_read(cache.ref, 4 if isinstance(cache, KVCache4) else 8, cu, max_rows,
-                     block_table, lens, kv[0], kv[1], stream=s)
-        return kv[0], kv[1]
+                     block_table, lens, k, v, stream=s)
+        return k, v
 
     return _run(cache, stream, call)
 
@@ -248,9 +251,12 @@ def cache_attention(q: torch.Tensor, cache: KVCache | KVCache4, block_table: tor
     d = cache.d
     window = nb * cache.block if window is None else int(window)
     scale = 1.0 / math.sqrt(d) if scale is None else scale
-    four = isinstance(cache, KVCache4)
+    if isinstance(cache, KVCache4):
+        if weights is not None:
+            _eight_bit(cache, "cache_attention with weights")
+        return _attention4(q, cache, block_table, lens, window, float(scale),
+                           out_dtype or q.dtype, stream, nb)
     if weights is not None:
-        _eight_bit(cache, "cache_attention with weights")
         if weights.dim() != 3:
             raise ValueError("weights must be [batch, Hkv, ld]")
         _want(weights, "weights", (_F32,), (b, cache.Hkv, weights.shape[2]), cache.index)
@@ -258,16 +264,34 @@ def cache_attention(q: torch.Tensor, cache: KVCache | KVCache4, block_table: tor
     def call(s):
         out = torch.empty((b, n_q, Hq, d), dtype=out_dtype or q.dtype, device=cache.device)
         lse = torch.empty((b, Hq, n_q), dtype=_F32, device=cache.device)
-        if four:
-            ws = torch.empty((B.cache4_attn_workspace_size(cache.ref, nb, b, n_q, Hq, q.dtype),),
-                             dtype=torch.uint8, device=cache.device)
-            B.cache4_attn(cache.ref, q, block_table, lens, window, scale, out, lse, ws, stream=s)
-            return out, lse
         ws = torch.empty((B.cache_attn_workspace_size(cache.ref, nb, b, n_q, Hq,
                                                       weights is not None, q.dtype),),
                          dtype=torch.uint8, device=cache.device)
         B.cache_attn(cache.ref, q, block_table, lens, window, scale, out, lse, weights, ws,
                      stream=s)
+        return out, lse
+
+    return _run(cache, stream, call)
+
+
+@functools.lru_cache(4096)
+def _attn4_bytes(n_pages: int, Hkv: int, d: int, block: int, *sizes) -> int:
+    """Bytes of workspace of an attention over a 4-bit cache: they follow from the
+    sizes, and are asked once for each."""
+    pool = B.KvCache4Struct(None, None, None, None, n_pages, Hkv, d, block)
+    return B.cache4_attn_workspace_size(ctypes.byref(pool), *sizes)
+
+
+def _attention4(q, cache: KVCache4, block_table, lens, window: int, scale: float, out_dtype,
+                stream, nb: int):
+    b, n_q, Hq, d = q.shape
+    nbytes = _attn4_bytes(cache.n_pages, cache.Hkv, d, cache.block, nb, b, n_q, Hq, q.dtype)
+
+    def call(s):
+        out = torch.empty(q.shape, dtype=out_dtype, device=cache.device)
+        lse = torch.empty((b, Hq, n_q), dtype=_F32, device=cache.device)
+        ws = torch.empty((nbytes,), dtype=torch.uint8, device=cache.device)
+        B.cache4_attn(cache.ref, q, block_table, lens, window, scale, out, lse, ws, stream=s)
         return out, lse
 
     return _run(cache, stream, call)

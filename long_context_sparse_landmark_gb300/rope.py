@@ -50,27 +50,32 @@ def _check(q, k, positions, freqs, q_weight, k_weight, grads=()):
         raise ValueError("q must be [n, Hq, d] and k [n, Hkv, d]")
     n, _, d = q.shape
     dev = q.get_device()
-    if q.dtype not in _INPUTS:
-        raise TypeError(f"q must be float32 or bfloat16, not {q.dtype}")
-    want = [(k, "k", (q.dtype,), (n, k.shape[1], d)),
-            (positions, "positions", (torch.int64,), (n,)),
-            (freqs, "freqs", (torch.int64,), (d // 2,))]
-    weights = [w for w in (q_weight, k_weight) if w is not None]
+    dt = q.dtype
+    if dt not in _INPUTS:
+        raise TypeError(f"q must be float32 or bfloat16, not {dt}")
+    _want(k, "k", dt, (n, k.shape[1], d), dev)
+    _want(positions, "positions", torch.int64, (n,), dev)
+    _want(freqs, "freqs", torch.int64, (d // 2,), dev)
+    w_dt = None
     for w, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
         if w is not None:
-            if w.dtype not in _INPUTS or w.dtype != weights[0].dtype:
+            if w.dtype not in _INPUTS or w_dt not in (None, w.dtype):
                 raise TypeError("the weights must be both float32 or both bfloat16")
-            want.append((w, what, _INPUTS, (d,)))
+            w_dt = w.dtype
+            _want(w, what, w_dt, (d,), dev)
     for g, x, what in grads:
-        want.append((g, what, (q.dtype,), tuple(x.shape)))
-    for t, what, dtypes, shape in want:
-        if t.dtype not in dtypes:
-            raise TypeError(f"{what} must be {' or '.join(str(x) for x in dtypes)}, not {t.dtype}")
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{what} must have shape {shape}, not {tuple(t.shape)}")
-        if t.get_device() != dev:
-            raise ValueError(f"{what} must be on {q.device}, not {t.device}")
+        _want(g, what, dt, x.shape, dev)
     return dev
+
+
+def _want(t, what: str, dtype, shape, dev: int):
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+        return
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    raise ValueError(f"{what} must be on device {dev}, not {t.device}")
 
 
 def _run(dev: int, stream, call):
@@ -83,7 +88,7 @@ def _run(dev: int, stream, call):
             raise ValueError("stream and tensors are on different devices")
         with torch.cuda.stream(stream):
             return call(stream.cuda_stream)
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:
         return call(torch._C._cuda_getCurrentRawStream(dev))
     with torch.cuda.device(dev):
         return call(torch._C._cuda_getCurrentRawStream(dev))
@@ -99,10 +104,10 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, freq
     slices of one tensor [n, heads, d].  Returns (q, k), new tensors
     (msa_qk_norm_rope)."""
     dev = _check(q, k, positions, freqs, q_weight, k_weight)
+    like = dict(dtype=q.dtype, device=q.device)
 
     def call(s):
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+        q_out, k_out = torch.empty(q.shape, **like), torch.empty(k.shape, **like)
         B.qk_norm_rope(q, k, positions, freqs, q_weight, k_weight, eps, mscale, interleaved,
                        q_out, k_out, stream=s)
         return q_out, k_out
@@ -121,10 +126,10 @@ def qk_norm_rope_backward(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.T
     dev = _check(q, k, positions, freqs, q_weight, k_weight,
                  ((dq_out, q, "dq_out"), (dk_out, k, "dk_out")))
     n, Hq, d = q.shape
+    like = dict(dtype=q.dtype, device=q.device)
 
     def call(s):
-        dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        dk = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+        dq, dk = torch.empty(q.shape, **like), torch.empty(k.shape, **like)
         dqw = None if q_weight is None else torch.empty_like(q_weight)
         dkw = None if k_weight is None else torch.empty_like(k_weight)
         ws = None

@@ -23,7 +23,7 @@
  * an infinity or a magnitude above 1.75 * 2^127, which no code stands for, all
  * its scales are 255 and its codes 0.
  * Conventions of every entry point, and what is checked on the device: as in
- * msa_cache.h.
+ * msa_cache.h; besides, n_pages * Hkv * block >= 2^32 - 1 is UNSUPPORTED.
  */
 #ifndef MSA_CACHE4_H_
 #define MSA_CACHE4_H_
@@ -66,12 +66,12 @@ size_t msa_cache4_attn_workspace_size(const msa_kv_cache4 *cache,
  * them; the same arguments, checks and errors.  A row that attends a slot
  * whose key has a scale of 255 gets NaN and an lse of NaN; one that attends a
  * slot whose value has one gets NaN in every dim, its lse stays.
- * All rows run on the tensor cores: codes times scales are halves, exactly
- * where a scale is no less than 2^-24 of the largest of the 32 slots it is
- * read with (what is below that is off by at most 2^-26 of that scale).  bf16
- * queries and softmax weights are one half each (11 bits), fp32 ones two (22
- * bits); sums are fp32.  As with the 8-bit cache the result does not depend on
- * the run, but its rounding does on the whole batch's lengths.
+ * All rows run on the tensor cores.  Codes times scales are halves, exactly
+ * where a scale is no less than 2^-27 of the largest of the same slot, head and
+ * side (a smaller one counts as 0).  bf16 queries and softmax weights are one
+ * half each (11 bits), fp32 ones two (22 bits); sums are fp32.  As with the
+ * 8-bit cache the result does not depend on the run, but its rounding does on
+ * the whole batch's lengths.
  */
 msa_status msa_cache4_attn(const msa_kv_cache4 *cache, const void *q,
                            const int32_t *table, int max_blocks,

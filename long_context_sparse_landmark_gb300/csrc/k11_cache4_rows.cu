@@ -47,8 +47,8 @@ struct Rows {
   static_assert(kRows <= kLanes, "a lane looks up one row");
   int64_t row0;          // first row of the CTA, of all rows of k and v
   int left;              // rows of the CTA
-  uint32_t slot[kRows];  // row in the pool ([n_pages * Hkv * block], at 136 bytes a slot or
-                         // more: 32 bits), kNoSlot: no such page
+  uint32_t slot[kRows];  // row in the pool ([n_pages * Hkv * block], fewer than 2^32 - 1: the
+                         // entry points check), kNoSlot: no such page
 
   __device__ __forceinline__ bool in(int i) const {
     return static_cast<int>(threadIdx.x) / kLanes + i * kStep < left;

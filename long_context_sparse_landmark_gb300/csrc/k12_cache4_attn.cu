@@ -841,8 +841,7 @@ struct Body4 {
   }
 };
 
-// Number in the pool of a unit's chunk x (136 bytes a slot: it fits 32 bits), or
-// kNoPage, which reads page 0 and attends nothing of it.
+// Number in the pool of a unit's chunk x (it fits: the entry points check), or kNoPage, which reads page 0 and attends nothing of it.
 constexpr uint32_t kNoPage = 0xffffffffu;
 __device__ __forceinline__ uint32_t chunk_at(const CacheAttnArgs& a, const Entry& e, int c, int x) {
   const int slot = e.win0 + x * kChunk;
@@ -1020,7 +1019,7 @@ cudaError_t launch_body4(const Cache4AttnArgs& a, cudaStream_t st) {
 
 template <int D>
 cudaError_t launch_d(const Cache4AttnArgs& a, cudaStream_t st) {
-  const int tile = cache4_attn_tile_rows(a.T * (a.Hq / a.c.Hkv), a.in_bf16);
+  const int tile = a.tile;
   if (!a.in_bf16)
     return tile == 8 ? launch_body4<D, Body4<D, 1, 2>>(a, st)
                      : launch_body4<D, Body4<D, 2, 2>>(a, st);
@@ -1031,9 +1030,13 @@ cudaError_t launch_d(const Cache4AttnArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-// Tiles of 8, 16 or (bf16) 32 rows: as many as the rows fill.
-int cache4_attn_tile_rows(int rows, int in_bf16) {
-  return rows <= 8 ? 8 : rows <= 16 || !in_bf16 ? 16 : 32;
+// Tiles of 8, 16 or (bf16) 32 rows: as many as the rows fill, but two of 16 for 32
+// over few slots: a CTA's start and end with 32 rows cost more than the second read
+// of the slots (four tokens of 64 heads on 8 of each of 16 sequences: over 32 slots
+// 24.8 us with 32 rows and 18.1 with 16, over 4096 53.7 and 52.0, over 16384 139 and
+// 150).
+int cache4_attn_tile_rows(int rows, int64_t slots, int in_bf16) {
+  return rows <= 8 ? 8 : rows <= 16 || !in_bf16 || slots <= 6144 ? 16 : 32;
 }
 int cache4_attn_max_ctas(int tile_rows, int in_bf16) {
   return kSms * (tile_rows == 8    ? Body4<128, 1, 1>::kPerSm

@@ -6,6 +6,15 @@
 
 namespace {
 
+// Slots of a pool and head are counted in 32 bits.
+template <class Cache>
+msa_status check_pool(const Cache* c) {
+  if (c->n_pages * c->Hkv * c->block >= int64_t(UINT32_MAX))
+    return fail(MSA_ERR_UNSUPPORTED, "n_pages=%lld Hkv=%d block=%d: too large a pool",
+                (long long)c->n_pages, c->Hkv, c->block);
+  return MSA_OK;
+}
+
 msa_status check_cache4(const msa_kv_cache4* c, const int32_t* table, int max_blocks,
                         const int32_t* lens, int batch) {
   if (!c) return fail(MSA_ERR_INVALID_ARG, "null cache");
@@ -16,7 +25,8 @@ msa_status check_cache4(const msa_kv_cache4* c, const int32_t* table, int max_bl
     return fail(MSA_ERR_INVALID_ARG, "cache pointer not 16-byte aligned");
   if (!aligned(table, 4) || !aligned(lens, 4))
     return fail(MSA_ERR_INVALID_ARG, "table or lens pointer not 4-byte aligned");
-  return check_sizes(c->n_pages, c->Hkv, c->d, c->block, batch, max_blocks);
+  const msa_status st = check_sizes(c->n_pages, c->Hkv, c->d, c->block, batch, max_blocks);
+  return st != MSA_OK ? st : check_pool(c);
 }
 
 // The rows of k and v that an append takes or a read writes.
@@ -75,23 +85,30 @@ msa_status run_read(const Cache* c, int bits, const int32_t* cu, int64_t total, 
 
 // Attention workspace: the parts of the units that several CTAs share.
 struct AttnPlan4 {
-  int n_ctas;
+  int n_ctas, tile;
   size_t part_stat, total;
 };
 
-AttnPlan4 attn_plan4(const msa_kv_cache4* c, int batch, int n_q, int Hq, int max_blocks,
+AttnPlan4 attn_plan4(const msa_kv_cache4* c, int batch, int n_q, int Hq, int max_blocks, int tile,
                      int in_bf16) {
   const int rows = n_q * (Hq / c->Hkv);
-  const int tile = msa::cache4_attn_tile_rows(rows, in_bf16);
   const int64_t units = static_cast<int64_t>(batch) * c->Hkv * ((rows + tile - 1) / tile);
   const int64_t chunks = units * (static_cast<int64_t>(max_blocks) * c->block / msa::kChunk);
   AttnPlan4 p{};
+  p.tile = tile;
   p.n_ctas = static_cast<int>(
       msa::max64(1, msa::min64(msa::cache4_attn_max_ctas(tile, in_bf16),
                                msa::max64(units, (chunks + 3) / 4))));
   p.part_stat = up(static_cast<size_t>(2) * p.n_ctas * tile * c->d * sizeof(float));
   p.total = p.part_stat + up(static_cast<size_t>(2) * p.n_ctas * tile * sizeof(float4));
   return p;
+}
+AttnPlan4 attn_plan4(const msa_kv_cache4* c, int batch, int n_q, int Hq, int max_blocks,
+                     int64_t window, int in_bf16) {
+  const int64_t slots = msa::min64(window < kMaxSlots ? window + n_q : kMaxSlots,
+                                   static_cast<int64_t>(max_blocks) * c->block);
+  return attn_plan4(c, batch, n_q, Hq, max_blocks,
+                    msa::cache4_attn_tile_rows(n_q * (Hq / c->Hkv), slots, in_bf16), in_bf16);
 }
 
 }  // namespace
@@ -122,9 +139,13 @@ size_t msa_cache4_attn_workspace_size(const msa_kv_cache4* cache, int max_blocks
                                       int n_q, int Hq, msa_dtype in_dt) {
   if (!cache ||
       check_sizes(cache->n_pages, cache->Hkv, cache->d, cache->block, batch, max_blocks) != MSA_OK ||
+      check_pool(cache) != MSA_OK ||
       check_query_sizes(cache, batch, n_q, Hq, max_blocks) != MSA_OK || !valid_dtype(in_dt))
     return 0;
-  return attn_plan4(cache, batch, n_q, Hq, max_blocks, in_dt == MSA_BF16).total;
+  // Whatever the window: its tiles are those of one slot, or of all.
+  const size_t few = attn_plan4(cache, batch, n_q, Hq, max_blocks, int64_t(1), in_dt == MSA_BF16).total;
+  const size_t all = attn_plan4(cache, batch, n_q, Hq, max_blocks, kMaxSlots, in_dt == MSA_BF16).total;
+  return few > all ? few : all;
 }
 
 msa_status msa_cache4_attn(const msa_kv_cache4* cache, const void* q, const int32_t* table,
@@ -136,7 +157,7 @@ msa_status msa_cache4_attn(const msa_kv_cache4* cache, const void* q, const int3
   MSA_TRY(check_cache4(cache, table, max_blocks, lens, batch));
   MSA_TRY(check_query_sizes(cache, batch, n_q, Hq, max_blocks));
   MSA_TRY(check_query(q, out, lse, window, scale, in_dt, out_dt));
-  const AttnPlan4 p = attn_plan4(cache, batch, n_q, Hq, max_blocks, in_dt == MSA_BF16);
+  const AttnPlan4 p = attn_plan4(cache, batch, n_q, Hq, max_blocks, window, in_dt == MSA_BF16);
   MSA_TRY(check_workspace(workspace, workspace_bytes, p.total));
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   msa::Cache4AttnArgs a{};
@@ -154,6 +175,7 @@ msa_status msa_cache4_attn(const msa_kv_cache4* cache, const void* q, const int3
   a.o_part = reinterpret_cast<float*>(ws);
   a.part_stat = reinterpret_cast<float4*>(ws + p.part_stat);
   a.n_ctas = p.n_ctas;
+  a.tile = p.tile;
   a.in_bf16 = in_dt == MSA_BF16;
   a.out_bf16 = out_dt == MSA_BF16;
   a.k_exp = static_cast<const uint8_t*>(cache->k_scale);
@@ -169,6 +191,7 @@ msa_status msa_cache_read(const msa_kv_cache* cache, const int32_t* cu, int64_t 
                           msa_stream_t stream) {
   MSA_NVTX_RANGE();
   MSA_TRY(check_cache(cache, table, max_blocks, lens, batch));
+  MSA_TRY(check_pool(cache));
   return run_read(cache, 8, cu, total, max_rows, table, max_blocks, lens, batch, k, v, out_dt,
                   stream);
 }

@@ -85,6 +85,7 @@ def test_every_call_refuses_a_bad_cache_or_batch(lib, call):
         assert lib.msa_last_error_string()
     if call in (append, attn):
         assert call(lib, v_scale=GOOD + 8) == INVALID
+    assert call(lib, n_pages=1 << 25) == UNSUPPORTED     # 2^32 slots of 2 heads
 
 
 @pytest.mark.parametrize("call", [append, read_of(4), read_of(8)])

@@ -261,6 +261,9 @@ def test_append_skips_what_cannot_be():
     ([1000, 77], 4, 8, 2, 128, 64, 33, "bf16"),
     ([1000, 77], 5, 8, 2, 64, 256, 257, "f32"),
     ([1000, 77], 4, 8, 2, 128, 64, 5000, "f32"),
+    ([7000, 6300, 12], 4, 8, 1, 128, 128, None, "bf16"),    # 32 rows together
+    ([7000, 6300], 5, 8, 1, 64, 64, None, "bf16"),
+    ([7000, 6300], 4, 8, 1, 128, 64, 6200, "bf16"),
 ])
 def test_attention(lens, T, hq, hkv, d, block, window, dtype):
     cache, pool, t = filled(lens, hkv, d, block, seed=sum(lens) + T, extra=1, width=2)
@@ -331,6 +334,28 @@ def test_scales_far_apart_between_slots(dtype):
         ref = R.attention(pool, q.double().cpu().numpy(), t, [n], 1 << 40, scale)
         out, lse = msa.cache_attention(q, cache, i32(t), i32([n]), scale=scale, out_dtype=torch.float32)
         check_attention(out, lse, ref, d, dtype == "bf16")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_groups_of_a_slot_far_apart(dtype):
+    """Values of one group 2^22 times those of another, in every slot: the dims of
+    the small one hold their own precision.  Keys likewise, the query's large dims
+    against the small ones."""
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    n, d = 200, 128
+    rng = np.random.default_rng(12)
+    apart = np.repeat([2.0 ** 20, 2.0 ** -2, 1.0, 2.0 ** 8], 32)
+    k = rng.normal(size=(n, 1, d)) * apart / 2.0 ** 8
+    v = rng.normal(size=(n, 1, d)) * apart
+    cache = new_cache(8, 1, d, 32)
+    t = rng.permutation(7)[None].astype(np.int32)
+    msa.cache_append(cache, torch.as_tensor(k, device=DEV).float(), torch.as_tensor(v, device=DEV).float(),
+                     i32([0, n]), i32(t), i32([n]), n)
+    pool = pool_of(cache)
+    q = torch.as_tensor(rng.normal(size=(1, 1, 4, d)) / apart, device=DEV).to(dt)
+    ref = R.attention(pool, q.double().cpu().numpy(), t, [n], 1 << 40, 0.5)
+    out, lse = msa.cache_attention(q, cache, i32(t), i32([n]), scale=0.5, out_dtype=torch.float32)
+    check_attention(out, lse, ref, d, dtype == "bf16")
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])

@@ -141,8 +141,8 @@ class KVCache4:
 
 
 def _eight_bit(cache, call: str):
-    if not isinstance(cache, KVCache):
-        raise TypeError(f"{call} takes a KVCache, not {type(cache).__name__}")
+    if isinstance(cache, KVCache4):
+        raise TypeError(f"{call} takes a KVCache, not a KVCache4")
 
 
 def _batch(cache: KVCache | KVCache4, table: torch.Tensor, lens: torch.Tensor):

@@ -4,9 +4,14 @@
 // A row is the d values of one token and KV head; a thread takes 16 of them, so
 // a row is 8 lanes (d = 128) or 4, and a group of 32 values 2 neighbouring
 // lanes.  Writing: the group's largest magnitude m, its scale 2^e, the least
-// with m <= 7 * 2^e, and codes of x * 2^-e, exact but for one rounding.  Reading: code * 2^e, rounded once.  Both move every byte once, and
-// HBM bounds them; a thread has kRows rows under way, K and V in CTAs of their
-// own.
+// with m <= 7 * 2^e, and codes of x * 2^-e, exact but for one rounding.
+// Reading: code * 2^e, rounded once.  Both move every byte once, and HBM bounds
+// them: 131072 tokens of 8 heads of 128 in bf16 (679 MB) are appended in about 100 us,
+// 6.8 TB/s (DRAM 82 % of its peak, issue slots 59 %, integer pipe 58 %), and read
+// back in 104.8, 6.5 TB/s (DRAM 76 %, issue slots 61 %).
+// A thread has 4 rows under way, K and V in CTAs of their own (append and then
+// read: 2 rows 207 us, 8 rows 237, 4 rows 202, 8 values a thread 238; of ragged
+// prompts up to 500 tokens 2 rows take 11.7 us and 4 rows 13.3).
 #include "cache4.cuh"
 
 namespace msa {

@@ -9,15 +9,30 @@
 // 2^{(s_j - M) + (y_j - D)}.  M, to 2^60, is the largest s so far, the
 // denominator's reference, and M + D, to 2^1.5, the largest s + y, the output's;
 // D is kept as an offset of M, so that a large score does not round the value
-// scale away.  No slot's scales touch another's.
+// scale away.  No slot's scales touch another's (the slow path: read_scales, softmax).
+//
+// Slots' scales hardly differ by more than a few binades.  So a warp holds one
+// reference for K's scales and one for V's, 2^{rk} and 2^{rv}: where none of a
+// pair's scales is above its reference or more than 27 binades below, code * 2^{13 -
+// (r - x)} is a half, exactly, all scores have one factor and all values one unit,
+// and an exponent is one multiply-add of a raw score (fits, softmax_one).  Where a
+// pair does not fit, new references are tried, with 4 binades of room; where those do
+// not either, each slot's own scales are taken.
 //
 // The work is read once, 136 bytes a slot and KV head of 128 dims, shared by the
-// group's rows: half of what the 8-bit cache takes, with the same arithmetic, so
-// that instructions bound it about as much as HBM does.  The list of 32-slot
-// chunks, its cut and the join are the 8-bit cache's (cache_attn.cuh).
+// group's rows: half of what the 8-bit cache takes.  Instructions bound it almost as
+// much as HBM does: 24 sequences of 16K to 32K slots, 64 heads on 8, run at 71 % of
+// DRAM's peak with 58 % of the issue slots, 45 % of the integer pipe (where codes
+// become halves, at half its rate) and 30 % of the tensor pipe in use, about 500
+// instructions a chunk of 32 slots; 64 such sequences take 285 us, 6.15 TB/s, where
+// each slot's own scales took 371.  The list of 32-slot chunks, its cut and the join
+// are the 8-bit cache's (cache_attn.cuh).
 //
 // All rows run on the tensor cores (mma.sync, fp16 operands): keys are the MMA's
 // 16 rows and query rows its 8 columns, so that a group of 8 heads wastes nothing.
+// (tcgen05 has 128 rows at least: 8 to 32 query rows would fill a sixteenth to a
+// quarter of them, and the codes would have to be widened into shared memory; the
+// tensor pipe is not what bounds this.)
 // A lane's share of a slot is a run of d / 4 dims of K, d / 8 of V: each within one
 // scale, so a fragment takes a conversion of two codes and one multiplication.
 // fp32 rows are two halves each, their weights too: 22 bits.
@@ -104,6 +119,8 @@ template <int D, int kNt, int kTerms>
 struct Body4 {
   static constexpr int kTile = 8 * kNt;
   static constexpr int kPerSm = kNt == 1 || kNt * kTerms == 2 ? 3 : 2;
+  // CTAs an SM: 3 where 168 registers do (4 and 5 of 8 rows spill: 377 and 431 us for
+  // 367, 64 sequences of 16K to 32K slots with each slot's own scales).
   // Chunks that a warp takes together: two, where the registers allow it, so that
   // one's fixed latencies pass in the other's shadow.
   static constexpr int kPair = kNt * kTerms == 1 ? 2 : 1;
@@ -141,7 +158,8 @@ struct Body4 {
   float o[kMt][kNt][4];
   float l[kNt][2];  // in units of 2^M, o of 2^{M + D0 - kPBits}
   // M and D0 of rows 2t, 2t+1: looked at where a reference moves or a chunk does not
-  // fit.  Those of four tiles are in shared memory (registers: 304 spilled bytes).
+  // fit.  Those of two and four tiles are in shared memory: with 32 rows in registers
+  // 304 bytes spilled, and 16 rows are 3 CTAs an SM (168 registers) without them.
   static constexpr bool kCold = kNt >= 2;
   struct Refs {
     float v[2][kNt][2];
@@ -662,8 +680,9 @@ struct Body4 {
     }
   }
 
+  // Of a chunk with its slots' own scales; masks are applied everywhere.  on: the
+  // chunk has a page.
   __device__ __forceinline__ void softmax(const CacheAttnArgs& a, int key0, bool on) {
-    constexpr bool kEdge = true;
     const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     float2 lvs[2][2];  // [step][slot g, g + 8]
     float mx[kNt][2];
@@ -679,12 +698,10 @@ struct Body4 {
         for (int n = 0; n < kNt; ++n) {
           const float2 f = __fmul2_rn(make_float2(qs(n, 0), qs(n, 1)), make_float2(of.x, of.x));
           float2 y = __fmul2_rn(make_float2(s[st][n][2 * k], s[st][n][2 * k + 1]), f);
-          if (kEdge) {
-            const int key = key0 + 16 * st + 8 * k + g;
-            const int p0 = rows->pos[8 * n + 2 * t4], p1 = rows->pos[8 * n + 2 * t4 + 1];
-            if (!on || key > p0 || p0 - key >= a.window) y.x = -INFINITY;
-            if (!on || key > p1 || p1 - key >= a.window) y.y = -INFINITY;
-          }
+          const int key = key0 + 16 * st + 8 * k + g;
+          const int p0 = rows->pos[8 * n + 2 * t4], p1 = rows->pos[8 * n + 2 * t4 + 1];
+          if (!on || key > p0 || p0 - key >= a.window) y.x = -INFINITY;
+          if (!on || key > p1 || p1 - key >= a.window) y.y = -INFINITY;
           s[st][n][2 * k] = y.x;
           s[st][n][2 * k + 1] = y.y;
           mx[n][0] = fmaxf(mx[n][0], y.x);
@@ -745,10 +762,9 @@ struct Body4 {
           const float2 t = __fadd2_rn(y, minus_M);
           sum = __fadd2_rn(sum, make_float2(ex2(t.x), ex2(t.y)));
           float2 w = make_float2(ex2(z[st][n][k].x), ex2(z[st][n][k].y));
-          if (kEdge) {  // whatever the slot's scales are, and where no slot was attended yet
-            if (y.x == -INFINITY) w.x = 0.f;
-            if (y.y == -INFINITY) w.y = 0.f;
-          }
+          // Whatever the slot's scales are, and where no slot was attended yet.
+          if (y.x == -INFINITY) w.x = 0.f;
+          if (y.y == -INFINITY) w.y = 0.f;
           put_weights(st, n, k, w);
         }
       l[n][0] = sum.x;
@@ -841,7 +857,8 @@ struct Body4 {
   }
 };
 
-// Number in the pool of a unit's chunk x (it fits: the entry points check), or kNoPage, which reads page 0 and attends nothing of it.
+// Number in the pool of a unit's chunk x (it fits: the entry points check), or
+// kNoPage, which reads page 0 and attends nothing of it.
 constexpr uint32_t kNoPage = 0xffffffffu;
 __device__ __forceinline__ uint32_t chunk_at(const CacheAttnArgs& a, const Entry& e, int c, int x) {
   const int slot = e.win0 + x * kChunk;

@@ -6,7 +6,9 @@
 // R^T dy and u = w g: dx = r (u - x r^2 mean(x u)), dw = the sum over tokens
 // and heads of g x r.  Everything is fp32 between one read and one rounding.
 //
-// Each value is read and written once, and HBM bounds a long call.  A thread
+// Each value is read and written once, and HBM bounds a long call: 32768 tokens of
+// 64 + 8 heads of 128 in bf16 take 194 us forward, 6.2 TB/s (DRAM 78 % of its peak),
+// and 276 us backward, 6.6 TB/s (DRAM 82 %), with half of the issue slots.  A thread
 // takes 16 values of a row, two runs of 8 half a row apart, so that both
 // members of a pair are its own in either pairing; a row is d / 16 lanes.  CTAs
 // take equal runs of rows of one side, whatever the tokens, with the next row's

@@ -12,6 +12,7 @@ from __future__ import annotations
 import math
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _binding as B
 
@@ -153,6 +154,7 @@ class _NormRope(torch.autograd.Function):
         return qk_norm_rope(q, k, positions, freqs, q_weight, k_weight, eps, interleaved, mscale)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dq_out, dk_out):
         q, k, positions, freqs, q_weight, k_weight = ctx.saved_tensors
         dq, dk, dqw, dkw = qk_norm_rope_backward(
@@ -165,5 +167,10 @@ def qk_norm_rope_trainable(q: torch.Tensor, k: torch.Tensor, positions: torch.Te
                            freqs: torch.Tensor, q_weight: torch.Tensor | None = None,
                            k_weight: torch.Tensor | None = None, eps: float = 1e-6,
                            interleaved: bool = False, mscale: float = 1.0):
-    """Differentiable ``qk_norm_rope``, in q, k and the weights."""
+    """Differentiable ``qk_norm_rope``, in q, k and the weights, once: a gradient of
+    the gradients raises.
+
+    A backward pass may be captured into a CUDA graph if its forward is in the
+    capture and no earlier graph of the same leaves is still held (PyTorch ties a
+    leaf's accumulation to the stream of the first one)."""
     return _NormRope.apply(q, k, positions, freqs, q_weight, k_weight, eps, interleaved, mscale)

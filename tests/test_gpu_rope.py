@@ -319,6 +319,48 @@ def test_trainable_and_module():
     assert (both[1] - both[0]).abs().max() > 0   # rounded anew: relative angles are the same, bits are not
 
 
+def test_second_derivatives_are_refused():
+    d = 64
+    q, k, pos = inputs(5, 2, 1, d, torch.float32, fused=False)
+    q.requires_grad_()
+    w = torch.ones((d,), device=DEV, requires_grad=True)
+    out, _ = msa.qk_norm_rope_trainable(q, k, pos, msa.rotary_frequencies(d), w, w)
+    g, = torch.autograd.grad((out * out).sum(), q, create_graph=True)
+    with pytest.raises(RuntimeError):
+        (g.sum() + q.sum()).backward()
+
+
+def test_a_captured_training_step_replays():
+    """Forward and backward of the differentiable form in a CUDA graph; nothing of
+    the first step, outside of it, is still held."""
+    d = 128
+    q, k, pos = inputs(70, 4, 2, d, torch.bfloat16, fused=False)
+    f = msa.rotary_frequencies(d)
+    ws = weights(d, "f32")
+    dys = [torch.randn(x.shape, device=DEV).bfloat16() for x in (q, k)]
+    leaves = [x.detach().requires_grad_() for x in (q, k, *ws)]
+
+    def step():
+        out = msa.qk_norm_rope_trainable(*leaves[:2], pos, f, *leaves[2:])
+        return torch.autograd.grad(out, leaves, dys)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        grads = step()
+    for i in range(3):
+        with torch.no_grad():
+            for x in (q, k, *dys):
+                x.copy_(torch.randn(x.shape, device=DEV))
+        g.replay()
+        for a, b in zip(grads, msa.qk_norm_rope_backward(*dys, q, k, pos, f, *ws)):
+            assert torch.equal(a, b)
+
+
 def test_a_captured_backward_replays():
     d = 128
     q, k, pos = inputs(100, 4, 2, d, torch.bfloat16)

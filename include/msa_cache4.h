@@ -19,7 +19,9 @@
  * (>= -126) with amax <= 7 * 2^e; values are rounded to the nearest code, ties
  * to the even one, those above 6 * 2^e to it (where amax lies between 6 and 7
  * times 2^e, twice the scale would bring the largest value no nearer, and the
- * others further off).  Where a slot's key (or value) of one head holds a NaN,
+ * others further off).  32 zeros beside other values have the largest scale of
+ * the slot and head (so that heads held with zeros behind them cost an attention
+ * nothing), a slot of zeros the least.  Where a slot's key (or value) of one head holds a NaN,
  * an infinity or a magnitude above 1.75 * 2^127, which no code stands for, all
  * its scales are 255 and its codes 0.
  * Conventions of every entry point, and what is checked on the device: as in

@@ -191,10 +191,16 @@ __global__ void __launch_bounds__(kThreads) cache4_append_kernel(const Append4Ar
   for (int i = 0; i < kRows; ++i) {
     uint32_t m = v[i].max_bits();
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    // A lane of the row holds what no code stands for.
-    const uint32_t bad = __ballot_sync(0xffffffffu, m > kMost4);
-    const uint32_t mine = ((1u << kLanes) - 1u) << (threadIdx.x & 31 & ~(kLanes - 1));
-    const bool poisoned = bad & mine;
+    // A group of the warp holds zeros only, or what no code stands for.
+    bool poisoned = false;
+    if (__any_sync(0xffffffffu, m - 1u >= kMost4)) {
+      uint32_t most = m;
+#pragma unroll
+      for (int o = 2; o < kLanes; o <<= 1)
+        most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+      poisoned = most > kMost4;
+      if (m == 0) m = most;
+    }
     const int e = poisoned ? 0 : group_exponent4(m);
     uint2 w = v[i].encode(pow2i(-e));
     if (poisoned) w = make_uint2(0, 0);

@@ -37,8 +37,9 @@ def pack(row):
     if not np.isfinite(row).all() or np.abs(row).max() > LARGEST:
         return np.zeros(len(row) // 2, np.uint8), np.full(len(row) // GROUP, 255, np.uint8)
     codes, scale = [], []
+    largest = exponent_of(np.abs(row).max())
     for g in row.reshape(-1, GROUP):
-        e = exponent_of(np.abs(g).max())
+        e = exponent_of(np.abs(g).max()) if g.any() else largest
         c = code_of(g / 2.0 ** e)
         codes.append(c[0::2] | c[1::2] << 4)
         scale.append(e + 127)

@@ -73,7 +73,7 @@ struct ReadArgs : RowsArgs {
 };
 cudaError_t launch_cache4_append(const Append4Args& a, cudaStream_t st);
 // CTAs along x that most * Hkv rows take (the entry points check that they fit).
-int64_t cache_rows_ctas(int64_t most, int Hkv, int d);
+int64_t cache_rows_ctas(int64_t most, int Hkv, int d, bool bf16);
 cudaError_t launch_cache_read(const ReadArgs& a, int bits, cudaStream_t st);
 
 struct Cache4AttnArgs : CacheAttnArgs {  // its cache's scales are not looked at

@@ -9,20 +9,22 @@
 // them: 131072 tokens of 8 heads of 128 in bf16 (679 MB) are appended in about 100 us,
 // 6.8 TB/s (DRAM 82 % of its peak, issue slots 59 %, integer pipe 58 %), and read
 // back in 104.8, 6.5 TB/s (DRAM 76 %, issue slots 61 %).
-// A thread has 4 rows under way, K and V in CTAs of their own (append and then
-// read: 2 rows 207 us, 8 rows 237, 4 rows 202, 8 values a thread 238; of ragged
-// prompts up to 500 tokens 2 rows take 11.7 us and 4 rows 13.3).
+// A thread has 128 bytes of rows under way, 4 rows in bf16 or 2 in fp32, K and V in
+// CTAs of their own.  Append and then read of 131072 tokens in bf16: 2 rows 207 us, 8
+// rows 237, 4 rows 202, 8 values a thread 238; of 8192 tokens 2 rows 14.7 us, 4 rows
+// 13.8; fp32, 24 ragged prompts of up to 501 tokens, 4 heads of 64: 2 rows 9.0, 4 rows
+// 10.7 (in CTAs of 256 threads 10.3 and 12.7).
 #include "cache4.cuh"
 
 namespace msa {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kPer = 16;  // values a thread
-constexpr int kRows = 4;  // rows a thread
+__host__ __device__ constexpr int thread_rows(bool bf16) { return bf16 ? 4 : 2; }
 
 // Rows (token, head) that a CTA takes.
-constexpr int cta_rows(int d) { return kThreads / (d / kPer) * kRows; }
+constexpr int cta_rows(int d, bool bf16) { return kThreads / (d / kPer) * thread_rows(bf16); }
 
 // The rows of a sequence, or none (and the status recorded) where the device
 // data cannot be.
@@ -46,7 +48,7 @@ __device__ __forceinline__ bool span_of(const RowsArgs& a, int b, Span* s) {
 
 // This thread's rows: kRows of the CTA's, kStep apart, in the order of k and v.
 constexpr uint32_t kNoSlot = 0xffffffffu;
-template <int D>
+template <int D, int kRows>
 struct Rows {
   static constexpr int kLanes = D / kPer, kStep = kThreads / kLanes;
   static_assert(kRows <= kLanes, "a lane looks up one row");
@@ -171,7 +173,8 @@ __global__ void __launch_bounds__(kThreads) cache4_append_kernel(const Append4Ar
   const int b = blockIdx.y, kv = blockIdx.x & 1;
   Span s;
   if (!span_of(a, b, &s)) return;
-  Rows<D> rows;
+  constexpr int kRows = thread_rows(kBf16);
+  Rows<D, kRows> rows;
   if (!rows.find(a, s, blockIdx.x >> 1)) return;
   const int lane = threadIdx.x & (kLanes - 1);
   const void* src = kv ? a.v : a.k;
@@ -227,7 +230,8 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReadArgs a) 
   const int b = blockIdx.y, kv = blockIdx.x & 1;
   Span s;
   if (!span_of(a, b, &s)) return;
-  Rows<D> rows;
+  constexpr int kRows = thread_rows(kBf16);
+  Rows<D, kRows> rows;
   if (!rows.find(a, s, blockIdx.x >> 1)) return;
   rows.look_up(a, b, s, blockIdx.x >> 1);
   const int lane = threadIdx.x & (kLanes - 1);
@@ -305,12 +309,13 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReadArgs a) 
 
 }  // namespace
 
-int64_t cache_rows_ctas(int64_t most, int Hkv, int d) {
-  return (most * Hkv + cta_rows(d) - 1) / cta_rows(d) * 2;
+int64_t cache_rows_ctas(int64_t most, int Hkv, int d, bool bf16) {
+  const int rows = cta_rows(d, bf16);
+  return (most * Hkv + rows - 1) / rows * 2;
 }
 
 cudaError_t launch_cache4_append(const Append4Args& a, cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>(cache_rows_ctas(a.most, a.Hkv, a.d)), a.s.batch);
+  const dim3 grid(static_cast<unsigned>(cache_rows_ctas(a.most, a.Hkv, a.d, a.bf16)), a.s.batch);
   const auto kernel = a.d == 128 ? (a.bf16 ? cache4_append_kernel<128, true>
                                            : cache4_append_kernel<128, false>)
                                  : (a.bf16 ? cache4_append_kernel<64, true>
@@ -319,7 +324,7 @@ cudaError_t launch_cache4_append(const Append4Args& a, cudaStream_t st) {
 }
 
 cudaError_t launch_cache_read(const ReadArgs& a, int bits, cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>(cache_rows_ctas(a.most, a.Hkv, a.d)), a.s.batch);
+  const dim3 grid(static_cast<unsigned>(cache_rows_ctas(a.most, a.Hkv, a.d, a.bf16)), a.s.batch);
   void (*kernel)(ReadArgs);
   if (bits == 4)
     kernel = a.d == 128 ? (a.bf16 ? cache_read_kernel<128, 4, true> : cache_read_kernel<128, 4, false>)

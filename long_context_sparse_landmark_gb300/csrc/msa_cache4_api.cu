@@ -41,7 +41,7 @@ msa_status check_rows(const int32_t* cu, int64_t total, int64_t most, const void
   if (!k || !v) return fail(MSA_ERR_INVALID_ARG, "null tensor pointer");
   if (!aligned(k, 16) || !aligned(v, 16))
     return fail(MSA_ERR_INVALID_ARG, "tensor pointer not 16-byte aligned");
-  if (msa::cache_rows_ctas(most, Hkv, d) > INT32_MAX)
+  if (msa::cache_rows_ctas(most, Hkv, d, dt == MSA_BF16) > INT32_MAX)
     return fail(MSA_ERR_UNSUPPORTED, "%lld rows: too many for one call", (long long)most);
   return MSA_OK;
 }

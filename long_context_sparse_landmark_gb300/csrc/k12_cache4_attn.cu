@@ -124,7 +124,12 @@ struct Body4 {
   // Chunks that a warp takes together: two, where the registers allow it, so that
   // one's fixed latencies pass in the other's shadow.
   static constexpr int kPair = kNt * kTerms == 1 ? 2 : 1;
-  static constexpr int kStages = (kPair == 2 || kNt == 4 ? 4 : 3) / kPair * (D == 128 ? 1 : 2);  // pairs
+  // Pairs under way.  16 bf16 rows, at 3 CTAs an SM, need no more than two (64
+  // sequences of 16K to 32K slots, two tokens: 417 us with 2, 427 with 3; with 4 only 2
+  // CTAs fit, 97 us for 68 with 8 sequences).
+  static constexpr int kStages =
+      (kPair == 2 || kNt == 4 ? 4 : kNt == 2 && kTerms == 1 ? 2 : 3) / kPair *
+      (D == 128 ? 1 : 2);
   static constexpr bool kQShared = kNt > 1;
   static constexpr int kCodes = kChunk * D / 2, kScales = kChunk * D / kGroup4;  // of K, or of V
   static constexpr int kChunkBytes = 2 * kCodes + 2 * kScales;

@@ -71,9 +71,11 @@ size_t msa_cache4_attn_workspace_size(const msa_kv_cache4 *cache,
  * All rows run on the tensor cores.  Codes times scales are halves, exactly
  * where a scale is no less than 2^-27 of the largest of the same slot, head and
  * side (a smaller one counts as 0).  bf16 queries and softmax weights are one
- * half each (11 bits), fp32 ones two (22 bits); sums are fp32.  As with the
- * 8-bit cache the result does not depend on the run, but its rounding does on
- * the whole batch's lengths.
+ * half each (11 bits), fp32 ones two (22 bits); a weight below 2^-23 of the
+ * row's largest is off by 2^-33 of that one (its product with the value by at most
+ * 2^-20 of the row's largest product, where values lie far apart).  Sums are fp32.
+ * As with the 8-bit cache the result does not depend on the run, but its rounding
+ * does on the whole batch's lengths.
  */
 msa_status msa_cache4_attn(const msa_kv_cache4 *cache, const void *q,
                            const int32_t *table, int max_blocks,

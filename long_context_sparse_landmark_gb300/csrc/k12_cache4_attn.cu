@@ -13,9 +13,12 @@
 //
 // Slots' scales hardly differ by more than a few binades.  So a warp holds one
 // reference for K's scales and one for V's, 2^{rk} and 2^{rv}: where none of a
-// pair's scales is above its reference or more than 27 binades below, code * 2^{13 -
-// (r - x)} is a half, exactly, all scores have one factor and all values one unit,
-// and an exponent is one multiply-add of a raw score (fits, softmax_one).  Where a
+// pair's scales is above its reference or more than 27 binades (V: 12) below, code *
+// 2^{13 - (r - x)} is a half, exactly, all scores have one factor and all values one
+// unit, and an exponent is one multiply-add of a raw score (fits, softmax_one).  V's
+// limit is that of the weights' halves: in one unit a weight has no part of its
+// value's scale, and one so small that its half is subnormal is off by 2^-34 of the
+// row's largest, times values 2^12 times the largest's at most.  Where a
 // pair does not fit, new references are tried, with 4 binades of room; where those do
 // not either, each slot's own scales are taken.
 //
@@ -42,11 +45,12 @@
 namespace msa {
 namespace {
 
-// Room above the largest weight when a reference is set, so that few chunks move
-// it again: a move scales all of a warp's sums, and of 32 rows some row's maximum
-// rises in most of a short range's chunks.  A weight's half keeps its 11 bits down
-// to 2^-23 of the largest.
+// Room above the largest weight when a reference is set from values in one unit, so
+// that few chunks move it again: a move scales all of a warp's sums, and of 32 rows
+// some row's maximum rises in most of a short range's chunks.  A weight's half keeps
+// its 11 bits down to 2^-23 of the largest.  (Slots far apart have no room to spare.)
 constexpr float kRoom = 5.f;
+constexpr uint32_t kKSpan = 27, kVSpan = 12;  // binades of scales below a reference
 constexpr float kTop = 13.f;  // a code of the slot's largest scale is code * 2^13
 
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
@@ -369,27 +373,29 @@ struct Body4 {
                    : "memory");
   }
 
-  // Whether no scale of the pair is above the warp's references or more than 27
-  // binades below: then code * 2^{13 - (r - x)} are halves, exactly, and the slots'
-  // own scales need no looking at.  (Slots that no row attends: see blank().)
+  // Whether no scale of the pair is above the warp's references or further below than
+  // their spans: then code * 2^{13 - (r - x)} are halves, exactly, and the slots' own
+  // scales need no looking at.  (Slots that no row attends: see blank().)
   __device__ __forceinline__ bool fits(uint32_t stage) const {
     const uint32_t at = stage + (threadIdx.x & 31) * kGroups;
     const uint32_t k2 = __byte_perm(rk, 0, 0x1010), v2 = __byte_perm(rv, 0, 0x1010);
-    uint32_t m = 0;
+    uint32_t mk = 0, mv = 0;
     each<kPair>([&](auto c) {
       constexpr int k_from = decltype(c)::value * kChunkBytes + 2 * kCodes, v_from = k_from + kScales;
       if constexpr (D == 128) {
         const uint32_t kw = lds32<k_from>(at), vw = lds32<v_from>(at);
-        m = __vimax3_u16x2(m, k2 - __byte_perm(kw, 0, 0x4240), k2 - __byte_perm(kw, 0, 0x4341));
-        m = __vimax3_u16x2(m, v2 - __byte_perm(vw, 0, 0x4240), v2 - __byte_perm(vw, 0, 0x4341));
+        mk = __vimax3_u16x2(mk, k2 - __byte_perm(kw, 0, 0x4240), k2 - __byte_perm(kw, 0, 0x4341));
+        mv = __vimax3_u16x2(mv, v2 - __byte_perm(vw, 0, 0x4240), v2 - __byte_perm(vw, 0, 0x4341));
       } else {
         const uint32_t k0 = lds8<k_from>(at), k1 = lds8<k_from + 1>(at);
         const uint32_t v0 = lds8<v_from>(at), v1 = lds8<v_from + 1>(at);
-        m = __vimax3_u16x2(m, k2 - (k0 | k1 << 16), v2 - (v0 | v1 << 16));
+        mk = __vmaxu2(mk, k2 - (k0 | k1 << 16));
+        mv = __vmaxu2(mv, v2 - (v0 | v1 << 16));
       }
     });
     // (A byte above its reference leaves a borrow, and 0xff.. in its own half.)
-    return __all_sync(0xffffffffu, __vmaxu2(m, 0x001b001bu) == 0x001b001bu);
+    constexpr uint32_t kK = kKSpan * 0x10001u, kV = kVSpan * 0x10001u;
+    return __all_sync(0xffffffffu, __vmaxu2(mk, kK) == kK && __vmaxu2(mv, kV) == kV);
   }
   // Slots that no row attends hold anything: their scales become the references,
   // so that they fit and are finite.  `off`: bit c for the lane's slot of chunk c.
@@ -573,11 +579,11 @@ struct Body4 {
     return x;
   }
   // Moves a row's references: `top` its largest score, `to` that or M, `v` the
-  // largest s + y, from `to`.
-  __device__ __forceinline__ void move(int n, int r, float top, float to, float v) {
+  // largest s + y, from `to`; room: above it.
+  __device__ __forceinline__ void move(int n, int r, float top, float to, float v, float room) {
     const float up = top - M(n, r), kept = D0(n, r) - (to - M(n, r));
     if (v - kept > 0.f || up > 60.f) {
-      const float off = fmaxf(kept, v + kRoom);  // kept: the output's unit stays
+      const float off = fmaxf(kept, v + room);  // kept: the output's unit stays
       const float down = ex2(kept - off);
       l[n][r] *= ex2(M(n, r) - to);
 #pragma unroll
@@ -656,7 +662,7 @@ struct Body4 {
             for (int k = 0; k < 2; ++k)
               mx = fmaxf(mx, s[st][n][2 * k + r] * (r ? f[n].y : f[n].x));
           const float top = row_max(mx), to = fmaxf(M(n, r), top);
-          move(n, r, top, to, (top - to) + lvs);
+          move(n, r, top, to, (top - to) + lvs, kRoom);
         }
       follow();
       exponents();
@@ -751,7 +757,7 @@ struct Body4 {
           for (int st = 0; st < 2; ++st)
 #pragma unroll
             for (int k = 0; k < 2; ++k) v = fmaxf(v, (s[st][n][2 * k + r] - to) + lvs[st][k].x);
-          move(n, r, top, to, row_max(v));
+          move(n, r, top, to, row_max(v), 0.f);
         }
       exponents();
     }

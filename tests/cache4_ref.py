@@ -79,14 +79,15 @@ def held(pool, x, table_row, h, n):
 
 def attention(pool, q, table, lens, window, scale):
     """out, lse, and for error bounds: absolute weighted values (like out), the
-    largest sum of |q k| scale over a row's slots, slots per row, and the largest
-    product of weight and value of a row."""
+    largest sum of |q k| scale over a row's slots, slots per row, the largest
+    product of weight and value of a row, and the largest product that a small weight's rounding is taken of: 2^5 times that of the row's
+    largest weight and largest value, or 2^13 times its largest product."""
     hkv = pool["k_codes"].shape[1]
     B, T, Hq, d = q.shape
     g = Hq // hkv
     out, absv = np.zeros((B, T, Hq, d)), np.zeros((B, T, Hq, d))
     lse = np.full((B, Hq, T), -np.inf)
-    s1, count, top = np.zeros((B, T, Hq)), np.zeros((B, T, Hq)), np.zeros((B, T, Hq))
+    s1, count, top, unit = (np.zeros((B, T, Hq)) for _ in range(4))
     for b in range(B):
         n = lens[b]
         for h in range(hkv):
@@ -107,5 +108,7 @@ def attention(pool, q, table, lens, window, scale):
                     lse[b, i, t] = m + np.log(e.sum())
                     s1[b, t, i] = (np.abs(k[at]) @ np.abs(row)).max() * scale
                     count[b, t, i] = len(at)
-                    top[b, t, i] = (w * np.abs(v[at]).max(axis=1)).max()
-    return out, lse, absv, s1, count, top
+                    size = np.abs(v[at]).max(axis=1)
+                    top[b, t, i] = (w * size).max()
+                    unit[b, t, i] = min(2.0 ** 5 * w.max() * size.max(), 2.0 ** 13 * top[b, t, i])
+    return out, lse, absv, s1, count, top, unit

@@ -70,7 +70,7 @@ def filled(lens, hkv, d, block, seed, extra=0, width=0, kscale=1.0, vscale=1.0):
     return cache, pool_of(cache), t
 
 
-def bounds(ref, d, bf16_in, out_dtype):
+def bounds(ref, d, bf16_in, out_dtype, apart=False):
     """How far out and lse may be off.
 
     Scores: sums of d exact products (fp32 queries as two halves: off by 2^-22 of
@@ -80,20 +80,26 @@ def bounds(ref, d, bf16_in, out_dtype):
     relative error 2 ds, two exponentials (2^-22 each) and their arguments' other
     part (the value's exponent over the largest, up to 2^5 where it counts:
     2^-19), the sums' steps (one per slot at most, 2^-23 each), and the rounding
-    to one half (2^-11) or two (2^-22), whose subnormals lose 2^-39 of the
-    largest product of weight and value a slot.  Output: half a step of its
-    type."""
-    out, lse, absv, s1, count, top = ref
+    to one half (2^-11) or two (2^-22).  A subnormal half is off by 2^-25 besides,
+    a slot.  A half is the weight times the unit of its value, and the largest of
+    them 2^9 or more when the output's unit was set (2^14 less five binades of
+    room): a slot is off by 2^-34 of that weight times 6 units.  The unit is the
+    scale of the largest value seen, four binades above it at most (2^4), and 2^12
+    that of any value in it at most (codes of 4 or more: 1.5 * 2^12): 2^-33 of
+    `unit`.  Where scales lie too far apart for a unit (`apart`: in every chunk) the
+    halves hold their values' scales, and the largest is 2^14 when set: 2^-39 of the
+    row's largest product, `top`, times 1.5.  Output: half a step of its type."""
+    out, lse, absv, s1, count, top, unit = ref
     ds = ((d + 8) * 2.0 ** -23 + (0.0 if bf16_in else 2.0 ** -22)) * s1
     rel = 2 * ds + 2.0 ** -21 + 2.0 ** -19 + count * 2.0 ** -23 + (2.0 ** -11 if bf16_in else 2.0 ** -22)
     half = 2.0 ** -8 if out_dtype == torch.bfloat16 else 2.0 ** -24
-    tol_o = (absv * rel[..., None] + (count * top)[..., None] * 2.0 ** -38) * (1 + half) + np.abs(out) * half
+    tol_o = (absv * rel[..., None] + (count * (top * 2.0 ** -38 if apart else unit * 2.0 ** -33))[..., None]) * (1 + half) + np.abs(out) * half
     tol_l = (ds + 2.0 ** -20 + count * 2.0 ** -24).transpose(0, 2, 1)
     return tol_o, tol_l + np.abs(np.where(np.isfinite(lse), lse, 0.0)) * 2.0 ** -22
 
 
-def check_attention(out, lse, ref, d, bf16_in):
-    tol_o, tol_l = bounds(ref, d, bf16_in, out.dtype)
+def check_attention(out, lse, ref, d, bf16_in, apart=False):
+    tol_o, tol_l = bounds(ref, d, bf16_in, out.dtype, apart)
     o, l = out.float().cpu().double().numpy(), lse.cpu().double().numpy()
     empty = np.isneginf(ref[1])
     assert np.array_equal(np.isneginf(l), empty)
@@ -333,6 +339,60 @@ def test_scales_far_apart_between_slots(dtype):
     for scale in (0.125, 0.01):
         ref = R.attention(pool, q.double().cpu().numpy(), t, [n], 1 << 40, scale)
         out, lse = msa.cache_attention(q, cache, i32(t), i32([n]), scale=scale, out_dtype=torch.float32)
+        check_attention(out, lse, ref, d, dtype == "bf16")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T", [1, 3, 5])
+def test_small_values_beside_zeros_of_large_slots(T, d, dtype):
+    """Values of neighbouring slots 2^28 apart: a dim in which the large slots hold
+    codes of 0 is the small ones' sum, to what their weights' halves leave."""
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    n = 200
+    rng = np.random.default_rng(T)
+    k = rng.normal(size=(n, 1, d)) * 0.1
+    v = rng.normal(size=(n, 1, d))
+    v[::2] *= 2.0 ** 28
+    t = np.array([[2, 0, 3, 1]], dtype=np.int32)
+    cache = new_cache(4, 1, d, 64)
+    msa.cache_append(cache, torch.as_tensor(k, device=DEV).float(), torch.as_tensor(v, device=DEV).float(),
+                     i32([0, n]), i32(t), i32([n]), n)
+    pool = pool_of(cache)
+    q = torch.as_tensor(rng.normal(size=(1, T, 8, d)), device=DEV).to(dt)
+    for window in (3, 8, 150):
+        ref = R.attention(pool, q.double().cpu().numpy(), t, [n], window, 0.125)
+        out, lse = msa.cache_attention(q, cache, i32(t), i32([n]), window=window, scale=0.125, out_dtype=torch.float32)
+        check_attention(out, lse, ref, d, dtype == "bf16", apart=True)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shift", [4, 9, 14, 19, 22, 24, 26, 30])
+def test_large_values_at_small_weights(dtype, shift):
+    """Every third slot's values are 2^shift times the others', its weight 2^-shift:
+    the sums of both are of one size, whatever a small weight's half holds."""
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    n, d = 400, 128
+    rng = np.random.default_rng(shift)
+    k = rng.normal(size=(n, 1, d)) * 0.01
+    k[:, 0, 0] = 0.0
+    k[::3, 0, 0] = -4.0
+    k[:, 0, 1] = rng.choice([0.0, 0.5, 1.0, 1.5, 2.0, 3.0], n)   # weights of many bits
+    v = rng.normal(size=(n, 1, d))
+    v[::3] *= 2.0 ** shift
+    t = np.array([[3, 1, 6, 0, 4, 2, 5]], dtype=np.int32)
+    cache = new_cache(7, 1, d, 64)
+    msa.cache_append(cache, torch.as_tensor(k, device=DEV).float(), torch.as_tensor(v, device=DEV).float(),
+                     i32([0, n]), i32(t), i32([n]), n)
+    pool = pool_of(cache)
+    q = rng.normal(size=(1, 1, 4, d)) * 0.01
+    q[..., 0] = 1.0
+    q[..., 1] = 0.1 + 0.01 * rng.normal(size=4)
+    q = torch.as_tensor(q, device=DEV).to(dt)
+    scale = shift * np.log(2.0) / 4
+    for window in (1 << 40, 40):
+        ref = R.attention(pool, q.double().cpu().numpy(), t, [n], window, scale)
+        out, lse = msa.cache_attention(q, cache, i32(t), i32([n]), window=min(window, 10000), scale=scale, out_dtype=torch.float32)
         check_attention(out, lse, ref, d, dtype == "bf16")
 
 

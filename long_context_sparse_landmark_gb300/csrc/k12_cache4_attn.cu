@@ -36,8 +36,8 @@
 // (tcgen05, with slots as its 128 rows and query rows as its columns, wants the codes
 // widened in shared memory, 64 KB written and read again for every 128 slots; the
 // tensor pipe is not what bounds this.  Measured with S and O in tensor memory and two
-// CTAs an SM: 895 us for 419, 64 sequences of 16K to 32K slots, two tokens, 64 heads on
-// 8; 113 for 52, 16 sequences, four tokens, a window of 4096.)
+// CTAs an SM: 857 us for 419, 64 sequences of 16K to 32K slots, two tokens, 64 heads on
+// 8; 94 for 52, 16 sequences, four tokens, a window of 4096.)
 // A lane's share of a slot is a run of d / 4 dims of K, d / 8 of V: each within one
 // scale, so a fragment takes a conversion of two codes and one multiplication.
 // fp32 rows are two halves each, their weights too: 22 bits.

@@ -319,6 +319,41 @@ def test_trainable_and_module():
     assert (both[1] - both[0]).abs().max() > 0   # rounded anew: relative angles are the same, bits are not
 
 
+def test_gradients_reach_the_common_projection():
+    """q and k as slices of one leaf, broadcast gradients: the leaf's gradient holds
+    both, and zeros where the values are."""
+    n, hq, hkv, d = 21, 4, 2, 64
+    q, k, pos = inputs(n, hq, hkv, d, torch.float32)
+    leaf = torch.cat([q, k, k], dim=1).requires_grad_()
+    f = msa.rotary_frequencies(d)
+    ws = [w.requires_grad_() for w in weights(d, "f32")]
+    a, b = msa.qk_norm_rope_trainable(leaf[:, :hq], leaf[:, hq:hq + hkv], pos, f, *ws)
+    (a.sum() + 2 * b.sum()).backward()
+    want = msa.qk_norm_rope_backward(torch.ones_like(a), 2 * torch.ones_like(b), q.contiguous(), k.contiguous(), pos, f,
+                                     *(w.detach() for w in ws))
+    assert torch.equal(leaf.grad[:, :hq], want[0]) and torch.equal(leaf.grad[:, hq:hq + hkv], want[1])
+    assert not leaf.grad[:, hq + hkv:].any()
+    assert torch.equal(ws[0].grad, want[2]) and torch.equal(ws[1].grad, want[3])
+    # one output alone
+    b, = torch.autograd.grad(msa.qk_norm_rope_trainable(q, leaf[:, hq:hq + hkv], pos, f)[1].sum(), leaf)
+    assert torch.equal(b[:, hq:hq + hkv], msa.qk_norm_rope_backward(torch.zeros_like(q).contiguous(), torch.ones_like(k).contiguous(),
+                                                                   q.contiguous(), k.contiguous(), pos, f)[1])
+
+
+def test_module_in_another_type_and_its_state():
+    d = 128
+    layer = msa.SparseLandmarkAttention(window=16, num_global=4, rotary=msa.rotary_frequencies(d), qk_norm=True, head_dim=d)
+    layer = layer.to(DEV).to(torch.bfloat16)
+    assert layer.q_weight.dtype == torch.bfloat16 and layer.rotary.dtype == torch.int64
+    assert sorted(layer.state_dict()) == ["k_weight", "q_weight"]
+    q, k, pos = inputs(64, 4, 2, d, torch.bfloat16)
+    with torch.no_grad():
+        out = layer(q, k, k.contiguous())
+        qn, kn = msa.qk_norm_rope(q, k, torch.arange(64, device=DEV), layer.rotary, layer.q_weight, layer.k_weight)
+    assert torch.equal(out, msa.msa_attention(qn, kn, k.contiguous(), 16, 4)[0])
+    assert not list(msa.SparseLandmarkAttention(window=16, num_global=4).state_dict())
+
+
 def test_second_derivatives_are_refused():
     d = 64
     q, k, pos = inputs(5, 2, 1, d, torch.float32, fused=False)

@@ -79,9 +79,12 @@ cudaError_t launch_cache_read(const ReadArgs& a, int bits, cudaStream_t st);
 struct Cache4AttnArgs : CacheAttnArgs {  // its cache's scales are not looked at
   const uint8_t *k_exp, *v_exp;  // [n_pages, Hkv, block, d / 32]
   int tile;                      // query rows that a CTA takes together
+  bool pairs;                    // a warp two chunks (8 bf16 rows)
 };
 // slots: the most that a sequence's rows attend.
 int cache4_attn_tile_rows(int rows, int64_t slots, int in_bf16);
+// chunks: the most of all units.
+bool cache4_attn_pairs(int64_t chunks, int max_ctas);
 int cache4_attn_max_ctas(int tile_rows, int in_bf16);
 cudaError_t launch_cache4_attn(const Cache4AttnArgs& a, cudaStream_t st);
 

@@ -121,15 +121,16 @@ __device__ __forceinline__ uint32_t slot_scales(uint32_t w, uint32_t* h) {
   return m;
 }
 
-template <int D, int kNt, int kTerms>
+// Of 8 kNt query rows, each kTerms halves.  kChunks: chunks that a warp takes together,
+// two where the registers allow it and there are many (cache4_attn_pairs), so that
+// one's fixed latencies pass in the other's shadow.
+template <int D, int kNt, int kTerms, int kChunks = 1>
 struct Body4 {
   static constexpr int kTile = 8 * kNt;
   static constexpr int kPerSm = kNt == 1 || kNt * kTerms == 2 ? 3 : 2;
   // CTAs an SM: 3 where 168 registers do (4 and 5 of 8 rows spill: 377 and 431 us for
   // 367, 64 sequences of 16K to 32K slots with each slot's own scales).
-  // Chunks that a warp takes together: two, where the registers allow it, so that
-  // one's fixed latencies pass in the other's shadow.
-  static constexpr int kPair = kNt * kTerms == 1 ? 2 : 1;
+  static constexpr int kPair = kChunks;
   // Pairs under way.  16 bf16 rows, at 3 CTAs an SM, need no more than two (64
   // sequences of 16K to 32K slots, two tokens: 417 us with 2, 427 with 3; with 4 only 2
   // CTAs fit, 97 us for 68 with 8 sequences).
@@ -1053,7 +1054,8 @@ cudaError_t launch_d(const Cache4AttnArgs& a, cudaStream_t st) {
   if (!a.in_bf16)
     return tile == 8 ? launch_body4<D, Body4<D, 1, 2>>(a, st)
                      : launch_body4<D, Body4<D, 2, 2>>(a, st);
-  return tile == 8    ? launch_body4<D, Body4<D, 1, 1>>(a, st)
+  return tile == 8    ? (a.pairs ? launch_body4<D, Body4<D, 1, 1, 2>>(a, st)
+                                 : launch_body4<D, Body4<D, 1, 1>>(a, st))
          : tile == 16 ? launch_body4<D, Body4<D, 2, 1>>(a, st)
                       : launch_body4<D, Body4<D, 4, 1>>(a, st);
 }
@@ -1068,6 +1070,13 @@ cudaError_t launch_d(const Cache4AttnArgs& a, cudaStream_t st) {
 int cache4_attn_tile_rows(int rows, int64_t slots, int in_bf16) {
   return rows <= 8 ? 8 : rows <= 16 || !in_bf16 || slots <= 6144 ? 16 : 32;
 }
+// Pairs of chunks from 96 chunks a CTA on, as many at most: a pair takes 5 to 8 % less
+// time than two chunks, but a range of few chunks is no whole number of pairs for
+// every warp, and the longer code is read for the first time (one token of 64 heads on
+// 8; 16 sequences: over 1024 slots 17.4 us with pairs and 16.2 without, over 4096 27.0
+// and 25.2, over 8192 40.2 and 40.0, over 16384 61.5 and 62.9; 64 sequences of 16K to
+// 32K slots 286 and 305).
+bool cache4_attn_pairs(int64_t chunks, int max_ctas) { return chunks >= int64_t(96) * max_ctas; }
 int cache4_attn_max_ctas(int tile_rows, int in_bf16) {
   return kSms * (tile_rows == 8    ? Body4<128, 1, 1>::kPerSm
                  : tile_rows == 32 ? Body4<128, 4, 1>::kPerSm

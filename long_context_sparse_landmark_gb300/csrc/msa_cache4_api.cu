@@ -86,19 +86,22 @@ msa_status run_read(const Cache* c, int bits, const int32_t* cu, int64_t total, 
 // Attention workspace: the parts of the units that several CTAs share.
 struct AttnPlan4 {
   int n_ctas, tile;
+  bool pairs;
   size_t part_stat, total;
 };
 
+// slots: the most that a sequence's rows attend.
 AttnPlan4 attn_plan4(const msa_kv_cache4* c, int batch, int n_q, int Hq, int max_blocks, int tile,
-                     int in_bf16) {
+                     int64_t slots, int in_bf16) {
   const int rows = n_q * (Hq / c->Hkv);
   const int64_t units = static_cast<int64_t>(batch) * c->Hkv * ((rows + tile - 1) / tile);
   const int64_t chunks = units * (static_cast<int64_t>(max_blocks) * c->block / msa::kChunk);
   AttnPlan4 p{};
   p.tile = tile;
+  const int most = msa::cache4_attn_max_ctas(tile, in_bf16);
   p.n_ctas = static_cast<int>(
-      msa::max64(1, msa::min64(msa::cache4_attn_max_ctas(tile, in_bf16),
-                               msa::max64(units, (chunks + 3) / 4))));
+      msa::max64(1, msa::min64(most, msa::max64(units, (chunks + 3) / 4))));
+  p.pairs = msa::cache4_attn_pairs(units * (slots / msa::kChunk), most);
   p.part_stat = up(static_cast<size_t>(2) * p.n_ctas * tile * c->d * sizeof(float));
   p.total = p.part_stat + up(static_cast<size_t>(2) * p.n_ctas * tile * sizeof(float4));
   return p;
@@ -108,7 +111,8 @@ AttnPlan4 attn_plan4(const msa_kv_cache4* c, int batch, int n_q, int Hq, int max
   const int64_t slots = msa::min64(window < kMaxSlots ? window + n_q : kMaxSlots,
                                    static_cast<int64_t>(max_blocks) * c->block);
   return attn_plan4(c, batch, n_q, Hq, max_blocks,
-                    msa::cache4_attn_tile_rows(n_q * (Hq / c->Hkv), slots, in_bf16), in_bf16);
+                    msa::cache4_attn_tile_rows(n_q * (Hq / c->Hkv), slots, in_bf16), slots,
+                    in_bf16);
 }
 
 }  // namespace
@@ -176,6 +180,7 @@ msa_status msa_cache4_attn(const msa_kv_cache4* cache, const void* q, const int3
   a.part_stat = reinterpret_cast<float4*>(ws + p.part_stat);
   a.n_ctas = p.n_ctas;
   a.tile = p.tile;
+  a.pairs = p.pairs;
   a.in_bf16 = in_dt == MSA_BF16;
   a.out_bf16 = out_dt == MSA_BF16;
   a.k_exp = static_cast<const uint8_t*>(cache->k_scale);

@@ -244,6 +244,34 @@ def test_append_skips_what_cannot_be():
 
 # -- attention ---------------------------------------------------------------
 
+@pytest.fixture(params=["singles", "pairs"])
+def either_form(request, monkeypatch):
+    """Up to 8 rows in bf16 take a warp's chunks one by one or in pairs: pairs where
+    there may be 96 chunks a CTA, as a table of many more columns allows."""
+    if request.param == "singles":
+        return
+    call = msa.cache_attention
+
+    def wide(q, cache, table, lens, **how):
+        columns = -(-96 * 456 * 32 // (cache.block * cache.Hkv * q.shape[0]))
+        more = torch.full((table.shape[0], max(0, columns - table.shape[1])), -1, dtype=torch.int32, device=DEV)
+        return call(q, cache, torch.cat([table, more], dim=1), lens, **how)
+
+    monkeypatch.setattr(msa, "cache_attention", wide)
+
+
+def test_pairs_of_chunks_at_a_window():
+    """Enough units for pairs although the window ends inside the long sequences."""
+    hkv, d, window = 8, 128, 6000
+    lens = [7001, 6010] + [0, 5, 70] * 10
+    cache, pool, t = filled(lens, hkv, d, 64, seed=4)
+    q = torch.randn((len(lens), 1, 16, d), generator=torch.Generator(device=DEV).manual_seed(3), device=DEV).bfloat16()
+    ref = R.attention(pool, q.double().cpu().numpy(), t, lens, window, d ** -0.5)
+    out, lse = msa.cache_attention(q, cache, i32(t), i32(lens), window=window)
+    check_attention(out, lse, ref, d, True)
+
+
+@pytest.mark.usefixtures("either_form")
 @pytest.mark.parametrize("lens,T,hq,hkv,d,block,window,dtype", [
     ([1], 1, 1, 1, 64, 32, None, "bf16"),
     ([1], 1, 4, 1, 128, 32, None, "f32"),
@@ -301,6 +329,7 @@ def test_attention_of_many_short_and_one_long_sequence(dtype):
     check_attention(out, lse, ref, 128, dtype == "bf16")
 
 
+@pytest.mark.usefixtures("either_form")
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("d", [64, 128])
 def test_large_scores_and_queries_of_any_size(d, dtype):
@@ -315,6 +344,7 @@ def test_large_scores_and_queries_of_any_size(d, dtype):
         check_attention(out, lse, ref, d, dtype == "bf16")
 
 
+@pytest.mark.usefixtures("either_form")
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_scales_far_apart_between_slots(dtype):
     """Slots whose values are 2^60 and more times others': where a large one draws
@@ -342,6 +372,7 @@ def test_scales_far_apart_between_slots(dtype):
         check_attention(out, lse, ref, d, dtype == "bf16")
 
 
+@pytest.mark.usefixtures("either_form")
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("T", [1, 3, 5])
@@ -366,6 +397,7 @@ def test_small_values_beside_zeros_of_large_slots(T, d, dtype):
         check_attention(out, lse, ref, d, dtype == "bf16", apart=True)
 
 
+@pytest.mark.usefixtures("either_form")
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("shift", [4, 9, 14, 19, 22, 24, 26, 30])
 def test_large_values_at_small_weights(dtype, shift):
@@ -396,6 +428,7 @@ def test_large_values_at_small_weights(dtype, shift):
         check_attention(out, lse, ref, d, dtype == "bf16")
 
 
+@pytest.mark.usefixtures("either_form")
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_groups_of_a_slot_far_apart(dtype):
     """Values of one group 2^22 times those of another, in every slot: the dims of
@@ -418,6 +451,7 @@ def test_groups_of_a_slot_far_apart(dtype):
     check_attention(out, lse, ref, d, dtype == "bf16")
 
 
+@pytest.mark.usefixtures("either_form")
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_nan_slots_reach_the_rows_that_attend_them_only(dtype):
     # rows that are not hit: values of a few units, out rounded to bf16 (2^-8) at
@@ -452,6 +486,7 @@ def test_nan_slots_reach_the_rows_that_attend_them_only(dtype):
                     assert np.abs(l[0, :, row] - ref[1][0, :, row]).max() < 1e-4
 
 
+@pytest.mark.usefixtures("either_form")
 def test_nan_slots_beside_the_largest_scales():
     """Scales next to NaN's byte, and slots that hold NaN among them."""
     n, d = 96, 64
@@ -474,6 +509,7 @@ def test_nan_slots_beside_the_largest_scales():
             assert torch.isfinite(short).all()
 
 
+@pytest.mark.usefixtures("either_form")
 def test_bad_pages_and_lengths():
     """A page that does not exist is not attended; a length that cannot be is clamped."""
     cache, pool, t = filled([100, 64], 1, 64, 32, seed=4, extra=2)
@@ -499,6 +535,7 @@ def test_bad_pages_and_lengths():
     assert not out[0].any() and torch.isneginf(lse[0]).all()
 
 
+@pytest.mark.usefixtures("either_form")
 def test_shared_prefix_pages():
     cache, pool, t = filled([128, 40], 2, 128, 64, seed=14, extra=2)
     t2 = np.array([[t[0, 0], t[0, 1]], [t[0, 0], t[1, 0]]], dtype=np.int32)

@@ -505,13 +505,14 @@ __global__ void __launch_bounds__(D * kSlices) norm_rope_dw_kernel(const RopeArg
 
 // CTAs of the two sides: at most `all`, shared by what their rows and angles cost
 // (with 64 + 8 heads by rows alone, the keys' CTAs ended last: 423 us for 276),
-// and none without a pass.
+// none without a pass, and each side that has rows at least one.
 void split_ctas(int64_t n, const int* heads, int d, int64_t all, int* ctas) {
   const int step = kThreads / (d / 16);
   const int64_t q = (n * heads[0] + step - 1) / step, k = (n * heads[1] + step - 1) / step;
   if (q + k > all) {
     const int64_t wq = heads[0] + kTokenCost, wk = heads[1] + kTokenCost;
-    ctas[1] = k ? static_cast<int>(max64(1, min64(k, (all * wk + (wq + wk) / 2) / (wq + wk)))) : 0;
+    const int64_t share = min64(all - 1, (all * wk + (wq + wk) / 2) / (wq + wk));
+    ctas[1] = k ? static_cast<int>(max64(1, min64(k, share))) : 0;
     ctas[0] = static_cast<int>(min64(q, all - ctas[1]));
   } else {
     ctas[0] = static_cast<int>(max64(1, q));

@@ -471,3 +471,26 @@ def test_refusals():
         msa.qk_norm_rope(q.cpu(), k.cpu(), pos.cpu(), f.cpu())
     with pytest.raises(ValueError):
         msa.SparseLandmarkAttention(window=4, num_global=0, qk_norm=True)
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("hq,hkv", [(1, 9000), (16, 16384), (16384, 16)])
+def test_sides_of_unequal_numbers_of_heads(hq, hkv, dt):
+    """Both sides are written, however few of the rows are one's."""
+    n, d = 8, 64
+    q, k, pos = inputs(n, hq, hkv, d, dt, fused=False)
+    f, (qw, kw) = msa.rotary_frequencies(d), weights(d, "f32")
+    ang = angles(range(n), f.tolist())
+    dys = [torch.randn(x.shape, generator=torch.Generator(device=DEV).manual_seed(4), device=DEV).to(dt) for x in (q, k)]
+    B = binding()
+    nan = float("nan")
+    outs = [gfull(x.shape, nan, dt) for x in (q, k)]
+    grads = [gfull(x.shape, nan, dt) for x in (q, k)] + [gfull((d,), nan) for _ in range(2)]
+    ws = gfull((B.qk_norm_rope_bwd_workspace_size(n, hq, hkv, d),), 0xFF, torch.uint8)
+    B.qk_norm_rope(q, k, pos, f, qw, kw, 1e-6, 1.0, False, *outs)
+    B.qk_norm_rope_bwd(*dys, q, k, pos, f, qw, kw, 1e-6, 1.0, False, *grads, ws)
+    for i, (x, w) in enumerate(((q, qw), (k, kw))):
+        close(outs[i], *forward(f64(x), f64(w), ang, 1e-6, False, 1.0), "qk"[i])
+        dx, tol, dw, tol_w = backward(f64(dys[i]), f64(x), f64(w), ang, 1e-6, False, 1.0)
+        close(grads[i], dx, tol, "d" + "qk"[i])
+        close(grads[2 + i], dw, tol_w, "dw of " + "qk"[i])

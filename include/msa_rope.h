@@ -34,7 +34,9 @@ extern "C" {
  *   freqs      [d / 2] device int64
  *   q_weight, k_weight  [d] in `w_dt`; NULL: that side is rotated only
  *   q_out, k_out  [n, Hq, d], [n, Hkv, d] in `dt`, written
- * Sums of squares are fp32.  Hkv may be 0 (k and k_out are not looked at), and
+ * Sums of squares are fp32: values above 2^60 pass its range (the row's norm
+ * gives zeros), and with an eps below 2^-120 those below 2^-64 lose bits of r.
+ * Hkv may be 0 (k and k_out are not looked at), and
  * so may n (nothing is done).
  * Errors: INVALID_ARG for null or misaligned pointers (16 bytes; positions and
  * freqs 8, weights 4), sizes out of range, strides below heads * d or not a

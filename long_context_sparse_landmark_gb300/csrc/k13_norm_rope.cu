@@ -440,7 +440,8 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm) norm_rope_bwd_kernel(cons
       const float r = rsqrtf(row_sum<Walk<D>::kLanes>(ss.x + ss.y) * (1.f / D) + a.eps);
       // Rows past the end are zeros: they add none to dw, unless r is infinite.
       const float rw = at.in() ? r : 0.f;
-      const float f = -r * r * (row_sum<Walk<D>::kLanes>(xu.x + xu.y) * (1.f / D));
+      // r times the mean first: r^2 alone passes fp32's range for rows below 2^-64.
+      const float f = -r * (r * (row_sum<Walk<D>::kLanes>(xu.x + xu.y) * (1.f / D)));
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         dw.a[k] = __ffma2_rn(g.a[k], __fmul2_rn(x.a[k], both(rw)), dw.a[k]);

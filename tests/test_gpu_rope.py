@@ -494,3 +494,23 @@ def test_sides_of_unequal_numbers_of_heads(hq, hkv, dt):
         dx, tol, dw, tol_w = backward(f64(dys[i]), f64(x), f64(w), ang, 1e-6, False, 1.0)
         close(grads[i], dx, tol, "d" + "qk"[i])
         close(grads[2 + i], dw, tol_w, "dw of " + "qk"[i])
+
+
+@pytest.mark.parametrize("d,dt", [(64, torch.float32), (128, torch.bfloat16)])
+def test_gradients_of_tiny_rows_without_eps(d, dt):
+    """Rows of 2^-64: r is 2^64, its square past fp32's range.  Squares are
+    subnormal, 2^-21 of themselves apart: r is off by 2^-22 more, within the bound's
+    room."""
+    q, k, pos = inputs(20, 2, 1, d, torch.float32, fused=False)
+    q, k = (torch.where(x.abs() < 0.25, 0.25, x).mul(2.0 ** -64).to(dt) for x in (q, k))
+    f, (qw, kw) = msa.rotary_frequencies(d), weights(d, "f32")
+    ang = angles(range(20), f.tolist())
+    gen = torch.Generator(device=DEV).manual_seed(4)
+    dys = [torch.randn(x.shape, generator=gen, device=DEV).to(dt) for x in (q, k)]
+    outs = msa.qk_norm_rope(q, k, pos, f, qw, kw, eps=0.0)
+    grads = msa.qk_norm_rope_backward(*dys, q, k, pos, f, qw, kw, eps=0.0)
+    for i, (x, w) in enumerate(((q, qw), (k, kw))):
+        close(outs[i], *forward(f64(x), f64(w), ang, 0.0, False, 1.0), "qk"[i])
+        dx, tol, dw, tol_w = backward(f64(dys[i]), f64(x), f64(w), ang, 0.0, False, 1.0)
+        close(grads[i], dx, tol, "d" + "qk"[i])
+        close(grads[2 + i], dw, tol_w, "dw of " + "qk"[i])

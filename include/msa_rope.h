@@ -62,7 +62,9 @@ size_t msa_qk_norm_rope_bwd_workspace_size(int64_t n, int Hq, int Hkv, int d);
  *   q, k, ...       what the forward took
  *   dq, dk          [n, Hq, d], [n, Hkv, d] in `dt`, written
  *   dq_weight, dk_weight  [d] in `w_dt`, written; NULL where the weight is
- * The weights' gradients are summed in fp32 in an order that the sizes fix.
+ * The weights' gradients are summed in an order that the sizes fix: few terms
+ * (a thread's 8 rows, 8 lanes) in fp32, beyond that in two floats each, so that
+ * their bits do not go with the number of rows.
  * n = 0 writes zeros to them.
  * Errors: as msa_qk_norm_rope, and a null, misaligned (256 bytes) or too small
  * workspace where there is a weight.

@@ -344,6 +344,76 @@ __global__ void __launch_bounds__(kThreads, kFwdPerSm) norm_rope_kernel(const Ro
   });
 }
 
+// A sum in two floats: lo takes what an addition to hi rounds off (Knuth's
+// two-sum), so that a sum of any length keeps fp32's bits.  (In 64 bits, at the 1.25 TFLOP/s that a GB300 is given, the
+// last kernel's additions alone would take some 2 us of the 2K-token step's 11.)
+struct Sum {
+  float hi, lo;
+  __device__ __forceinline__ void add(float x) {
+    const float s = hi + x, b = s - hi;
+    lo += (hi - (s - b)) + (x - b);
+    hi = s;
+  }
+  __device__ __forceinline__ void add(const Sum& x) {
+    add(x.hi);
+    lo += x.lo;
+  }
+  __device__ __forceinline__ float value() const {  // hi infinite: lo is a NaN
+    return fabsf(hi) < INFINITY ? hi + lo : hi;
+  }
+};
+
+// A thread's sums of the weights' gradients: kSumPasses passes in registers, then
+// over the warp's lanes of the same dims, each of which gets kOwn of the 16 values to
+// add to sums of its own in shared memory: [hi, lo][thread][kOwn].
+constexpr int kSumPasses = 8;
+template <int D>
+struct Columns {
+  static constexpr int kLanes = D / 16, kOwn = 16 * kLanes / 32;
+  static constexpr int kBytes = 2 * kThreads * kOwn * static_cast<int>(sizeof(float));
+  __device__ __forceinline__ static float* at(float* sums, int half, int thread) {
+    return sums + (half * kThreads + thread) * kOwn;
+  }
+  __device__ __forceinline__ static void clear(float* sums) {
+#pragma unroll
+    for (int k = 0; k < kOwn; ++k)
+      at(sums, 0, threadIdx.x)[k] = at(sums, 1, threadIdx.x)[k] = 0.f;
+  }
+  __device__ __forceinline__ static void add(float* sums, float* v) {
+#pragma unroll
+    for (int o = 16, n = 8; o >= kLanes; o >>= 1, n >>= 1) {
+      const bool up = threadIdx.x & o;
+#pragma unroll
+      for (int k = 0; k < n; ++k) {
+        const float give = up ? v[k] : v[n + k], keep = up ? v[n + k] : v[k];
+        v[k] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+      }
+    }
+    float *hi = at(sums, 0, threadIdx.x), *lo = at(sums, 1, threadIdx.x);
+#pragma unroll
+    for (int k = 0; k < kOwn; ++k) {
+      Sum s{hi[k], lo[k]};
+      s.add(v[k]);
+      hi[k] = s.hi;
+      lo[k] = s.lo;
+    }
+  }
+  // Column `dim` of all warps.
+  __device__ __forceinline__ static Sum column(float* sums, int dim) {
+    const int k = dim / (D / 2) * 8 + (dim & 7);  // the value among a lane's 16
+    int lane = dim % (D / 2) / 8;
+#pragma unroll
+    for (int o = 16, n = 8; o >= kLanes; o >>= 1, n >>= 1) lane |= k & n ? o : 0;
+    Sum s{0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      const int thread = 32 * w + lane;
+      s.add(Sum{at(sums, 0, thread)[k % kOwn], at(sums, 1, thread)[k % kOwn]});
+    }
+    return s;
+  }
+};
+
 // The gradients' kernel has two inputs: bf16 values come through a ring in shared
 // memory, kDepth passes under way.  fp32 ones, which are twice the bytes a pass,
 // come in registers, one pass ahead, as the forward's do (32K tokens of 32 + 4 heads
@@ -354,21 +424,24 @@ struct Ring {
   using R = Raw<D, kBf16>;
   static constexpr int kDepth = kBf16 ? 3 : 1;
   static constexpr int kPass = kBf16 ? 2 * R::kBytes : 0;
-  static constexpr int kSmem = static_cast<int>(2 * kAngles * sizeof(float)) + kDepth * kPass;
+  static constexpr int kSums = static_cast<int>(2 * kAngles * sizeof(float));  // from here on
+  static constexpr int kRing = kSums + Columns<D>::kBytes;
+  static constexpr int kSmem = kRing + kDepth * kPass;
 };
 template <int D, bool kBf16, bool kInterleaved>
 __global__ void __launch_bounds__(kThreads, kBwdPerSm) norm_rope_bwd_kernel(const RopeArgs a) {
   using R = Raw<D, kBf16>;
   constexpr int kDepth = Ring<D, kBf16>::kDepth, kPass = Ring<D, kBf16>::kPass;
-  extern __shared__ __align__(16) uint8_t dyn[];  // the angles, then the ring
+  extern __shared__ __align__(16) uint8_t dyn[];  // the angles, the weights' sums, the ring
   float(*cs)[kAngles] = reinterpret_cast<float(*)[kAngles]>(dyn);
-  uint8_t* mine = dyn + 2 * kAngles * sizeof(float) + threadIdx.x * 16;
+  float* sums = reinterpret_cast<float*>(dyn + Ring<D, kBf16>::kSums);
+  uint8_t* mine = dyn + Ring<D, kBf16>::kRing + threadIdx.x * 16;
   const uint32_t place = static_cast<uint32_t>(__cvta_generic_to_shared(mine));
   Walk<D> w;
   let_next_start();
   if (!w.begin(a)) {  // its sums are read
     if (a.weight[w.side] && threadIdx.x < D)
-      a.part[static_cast<int64_t>(blockIdx.x) * D + threadIdx.x] = 0.f;
+      a.part[static_cast<int64_t>(blockIdx.x) * D + threadIdx.x] = make_float2(0.f, 0.f);
     return;
   }
   const int lane = w.lane, H = w.H;
@@ -384,8 +457,18 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm) norm_rope_bwd_kernel(cons
                   : 1.f;
     weight.set(v);
   }
+  int summed = 0;  // passes in dw
+  const auto sum_up = [&] {
+    float v[16];
+    dw.get(v);
+    Columns<D>::add(sums, v);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) dw.a[k] = dw.b[k] = both(0.f);
+    summed = 0;
+  };
 #pragma unroll
   for (int k = 0; k < 4; ++k) dw.a[k] = dw.b[k] = both(0.f);
+  if (norm) Columns<D>::clear(sums);
   Walk<D> ahead = w;
   R next_g, next_x;  // fp32
   const auto fetch = [&](int slot) {
@@ -449,6 +532,7 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm) norm_rope_bwd_kernel(cons
         g.a[k] = __fmul2_rn(both(r), __ffma2_rn(x.a[k], both(f), u[k]));
         g.b[k] = __fmul2_rn(both(r), __ffma2_rn(x.b[k], both(f), u[4 + k]));
       }
+      if (++summed == kSumPasses) sum_up();
     }
     const int64_t to = ((at.t0 + at.t) * H + at.h) * D + lane * 8;
     if (at.in() && MSA_IN_RANGE(to, D / 2 + 8, a.n * H * D, a.status)) g.store(a.out[w.side], to);
@@ -458,25 +542,11 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm) norm_rope_bwd_kernel(cons
     }
   });
   if (!norm) return;
-  // Lanes of the same dims are kLanes apart, then the warps, in order.
-  float v[16];
-  dw.get(v);
-#pragma unroll
-  for (int k = 0; k < 16; ++k)
-#pragma unroll
-    for (int o = Walk<D>::kLanes; o < 32; o <<= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-  float* sums = cs[0];
-  if ((threadIdx.x & 31) < Walk<D>::kLanes) {
-#pragma unroll
-    for (int k = 0; k < 16; ++k)
-      sums[(threadIdx.x >> 5) * D + (k >> 3) * (D / 2) + lane * 8 + (k & 7)] = v[k];
-  }
+  if (summed) sum_up();
   __syncthreads();
   if (threadIdx.x < D) {
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) sum += sums[i * D + threadIdx.x];
-    a.part[static_cast<int64_t>(blockIdx.x) * D + threadIdx.x] = sum;
+    const Sum sum = Columns<D>::column(sums, threadIdx.x);
+    a.part[static_cast<int64_t>(blockIdx.x) * D + threadIdx.x] = make_float2(sum.hi, sum.lo);
   }
 }
 
@@ -485,23 +555,28 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm) norm_rope_bwd_kernel(cons
 constexpr int kSlices = 8;
 template <int D>
 __global__ void __launch_bounds__(D * kSlices) norm_rope_dw_kernel(const RopeArgs a) {
-  __shared__ float sums[kSlices][D];
+  __shared__ Sum sums[kSlices][D];
   const int side = blockIdx.x, k = threadIdx.x % D, slice = threadIdx.x / D;
   wait_for_inputs();
   if (!a.dweight[side]) return;
-  const float* part = a.part + (side ? static_cast<int64_t>(a.ctas[0]) * D : 0) + k;
-  float sum = 0.f;
-  if (a.n > 0)
-    for (int c = slice; c < a.ctas[side]; c += kSlices) sum += part[static_cast<int64_t>(c) * D];
+  const float2* part = a.part + (side ? static_cast<int64_t>(a.ctas[0]) * D : 0) + k;
+  Sum sum{0.f, 0.f};
+  if (a.n > 0) {
+#pragma unroll 8
+    for (int c = slice; c < a.ctas[side]; c += kSlices) {
+      const float2 x = part[static_cast<int64_t>(c) * D];
+      sum.add(Sum{x.x, x.y});
+    }
+  }
   sums[slice][k] = sum;
   __syncthreads();
   if (slice) return;
 #pragma unroll
-  for (int i = 1; i < kSlices; ++i) sum += sums[i][k];
+  for (int i = 1; i < kSlices; ++i) sum.add(sums[i][k]);
   if (a.w_bf16)
-    static_cast<__nv_bfloat16*>(a.dweight[side])[k] = __float2bfloat16_rn(sum);
+    static_cast<__nv_bfloat16*>(a.dweight[side])[k] = __float2bfloat16_rn(sum.value());
   else
-    static_cast<float*>(a.dweight[side])[k] = sum;
+    static_cast<float*>(a.dweight[side])[k] = sum.value();
 }
 
 // CTAs of the two sides: at most `all`, shared by what their rows and angles cost

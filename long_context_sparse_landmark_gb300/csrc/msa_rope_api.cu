@@ -76,7 +76,7 @@ msa_status check_rope(msa::RopeArgs* a, const void* q, int64_t q_stride, const v
 size_t bwd_bytes(int64_t n, int Hq, int Hkv, int d, int* ctas) {
   const int heads[2] = {Hq, Hkv};
   msa::norm_rope_bwd_ctas(n, heads, d, ctas);
-  return up(static_cast<size_t>(ctas[0] + ctas[1]) * d * sizeof(float));
+  return up(static_cast<size_t>(ctas[0] + ctas[1]) * d * sizeof(float2));
 }
 
 }  // namespace
@@ -131,7 +131,7 @@ msa_status msa_qk_norm_rope_bwd(const void* dq_out, int64_t dq_out_stride, const
   a.dweight[1] = k_weight ? dk_weight : nullptr;
   const size_t need = bwd_bytes(n, Hq, Hkv, d, a.ctas);
   if (q_weight || k_weight) MSA_TRY(check_workspace(workspace, workspace_bytes, need));
-  a.part = static_cast<float*>(workspace);
+  a.part = static_cast<float2*>(workspace);
   MSA_TRY(msa::api_status_word(&a.status));
   return launched(msa::launch_norm_rope_bwd(a, reinterpret_cast<cudaStream_t>(stream)),
                   "norm and rotation backward");

@@ -16,7 +16,8 @@ struct RopeArgs {
   int heads[2];
   const void* weight[2];  // [d], null: no norm
   void* dweight[2];       // backward: [d]
-  float* part;            // backward: [ctas][d] sums of the weights' gradients, queries' CTAs first
+  float2* part;           // backward: [ctas][d] sums of the weights' gradients in two floats,
+                          // queries' CTAs first
   int ctas[2];            // of queries, of keys
   int64_t n;
   int d;

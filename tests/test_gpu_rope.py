@@ -514,3 +514,41 @@ def test_gradients_of_tiny_rows_without_eps(d, dt):
         dx, tol, dw, tol_w = backward(f64(dys[i]), f64(x), f64(w), ang, 0.0, False, 1.0)
         close(grads[i], dx, tol, "d" + "qk"[i])
         close(grads[2 + i], dw, tol_w, "dw of " + "qk"[i])
+
+
+@pytest.mark.parametrize("d,dtype", [(64, "f32"), (128, "bf16")])
+def test_long_sums_of_the_weights_gradients(d, dtype):
+    """Equal terms 1 + 2^-17 - 2^-23, some 216 passes a thread: a sum of 32 bits
+    beyond 128 drops 2^-17 of each.  Where no fp32 sum is longer than a group of 8
+    passes and 8 lanes (11 half steps), a term has 4 half steps (its product, and
+    two ulps of rsqrtf twice over) and the result one: 2^-20 of it."""
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    n = 304 * 216 * (4096 // d)
+    m = 1 + 2.0 ** -17 - 2.0 ** -23
+    x = torch.ones((n, 1, d), dtype=dt, device=DEV)
+    pos = torch.zeros((n,), dtype=torch.int64, device=DEV)
+    w = torch.ones((d,), device=DEV)
+    for hkv in (0, 1):
+        k = x[:, :hkv]
+        g = msa.qk_norm_rope_backward(x, k, x, k, pos, msa.rotary_frequencies(d), w, w, eps=0.0, mscale=m)
+        for i in range(1 + hkv):
+            off = (g[2 + i].double() / (n * m) - 1).abs().max().item()
+            assert off <= 2.0 ** -20, off * 2.0 ** 24
+
+
+def test_infinite_sums_of_the_weights_gradients():
+    """Terms past fp32's range give infinities, not NaN; a NaN among them a NaN."""
+    d, n = 64, 40000
+    x = torch.ones((n, 1, d), device=DEV)
+    dy = torch.ones((n, 1, d), device=DEV)
+    dy[100:200, 0, 3] = 2e38
+    dy[30000:, 0, 4] = -2e38
+    dy[7, 0, 5] = float("inf")
+    dy[9, 0, 6] = float("nan")
+    w = torch.ones((d,), device=DEV)
+    pos = torch.zeros((n,), dtype=torch.int64, device=DEV)
+    g = msa.qk_norm_rope_backward(dy, x[:, :0], x, x[:, :0], pos, msa.rotary_frequencies(d), w, None, eps=0.0)[2]
+    # (dims 3 .. 5 are the first of their pairs: a zero sine times an infinity is a NaN in the others')
+    assert g[3] == math.inf and g[4] == -math.inf and g[5] == math.inf and torch.isnan(g[6])
+    keep = [i for i in range(d) if i % 32 not in (3, 4, 5, 6)]
+    assert (g[keep] == n).all()

@@ -317,8 +317,8 @@ class SparseLandmarkAttention(torch.nn.Module):
     positions before they attend, and ``qk_norm`` norms each head of them with
     the weights q_weight, k_weight [head_dim] before that, in one pass
     (``qk_norm_rope``, which has ``eps``, ``interleaved`` and ``mscale``);
-    forward(..., positions=) gives the positions, [n] or [batch, n] int64, by
-    default 0 .. n - 1.
+    forward(..., positions=) gives the positions, [n] (of every sequence of a
+    batch) or [batch, n] int64, by default 0 .. n - 1.
     """
 
     def __init__(self, window: int | None = None, num_global: int | None = None,
@@ -371,5 +371,10 @@ class SparseLandmarkAttention(torch.nn.Module):
             raise ValueError("positions without rotary")
         if q.dim() == 3:
             return self._one(q, k, v, positions)
-        return torch.stack([self._one(q[b], k[b], v[b], None if positions is None else positions[b])
-                            for b in range(q.shape[0])])
+        if positions is None or positions.dim() == 1:
+            each = [positions] * q.shape[0]
+        elif positions.dim() == 2 and positions.shape[0] == q.shape[0]:
+            each = list(positions)
+        else:
+            raise ValueError(f"positions must be [n] or [batch, n], not {tuple(positions.shape)}")
+        return torch.stack([self._one(q[b], k[b], v[b], p) for b, p in enumerate(each)])

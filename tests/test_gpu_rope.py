@@ -552,3 +552,20 @@ def test_infinite_sums_of_the_weights_gradients():
     assert g[3] == math.inf and g[4] == -math.inf and g[5] == math.inf and torch.isnan(g[6])
     keep = [i for i in range(d) if i % 32 not in (3, 4, 5, 6)]
     assert (g[keep] == n).all()
+
+
+def test_positions_of_a_batch_in_the_module():
+    """One sequence's positions [n] serve every sequence of a batch."""
+    n, d = 64, 128
+    layer = msa.SparseLandmarkAttention(window=16, num_global=4, rotary=msa.rotary_frequencies(d))
+    layer = layer.to(DEV)
+    q, k, _ = inputs(n, 4, 2, d, torch.bfloat16, fused=False)
+    pos = torch.arange(n, device=DEV) * 3 + 1000
+    with torch.no_grad():
+        one = layer(q, k, k, positions=pos)
+        both = layer(torch.stack([q, q]), torch.stack([k, k]), torch.stack([k, k]), positions=pos)
+    assert torch.equal(both[0], one) and torch.equal(both[1], one)
+    with pytest.raises(ValueError):
+        layer(torch.stack([q, q]), torch.stack([k, k]), torch.stack([k, k]), positions=pos[:5])
+    with pytest.raises(ValueError):
+        layer(torch.stack([q, q]), torch.stack([k, k]), torch.stack([k, k]), positions=torch.stack([pos] * 3))

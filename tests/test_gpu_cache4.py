@@ -877,3 +877,22 @@ def test_refusals():
                        torch.zeros((2, 1, 48, 2), dtype=torch.uint8, device=DEV), torch.zeros((2, 1, 48, 2), dtype=torch.uint8, device=DEV))
     with pytest.raises(binding().MsaError):
         msa.cache_attention(torch.ones((1, 1, 1, 64), device=DEV), bad, table, lens)
+
+
+def test_a_read_refuses_outputs_that_overlap():
+    n, hkv, d = 64, 2, 64
+    cache, _, t = filled([n], hkv, d, 32, seed=3)
+    buf = torch.zeros((2 * n * hkv * d,), device=DEV)
+
+    def read(k, v):
+        return msa.cache_read(cache, i32([0, n]), i32(t), i32([n]), n, n, dtype=torch.float32, out=(k, v))
+
+    def at(i):
+        return buf[i:i + n * hkv * d].view(n, hkv, d)
+
+    for a, b in ((0, 0), (0, d), (d, 0), (0, n * hkv * d - 4), (n * hkv * d - 4, 0)):
+        with pytest.raises(ValueError):
+            read(at(a), at(b))
+    k, v = msa.cache_read(cache, i32([0, n]), i32(t), i32([n]), n, n, dtype=torch.float32)
+    read(at(n * hkv * d), at(0))   # side by side
+    assert torch.equal(at(n * hkv * d), k) and torch.equal(at(0), v)

@@ -569,3 +569,69 @@ def test_positions_of_a_batch_in_the_module():
         layer(torch.stack([q, q]), torch.stack([k, k]), torch.stack([k, k]), positions=pos[:5])
     with pytest.raises(ValueError):
         layer(torch.stack([q, q]), torch.stack([k, k]), torch.stack([k, k]), positions=torch.stack([pos] * 3))
+
+
+# Sizes of 20 passes a CTA and more, forward (608 CTAs) and backward (304), both
+# sides: several groups of 8 passes, and a ring that wraps.  Of hq + hkv heads, 32
+# (d = 128) or 64 rows a pass.
+LONG = [
+    # hq, hkv, d, dtype, interleaved, norm
+    (5, 3, 128, "bf16", False, True),
+    (5, 3, 128, "f32", True, True),
+    (24, 8, 128, "bf16", True, True),
+    (24, 8, 128, "f32", False, True),
+    (4, 1, 128, "bf16", False, False),
+    (7, 2, 64, "bf16", False, True),
+    (7, 2, 64, "f32", True, True),
+    (1, 1, 64, "bf16", True, True),    # groups of one pass
+    (1, 1, 64, "f32", False, False),
+]
+
+
+def long_tokens(hq, hkv, d, ctas):
+    return (32 * ctas * (4096 // d) * 4 // 3) // (hq + hkv) | 1
+
+
+@pytest.mark.parametrize("hq,hkv,d,dtype,inter,norm", LONG)
+def test_many_passes_give_what_one_gives(hq, hkv, d, dtype, inter, norm):
+    """Rows of a long call equal those of calls so short that each CTA has one
+    pass, which the other tests hold to the formulas: a row's arithmetic is the
+    same wherever it lies."""
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    n = long_tokens(hq, hkv, d, 608)
+    q, k, pos = inputs(n, hq, hkv, d, dt, far=1 << 40)
+    qw, kw = weights(d, "f32" if norm else None)
+    gen = torch.Generator(device=DEV).manual_seed(4)
+    dys = [torch.randn(x.shape, generator=gen, device=DEV).to(dt) for x in (q, k)]
+    f = msa.rotary_frequencies(d)
+    how = dict(q_weight=qw, k_weight=kw, interleaved=inter, mscale=0.75)
+    outs = msa.qk_norm_rope(q, k, pos, f, **how)
+    grads = msa.qk_norm_rope_backward(*dys, q, k, pos, f, **how)
+    step = 300 * (4096 // d) // (hq + hkv)
+    for at in range(0, n, step):
+        s = slice(at, at + step)
+        few = msa.qk_norm_rope(q[s], k[s], pos[s], f, **how)
+        few_g = msa.qk_norm_rope_backward(*(x[s] for x in dys), q[s], k[s], pos[s], f, **how)
+        for a, b in zip((*outs, *grads[:2]), (*few, *few_g[:2])):
+            assert torch.equal(a[s], b), f"tokens {at} on"
+
+
+@pytest.mark.parametrize("hq,hkv,d,dtype,inter,norm", [c for c in LONG if c[-1]])
+def test_every_row_counts_in_the_weights_gradients(hq, hkv, d, dtype, inter, norm):
+    """Values of +-1, no angle, no eps: r is 1 (rsqrtf: two ulps, 2^-22), each term
+    an odd integer and every partial sum an integer below 2^24: exact but for r,
+    2^-22 of the sum of their magnitudes (2 on average), below the 1 that a row
+    adds at least."""
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    n = long_tokens(hq, hkv, d, 304)
+    gen = torch.Generator(device=DEV).manual_seed(6)
+    x = [(torch.randint(0, 2, (n, h, d), generator=gen, device=DEV) * 2 - 1).to(dt) for h in (hq, hkv)]
+    dy = [(torch.randint(0, 4, (n, h, d), generator=gen, device=DEV) * 2 - 3).to(dt) for h in (hq, hkv)]
+    pos = torch.zeros((n,), dtype=torch.int64, device=DEV)
+    w = weights(d, "f32")
+    grads = msa.qk_norm_rope_backward(*dy, *x, pos, msa.rotary_frequencies(d), *w, eps=0.0, interleaved=inter)
+    for i in range(2):
+        terms = x[i].double() * dy[i].double()
+        want, tol = terms.sum((0, 1)), terms.abs().sum((0, 1)) * 2.0 ** -22
+        assert tol.max() < 0.5
+        assert ((grads[2 + i].double() - want).abs() <= tol).all()

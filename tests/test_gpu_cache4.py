@@ -896,3 +896,157 @@ def test_a_read_refuses_outputs_that_overlap():
     k, v = msa.cache_read(cache, i32([0, n]), i32(t), i32([n]), n, n, dtype=torch.float32)
     read(at(n * hkv * d), at(0))   # side by side
     assert torch.equal(at(n * hkv * d), k) and torch.equal(at(0), v)
+
+
+# -- long ranges a warp ------------------------------------------------------
+# Lookups of pages are 32 of a warp's steps ahead; a stage of its ring is filled
+# again after 2 to 8 steps.  The cases below give a warp 40 steps and more (the form
+# that takes chunks one by one in bf16 has at most 24: from 96 chunks a CTA on it is
+# the pairs').  CTAs: 3 an SM where a tile is 8 rows, or 16 in bf16, else 2.
+
+def random_pool(pages, hkv, d, block, gen):
+    """A pool of random codes: keys of 2^-6 to 2^-2 (scores of a third of a unit), values of
+    2^-6 to 2^5, alike within a page and head.  Then, at random, one slot in 640: a key
+    of 6 * 2^-1 in its first 32 dims, which queries of ones there weigh e^9; one in
+    1500: zeros of a large scale, which move K's or V's references or fit none; one in
+    2000: all zeros with the least scale, as appends write them, which fit none."""
+    shape = (pages, hkv, block)
+    codes = [torch.randint(0, 256, (*shape, d // 2), generator=gen, device=DEV, dtype=torch.uint8) for _ in range(2)]
+    scale = [torch.randint(*span, (pages, hkv, 1, 1), generator=gen, device=DEV).expand(*shape, d // 32)
+             .to(torch.uint8).contiguous() for span in ((121, 126), (121, 133))]
+
+    def some(one_in):
+        return torch.randint(0, one_in, shape, generator=gen, device=DEV) == 0
+
+    heavy = some(640)
+    codes[0][..., :16][heavy] = 0x77
+    scale[0][..., 0][heavy] = 126
+    for x, least in ((0, 143), (1, 130)):
+        at = some(1500) & ~heavy
+        codes[x][..., 16:32][at] = 0
+        scale[x][..., 1][at] = torch.randint(least, least + 7, (int(at.sum()),), generator=gen, device=DEV).to(torch.uint8)
+    at = some(2000) & ~heavy
+    for x in range(2):
+        codes[x][at] = 0
+        scale[x][at] = 1
+    return msa.KVCache4(*codes, *scale)
+
+
+def dense_attention(cache, q, table, lens, window, scale):
+    """R.attention's results (and the same besides) on the GPU, in 64 bits; slots of
+    pages that do not exist are not attended."""
+    steps = torch.as_tensor(np.concatenate([R.E2M1, -R.E2M1]), device=DEV)
+    B, T, hq, d = q.shape
+    hkv, block = cache.Hkv, cache.block
+    g = hq // hkv
+    out, absv = (torch.zeros((B, T, hq, d), dtype=torch.float64, device=DEV) for _ in range(2))
+    lse = torch.full((B, hq, T), -np.inf, dtype=torch.float64, device=DEV)
+    s1, count, top, unit = (torch.zeros((B, T, hq), dtype=torch.float64, device=DEV) for _ in range(4))
+    q = q.double()
+
+    def values(x, pages, h, n):
+        c = getattr(cache, x + "_codes")[pages, h].reshape(-1, d // 2)[:n].int()
+        e = getattr(cache, x + "_scale")[pages, h].reshape(-1, d // 32)[:n].double() - 127
+        val = torch.stack([steps[c & 15], steps[c >> 4]], dim=-1).reshape(n, d)
+        return val * torch.exp2(e).repeat_interleave(32, dim=-1)
+
+    for b, n in enumerate(lens):
+        if n == 0:
+            continue
+        pages = torch.as_tensor(table[b][:-(-n // block)].astype(np.int64), device=DEV)
+        slot = torch.arange(n, device=DEV)
+        there = (pages >= 0).repeat_interleave(block)[:n]
+        for h in range(hkv):
+            k, v = (values(x, pages.clamp(min=0), h, n) for x in ("k", "v"))
+            size = v.abs().amax(dim=1)
+            for t in range(T):
+                p = n - T + t
+                may = there & (slot <= p) & (slot > p - window)
+                if not may.any():
+                    continue
+                rows = slice(h * g, (h + 1) * g)
+                row = q[b, t, rows]
+                s = torch.where(may, row @ k.T * scale, -np.inf)
+                w = torch.softmax(s, dim=-1)
+                out[b, t, rows], absv[b, t, rows] = w @ v, w @ v.abs()
+                lse[b, rows, t] = torch.logsumexp(s, dim=-1)
+                s1[b, t, rows] = torch.where(may, row.abs() @ k.abs().T * scale, 0.0).amax(dim=-1)
+                count[b, t, rows] = may.sum()
+                top[b, t, rows] = (w * size).amax(dim=-1)
+                most = torch.where(may, size, 0.0).amax()
+                unit[b, t, rows] = torch.minimum(2.0 ** 5 * w.amax(dim=-1) * most, 2.0 ** 13 * top[b, t, rows])
+    return tuple(x.cpu().numpy() for x in (out, lse, absv, s1, count, top, unit))
+
+
+def check_long(out, lse, ref, d, bf16_in, steps):
+    """``bounds`` with the sums as they are made: a warp's chain of `steps` MMAs of 16
+    slots (17 terms each, fp32), the lanes', warps' and parts' joins below 100 steps,
+    not one step a slot; and the subnormal halves of slots whose scales lie apart."""
+    out64, lse64, absv, s1, count, top, unit = ref
+    ds = ((d + 8) * 2.0 ** -23 + (0.0 if bf16_in else 2.0 ** -22)) * s1
+    chain = (17 * steps + 100) * 2.0 ** -23
+    rel = 2 * ds + 2.0 ** -21 + 2.0 ** -19 + chain + (2.0 ** -11 if bf16_in else 2.0 ** -22)
+    half = 2.0 ** -8 if out.dtype == torch.bfloat16 else 2.0 ** -24
+    small = (count * np.maximum(unit * 2.0 ** -33, top * 2.0 ** -38))[..., None]
+    tol_o = (absv * rel[..., None] + small) * (1 + half) + np.abs(out64) * half
+    o, l = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    assert np.array_equal(np.isneginf(l), np.isneginf(lse64))
+    fin = np.isfinite(lse64)
+    err = np.abs(o - out64)
+    assert (err <= tol_o).all(), f"out: worst {np.max(err / np.maximum(tol_o, 1e-300)):.3g} of the bound"
+    tol_l = (ds + 2.0 ** -20 + chain).transpose(0, 2, 1) + np.abs(np.where(fin, lse64, 0)) * 2.0 ** -22
+    err = np.abs(l - np.where(fin, lse64, 0))[fin]
+    assert (err <= tol_l[fin]).all(), f"lse: worst {np.max(err / tol_l[fin]):.3g} of the bound"
+    # of some 80 heavy slots one weighs many times what the bounds let pass
+    assert np.median(tol_l[fin]) < 2.0 ** -9
+
+
+LONG = [
+    # sequences, their length, T, query heads on 8, d, block, dtype, chunks a warp's step
+    (9, 68000, 1, 64, 128, 64, "bf16", 2),     # 8 rows, pairs
+    (9, 68000, 1, 40, 64, 32, "bf16", 2),
+    (6, 26000, 1, 64, 128, 128, "bf16", 1),    # 8 rows, one by one
+    (6, 26001, 1, 64, 64, 64, "bf16", 1),
+    (7, 46000, 2, 64, 128, 64, "bf16", 1),     # 16 rows
+    (7, 46000, 1, 128, 64, 256, "bf16", 1),
+    (5, 46000, 4, 64, 128, 64, "bf16", 1),     # 32 rows
+    (5, 46000, 3, 64, 64, 32, "bf16", 1),      # 24 rows of 32
+    (7, 46000, 1, 64, 128, 32, "f32", 1),      # 8 rows of two halves
+    (7, 46000, 1, 32, 64, 64, "f32", 1),
+    (5, 46000, 2, 64, 128, 64, "f32", 1),      # 16 rows
+    (5, 46000, 3, 64, 64, 128, "f32", 1),      # 24: two tiles
+]
+
+
+@pytest.mark.parametrize("missing", [False, True])
+@pytest.mark.parametrize("batch,n,T,hq,d,block,dtype,pair", LONG)
+def test_ranges_of_many_steps_a_warp(batch, n, T, hq, d, block, dtype, pair, missing):
+    hkv = 8
+    rng = np.random.default_rng(batch * n + T)
+    gen = torch.Generator(device=DEV).manual_seed(n + T + d)
+    lens = [n - int(x) for x in rng.integers(0, 2000, batch)]
+    table = tables(lens, block, rng, 1)
+    cache = random_pool(int(table.max()) + 2, hkv, d, block, gen)
+    if missing:  # one page in 50, anywhere, and of one sequence a run of them
+        table[rng.random(table.shape) < 0.02] = -1
+        table[1, 100:100 + 4000 // block] = cache.n_pages + 7
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    q = torch.randn((batch, T, hq, d), generator=gen, device=DEV)
+    q[..., :32] = 1 + 0.1 * q[..., :32]
+    q = q.to(dt)
+    scale = 9 / 96
+    rows = T * hq // hkv
+    tile = 8 if rows <= 8 else 16 if rows <= 16 or dtype == "f32" else 32
+    ctas = 152 * (3 if tile == 8 or (tile == 16 and dtype == "bf16") else 2)
+    chunks = sum(-(-x // 32) for x in lens) * hkv * -(-rows // tile)
+    wide = batch * hkv * -(-rows // tile) * (table.shape[1] * block // 32)
+    if tile == 8 and dtype == "bf16":
+        assert (wide >= 96 * ctas) == (pair == 2)
+    steps = chunks / ctas / 4 / pair
+    assert steps >= (40 if (tile, dtype, pair) != (8, "bf16", 1) else 18)
+    out, lse = msa.cache_attention(q, cache, i32(table), i32(lens), scale=scale, out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    assert binding().device_status() == (1 if missing else 0)
+    there = np.where(table < cache.n_pages, table, -1)
+    ref = dense_attention(cache, q, there, lens, 1 << 40, scale)
+    check_long(out, lse, ref, d, dtype == "bf16", 2 * pair * (steps + 2) * (1 if dtype == "bf16" else 2))

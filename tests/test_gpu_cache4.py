@@ -1050,3 +1050,78 @@ def test_ranges_of_many_steps_a_warp(batch, n, T, hq, d, block, dtype, pair, mis
     there = np.where(table < cache.n_pages, table, -1)
     ref = dense_attention(cache, q, there, lens, 1 << 40, scale)
     check_long(out, lse, ref, d, dtype == "bf16", 2 * pair * (steps + 2) * (1 if dtype == "bf16" else 2))
+
+
+# -- pairs of chunks at windows ----------------------------------------------
+
+@pytest.fixture
+def padded_for_pairs(monkeypatch):
+    """Calls with so many empty sequences behind their own that a window of few
+    slots, too, has 96 chunks a CTA by what the launch knows."""
+    call = msa.cache_attention
+
+    def padded(q, cache, table, lens, window=None, **how):
+        assert q.dtype == torch.bfloat16 and q.shape[1] * q.shape[2] <= 8 * cache.Hkv
+        width = table.shape[1] * cache.block
+        slots = min(width if window is None else window + q.shape[1], width)
+        b = q.shape[0]
+        more = -(-96 * 456 // (slots // 32 * cache.Hkv)) - b
+        assert 0 < more + b <= 65535
+        q = torch.cat([q, q.new_ones((more, *q.shape[1:]))])
+        table = torch.cat([table, table.new_full((more, table.shape[1]), -1)])
+        lens = torch.cat([lens, lens.new_zeros((more,))])
+        out, lse = call(q, cache, table, lens, window=window, **how)
+        assert not out[b:].any() and torch.isneginf(lse[b:]).all()
+        return out[:b], lse[:b]
+
+    monkeypatch.setattr(msa, "cache_attention", padded)
+
+
+@pytest.mark.usefixtures("padded_for_pairs")
+@pytest.mark.parametrize("lens,T,hq,hkv,d,block,window", [
+    ([1000, 77], 1, 8, 2, 128, 64, 100),
+    ([1000, 77], 2, 8, 2, 128, 64, 33),
+    ([1000, 77], 4, 4, 2, 64, 256, 257),
+    ([513, 0, 3, 64], 3, 4, 2, 128, 32, 31),
+    ([513, 0, 3, 64], 8, 2, 2, 64, 32, 64),
+])
+def test_pairs_of_chunks_at_small_windows(lens, T, hq, hkv, d, block, window):
+    cache, pool, t = filled(lens, hkv, d, block, seed=sum(lens) + T, extra=1, width=2)
+    q = torch.randn((len(lens), T, hq, d), generator=torch.Generator(device=DEV).manual_seed(3), device=DEV).bfloat16()
+    ref = R.attention(pool, q.double().cpu().numpy(), t, lens, window, d ** -0.5)
+    out, lse = msa.cache_attention(q, cache, i32(t), i32(lens), window=window)
+    check_attention(out, lse, ref, d, True)
+
+
+@pytest.mark.usefixtures("padded_for_pairs")
+@pytest.mark.parametrize("shift", [4, 14, 22, 24, 26, 30])
+def test_pairs_with_large_values_at_small_weights(shift):
+    test_large_values_at_small_weights("bf16", shift)
+
+
+@pytest.mark.usefixtures("padded_for_pairs")
+@pytest.mark.parametrize("window", [32, 40, 45, 64])
+@pytest.mark.parametrize("where,at", [("k", 79), ("v", 78), ("v", 40), ("k", 39), ("v", 39), ("v", 35), ("k", 10), ("v", 10)])
+def test_pairs_with_nan_slots_at_a_windows_edges(where, at, window):
+    """A row is NaN if it attends the slot, and what it is without the slot if not
+    (its softmax's references may be other ones: within the bounds)."""
+    n, d, T = 80, 128, 4
+    rng = np.random.default_rng(77)
+    k, v = rng.normal(size=(2, n, 1, d)).astype(np.float32)
+    q = torch.as_tensor(rng.normal(size=(1, T, 2, d)), device=DEV).bfloat16()
+    t = np.array([[1, 3, 0]], dtype=np.int32)
+
+    def pooled(x, y):
+        cache = new_cache(4, 1, d, 32)
+        msa.cache_append(cache, torch.as_tensor(x, device=DEV), torch.as_tensor(y, device=DEV), i32([0, n]), i32(t), i32([n]), n)
+        return cache
+
+    ref = R.attention(pool_of(pooled(k, v)), q.double().cpu().numpy(), t, [n], window, d ** -0.5)
+    (k if where == "k" else v)[at, 0, 100] = np.nan
+    out, lse = msa.cache_attention(q, pooled(k, v), i32(t), i32([n]), window=window)
+    hit = [row for row in range(T) if n - T + row - window < at <= n - T + row]
+    assert torch.isnan(out[0, hit]).all()
+    assert torch.isnan(lse[0, :, hit]).all() if where == "k" else torch.isfinite(lse).all()
+    rows = [row for row in range(T) if row not in hit]
+    if rows:
+        check_attention(out[:, rows], lse[:, :, rows], tuple(x[:, :, rows] if i == 1 else x[:, rows] for i, x in enumerate(ref)), d, True)

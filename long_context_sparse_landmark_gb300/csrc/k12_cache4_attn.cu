@@ -216,7 +216,8 @@ struct Body4 {
       float v[8], mx = 0.f;
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[k] = 0.f;
-      if (m < p.rows) {
+      if (m < p.rows && MSA_IN_RANGE(at, 8, static_cast<int64_t>(a.s.batch) * a.T * a.Hq * D,
+                                     a.status)) {
         if constexpr (kTerms == 1) {
           const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at);
           const uint32_t w[4] = {x.x, x.y, x.z, x.w};

@@ -204,6 +204,7 @@ __device__ __forceinline__ void angles(const RopeArgs& a, int64_t freq, int64_t 
   const int f = threadIdx.x % kFreqs;
   const int at = kInterleaved ? f : (f >> 2 & 1) * (D / 4) + (f >> 3) * 4 + (f & 3);
   for (int t = threadIdx.x / kFreqs; t < tokens; t += kThreads / kFreqs) {
+    if (!MSA_IN_RANGE(t0 + t, 1, a.n, a.status)) continue;
     const float2 x = turn_of(a.positions[t0 + t], freq, a.mscale);
     cs[t * D + at] = x.x;
     cs[t * D + D / 2 + at] = x.y;
@@ -314,8 +315,9 @@ __global__ void __launch_bounds__(kThreads, kFwdPerSm) norm_rope_kernel(const Ro
   // A row's values come in while the one before is worked on.
   Raw<D, kBf16> ahead;
   const auto load = [&](const Walk<D>& at) {
-    if (at.in())
-      ahead.load(src, (at.t0 + at.t) * stride + at.h * D + lane * 8);
+    const int64_t from = (at.t0 + at.t) * stride + at.h * D + lane * 8;
+    if (at.in() && MSA_IN_RANGE(from, D / 2 + 8, (a.n - 1) * stride + H * D, a.status))
+      ahead.load(src, from);
     else
       ahead.clear();
   };
@@ -345,8 +347,9 @@ __global__ void __launch_bounds__(kThreads, kFwdPerSm) norm_rope_kernel(const Ro
 }
 
 // A sum in two floats: lo takes what an addition to hi rounds off (Knuth's
-// two-sum), so that a sum of any length keeps fp32's bits.  (In 64 bits, at the 1.25 TFLOP/s that a GB300 is given, the
-// last kernel's additions alone would take some 2 us of the 2K-token step's 11.)
+// two-sum), so that a sum of any length keeps fp32's bits.  (In 64 bits, at the 1.25
+// TFLOP/s that a GB300 is given, the last kernel's additions alone would take some 2 us
+// of the 2K-token step's 11.)
 struct Sum {
   float hi, lo;
   __device__ __forceinline__ void add(float x) {
@@ -478,12 +481,16 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm) norm_rope_bwd_kernel(cons
     }
     if (ahead.in()) {
       const int64_t t = ahead.t0 + ahead.t, h = ahead.h * D + lane * 8;
+      const bool g_in = MSA_IN_RANGE(t * dy_stride + h, D / 2 + 8,
+                                     (a.n - 1) * dy_stride + H * D, a.status);
+      const bool x_in = norm && MSA_IN_RANGE(t * stride + h, D / 2 + 8,
+                                             (a.n - 1) * stride + H * D, a.status);
       if constexpr (kBf16) {
-        R::fetch(place + slot * kPass, grad, t * dy_stride + h);
-        if (norm) R::fetch(place + slot * kPass + R::kBytes, src, t * stride + h);
+        if (g_in) R::fetch(place + slot * kPass, grad, t * dy_stride + h);
+        if (x_in) R::fetch(place + slot * kPass + R::kBytes, src, t * stride + h);
       } else {
-        next_g.load(grad, t * dy_stride + h);
-        if (norm) next_x.load(src, t * stride + h);
+        if (g_in) next_g.load(grad, t * dy_stride + h);
+        if (x_in) next_x.load(src, t * stride + h);
       }
     }
     ahead.next();

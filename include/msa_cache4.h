@@ -75,7 +75,9 @@ size_t msa_cache4_attn_workspace_size(const msa_kv_cache4 *cache,
  * row's largest is off by 2^-33 of that one (its product with the value by at most
  * 2^-20 of the row's largest product, where values lie far apart).  Sums are fp32.
  * As with the 8-bit cache the result does not depend on the run, but its rounding
- * does on the whole batch's lengths.
+ * does on the whole batch's lengths; here also on max_blocks and window (and the
+ * sizes), which choose the rows and chunks taken together: a wider table can give
+ * other last bits.
  */
 msa_status msa_cache4_attn(const msa_kv_cache4 *cache, const void *q,
                            const int32_t *table, int max_blocks,

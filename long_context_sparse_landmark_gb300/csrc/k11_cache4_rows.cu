@@ -13,7 +13,8 @@
 // CTAs of their own.  Append and then read of 131072 tokens in bf16: 2 rows 207 us, 8
 // rows 237, 4 rows 202, 8 values a thread 238; of 8192 tokens 2 rows 14.7 us, 4 rows
 // 13.8; fp32, 24 ragged prompts of up to 501 tokens, 4 heads of 64: 2 rows 9.0, 4 rows
-// 10.7 (in CTAs of 256 threads 10.3 and 12.7).
+// 10.7 (in CTAs of 256 threads 10.3 and 12.7; the same prompts over and over, which L2
+// holds: new ones each time, in blocks of 32, take 11.3, and 13.4 with 4 rows and 256).
 #include "cache4.cuh"
 
 namespace msa {

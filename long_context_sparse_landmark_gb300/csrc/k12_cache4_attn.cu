@@ -171,7 +171,8 @@ struct Body4 {
   float l[kNt][2];  // in units of 2^M, o of 2^{M + D0 - kPBits}
   // M and D0 of rows 2t, 2t+1: looked at where a reference moves or a chunk does not
   // fit.  Those of two and four tiles are in shared memory: with 32 rows in registers
-  // 304 bytes spilled, and 16 rows are 3 CTAs an SM (168 registers) without them.
+  // 304 bytes spilled (162 still do at d = 128, 255 registers), and 16 rows are 3 CTAs
+  // an SM (168 registers, 28 bytes spilled) without them.
   static constexpr bool kCold = kNt >= 2;
   struct Refs {
     float v[2][kNt][2];

@@ -7,8 +7,8 @@
 // and heads of g x r.  Everything is fp32 between one read and one rounding.
 //
 // Each value is read and written once, and HBM bounds a long call: 32768 tokens of
-// 64 + 8 heads of 128 in bf16 take 194 us forward, 6.2 TB/s (DRAM 78 % of its peak),
-// and 276 us backward, 6.6 TB/s (DRAM 82 %), with half of the issue slots.  A thread
+// 64 + 8 heads of 128 in bf16 take 192 us forward, 6.3 TB/s (DRAM 78 % of its peak),
+// and 279 us backward, 6.5 TB/s (DRAM 83 %), with half of the issue slots.  A thread
 // takes 16 values of a row, two runs of 8 half a row apart, so that both
 // members of a pair are its own in either pairing; a row is d / 16 lanes.  CTAs
 // take equal runs of rows of one side, whatever the tokens, with the next row's
@@ -21,7 +21,7 @@ namespace msa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kFwdPerSm = 4, kBwdPerSm = 2;  // CTAs
+constexpr int kFwdPerSm = 4, kBwdPerSm = 2;  // CTAs (4: the fp32 forward spills 48 bytes a thread)
 constexpr int kGroup = 8;                    // passes over which the angles are held
 // Floats of the angles of a group's tokens: 8 passes of 32 rows (d = 128) or 64 are
 // 2 + 256 / heads tokens and more; fewer passes a group where that does not fit.
